@@ -1,7 +1,8 @@
 /*
  * mla_decode.h -- C ABI of libmla_decode.so: paged multi-head-latent-attention (MLA)
  * decode with decode-context-parallel (DCP) shards, the LSE merge of shard partials,
- * and DCP slot mapping, for NVIDIA GB300 (sm_103a).
+ * DCP slot mapping, and the 8-bit form of the paged cache (a step's tables from request
+ * lengths, the quantising store, the decode over it), for NVIDIA GB300 (sm_103a).
  *
  * Sources (web pages summarising vLLM pull requests):
  *   [#52188] "支持 Kimi-K3 DSpark 推测解码与 DCP 并行组合" (vLLM PR 52188)
@@ -53,6 +54,15 @@ typedef struct CUstream_st* mla_stream_t;
 #define MLA_STATUS_SEQ_TOO_LONG 2u    /* seq_lens[b] > max_blocks * block_size          */
 #define MLA_STATUS_BAD_VBLOCK 4u      /* cp_local_slot: virtual block >= max_blocks     */
 #define MLA_STATUS_WAIT_TIMEOUT 8u    /* a bounded on-chip wait gave up                 */
+#define MLA_STATUS_BAD_SCALE 16u      /* a scale of the 8-bit cache outside its range   */
+#define MLA_STATUS_OUT_OF_PAGES 32u   /* cp_step_tables: too few free pages             */
+#define MLA_STATUS_BAD_STEP 64u       /* a length or a ring state outside its range     */
+
+/* The 8-bit cache: e4m3 rows, one float scale for every MLA_Q8_GROUP consecutive slots of
+ * a page; a scale is at least MLA_Q8_SCALE_MIN and at most MLA_Q8_SCALE_MAX. */
+#define MLA_Q8_GROUP 16
+#define MLA_Q8_SCALE_MIN 2.3283064365386963e-10f /* 2^-32 */
+#define MLA_Q8_SCALE_MAX 1.8446744073709552e19f  /* 2^64  */
 
 /*
  * Bytes of workspace that mla_decode uses to split one request's KV range over several
@@ -220,6 +230,137 @@ int cp_local_slot_scatter(const int64_t* positions, const void* kv_new,
                           void* kv_cache, int num_blocks, int64_t* slots, mla_stream_t stream);
 
 /*
+ * cp_step_tables -- the tables of one serving step, built on the GPU from request lengths:
+ * pages taken and given back, global and shard-local lengths, the new tokens' positions and
+ * their slots.  Everything cp_store_q8, cp_local_slot_scatter and the decode calls read
+ * comes from it, so that a step needs no host round trip and can be captured in a graph.
+ *
+ * With vbs = block_size * cp_size (a virtual block, see cp_local_slot) and
+ * pages(x) = ceil(x / vbs), request b holds pages(prev_lens[b]) pages, has ctx_lens[b]
+ * tokens in the cache (fewer than prev_lens[b] after a rejected draft, 0 when it has
+ * finished) and brings new_lens[b] new tokens:
+ *   take_b  = max(0, pages(ctx + new) - pages(prev));  request b is granted when
+ *             pages(ctx + new) <= max_blocks and take_b is 0 or take_0 + .. + take_b is at
+ *             most the number of free pages (requests that do not fit the table take none);
+ *   total_b = ctx + new if granted, else min(ctx, prev) (then it has no new token);
+ *   give_b  = max(0, pages(prev) - pages(total)).
+ * free_pages is a ring of free_cap entries; free_state = {head, count}.  Granted requests
+ * take their pages from the head in the order of b, the page of virtual block j going to
+ * block_table[b, j]; pages given back (virtual blocks pages(total) .. pages(prev) - 1, in
+ * the order of b) join the end, and can be taken from the next call on.  Other table entries
+ * are left as they were.  free_state_out = {(head + taken) % free_cap, count - taken + given}.
+ *   total_lens[b]      = total_b  (causal_seqlens_global of the decode calls);
+ *   seq_lens[r, b]     = local_len(total_b) on rank cp_rank + r (see mla_decode);
+ *   positions[b, n]    = ctx_lens[b] + n for n < new_lens[b] of a granted request, else -1;
+ *   slots[r, b, n]     = the slot cp_local_slot gives that position on rank cp_rank + r.
+ * A call reads and writes disjoint entries, so repeating it with the same inputs gives the
+ * same result.
+ *
+ * Arguments:
+ *   prev_lens, ctx_lens, new_lens  int32 [B], values in [0, 2^31) with new_lens[b] <= N.
+ *   block_table  int32 [B, bt_stride], max_blocks columns in use; updated.
+ *   free_pages   int32 [free_cap], free_cap at least the number of pages of the pool; updated.
+ *   free_state   int32 [2];  free_state_out  int32 [2].
+ *   total_lens   int32 [B].
+ *   seq_lens     int32 [n_ranks, B] or NULL;  positions  int64 [B, N] or NULL;
+ *   slots        int64 [n_ranks, B, N] or NULL.
+ *   B >= 0, N >= 0, n_ranks >= 1, 0 <= cp_rank, cp_rank + n_ranks <= cp_size, free_cap >= 1;
+ *   block_size, cp_size, interleave, max_blocks, bt_stride as for cp_local_slot.
+ *   The outputs may not overlap the inputs (total_lens and prev_lens are two buffers that a
+ *   caller swaps; so are free_state and free_state_out).
+ * Bad data is flagged and bounded: a request that does not fit the table sets
+ * MLA_STATUS_SEQ_TOO_LONG, one that finds too few free pages MLA_STATUS_OUT_OF_PAGES (both
+ * are not granted); a negative length is read as 0, a new_lens above N as N, prev_lens beyond
+ * the table as the whole table, a ring state outside the ring as an empty ring, and pages
+ * given back to a full ring are dropped, each with MLA_STATUS_BAD_STEP.
+ * Errors: MLA_ERR_INVALID_ARGUMENT, MLA_ERR_UNSUPPORTED (n_ranks*B*N or block_size*cp_size
+ *   beyond 2^31-1), MLA_ERR_CUDA.
+ */
+int cp_step_tables(const int32_t* prev_lens, const int32_t* ctx_lens, const int32_t* new_lens,
+                   int B, int N, int32_t* block_table, int64_t bt_stride, int max_blocks,
+                   int32_t* free_pages, int free_cap, const int32_t* free_state,
+                   int32_t* free_state_out, int block_size, int cp_size, int cp_rank,
+                   int n_ranks, int interleave, int32_t* total_lens, int32_t* seq_lens,
+                   int64_t* positions, int64_t* slots, mla_stream_t stream);
+
+/*
+ * cp_store_q8 -- writes a step's new KV rows into this rank's 8-bit pool.
+ *
+ * New token n of request b (0 <= n < total_lens[b] - ctx_lens[b], at most N) has position
+ * ctx_lens[b] + n; the rank stores those cp_local_slot gives it a slot for.  The slots of a
+ * page are grouped by MLA_Q8_GROUP consecutive ones, which share one scale s; a row x is
+ * stored as e4m3(x / s), rounded to nearest even, and stands for s times that.  For each
+ * group that gets a new row, with a = the largest finite |x| of its new rows:
+ *   s = the smallest power of two with a <= 448 s, within [MLA_Q8_SCALE_MIN,
+ *       MLA_Q8_SCALE_MAX] (larger values are stored as +-448);
+ *   where the group begins with earlier rows of the request (the first new row is not its
+ *   first), s is at least the scale s_old that is there; if s grows, the earlier rows are
+ *   stored again as e4m3(v * (s_old / s)).
+ * Slots of the group behind the new rows are left as they were (whatever they held before
+ * they are no longer scaled by the scale they were stored with).  NaN and infinities are
+ * stored as NaN and take no part in a.
+ *
+ * Arguments (as cp_local_slot unless stated):
+ *   kv_new       bf16 [B, N, 576], 16-byte aligned.
+ *   ctx_lens, total_lens  int32 [B], as cp_step_tables takes and gives them.
+ *   kv_cache     e4m3 [num_blocks, block_size, 576] (this rank's pool), 16-byte aligned.
+ *   kv_scales    float [num_blocks, block_size / 16].
+ *   block_size   a multiple of 16.
+ * Two requests with new rows in one page race (pages that requests share hold whole blocks
+ * of common tokens, which no one writes).  A table entry outside [0, num_blocks) writes
+ * nothing and sets MLA_STATUS_BAD_PAGE, a virtual block past the table MLA_STATUS_BAD_VBLOCK;
+ * an earlier scale outside its range is taken as 1 with MLA_STATUS_BAD_SCALE; a negative
+ * ctx_lens (the request is skipped) or more than N new tokens (N are stored) sets
+ * MLA_STATUS_BAD_STEP.
+ * Errors: MLA_ERR_INVALID_ARGUMENT, MLA_ERR_UNSUPPORTED (B*N or block_size*cp_size beyond
+ *   2^31-1), MLA_ERR_CUDA.
+ */
+int cp_store_q8(const void* kv_new, const int32_t* ctx_lens, const int32_t* total_lens,
+                const int32_t* block_table, int64_t bt_stride, int max_blocks, int B, int N,
+                int block_size, int cp_size, int cp_rank, int interleave, void* kv_cache,
+                float* kv_scales, int num_blocks, mla_stream_t stream);
+
+/*
+ * mla_decode_q8, mla_decode_shards_q8 -- mla_decode and mla_decode_shards over the 8-bit
+ * cache that cp_store_q8 writes: key l of the definition there is the row's 576 e4m3 values
+ * times the scale of its group, and everything else is the same (row bounds, empty rows,
+ * LSE bases, the outputs' layouts).
+ *
+ * Arguments (as mla_decode / mla_decode_shards unless stated):
+ *   kv_cache     e4m3 [num_blocks, block_size, 576], 16-byte aligned;
+ *   kv_scales    float [num_blocks, block_size / 16]; any finite scale within
+ *                [MLA_Q8_SCALE_MIN, MLA_Q8_SCALE_MAX], powers of two or not.  A scale outside
+ *                that range of a group with a visible key is taken as 1 and sets
+ *                MLA_STATUS_BAD_SCALE; scales of other groups are not used.
+ *   block_size   a multiple of 16.
+ *   q            finite values; a row of q with a NaN or an infinity gives NaN outputs.
+ *   ceil(q_len*H/64) <= SMs.
+ *   workspace    scratch for split-KV, sized by mla_decode_q8_workspace_size (for the shards
+ *                call with n_shards*B), or NULL / 0: without all of it no request is split.
+ * Accuracy: products and sums are fp32; q is used to within 2^-17 of its row's largest
+ * magnitude (exactly, for elements within 2^-9 of it), and a softmax weight to within 2^-7
+ * of itself plus 2^-14 of the row's largest weight times scale, where the bf16 cache's
+ * decode rounds it to bf16.
+ * Errors: as mla_decode / mla_decode_shards.
+ */
+size_t mla_decode_q8_workspace_size(int B, int H, int q_len, int num_sms);
+
+int mla_decode_q8(const void* q, const void* kv_cache, const float* kv_scales,
+                  const int32_t* block_table, int64_t bt_stride, const int32_t* seq_lens,
+                  const int32_t* causal_seqlens_global, int B, int H, int q_len, int causal,
+                  int block_size, int num_blocks, int max_blocks, int cp_world, int cp_rank,
+                  int interleave, float scale, void* out, float* lse, int lse_base_e,
+                  void* workspace, size_t workspace_bytes, mla_stream_t stream);
+
+int mla_decode_shards_q8(const void* q, const void* kv_cache, const float* kv_scales,
+                         const int32_t* block_table, int64_t bt_stride,
+                         const int32_t* seq_lens, const int32_t* causal_seqlens_global, int B,
+                         int H, int q_len, int causal, int block_size, int num_blocks,
+                         int max_blocks, int n_shards, int interleave, float scale, void* out,
+                         float* lse, int lse_base_e, void* workspace, size_t workspace_bytes,
+                         mla_stream_t stream);
+
+/*
  * mla_decode_noalloc -- mla_decode for callers that cannot allocate device memory.
  *
  * The pages have no counterpart to this call.  It computes exactly what mla_decode
@@ -297,7 +438,7 @@ int mla_set_test_stall(int on);
 /* Message of the calling thread's last failed call (empty string if none). */
 const char* mla_last_error(void);
 
-/* ABI version of this library: (major << 16) | minor (2.0). */
+/* ABI version of this library: (major << 16) | minor (2.1). */
 int mla_abi_version(void);
 
 #ifdef __cplusplus

@@ -8,6 +8,9 @@ Thin PyTorch-facing wrappers over the C ABI of ``libmla_decode.so``:
   lse_merge              merge shard partials through their LSEs
   cp_local_slot          global position -> this rank's KV slot (PAD_SLOT_ID = -1 otherwise)
   cp_local_slot_scatter  write new KV rows into this rank's pool at those slots
+  cp_step_tables         a step's pages, lengths, positions and slots from request lengths
+  cp_store_q8            quantise new KV rows into the 8-bit cache (e4m3, a scale per 16 slots)
+  mla_decode_q8          mla_decode over the 8-bit cache (mla_decode_shards_q8: every shard)
 
 PyTorch provides device memory and the current stream; every step of the computation
 runs in the library's CUDA kernels.  All tensors must live on the current CUDA device.
@@ -27,7 +30,9 @@ D_V = 512
 
 __all__ = ["mla_decode", "mla_decode_shards", "lse_merge", "cp_local_slot",
            "cp_local_slot_scatter", "workspace_size", "device_status", "set_decode_kernel",
-           "set_rescale_budget", "set_wait_limit_ns", "PAD_SLOT_ID", "MlaError", "D_QK", "D_V"]
+           "set_rescale_budget", "set_wait_limit_ns", "PAD_SLOT_ID", "MlaError", "D_QK", "D_V",
+           "cp_step_tables", "cp_store_q8", "mla_decode_q8", "mla_decode_shards_q8", "StepTables",
+           "workspace_size_q8", "alloc_workspace_q8", "Q8_GROUP"]
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -303,3 +308,7 @@ def device_status(stream=None) -> int:
     if rc not in (_lib.MLA_OK, _lib.MLA_ERR_DEVICE):
         _lib.check(rc)
     return int(bits.value)
+
+
+from .q8 import (Q8_GROUP, StepTables, alloc_workspace_q8, cp_step_tables,  # noqa: E402,F401
+                 cp_store_q8, mla_decode_q8, mla_decode_shards_q8, workspace_size_q8)

@@ -20,7 +20,9 @@ MLA_ERR_DEVICE = -4
 PAD_SLOT_ID = -1
 
 EXPORTED = ("mla_decode_workspace_size", "mla_decode", "mla_decode_shards", "mla_decode_noalloc",
-            "lse_merge", "cp_local_slot", "cp_local_slot_scatter",
+            "lse_merge", "cp_local_slot", "cp_local_slot_scatter", "cp_step_tables",
+            "cp_store_q8", "mla_decode_q8_workspace_size", "mla_decode_q8",
+            "mla_decode_shards_q8",
             "mla_get_device_status", "mla_set_decode_kernel", "mla_set_rescale_budget",
             "mla_set_wait_limit_ns", "mla_set_test_stall", "mla_last_error",
             "mla_abi_version")
@@ -81,6 +83,23 @@ def load() -> ctypes.CDLL:
         lib.cp_local_slot_scatter.argtypes = [c_vp, c_vp, c_vp, c_i64, c_int, c_int, c_int,
                                               c_int, c_int, c_int, c_int, c_vp, c_int, c_vp,
                                               c_vp]
+        lib.cp_step_tables.restype = c_int
+        lib.cp_step_tables.argtypes = [c_vp, c_vp, c_vp, c_int, c_int, c_vp, c_i64, c_int, c_vp,
+                                       c_int, c_vp, c_vp, c_int, c_int, c_int, c_int, c_int,
+                                       c_vp, c_vp, c_vp, c_vp, c_vp]
+        lib.cp_store_q8.restype = c_int
+        lib.cp_store_q8.argtypes = [c_vp, c_vp, c_vp, c_vp, c_i64, c_int, c_int, c_int, c_int,
+                                    c_int, c_int, c_int, c_vp, c_vp, c_int, c_vp]
+        # as the bf16 calls, with kv_scales after kv_cache
+        head8 = head[:2] + [c_vp] + head[2:]
+        lib.mla_decode_q8_workspace_size.restype = c_sz
+        lib.mla_decode_q8_workspace_size.argtypes = [c_int, c_int, c_int, c_int]
+        lib.mla_decode_q8.restype = c_int
+        lib.mla_decode_q8.argtypes = head8 + [c_int, c_int, c_int, c_f, c_vp, c_vp, c_int, c_vp,
+                                              c_sz, c_vp]
+        lib.mla_decode_shards_q8.restype = c_int
+        lib.mla_decode_shards_q8.argtypes = head8 + [c_int, c_int, c_f, c_vp, c_vp, c_int, c_vp,
+                                                     c_sz, c_vp]
         lib.mla_get_device_status.restype = c_int
         lib.mla_get_device_status.argtypes = [c_vp, ctypes.POINTER(ctypes.c_uint32)]
         lib.mla_last_error.restype = ctypes.c_char_p

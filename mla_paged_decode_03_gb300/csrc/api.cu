@@ -97,7 +97,7 @@ int api_fail(int code, const char* fmt, ...) {
 
 extern "C" {
 
-int mla_abi_version(void) { return (2 << 16) | 0; }
+int mla_abi_version(void) { return (2 << 16) | 1; }
 
 int mla_set_decode_kernel(int choice) {
   static std::atomic<int> current{0};
@@ -134,26 +134,35 @@ size_t mla_decode_workspace_size(int B, int H, int q_len, int num_sms) {
   return mla::decode_workspace_size(B, H, q_len, num_sms);
 }
 
+size_t mla_decode_q8_workspace_size(int B, int H, int q_len, int num_sms) {
+  if (B <= 0 || H <= 0 || q_len <= 0 || num_sms <= 0) return 0;
+  return mla::q8_workspace_size(B, H, q_len, num_sms);
+}
+
 }  // extern "C"
 
 namespace mla {
 
 // Shared by mla_decode (n_shards == 1, the given rank), mla_decode_shards (ranks
-// 0 .. n_shards-1 of cp_world == n_shards, shard-major tables and outputs) and
-// mla_decode_noalloc (require_full_split: the workspace must hold the scratch of the full
+// 0 .. n_shards-1 of cp_world == n_shards, shard-major tables and outputs), their forms over
+// the 8-bit cache (q8: kv_cache is e4m3 and kv_scales its scales) and mla_decode_noalloc (require_full_split: the workspace must hold the scratch of the full
 // split-KV schedule, else the call is refused after every other check).
-int decode_entry(const char* fn, const void* q, const void* kv_cache, const int32_t* block_table,
-                 int64_t bt_stride, const int32_t* seq_lens, const int32_t* causal_seqlens_global,
-                 int B, int H, int q_len, int causal, int block_size, int num_blocks,
-                 int max_blocks, int cp_world, int cp_rank, int interleave, int n_shards,
-                 float scale, void* out, float* lse, int lse_base_e, void* workspace,
-                 size_t workspace_bytes, bool require_full_split, mla_stream_t stream) {
+int decode_entry(const char* fn, const void* q, const void* kv_cache, bool q8,
+                 const float* kv_scales, const int32_t* block_table, int64_t bt_stride,
+                 const int32_t* seq_lens, const int32_t* causal_seqlens_global, int B, int H,
+                 int q_len, int causal, int block_size, int num_blocks, int max_blocks,
+                 int cp_world, int cp_rank, int interleave, int n_shards, float scale, void* out,
+                 float* lse, int lse_base_e, void* workspace, size_t workspace_bytes,
+                 bool require_full_split, mla_stream_t stream) {
   if (B < 0) return fail(MLA_ERR_INVALID_ARGUMENT, "%s: B=%d < 0", fn, B);
   if (H < 1) return fail(MLA_ERR_INVALID_ARGUMENT, "%s: H=%d < 1", fn, H);
   if (q_len < 1 || q_len > MLA_MAX_Q_LEN)
     return fail(q_len < 1 ? MLA_ERR_INVALID_ARGUMENT : MLA_ERR_UNSUPPORTED,
                 "%s: q_len=%d outside [1, %d]", fn, q_len, MLA_MAX_Q_LEN);
   if (block_size < 1) return fail(MLA_ERR_INVALID_ARGUMENT, "%s: block_size < 1", fn);
+  if (q8 && block_size % MLA_Q8_GROUP != 0)
+    return fail(MLA_ERR_INVALID_ARGUMENT, "%s: block_size (%d) must be a multiple of %d", fn,
+                block_size, MLA_Q8_GROUP);
   if (num_blocks < 1) return fail(MLA_ERR_INVALID_ARGUMENT, "%s: num_blocks < 1", fn);
   if (max_blocks < 1 || bt_stride < max_blocks)
     return fail(MLA_ERR_INVALID_ARGUMENT, "%s: need 1 <= max_blocks (%d) <= bt_stride (%lld)",
@@ -176,13 +185,15 @@ int decode_entry(const char* fn, const void* q, const void* kv_cache, const int3
   if (B == 0) return ok();
   if (!q || !kv_cache || !block_table || !seq_lens || !out)
     return fail(MLA_ERR_INVALID_ARGUMENT, "%s: null q/kv_cache/block_table/seq_lens/out", fn);
+  if (q8 && !kv_scales) return fail(MLA_ERR_INVALID_ARGUMENT, "%s: null kv_scales", fn);
   if (causal_seqlens_global == nullptr && cp_world != 1 && causal)
     return fail(MLA_ERR_INVALID_ARGUMENT,
                 "%s: causal_seqlens_global is required when cp_world > 1", fn);
   if (!aligned(q, 16) || !aligned(kv_cache, 16) || !aligned(out, 16))
     return fail(MLA_ERR_INVALID_ARGUMENT, "%s: q, kv_cache and out must be 16-byte aligned", fn);
   if (!aligned(block_table, 4) || !aligned(seq_lens, 4) ||
-      (causal_seqlens_global && !aligned(causal_seqlens_global, 4)) || (lse && !aligned(lse, 4)))
+      (causal_seqlens_global && !aligned(causal_seqlens_global, 4)) || (lse && !aligned(lse, 4)) ||
+      (q8 && !aligned(kv_scales, 4)))
     return fail(MLA_ERR_INVALID_ARGUMENT, "%s: misaligned int32/float argument", fn);
   if (workspace && !aligned(workspace, 256))
     return fail(MLA_ERR_INVALID_ARGUMENT, "%s: workspace must be 256-byte aligned", fn);
@@ -196,6 +207,7 @@ int decode_entry(const char* fn, const void* q, const void* kv_cache, const int3
   mla::DecodeArgs a;
   a.q = static_cast<const uint16_t*>(q);
   a.kv = static_cast<const uint16_t*>(kv_cache);
+  a.kv_scales = q8 ? kv_scales : nullptr;
   a.block_table = block_table;
   a.bt_stride = bt_stride;
   a.seq_lens = seq_lens;
@@ -223,6 +235,11 @@ int decode_entry(const char* fn, const void* q, const void* kv_cache, const int3
   a.num_sms = dev->num_sms;
   a.status = dev->status;
   const mla::DecodeKernel k = mla::choose_decode_kernel(a);
+  if (k == mla::kDecodeNone && q8)
+    return fail(MLA_ERR_UNSUPPORTED,
+                "%s: q_len*H = %d rows need at most %d row tiles of 64, and num_blocks*block_size "
+                "must stay below 2^31 - 128",
+                fn, q_len * H, dev->num_sms);
   if (k == mla::kDecodeNone)
     return fail(MLA_ERR_UNSUPPORTED,
                 "%s: no decode kernel for this layout (block_size %d: the tcgen05 kernel takes "
@@ -251,8 +268,8 @@ int mla_decode(const void* q, const void* kv_cache, const int32_t* block_table,
                int block_size, int num_blocks, int max_blocks, int cp_world, int cp_rank,
                int interleave, float scale, void* out, float* lse, int lse_base_e,
                void* workspace, size_t workspace_bytes, mla_stream_t stream) {
-  return mla::decode_entry("mla_decode", q, kv_cache, block_table, bt_stride, seq_lens,
-                           causal_seqlens_global, B, H, q_len, causal, block_size, num_blocks,
+  return mla::decode_entry("mla_decode", q, kv_cache, false, nullptr, block_table, bt_stride,
+                           seq_lens, causal_seqlens_global, B, H, q_len, causal, block_size, num_blocks,
                            max_blocks, cp_world, cp_rank, interleave, 1, scale, out, lse,
                            lse_base_e, workspace, workspace_bytes, false, stream);
 }
@@ -267,10 +284,42 @@ int mla_decode_shards(const void* q, const void* kv_cache, const int32_t* block_
     return fail(MLA_ERR_INVALID_ARGUMENT, "mla_decode_shards: n_shards=%d < 1", n_shards);
   if (n_shards > 1 && B > 0 && (unsigned long long)n_shards * B * B >= (1ull << 32))
     return fail(MLA_ERR_UNSUPPORTED, "mla_decode_shards: n_shards * B^2 must stay below 2^32");
-  return mla::decode_entry("mla_decode_shards", q, kv_cache, block_table, bt_stride, seq_lens,
-                           causal_seqlens_global, B, H, q_len, causal, block_size, num_blocks,
-                           max_blocks, n_shards, 0, interleave, n_shards, scale, out, lse,
-                           lse_base_e, workspace, workspace_bytes, false, stream);
+  return mla::decode_entry("mla_decode_shards", q, kv_cache, false, nullptr, block_table,
+                           bt_stride, seq_lens, causal_seqlens_global, B, H, q_len, causal,
+                           block_size, num_blocks, max_blocks, n_shards, 0, interleave, n_shards,
+                           scale, out, lse, lse_base_e, workspace, workspace_bytes, false,
+                           stream);
+}
+
+int mla_decode_q8(const void* q, const void* kv_cache, const float* kv_scales,
+                  const int32_t* block_table, int64_t bt_stride, const int32_t* seq_lens,
+                  const int32_t* causal_seqlens_global, int B, int H, int q_len, int causal,
+                  int block_size, int num_blocks, int max_blocks, int cp_world, int cp_rank,
+                  int interleave, float scale, void* out, float* lse, int lse_base_e,
+                  void* workspace, size_t workspace_bytes, mla_stream_t stream) {
+  return mla::decode_entry("mla_decode_q8", q, kv_cache, true, kv_scales, block_table, bt_stride,
+                           seq_lens, causal_seqlens_global, B, H, q_len, causal, block_size,
+                           num_blocks, max_blocks, cp_world, cp_rank, interleave, 1, scale, out,
+                           lse, lse_base_e, workspace, workspace_bytes, false, stream);
+}
+
+int mla_decode_shards_q8(const void* q, const void* kv_cache, const float* kv_scales,
+                         const int32_t* block_table, int64_t bt_stride,
+                         const int32_t* seq_lens, const int32_t* causal_seqlens_global, int B,
+                         int H, int q_len, int causal, int block_size, int num_blocks,
+                         int max_blocks, int n_shards, int interleave, float scale, void* out,
+                         float* lse, int lse_base_e, void* workspace, size_t workspace_bytes,
+                         mla_stream_t stream) {
+  if (n_shards < 1)
+    return fail(MLA_ERR_INVALID_ARGUMENT, "mla_decode_shards_q8: n_shards=%d < 1", n_shards);
+  if (n_shards > 1 && B > 0 && (unsigned long long)n_shards * B * B >= (1ull << 32))
+    return fail(MLA_ERR_UNSUPPORTED,
+                "mla_decode_shards_q8: n_shards * B^2 must stay below 2^32");
+  return mla::decode_entry("mla_decode_shards_q8", q, kv_cache, true, kv_scales, block_table,
+                           bt_stride, seq_lens, causal_seqlens_global, B, H, q_len, causal,
+                           block_size, num_blocks, max_blocks, n_shards, 0, interleave, n_shards,
+                           scale, out, lse, lse_base_e, workspace, workspace_bytes, false,
+                           stream);
 }
 
 int lse_merge(const void* partials, int partials_fp32, const float* lses, int n_shards,
@@ -363,6 +412,138 @@ int cp_local_slot_scatter(const int64_t* positions, const void* kv_new,
   return ok();
 }
 
+int cp_step_tables(const int32_t* prev_lens, const int32_t* ctx_lens, const int32_t* new_lens,
+                   int B, int N, int32_t* block_table, int64_t bt_stride, int max_blocks,
+                   int32_t* free_pages, int free_cap, const int32_t* free_state,
+                   int32_t* free_state_out, int block_size, int cp_size, int cp_rank,
+                   int n_ranks, int interleave, int32_t* total_lens, int32_t* seq_lens,
+                   int64_t* positions, int64_t* slots, mla_stream_t stream) {
+  const char* fn = "cp_step_tables";
+  int rc = slot_args_check(fn, B, N, block_size, cp_size, cp_rank, interleave, max_blocks,
+                           bt_stride);
+  if (rc != MLA_OK) return rc;
+  if (n_ranks < 1 || n_ranks > cp_size - cp_rank)
+    return fail(MLA_ERR_INVALID_ARGUMENT, "%s: need 1 <= n_ranks (%d) <= cp_size - cp_rank (%d)",
+                fn, n_ranks, cp_size - cp_rank);
+  if ((long long)B * N > ((1LL << 31) - 1) / n_ranks || (long long)B * n_ranks > (1LL << 31) - 1)
+    return fail(MLA_ERR_UNSUPPORTED, "%s: n_ranks*B*N exceeds 2^31-1", fn);
+  if (free_cap < 1) return fail(MLA_ERR_INVALID_ARGUMENT, "%s: free_cap=%d < 1", fn, free_cap);
+  if (!free_pages || !free_state || !free_state_out)
+    return fail(MLA_ERR_INVALID_ARGUMENT, "%s: null free_pages/free_state/free_state_out", fn);
+  if (B > 0 && (!prev_lens || !ctx_lens || !new_lens || !block_table || !total_lens))
+    return fail(MLA_ERR_INVALID_ARGUMENT,
+                "%s: null prev_lens/ctx_lens/new_lens/block_table/total_lens", fn);
+  const void* words[] = {prev_lens, ctx_lens, new_lens, block_table, free_pages, free_state,
+                         free_state_out, total_lens, seq_lens};
+  for (const void* w : words)
+    if (!aligned(w, 4)) return fail(MLA_ERR_INVALID_ARGUMENT, "%s: misaligned int32 argument", fn);
+  if (!aligned(positions, 8) || !aligned(slots, 8))
+    return fail(MLA_ERR_INVALID_ARGUMENT, "%s: misaligned int64 argument", fn);
+  // no output (the two updated in place included) may touch an input or another output
+  struct Range {
+    const void* p;
+    unsigned long long bytes;
+    bool written;
+  };
+  const unsigned long long b4 = 4ull * B, bn8 = 8ull * B * N;
+  const Range ranges[] = {
+      {prev_lens, b4, false},
+      {ctx_lens, b4, false},
+      {new_lens, b4, false},
+      {free_state, 8, false},
+      {block_table, B > 0 ? 4ull * ((unsigned long long)(B - 1) * bt_stride + max_blocks) : 0, true},
+      {free_pages, 4ull * free_cap, true},
+      {free_state_out, 8, true},
+      {total_lens, b4, true},
+      {seq_lens, b4 * n_ranks, true},
+      {positions, bn8, true},
+      {slots, bn8 * n_ranks, true}};
+  const int nr = (int)(sizeof(ranges) / sizeof(ranges[0]));
+  for (int i = 0; i < nr; ++i)
+    for (int j = 0; j < i; ++j) {
+      const Range &x = ranges[i], &y = ranges[j];
+      if (!x.p || !y.p || x.bytes == 0 || y.bytes == 0 || !(x.written || y.written)) continue;
+      const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+      if (a < b + y.bytes && b < a + x.bytes)
+        return fail(MLA_ERR_INVALID_ARGUMENT, "%s: an output overlaps another argument", fn);
+    }
+  DeviceInfo* dev = nullptr;
+  rc = device_info(&dev);
+  if (rc != MLA_OK) return rc;
+  mla::StepArgs a;
+  a.prev = prev_lens;
+  a.ctx = ctx_lens;
+  a.fresh = new_lens;
+  a.B = B;
+  a.N = N;
+  a.table = block_table;
+  a.bt_stride = bt_stride;
+  a.max_blocks = max_blocks;
+  a.ring = free_pages;
+  a.cap = free_cap;
+  a.state = free_state;
+  a.state_out = free_state_out;
+  a.block_size = block_size;
+  a.cp_size = cp_size;
+  a.cp_rank = cp_rank;
+  a.n_ranks = n_ranks;
+  a.interleave = interleave;
+  a.total = total_lens;
+  a.seq = seq_lens;
+  a.positions = positions;
+  a.slots = slots;
+  a.num_sms = dev->num_sms;
+  a.status = dev->status;
+  cudaError_t e = mla::launch_cp_step_tables(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "%s launch: %s", fn, cudaGetErrorString(e));
+  return ok();
+}
+
+int cp_store_q8(const void* kv_new, const int32_t* ctx_lens, const int32_t* total_lens,
+                const int32_t* block_table, int64_t bt_stride, int max_blocks, int B, int N,
+                int block_size, int cp_size, int cp_rank, int interleave, void* kv_cache,
+                float* kv_scales, int num_blocks, mla_stream_t stream) {
+  const char* fn = "cp_store_q8";
+  int rc = slot_args_check(fn, B, N, block_size, cp_size, cp_rank, interleave, max_blocks,
+                           bt_stride);
+  if (rc != MLA_OK) return rc;
+  if (block_size % MLA_Q8_GROUP != 0)
+    return fail(MLA_ERR_INVALID_ARGUMENT, "%s: block_size (%d) must be a multiple of %d", fn,
+                block_size, MLA_Q8_GROUP);
+  if (num_blocks < 1) return fail(MLA_ERR_INVALID_ARGUMENT, "%s: num_blocks < 1", fn);
+  if ((long long)B * N == 0) return ok();
+  if (!kv_new || !ctx_lens || !total_lens || !block_table || !kv_cache || !kv_scales)
+    return fail(MLA_ERR_INVALID_ARGUMENT,
+                "%s: null kv_new/ctx_lens/total_lens/block_table/kv_cache/kv_scales", fn);
+  if (!aligned(kv_new, 16) || !aligned(kv_cache, 16) || !aligned(ctx_lens, 4) ||
+      !aligned(total_lens, 4) || !aligned(block_table, 4) || !aligned(kv_scales, 4))
+    return fail(MLA_ERR_INVALID_ARGUMENT,
+                "%s: misaligned pointer (kv_new and kv_cache need 16 bytes)", fn);
+  DeviceInfo* dev = nullptr;
+  rc = device_info(&dev);
+  if (rc != MLA_OK) return rc;
+  mla::StoreQ8Args a;
+  a.kv_new = static_cast<const uint16_t*>(kv_new);
+  a.ctx = ctx_lens;
+  a.total = total_lens;
+  a.table = block_table;
+  a.bt_stride = bt_stride;
+  a.max_blocks = max_blocks;
+  a.B = B;
+  a.N = N;
+  a.block_size = block_size;
+  a.cp_size = cp_size;
+  a.cp_rank = cp_rank;
+  a.interleave = interleave;
+  a.cache = static_cast<uint8_t*>(kv_cache);
+  a.scales = kv_scales;
+  a.num_blocks = num_blocks;
+  a.status = dev->status;
+  cudaError_t e = mla::launch_cp_store_q8(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "%s launch: %s", fn, cudaGetErrorString(e));
+  return ok();
+}
+
 int mla_get_device_status(mla_stream_t stream, uint32_t* bits_out) {
   DeviceInfo* dev = nullptr;
   int rc = device_info(&dev);
@@ -381,11 +562,14 @@ int mla_get_device_status(mla_stream_t stream, uint32_t* bits_out) {
     return fail(MLA_ERR_CUDA, "mla_get_device_status: %s", cudaGetErrorString(e));
   if (bits_out) *bits_out = bits;
   if (bits == 0) return ok();
-  return fail(MLA_ERR_DEVICE, "device status 0x%x:%s%s%s%s", bits,
+  return fail(MLA_ERR_DEVICE, "device status 0x%x:%s%s%s%s%s%s%s", bits,
               (bits & MLA_STATUS_BAD_PAGE) ? " bad block_table entry;" : "",
               (bits & MLA_STATUS_SEQ_TOO_LONG) ? " seq_len beyond max_blocks*block_size;" : "",
               (bits & MLA_STATUS_BAD_VBLOCK) ? " virtual block beyond max_blocks;" : "",
-              (bits & MLA_STATUS_WAIT_TIMEOUT) ? " on-chip wait timed out;" : "");
+              (bits & MLA_STATUS_WAIT_TIMEOUT) ? " on-chip wait timed out;" : "",
+              (bits & MLA_STATUS_BAD_SCALE) ? " 8-bit cache scale out of range;" : "",
+              (bits & MLA_STATUS_OUT_OF_PAGES) ? " too few free pages;" : "",
+              (bits & MLA_STATUS_BAD_STEP) ? " length or ring state out of range;" : "");
 }
 
 }  // extern "C"

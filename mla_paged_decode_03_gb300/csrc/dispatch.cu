@@ -18,6 +18,10 @@ size_t decode_workspace_size(int B, int H, int q_len, int num_sms) {
   return a > b ? a : b;
 }
 
+size_t q8_workspace_size(int B, int H, int q_len, int num_sms) {
+  return mma_workspace_size(B, H, q_len, num_sms);
+}
+
 size_t decode_workspace_for(int B, int H, int q_len, int num_sms, int block_size) {
   if (g_choice != 1 && tc_block_size_ok(block_size)) return tc_workspace_size(B, H, q_len, num_sms);
   return mma_workspace_size(B, H, q_len, num_sms);
@@ -25,6 +29,7 @@ size_t decode_workspace_for(int B, int H, int q_len, int num_sms, int block_size
 
 DecodeKernel choose_decode_kernel(const DecodeArgs& a) {
   if (g_choice == 1) return kDecodeMma;
+  if (a.kv_scales != nullptr) return kDecodeMma;
   return tc_supported(a) ? kDecodeTc : kDecodeNone;
 }
 

@@ -11,7 +11,8 @@ namespace mla {
 // Arguments of one mla_decode call after host validation.
 struct DecodeArgs {
   const uint16_t* q;             // bf16 [B*q_len*H, 576]
-  const uint16_t* kv;            // bf16 [num_blocks*block_size, 576]
+  const uint16_t* kv;            // bf16 [num_blocks*block_size, 576] (e4m3 with kv_scales)
+  const float* kv_scales;        // null, or the 8-bit cache's scales [num_blocks, block_size/16]
   const int32_t* block_table;    // [B, bt_stride]
   int64_t bt_stride;
   const int32_t* seq_lens;       // [B]
@@ -37,7 +38,7 @@ struct DecodeArgs {
 
 // Which decode kernel a call runs: the tensor-core (tcgen05) kernel whenever the cache
 // layout allows its TMA tiles; the warp-level MMA kernel only when a test selected it.
-enum DecodeKernel { kDecodeTc, kDecodeMma, kDecodeNone };
+enum DecodeKernel { kDecodeTc, kDecodeMma, kDecodeQ8, kDecodeNone };
 DecodeKernel choose_decode_kernel(const DecodeArgs& a);
 
 // Split-KV decode with the kernel choose_decode_kernel picks (not kDecodeNone).
@@ -56,22 +57,28 @@ void set_rescale_budget_choice(int choice);
 size_t mma_workspace_size(int B, int H, int q_len, int num_sms);
 cudaError_t launch_decode_mma(const DecodeArgs& a, cudaStream_t stream);
 
+// tcgen05 kernel over the 8-bit cache (mla_decode_q8.cu)
+bool q8_supported(const DecodeArgs& a);
+size_t q8_workspace_size(int B, int H, int q_len, int num_sms);
+cudaError_t launch_decode_q8(const DecodeArgs& a, cudaStream_t stream);
+
 // Split-KV scratch the kernel chosen for this block size uses at its preferred split.
 size_t decode_workspace_for(int B, int H, int q_len, int num_sms, int block_size);
 
 // Records a message for mla_last_error() and returns `code` (api.cu).
 int api_fail(int code, const char* fmt, ...);
 
-// Validation and launch behind mla_decode, mla_decode_shards and mla_decode_noalloc
-// (api.cu); `stream` is a cudaStream_t.  With require_full_split the workspace must hold
+// Validation and launch behind mla_decode, mla_decode_shards, mla_decode_noalloc and the
+// decode calls of the 8-bit cache (q8, with kv_scales; api.cu); `stream` is a cudaStream_t.  With require_full_split the workspace must hold
 // the scratch of the full split-KV schedule, else MLA_ERR_UNSUPPORTED (after every other
 // check).
-int decode_entry(const char* fn, const void* q, const void* kv_cache, const int32_t* block_table,
-                 int64_t bt_stride, const int32_t* seq_lens, const int32_t* causal_seqlens_global,
-                 int B, int H, int q_len, int causal, int block_size, int num_blocks,
-                 int max_blocks, int cp_world, int cp_rank, int interleave, int n_shards,
-                 float scale, void* out, float* lse, int lse_base_e, void* workspace,
-                 size_t workspace_bytes, bool require_full_split, struct CUstream_st* stream);
+int decode_entry(const char* fn, const void* q, const void* kv_cache, bool q8,
+                 const float* kv_scales, const int32_t* block_table, int64_t bt_stride,
+                 const int32_t* seq_lens, const int32_t* causal_seqlens_global, int B,
+                 int H, int q_len, int causal, int block_size, int num_blocks, int max_blocks,
+                 int cp_world, int cp_rank, int interleave, int n_shards, float scale, void* out,
+                 float* lse, int lse_base_e, void* workspace, size_t workspace_bytes,
+                 bool require_full_split, struct CUstream_st* stream);
 
 // Testing hook: 0 = automatic choice, 1 = force the warp-level kernel, 2 = force tcgen05.
 void set_decode_kernel_choice(int choice);
@@ -132,5 +139,38 @@ cudaError_t launch_cp_local_slot_scatter(const int64_t* positions, const uint16_
                                          uint16_t* kv_cache, long long num_blocks,
                                          int64_t* slots, unsigned int* status,
                                          cudaStream_t stream);
+
+// A step's tables from request lengths (cp_step_tables.cu).
+struct StepArgs {
+  const int32_t *prev, *ctx, *fresh;     // [B] lengths: last step's, cached, new
+  int B, N;
+  int32_t* table;
+  int64_t bt_stride;
+  int max_blocks;
+  int32_t* ring;
+  int cap;
+  const int32_t* state;
+  int32_t* state_out;
+  int block_size, cp_size, cp_rank, n_ranks, interleave;
+  int32_t *total, *seq;
+  int64_t *positions, *slots;
+  int num_sms;
+  unsigned int* status;
+};
+cudaError_t launch_cp_step_tables(const StepArgs& a, cudaStream_t stream);
+
+// New rows into the 8-bit cache (cp_store_q8.cu).
+struct StoreQ8Args {
+  const uint16_t* kv_new;
+  const int32_t *ctx, *total;
+  const int32_t* table;
+  int64_t bt_stride;
+  int max_blocks, B, N, block_size, cp_size, cp_rank, interleave;
+  uint8_t* cache;
+  float* scales;
+  int num_blocks;
+  unsigned int* status;
+};
+cudaError_t launch_cp_store_q8(const StoreQ8Args& a, cudaStream_t stream);
 
 }  // namespace mla

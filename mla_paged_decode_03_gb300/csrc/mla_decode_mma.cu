@@ -23,10 +23,16 @@
 // softmax runs in registers in base 2; P feeds the PV MMA straight from the S
 // accumulators.  Splits write normalised fp32 partials + base-2 LSE to the workspace and
 // the LSE combine kernel reduces them.
+//
+// The 8-bit cache (template argument kQ8): a row's 576 e4m3 values are converted to bf16
+// (exactly) on the way into the shared-memory tile and the scale of its group of 16 slots
+// goes to s_scale; it multiplies the key's column of S, and of P before P is rounded to bf16.
 #include <math.h>
 #include <stdint.h>
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
 
 #include "internal.h"
 #include "../../include/mla_decode.h"
@@ -46,6 +52,7 @@ constexpr int kMaxSplits = 32;
 struct Params {
   const uint16_t* q;
   const uint16_t* kv;
+  const float* scales;   // 8-bit cache: [num_blocks, bs / 16]
   const int32_t* bt;
   long long bt_stride;
   const int32_t* seq_lens;
@@ -118,8 +125,24 @@ __device__ __forceinline__ int row_bound(const Params& p, int r, long long G, in
   return (int)(loc < cap ? loc : cap);
 }
 
+// 16 e4m3 values as bf16 (exact: 4 significant bits, and bf16's exponents cover e4m3's).
+__device__ __forceinline__ void widen16(const uint4& v, uint4& lo, uint4& hi) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const __nv_fp8x2_storage_t two = (__nv_fp8x2_storage_t)(w[k >> 1] >> (16 * (k & 1)));
+    const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3)));
+    o[k] = pack_bf16(f.x, f.y);
+  }
+  lo = make_uint4(o[0], o[1], o[2], o[3]);
+  hi = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+template <bool kQ8>
 __global__ void __launch_bounds__(kThreads, 1) mla_decode_mma_kernel(const Params p) {
   extern __shared__ __align__(128) uint16_t smem[];
+  __shared__ float s_scale[2][kTok];          // scale of each key of the two tiles (kQ8)
   uint16_t* Qs = smem;                        // [64][kStride]
   uint16_t* Ks = smem + kRows * kStride;      // [2][32][kStride]
 
@@ -160,18 +183,38 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_mma_kernel(const Param
     cp_async16(qs_base + (rr * kStride + ch * 8) * 2, src, ok ? 16 : 0);
   }
 
-  bool bad_page = false;
+  bool bad_page = false, bad_scale = false;
   const int ld_tok = tid >> 3, ld_c0 = tid & 7;
   auto load_tile = [&](int buf, int t0) {
     const int l = t0 + ld_tok;
-    const uint16_t* src = nullptr;
+    long long slot = -1;
     if (l < end) {
       const int page = __ldg(p.bt + (long long)b * p.bt_stride + l / p.bs);
       if (page < 0 || page >= p.num_blocks)
         bad_page = true;
       else
-        src = p.kv + ((long long)page * p.bs + l % p.bs) * kD;
+        slot = (long long)page * p.bs + l % p.bs;
     }
+    if constexpr (kQ8) {
+      uint4* dst = reinterpret_cast<uint4*>(Ks + (buf * kTok + ld_tok) * kStride);
+      const uint4* row = reinterpret_cast<const uint4*>(p.kv) + slot * (kD / 16);
+      for (int ch = ld_c0; ch < kD / 16; ch += 8) {
+        uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+        if (slot >= 0) widen16(__ldg(row + ch), lo, hi);
+        dst[2 * ch] = lo;
+        dst[2 * ch + 1] = hi;
+      }
+      if (ld_c0 == 0) {
+        float sc = slot >= 0 ? __ldg(p.scales + slot / MLA_Q8_GROUP) : 1.f;
+        if (!(sc >= MLA_Q8_SCALE_MIN && sc <= MLA_Q8_SCALE_MAX)) {
+          bad_scale = true;
+          sc = 1.f;
+        }
+        s_scale[buf][ld_tok] = sc;
+      }
+      return;
+    }
+    const uint16_t* src = slot >= 0 ? p.kv + slot * kD : nullptr;
     const uint32_t dst = ks_base + ((buf * kTok + ld_tok) * kStride) * 2;
 #pragma unroll
     for (int k = 0; k < kD / 64; ++k) {
@@ -229,6 +272,12 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_mma_kernel(const Param
 
     // ---- mask + online softmax (base 2) ------------------------------------------
     const int la = limA - t0, lb = limB - t0;
+    if constexpr (kQ8) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[j][e] *= s_scale[it & 1][j * 8 + 2 * c + (e & 1)];
+    }
     float mxA = -INFINITY, mxB = -INFINITY;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -264,6 +313,12 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_mma_kernel(const Param
     }
     lA = lA * alA + sumA;
     lB = lB * alB + sumB;
+    if constexpr (kQ8) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[j][e] *= s_scale[it & 1][j * 8 + 2 * c + (e & 1)];
+    }
 #pragma unroll
     for (int n = 0; n < 32; ++n) {
       acc[n][0] *= alA;
@@ -292,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_decode_mma_kernel(const Param
   }
   cp_async_wait<0>();
   if (bad_page) atomicOr(p.status, MLA_STATUS_BAD_PAGE);
+  if (bad_scale) atomicOr(p.status, MLA_STATUS_BAD_SCALE);
 
   // ---- epilogue ----------------------------------------------------------------------
 #pragma unroll
@@ -371,6 +427,7 @@ cudaError_t launch_decode_mma(const DecodeArgs& a, cudaStream_t stream) {
   Params p;
   p.q = a.q;
   p.kv = a.kv;
+  p.scales = a.kv_scales;
   p.bt = a.block_table;
   p.bt_stride = a.bt_stride;
   p.seq_lens = a.seq_lens;
@@ -406,14 +463,13 @@ cudaError_t launch_decode_mma(const DecodeArgs& a, cudaStream_t stream) {
 
   // the shared-memory attribute is set on every call: this kernel runs only in tests,
   // and the call is cheap and safe from several host threads at once
-  {
-    cudaError_t e = cudaFuncSetAttribute(mla_decode_mma_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    if (e != cudaSuccess) return e;
-  }
+  auto kernel = a.kv_scales != nullptr ? mla_decode_mma_kernel<true> : mla_decode_mma_kernel<false>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return e;
   dim3 grid(splits, (rows + kRows - 1) / kRows, a.B);
-  mla_decode_mma_kernel<<<grid, kThreads, kSmemBytes, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
+  kernel<<<grid, kThreads, kSmemBytes, stream>>>(p);
+  e = cudaGetLastError();
   if (e != cudaSuccess || splits == 1) return e;
   return launch_lse_combine(p.ws_o, true, p.ws_lse, splits, p.total_rows, p.total_rows, true,
                             p.lse_mul, a.out, a.lse, stream);

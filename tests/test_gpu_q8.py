@@ -1,0 +1,706 @@
+"""The 8-bit paged cache on the GPU against its float64 oracle: step tables (exact), the
+quantising store (exact) and the decode, and a serving run of them together.
+
+Tolerance of the decode, per row, head and dim, with w_l = softmax weights, S_l the key's
+scale, v_l the stored e4m3 values, A = sum_l w_l S_l |v_l|, M = max_l w_l S_l:
+  * out is rounded to bf16 once: 2^-8 |out|; the warp-level kernel's splits and the tcgen05
+    kernel's partials are fp32 (no rounding worth counting);
+  * a weight that meets v_l is rounded to bf16 (warp-level kernel: 2^-8) or to an e5m2 value
+    plus an e4m3 remainder: 2^-3 * 2^-4 = 2^-7 of itself, plus, where the remainder is
+    subnormal, half a step, 2^-10, where the row's largest weight times scale is at least
+    2^5 when the reference is set: 2^-15 M, doubled to 2^-14 M:
+    (2^-7) A + 2^-14 M sum_l |v_l|;
+  * scores: q times its row's power of two is the sum of two e4m3 values to within 2^-10 of a
+    row maximum of at least 2^7 (exact above 2^-9 of the maximum): 2^-17 max|q| sum_d |k_d|;
+    the products are exact in fp32 and summed in 36 steps of 32: (31 + 35) u, doubled for
+    truncation: 132 u sum_d |q_d k_d|; base-2 exponent arguments are rounded to fp32 three
+    times (times scale, plus log2 S, minus the reference): 4 u max|s| log2 e and the like,
+    covered by 8 u (|s| + |log2 S| + 64); 2^x by 2^-22.  With delta their sum, weights move by e^{+-delta} against each
+    other, the output by 2 (e^{2 delta} - 1) A, the LSE by delta (+ 1e-6 (1 + |lse|) for its own
+    rounding and log).
+Besides, the norm of the output's error is at most 2^-7 of the output's (roundings are
+independent; each is at most that)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import mla_paged_decode_03_gb300 as M
+import oracle.mla_ref as R
+import oracle.q8_ref as Q
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+SCALE = 1.0 / math.sqrt(192.0)
+BAD_PAGE, TOO_LONG, BAD_VBLOCK, BAD_SCALE, NO_PAGES, BAD_STEP = 1, 2, 4, 16, 32, 64
+
+
+@pytest.fixture(autouse=True)
+def _clean():
+    M.device_status()
+    prev = M.set_decode_kernel(M.KERNEL_AUTO)
+    yield
+    M.set_decode_kernel(prev)
+
+
+@pytest.fixture(params=["mma", "auto"])
+def kernel(request):
+    prev = M.set_decode_kernel(M.KERNEL_MMA if request.param == "mma" else M.KERNEL_AUTO)
+    yield request.param
+    M.set_decode_kernel(prev)
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device=DEV)
+
+
+def n64(t):
+    return t.detach().cpu().to(torch.float64).numpy() if t.is_floating_point() else t.cpu().numpy()
+
+
+# =============================================================================================
+# step tables
+# =============================================================================================
+def check_step(prev, ctx, new, table, ring, state, bs, N, cp, rank, ranks, il, bits=0):
+    d = dict(table=i32(table), ring=i32(ring), state=i32(state))
+    t = M.cp_step_tables(i32(prev), i32(ctx), i32(new), d["table"], d["ring"], d["state"], bs, N,
+                         cp, rank, ranks, il)
+    want = Q.ref_step_tables(prev, ctx, new, table, ring, state, bs, N, cp,
+                             range(rank, rank + ranks), il)
+    got = (t.total_lens, t.seq_lens, t.positions, t.slots, d["table"], d["ring"], t.free_state)
+    for name, g, w in zip(("total", "seq", "positions", "slots", "table", "ring", "state"), got, want):
+        assert np.array_equal(n64(g), w), name
+    assert M.device_status() == bits
+    # a call does not change what it reads: repeated, it gives the same
+    t2 = M.cp_step_tables(i32(prev), i32(ctx), i32(new), d["table"], d["ring"], d["state"], bs, N,
+                          cp, rank, ranks, il, seq_lens=torch.empty_like(t.seq_lens))
+    for a, b in zip(t, t2):
+        assert torch.equal(a, b)
+    assert np.array_equal(n64(d["table"]), want[4]) and np.array_equal(n64(d["ring"]), want[5])
+    assert M.device_status() == bits
+    return want
+
+
+@pytest.mark.parametrize("B,N,bs,cp,il,ranks,supply", [
+    (1, 1, 16, 1, 1, 1, 1.0),
+    (8, 1, 64, 1, 1, 1, 1.0),
+    (5, 4, 16, 2, 2, 2, 0.5),
+    (37, 3, 7, 3, 7, 2, 1.0),          # odd sizes (pages of any size here)
+    (256, 4, 64, 8, 1, 8, 1.0),
+    (300, 1, 16, 4, 16, 1, 0.3),       # more requests than a block scans at once
+    (3, 2500, 16, 2, 1, 2, 1.0),       # more positions than a tile
+    (2, 4096, 64, 1, 64, 1, 0.6),
+    (70, 33, 16, 16, 4, 16, 0.8),
+    (1025, 2, 32, 1, 1, 1, 0.9),
+    (4, 0, 16, 2, 1, 2, 1.0),          # lengths only
+])
+def test_step_tables_over_several_steps(B, N, bs, cp, il, ranks, supply):
+    """A simulated loop: requests grow by up to N, have drafts rejected, finish and start over,
+    with a pool of `supply` of what they need at most."""
+    rng = np.random.default_rng(B * 1000 + N)
+    vbs = bs * cp
+    longest = 3 * N + 5 * vbs
+    width = -(-longest // vbs) + 1
+    cap = max(2, int(B * width * supply)) + 3
+    table = np.full((B, width), -1)
+    ring = rng.permutation(cap)
+    state = (int(rng.integers(cap)), cap)
+    ring = np.roll(ring, state[0])
+    prev = np.zeros(B, np.int64)
+    for step in range(4):
+        ctx = np.maximum(prev - rng.integers(0, 4, B), 0)
+        if step == 0:
+            new = rng.integers(0, N + 1, B)
+        else:
+            new = rng.integers(0, N + 1, B)
+            new[ctx + new > longest] = 0
+        done = rng.random(B) < 0.2
+        ctx[done], new[done] = 0, 0
+        asked = np.cumsum([max(0, -(-int(c + n) // vbs) - -(-int(p) // vbs)) for c, n, p in zip(ctx, new, prev)])
+        short = bool(np.any((asked > state[1]) & (np.diff(asked, prepend=0) > 0)))
+        total, _, _, _, table, ring, state = check_step(
+            prev, ctx, new, table, ring, state, bs, N, cp, cp - ranks if cp > ranks else 0, ranks, il,
+            NO_PAGES if short else 0)
+        held = [int(x) for b in range(B) for x in table[b, :-(-int(total[b]) // vbs)]]
+        free = [int(ring[(int(state[0]) + k) % cap]) for k in range(int(state[1]))]
+        assert sorted(held + free) == list(range(cap))            # no page lost or used twice
+        prev = total
+
+
+def test_step_tables_refuse_a_request_beyond_its_table():
+    table = np.array([[0, 1], [2, -1], [3, -1]])
+    check_step([30, 16, 10], [30, 16, 10], [3, 1, 1], table, [4, 5, 6, 7], (1, 3), 16, 4, 1, 0, 1, 1,
+               TOO_LONG)
+    # the request beyond its table takes no page from those behind it
+    check_step([0, 0], [0, 0], [40, 16], np.full((2, 2), -1), [4, 5], (0, 1), 16, 40, 1, 0, 1, 1, TOO_LONG)
+
+
+def test_step_tables_bad_data_is_flagged_and_bounded():
+    def call(prev, ctx, new, state, ring=(4, 5, 6, 7), N=4, width=2):
+        tab = torch.full((len(prev), width), -1, dtype=torch.int32, device=DEV)
+        r = i32(ring)
+        t = M.cp_step_tables(i32(prev), i32(ctx), i32(new), tab, r, i32(state), 16, N)
+        return t, tab, r
+    # a ring state outside the ring: an empty ring
+    for state in ((-1, 2), (4, 1), (0, 5), (0, -1)):
+        t, tab, r = call([0], [0], [1], state)
+        assert M.device_status() == BAD_STEP | NO_PAGES
+        assert t.total_lens.tolist() == [0] and tab.tolist() == [[-1, -1]] and t.free_state.tolist() == [0, 0]
+    # negative lengths are 0, more than N new tokens N, prev beyond the table the whole table
+    t, tab, _ = call([0, -5], [-3, 0], [2, -1], (0, 4))
+    assert M.device_status() == BAD_STEP and t.total_lens.tolist() == [2, 0]
+    assert tab.tolist() == [[4, -1], [-1, -1]] and t.positions.tolist() == [[0, 1, -1, -1], [-1] * 4]
+    t, _, _ = call([0], [0], [9], (0, 4))
+    assert M.device_status() == BAD_STEP and t.total_lens.tolist() == [4]
+    t, _, r = call([1000], [0], [0], (0, 1))
+    assert M.device_status() == BAD_STEP and t.free_state.tolist() == [0, 3] and r.tolist() == [4, -1, -1, 7]
+    # pages given back to a full ring are dropped
+    t, _, r = call([20], [0], [0], (1, 4))
+    assert M.device_status() == BAD_STEP and t.free_state.tolist() == [1, 4] and r.tolist() == [4, 5, 6, 7]
+    # lengths whose sum passes 31 bits
+    t, _, _ = call([5], [2 ** 31 - 2], [4], (0, 4))
+    assert M.device_status() == TOO_LONG and t.total_lens.tolist() == [5]
+
+
+def test_step_tables_large_lengths():
+    # positions near 2^31 with a virtual block of 2^20: 64-bit slots
+    pages = [2 ** 31 - 1, 2 ** 30]
+    bs, N = 1 << 20, 3
+    table = np.full((1, 2048), -1)
+    table[0, 2046] = pages[0]
+    ctx = 2047 * bs - 2
+    check_step([2047 * bs - 1], [ctx], [3], table, [pages[1], 9], (0, 2), bs, N, 1, 0, 1, 1)
+
+
+def test_step_tables_empty_batch_copies_the_ring_state():
+    e = torch.empty(0, dtype=torch.int32, device=DEV)
+    t = M.cp_step_tables(e, e, e, torch.empty(0, 3, dtype=torch.int32, device=DEV), i32([1, 2, 3]), i32([2, 1]),
+                         16, 4)
+    assert t.free_state.tolist() == [2, 1] and M.device_status() == 0
+
+
+def test_step_tables_strided_table_and_other_stream():
+    wide = torch.full((3, 9), -7, dtype=torch.int32, device=DEV)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    ring, state = i32([3, 4, 5, 6]), i32([0, 4])
+    prev, ctx, new = i32([0, 0, 0]), i32([0, 0, 0]), i32([5, 0, 17])
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        t = M.cp_step_tables(prev, ctx, new, wide[:, 2:5], ring, state, 16, 17)
+    s.synchronize()
+    assert wide[:, 2:5].tolist() == [[3, -7, -7], [-7, -7, -7], [4, 5, -7]]
+    assert (wide[:, :2] == -7).all() and (wide[:, 5:] == -7).all() and t.free_state.tolist() == [3, 1]
+
+
+def test_step_tables_refuses_outputs_over_inputs():
+    a, tab, ring, st = i32([0, 0]), torch.zeros(2, 2, dtype=torch.int32, device=DEV), i32([1, 2]), i32([0, 2])
+    with pytest.raises(M.MlaError):
+        M.cp_step_tables(a, i32([0, 0]), i32([1, 1]), tab, ring, st, 16, 1, total_lens=a)
+    with pytest.raises(M.MlaError):
+        M.cp_step_tables(a, i32([0, 0]), i32([1, 1]), tab, ring, st, 16, 1, free_state_out=st)
+
+
+# =============================================================================================
+# store
+# =============================================================================================
+def f8(x):
+    return torch.tensor(np.asarray(x), dtype=torch.float32, device=DEV).to(torch.float8_e4m3fn)
+
+
+def new_pool(nb, bs, poison=True):
+    """A pool nobody wrote: NaN bytes and NaN scales (or zeros and ones)."""
+    c = torch.full((nb, bs, 576), 0x7f if poison else 0, dtype=torch.uint8, device=DEV)
+    return c.view(torch.float8_e4m3fn), torch.full((nb, bs // 16), float("nan") if poison else 1.0, device=DEV)
+
+
+def random_table(rng, B, pages, num_blocks):
+    return rng.permutation(num_blocks)[:B * pages].reshape(B, pages)
+
+
+def check_store(rows, ctx, total, table, cache, scales, cp, rank, il, bits=0):
+    want_c, want_s = Q.ref_store_q8(n64(rows), ctx, total, table, n64(cache.float()), n64(scales), cp, rank, il)
+    M.cp_store_q8(rows, i32(ctx), i32(total), i32(table), cache, scales, cp, rank, il)
+    assert M.device_status() == bits
+    assert np.array_equal(n64(cache.float()), want_c, equal_nan=True)
+    assert np.array_equal(n64(scales), want_s, equal_nan=True)
+
+
+@pytest.mark.parametrize("B,N,bs,cp,il,top", [
+    (1, 1, 16, 1, 1, 40), (7, 1, 64, 1, 1, 100), (5, 4, 16, 2, 2, 70), (3, 5, 48, 3, 4, 200),
+    (4, 37, 64, 4, 16, 90), (2, 333, 16, 1, 1, 50), (2, 700, 128, 8, 1, 3000), (64, 3, 32, 2, 1, 64),
+    (3, 17, 16, 16, 16, 700),
+])
+def test_store_matches_oracle(B, N, bs, cp, il, top):
+    """Every rank's pool, two stores in a row (the second begins inside blocks the first left
+    partly filled, with rows of very different size)."""
+    rng = np.random.default_rng(N * 100 + bs)
+    g = torch.Generator().manual_seed(B + N)
+    pages = -(-(top + 2 * N) // (bs * cp)) + 1
+    nb = B * pages + 2
+    table = random_table(rng, B, pages, nb)
+    ctx = rng.integers(0, top + 1, B)
+    for rank in range(cp):
+        cache, scales = new_pool(nb, bs, poison=False)
+        cache.view(torch.uint8).copy_(torch.randint(0, 127, (nb, bs, 576), generator=g).to(torch.uint8))
+        at = ctx
+        for _ in range(2):
+            total = at + rng.integers(max(0, N - 3), N + 1, B)
+            rows = torch.randn(B, N, 576, generator=g)
+            rows *= 10.0 ** torch.randint(-3, 3, (B, N, 1), generator=g)
+            check_store(rows.to(torch.bfloat16).to(DEV), at, total, table, cache, scales, cp, rank, il)
+            at = total
+
+
+def test_store_token_by_token_equals_scales_of_the_whole():
+    # rows of falling size: the first sets the scale, so one by one gives what one call gives
+    rows = (torch.randn(1, 40, 576, generator=torch.Generator().manual_seed(3)).clamp(-2, 2)
+            * torch.linspace(8, 1, 40)[None, :, None])
+    rows[0, 0, 0] = rows[0, 16, 0] = rows[0, 32, 0] = 32.0
+    rows = rows.to(torch.bfloat16).to(DEV)
+    table = [[2, 0, 1]]
+    a, sa = new_pool(3, 16)
+    b, sb = new_pool(3, 16)
+    M.cp_store_q8(rows, i32([0]), i32([40]), i32(table), a, sa)
+    for n in range(40):
+        M.cp_store_q8(rows[:, n:n + 1].contiguous(), i32([n]), i32([n + 1]), i32(table), b, sb)
+    assert M.device_status() == 0
+    assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert torch.equal(sa, sb)
+
+
+@pytest.mark.parametrize("values", [
+    [0.0], [float("nan"), 1.0], [float("inf"), -float("inf"), 3.0], [float("nan")], [3.0e38, 1.0],
+    [1e-30, -1e-38], [448.0, 449.0], [1.75, 1.7578125], [2.0 ** -40],
+])
+def test_store_special_values(values):
+    rows = torch.zeros(1, 3, 576, dtype=torch.bfloat16, device=DEV)
+    rows[0, 1, :len(values)] = torch.tensor(values).to(torch.bfloat16).to(DEV)
+    cache, scales = new_pool(2, 16, poison=False)
+    check_store(rows, [0], [3], [[1]], cache, scales, 1, 0, 1)
+    # behind earlier rows
+    rows[0, 0, 3] = 5.0
+    check_store(rows, [3], [6], [[1]], cache, scales, 1, 0, 1)
+
+
+def test_store_keeps_or_grows_any_earlier_scale():
+    rows = torch.full((1, 1, 576), 3.0, dtype=torch.bfloat16, device=DEV)
+    for old in (0.3, 1.0, 1e-4, 7.7e-3, 2.0 ** -32, 2.0 ** 64):
+        cache, scales = new_pool(1, 16, poison=False)
+        cache[0, :5] = f8(np.linspace(-448, 448, 5 * 576).reshape(5, 576))
+        scales.fill_(old)
+        old32 = float(scales[0, 0])
+        new = max(old32, 2.0 ** -7)
+        M.cp_store_q8(rows, i32([5]), i32([6]), i32([[0]]), cache, scales)
+        assert M.device_status() == 0 and float(scales[0, 0]) == new
+        stands = n64(cache[0, :5].float()) * new
+        was = n64(f8(np.linspace(-448, 448, 5 * 576).reshape(5, 576)).float()) * old32
+        # one more rounding: half a step, or half a subnormal step
+        assert np.all(np.abs(stands - was) <= np.maximum(2.0 ** -4 * np.abs(was), 2.0 ** -10 * new) * 1.001)
+        got = n64(cache[0, 5].float()) * new
+        assert np.all(np.abs(got - 3.0) <= max(2.0 ** -4 * 3, 2.0 ** -10 * new) * 1.001)
+    # an earlier scale outside the range is taken as 1
+    for old in (0.0, -1.0, float("nan"), float("inf"), 1e-12):
+        cache, scales = new_pool(1, 16, poison=False)
+        scales.fill_(old)
+        M.cp_store_q8(rows, i32([5]), i32([6]), i32([[0]]), cache, scales)
+        assert M.device_status() == BAD_SCALE and float(scales[0, 0]) == 1.0 and (cache[0, 5].float() == 3).all()
+
+
+def test_store_bad_data_writes_nothing():
+    rows = torch.ones(3, 20, 576, dtype=torch.bfloat16, device=DEV)
+
+    def call(ctx, total, table, bits, N=20):
+        cache, scales = new_pool(4, 16)
+        before = cache.view(torch.uint8).clone()
+        M.cp_store_q8(rows[:len(ctx), :N].contiguous(), i32(ctx), i32(total), i32(table), cache, scales)
+        assert M.device_status() == bits
+        return cache.view(torch.uint8) != before
+    assert not call([0], [16], [[9]], BAD_PAGE).any()
+    assert not call([0], [16], [[-1]], BAD_PAGE).any()
+    w = call([0], [20], [[1]], BAD_VBLOCK)                # the second page is past the table
+    assert w[1].all() and not w[[0, 2, 3]].any()
+    assert not call([-1], [5], [[1]], BAD_STEP).any()
+    w = call([0], [9], [[2]], BAD_STEP, N=4)              # four rows are there, four are stored
+    assert w[2, :4].all() and not w[2, 4:].any()
+    assert not call([5, 7, 3], [5, 6, 0], [[0], [1], [2]], 0).any()   # nothing new
+
+
+def test_store_offsets_beyond_31_bits():
+    """A pool of more than 2^31 bytes: pages behind byte 2^31 and 2^32."""
+    bs = 64
+    nb = (5 << 30) // (bs * 576)
+    cache = torch.zeros(nb, bs, 576, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+    scales = torch.ones(nb, 4, device=DEV)
+    table = i32([[nb - 1], [(3 << 30) // (bs * 576)], [0]])
+    rows = torch.randn(3, 5, 576, generator=torch.Generator().manual_seed(9)).to(torch.bfloat16).to(DEV)
+    M.cp_store_q8(rows, i32([0, 0, 0]), i32([5, 5, 5]), table, cache, scales)
+    assert M.device_status() == 0
+    for b in range(3):
+        pg = int(table[b, 0])
+        got = cache[pg, :5].float() * scales[pg, 0]
+        x = rows[b].float()
+        assert ((got - x).abs() <= 2.0 ** -4 * x.abs() + 2.0 ** -10 * scales[pg, 0]).all()
+    # and the decode reads them there
+    q = torch.randn(3, 1, 16, 576, generator=torch.Generator().manual_seed(10)).to(torch.bfloat16).to(DEV)
+    out, lse = M.mla_decode_q8(q, cache, scales, table, i32([5, 5, 5]), None, 1, 1, 0, SCALE)
+    assert M.device_status() == 0
+    for b in range(3):
+        pg = int(table[b, 0])
+        check_rows(q[b], out[b:b + 1], lse[b:b + 1], n64(cache[pg, :5].float()), n64(scales[pg, :1]).repeat(16)[:5],
+                   [5], True)
+
+
+# =============================================================================================
+# decode
+# =============================================================================================
+def check_rows(q, out, lse, v8, sc, see, base_e):
+    """One request: q [q_len, H, 576], its stored values v8 [n, 576] and each key's scale, see[i]
+    the keys row i sees."""
+    u = 2.0 ** -24
+    worst = 0.0
+    q, out, lse = n64(q), n64(out), n64(lse)
+    err2 = ref2 = 0.0
+    for i, n in enumerate(see):
+        o, l = out[i], lse[i]
+        if n == 0:
+            assert np.all(o == 0) and np.all(np.isneginf(l))
+            continue
+        k = v8[:n] * sc[:n, None]
+        s = SCALE * (q[i] @ k.T)
+        top = s.max(1, keepdims=True)
+        e = np.exp(s - top)
+        z = e.sum(1, keepdims=True)
+        w = e / z
+        ref = w @ k[:, :512]
+        A = w @ np.abs(k[:, :512])
+        ws = w * sc[:n]
+        qmax = np.abs(q[i]).max(1, keepdims=True)
+        ka = np.abs(k)
+        delta = SCALE * (2.0 ** -17 * qmax * ka.sum(1)[None] + 132 * u * (np.abs(q[i]) @ ka.T))
+        delta = (delta + 8 * u * (np.abs(s) + np.abs(np.log2(sc[:n])) + 64) + 2.0 ** -22).max(1)[:, None]
+        bound = (2.0 ** -8 * np.abs(ref) + (2.0 ** -7 + 2 * np.expm1(2 * delta)) * A
+                 + 2.0 ** -14 * ws.max(1)[:, None] * np.abs(v8[:n, :512]).sum(0)[None] + 1e-30)
+        assert np.all(np.isfinite(o))
+        worst = max(worst, float((np.abs(o - ref) / bound).max()))
+        err2 += float(((o - ref) ** 2).sum())
+        ref2 += float((ref ** 2).sum())
+        ref_l = (top + np.log(z))[:, 0] / (1.0 if base_e else math.log(2.0))
+        lb = (delta[:, 0] + 1e-6 * (1 + np.abs(ref_l))) / (1.0 if base_e else math.log(2.0))
+        assert np.all(np.abs(l - ref_l) <= lb), (float((np.abs(l - ref_l) / lb).max()), n)
+    assert worst <= 1.0, worst
+    assert err2 <= 2.0 ** -14 * ref2, math.sqrt(err2 / max(ref2, 1e-300))
+    return worst
+
+
+def make_case(B, H, q_len, G, bs, cp, il, seed, spread=0, width_extra=1, pow2=True):
+    """Queries, and every rank's pool filled by the oracle's store (unwritten slots and their
+    scales NaN).  spread: rows' sizes vary by 2^+-spread."""
+    g = torch.Generator().manual_seed(seed)
+    rng = np.random.default_rng(seed)
+    G = np.asarray(G)
+    pages = -(-int(G.max()) // (bs * cp)) + width_extra
+    nb = B * pages + 1
+    table = random_table(rng, B, pages, nb)
+    q = torch.randn(B, q_len, H, 576, generator=g).to(torch.bfloat16)
+    pools = []
+    for rank in range(cp):
+        cache = np.full((nb, bs, 576), np.nan)
+        scales = np.full((nb, bs // 16), np.nan)
+        for b in range(B):
+            n = int(R.ref_local_len(int(G[b]), cp, rank, il))
+            if n == 0:
+                continue
+            x = torch.randn(n, 576, generator=g).numpy().astype(np.float64)
+            x *= 2.0 ** rng.integers(-spread, spread + 1, (n, 1)) if spread else 1.0
+            ng = -(-n // 16)
+            xp = np.zeros((ng * 16, 576))
+            xp[:n] = x
+            s = np.array([Q.ref_scale(float(np.abs(t).max())) for t in xp.reshape(ng, -1)])
+            if not pow2:
+                s = np.float32(s * rng.uniform(0.7, 1.9, ng)).astype(np.float64)
+            v = Q.ref_e4m3(xp / np.repeat(s, 16)[:, None])
+            for j in range(-(-n // bs)):
+                m = min(bs, n - j * bs)
+                cache[table[b, j], :m] = v[j * bs:j * bs + m]
+                mg = -(-m // 16)
+                scales[table[b, j], :mg] = s[j * bs // 16:j * bs // 16 + mg]
+        pools.append((cache, scales))
+    return q, G, table, pools
+
+
+def gpu_pool(pool):
+    return f8(pool[0]), torch.tensor(pool[1], dtype=torch.float32, device=DEV)
+
+
+def check_request(b, q, out, lse, G, table, pool, q_len, cp, rank, il, causal, base_e):
+    n = int(R.ref_local_len(int(G[b]), cp, rank, il))
+    bs = pool[0].shape[1]
+    pg = table[b, :max(1, -(-n // bs))]
+    v8 = pool[0][pg].reshape(-1, 576)[:n]
+    sc = np.repeat(pool[1][pg].reshape(-1), 16)[:n]
+    pre = R.ref_row_global_prefix(int(G[b]), q_len, causal)
+    see = [min(n, int(R.ref_local_len(int(x), cp, rank, il))) for x in pre] if causal else [n] * q_len
+    T = slice(b * q_len, (b + 1) * q_len)
+    return check_rows(q[b], out[T], lse[T], v8, sc, see, base_e)
+
+
+CASES = [
+    # B, H, q_len, G, bs, cp, il, causal, base_e, spread
+    (2, 16, 3, [37, 130], 16, 1, 1, True, True, 0),
+    (1, 1, 1, [1], 16, 1, 1, True, True, 0),
+    (3, 5, 2, [1, 16, 17], 16, 1, 1, True, False, 2),
+    (4, 16, 4, [3, 1, 2, 4], 32, 1, 1, True, True, 0),        # rows that see no key
+    (2, 64, 1, [127, 129], 64, 1, 1, True, True, 1),
+    (2, 128, 1, [1000, 128], 64, 1, 1, True, True, 0),
+    (2, 128, 4, [900, 257], 64, 2, 1, True, False, 3),
+    (2, 24, 5, [300, 777], 48, 3, 4, True, True, 0),          # 48-slot pages, 120 rows
+    (3, 64, 4, [1100, 64, 7], 64, 2, 1, True, False, 0),
+    (2, 100, 3, [640, 65], 192, 1, 1, True, True, 2),
+    (2, 96, 16, [400, 33], 128, 4, 16, True, True, 0),        # 1,536 rows
+    (2, 16, 8, [700, 129], 32, 8, 2, False, True, 0),         # non-causal
+    (1, 8, 1, [5000], 64, 1, 1, True, True, 4),               # split over many blocks
+    (2, 128, 2, [3000, 1], 64, 16, 1, True, True, 0),         # ranks without a key
+]
+
+
+@pytest.mark.parametrize("B,H,q_len,G,bs,cp,il,causal,base_e,spread", CASES)
+def test_decode_matches_oracle(B, H, q_len, G, bs, cp, il, causal, base_e, spread, kernel):
+    q, G, table, pools = make_case(B, H, q_len, G, bs, cp, il, 700 + H + q_len, spread)
+    worst = 0.0
+    for rank in sorted({0, cp // 2, cp - 1}):
+        cache, scales = gpu_pool(pools[rank])
+        seq = R.ref_local_len(G, cp, rank, il)
+        out = torch.full((B * q_len, H, 512), float("nan"), dtype=torch.bfloat16, device=DEV)
+        lse = torch.full((B * q_len, H), float("nan"), device=DEV)
+        M.mla_decode_q8(q.to(DEV), cache, scales, i32(table), i32(seq), i32(G), q_len, cp, rank, SCALE,
+                        out=out, lse=lse, lse_base_e=base_e, causal=causal, interleave=il)
+        assert M.device_status() == 0
+        for b in range(B):
+            worst = max(worst, check_request(b, q, out, lse, G, table, pools[rank], q_len, cp, rank, il,
+                                             causal, base_e))
+    print(f"[q8] {kernel} B{B} H{H} q{q_len}: bound used {worst:.3f}")
+
+
+@pytest.mark.parametrize("B,H,q_len,G", [(2, 128, 2, [700, 2000]), (3, 16, 1, [100, 1, 515])])
+def test_decode_without_workspace_and_without_lse(B, H, q_len, G):
+    q, G, table, pools = make_case(B, H, q_len, G, 64, 1, 1, 41)
+    cache, scales = gpu_pool(pools[0])
+    none = torch.empty(0, dtype=torch.uint8, device=DEV)
+    args = (q.to(DEV), cache, scales, i32(table), i32(G), None, q_len, 1, 0, SCALE)
+    out, lse = M.mla_decode_q8(*args, workspace=none)
+    for b in range(B):
+        check_request(b, q, out, lse, G, table, pools[0], q_len, 1, 0, 1, True, True)
+    o2, l2 = M.mla_decode_q8(*args, workspace=none, return_lse=False)
+    assert l2 is None and torch.equal(out, o2) and M.device_status() == 0
+
+
+def test_decode_any_scales(kernel):
+    # scales that are no powers of two, from 2^-32 to 2^64
+    q, G, table, pools = make_case(2, 16, 2, [200, 75], 32, 1, 1, 43, spread=3, pow2=False)
+    cache, scales = gpu_pool(pools[0])
+    pool = (pools[0][0], n64(scales))
+    out, lse = M.mla_decode_q8(q.to(DEV), cache, scales, i32(table), i32(G), None, 2, 1, 0, SCALE)
+    assert M.device_status() == 0
+    for b in range(2):
+        check_request(b, q, out, lse, G, table, pool, 2, 1, 0, 1, True, True)
+
+
+def test_decode_zero_blocks_and_growing_scores(kernel):
+    """Blocks of zeros (smallest scale) among ordinary ones, and scores that grow along the
+    context by far more than a weight's 8-bit range."""
+    q, G, table, pools = make_case(1, 32, 2, [900], 64, 1, 1, 44)
+    v, s = pools[0]
+    s[table[0, 3]] = 2.0 ** -32
+    v[table[0, 3]] = 0.0
+    qs = q.double().numpy()[0, 1, 0]
+    for l, x in ((200, 30.0), (500, 80.0), (501, 79.0), (800, 150.0)):   # scores, in log units
+        k = qs * (x / SCALE / float(qs @ qs))
+        pg, sl = table[0, l // 64], l % 64
+        s[pg, sl // 16] = max(s[pg, sl // 16], Q.ref_scale(np.abs(k).max()))
+        v[pg, sl] = Q.ref_e4m3(k / s[pg, sl // 16])
+    cache, scales = gpu_pool((v, s))
+    for ws in (None, torch.empty(0, dtype=torch.uint8, device=DEV)):
+        out, lse = M.mla_decode_q8(q.to(DEV), cache, scales, i32(table), i32(G), None, 2, 1, 0, SCALE, workspace=ws)
+        assert M.device_status() == 0
+        check_request(0, q, out, lse, G, table, (v, s), 2, 1, 0, 1, True, True)
+
+
+def test_decode_queries_of_any_size(kernel):
+    # rows of q from 1e-30 to 1, one of zeros
+    q, G, table, pools = make_case(2, 64, 1, [333, 64], 64, 1, 1, 45)
+    q = q * (10.0 ** torch.linspace(-30, 0, 64))[None, None, :, None]
+    q[:, :, 5] = 0
+    q = q.to(torch.bfloat16)
+    cache, scales = gpu_pool(pools[0])
+    out, lse = M.mla_decode_q8(q.to(DEV), cache, scales, i32(table), i32(G), None, 1, 1, 0, SCALE)
+    for b in range(2):
+        check_request(b, q, out, lse, G, table, pools[0], 1, 1, 0, 1, True, True)
+    assert M.device_status() == 0
+
+
+def test_decode_bad_scale_and_bad_page_are_flagged(kernel):
+    q, G, table, pools = make_case(1, 16, 1, [100], 16, 1, 1, 46)
+    v, s = pools[0]
+    for bad in (0.0, -1.0, float("nan"), float("inf"), 1e-12):
+        s2 = s.copy()
+        s2[table[0, 2]] = bad
+        cache, scales = gpu_pool((v, s2))
+        out, lse = M.mla_decode_q8(q.to(DEV), cache, scales, i32(table), i32(G), None, 1, 1, 0, SCALE)
+        assert M.device_status() == BAD_SCALE
+        s2[table[0, 2]] = 1.0
+        check_request(0, q, out, lse, G, table, (v, s2), 1, 1, 0, 1, True, True)
+    cache, scales = gpu_pool((v, s))
+    for page in (-1, cache.shape[0], 2 ** 31 - 1, -2 ** 31):
+        t2 = table.copy()
+        t2[0, 2] = page
+        out, lse = M.mla_decode_q8(q.to(DEV), cache, scales, i32(t2), i32(G), None, 1, 1, 0, SCALE)
+        assert M.device_status() == BAD_PAGE
+        v2, s2 = v.copy(), s.copy()                       # its keys are read as zeros
+        v2[table[0, 2]], s2[table[0, 2]] = 0.0, 1.0
+        check_request(0, q, out, lse, G, table, (v2, s2), 1, 1, 0, 1, True, True)
+
+
+def test_decode_seq_lens_beyond_the_table_are_clamped(kernel):
+    q, G, table, pools = make_case(1, 16, 1, [64], 16, 1, 1, 47, width_extra=0)
+    cache, scales = gpu_pool(pools[0])
+    out, lse = M.mla_decode_q8(q.to(DEV), cache, scales, i32(table), i32([1000]), i32([1000]), 1, 1, 0, SCALE)
+    assert M.device_status() == TOO_LONG
+    check_request(0, q, out, lse, G, table, pools[0], 1, 1, 0, 1, True, True)
+    out, lse = M.mla_decode_q8(q.to(DEV), cache, scales, i32(table), i32([-5]), i32([64]), 1, 1, 0, SCALE)
+    assert (out == 0).all() and torch.isneginf(lse).all() and M.device_status() == 0
+
+
+@pytest.mark.parametrize("cp,il,causal", [(2, 1, True), (8, 2, True), (3, 1, False)])
+def test_decode_shards_equals_rank_by_rank(cp, il, causal, kernel):
+    B, H, q_len = 3, 64, 2
+    q, G, table, pools = make_case(B, H, q_len, [700, 5, 260], 32, cp, il, 48)
+    nb = pools[0][0].shape[0]
+    cache = torch.cat([gpu_pool(p)[0].view(torch.uint8) for p in pools]).view(torch.float8_e4m3fn)
+    scales = torch.cat([gpu_pool(p)[1] for p in pools])
+    seq = np.concatenate([R.ref_local_len(G, cp, r, il) for r in range(cp)])
+    bt = np.concatenate([table + r * nb for r in range(cp)])
+    out, lse = M.mla_decode_shards_q8(q.to(DEV), cache, scales, i32(bt), i32(seq), i32(G), q_len, cp, SCALE,
+                                      causal=causal, interleave=il)
+    for r in range(cp):
+        for b in range(B):
+            check_request(b, q, out[r], lse[r], G, table, pools[r], q_len, cp, r, il, causal, True)
+    # merged, it is attention over every rank's keys
+    mo, ml = R.ref_lse_merge(n64(out), n64(lse))
+    go = torch.empty(B * q_len, H, device=DEV)
+    go_out, _ = M.lse_merge(out, lse, out_lse=go)
+    assert np.abs(n64(go_out) - mo).max() <= 2.0 ** -8 * np.abs(mo).max() + 1e-6
+    assert np.nanmax(np.abs(n64(go) - ml)) <= 1e-4
+    assert M.device_status() == 0
+
+
+def test_decode_on_a_stream_and_in_a_graph():
+    """Captured with its tables and its store, and replayed with other inputs."""
+    B, H, q_len, bs = 2, 64, 2, 64
+    g = torch.Generator().manual_seed(50)
+    nb = 40
+    cache, scales = new_pool(nb, bs)
+    table = torch.full((B, 16), -1, dtype=torch.int32, device=DEV)
+    ring, state = torch.randperm(nb, generator=g).to(torch.int32).to(DEV), i32([0, nb])
+    prev, ctx, new = i32([0, 0]), i32([0, 0]), i32([2, 2])
+    rows = torch.randn(B, q_len, 576, generator=g).to(torch.bfloat16).to(DEV)
+    q = torch.randn(B, q_len, H, 576, generator=g).to(torch.bfloat16).to(DEV)
+    ws = M.alloc_workspace_q8(B, H, q_len)
+    t = M.cp_step_tables(prev, ctx, new, table, ring, state, bs, q_len)
+    M.cp_store_q8(rows, ctx, t.total_lens, table, cache, scales)
+    M.mla_decode_q8(q, cache, scales, table, t.seq_lens[0], t.total_lens, q_len, 1, 0, SCALE, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        t = M.cp_step_tables(prev, ctx, new, table, ring, state, bs, q_len)
+        M.cp_store_q8(rows, ctx, t.total_lens, table, cache, scales)
+        out, lse = M.mla_decode_q8(q, cache, scales, table, t.seq_lens[0], t.total_lens, q_len, 1, 0, SCALE,
+                                   workspace=ws)
+        prev.copy_(t.total_lens)
+        state.copy_(t.free_state)
+    vc, vs = n64(cache.float()), n64(scales)
+    held = np.zeros(B, np.int64)
+    for step in range(40):
+        n = np.array([2, 1 + step % 2])
+        new.copy_(i32(n))
+        ctx.copy_(i32(held))
+        rows.copy_(torch.randn(B, q_len, 576, generator=g).to(torch.bfloat16))
+        q.copy_(torch.randn(B, q_len, H, 576, generator=g).to(torch.bfloat16))
+        graph.replay()
+        torch.cuda.synchronize()
+        tab = table.cpu().numpy()
+        vc, vs = Q.ref_store_q8(n64(rows), held, held + n, np.maximum(tab, 0), vc, vs, 1, 0)
+        held = held + n
+        assert t.total_lens.tolist() == held.tolist()
+    assert np.array_equal(n64(cache.float()), vc, equal_nan=True)
+    for b in range(B):
+        check_request(b, q.cpu(), out, lse, held, tab, (vc, vs), q_len, 1, 0, 1, True, True)
+    assert M.device_status() == 0
+
+
+def test_decode_is_repeatable_and_leaves_its_inputs():
+    q, G, table, pools = make_case(4, 128, 2, [900, 33, 1500, 400], 64, 1, 1, 51)
+    cache, scales = gpu_pool(pools[0])
+    a = (q.to(DEV), cache, scales, i32(table), i32(G), None, 2, 1, 0, SCALE)
+    ws = M.alloc_workspace_q8(4, 128, 2)
+    before = cache.view(torch.uint8).clone()
+    o1, l1 = M.mla_decode_q8(*a, workspace=ws)
+    ws.fill_(0xff)                                      # whatever the workspace holds
+    for _ in range(5):
+        o2, l2 = M.mla_decode_q8(*a, workspace=ws)
+        assert torch.equal(o1, o2) and torch.equal(l1, l2)
+    assert torch.equal(cache.view(torch.uint8), before) and M.device_status() == 0
+
+
+# =============================================================================================
+# together
+# =============================================================================================
+@pytest.mark.parametrize("cp,il,bs,q_len,H", [(1, 1, 16, 4, 16), (2, 2, 16, 3, 64), (4, 1, 32, 1, 128)])
+def test_serving_run(cp, il, bs, q_len, H):
+    """Prompts, then draft blocks with rejections, a request that finishes and one that takes its
+    place: tables, store and decode on every rank, against oracles fed with the same rows."""
+    B = 3
+    rng = np.random.default_rng(cp * 10 + bs)
+    g = torch.Generator().manual_seed(cp)
+    width, nb = 12, 60
+    table = torch.full((B, width), -1, dtype=torch.int32, device=DEV)
+    ring, state = i32(rng.permutation(nb)), i32([0, nb])
+    pools = [new_pool(nb, bs) for _ in range(cp)]
+    ref = [(n64(c.float()), n64(s)) for c, s in pools]
+    prev = i32([0] * B)
+    held = np.zeros(B, np.int64)
+    for step in range(7):
+        if step == 0:
+            N, new = 50, np.array([50, 17, 1])
+        else:
+            N, new = q_len, np.array([q_len] * B)
+        if step == 4:
+            held[1], new[1] = 0, 0                     # finished
+        if step == 5:
+            new[1] = min(q_len, 2)                     # another one begins
+        ctx = i32(held)
+        t = M.cp_step_tables(prev, ctx, i32(new), table, ring, state, bs, N, cp, 0, cp, il)
+        rows = torch.randn(B, N, 576, generator=g).to(torch.bfloat16)
+        tab = table.cpu().numpy()
+        outs, lses = [], []
+        G = held + new
+        q = torch.randn(B, q_len, H, 576, generator=g).to(torch.bfloat16)
+        for r in range(cp):
+            M.cp_store_q8(rows.to(DEV), ctx, t.total_lens, table, *pools[r], cp, r, il)
+            ref[r] = Q.ref_store_q8(n64(rows), held, G, np.maximum(tab, 0), *ref[r], cp, r, il)
+            assert np.array_equal(n64(pools[r][0].float()), ref[r][0], equal_nan=True)
+            assert np.array_equal(n64(pools[r][1]), ref[r][1], equal_nan=True)
+            o, l = M.mla_decode_q8(q.to(DEV), *pools[r], table, t.seq_lens[r], t.total_lens, q_len, cp, r, SCALE,
+                                   interleave=il)
+            for b in range(B):
+                check_request(b, q, o, l, G, tab, ref[r], q_len, cp, r, il, True, True)
+            outs.append(o)
+            lses.append(l)
+        assert t.total_lens.tolist() == G.tolist()
+        if cp > 1:
+            M.lse_merge(torch.stack(outs), torch.stack(lses))
+        prev, state = t.total_lens, t.free_state
+        held = np.maximum(G - rng.integers(0, 2, B) * (new > 1), 0)    # a draft is rejected
+    assert M.device_status() == 0
