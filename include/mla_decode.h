@@ -333,8 +333,9 @@ int cp_store_q8(const void* kv_new, const int32_t* ctx_lens, const int32_t* tota
  *                that range of a group with a visible key is taken as 1 and sets
  *                MLA_STATUS_BAD_SCALE; scales of other groups are not used.
  *   block_size   a multiple of 16.
- *   q            finite values; a row of q with a NaN or an infinity gives NaN outputs.
- *   ceil(q_len*H/64) <= SMs.
+ *   q            a row (one head of one token) with a NaN or an infinity gives NaN outputs.
+ *   ceil(q_len*H/64) <= SMs; num_blocks*block_size and max_blocks*block_size below
+ *   2^31 - 65536 (else MLA_ERR_UNSUPPORTED).
  *   workspace    scratch for split-KV, sized by mla_decode_q8_workspace_size (for the shards
  *                call with n_shards*B), or NULL / 0: without all of it no request is split.
  * Accuracy: products and sums are fp32; q is used to within 2^-17 of its row's largest

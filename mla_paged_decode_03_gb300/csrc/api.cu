@@ -237,8 +237,8 @@ int decode_entry(const char* fn, const void* q, const void* kv_cache, bool q8,
   const mla::DecodeKernel k = mla::choose_decode_kernel(a);
   if (k == mla::kDecodeNone && q8)
     return fail(MLA_ERR_UNSUPPORTED,
-                "%s: q_len*H = %d rows need at most %d row tiles of 64, and num_blocks*block_size "
-                "must stay below 2^31 - 128",
+                "%s: q_len*H = %d rows may be %d row tiles of 64, and num_blocks*block_size and "
+                "max_blocks*block_size must stay below 2^31 - 65536",
                 fn, q_len * H, dev->num_sms);
   if (k == mla::kDecodeNone)
     return fail(MLA_ERR_UNSUPPORTED,

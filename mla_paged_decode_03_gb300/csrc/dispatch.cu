@@ -18,10 +18,6 @@ size_t decode_workspace_size(int B, int H, int q_len, int num_sms) {
   return a > b ? a : b;
 }
 
-size_t q8_workspace_size(int B, int H, int q_len, int num_sms) {
-  return mma_workspace_size(B, H, q_len, num_sms);
-}
-
 size_t decode_workspace_for(int B, int H, int q_len, int num_sms, int block_size) {
   if (g_choice != 1 && tc_block_size_ok(block_size)) return tc_workspace_size(B, H, q_len, num_sms);
   return mma_workspace_size(B, H, q_len, num_sms);
@@ -29,7 +25,7 @@ size_t decode_workspace_for(int B, int H, int q_len, int num_sms, int block_size
 
 DecodeKernel choose_decode_kernel(const DecodeArgs& a) {
   if (g_choice == 1) return kDecodeMma;
-  if (a.kv_scales != nullptr) return kDecodeMma;
+  if (a.kv_scales != nullptr) return q8_supported(a) ? kDecodeQ8 : kDecodeNone;
   return tc_supported(a) ? kDecodeTc : kDecodeNone;
 }
 
@@ -37,6 +33,7 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream) {
   if (a.B == 0 || a.H * a.q_len == 0) return cudaSuccess;
   const DecodeKernel k = choose_decode_kernel(a);
   if (k == kDecodeTc) return launch_decode_tc(a, stream);
+  if (k == kDecodeQ8) return launch_decode_q8(a, stream);
   if (k != kDecodeMma) return cudaErrorNotSupported;
   if (a.shard_B == a.B) return launch_decode_mma(a, stream);
   // several shards in one call: the warp-level kernel takes them one launch each

@@ -1,0 +1,1251 @@
+// Paged MLA decode over the 8-bit cache on the Blackwell tensor cores (tcgen05 + TMEM + TMA).
+//
+// What it computes: mla_decode's shard-local attention (row bounds and LSE as there: "vLLM PR
+// #52188 (DSpark + DCP)" page, section "关键源码片段"; "vLLM PR #54012" page, section
+// "实现拆解" step 3) with key l = S_l k8_l, k8 the row's 576 e4m3 values and S_l the scale of
+// its group of 16 slots:
+//   t_l = scale S_l <q, k8_l>,  out = sum_l 2^(t'_l - m) S_l v8_l / sum_l 2^(t'_l - m)  (t' in log2).
+//
+// Transposed products.  A unit is kN query rows of one request (32 or 64).  Keys are the
+// M side of both products, query rows the N side:
+//   S^T [128 keys x rows] = K8 [128 x 576] Q^T,   O^T [512 dims x rows] += V8^T [512 x 128] P^T.
+// The tile of 128 keys lies in shared memory once, as TMA brings it (128-byte rows of 128
+// dims, 128-byte swizzle); QK reads it K-major, PV reads the same bytes M-major (the
+// transpose bit of the instruction).  O^T of 64 rows takes 256 tensor-memory columns, so S
+// and O fit one SM and a unit needs no second CTA; the time of both products goes with the
+// number of rows, where rows as M would always pay for 128.
+//
+// 8-bit operands without losing bits.  Both factors of a product must be 8-bit types, and
+// a query or a weight rounded to one e4m3 value would be off by up to 2^-4.  So:
+//   * q, times a power of two that puts its row's maximum in [128, 256), is the sum of two
+//     e4m3 values hi + lo: a bf16 has 8 significant bits, each e4m3 holds 4, and hi's residue
+//     is at most 8 units of q's last place; exact for elements within 2^-9 of the maximum,
+//     off by at most 2^-10 (2^-17 of the maximum) below.  hi and lo are columns of one
+//     product with N = 2 kN (the keys are read once), added when S is read.
+//   * a weight p = S_l 2^(t'_l - m) is an e5m2 value (3 bits, range to 2^-16) plus its residue
+//     in e4m3: off by at most 2^-7 p or 2^-10; two products into the same accumulator.
+// p stays within 2^12 (the residue within e4m3's 448): m is set 2^5 below a tile's largest
+// S_l 2^t'_l and moved only when a tile exceeds 2^12 (then O, l and m move together).
+//
+// Roles (10 warps): warp 0 loads tiles (TMA, four 16 KB chunks of latent dims and one of rope
+// dims each, chunk by chunk as PV frees them), warp 1 issues the products in the order in
+// which their inputs come (the next tile's QK before this tile's PV where its keys are there),
+// warps 2-9 hold one key a lane: they read S^T, scale, mask, exponentiate and write P^T, two
+// warps per 32 keys, each half of the rows; they also prepare Q and write the output.
+//
+// Bounds: few rows by the cache's bytes; 64 rows by shared-memory bandwidth: a tile's
+// QK reads 18 x (4 + 4) KB and its PV 32 x (4 + 2) KB, with TMA's and P's writes 426 KB, 3,330
+// cycles at 128 bytes a cycle, against 2,176 cycles of tensor time and about 3,100 of this
+// SM's share of HBM.
+//
+// Work split, partials and the combine: as in mla_decode_tc.cu (tiles of all requests on one
+// line, equal ranges, units cut between blocks merged by a second kernel), with fp32 partials
+// (a block has at most two: the unit it continues and the unit it does not finish).
+//
+// Safety: every wait is bounded; one that runs out sets the block's abort word, every later
+// wait then returns at once, the softmax warps go through their remaining tiles without
+// waiting (their barriers stay balanced), the other roles leave, copies in flight and
+// issued products are waited for (bounded), and the block frees its tensor memory.
+#include <math.h>
+#include <stdint.h>
+
+#include <functional>
+#include <mutex>
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cudaTypedefs.h>
+
+#include "internal.h"
+#include "sm100.cuh"
+#include "../../include/mla_decode.h"
+
+namespace mla {
+namespace {
+
+using namespace sm100;
+
+constexpr int kD = 576;
+constexpr int kDv = 512;
+constexpr int kTile = 128;                 // keys per tile
+constexpr int kChunkBytes = kTile * 128;   // 128 keys x 128 dims
+constexpr int kRopeBytes = kTile * 64;
+constexpr int kThreads = 320;              // warps 0, 1: loads, products; 2-9: softmax
+// log2 of the largest weight a tile may have, of where a new reference puts a tile's largest,
+// and of the excess that moves a reference when some row's weights pass the first
+constexpr float kTop = 12.f, kPlace = 5.f, kMove = 7.f;
+
+template <int kN>
+struct Cfg {
+  static constexpr int kR = kN / 2;                        // rows per softmax thread
+  static constexpr int kQChunk = 2 * kN * 128;             // hi and lo rows of 128 dims
+  static constexpr int kOffQRope = 4 * kQChunk;
+  static constexpr int kSlots = kN == 64 ? 8 : 9;          // latent chunks in the ring
+  static constexpr int kRopes = kN == 64 ? 1 : 2;
+  static constexpr int kPBufs = kN == 64 ? 1 : 2;
+  static constexpr int kPHalf = kTile * kN;                // hi or lo of P^T
+  static constexpr int kOffK = 2 * kN * kD;
+  static constexpr int kOffRope = kOffK + kSlots * kChunkBytes;
+  static constexpr int kOffP = kOffRope + kRopes * kRopeBytes;
+  static constexpr int kOffBar = kOffP + kPBufs * 2 * kPHalf;
+  static constexpr int kOffRc = kOffBar + 384;             // float4 per 2 rows {a, a, -m, -m}
+  static constexpr int kOffShift = kOffRc + 8 * kN;        // move of m / 1 / l of each row
+  static constexpr int kOffLim = kOffShift + 4 * kN;       // keys each row sees
+  static constexpr int kOffMisc = kOffLim + 4 * kN;        // tmem base, abort, scan result
+  static constexpr int kSmem = kOffMisc + 48 + 1024;       // + alignment slack
+  static constexpr uint32_t kTmemCols = 8 * kN;            // O^T 4 kN, S^T 2 x 2 kN
+  static_assert(kOffK % 1024 == 0 && kOffRope % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms");
+  static_assert(kSmem <= 232448, "shared memory of a block");
+};
+
+enum Bar : int {
+  B_KF = 0,        // [9] latent chunk loaded
+  B_KE = 9,        // [9] its PV done
+  B_RF = 18,       // [2] rope chunk loaded
+  B_RE = 20,       // [2] its QK done
+  B_SF = 22,       // [2] S^T written
+  B_SE = 24,       // [2] S^T read (8 warps)
+  B_PF = 26,       // [2] P^T written (8 warps)
+  B_PE = 28,       // [2] its PV done
+  B_QF = 30,       // the segment's Q written (8 warps)
+  B_DRAIN = 31,    // the MMA warp's last operations
+  B_NEVER = 32,    // never arrived at (tests of the timeout path)
+  B_COUNT = 33
+};
+
+struct Params {
+  const uint16_t* q;
+  const float* scales;
+  const int32_t* bt;
+  long long bt_stride;
+  const int32_t* seq_lens;
+  const int32_t* gseq;
+  int B, H, q_len, bs, num_blocks, max_blocks, rank;
+  int causal, il;
+  long long span;              // cp * il
+  unsigned long long wait_ns;
+  int stall_test;
+  int seg_tiles;               // start-up share of a request on the split line, in tiles
+  int shard_B;
+  unsigned shard_mul;          // as in mla_decode_tc.cu
+  int rows;                    // H * q_len
+  int row_tiles;               // R
+  int units;
+  int groups;                  // G: blocks g*R .. g*R + R-1 take the g-th range of the line
+  int whole_units;             // no workspace: requests go round the groups uncut
+  int box_rows;                // rows per TMA box (a page is whole boxes)
+  FastDiv div_bs;
+  float scale_log2, lse_mul;
+  uint16_t* out;
+  float* lse;
+  long long* hdr;              // [0] = T
+  int2* meta;                  // [units] first / last group of each unit
+  float* ws_lse;               // [2 * blocks][kN] base 2
+  float* ws_o;                 // [2 * blocks][kN][512] normalised
+  unsigned int* status;
+};
+
+// ---- small device helpers ------------------------------------------------------------------
+__device__ __forceinline__ unsigned int fdiv(unsigned int n, const FastDiv& f) {
+  return f.d == 1u ? n : (unsigned int)__umul64hi(f.m, (unsigned long long)n);
+}
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float fast_log2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void f32x2_split(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// Two values as e4m3 / e5m2 bytes (lo in the low byte), to nearest even, saturating.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ uint32_t e5m2x2(float lo, float hi) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E5M2);
+}
+// Named barrier 1 over the softmax warps, alone and with an OR across them.
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ bool soft_or(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 256, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, "
+      "p;\n}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+// kR consecutive 32-bit columns of the warp's 32 lanes.
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[32]) { tmem_ld32(addr, r); }
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+
+// Instruction descriptor of kind::f8f6f4 with an fp32 accumulator; formats 0 = e4m3, 1 = e5m2;
+// mn: both operands are stored M- (N-) major.
+__host__ __device__ constexpr uint32_t idesc_f8(int N, uint32_t b_format, bool mn) {
+  return (1u << 4) | (b_format << 10) | ((mn ? 1u : 0u) << 15) | ((mn ? 1u : 0u) << 16) |
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
+}
+constexpr uint32_t kSwizzle64B = 4, kSwizzle32B = 6;
+
+// kSteps products along K under one election, descriptors 32 bytes apart (K-major rows).
+template <int kSteps>
+__device__ __forceinline__ void qk_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  static_assert(kSteps == 2 || kSteps == 4, "chunks of 64 or 128 dims");
+  if constexpr (kSteps == 4)
+    asm volatile(
+        "{\n .reg .pred p, t, e;\n .reg .b64 x, y;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 t, %5, 0;\n"
+        " elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
+        " add.u64 x, %1, 2; add.u64 y, %2, 2;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, t;\n"
+        " add.u64 x, %1, 4; add.u64 y, %2, 4;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, t;\n"
+        " add.u64 x, %1, 6; add.u64 y, %2, 6;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, t;\n"
+        "}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(1u)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p, t, e;\n .reg .b64 x, y;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 t, %5, 0;\n"
+        " elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
+        " add.u64 x, %1, 2; add.u64 y, %2, 2;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, t;\n"
+        "}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(1u)
+        : "memory");
+}
+
+// One step of 32 keys: the weights' e5m2 part (bh, ih) and their e4m3 part (bl, il).
+__device__ __forceinline__ void pv_mma(uint32_t d, uint64_t a, uint64_t bh, uint64_t bl, uint32_t ih,
+                                       uint32_t il, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, t, e;\n setp.ne.b32 p, %6, 0;\n setp.ne.b32 t, %7, 0;\n"
+      " elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %4, p;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %3, %5, t;\n"
+      "}" ::"r"(d), "l"(a), "l"(bh), "l"(bl), "r"(ih), "r"(il), "r"(acc), "r"(1u)
+      : "memory");
+}
+
+// ---- row bounds and the work split (as in mla_decode_tc.cu, with units of kN rows and tiles
+// of 128 keys) ---------------------------------------------------------------------------------
+__device__ __noinline__ int row_bound(const Params& p, int r, long long G, int cap, int rank) {
+  if (!p.causal) return cap;
+  const int i = r / p.H;
+  long long Gi = G - (p.q_len - 1 - i);
+  if (Gi < 0) Gi = 0;
+  long long rem = Gi % p.span - (long long)rank * p.il;
+  rem = rem < 0 ? 0 : (rem > p.il ? p.il : rem);
+  const long long loc = Gi / p.span * p.il + rem;
+  return (int)(loc < cap ? loc : cap);
+}
+__device__ __forceinline__ int shard_of(const Params& p, int b) {
+  return (int)__umulhi((unsigned)b, p.shard_mul);
+}
+__device__ __forceinline__ int seq_cap(const Params& p, int b) {
+  int cap = __ldg(p.seq_lens + b);
+  const int lim = p.max_blocks * p.bs;
+  if (cap > lim) cap = lim;
+  return cap < 0 ? 0 : cap;
+}
+// Keys that row r of request b sees.
+__device__ __forceinline__ int row_keys(const Params& p, int b, int r) {
+  const int sh = shard_of(p, b);
+  return row_bound(p, r, __ldg(p.gseq + (b - sh * p.shard_B)), seq_cap(p, b), p.rank + sh);
+}
+template <int kN>
+__device__ __forceinline__ int unit_keys(const Params& p, int b, int rt) {
+  return row_keys(p, b, min((rt + 1) * kN, p.rows) - 1);     // its last row sees the most
+}
+template <int kN>
+__device__ __forceinline__ int unit_tiles(const Params& p, int b, int rt) {
+  return (unit_keys<kN>(p, b, rt) + kTile - 1) / kTile;
+}
+template <int kN>
+__device__ __forceinline__ long long req_span(const Params& p, int b) {
+  const int nt = unit_tiles<kN>(p, b, p.row_tiles - 1);
+  return nt > 0 ? (long long)nt + p.seg_tiles : 0;
+}
+__device__ __forceinline__ long long range_start(long long T, int c, int C) { return T * c / C; }
+__device__ __forceinline__ int owner_of(long long x, long long T, int C) {
+  return (int)(((x + 1) * C - 1) / T);
+}
+
+// One block's segments (request, tile range) in order; each role walks its own copy.
+template <int kN>
+struct SegIter {
+  int b, rt, grp;
+  int t_begin, t_end, keys, nt;
+  long long g0, g_end;
+  bool single;                    // the segment covers its whole unit
+
+  __device__ bool set(const Params& p, int tb) {
+    keys = unit_keys<kN>(p, b, rt);
+    nt = (keys + kTile - 1) / kTile;
+    int te = nt;
+    if (!p.whole_units) te = (int)min((long long)te, g_end - g0);
+    if (tb >= te) return false;
+    t_begin = tb;
+    t_end = te;
+    single = tb == 0 && te == nt;
+    return true;
+  }
+  __device__ bool next(const Params& p) {
+    if (p.whole_units) {
+      for (b += p.groups; b < p.B; b += p.groups)
+        if (set(p, 0)) return true;
+      return false;
+    }
+    for (;;) {
+      const long long g = g0 + unit_tiles<kN>(p, b, p.row_tiles - 1) + p.seg_tiles;
+      if (g >= g_end) return false;
+      int nb = b + 1;
+      while (nb < p.B && req_span<kN>(p, nb) == 0) ++nb;
+      if (nb >= p.B) return false;
+      b = nb;
+      g0 = g;
+      if (set(p, 0)) return true;
+    }
+  }
+  // scan: the request that holds the range's first position, and where its tiles begin
+  __device__ bool first(const Params& p, long long T, const int* scan) {
+    grp = blockIdx.x / p.row_tiles;
+    rt = blockIdx.x - grp * p.row_tiles;
+    if (p.whole_units) {
+      g0 = g_end = 0;
+      b = grp - p.groups;
+      return next(p);
+    }
+    const long long a = range_start(T, grp, p.groups), e = range_start(T, grp + 1, p.groups);
+    if (a >= e || scan[0] < 0) return false;
+    b = scan[0];
+    g0 = ((long long)scan[2] << 32) | (unsigned)scan[1];
+    g_end = e;
+    return set(p, a > g0 ? (int)(a - g0) : 0) || next(p);
+  }
+};
+
+struct Ctx {
+  uint32_t base;                 // shared address of the aligned base
+  uint8_t* ptr;
+  volatile int* abort;
+};
+
+template <int kN>
+__device__ __forceinline__ uint32_t bar(const Ctx& s, int i) {
+  return s.base + Cfg<kN>::kOffBar + 8 * i;
+}
+template <int kN>
+__device__ __forceinline__ bool wait(const Ctx& s, int i, uint32_t parity, const Params& p) {
+  return mbar_wait(bar<kN>(s, i), parity, s.abort, p.status, p.wait_ns);
+}
+__device__ __forceinline__ bool warp_all(bool ok) { return __all_sync(0xffffffffu, ok); }
+
+// Largest (or sum) over the warp's 32 lanes of each of kR values: lane j returns value j (kR =
+// 32), lanes 2j and 2j + 1 value j (kR = 16).  Halving exchanges: kR - 1 (+ 1) shuffles.
+template <int kR, bool kMax>
+__device__ __forceinline__ float lane_reduce(float (&v)[kR], int lane) {
+  constexpr int kTopBit = 16;
+#pragma unroll
+  for (int n = kR / 2, bit = kTopBit; n >= 1; n >>= 1, bit >>= 1) {
+    const bool up = (lane & bit) != 0;
+#pragma unroll
+    for (int k = 0; k < n; ++k) {
+      const float give = up ? v[k] : v[k + n];
+      const float keep = up ? v[k + n] : v[k];
+      const float got = __shfl_xor_sync(0xffffffffu, give, bit);
+      v[k] = kMax ? fmaxf(keep, got) : keep + got;
+    }
+  }
+  if (kR == 16) {
+    const float got = __shfl_xor_sync(0xffffffffu, v[0], 1);
+    v[0] = kMax ? fmaxf(v[0], got) : v[0] + got;
+  }
+  return v[0];
+}
+
+// ---------------------------------------------------------------------------------------------
+template <int kN>
+__global__ void __launch_bounds__(kThreads, 1)
+    mla_decode_q8_kernel(const __grid_constant__ CUtensorMap kmap,
+                         const __grid_constant__ CUtensorMap rmap, const Params p) {
+  using C = Cfg<kN>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Ctx s;
+  s.ptr = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  s.base = smem_u32(s.ptr);
+  uint32_t* misc = reinterpret_cast<uint32_t*>(s.ptr + C::kOffMisc);   // [0] tmem base, [1] abort
+  s.abort = reinterpret_cast<volatile int*>(misc + 1);
+  int* s_scan = reinterpret_cast<int*>(misc + 4);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // ---- setup: barriers, tensor memory, schedule scan --------------------------------------------
+  if (tid == 64) {
+    prefetch_tensormap(&kmap);
+    prefetch_tensormap(&rmap);
+  }
+  if (tid == 0) {
+    *s.abort = 0;
+    for (int i = 0; i < B_COUNT; ++i) {
+      const bool by_warps = i == B_SE || i == B_SE + 1 || i == B_PF || i == B_PF + 1 || i == B_QF;
+      mbar_init(bar<kN>(s, i), by_warps ? 8 : 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(s.base + C::kOffMisc, C::kTmemCols);
+    tmem_relinquish();
+  }
+  long long T = 0;
+  {
+    // T = length of the split line; the request that holds this group's first position.  The
+    // per-warp sums use the P buffer, which nothing else touches yet.
+    long long* s_warp = reinterpret_cast<long long*>(s.ptr + C::kOffP);
+    constexpr int kWarps = kThreads / 32;
+    if (tid == 0) s_scan[0] = -1;
+    long long local = 0;
+    for (int b = tid; b < p.B; b += kThreads) local += req_span<kN>(p, b);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) local += __shfl_xor_sync(0xffffffffu, local, o);
+    if (lane == 0) s_warp[warp] = local;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) T += s_warp[w];
+    __syncthreads();
+    if (!p.whole_units && T > 0) {
+      const long long a = range_start(T, blockIdx.x / p.row_tiles, p.groups);
+      long long running = 0;
+      for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+        const int b = b0 + tid;
+        const long long n = b < p.B ? req_span<kN>(p, b) : 0;
+        long long incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += v;
+        }
+        if (lane == 31) s_warp[warp] = incl;
+        __syncthreads();
+        long long before = running, total = 0;
+        for (int w = 0; w < kWarps; ++w) {
+          if (w < warp) before += s_warp[w];
+          total += s_warp[w];
+        }
+        const long long excl = before + incl - n;
+        if (n > 0 && excl <= a && a < excl + n) {
+          const long long first = excl + p.seg_tiles;
+          s_scan[0] = b;
+          s_scan[1] = (int)(first & 0xffffffffLL);
+          s_scan[2] = (int)(first >> 32);
+        }
+        running += total;
+        __syncthreads();
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
+  if (blockIdx.x == 0 && tid == 0 && !p.whole_units) p.hdr[0] = T;
+
+  SegIter<kN> it;
+  if (warp == 0) {
+    // ================= loads: per tile four latent chunks and the rope chunk ====================
+    const int nbox = kTile / p.box_rows;
+    const uint32_t box_lat = (uint32_t)p.box_rows * 128, box_rope = (uint32_t)p.box_rows * 64;
+    bool ok = true, bad = false;
+    int slot = 0, rope = 0;
+    uint32_t kpar = 1, rpar = 1;            // a slot's first use passes at once
+    long long chunks = 0, ropes = 0;
+    if (it.first(p, T, s_scan)) {
+      do {
+        const int32_t* btrow = p.bt + (long long)it.b * p.bt_stride;
+        // cache row of the segment's box i; a missing or invalid page becomes a row past the
+        // cache, which TMA fills with zeros
+        auto row_of = [&](int i) {
+          const int tok = i * p.box_rows;          // below 2^31: see q8_supported
+          int y = p.num_blocks * p.bs;
+          if (tok < it.keys) {
+            const int pg = (int)fdiv((unsigned)tok, p.div_bs);
+            const int page = __ldg(btrow + pg);
+            if (page >= 0 && page < p.num_blocks)
+              y = page * p.bs + (tok - pg * p.bs);
+            else
+              bad = true;
+          }
+          return y;
+        };
+        // lane l holds box i0 + l of the current window, the next window one ahead
+        int i0 = it.t_begin * nbox;
+        int cur = row_of(i0 + lane), nxt = row_of(i0 + 32 + lane);
+        // the owner of a unit's first tile records which groups hold the unit
+        if (lane == 0 && it.t_begin == 0 && !p.whole_units)
+          p.meta[it.b * p.row_tiles + it.rt] = make_int2(it.grp, owner_of(it.g0 + it.nt - 1, T, p.groups));
+        for (int t = it.t_begin; t < it.t_end && ok; ++t) {
+          if (t * nbox >= i0 + 32) {
+            i0 += 32;
+            cur = nxt;
+            nxt = row_of(i0 + 32 + lane);
+          }
+          // lane l < nbox issues the tile's box l
+          const int y = __shfl_sync(0xffffffffu, cur, (t * nbox + lane - i0) & 31);
+          for (int c = 0; c < 4; ++c) {
+            ok = warp_all(wait<kN>(s, B_KE + slot, kpar, p));
+            if (!ok) break;
+            const uint32_t fb = bar<kN>(s, B_KF + slot);
+            if (lane == 0) mbar_arrive_expect_tx(fb, kChunkBytes);
+            __syncwarp();
+            if (lane < nbox)
+              tma_load_2d(s.base + C::kOffK + slot * kChunkBytes + lane * box_lat, &kmap, c * 128, y, fb);
+            ++chunks;
+            if (++slot == C::kSlots) {
+              slot = 0;
+              kpar ^= 1u;
+            }
+          }
+          if (!ok) break;
+          ok = warp_all(wait<kN>(s, B_RE + rope, rpar, p));
+          if (!ok) break;
+          const uint32_t fb = bar<kN>(s, B_RF + rope);
+          if (lane == 0) mbar_arrive_expect_tx(fb, kRopeBytes);
+          __syncwarp();
+          if (lane < nbox)
+            tma_load_2d(s.base + C::kOffRope + rope * kRopeBytes + lane * box_rope, &rmap, kDv, y, fb);
+          ++ropes;
+          if (++rope == C::kRopes) {
+            rope = 0;
+            rpar ^= 1u;
+          }
+        }
+      } while (ok && warp_all(*s.abort == 0) && it.next(p));
+    }
+    if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.status, MLA_STATUS_BAD_PAGE);
+    if (*s.abort && lane == 0) {
+      // loads already issued land before the block exits
+      for (long long m = chunks > C::kSlots ? chunks - C::kSlots : 0; m < chunks; ++m)
+        mbar_wait_drain(bar<kN>(s, B_KF + (int)(m % C::kSlots)), (uint32_t)((m / C::kSlots) & 1));
+      for (long long m = ropes > C::kRopes ? ropes - C::kRopes : 0; m < ropes; ++m)
+        mbar_wait_drain(bar<kN>(s, B_RF + (int)(m % C::kRopes)), (uint32_t)((m / C::kRopes) & 1));
+    }
+  } else if (warp == 1) {
+    // ================= products ==================================================================
+    constexpr uint32_t id_qk = idesc_f8(2 * kN, 0, false);
+    constexpr uint32_t id_hi = idesc_f8(kN, 1, true), id_lo = idesc_f8(kN, 0, true);
+    constexpr uint32_t kPSwizzle = kN == 64 ? kSwizzle64B : kSwizzle32B;
+    bool ok = true;
+    if (p.stall_test) ok = warp_all(wait<kN>(s, B_NEVER, 0, p));
+    long long n_qk = 0, n_pv = 0;           // tiles issued so far, over all segments
+    int kslot = 0, vslot = 0;               // ring slots of the next QK's / PV's first chunk
+    uint32_t kpar = 0;
+    int nseg = 0;
+    if (ok && it.first(p, T, s_scan)) {
+      do {
+        ok = warp_all(wait<kN>(s, B_QF, (uint32_t)(nseg & 1), p));
+        if (!ok) break;
+        ++nseg;
+        const int nt = it.t_end - it.t_begin;
+        int qk = 0, pv = 0;
+        unsigned long long t0 = 0;
+        uint32_t spins = 0;
+        while (ok && pv < nt) {
+          const int g = (int)(n_qk & 1);
+          bool did = false;
+          if (qk < nt && qk - pv < 2) {
+            // the next tile's QK: its rope chunk is loaded last; S^T must have been read
+            const int r = (int)(n_qk % C::kRopes);
+            const bool ready = warp_all(mbar_test(bar<kN>(s, B_RF + r), (uint32_t)((n_qk / C::kRopes) & 1)) &&
+                                        mbar_test(bar<kN>(s, B_SE + g), (uint32_t)(((n_qk >> 1) + 1) & 1)));
+            if (ready) {
+              const uint32_t d = tmem + 4 * kN + g * 2 * kN;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                ok = ok && warp_all(wait<kN>(s, B_KF + kslot, kpar, p));
+                if (!ok) break;
+                tc_fence_after();
+                qk_mma<4>(d, smem_desc(s.base + C::kOffK + kslot * kChunkBytes, 16, 1024, kSwizzle128B),
+                          smem_desc(s.base + c * C::kQChunk, 16, 1024, kSwizzle128B), id_qk, c != 0);
+                if (++kslot == C::kSlots) {
+                  kslot = 0;
+                  kpar ^= 1u;
+                }
+              }
+              if (!ok) break;
+              qk_mma<2>(d, smem_desc(s.base + C::kOffRope + r * kRopeBytes, 16, 512, kSwizzle64B),
+                        smem_desc(s.base + C::kOffQRope, 16, 512, kSwizzle64B), id_qk, 1);
+              mma_commit_warp(bar<kN>(s, B_RE + r));
+              mma_commit_warp(bar<kN>(s, B_SF + g));
+              ++qk;
+              ++n_qk;
+              did = true;
+            }
+          }
+          if (!did && pv < qk) {
+            const int pb = (int)(n_pv % C::kPBufs);
+            if (warp_all(mbar_test(bar<kN>(s, B_PF + pb), (uint32_t)((n_pv / C::kPBufs) & 1)))) {
+              tc_fence_after();
+              const uint32_t pa = s.base + C::kOffP + pb * 2 * C::kPHalf;
+              for (int c = 0; c < 4; ++c) {
+                const uint32_t va = s.base + C::kOffK + vslot * kChunkBytes;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  pv_mma(tmem + c * kN, smem_desc(va + k * 4096, 16, 1024, kSwizzle128B),
+                         smem_desc(pa + k * 32 * kN, 16, 8 * kN, kPSwizzle),
+                         smem_desc(pa + C::kPHalf + k * 32 * kN, 16, 8 * kN, kPSwizzle), id_hi, id_lo,
+                         (pv == 0 && k == 0) ? 0u : 1u);
+                mma_commit_warp(bar<kN>(s, B_KE + vslot));
+                if (++vslot == C::kSlots) vslot = 0;
+              }
+              mma_commit_warp(bar<kN>(s, B_PE + pb));
+              ++pv;
+              ++n_pv;
+              did = true;
+            }
+          }
+          if (did) {
+            spins = 0;
+          } else if ((++spins & 63u) == 0u) {
+            // a bounded wait over whichever input comes next
+            const unsigned long long now = globaltimer();
+            if (spins == 64u) t0 = now;
+            if (warp_all(*s.abort != 0)) {
+              ok = false;
+            } else if (warp_all(now - t0 > p.wait_ns)) {
+              if (lane == 0) {
+                *s.abort = 1;
+                atomicOr(p.status, MLA_STATUS_WAIT_TIMEOUT);
+              }
+              ok = false;
+            }
+          }
+        }
+      } while (ok && warp_all(*s.abort == 0) && it.next(p));
+    }
+    // every operation issued here completes before the block tears down
+    mma_commit_warp(bar<kN>(s, B_DRAIN));
+    mbar_wait_drain(bar<kN>(s, B_DRAIN), 0);
+  } else {
+    // ================= softmax: lane = key, half the rows each ==================================
+    constexpr int kR = C::kR;
+    const int q4 = warp & 3, hr = (warp - 2) >> 2;
+    const int key = q4 * 32 + lane;                // key within the tile, tensor-memory lane
+    const int st = tid - 64;                       // 0..255
+    const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
+    const float4* rc = reinterpret_cast<const float4*>(s.ptr + C::kOffRc) + hr * (kR / 2);
+    float* shift = reinterpret_cast<float*>(s.ptr + C::kOffShift);
+    int* lim = reinterpret_cast<int*>(s.ptr + C::kOffLim);
+    bool bad_scale = false;
+    long long n = 0;
+    if (it.first(p, T, s_scan)) {
+      do {
+        const int row0 = it.rt * kN;
+        // ---- Q: a warp per row, hi and lo written where the products read them ----------------
+        {
+          const int sh = shard_of(p, it.b);
+          const long long qrow = (long long)(it.b - sh * p.shard_B) * p.rows + row0;
+          constexpr int kBatch = 4;
+#pragma unroll 1
+          for (int r0 = (warp - 2) * (kN / 8); r0 < (warp - 1) * (kN / 8); r0 += kBatch) {
+            uint32_t w[kBatch][9];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+              const bool valid = row0 + r0 + j < p.rows;
+              const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + (qrow + r0 + j) * kD);
+#pragma unroll
+              for (int i = 0; i < 9; ++i) w[j][i] = valid ? __ldg(src + lane + 32 * i) : 0u;
+            }
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+              const int r = r0 + j;
+              uint32_t m = 0;
+#pragma unroll
+              for (int i = 0; i < 9; ++i) m = max(m, max(w[j][i] & 0x7fffu, (w[j][i] >> 16) & 0x7fffu));
+              m = __reduce_max_sync(0xffffffffu, m);
+              // 2^up puts the row's maximum in [128, 256) (a maximum below 2^-119 less far up)
+              const int ex = (int)(m >> 7);
+              const int up = min(134 - ex, 126);
+              const float f = __int_as_float((up + 127) << 23);
+              if (lane == 0) {
+                float a = __int_as_float((127 - up) << 23) * p.scale_log2;
+                if (ex == 255) a = __int_as_float(0x7fc00000);        // NaN or infinity: a NaN row
+                float* rcw = reinterpret_cast<float*>(s.ptr + C::kOffRc) + (r >> 1) * 4 + (r & 1);
+                rcw[0] = a;
+                rcw[2] = 0.f;
+                lim[r] = row0 + r < p.rows ? row_keys(p, it.b, row0 + r) : it.keys;
+              }
+#pragma unroll
+              for (int i = 0; i < 9; ++i) {
+                const float x0 = __uint_as_float(w[j][i] << 16) * f;
+                const float x1 = __uint_as_float(w[j][i] & 0xffff0000u) * f;
+                const uint32_t hi = e4m3x2(x0, x1);
+                const float2 h = __half22float2(
+                    __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3)));
+                const uint32_t lo = e4m3x2(x0 - h.x, x1 - h.y);
+                uint32_t at, half;                 // of the hi row; the lo row is kN rows on
+                if (i < 8) {
+                  const int dd = (i & 1) * 64 + 2 * lane;
+                  at = (i >> 1) * C::kQChunk + r * 128 + (((dd >> 4) ^ (r & 7)) << 4) + (dd & 15);
+                  half = kN * 128;
+                } else {
+                  const int dd = 2 * lane;
+                  at = C::kOffQRope + r * 64 + (((dd >> 4) ^ ((r >> 1) & 3)) << 4) + (dd & 15);
+                  half = kN * 64;
+                }
+                *reinterpret_cast<uint16_t*>(s.ptr + at) = (uint16_t)hi;
+                *reinterpret_cast<uint16_t*>(s.ptr + at + half) = (uint16_t)lo;
+              }
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar<kN>(s, B_QF));
+        }
+        soft_sync();                               // row constants and limits
+        const int all_see = row_keys(p, it.b, row0);   // every row sees this many keys
+
+        // ---- scales, two steps ahead: the page of tile t + 2, the scale of tile t + 1 ----------
+        const int32_t* btrow = p.bt + (long long)it.b * p.bt_stride;
+        auto page_of = [&](int t) {
+          const int k = t * kTile + key;
+          return k < it.keys && t < it.t_end ? __ldg(btrow + fdiv((unsigned)k, p.div_bs)) : -1;
+        };
+        auto scale_of = [&](int t, int page) {
+          if (page < 0 || page >= p.num_blocks) return 1.f;
+          const unsigned k = (unsigned)(t * kTile + key);
+          const unsigned off = k - fdiv(k, p.div_bs) * (unsigned)p.bs;
+          return __ldg(p.scales + (long long)page * (p.bs / MLA_Q8_GROUP) + off / MLA_Q8_GROUP);
+        };
+        float sc_next = scale_of(it.t_begin, page_of(it.t_begin));
+        int pg_next = page_of(it.t_begin + 1);
+
+        uint64_t l2[kR / 2];
+#pragma unroll
+        for (int k = 0; k < kR / 2; ++k) l2[k] = 0;
+        for (int t = it.t_begin; t < it.t_end; ++t, ++n) {
+          const int g = (int)(n & 1), pb = (int)(n % C::kPBufs);
+          float sc = sc_next;
+          sc_next = scale_of(t + 1, pg_next);
+          pg_next = page_of(t + 2);
+          if (!(sc >= MLA_Q8_SCALE_MIN && sc <= MLA_Q8_SCALE_MAX)) {
+            bad_scale = true;
+            sc = 1.f;
+          }
+          wait<kN>(s, B_SF + g, (uint32_t)((n >> 1) & 1), p);
+          tc_fence_after();
+          float y[kR];
+          {
+            uint32_t hi[kR], lo[kR];
+            tmem_load(tmem + lane_off + 4 * kN + g * 2 * kN + hr * kR, hi);
+            tmem_load(tmem + lane_off + 4 * kN + g * 2 * kN + kN + hr * kR, lo);
+            tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar<kN>(s, B_SE + g));
+            const uint64_t s2 = f32x2(sc, sc);
+            const float lg = fast_log2(sc);
+            const uint64_t lg2 = f32x2(lg, lg);
+#pragma unroll
+            for (int k = 0; k < kR / 2; ++k) {
+              const float4 c4 = rc[k];
+              const uint64_t acc = add2(f32x2(__uint_as_float(hi[2 * k]), __uint_as_float(hi[2 * k + 1])),
+                                        f32x2(__uint_as_float(lo[2 * k]), __uint_as_float(lo[2 * k + 1])));
+              f32x2_split(fma2(mul2(acc, s2), f32x2(c4.x, c4.y), add2(f32x2(c4.z, c4.w), lg2)), y[2 * k],
+                          y[2 * k + 1]);
+            }
+          }
+          const int k_abs = t * kTile + key;
+          if ((t + 1) * kTile > all_see) {
+            // a key that a row does not see weighs nothing, whatever its slot holds
+            const int4* l4 = reinterpret_cast<const int4*>(lim + hr * kR);
+#pragma unroll
+            for (int k = 0; k < kR / 4; ++k) {
+              const int4 v = l4[k];
+              if (k_abs >= v.x) y[4 * k] = -INFINITY;
+              if (k_abs >= v.y) y[4 * k + 1] = -INFINITY;
+              if (k_abs >= v.z) y[4 * k + 2] = -INFINITY;
+              if (k_abs >= v.w) y[4 * k + 3] = -INFINITY;
+            }
+          }
+          float mx = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < kR; k += 2) mx = fmax3(mx, y[k], y[k + 1]);
+          const bool first = t == it.t_begin;
+          if (soft_or(first || mx > kTop)) {
+            // ---- set or move the references: O must not be written to meanwhile ----------------
+            if (!first) {
+              wait<kN>(s, B_PE + (int)((n - 1) % C::kPBufs), (uint32_t)(((n - 1) / C::kPBufs) & 1), p);
+              tc_fence_after();
+            }
+            float* xm = reinterpret_cast<float*>(s.ptr + C::kOffP + pb * 2 * C::kPHalf);   // [4][kN]
+            {
+              float v[kR];
+#pragma unroll
+              for (int k = 0; k < kR; ++k) v[k] = y[k];
+              const float m = lane_reduce<kR, true>(v, lane);
+              if (kR == 32 || (lane & 1) == 0) xm[q4 * kN + hr * kR + (kR == 32 ? lane : lane >> 1)] = m;
+            }
+            soft_sync();
+            if (st < kN) {
+              const float m = fmaxf(fmaxf(xm[st], xm[kN + st]), fmaxf(xm[2 * kN + st], xm[3 * kN + st]));
+              float* nm = reinterpret_cast<float*>(s.ptr + C::kOffRc) + (st >> 1) * 4 + (st & 1) + 2;
+              float by = 0.f;
+              if (m != -INFINITY && (first || m > kMove)) by = kPlace - m;
+              shift[st] = by;
+              *nm += by;                           // -m
+            }
+            soft_sync();
+            if (!first) {
+              // O^T, columns = rows: this warp's lanes of blocks 2 hr and 2 hr + 1
+              for (int c32 = 0; c32 < 2 * kN / 32; ++c32) {
+                const uint32_t col = (uint32_t)(hr * 2 * kN + c32 * 32);
+                uint32_t v[32];
+                tmem_ld32(tmem + lane_off + col, v);
+                tmem_wait_ld();
+                const float* sh4 = shift + (c32 * 32) % kN;
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                  v[k] = __float_as_uint(__uint_as_float(v[k]) * fast_exp2(sh4[k]));
+                tmem_st32(tmem + lane_off + col, v);
+              }
+              tmem_wait_st();
+              tc_fence_before();
+            }
+#pragma unroll
+            for (int k = 0; k < kR / 2; ++k) {
+              const float2 by = *reinterpret_cast<const float2*>(shift + hr * kR + 2 * k);
+              y[2 * k] += by.x;
+              y[2 * k + 1] += by.y;
+              l2[k] = mul2(l2[k], f32x2(fast_exp2(by.x), fast_exp2(by.y)));
+            }
+          }
+          // ---- weights, their sums over this lane's keys, and their two 8-bit parts --------------
+          uint32_t ph[kR / 4], pl[kR / 4];
+          {
+            const float inv = __frcp_rn(sc);
+            const uint64_t inv2 = f32x2(inv, inv), neg2 = f32x2(-1.f, -1.f);
+#pragma unroll
+            for (int k = 0; k < kR / 4; ++k) {
+              uint32_t h[2], r[2];
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const float e0 = fast_exp2(y[4 * k + 2 * j]), e1 = fast_exp2(y[4 * k + 2 * j + 1]);
+                const uint64_t e2 = f32x2(e0, e1);
+                l2[2 * k + j] = fma2(e2, inv2, l2[2 * k + j]);
+                // rounded to 3 significant bits, and what that leaves
+                const float h0 = __uint_as_float((__float_as_uint(e0) + 0x00100000u) & 0xffe00000u);
+                const float h1 = __uint_as_float((__float_as_uint(e1) + 0x00100000u) & 0xffe00000u);
+                float r0, r1;
+                f32x2_split(fma2(f32x2(h0, h1), neg2, e2), r0, r1);
+                h[j] = e5m2x2(h0, h1);
+                r[j] = e4m3x2(r0, r1);
+              }
+              ph[k] = h[0] | h[1] << 16;
+              pl[k] = r[0] | r[1] << 16;
+            }
+          }
+          wait<kN>(s, B_PE + pb, (uint32_t)(((n / C::kPBufs) + 1) & 1), p);
+          {
+            uint8_t* dst = s.ptr + C::kOffP + pb * 2 * C::kPHalf + key * kN;
+#pragma unroll
+            for (int c = 0; c < kR / 16; ++c) {
+              const int cc = hr * (kR / 16) + c;
+              const int sw = kN == 64 ? cc ^ ((key >> 1) & 3) : cc ^ ((key >> 2) & 1);
+              *reinterpret_cast<uint4*>(dst + 16 * sw) =
+                  make_uint4(ph[4 * c], ph[4 * c + 1], ph[4 * c + 2], ph[4 * c + 3]);
+              *reinterpret_cast<uint4*>(dst + C::kPHalf + 16 * sw) =
+                  make_uint4(pl[4 * c], pl[4 * c + 1], pl[4 * c + 2], pl[4 * c + 3]);
+            }
+          }
+          if (k_abs >= all_see) {
+            // a weight of 0 does not keep a NaN out of O (0 * NaN): behind the request's last key,
+            // where slots may hold anything, this key's values become 0; a key that only some
+            // rows see loses its NaN (the rows that see it have a NaN score, so their whole
+            // output is NaN in any case).  Two of the row's four chunks for each half.
+            const bool gone = k_abs >= it.keys;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int vs = (int)((4 * n + 2 * hr + c) % C::kSlots);
+              uint4* row = reinterpret_cast<uint4*>(s.ptr + C::kOffK + vs * kChunkBytes + key * 128);
+#pragma unroll 1
+              for (int j = 0; j < 8; ++j) {
+                uint4 v = gone ? make_uint4(0, 0, 0, 0) : row[j];
+                v.x &= ~__vcmpeq4(v.x & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                v.y &= ~__vcmpeq4(v.y & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                v.z &= ~__vcmpeq4(v.z & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                v.w &= ~__vcmpeq4(v.w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                row[j] = v;
+              }
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar<kN>(s, B_PF + pb));
+        }
+
+        // ---- the segment's output ---------------------------------------------------------------
+        wait<kN>(s, B_PE + (int)((n - 1) % C::kPBufs), (uint32_t)(((n - 1) / C::kPBufs) & 1), p);
+        tc_fence_after();
+        {
+          float* xs = reinterpret_cast<float*>(s.ptr + C::kOffP);        // [4][kN]
+          float v[kR];
+#pragma unroll
+          for (int k = 0; k < kR / 2; ++k) f32x2_split(l2[k], v[2 * k], v[2 * k + 1]);
+          const float sum = lane_reduce<kR, false>(v, lane);
+          if (kR == 32 || (lane & 1) == 0) xs[q4 * kN + hr * kR + (kR == 32 ? lane : lane >> 1)] = sum;
+          soft_sync();
+          const long long slot = 2ll * blockIdx.x + (it.t_begin == 0 ? 1 : 0);
+          if (st < kN) {
+            const float l = (xs[st] + xs[kN + st]) + (xs[2 * kN + st] + xs[3 * kN + st]);
+            const float nm = (reinterpret_cast<const float*>(s.ptr + C::kOffRc) + (st >> 1) * 4 + (st & 1))[2];
+            shift[st] = l == 0.f ? 0.f : 1.f / l;                         // NaN stays NaN
+            const float lse2 = l == 0.f ? -INFINITY : log2f(l) - nm;
+            if (!it.single) {
+              p.ws_lse[slot * kN + st] = lse2;
+            } else if (p.lse != nullptr && row0 + st < p.rows) {
+              p.lse[(long long)it.b * p.rows + row0 + st] = lse2 * p.lse_mul;
+            }
+          }
+          soft_sync();
+          const int nrow = min(kN, p.rows - row0);
+          for (int c32 = 0; c32 < 2 * kN / 32; ++c32) {
+            const int blk = hr * 2 + c32 * 32 / kN, r0 = (c32 * 32) % kN;
+            uint32_t v2[32];
+            tmem_ld32(tmem + lane_off + (uint32_t)(blk * kN + r0), v2);
+            tmem_wait_ld();
+            const int dim = blk * 128 + key;
+            if (!it.single) {
+              float* dst = p.ws_o + (slot * kN + r0) * kDv + dim;
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (r0 + k < nrow) dst[(long long)k * kDv] = __uint_as_float(v2[k]) * shift[r0 + k];
+            } else {
+              // neighbouring lanes hold neighbouring dims: even lanes store both of row k, odd
+              // lanes both of row k + 1
+              uint16_t* dst = p.out + ((long long)it.b * p.rows + row0 + r0) * kDv + (dim & ~1);
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) {
+                const float a = __uint_as_float(v2[k]) * shift[r0 + k];
+                const float b = __uint_as_float(v2[k + 1]) * shift[r0 + k + 1];
+                const bool odd = lane & 1;
+                const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+                const __nv_bfloat162 h = odd ? __floats2bfloat162_rn(got, b) : __floats2bfloat162_rn(a, got);
+                const int r = k + (odd ? 1 : 0);
+                if (r0 + r < nrow) *reinterpret_cast<__nv_bfloat162*>(dst + (long long)r * kDv) = h;
+              }
+            }
+          }
+          tc_fence_before();
+          soft_sync();                             // shift and the row constants are free again
+        }
+      } while (!soft_or(*s.abort != 0) && it.next(p));
+    }
+    if (__any_sync(0xffffffffu, bad_scale) && lane == 0) atomicOr(p.status, MLA_STATUS_BAD_SCALE);
+  }
+
+  // ---- teardown ----------------------------------------------------------------------------------
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// Merges the partials of units cut between blocks; a unit with no key gets out = 0, lse = -inf.
+// A warp per row, eight rows a block.  The unit's first holder wrote its slot 1, the others,
+// which continue the unit, their slot 0.
+template <int kN>
+__global__ void __launch_bounds__(256) mla_q8_combine_kernel(const Params p) {
+  __shared__ int s_nt;
+  __shared__ int2 s_m;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int kBlocks = kN / 8;
+  const int u = blockIdx.x / kBlocks, rb = blockIdx.x % kBlocks;
+  const int b = u / p.row_tiles, rt = u - b * p.row_tiles;
+  if (threadIdx.x == 0) {
+    if (rt == 0 && rb == 0 && __ldg(p.seq_lens + b) > p.max_blocks * p.bs)
+      atomicOr(p.status, MLA_STATUS_SEQ_TOO_LONG);
+    const int nt = unit_tiles<kN>(p, b, rt);
+    int2 m = make_int2(0, 0);
+    if (nt > 0 && !p.whole_units) {
+      m = p.meta[u];
+      // inside [0, groups) whatever a decode that gave up early left there
+      m.x = min(max(m.x, 0), p.groups - 1);
+      m.y = min(max(m.y, m.x), p.groups - 1);
+    }
+    s_nt = nt;
+    s_m = m;
+  }
+  __syncthreads();
+  const int2 m = s_m;
+  if (s_nt > 0 && m.x == m.y) return;               // one block wrote the result
+  const int lane = threadIdx.x & 31, r = rb * 8 + (threadIdx.x >> 5);
+  const int row = rt * kN + r;
+  if (row >= p.rows) return;
+  const long long grow = (long long)b * p.rows + row;
+  uint16_t* o = p.out + grow * kDv;
+  if (s_nt == 0) {
+    *reinterpret_cast<uint4*>(o + 8 * lane) = make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(o + 256 + 8 * lane) = make_uint4(0, 0, 0, 0);
+    if (p.lse != nullptr && lane == 0) p.lse[grow] = -INFINITY;
+    return;
+  }
+  const long long T = p.hdr[0];
+  auto holds = [&](int g) { return range_start(T, g, p.groups) < range_start(T, g + 1, p.groups); };
+  auto slot_of = [&](int g) { return (2ll * (g * p.row_tiles + rt) + (g == m.x ? 1 : 0)) * kN + r; };
+  float mx = -INFINITY;
+  bool nan = false;
+  for (int g0 = m.x; g0 <= m.y; g0 += 32) {
+    const int g = g0 + lane;
+    if (g <= m.y && holds(g)) {
+      const float l = p.ws_lse[slot_of(g)];
+      nan |= l != l;
+      mx = fmaxf(mx, l);
+    }
+  }
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+  if (__any_sync(0xffffffffu, nan)) mx = __int_as_float(0x7fc00000);
+  float acc[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) acc[k] = 0.f;
+  float wsum = 0.f;
+  if (mx != -INFINITY) {
+    for (int g0 = m.x; g0 <= m.y; g0 += 32) {
+      const int g = g0 + lane;
+      const float wl = g <= m.y && holds(g) ? exp2f(p.ws_lse[slot_of(g)] - mx) : 0.f;
+      const int nh = min(32, m.y - g0 + 1);
+#pragma unroll 2
+      for (int k = 0; k < nh; ++k) {
+        const float w = __shfl_sync(0xffffffffu, wl, k);
+        if (w == 0.f) continue;                     // nothing there, or nothing that counts
+        wsum += w;
+        const float4* src = reinterpret_cast<const float4*>(p.ws_o + slot_of(g0 + k) * kDv);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 v = __ldcs(src + 32 * j + lane);
+          acc[4 * j] = fmaf(w, v.x, acc[4 * j]);
+          acc[4 * j + 1] = fmaf(w, v.y, acc[4 * j + 1]);
+          acc[4 * j + 2] = fmaf(w, v.z, acc[4 * j + 2]);
+          acc[4 * j + 3] = fmaf(w, v.w, acc[4 * j + 3]);
+        }
+      }
+    }
+  }
+  const float inv = mx == -INFINITY ? 0.f : 1.f / wsum;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(acc[4 * j] * inv, acc[4 * j + 1] * inv);
+    const __nv_bfloat162 c = __floats2bfloat162_rn(acc[4 * j + 2] * inv, acc[4 * j + 3] * inv);
+    uint2 w2;
+    w2.x = *reinterpret_cast<const uint32_t*>(&a);
+    w2.y = *reinterpret_cast<const uint32_t*>(&c);
+    *reinterpret_cast<uint2*>(o + 128 * j + 4 * lane) = w2;
+  }
+  if (p.lse != nullptr && lane == 0)
+    p.lse[grow] = mx == -INFINITY ? -INFINITY : (mx + log2f(wsum)) * p.lse_mul;
+}
+
+// ---- host ---------------------------------------------------------------------------------------
+PFN_cuTensorMapEncodeTiled_v12000 lookup_encoder() {
+  cudaDriverEntryPointQueryResult q;
+  void* f = nullptr;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+          cudaSuccess &&
+      q == cudaDriverEntryPointSuccess)
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  return nullptr;
+}
+PFN_cuTensorMapEncodeTiled_v12000 get_encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = lookup_encoder();
+  return fn;
+}
+
+// Rows per unit: 32 where a request has no more (half the tensor and shared-memory time of a
+// tile), else 64.
+int rows_per_unit(int rows) { return rows <= 32 ? 32 : 64; }
+
+size_t ws_bytes(int units, int blocks, int kN) {
+  size_t b = 256;                                                    // header
+  b += ((size_t)units * sizeof(int2) + 255) / 256 * 256;
+  b += (2 * (size_t)blocks * kN * sizeof(float) + 255) / 256 * 256;
+  return b + 2 * (size_t)blocks * kN * kDv * sizeof(float);
+}
+
+struct Q8Device {
+  std::once_flag once;
+  cudaError_t err = cudaSuccess;
+};
+constexpr int kMaxDevices = 64;
+Q8Device g_q8_dev[kMaxDevices];
+
+void device_setup(Q8Device& d) {
+  d.err = cudaFuncSetAttribute(mla_decode_q8_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               Cfg<32>::kSmem);
+  if (d.err == cudaSuccess)
+    d.err = cudaFuncSetAttribute(mla_decode_q8_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Cfg<64>::kSmem);
+}
+
+template <int kN>
+cudaError_t launch(const CUtensorMap& kmap, const CUtensorMap& rmap, const Params& p, int blocks,
+                   cudaStream_t stream) {
+  mla_decode_q8_kernel<kN><<<blocks, kThreads, Cfg<kN>::kSmem, stream>>>(kmap, rmap, p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  DependentLaunch dl(dim3((unsigned)p.units * (kN / 8)), dim3(256), stream);
+  return cudaLaunchKernelEx(&dl.cfg, mla_q8_combine_kernel<kN>, p);
+}
+
+}  // namespace
+
+bool q8_supported(const DecodeArgs& a) {
+  const int rows = a.H * a.q_len, n = rows_per_unit(rows);
+  const long long tiles = (rows + n - 1) / n;
+  if (tiles > a.num_sms) return false;              // a block for every row tile of a request
+  // token and cache row numbers, with the look-ahead of the page window, fit 32 bits
+  if ((long long)a.num_blocks * a.block_size + kTile >= (1LL << 31)) return false;
+  if ((long long)a.max_blocks * a.block_size >= (1LL << 31) - 65536) return false;
+  if (a.B * tiles > 0x7fffffffLL / 8) return false;
+  return get_encoder() != nullptr;
+}
+
+size_t q8_workspace_size(int B, int H, int q_len, int num_sms) {
+  const int n = rows_per_unit(H * q_len);
+  return ws_bytes(B * ((H * q_len + n - 1) / n), num_sms, n);
+}
+
+cudaError_t launch_decode_q8(const DecodeArgs& a, cudaStream_t stream) {
+  Params p;
+  p.q = a.q;
+  p.scales = a.kv_scales;
+  p.bt = a.block_table;
+  p.bt_stride = a.bt_stride;
+  p.seq_lens = a.seq_lens;
+  p.gseq = a.gseq;
+  p.B = a.B;
+  p.H = a.H;
+  p.q_len = a.q_len;
+  p.bs = a.block_size;
+  p.num_blocks = a.num_blocks;
+  p.max_blocks = a.max_blocks;
+  p.rank = a.cp_rank;
+  p.causal = a.causal ? 1 : 0;
+  p.il = a.interleave;
+  p.span = (long long)a.cp_world * a.interleave;
+  p.wait_ns = a.wait_ns;
+  p.stall_test = a.stall_test;
+  p.shard_B = a.shard_B;
+  p.shard_mul = a.shard_B == a.B ? 0u
+                                 : (unsigned)((0x100000000ull + (unsigned long long)a.shard_B - 1) /
+                                              (unsigned long long)a.shard_B);
+  p.rows = a.H * a.q_len;
+  const int n = rows_per_unit(p.rows);
+  p.row_tiles = (p.rows + n - 1) / n;
+  p.units = a.B * p.row_tiles;
+  p.box_rows = a.block_size % 128 == 0 ? 128 : a.block_size % 64 == 0 ? 64 : a.block_size % 32 == 0 ? 32 : 16;
+  p.div_bs = make_fastdiv((unsigned)a.block_size);
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.lse_mul = a.lse_base_e ? 0.6931471805599453f : 1.0f;
+  p.out = a.out;
+  p.lse = a.lse;
+  p.status = a.status;
+  p.seg_tiles = 3;
+
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  Q8Device& qd = g_q8_dev[dev];
+  std::call_once(qd.once, device_setup, std::ref(qd));
+  if (qd.err != cudaSuccess) return qd.err;
+
+  p.groups = a.num_sms / p.row_tiles;
+  if (a.workspace != nullptr && a.workspace_bytes >= ws_bytes(p.units, a.num_sms, n)) {
+    char* ws = static_cast<char*>(a.workspace);
+    p.hdr = reinterpret_cast<long long*>(ws);
+    ws += 256;
+    p.meta = reinterpret_cast<int2*>(ws);
+    ws += ((size_t)p.units * sizeof(int2) + 255) / 256 * 256;
+    p.ws_lse = reinterpret_cast<float*>(ws);
+    ws += (2 * (size_t)a.num_sms * n * sizeof(float) + 255) / 256 * 256;
+    p.ws_o = reinterpret_cast<float*>(ws);
+    p.whole_units = 0;
+  } else {
+    p.hdr = nullptr;
+    p.meta = nullptr;
+    p.ws_lse = nullptr;
+    p.ws_o = nullptr;
+    p.whole_units = 1;
+    if (p.groups > a.B) p.groups = a.B;
+  }
+  const int blocks = p.groups * p.row_tiles;
+
+  // the cache as rows of 576 bytes: boxes of 128 latent bytes (x = 0, 128, 256, 384; 128-byte
+  // swizzle) and of the 64 rope bytes (x = 512; 64-byte swizzle)
+  CUtensorMap kmap, rmap;
+  cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)a.num_blocks * a.block_size};
+  cuuint64_t strides[1] = {(cuuint64_t)kD};
+  cuuint32_t es[2] = {1, 1};
+  for (int i = 0; i < 2; ++i) {
+    cuuint32_t box[2] = {i == 0 ? 128u : 64u, (cuuint32_t)p.box_rows};
+    const CUresult r = get_encoder()(
+        i == 0 ? &kmap : &rmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint16_t*>(a.kv), dims, strides,
+        box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+        i == 0 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
+  }
+  return n == 32 ? launch<32>(kmap, rmap, p, blocks, stream) : launch<64>(kmap, rmap, p, blocks, stream);
+}
+
+}  // namespace mla

@@ -541,6 +541,57 @@ def test_decode_queries_of_any_size(kernel):
     assert M.device_status() == 0
 
 
+def test_decode_nan_rows_and_nan_keys():
+    """A NaN or an infinity in a row of q makes that row NaN, and only it; a NaN in a stored key
+    makes the rows that see the key NaN, and only them."""
+    for B, H, q_len, G in ((2, 64, 1, [333, 64]), (1, 16, 2, [4000])):
+        q, G, table, pools = make_case(B, H, q_len, G, 64, 1, 1, 52)
+        cache, scales = gpu_pool(pools[0])
+        args = (cache, scales, i32(table), i32(G), None, q_len, 1, 0, SCALE)
+        out, lse = M.mla_decode_q8(q.to(DEV), *args)
+        bad = q.clone()
+        bad[0, 0, 7, 100] = float("nan")
+        bad[0, 0, 9, 3] = -float("inf")
+        o2, l2 = M.mla_decode_q8(bad.to(DEV), *args)
+        hit = torch.zeros(B * q_len, H, dtype=torch.bool, device=DEV)
+        hit[0, [7, 9]] = True
+        assert torch.isnan(o2[hit]).all() and torch.isnan(l2[hit]).all()
+        assert torch.equal(o2[~hit], out[~hit]) and torch.equal(l2[~hit], lse[~hit])
+    # draft rows: the last key is NaN, which only the last row sees
+    for G in (100, 128, 129, 700):
+        q, Gs, table, pools = make_case(1, 16, 4, [G], 32, 1, 1, 53)
+        v, s = pools[0]
+        v[table[0, (G - 1) // 32], (G - 1) % 32, 5:576:70] = np.nan
+        cache, scales = gpu_pool((v, s))
+        out, lse = M.mla_decode_q8(q.to(DEV), cache, scales, i32(table), i32(Gs), None, 4, 1, 0, SCALE)
+        assert torch.isnan(out[3]).all() and torch.isnan(lse[3]).all()
+        pre = np.concatenate([v[table[0, j]] for j in range(-(-G // 32))])[:G - 1]
+        sc = np.concatenate([np.repeat(s[table[0, j]], 16) for j in range(-(-G // 32))])[:G - 1]
+        check_rows(q[0, :3], out[:3], lse[:3], pre, sc, [G - 3, G - 2, G - 1], True)
+    assert M.device_status() == 0
+
+
+def test_decode_timeout_reports_and_recovers():
+    """One role of every block first waits for an arrival that never comes, with a limit of 200 us:
+    the call returns, reports it, and the next call is right."""
+    q, G, table, pools = make_case(2, 128, 2, [3000, 200], 64, 1, 1, 54)
+    cache, scales = gpu_pool(pools[0])
+    args = (q.to(DEV), cache, scales, i32(table), i32(G), None, 2, 1, 0, SCALE)
+    prev, stall = M.set_wait_limit_ns(200_000), M.set_test_stall(True)
+    try:
+        M.mla_decode_q8(*args)
+        torch.cuda.synchronize()
+        bits = M.device_status()
+    finally:
+        M.set_test_stall(stall)
+        M.set_wait_limit_ns(prev)
+    assert bits == 8, f"{bits:#x}"
+    out, lse = M.mla_decode_q8(*args)
+    assert M.device_status() == 0
+    for b in range(2):
+        check_request(b, q, out, lse, G, table, pools[0], 2, 1, 0, 1, True, True)
+
+
 def test_decode_bad_scale_and_bad_page_are_flagged(kernel):
     q, G, table, pools = make_case(1, 16, 1, [100], 16, 1, 1, 46)
     v, s = pools[0]
