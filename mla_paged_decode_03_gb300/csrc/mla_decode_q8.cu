@@ -27,11 +27,12 @@
 // p stays within 2^12 (the residue within e4m3's 448): m is set 2^5 below a tile's largest
 // S_l 2^t'_l and moved only when a tile exceeds 2^12 (then O, l and m move together).
 //
-// Roles (10 warps): warp 0 loads tiles (TMA, four 16 KB chunks of latent dims and one of rope
-// dims each, chunk by chunk as PV frees them), warp 1 issues the products in the order in
-// which their inputs come (the next tile's QK before this tile's PV where its keys are there),
-// warps 2-9 hold one key a lane: they read S^T, scale, mask, exponentiate and write P^T, two
-// warps per 32 keys, each half of the rows; they also prepare Q and write the output.
+// Roles (20 warps, 12 for 32 rows): warp 0 loads tiles (TMA, four 16 KB chunks of latent dims
+// and one of rope dims each, chunk by chunk as PV frees them), warp 1 issues the QK products and
+// warp 2 the PV products, each when its inputs have come (one warp for both in a fixed order
+// waits for the later of two inputs; one that polls both takes issue slots from the softmax
+// warps of its scheduler), warp 3 only fills its group, the others hold one key a lane and 16 rows a thread: they read S^T, scale, mask, exponentiate
+// and write P^T; they also prepare Q and write the output.
 //
 // Bounds: few rows by the cache's bytes; 64 rows by shared-memory bandwidth: a tile's
 // QK reads 18 x (4 + 4) KB and its PV 32 x (4 + 2) KB, with TMA's and P's writes 426 KB, 3,330
@@ -72,14 +73,15 @@ constexpr int kDv = 512;
 constexpr int kTile = 128;                 // keys per tile
 constexpr int kChunkBytes = kTile * 128;   // 128 keys x 128 dims
 constexpr int kRopeBytes = kTile * 64;
-constexpr int kThreads = 320;              // warps 0, 1: loads, products; 2-9: softmax
+constexpr int kR = 16;                     // query rows per softmax thread
 // log2 of the largest weight a tile may have, of where a new reference puts a tile's largest,
 // and of the excess that moves a reference when some row's weights pass the first
 constexpr float kTop = 12.f, kPlace = 5.f, kMove = 7.f;
 
 template <int kN>
 struct Cfg {
-  static constexpr int kR = kN / 2;                        // rows per softmax thread
+  static constexpr int kSoftWarps = 4 * (kN / kR);         // 4 x 32 keys, kR rows each
+  static constexpr int kThreads = 128 + 32 * kSoftWarps;   // warps 0-2: loads, QK, PV
   static constexpr int kQChunk = 2 * kN * 128;             // hi and lo rows of 128 dims
   static constexpr int kOffQRope = 4 * kQChunk;
   static constexpr int kSlots = kN == 64 ? 8 : 9;          // latent chunks in the ring
@@ -106,13 +108,13 @@ enum Bar : int {
   B_RF = 18,       // [2] rope chunk loaded
   B_RE = 20,       // [2] its QK done
   B_SF = 22,       // [2] S^T written
-  B_SE = 24,       // [2] S^T read (8 warps)
-  B_PF = 26,       // [2] P^T written (8 warps)
+  B_SE = 24,       // [2] S^T read (the softmax warps)
+  B_PF = 26,       // [2] P^T written (the softmax warps)
   B_PE = 28,       // [2] its PV done
-  B_QF = 30,       // the segment's Q written (8 warps)
-  B_DRAIN = 31,    // the MMA warp's last operations
-  B_NEVER = 32,    // never arrived at (tests of the timeout path)
-  B_COUNT = 33
+  B_QF = 30,       // the segment's Q written (the softmax warps)
+  B_DRAIN = 31,    // [2] the QK / PV warp's last operations
+  B_NEVER = 33,    // never arrived at (tests of the timeout path)
+  B_COUNT = 34
 };
 
 struct Params {
@@ -197,30 +199,22 @@ __device__ __forceinline__ uint32_t e5m2x2(float lo, float hi) {
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E5M2);
 }
 // Named barrier 1 over the softmax warps, alone and with an OR across them.
-__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+template <int kN>
+__device__ __forceinline__ void soft_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * Cfg<kN>::kSoftWarps) : "memory");
+}
+template <int kN>
 __device__ __forceinline__ bool soft_or(bool v) {
   uint32_t r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 256, p;\n"
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, %2, p;\n"
       " selp.u32 %0, 1, 0, q;\n}"
       : "=r"(r)
-      : "r"((uint32_t)v)
+      : "r"((uint32_t)v), "n"(32 * Cfg<kN>::kSoftWarps)
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, "
-      "p;\n}"
-      : "=r"(done)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-
-// kR consecutive 32-bit columns of the warp's 32 lanes.
-__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[32]) { tmem_ld32(addr, r); }
+// 16 consecutive 32-bit columns of the warp's 32 lanes.
 __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
@@ -390,13 +384,12 @@ __device__ __forceinline__ bool wait(const Ctx& s, int i, uint32_t parity, const
 }
 __device__ __forceinline__ bool warp_all(bool ok) { return __all_sync(0xffffffffu, ok); }
 
-// Largest (or sum) over the warp's 32 lanes of each of kR values: lane j returns value j (kR =
-// 32), lanes 2j and 2j + 1 value j (kR = 16).  Halving exchanges: kR - 1 (+ 1) shuffles.
-template <int kR, bool kMax>
+// Largest (or sum) over the warp's 32 lanes of each of 16 values: lanes 2j and 2j + 1 return
+// value j.  Halving exchanges, 16 shuffles in all.
+template <bool kMax>
 __device__ __forceinline__ float lane_reduce(float (&v)[kR], int lane) {
-  constexpr int kTopBit = 16;
 #pragma unroll
-  for (int n = kR / 2, bit = kTopBit; n >= 1; n >>= 1, bit >>= 1) {
+  for (int n = kR / 2, bit = 16; n >= 1; n >>= 1, bit >>= 1) {
     const bool up = (lane & bit) != 0;
 #pragma unroll
     for (int k = 0; k < n; ++k) {
@@ -406,16 +399,13 @@ __device__ __forceinline__ float lane_reduce(float (&v)[kR], int lane) {
       v[k] = kMax ? fmaxf(keep, got) : keep + got;
     }
   }
-  if (kR == 16) {
-    const float got = __shfl_xor_sync(0xffffffffu, v[0], 1);
-    v[0] = kMax ? fmaxf(v[0], got) : v[0] + got;
-  }
-  return v[0];
+  const float got = __shfl_xor_sync(0xffffffffu, v[0], 1);
+  return kMax ? fmaxf(v[0], got) : v[0] + got;
 }
 
 // ---------------------------------------------------------------------------------------------
 template <int kN>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
     mla_decode_q8_kernel(const __grid_constant__ CUtensorMap kmap,
                          const __grid_constant__ CUtensorMap rmap, const Params p) {
   using C = Cfg<kN>;
@@ -438,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     *s.abort = 0;
     for (int i = 0; i < B_COUNT; ++i) {
       const bool by_warps = i == B_SE || i == B_SE + 1 || i == B_PF || i == B_PF + 1 || i == B_QF;
-      mbar_init(bar<kN>(s, i), by_warps ? 8 : 1);
+      mbar_init(bar<kN>(s, i), by_warps ? C::kSoftWarps : 1);
     }
     fence_mbar_init();
   }
@@ -451,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // T = length of the split line; the request that holds this group's first position.  The
     // per-warp sums use the P buffer, which nothing else touches yet.
     long long* s_warp = reinterpret_cast<long long*>(s.ptr + C::kOffP);
-    constexpr int kWarps = kThreads / 32;
+    constexpr int kThreads = C::kThreads, kWarps = kThreads / 32;
     if (tid == 0) s_scan[0] = -1;
     long long local = 0;
     for (int b = tid; b < p.B; b += kThreads) local += req_span<kN>(p, b);
@@ -578,107 +568,84 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait_drain(bar<kN>(s, B_RF + (int)(m % C::kRopes)), (uint32_t)((m / C::kRopes) & 1));
     }
   } else if (warp == 1) {
-    // ================= products ==================================================================
+    // ================= QK ========================================================================
     constexpr uint32_t id_qk = idesc_f8(2 * kN, 0, false);
-    constexpr uint32_t id_hi = idesc_f8(kN, 1, true), id_lo = idesc_f8(kN, 0, true);
-    constexpr uint32_t kPSwizzle = kN == 64 ? kSwizzle64B : kSwizzle32B;
     bool ok = true;
     if (p.stall_test) ok = warp_all(wait<kN>(s, B_NEVER, 0, p));
-    long long n_qk = 0, n_pv = 0;           // tiles issued so far, over all segments
-    int kslot = 0, vslot = 0;               // ring slots of the next QK's / PV's first chunk
-    uint32_t kpar = 0;
-    int nseg = 0;
+    long long n = 0;
+    int slot = 0, nseg = 0;
+    uint32_t par = 0;
     if (ok && it.first(p, T, s_scan)) {
       do {
         ok = warp_all(wait<kN>(s, B_QF, (uint32_t)(nseg & 1), p));
-        if (!ok) break;
         ++nseg;
-        const int nt = it.t_end - it.t_begin;
-        int qk = 0, pv = 0;
-        unsigned long long t0 = 0;
-        uint32_t spins = 0;
-        while (ok && pv < nt) {
-          const int g = (int)(n_qk & 1);
-          bool did = false;
-          if (qk < nt && qk - pv < 2) {
-            // the next tile's QK: its rope chunk is loaded last; S^T must have been read
-            const int r = (int)(n_qk % C::kRopes);
-            const bool ready = warp_all(mbar_test(bar<kN>(s, B_RF + r), (uint32_t)((n_qk / C::kRopes) & 1)) &&
-                                        mbar_test(bar<kN>(s, B_SE + g), (uint32_t)(((n_qk >> 1) + 1) & 1)));
-            if (ready) {
-              const uint32_t d = tmem + 4 * kN + g * 2 * kN;
+        for (int t = it.t_begin; t < it.t_end && ok; ++t, ++n) {
+          const int g = (int)(n & 1), r = (int)(n % C::kRopes);
+          ok = warp_all(wait<kN>(s, B_SE + g, (uint32_t)(((n >> 1) + 1) & 1), p));   // S^T read
+          const uint32_t d = tmem + 4 * kN + g * 2 * kN;
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                ok = ok && warp_all(wait<kN>(s, B_KF + kslot, kpar, p));
-                if (!ok) break;
-                tc_fence_after();
-                qk_mma<4>(d, smem_desc(s.base + C::kOffK + kslot * kChunkBytes, 16, 1024, kSwizzle128B),
-                          smem_desc(s.base + c * C::kQChunk, 16, 1024, kSwizzle128B), id_qk, c != 0);
-                if (++kslot == C::kSlots) {
-                  kslot = 0;
-                  kpar ^= 1u;
-                }
-              }
-              if (!ok) break;
-              qk_mma<2>(d, smem_desc(s.base + C::kOffRope + r * kRopeBytes, 16, 512, kSwizzle64B),
-                        smem_desc(s.base + C::kOffQRope, 16, 512, kSwizzle64B), id_qk, 1);
-              mma_commit_warp(bar<kN>(s, B_RE + r));
-              mma_commit_warp(bar<kN>(s, B_SF + g));
-              ++qk;
-              ++n_qk;
-              did = true;
+          for (int c = 0; c < 4; ++c) {
+            ok = ok && warp_all(wait<kN>(s, B_KF + slot, par, p));
+            if (!ok) break;
+            tc_fence_after();
+            qk_mma<4>(d, smem_desc(s.base + C::kOffK + slot * kChunkBytes, 16, 1024, kSwizzle128B),
+                      smem_desc(s.base + c * C::kQChunk, 16, 1024, kSwizzle128B), id_qk, c != 0);
+            if (++slot == C::kSlots) {
+              slot = 0;
+              par ^= 1u;
             }
           }
-          if (!did && pv < qk) {
-            const int pb = (int)(n_pv % C::kPBufs);
-            if (warp_all(mbar_test(bar<kN>(s, B_PF + pb), (uint32_t)((n_pv / C::kPBufs) & 1)))) {
-              tc_fence_after();
-              const uint32_t pa = s.base + C::kOffP + pb * 2 * C::kPHalf;
-              for (int c = 0; c < 4; ++c) {
-                const uint32_t va = s.base + C::kOffK + vslot * kChunkBytes;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  pv_mma(tmem + c * kN, smem_desc(va + k * 4096, 16, 1024, kSwizzle128B),
-                         smem_desc(pa + k * 32 * kN, 16, 8 * kN, kPSwizzle),
-                         smem_desc(pa + C::kPHalf + k * 32 * kN, 16, 8 * kN, kPSwizzle), id_hi, id_lo,
-                         (pv == 0 && k == 0) ? 0u : 1u);
-                mma_commit_warp(bar<kN>(s, B_KE + vslot));
-                if (++vslot == C::kSlots) vslot = 0;
-              }
-              mma_commit_warp(bar<kN>(s, B_PE + pb));
-              ++pv;
-              ++n_pv;
-              did = true;
-            }
-          }
-          if (did) {
-            spins = 0;
-          } else if ((++spins & 63u) == 0u) {
-            // a bounded wait over whichever input comes next
-            const unsigned long long now = globaltimer();
-            if (spins == 64u) t0 = now;
-            if (warp_all(*s.abort != 0)) {
-              ok = false;
-            } else if (warp_all(now - t0 > p.wait_ns)) {
-              if (lane == 0) {
-                *s.abort = 1;
-                atomicOr(p.status, MLA_STATUS_WAIT_TIMEOUT);
-              }
-              ok = false;
-            }
-          }
+          ok = ok && warp_all(wait<kN>(s, B_RF + r, (uint32_t)((n / C::kRopes) & 1), p));
+          if (!ok) break;
+          tc_fence_after();
+          qk_mma<2>(d, smem_desc(s.base + C::kOffRope + r * kRopeBytes, 16, 512, kSwizzle64B),
+                    smem_desc(s.base + C::kOffQRope, 16, 512, kSwizzle64B), id_qk, 1);
+          mma_commit_warp(bar<kN>(s, B_RE + r));
+          mma_commit_warp(bar<kN>(s, B_SF + g));
         }
       } while (ok && warp_all(*s.abort == 0) && it.next(p));
     }
     // every operation issued here completes before the block tears down
     mma_commit_warp(bar<kN>(s, B_DRAIN));
     mbar_wait_drain(bar<kN>(s, B_DRAIN), 0);
-  } else {
+  } else if (warp == 2) {
+    // ================= PV ========================================================================
+    constexpr uint32_t id_hi = idesc_f8(kN, 1, true), id_lo = idesc_f8(kN, 0, true);
+    constexpr uint32_t kPSwizzle = kN == 64 ? kSwizzle64B : kSwizzle32B;
+    bool ok = true;
+    long long n = 0;
+    int slot = 0;
+    if (it.first(p, T, s_scan)) {
+      do {
+        for (int t = it.t_begin; t < it.t_end; ++t, ++n) {
+          const int pb = (int)(n % C::kPBufs);
+          ok = warp_all(wait<kN>(s, B_PF + pb, (uint32_t)((n / C::kPBufs) & 1), p));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t pa = s.base + C::kOffP + pb * 2 * C::kPHalf;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t va = s.base + C::kOffK + slot * kChunkBytes;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              pv_mma(tmem + c * kN, smem_desc(va + k * 4096, 16, 1024, kSwizzle128B),
+                     smem_desc(pa + k * 32 * kN, 16, 8 * kN, kPSwizzle),
+                     smem_desc(pa + C::kPHalf + k * 32 * kN, 16, 8 * kN, kPSwizzle), id_hi, id_lo,
+                     (t == it.t_begin && k == 0) ? 0u : 1u);
+            mma_commit_warp(bar<kN>(s, B_KE + slot));
+            if (++slot == C::kSlots) slot = 0;
+          }
+          mma_commit_warp(bar<kN>(s, B_PE + pb));
+        }
+      } while (ok && warp_all(*s.abort == 0) && it.next(p));
+    }
+    mma_commit_warp(bar<kN>(s, B_DRAIN + 1));
+    mbar_wait_drain(bar<kN>(s, B_DRAIN + 1), 0);
+  } else if (warp >= 4) {
     // ================= softmax: lane = key, half the rows each ==================================
-    constexpr int kR = C::kR;
-    const int q4 = warp & 3, hr = (warp - 2) >> 2;
+    const int q4 = warp & 3, hr = (warp - 4) >> 2;  // keys 32 q4 .., rows 16 hr ..
     const int key = q4 * 32 + lane;                // key within the tile, tensor-memory lane
-    const int st = tid - 64;                       // 0..255
+    const int st = tid - 128;
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
     const float4* rc = reinterpret_cast<const float4*>(s.ptr + C::kOffRc) + hr * (kR / 2);
     float* shift = reinterpret_cast<float*>(s.ptr + C::kOffShift);
@@ -692,9 +659,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         {
           const int sh = shard_of(p, it.b);
           const long long qrow = (long long)(it.b - sh * p.shard_B) * p.rows + row0;
-          constexpr int kBatch = 4;
-#pragma unroll 1
-          for (int r0 = (warp - 2) * (kN / 8); r0 < (warp - 1) * (kN / 8); r0 += kBatch) {
+          constexpr int kBatch = kN / C::kSoftWarps;
+          const int r0 = (warp - 4) * kBatch;
+          if (st < kN) lim[st] = row0 + st < p.rows ? row_keys(p, it.b, row0 + st) : it.keys;
+          {
             uint32_t w[kBatch][9];
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
@@ -720,7 +688,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float* rcw = reinterpret_cast<float*>(s.ptr + C::kOffRc) + (r >> 1) * 4 + (r & 1);
                 rcw[0] = a;
                 rcw[2] = 0.f;
-                lim[r] = row0 + r < p.rows ? row_keys(p, it.b, row0 + r) : it.keys;
               }
 #pragma unroll
               for (int i = 0; i < 9; ++i) {
@@ -749,8 +716,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(bar<kN>(s, B_QF));
         }
-        soft_sync();                               // row constants and limits
-        const int all_see = row_keys(p, it.b, row0);   // every row sees this many keys
+        soft_sync<kN>();                               // row constants and limits
+        const int all_see = lim[0];                // every row of the unit sees this many keys
 
         // ---- scales, two steps ahead: the page of tile t + 2, the scale of tile t + 1 ----------
         const int32_t* btrow = p.bt + (long long)it.b * p.bt_stride;
@@ -819,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < kR; k += 2) mx = fmax3(mx, y[k], y[k + 1]);
           const bool first = t == it.t_begin;
-          if (soft_or(first || mx > kTop)) {
+          if (soft_or<kN>(first || mx > kTop)) {
             // ---- set or move the references: O must not be written to meanwhile ----------------
             if (!first) {
               wait<kN>(s, B_PE + (int)((n - 1) % C::kPBufs), (uint32_t)(((n - 1) / C::kPBufs) & 1), p);
@@ -830,10 +797,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               float v[kR];
 #pragma unroll
               for (int k = 0; k < kR; ++k) v[k] = y[k];
-              const float m = lane_reduce<kR, true>(v, lane);
-              if (kR == 32 || (lane & 1) == 0) xm[q4 * kN + hr * kR + (kR == 32 ? lane : lane >> 1)] = m;
+              const float m = lane_reduce<true>(v, lane);
+              if ((lane & 1) == 0) xm[q4 * kN + hr * kR + (lane >> 1)] = m;
             }
-            soft_sync();
+            soft_sync<kN>();
             if (st < kN) {
               const float m = fmaxf(fmaxf(xm[st], xm[kN + st]), fmaxf(xm[2 * kN + st], xm[3 * kN + st]));
               float* nm = reinterpret_cast<float*>(s.ptr + C::kOffRc) + (st >> 1) * 4 + (st & 1) + 2;
@@ -842,18 +809,24 @@ __global__ void __launch_bounds__(kThreads, 1)
               shift[st] = by;
               *nm += by;                           // -m
             }
-            soft_sync();
+            soft_sync<kN>();
             if (!first) {
-              // O^T, columns = rows: this warp's lanes of blocks 2 hr and 2 hr + 1
-              for (int c32 = 0; c32 < 2 * kN / 32; ++c32) {
-                const uint32_t col = (uint32_t)(hr * 2 * kN + c32 * 32);
+              // O^T, columns = rows: 64 of its columns for each group of 16 rows' warps
+#pragma unroll 1
+              for (int c32 = 0; c32 < 2; ++c32) {
+                const uint32_t col = (uint32_t)(hr * 64 + c32 * 32);
                 uint32_t v[32];
                 tmem_ld32(tmem + lane_off + col, v);
                 tmem_wait_ld();
-                const float* sh4 = shift + (c32 * 32) % kN;
+                const float4* by = reinterpret_cast<const float4*>(shift + col % kN);
 #pragma unroll
-                for (int k = 0; k < 32; ++k)
-                  v[k] = __float_as_uint(__uint_as_float(v[k]) * fast_exp2(sh4[k]));
+                for (int k = 0; k < 8; ++k) {
+                  const float4 f = by[k];
+                  v[4 * k] = __float_as_uint(__uint_as_float(v[4 * k]) * fast_exp2(f.x));
+                  v[4 * k + 1] = __float_as_uint(__uint_as_float(v[4 * k + 1]) * fast_exp2(f.y));
+                  v[4 * k + 2] = __float_as_uint(__uint_as_float(v[4 * k + 2]) * fast_exp2(f.z));
+                  v[4 * k + 3] = __float_as_uint(__uint_as_float(v[4 * k + 3]) * fast_exp2(f.w));
+                }
                 tmem_st32(tmem + lane_off + col, v);
               }
               tmem_wait_st();
@@ -895,25 +868,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait<kN>(s, B_PE + pb, (uint32_t)(((n / C::kPBufs) + 1) & 1), p);
           {
             uint8_t* dst = s.ptr + C::kOffP + pb * 2 * C::kPHalf + key * kN;
-#pragma unroll
-            for (int c = 0; c < kR / 16; ++c) {
-              const int cc = hr * (kR / 16) + c;
-              const int sw = kN == 64 ? cc ^ ((key >> 1) & 3) : cc ^ ((key >> 2) & 1);
-              *reinterpret_cast<uint4*>(dst + 16 * sw) =
-                  make_uint4(ph[4 * c], ph[4 * c + 1], ph[4 * c + 2], ph[4 * c + 3]);
-              *reinterpret_cast<uint4*>(dst + C::kPHalf + 16 * sw) =
-                  make_uint4(pl[4 * c], pl[4 * c + 1], pl[4 * c + 2], pl[4 * c + 3]);
-            }
+            const int sw = kN == 64 ? hr ^ ((key >> 1) & 3) : hr ^ ((key >> 2) & 1);
+            *reinterpret_cast<uint4*>(dst + 16 * sw) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+            *reinterpret_cast<uint4*>(dst + C::kPHalf + 16 * sw) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
           }
           if (k_abs >= all_see) {
             // a weight of 0 does not keep a NaN out of O (0 * NaN): behind the request's last key,
             // where slots may hold anything, this key's values become 0; a key that only some
             // rows see loses its NaN (the rows that see it have a NaN score, so their whole
-            // output is NaN in any case).  Two of the row's four chunks for each half.
+            // output is NaN in any case).  The row's four chunks are shared out to the groups.
             const bool gone = k_abs >= it.keys;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int vs = (int)((4 * n + 2 * hr + c) % C::kSlots);
+            constexpr int kShare = 64 / kN;
+#pragma unroll 1
+            for (int c = 0; c < kShare; ++c) {
+              const int vs = (int)((4 * n + kShare * hr + c) % C::kSlots);
               uint4* row = reinterpret_cast<uint4*>(s.ptr + C::kOffK + vs * kChunkBytes + key * 128);
 #pragma unroll 1
               for (int j = 0; j < 8; ++j) {
@@ -939,9 +907,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           float v[kR];
 #pragma unroll
           for (int k = 0; k < kR / 2; ++k) f32x2_split(l2[k], v[2 * k], v[2 * k + 1]);
-          const float sum = lane_reduce<kR, false>(v, lane);
-          if (kR == 32 || (lane & 1) == 0) xs[q4 * kN + hr * kR + (kR == 32 ? lane : lane >> 1)] = sum;
-          soft_sync();
+          const float sum = lane_reduce<false>(v, lane);
+          if ((lane & 1) == 0) xs[q4 * kN + hr * kR + (lane >> 1)] = sum;
+          soft_sync<kN>();
           const long long slot = 2ll * blockIdx.x + (it.t_begin == 0 ? 1 : 0);
           if (st < kN) {
             const float l = (xs[st] + xs[kN + st]) + (xs[2 * kN + st] + xs[3 * kN + st]);
@@ -954,39 +922,48 @@ __global__ void __launch_bounds__(kThreads, 1)
               p.lse[(long long)it.b * p.rows + row0 + st] = lse2 * p.lse_mul;
             }
           }
-          soft_sync();
+          soft_sync<kN>();
           const int nrow = min(kN, p.rows - row0);
-          for (int c32 = 0; c32 < 2 * kN / 32; ++c32) {
-            const int blk = hr * 2 + c32 * 32 / kN, r0 = (c32 * 32) % kN;
+#pragma unroll 1
+          for (int c32 = 0; c32 < 2; ++c32) {
+            const int col = hr * 64 + c32 * 32, blk = col / kN, r0 = col % kN;
             uint32_t v2[32];
-            tmem_ld32(tmem + lane_off + (uint32_t)(blk * kN + r0), v2);
+            tmem_ld32(tmem + lane_off + (uint32_t)col, v2);
             tmem_wait_ld();
+            const float4* inv = reinterpret_cast<const float4*>(shift + r0);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float4 f = inv[k];
+              v2[4 * k] = __float_as_uint(__uint_as_float(v2[4 * k]) * f.x);
+              v2[4 * k + 1] = __float_as_uint(__uint_as_float(v2[4 * k + 1]) * f.y);
+              v2[4 * k + 2] = __float_as_uint(__uint_as_float(v2[4 * k + 2]) * f.z);
+              v2[4 * k + 3] = __float_as_uint(__uint_as_float(v2[4 * k + 3]) * f.w);
+            }
             const int dim = blk * 128 + key;
             if (!it.single) {
               float* dst = p.ws_o + (slot * kN + r0) * kDv + dim;
 #pragma unroll
               for (int k = 0; k < 32; ++k)
-                if (r0 + k < nrow) dst[(long long)k * kDv] = __uint_as_float(v2[k]) * shift[r0 + k];
+                if (r0 + k < nrow) dst[k * kDv] = __uint_as_float(v2[k]);
             } else {
               // neighbouring lanes hold neighbouring dims: even lanes store both of row k, odd
               // lanes both of row k + 1
-              uint16_t* dst = p.out + ((long long)it.b * p.rows + row0 + r0) * kDv + (dim & ~1);
+              const bool odd = lane & 1;
+              uint16_t* dst = p.out + ((long long)it.b * p.rows + row0 + r0 + (odd ? 1 : 0)) * kDv + (dim & ~1);
+              const int left = nrow - r0 - (odd ? 1 : 0);
 #pragma unroll
               for (int k = 0; k < 32; k += 2) {
-                const float a = __uint_as_float(v2[k]) * shift[r0 + k];
-                const float b = __uint_as_float(v2[k + 1]) * shift[r0 + k + 1];
-                const bool odd = lane & 1;
+                const float a = __uint_as_float(v2[k]), b = __uint_as_float(v2[k + 1]);
                 const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
                 const __nv_bfloat162 h = odd ? __floats2bfloat162_rn(got, b) : __floats2bfloat162_rn(a, got);
-                const int r = k + (odd ? 1 : 0);
-                if (r0 + r < nrow) *reinterpret_cast<__nv_bfloat162*>(dst + (long long)r * kDv) = h;
+                if (k < left) *reinterpret_cast<__nv_bfloat162*>(dst + k * kDv) = h;
               }
             }
           }
           tc_fence_before();
-          soft_sync();                             // shift and the row constants are free again
+          soft_sync<kN>();                             // shift and the row constants are free again
         }
-      } while (!soft_or(*s.abort != 0) && it.next(p));
+      } while (!soft_or<kN>(*s.abort != 0) && it.next(p));
     }
     if (__any_sync(0xffffffffu, bad_scale) && lane == 0) atomicOr(p.status, MLA_STATUS_BAD_SCALE);
   }
@@ -1139,7 +1116,7 @@ void device_setup(Q8Device& d) {
 template <int kN>
 cudaError_t launch(const CUtensorMap& kmap, const CUtensorMap& rmap, const Params& p, int blocks,
                    cudaStream_t stream) {
-  mla_decode_q8_kernel<kN><<<blocks, kThreads, Cfg<kN>::kSmem, stream>>>(kmap, rmap, p);
+  mla_decode_q8_kernel<kN><<<blocks, Cfg<kN>::kThreads, Cfg<kN>::kSmem, stream>>>(kmap, rmap, p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   DependentLaunch dl(dim3((unsigned)p.units * (kN / 8)), dim3(256), stream);
