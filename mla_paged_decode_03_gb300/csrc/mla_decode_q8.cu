@@ -31,8 +31,8 @@
 // and one of rope dims each, chunk by chunk as PV frees them), warp 1 issues the QK products and
 // warp 2 the PV products, each when its inputs have come (one warp for both in a fixed order
 // waits for the later of two inputs; one that polls both takes issue slots from the softmax
-// warps of its scheduler), warp 3 only fills its group, the others hold one key a lane and 16 rows a thread: they read S^T, scale, mask, exponentiate
-// and write P^T; they also prepare Q and write the output.
+// warps of its scheduler), warp 3 only fills its group, the others take 32 keys and 16 rows each:
+// they read S^T, scale, mask, exponentiate and write P^T; they also prepare Q and write the output.
 //
 // Bounds: few rows by the cache's bytes; 64 rows by shared-memory bandwidth: a tile's
 // QK reads 18 x (4 + 4) KB and its PV 32 x (4 + 2) KB, with TMA's and P's writes 426 KB, 3,330
@@ -73,7 +73,7 @@ constexpr int kDv = 512;
 constexpr int kTile = 128;                 // keys per tile
 constexpr int kChunkBytes = kTile * 128;   // 128 keys x 128 dims
 constexpr int kRopeBytes = kTile * 64;
-constexpr int kR = 16;                     // query rows per softmax thread
+constexpr int kR = 16;                     // query rows per softmax warp
 // log2 of the largest weight a tile may have, of where a new reference puts a tile's largest,
 // and of the excess that moves a reference when some row's weights pass the first
 constexpr float kTop = 12.f, kPlace = 5.f, kMove = 7.f;
@@ -92,10 +92,8 @@ struct Cfg {
   static constexpr int kOffRope = kOffK + kSlots * kChunkBytes;
   static constexpr int kOffP = kOffRope + kRopes * kRopeBytes;
   static constexpr int kOffBar = kOffP + kPBufs * 2 * kPHalf;
-  static constexpr int kOffRc = kOffBar + 384;             // float4 per 2 rows {a, a, -m, -m}
-  static constexpr int kOffShift = kOffRc + 8 * kN;        // move of m / 1 / l of each row
-  static constexpr int kOffLim = kOffShift + 4 * kN;       // keys each row sees
-  static constexpr int kOffMisc = kOffLim + 4 * kN;        // tmem base, abort, scan result
+  static constexpr int kOffRow = kOffBar + 384;            // four words for each row (softmax warps)
+  static constexpr int kOffMisc = kOffRow + 16 * kN;       // tmem base, abort, scan result
   static constexpr int kSmem = kOffMisc + 48 + 1024;       // + alignment slack
   static constexpr uint32_t kTmemCols = 8 * kN;            // O^T 4 kN, S^T 2 x 2 kN
   static_assert(kOffK % 1024 == 0 && kOffRope % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms");
@@ -119,6 +117,7 @@ enum Bar : int {
 
 struct Params {
   const uint16_t* q;
+  const uint8_t* kv;
   const float* scales;
   const int32_t* bt;
   long long bt_stride;
@@ -139,6 +138,7 @@ struct Params {
   int whole_units;             // no workspace: requests go round the groups uncut
   int box_rows;                // rows per TMA box (a page is whole boxes)
   FastDiv div_bs;
+  int tile_pages, tile_rest;   // 128 keys = tile_pages pages and tile_rest slots
   float scale_log2, lse_mul;
   uint16_t* out;
   float* lse;
@@ -191,12 +191,9 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-// Two values as e4m3 / e5m2 bytes (lo in the low byte), to nearest even, saturating.
+// Two values as e4m3 bytes (lo in the low byte), to nearest even, saturating.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
-}
-__device__ __forceinline__ uint32_t e5m2x2(float lo, float hi) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E5M2);
 }
 // Named barrier 1 over the softmax warps, alone and with an OR across them.
 template <int kN>
@@ -214,16 +211,34 @@ __device__ __forceinline__ bool soft_or(bool v) {
       : "memory");
   return r != 0;
 }
-// 16 consecutive 32-bit columns of the warp's 32 lanes.
-__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(addr)
-      : "memory");
+// 16 lanes x 16 columns of tensor memory: a thread gets lanes lane / 4 (registers 0, 1, 4, 5) and
+// lane / 4 + 8 (2, 3, 6, 7), columns 2 (lane % 4) and the next (0-3) and those 8 further (4-7).
+__device__ __forceinline__ void tmem_load_16x16(uint32_t addr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                 "=r"(r[7])
+               : "r"(addr)
+               : "memory");
+}
+// Four 8 x 8 matrices of 16-bit elements; lane l holds elements 2 (l % 4) and the next of row l / 4
+// of each, and gives the address of row l % 8 of matrix l / 8.
+__device__ __forceinline__ void stmatrix_x4(uint32_t addr, const uint32_t (&v)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
+}
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t sub_half2(uint32_t a, uint32_t b) {
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t e4m3x2_of_half2(uint32_t a) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(a));
+  return r;
 }
 
 // Instruction descriptor of kind::f8f6f4 with an fp32 accumulator; formats 0 = e4m3, 1 = e5m2;
@@ -384,25 +399,6 @@ __device__ __forceinline__ bool wait(const Ctx& s, int i, uint32_t parity, const
 }
 __device__ __forceinline__ bool warp_all(bool ok) { return __all_sync(0xffffffffu, ok); }
 
-// Largest (or sum) over the warp's 32 lanes of each of 16 values: lanes 2j and 2j + 1 return
-// value j.  Halving exchanges, 16 shuffles in all.
-template <bool kMax>
-__device__ __forceinline__ float lane_reduce(float (&v)[kR], int lane) {
-#pragma unroll
-  for (int n = kR / 2, bit = 16; n >= 1; n >>= 1, bit >>= 1) {
-    const bool up = (lane & bit) != 0;
-#pragma unroll
-    for (int k = 0; k < n; ++k) {
-      const float give = up ? v[k] : v[k + n];
-      const float keep = up ? v[k + n] : v[k];
-      const float got = __shfl_xor_sync(0xffffffffu, give, bit);
-      v[k] = kMax ? fmaxf(keep, got) : keep + got;
-    }
-  }
-  const float got = __shfl_xor_sync(0xffffffffu, v[0], 1);
-  return kMax ? fmaxf(v[0], got) : v[0] + got;
-}
-
 // ---------------------------------------------------------------------------------------------
 template <int kN>
 __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
@@ -527,8 +523,16 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
             cur = nxt;
             nxt = row_of(i0 + 32 + lane);
           }
-          // lane l < nbox issues the tile's box l
-          const int y = __shfl_sync(0xffffffffu, cur, (t * nbox + lane - i0) & 31);
+          // lane l < nbox issues the tile's box l, and asks L2 for the next tile's (its rows are
+          // consecutive bytes): the ring holds two tiles, so a load begins only when PV has let go
+          // of a chunk, and must not wait for HBM then
+          const int at = t * nbox + lane - i0;
+          const int y = __shfl_sync(0xffffffffu, cur, at & 31);
+          const int y1 = __shfl_sync(0xffffffffu, (t + 1) * nbox >= i0 + 32 ? nxt : cur, (at + nbox) & 31);
+          if (lane < nbox && t + 1 < it.t_end && y1 < p.num_blocks * p.bs)
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.kv + (long long)y1 * kD),
+                         "r"(p.box_rows * kD)
+                         : "memory");
           for (int c = 0; c < 4; ++c) {
             ok = warp_all(wait<kN>(s, B_KE + slot, kpar, p));
             if (!ok) break;
@@ -642,16 +646,25 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
     mma_commit_warp(bar<kN>(s, B_DRAIN + 1));
     mbar_wait_drain(bar<kN>(s, B_DRAIN + 1), 0);
   } else if (warp >= 4) {
-    // ================= softmax: lane = key, half the rows each ==================================
-    const int q4 = warp & 3, hr = (warp - 4) >> 2;  // keys 32 q4 .., rows 16 hr ..
-    const int key = q4 * 32 + lane;                // key within the tile, tensor-memory lane
+    // ================= softmax ===================================================================
+    // A warp has keys 32 q4 .. + 31 of a tile and rows 16 hr .. + 15 of the unit.  S^T is read in
+    // pieces of 16 keys x 8 columns, of which a thread gets keys lane / 4 and + 8, columns 2 c and
+    // 2 c + 1 (c = lane % 4); Q's rows are laid out so that those columns of two pieces are rows
+    // 4 c .. 4 c + 3.  So a thread has four keys (lane / 4 + 8 i) and four consecutive rows: the
+    // rows' constants and sums stay in registers, a key's four weights are one word of P^T.
+    const int q4 = warp & 3, hr = (warp - 4) >> 2;
+    const int c4 = lane & 3;
+    const int my_rows = hr * kR + 4 * c4;
+    const int key = q4 * 32 + lane;                // the key whose cache row this thread scrubs
     const int st = tid - 128;
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
-    const float4* rc = reinterpret_cast<const float4*>(s.ptr + C::kOffRc) + hr * (kR / 2);
-    float* shift = reinterpret_cast<float*>(s.ptr + C::kOffShift);
-    int* lim = reinterpret_cast<int*>(s.ptr + C::kOffLim);
+    float* row_a = reinterpret_cast<float*>(s.ptr + C::kOffRow);     // log2 units per unit of S
+    float* row_nm = row_a + kN;                                      // minus the reference
+    float* shift = row_nm + kN;                                      // its move; later 1 / l
+    int* lim = reinterpret_cast<int*>(shift + kN);                   // keys the row sees
+    const int groups_per_page = p.bs / MLA_Q8_GROUP;
     bool bad_scale = false;
-    long long n = 0;
+    uint32_t n = 0;
     if (it.first(p, T, s_scan)) {
       do {
         const int row0 = it.rt * kN;
@@ -661,153 +674,186 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
           const long long qrow = (long long)(it.b - sh * p.shard_B) * p.rows + row0;
           constexpr int kBatch = kN / C::kSoftWarps;
           const int r0 = (warp - 4) * kBatch;
+          uint32_t w[kBatch][9];
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            const bool valid = row0 + r0 + j < p.rows;
+            const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + (qrow + r0 + j) * kD);
+#pragma unroll
+            for (int i = 0; i < 9; ++i) w[j][i] = valid ? __ldg(src + lane + 32 * i) : 0u;
+          }
           if (st < kN) lim[st] = row0 + st < p.rows ? row_keys(p, it.b, row0 + st) : it.keys;
-          {
-            uint32_t w[kBatch][9];
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-              const bool valid = row0 + r0 + j < p.rows;
-              const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + (qrow + r0 + j) * kD);
+          for (int j = 0; j < kBatch; ++j) {
+            const int r = r0 + j;
+            uint32_t m = 0;
 #pragma unroll
-              for (int i = 0; i < 9; ++i) w[j][i] = valid ? __ldg(src + lane + 32 * i) : 0u;
+            for (int i = 0; i < 9; ++i) m = max(m, max(w[j][i] & 0x7fffu, (w[j][i] >> 16) & 0x7fffu));
+            m = __reduce_max_sync(0xffffffffu, m);
+            // 2^up puts the row's maximum in [128, 256) (a maximum below 2^-119 less far up)
+            const int ex = (int)(m >> 7);
+            const int up = min(134 - ex, 126);
+            const float f = __int_as_float((up + 127) << 23);
+            if (lane == 0) {
+              const float a = __int_as_float((127 - up) << 23) * p.scale_log2;
+              row_a[r] = ex == 255 ? __int_as_float(0x7fc00000) : a;    // NaN or infinity: a NaN row
+              row_nm[r] = 0.f;
             }
+            // its column of S^T (see above)
+            const int col = (r & ~15) + ((r & 2) << 2) + ((r & 12) >> 1) + (r & 1);
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-              const int r = r0 + j;
-              uint32_t m = 0;
-#pragma unroll
-              for (int i = 0; i < 9; ++i) m = max(m, max(w[j][i] & 0x7fffu, (w[j][i] >> 16) & 0x7fffu));
-              m = __reduce_max_sync(0xffffffffu, m);
-              // 2^up puts the row's maximum in [128, 256) (a maximum below 2^-119 less far up)
-              const int ex = (int)(m >> 7);
-              const int up = min(134 - ex, 126);
-              const float f = __int_as_float((up + 127) << 23);
-              if (lane == 0) {
-                float a = __int_as_float((127 - up) << 23) * p.scale_log2;
-                if (ex == 255) a = __int_as_float(0x7fc00000);        // NaN or infinity: a NaN row
-                float* rcw = reinterpret_cast<float*>(s.ptr + C::kOffRc) + (r >> 1) * 4 + (r & 1);
-                rcw[0] = a;
-                rcw[2] = 0.f;
+            for (int i = 0; i < 9; ++i) {
+              const float x0 = __uint_as_float(w[j][i] << 16) * f;
+              const float x1 = __uint_as_float(w[j][i] & 0xffff0000u) * f;
+              const uint32_t hi = e4m3x2(x0, x1);
+              const float2 h = __half22float2(
+                  __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3)));
+              const uint32_t lo = e4m3x2(x0 - h.x, x1 - h.y);
+              uint32_t at, half;                   // of the hi row; the lo row is kN rows on
+              if (i < 8) {
+                const int dd = (i & 1) * 64 + 2 * lane;
+                at = (i >> 1) * C::kQChunk + col * 128 + (((dd >> 4) ^ (col & 7)) << 4) + (dd & 15);
+                half = kN * 128;
+              } else {
+                const int dd = 2 * lane;
+                at = C::kOffQRope + col * 64 + (((dd >> 4) ^ ((col >> 1) & 3)) << 4) + (dd & 15);
+                half = kN * 64;
               }
-#pragma unroll
-              for (int i = 0; i < 9; ++i) {
-                const float x0 = __uint_as_float(w[j][i] << 16) * f;
-                const float x1 = __uint_as_float(w[j][i] & 0xffff0000u) * f;
-                const uint32_t hi = e4m3x2(x0, x1);
-                const float2 h = __half22float2(
-                    __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3)));
-                const uint32_t lo = e4m3x2(x0 - h.x, x1 - h.y);
-                uint32_t at, half;                 // of the hi row; the lo row is kN rows on
-                if (i < 8) {
-                  const int dd = (i & 1) * 64 + 2 * lane;
-                  at = (i >> 1) * C::kQChunk + r * 128 + (((dd >> 4) ^ (r & 7)) << 4) + (dd & 15);
-                  half = kN * 128;
-                } else {
-                  const int dd = 2 * lane;
-                  at = C::kOffQRope + r * 64 + (((dd >> 4) ^ ((r >> 1) & 3)) << 4) + (dd & 15);
-                  half = kN * 64;
-                }
-                *reinterpret_cast<uint16_t*>(s.ptr + at) = (uint16_t)hi;
-                *reinterpret_cast<uint16_t*>(s.ptr + at + half) = (uint16_t)lo;
-              }
+              *reinterpret_cast<uint16_t*>(s.ptr + at) = (uint16_t)hi;
+              *reinterpret_cast<uint16_t*>(s.ptr + at + half) = (uint16_t)lo;
             }
           }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar<kN>(s, B_QF));
         }
-        soft_sync<kN>();                               // row constants and limits
+        soft_sync<kN>();                           // row constants and limits
         const int all_see = lim[0];                // every row of the unit sees this many keys
+        const float4 a4 = *reinterpret_cast<const float4*>(row_a + my_rows);
+        float4 nm4 = make_float4(0.f, 0.f, 0.f, 0.f);
 
-        // ---- scales, two steps ahead: the page of tile t + 2, the scale of tile t + 1 ----------
+        // ---- scales: lanes 0-15 and 16-31 follow one group of 16 keys each, two steps ahead (the
+        // page of tile t + 2, the scale of tile t + 1); (pg, off) is the place of the group in
+        // the request, moved by 128 keys a tile --------------------------------------------------
         const int32_t* btrow = p.bt + (long long)it.b * p.bt_stride;
-        auto page_of = [&](int t) {
-          const int k = t * kTile + key;
-          return k < it.keys && t < it.t_end ? __ldg(btrow + fdiv((unsigned)k, p.div_bs)) : -1;
+        int at = it.t_begin * kTile + q4 * 32 + (lane & 16);
+        int pg = (int)fdiv((unsigned)at, p.div_bs), off = at - pg * p.bs;
+        const int at_end = min(it.keys, it.t_end * kTile);
+        auto page_here = [&]() { return at < at_end ? __ldg(btrow + pg) : -1; };
+        auto scale_in = [&](int page) {
+          return page >= 0 && page < p.num_blocks
+                     ? __ldg(p.scales + (long long)page * groups_per_page + (off >> 4))
+                     : 1.f;
         };
-        auto scale_of = [&](int t, int page) {
-          if (page < 0 || page >= p.num_blocks) return 1.f;
-          const unsigned k = (unsigned)(t * kTile + key);
-          const unsigned off = k - fdiv(k, p.div_bs) * (unsigned)p.bs;
-          return __ldg(p.scales + (long long)page * (p.bs / MLA_Q8_GROUP) + off / MLA_Q8_GROUP);
+        auto step = [&]() {
+          at += kTile;
+          pg += p.tile_pages;
+          off += p.tile_rest;
+          if (off >= p.bs) {
+            off -= p.bs;
+            ++pg;
+          }
         };
-        float sc_next = scale_of(it.t_begin, page_of(it.t_begin));
-        int pg_next = page_of(it.t_begin + 1);
+        float sc_next = scale_in(page_here());
+        step();
+        int page_next = page_here();
 
-        uint64_t l2[kR / 2];
-#pragma unroll
-        for (int k = 0; k < kR / 2; ++k) l2[k] = 0;
+        uint64_t l01 = 0, l23 = 0;                 // sums of the four rows' weights / S, this thread's keys
         for (int t = it.t_begin; t < it.t_end; ++t, ++n) {
-          const int g = (int)(n & 1), pb = (int)(n % C::kPBufs);
+          const uint32_t g = n & 1, pb = n % C::kPBufs;
           float sc = sc_next;
-          sc_next = scale_of(t + 1, pg_next);
-          pg_next = page_of(t + 2);
+          sc_next = scale_in(page_next);
+          step();
+          page_next = page_here();
           if (!(sc >= MLA_Q8_SCALE_MIN && sc <= MLA_Q8_SCALE_MAX)) {
             bad_scale = true;
             sc = 1.f;
           }
-          wait<kN>(s, B_SF + g, (uint32_t)((n >> 1) & 1), p);
+          // t' = acc * (a S) + (log2 S - m), for the group of keys i = 0, 1 and that of 2, 3
+          const float lg = fast_log2(sc), inv = __frcp_rn(sc);
+          uint64_t A[2][2], Bc[2][2];
+          float inv_g[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float sj = __shfl_sync(0xffffffffu, sc, 16 * j), lj = __shfl_sync(0xffffffffu, lg, 16 * j);
+            inv_g[j] = __shfl_sync(0xffffffffu, inv, 16 * j);
+            A[j][0] = mul2(f32x2(a4.x, a4.y), f32x2(sj, sj));
+            A[j][1] = mul2(f32x2(a4.z, a4.w), f32x2(sj, sj));
+            Bc[j][0] = add2(f32x2(nm4.x, nm4.y), f32x2(lj, lj));
+            Bc[j][1] = add2(f32x2(nm4.z, nm4.w), f32x2(lj, lj));
+          }
+          wait<kN>(s, B_SF + g, (n >> 1) & 1, p);
           tc_fence_after();
-          float y[kR];
+          // y[i][k]: key lane / 4 + 8 i, row my_rows + k
+          float y[4][4];
           {
-            uint32_t hi[kR], lo[kR];
-            tmem_load(tmem + lane_off + 4 * kN + g * 2 * kN + hr * kR, hi);
-            tmem_load(tmem + lane_off + 4 * kN + g * 2 * kN + kN + hr * kR, lo);
+            uint32_t hi[2][8], lo[2][8];
+            const uint32_t src = tmem + lane_off + 4 * kN + g * 2 * kN + hr * kR;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              tmem_load_16x16(src + ((uint32_t)(16 * j) << 16), hi[j]);
+              tmem_load_16x16(src + ((uint32_t)(16 * j) << 16) + kN, lo[j]);
+            }
             tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar<kN>(s, B_SE + g));
-            const uint64_t s2 = f32x2(sc, sc);
-            const float lg = fast_log2(sc);
-            const uint64_t lg2 = f32x2(lg, lg);
 #pragma unroll
-            for (int k = 0; k < kR / 2; ++k) {
-              const float4 c4 = rc[k];
-              const uint64_t acc = add2(f32x2(__uint_as_float(hi[2 * k]), __uint_as_float(hi[2 * k + 1])),
-                                        f32x2(__uint_as_float(lo[2 * k]), __uint_as_float(lo[2 * k + 1])));
-              f32x2_split(fma2(mul2(acc, s2), f32x2(c4.x, c4.y), add2(f32x2(c4.z, c4.w), lg2)), y[2 * k],
-                          y[2 * k + 1]);
-            }
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const int j = i >> 1, r = (i & 1) * 2 + k * 4;
+                const uint64_t acc =
+                    add2(f32x2(__uint_as_float(hi[j][r]), __uint_as_float(hi[j][r + 1])),
+                         f32x2(__uint_as_float(lo[j][r]), __uint_as_float(lo[j][r + 1])));
+                f32x2_split(fma2(acc, A[j][k], Bc[j][k]), y[i][2 * k], y[i][2 * k + 1]);
+              }
           }
-          const int k_abs = t * kTile + key;
           if ((t + 1) * kTile > all_see) {
             // a key that a row does not see weighs nothing, whatever its slot holds
-            const int4* l4 = reinterpret_cast<const int4*>(lim + hr * kR);
+            const int4 l4 = *reinterpret_cast<const int4*>(lim + my_rows);
 #pragma unroll
-            for (int k = 0; k < kR / 4; ++k) {
-              const int4 v = l4[k];
-              if (k_abs >= v.x) y[4 * k] = -INFINITY;
-              if (k_abs >= v.y) y[4 * k + 1] = -INFINITY;
-              if (k_abs >= v.z) y[4 * k + 2] = -INFINITY;
-              if (k_abs >= v.w) y[4 * k + 3] = -INFINITY;
+            for (int i = 0; i < 4; ++i) {
+              const int k_abs = t * kTile + q4 * 32 + (lane >> 2) + 8 * i;
+              if (k_abs >= l4.x) y[i][0] = -INFINITY;
+              if (k_abs >= l4.y) y[i][1] = -INFINITY;
+              if (k_abs >= l4.z) y[i][2] = -INFINITY;
+              if (k_abs >= l4.w) y[i][3] = -INFINITY;
             }
           }
           float mx = -INFINITY;
 #pragma unroll
-          for (int k = 0; k < kR; k += 2) mx = fmax3(mx, y[k], y[k + 1]);
+          for (int i = 0; i < 4; ++i) mx = fmax3(fmax3(mx, y[i][0], y[i][1]), y[i][2], y[i][3]);
           const bool first = t == it.t_begin;
           if (soft_or<kN>(first || mx > kTop)) {
             // ---- set or move the references: O must not be written to meanwhile ----------------
             if (!first) {
-              wait<kN>(s, B_PE + (int)((n - 1) % C::kPBufs), (uint32_t)(((n - 1) / C::kPBufs) & 1), p);
+              wait<kN>(s, B_PE + (n - 1) % C::kPBufs, ((n - 1) / C::kPBufs) & 1, p);
               tc_fence_after();
             }
             float* xm = reinterpret_cast<float*>(s.ptr + C::kOffP + pb * 2 * C::kPHalf);   // [4][kN]
             {
-              float v[kR];
+              float4 m;
+              m.x = fmaxf(fmax3(y[0][0], y[1][0], y[2][0]), y[3][0]);
+              m.y = fmaxf(fmax3(y[0][1], y[1][1], y[2][1]), y[3][1]);
+              m.z = fmaxf(fmax3(y[0][2], y[1][2], y[2][2]), y[3][2]);
+              m.w = fmaxf(fmax3(y[0][3], y[1][3], y[2][3]), y[3][3]);
 #pragma unroll
-              for (int k = 0; k < kR; ++k) v[k] = y[k];
-              const float m = lane_reduce<true>(v, lane);
-              if ((lane & 1) == 0) xm[q4 * kN + hr * kR + (lane >> 1)] = m;
+              for (int o = 4; o <= 16; o <<= 1) {
+                m.x = fmaxf(m.x, __shfl_xor_sync(0xffffffffu, m.x, o));
+                m.y = fmaxf(m.y, __shfl_xor_sync(0xffffffffu, m.y, o));
+                m.z = fmaxf(m.z, __shfl_xor_sync(0xffffffffu, m.z, o));
+                m.w = fmaxf(m.w, __shfl_xor_sync(0xffffffffu, m.w, o));
+              }
+              if (lane < 4) *reinterpret_cast<float4*>(xm + q4 * kN + my_rows) = m;
             }
             soft_sync<kN>();
             if (st < kN) {
               const float m = fmaxf(fmaxf(xm[st], xm[kN + st]), fmaxf(xm[2 * kN + st], xm[3 * kN + st]));
-              float* nm = reinterpret_cast<float*>(s.ptr + C::kOffRc) + (st >> 1) * 4 + (st & 1) + 2;
               float by = 0.f;
               if (m != -INFINITY && (first || m > kMove)) by = kPlace - m;
               shift[st] = by;
-              *nm += by;                           // -m
+              row_nm[st] += by;
             }
             soft_sync<kN>();
             if (!first) {
@@ -832,52 +878,54 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
               tmem_wait_st();
               tc_fence_before();
             }
+            const float4 by = *reinterpret_cast<const float4*>(shift + my_rows);
+            nm4 = *reinterpret_cast<const float4*>(row_nm + my_rows);
+            l01 = mul2(l01, f32x2(fast_exp2(by.x), fast_exp2(by.y)));
+            l23 = mul2(l23, f32x2(fast_exp2(by.z), fast_exp2(by.w)));
 #pragma unroll
-            for (int k = 0; k < kR / 2; ++k) {
-              const float2 by = *reinterpret_cast<const float2*>(shift + hr * kR + 2 * k);
-              y[2 * k] += by.x;
-              y[2 * k + 1] += by.y;
-              l2[k] = mul2(l2[k], f32x2(fast_exp2(by.x), fast_exp2(by.y)));
+            for (int i = 0; i < 4; ++i) {
+              y[i][0] += by.x;
+              y[i][1] += by.y;
+              y[i][2] += by.z;
+              y[i][3] += by.w;
             }
           }
-          // ---- weights, their sums over this lane's keys, and their two 8-bit parts --------------
-          uint32_t ph[kR / 4], pl[kR / 4];
-          {
-            const float inv = __frcp_rn(sc);
-            const uint64_t inv2 = f32x2(inv, inv), neg2 = f32x2(-1.f, -1.f);
+          // ---- weights, their sums, and their two 8-bit parts ------------------------------------
+          // In half precision (11 bits): h = the value rounded to e5m2, that is to its upper byte;
+          // the residue is exact, and goes to e4m3.
+          uint32_t ph[4], pl[4];
 #pragma unroll
-            for (int k = 0; k < kR / 4; ++k) {
-              uint32_t h[2], r[2];
+          for (int j = 0; j < 2; ++j) {
+            uint64_t s01 = 0, s23 = 0;
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const float e0 = fast_exp2(y[4 * k + 2 * j]), e1 = fast_exp2(y[4 * k + 2 * j + 1]);
-                const uint64_t e2 = f32x2(e0, e1);
-                l2[2 * k + j] = fma2(e2, inv2, l2[2 * k + j]);
-                // rounded to 3 significant bits, and what that leaves
-                const float h0 = __uint_as_float((__float_as_uint(e0) + 0x00100000u) & 0xffe00000u);
-                const float h1 = __uint_as_float((__float_as_uint(e1) + 0x00100000u) & 0xffe00000u);
-                float r0, r1;
-                f32x2_split(fma2(f32x2(h0, h1), neg2, e2), r0, r1);
-                h[j] = e5m2x2(h0, h1);
-                r[j] = e4m3x2(r0, r1);
-              }
-              ph[k] = h[0] | h[1] << 16;
-              pl[k] = r[0] | r[1] << 16;
+            for (int i = 2 * j; i < 2 * j + 2; ++i) {
+              const float e0 = fast_exp2(y[i][0]), e1 = fast_exp2(y[i][1]);
+              const float e2 = fast_exp2(y[i][2]), e3 = fast_exp2(y[i][3]);
+              s01 = add2(s01, f32x2(e0, e1));
+              s23 = add2(s23, f32x2(e2, e3));
+              const uint32_t u = half2_of(e0, e1), v = half2_of(e2, e3);
+              const uint32_t hu = (u + 0x00800080u) & 0xff00ff00u, hv = (v + 0x00800080u) & 0xff00ff00u;
+              ph[i] = __byte_perm(hu, hv, 0x7531);
+              pl[i] = e4m3x2_of_half2(sub_half2(u, hu)) | e4m3x2_of_half2(sub_half2(v, hv)) << 16;
             }
+            const uint64_t ij = f32x2(inv_g[j], inv_g[j]);
+            l01 = fma2(s01, ij, l01);
+            l23 = fma2(s23, ij, l23);
           }
-          wait<kN>(s, B_PE + pb, (uint32_t)(((n / C::kPBufs) + 1) & 1), p);
+          wait<kN>(s, B_PE + pb, ((n / C::kPBufs) + 1) & 1, p);
           {
-            uint8_t* dst = s.ptr + C::kOffP + pb * 2 * C::kPHalf + key * kN;
-            const int sw = kN == 64 ? hr ^ ((key >> 1) & 3) : hr ^ ((key >> 2) & 1);
-            *reinterpret_cast<uint4*>(dst + 16 * sw) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
-            *reinterpret_cast<uint4*>(dst + C::kPHalf + 16 * sw) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
+            // lane l gives the address of row l % 8 of matrix l / 8: key 32 q4 + l, its 16 bytes hr
+            const uint32_t dst = s.base + C::kOffP + pb * 2 * C::kPHalf + key * kN +
+                                 16 * (hr ^ (kN == 64 ? (key >> 1) & 3 : (key >> 2) & 1));
+            stmatrix_x4(dst, ph);
+            stmatrix_x4(dst + C::kPHalf, pl);
           }
-          if (k_abs >= all_see) {
+          if (t * kTile + key >= all_see) {
             // a weight of 0 does not keep a NaN out of O (0 * NaN): behind the request's last key,
-            // where slots may hold anything, this key's values become 0; a key that only some
+            // where slots may hold anything, a key's values become 0; a key that only some
             // rows see loses its NaN (the rows that see it have a NaN score, so their whole
             // output is NaN in any case).  The row's four chunks are shared out to the groups.
-            const bool gone = k_abs >= it.keys;
+            const bool gone = t * kTile + key >= it.keys;
             constexpr int kShare = 64 / kN;
 #pragma unroll 1
             for (int c = 0; c < kShare; ++c) {
@@ -900,22 +948,27 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
         }
 
         // ---- the segment's output ---------------------------------------------------------------
-        wait<kN>(s, B_PE + (int)((n - 1) % C::kPBufs), (uint32_t)(((n - 1) / C::kPBufs) & 1), p);
+        wait<kN>(s, B_PE + (n - 1) % C::kPBufs, ((n - 1) / C::kPBufs) & 1, p);
         tc_fence_after();
         {
           float* xs = reinterpret_cast<float*>(s.ptr + C::kOffP);        // [4][kN]
-          float v[kR];
+          float4 sum;
+          f32x2_split(l01, sum.x, sum.y);
+          f32x2_split(l23, sum.z, sum.w);
 #pragma unroll
-          for (int k = 0; k < kR / 2; ++k) f32x2_split(l2[k], v[2 * k], v[2 * k + 1]);
-          const float sum = lane_reduce<false>(v, lane);
-          if ((lane & 1) == 0) xs[q4 * kN + hr * kR + (lane >> 1)] = sum;
+          for (int o = 4; o <= 16; o <<= 1) {
+            sum.x += __shfl_xor_sync(0xffffffffu, sum.x, o);
+            sum.y += __shfl_xor_sync(0xffffffffu, sum.y, o);
+            sum.z += __shfl_xor_sync(0xffffffffu, sum.z, o);
+            sum.w += __shfl_xor_sync(0xffffffffu, sum.w, o);
+          }
+          if (lane < 4) *reinterpret_cast<float4*>(xs + q4 * kN + my_rows) = sum;
           soft_sync<kN>();
           const long long slot = 2ll * blockIdx.x + (it.t_begin == 0 ? 1 : 0);
           if (st < kN) {
             const float l = (xs[st] + xs[kN + st]) + (xs[2 * kN + st] + xs[3 * kN + st]);
-            const float nm = (reinterpret_cast<const float*>(s.ptr + C::kOffRc) + (st >> 1) * 4 + (st & 1))[2];
             shift[st] = l == 0.f ? 0.f : 1.f / l;                         // NaN stays NaN
-            const float lse2 = l == 0.f ? -INFINITY : log2f(l) - nm;
+            const float lse2 = l == 0.f ? -INFINITY : log2f(l) - row_nm[st];
             if (!it.single) {
               p.ws_lse[slot * kN + st] = lse2;
             } else if (p.lse != nullptr && row0 + st < p.rows) {
@@ -1144,6 +1197,7 @@ size_t q8_workspace_size(int B, int H, int q_len, int num_sms) {
 cudaError_t launch_decode_q8(const DecodeArgs& a, cudaStream_t stream) {
   Params p;
   p.q = a.q;
+  p.kv = reinterpret_cast<const uint8_t*>(a.kv);
   p.scales = a.kv_scales;
   p.bt = a.block_table;
   p.bt_stride = a.bt_stride;
@@ -1171,6 +1225,8 @@ cudaError_t launch_decode_q8(const DecodeArgs& a, cudaStream_t stream) {
   p.units = a.B * p.row_tiles;
   p.box_rows = a.block_size % 128 == 0 ? 128 : a.block_size % 64 == 0 ? 64 : a.block_size % 32 == 0 ? 32 : 16;
   p.div_bs = make_fastdiv((unsigned)a.block_size);
+  p.tile_pages = kTile / a.block_size;
+  p.tile_rest = kTile % a.block_size;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.lse_mul = a.lse_base_e ? 0.6931471805599453f : 1.0f;
   p.out = a.out;
