@@ -40,8 +40,8 @@
 // SM's share of HBM.
 //
 // Work split, partials and the combine: as in mla_decode_tc.cu (tiles of all requests on one
-// line, equal ranges, units cut between blocks merged by a second kernel), with fp32 partials
-// (a block has at most two: the unit it continues and the unit it does not finish).
+// line, equal ranges, units cut between blocks merged by a second kernel); a block has at most
+// two partials, the unit it continues and the unit it does not finish.
 //
 // Safety: every wait is bounded; one that runs out sets the block's abort word, every later
 // wait then returns at once, the softmax warps go through their remaining tiles without
@@ -56,7 +56,6 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 #include <cudaTypedefs.h>
 
 #include "internal.h"
@@ -84,6 +83,7 @@ struct Cfg {
   static constexpr int kThreads = 128 + 32 * kSoftWarps;   // warps 0-2: loads, QK, PV
   static constexpr int kQChunk = 2 * kN * 128;             // hi and lo rows of 128 dims
   static constexpr int kOffQRope = 4 * kQChunk;
+  static constexpr int kSegTiles = kN == 64 ? 3 : 6;       // cost of starting a segment, in tiles
   static constexpr int kSlots = kN == 64 ? 8 : 9;          // latent chunks in the ring
   static constexpr int kRopes = kN == 64 ? 1 : 2;
   static constexpr int kPBufs = kN == 64 ? 1 : 2;
@@ -125,7 +125,8 @@ struct Params {
   const int32_t* gseq;
   int B, H, q_len, bs, num_blocks, max_blocks, rank;
   int causal, il;
-  long long span;              // cp * il
+  int span;                    // cp * il
+  FastDiv div_H, div_span, div_rt, div_groups;
   unsigned long long wait_ns;
   int stall_test;
   int seg_tiles;               // start-up share of a request on the split line, in tiles
@@ -142,10 +143,10 @@ struct Params {
   float scale_log2, lse_mul;
   uint16_t* out;
   float* lse;
-  long long* hdr;              // [0] = T
+  unsigned int* hdr;           // [0] = T
   int2* meta;                  // [units] first / last group of each unit
-  float* ws_lse;               // [2 * blocks][kN] base 2
-  float* ws_o;                 // [2 * blocks][kN][512] normalised
+  float2* ws_lse;              // [2 * blocks][kN] LSE (base 2), sum of weights / l
+  uint16_t* ws_o;              // [2 * blocks][kN][512] O / sum of weights, half precision
   unsigned int* status;
 };
 
@@ -191,10 +192,6 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-// Two values as e4m3 bytes (lo in the low byte), to nearest even, saturating.
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
-}
 // Named barrier 1 over the softmax warps, alone and with an OR across them.
 template <int kN>
 __device__ __forceinline__ void soft_sync() {
@@ -235,6 +232,12 @@ __device__ __forceinline__ uint32_t sub_half2(uint32_t a, uint32_t b) {
   const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+__device__ __forceinline__ uint32_t half2_of_e4m3x2(uint32_t a) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)a));
+  return r;
+}
+// Two halves as e4m3 bytes (the low one in the low byte), to nearest even, saturating.
 __device__ __forceinline__ uint32_t e4m3x2_of_half2(uint32_t a) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(a));
@@ -287,29 +290,25 @@ __device__ __forceinline__ void pv_mma(uint32_t d, uint64_t a, uint64_t bh, uint
 
 // ---- row bounds and the work split (as in mla_decode_tc.cu, with units of kN rows and tiles
 // of 128 keys) ---------------------------------------------------------------------------------
-__device__ __noinline__ int row_bound(const Params& p, int r, long long G, int cap, int rank) {
-  if (!p.causal) return cap;
-  const int i = r / p.H;
-  long long Gi = G - (p.q_len - 1 - i);
-  if (Gi < 0) Gi = 0;
-  long long rem = Gi % p.span - (long long)rank * p.il;
-  rem = rem < 0 ? 0 : (rem > p.il ? p.il : rem);
-  const long long loc = Gi / p.span * p.il + rem;
-  return (int)(loc < cap ? loc : cap);
-}
+// All of it in 32 bits, with reciprocals from the host: lengths, cp * il and the split line are
+// below 2^31 (the entry point and q8_supported see to it), and every block goes through this
+// code before its first load (with 64-bit divisions that took 5 us).
 __device__ __forceinline__ int shard_of(const Params& p, int b) {
   return (int)__umulhi((unsigned)b, p.shard_mul);
 }
-__device__ __forceinline__ int seq_cap(const Params& p, int b) {
-  int cap = __ldg(p.seq_lens + b);
-  const int lim = p.max_blocks * p.bs;
-  if (cap > lim) cap = lim;
-  return cap < 0 ? 0 : cap;
-}
-// Keys that row r of request b sees.
+// Keys that row r (0-based within the request's q_len*H rows) of request b sees: the shard's
+// share of the row's global prefix, at most its keys.
 __device__ __forceinline__ int row_keys(const Params& p, int b, int r) {
   const int sh = shard_of(p, b);
-  return row_bound(p, r, __ldg(p.gseq + (b - sh * p.shard_B)), seq_cap(p, b), p.rank + sh);
+  int keys = max(min(__ldg(p.seq_lens + b), p.max_blocks * p.bs), 0);
+  if (p.causal) {
+    const int i = (int)fdiv((unsigned)r, p.div_H);
+    const int g = max(max(__ldg(p.gseq + (b - sh * p.shard_B)), 0) - (p.q_len - 1 - i), 0);
+    const int q = (int)fdiv((unsigned)g, p.div_span);
+    const int over = g - q * p.span - (p.rank + sh) * p.il;
+    keys = min(keys, q * p.il + min(max(over, 0), p.il));
+  }
+  return keys;
 }
 template <int kN>
 __device__ __forceinline__ int unit_keys(const Params& p, int b, int rt) {
@@ -319,14 +318,20 @@ template <int kN>
 __device__ __forceinline__ int unit_tiles(const Params& p, int b, int rt) {
   return (unit_keys<kN>(p, b, rt) + kTile - 1) / kTile;
 }
+// A request's length on the split line: its tiles after the start-up share.
 template <int kN>
-__device__ __forceinline__ long long req_span(const Params& p, int b) {
+__device__ __forceinline__ unsigned int req_span(const Params& p, int b) {
   const int nt = unit_tiles<kN>(p, b, p.row_tiles - 1);
-  return nt > 0 ? (long long)nt + p.seg_tiles : 0;
+  return nt > 0 ? (unsigned)(nt + p.seg_tiles) : 0u;
 }
-__device__ __forceinline__ long long range_start(long long T, int c, int C) { return T * c / C; }
-__device__ __forceinline__ int owner_of(long long x, long long T, int C) {
-  return (int)(((x + 1) * C - 1) / T);
+// floor(T * c / G) for 0 <= c <= G (G <= 2^15)
+__device__ __forceinline__ unsigned int range_start(const Params& p, unsigned int T, int c) {
+  const unsigned int q = fdiv(T, p.div_groups), rest = T - q * (unsigned)p.groups;
+  return q * (unsigned)c + fdiv(rest * (unsigned)c, p.div_groups);
+}
+// The group whose range holds position x < T.
+__device__ __forceinline__ int owner_of(const Params& p, unsigned int x, unsigned int T) {
+  return (int)((((unsigned long long)x + 1) * (unsigned)p.groups - 1) / T);
 }
 
 // One block's segments (request, tile range) in order; each role walks its own copy.
@@ -334,14 +339,15 @@ template <int kN>
 struct SegIter {
   int b, rt, grp;
   int t_begin, t_end, keys, nt;
-  long long g0, g_end;
+  unsigned int g0, g_end;         // the request's first tile and the range's end on the line
   bool single;                    // the segment covers its whole unit
 
   __device__ bool set(const Params& p, int tb) {
     keys = unit_keys<kN>(p, b, rt);
     nt = (keys + kTile - 1) / kTile;
     int te = nt;
-    if (!p.whole_units) te = (int)min((long long)te, g_end - g0);
+    // a range may end inside the start-up share, before the request's first tile
+    if (!p.whole_units) te = min(te, (int)(g_end - g0));
     if (tb >= te) return false;
     t_begin = tb;
     t_end = te;
@@ -355,7 +361,7 @@ struct SegIter {
       return false;
     }
     for (;;) {
-      const long long g = g0 + unit_tiles<kN>(p, b, p.row_tiles - 1) + p.seg_tiles;
+      const unsigned int g = g0 + unit_tiles<kN>(p, b, p.row_tiles - 1) + p.seg_tiles;
       if (g >= g_end) return false;
       int nb = b + 1;
       while (nb < p.B && req_span<kN>(p, nb) == 0) ++nb;
@@ -366,19 +372,19 @@ struct SegIter {
     }
   }
   // scan: the request that holds the range's first position, and where its tiles begin
-  __device__ bool first(const Params& p, long long T, const int* scan) {
-    grp = blockIdx.x / p.row_tiles;
+  __device__ bool first(const Params& p, unsigned int T, const int* scan) {
+    grp = (int)fdiv(blockIdx.x, p.div_rt);
     rt = blockIdx.x - grp * p.row_tiles;
     if (p.whole_units) {
       g0 = g_end = 0;
       b = grp - p.groups;
       return next(p);
     }
-    const long long a = range_start(T, grp, p.groups), e = range_start(T, grp + 1, p.groups);
-    if (a >= e || scan[0] < 0) return false;
+    const unsigned int a = range_start(p, T, grp);
+    g_end = range_start(p, T, grp + 1);
+    if (a >= g_end || scan[0] < 0) return false;
     b = scan[0];
-    g0 = ((long long)scan[2] << 32) | (unsigned)scan[1];
-    g_end = e;
+    g0 = (unsigned)scan[1];
     return set(p, a > g0 ? (int)(a - g0) : 0) || next(p);
   }
 };
@@ -432,49 +438,50 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
     tmem_alloc(s.base + C::kOffMisc, C::kTmemCols);
     tmem_relinquish();
   }
-  long long T = 0;
+  unsigned int T = 0;
   {
     // T = length of the split line; the request that holds this group's first position.  The
     // per-warp sums use the P buffer, which nothing else touches yet.
-    long long* s_warp = reinterpret_cast<long long*>(s.ptr + C::kOffP);
+    unsigned int* s_warp = reinterpret_cast<unsigned int*>(s.ptr + C::kOffP);
     constexpr int kThreads = C::kThreads, kWarps = kThreads / 32;
     if (tid == 0) s_scan[0] = -1;
-    long long local = 0;
-    for (int b = tid; b < p.B; b += kThreads) local += req_span<kN>(p, b);
+    // inclusive sum over the block; `before` is what the earlier warps add to it
+    auto scan = [&](unsigned int n, unsigned int& total) {
+      unsigned int incl = n;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) local += __shfl_xor_sync(0xffffffffu, local, o);
-    if (lane == 0) s_warp[warp] = local;
-    __syncthreads();
-    for (int w = 0; w < kWarps; ++w) T += s_warp[w];
-    __syncthreads();
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      if (lane == 31) s_warp[warp] = incl;
+      __syncthreads();
+      const unsigned int w = lane < kWarps ? s_warp[lane] : 0u;
+      total = __reduce_add_sync(0xffffffffu, w);
+      incl += __reduce_add_sync(0xffffffffu, lane < warp ? w : 0u);
+      __syncthreads();
+      return incl;
+    };
+    unsigned int n = tid < p.B ? req_span<kN>(p, tid) : 0u, total;
+    unsigned int end = scan(n, total);
+    T = total;
+    for (int b0 = kThreads; b0 < p.B; b0 += kThreads) {
+      scan(b0 + tid < p.B ? req_span<kN>(p, b0 + tid) : 0u, total);
+      T += total;
+    }
     if (!p.whole_units && T > 0) {
-      const long long a = range_start(T, blockIdx.x / p.row_tiles, p.groups);
-      long long running = 0;
+      const unsigned int a = range_start(p, T, (int)fdiv(blockIdx.x, p.div_rt));
+      unsigned int running = 0;
       for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-        const int b = b0 + tid;
-        const long long n = b < p.B ? req_span<kN>(p, b) : 0;
-        long long incl = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += v;
+        if (p.B > kThreads) {                      // more requests than threads: summed again
+          n = b0 + tid < p.B ? req_span<kN>(p, b0 + tid) : 0u;
+          end = scan(n, total);
         }
-        if (lane == 31) s_warp[warp] = incl;
-        __syncthreads();
-        long long before = running, total = 0;
-        for (int w = 0; w < kWarps; ++w) {
-          if (w < warp) before += s_warp[w];
-          total += s_warp[w];
-        }
-        const long long excl = before + incl - n;
+        const unsigned int excl = running + end - n;
         if (n > 0 && excl <= a && a < excl + n) {
-          const long long first = excl + p.seg_tiles;
-          s_scan[0] = b;
-          s_scan[1] = (int)(first & 0xffffffffLL);
-          s_scan[2] = (int)(first >> 32);
+          s_scan[0] = b0 + tid;
+          s_scan[1] = (int)(excl + p.seg_tiles);
         }
         running += total;
-        __syncthreads();
       }
     }
   }
@@ -516,20 +523,21 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
         int cur = row_of(i0 + lane), nxt = row_of(i0 + 32 + lane);
         // the owner of a unit's first tile records which groups hold the unit
         if (lane == 0 && it.t_begin == 0 && !p.whole_units)
-          p.meta[it.b * p.row_tiles + it.rt] = make_int2(it.grp, owner_of(it.g0 + it.nt - 1, T, p.groups));
+          p.meta[it.b * p.row_tiles + it.rt] = make_int2(it.grp, owner_of(p, it.g0 + it.nt - 1, T));
         for (int t = it.t_begin; t < it.t_end && ok; ++t) {
           if (t * nbox >= i0 + 32) {
             i0 += 32;
             cur = nxt;
             nxt = row_of(i0 + 32 + lane);
           }
-          // lane l < nbox issues the tile's box l, and asks L2 for the next tile's (its rows are
-          // consecutive bytes): the ring holds two tiles, so a load begins only when PV has let go
-          // of a chunk, and must not wait for HBM then
+          // lane l < nbox issues the tile's box l, and for units of 64 rows asks L2 for the next
+          // tile's (its rows are consecutive bytes): that ring holds two tiles, so a load begins only
+          // when PV has let go of a chunk, and must not wait for HBM then (8 % of 64 x 32k; with 32
+          // rows, where HBM bounds and the ring is longer, it cost 1 %)
           const int at = t * nbox + lane - i0;
           const int y = __shfl_sync(0xffffffffu, cur, at & 31);
           const int y1 = __shfl_sync(0xffffffffu, (t + 1) * nbox >= i0 + 32 ? nxt : cur, (at + nbox) & 31);
-          if (lane < nbox && t + 1 < it.t_end && y1 < p.num_blocks * p.bs)
+          if (kN == 64 && lane < nbox && t + 1 < it.t_end && y1 < p.num_blocks * p.bs)
             asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.kv + (long long)y1 * kD),
                          "r"(p.box_rows * kD)
                          : "memory");
@@ -627,17 +635,34 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
           if (!ok) break;
           tc_fence_after();
           const uint32_t pa = s.base + C::kOffP + pb * 2 * C::kPHalf;
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t va = s.base + C::kOffK + slot * kChunkBytes;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              pv_mma(tmem + c * kN, smem_desc(va + k * 4096, 16, 1024, kSwizzle128B),
-                     smem_desc(pa + k * 32 * kN, 16, 8 * kN, kPSwizzle),
-                     smem_desc(pa + C::kPHalf + k * 32 * kN, 16, 8 * kN, kPSwizzle), id_hi, id_lo,
-                     (t == it.t_begin && k == 0) ? 0u : 1u);
+          // chunk c of the values (dims 128 c ..), step k of 32 keys
+          auto product = [&](int c, int k) {
+            const uint32_t va = s.base + C::kOffK + slot * kChunkBytes + k * 4096;
+            pv_mma(tmem + c * kN, smem_desc(va, 16, 1024, kSwizzle128B),
+                   smem_desc(pa + k * 32 * kN, 16, 8 * kN, kPSwizzle),
+                   smem_desc(pa + C::kPHalf + k * 32 * kN, 16, 8 * kN, kPSwizzle), id_hi, id_lo,
+                   (t == it.t_begin && k == 0) ? 0u : 1u);
+          };
+          auto release = [&]() {
             mma_commit_warp(bar<kN>(s, B_KE + slot));
             if (++slot == C::kSlots) slot = 0;
+          };
+          if ((t + 1) * kTile <= it.keys) {
+            // no branch between the products of a whole tile (one cost 3 % there)
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) product(c, k);
+              release();
+            }
+          } else {
+            const int steps = (it.keys - t * kTile + 31) / 32;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+#pragma unroll 1
+              for (int k = 0; k < steps; ++k) product(c, k);
+              release();
+            }
           }
           mma_commit_warp(bar<kN>(s, B_PE + pb));
         }
@@ -668,70 +693,6 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
     if (it.first(p, T, s_scan)) {
       do {
         const int row0 = it.rt * kN;
-        // ---- Q: a warp per row, hi and lo written where the products read them ----------------
-        {
-          const int sh = shard_of(p, it.b);
-          const long long qrow = (long long)(it.b - sh * p.shard_B) * p.rows + row0;
-          constexpr int kBatch = kN / C::kSoftWarps;
-          const int r0 = (warp - 4) * kBatch;
-          uint32_t w[kBatch][9];
-#pragma unroll
-          for (int j = 0; j < kBatch; ++j) {
-            const bool valid = row0 + r0 + j < p.rows;
-            const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + (qrow + r0 + j) * kD);
-#pragma unroll
-            for (int i = 0; i < 9; ++i) w[j][i] = valid ? __ldg(src + lane + 32 * i) : 0u;
-          }
-          if (st < kN) lim[st] = row0 + st < p.rows ? row_keys(p, it.b, row0 + st) : it.keys;
-#pragma unroll
-          for (int j = 0; j < kBatch; ++j) {
-            const int r = r0 + j;
-            uint32_t m = 0;
-#pragma unroll
-            for (int i = 0; i < 9; ++i) m = max(m, max(w[j][i] & 0x7fffu, (w[j][i] >> 16) & 0x7fffu));
-            m = __reduce_max_sync(0xffffffffu, m);
-            // 2^up puts the row's maximum in [128, 256) (a maximum below 2^-119 less far up)
-            const int ex = (int)(m >> 7);
-            const int up = min(134 - ex, 126);
-            const float f = __int_as_float((up + 127) << 23);
-            if (lane == 0) {
-              const float a = __int_as_float((127 - up) << 23) * p.scale_log2;
-              row_a[r] = ex == 255 ? __int_as_float(0x7fc00000) : a;    // NaN or infinity: a NaN row
-              row_nm[r] = 0.f;
-            }
-            // its column of S^T (see above)
-            const int col = (r & ~15) + ((r & 2) << 2) + ((r & 12) >> 1) + (r & 1);
-#pragma unroll
-            for (int i = 0; i < 9; ++i) {
-              const float x0 = __uint_as_float(w[j][i] << 16) * f;
-              const float x1 = __uint_as_float(w[j][i] & 0xffff0000u) * f;
-              const uint32_t hi = e4m3x2(x0, x1);
-              const float2 h = __half22float2(
-                  __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3)));
-              const uint32_t lo = e4m3x2(x0 - h.x, x1 - h.y);
-              uint32_t at, half;                   // of the hi row; the lo row is kN rows on
-              if (i < 8) {
-                const int dd = (i & 1) * 64 + 2 * lane;
-                at = (i >> 1) * C::kQChunk + col * 128 + (((dd >> 4) ^ (col & 7)) << 4) + (dd & 15);
-                half = kN * 128;
-              } else {
-                const int dd = 2 * lane;
-                at = C::kOffQRope + col * 64 + (((dd >> 4) ^ ((col >> 1) & 3)) << 4) + (dd & 15);
-                half = kN * 64;
-              }
-              *reinterpret_cast<uint16_t*>(s.ptr + at) = (uint16_t)hi;
-              *reinterpret_cast<uint16_t*>(s.ptr + at + half) = (uint16_t)lo;
-            }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar<kN>(s, B_QF));
-        }
-        soft_sync<kN>();                           // row constants and limits
-        const int all_see = lim[0];                // every row of the unit sees this many keys
-        const float4 a4 = *reinterpret_cast<const float4*>(row_a + my_rows);
-        float4 nm4 = make_float4(0.f, 0.f, 0.f, 0.f);
-
         // ---- scales: lanes 0-15 and 16-31 follow one group of 16 keys each, two steps ahead (the
         // page of tile t + 2, the scale of tile t + 1); (pg, off) is the place of the group in
         // the request, moved by 128 keys a tile --------------------------------------------------
@@ -754,10 +715,78 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
             ++pg;
           }
         };
-        float sc_next = scale_in(page_here());
-        step();
-        int page_next = page_here();
+        const int page_first = page_here();
+        float sc_next;
+        int page_next;
 
+        // ---- Q: eight lanes a row, hi and lo written where the products read them --------------
+        {
+          static_assert(kN == 4 * C::kSoftWarps, "four rows a warp");
+          const int r = (warp - 4) * 4 + (lane >> 3), l8 = lane & 7;
+          const bool valid = row0 + r < p.rows;
+          const int sh = shard_of(p, it.b);
+          const uint4* src = reinterpret_cast<const uint4*>(
+              p.q + ((long long)(it.b - sh * p.shard_B) * p.rows + row0 + (valid ? r : 0)) * kD) + l8;
+          uint4 w[9];                              // elements 8 (l8 + 8 i) .. + 7
+#pragma unroll
+          for (int i = 0; i < 9; ++i) w[i] = valid ? __ldg(src + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+          sc_next = scale_in(page_first);
+          step();
+          page_next = page_here();
+          if (st < kN) lim[st] = row0 + st < p.rows ? row_keys(p, it.b, row0 + st) : it.keys;
+          uint32_t m2 = 0;
+#pragma unroll
+          for (int i = 0; i < 9; ++i) {
+            m2 = __vmaxu2(m2, __vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu));
+            m2 = __vmaxu2(m2, __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
+          }
+          uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+#pragma unroll
+          for (int o = 1; o <= 4; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+          // 2^up puts the row's maximum in [128, 256) (a maximum below 2^-119 less far up)
+          const int ex = (int)(m >> 7);
+          const int up = min(134 - ex, 126);
+          const float f = __int_as_float((up + 127) << 23);
+          if (l8 == 0) {
+            const float a = __int_as_float((127 - up) << 23) * p.scale_log2;
+            row_a[r] = ex == 255 ? __int_as_float(0x7fc00000) : a;      // NaN or infinity: a NaN row
+            row_nm[r] = 0.f;
+          }
+          // its column of S^T (see above); in half precision every scaled element is exact but for
+          // what lies below 2^-24
+          const int col = (r & ~15) + ((r & 2) << 2) + ((r & 12) >> 1) + (r & 1);
+          uint8_t* lat = s.ptr + col * 128 + (l8 & 1) * 8;
+          uint8_t* rope = s.ptr + C::kOffQRope + col * 64 + (((l8 >> 1) ^ ((col >> 1) & 3)) << 4) + (l8 & 1) * 8;
+          const uint64_t f2 = f32x2(f, f);
+#pragma unroll
+          for (int i = 0; i < 9; ++i) {
+            const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float x0, x1;
+              f32x2_split(mul2(f32x2(__uint_as_float(x[k] << 16), __uint_as_float(x[k] & 0xffff0000u)), f2),
+                          x0, x1);
+              const uint32_t u = half2_of(x0, x1);
+              hi[k] = e4m3x2_of_half2(u);
+              lo[k] = e4m3x2_of_half2(sub_half2(u, half2_of_e4m3x2(hi[k])));
+            }
+            uint8_t* dst = i < 8 ? lat + (i >> 1) * C::kQChunk + ((((i & 1) * 4 + (l8 >> 1)) ^ (col & 7)) << 4)
+                                 : rope;
+            *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+            *reinterpret_cast<uint2*>(dst + (i < 8 ? kN * 128 : kN * 64)) =
+                make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar<kN>(s, B_QF));
+        }
+        soft_sync<kN>();                           // row constants and limits
+        const int all_see = lim[0];                // every row of the unit sees this many keys
+        const float4 a4 = *reinterpret_cast<const float4*>(row_a + my_rows);
+        float4 nm4 = make_float4(0.f, 0.f, 0.f, 0.f);
+
+        uint64_t w01 = 0, w23 = 0;                 // sums of the four rows' weights, this thread's keys
         uint64_t l01 = 0, l23 = 0;                 // sums of the four rows' weights / S, this thread's keys
         for (int t = it.t_begin; t < it.t_end; ++t, ++n) {
           const uint32_t g = n & 1, pb = n % C::kPBufs;
@@ -880,8 +909,12 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
             }
             const float4 by = *reinterpret_cast<const float4*>(shift + my_rows);
             nm4 = *reinterpret_cast<const float4*>(row_nm + my_rows);
-            l01 = mul2(l01, f32x2(fast_exp2(by.x), fast_exp2(by.y)));
-            l23 = mul2(l23, f32x2(fast_exp2(by.z), fast_exp2(by.w)));
+            const uint64_t b01 = f32x2(fast_exp2(by.x), fast_exp2(by.y));
+            const uint64_t b23 = f32x2(fast_exp2(by.z), fast_exp2(by.w));
+            l01 = mul2(l01, b01);
+            l23 = mul2(l23, b23);
+            w01 = mul2(w01, b01);
+            w23 = mul2(w23, b23);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               y[i][0] += by.x;
@@ -911,6 +944,8 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
             const uint64_t ij = f32x2(inv_g[j], inv_g[j]);
             l01 = fma2(s01, ij, l01);
             l23 = fma2(s23, ij, l23);
+            w01 = add2(w01, s01);
+            w23 = add2(w23, s23);
           }
           wait<kN>(s, B_PE + pb, ((n / C::kPBufs) + 1) & 1, p);
           {
@@ -951,65 +986,66 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
         wait<kN>(s, B_PE + (n - 1) % C::kPBufs, ((n - 1) / C::kPBufs) & 1, p);
         tc_fence_after();
         {
-          float* xs = reinterpret_cast<float*>(s.ptr + C::kOffP);        // [4][kN]
-          float4 sum;
-          f32x2_split(l01, sum.x, sum.y);
-          f32x2_split(l23, sum.z, sum.w);
+          float* xs = reinterpret_cast<float*>(s.ptr + C::kOffP);        // [2][4][kN]
 #pragma unroll
-          for (int o = 4; o <= 16; o <<= 1) {
-            sum.x += __shfl_xor_sync(0xffffffffu, sum.x, o);
-            sum.y += __shfl_xor_sync(0xffffffffu, sum.y, o);
-            sum.z += __shfl_xor_sync(0xffffffffu, sum.z, o);
-            sum.w += __shfl_xor_sync(0xffffffffu, sum.w, o);
+          for (int v = 0; v < 2; ++v) {
+            float4 sum;
+            f32x2_split(v ? w01 : l01, sum.x, sum.y);
+            f32x2_split(v ? w23 : l23, sum.z, sum.w);
+#pragma unroll
+            for (int o = 4; o <= 16; o <<= 1) {
+              sum.x += __shfl_xor_sync(0xffffffffu, sum.x, o);
+              sum.y += __shfl_xor_sync(0xffffffffu, sum.y, o);
+              sum.z += __shfl_xor_sync(0xffffffffu, sum.z, o);
+              sum.w += __shfl_xor_sync(0xffffffffu, sum.w, o);
+            }
+            if (lane < 4) *reinterpret_cast<float4*>(xs + (v * 4 + q4) * kN + my_rows) = sum;
           }
-          if (lane < 4) *reinterpret_cast<float4*>(xs + q4 * kN + my_rows) = sum;
           soft_sync<kN>();
           const long long slot = 2ll * blockIdx.x + (it.t_begin == 0 ? 1 : 0);
           if (st < kN) {
             const float l = (xs[st] + xs[kN + st]) + (xs[2 * kN + st] + xs[3 * kN + st]);
-            shift[st] = l == 0.f ? 0.f : 1.f / l;                         // NaN stays NaN
+            const float* xw = xs + 4 * kN;
+            const float w = (xw[st] + xw[kN + st]) + (xw[2 * kN + st] + xw[3 * kN + st]);
             const float lse2 = l == 0.f ? -INFINITY : log2f(l) - row_nm[st];
+            const float by = it.single ? l : w;
+            shift[st] = by == 0.f ? 0.f : 1.f / by;                       // NaN stays NaN
             if (!it.single) {
-              p.ws_lse[slot * kN + st] = lse2;
+              p.ws_lse[slot * kN + st] = make_float2(lse2, l == 0.f ? 0.f : w / l);
             } else if (p.lse != nullptr && row0 + st < p.rows) {
               p.lse[(long long)it.b * p.rows + row0 + st] = lse2 * p.lse_mul;
             }
           }
           soft_sync<kN>();
-          const int nrow = min(kN, p.rows - row0);
+          // O^T: a lane has one dim of 32 rows; neighbouring lanes have neighbouring dims, so even
+          // lanes store two dims of row k and odd lanes two of row k + 1.  The unit's output (bf16) is
+          // O / l.  A partial is O / w, w the sum of the weights (scales included): a mean of
+          // e4m3 values, at most 448, so that half precision holds it to 2^-11 in half the bytes of
+          // fp32; w / l goes with the row's LSE.
+          const bool odd = lane & 1;
+          const int nrow = min(kN, p.rows - row0) - (odd ? 1 : 0);
+          uint16_t* dst0 = it.single ? p.out + ((long long)it.b * p.rows + row0) * kDv : p.ws_o + slot * kN * kDv;
+          dst0 += (odd ? kDv : 0) + (key & ~1);
 #pragma unroll 1
           for (int c32 = 0; c32 < 2; ++c32) {
-            const int col = hr * 64 + c32 * 32, blk = col / kN, r0 = col % kN;
+            const int col = hr * 64 + c32 * 32, r0 = col % kN;
             uint32_t v2[32];
             tmem_ld32(tmem + lane_off + (uint32_t)col, v2);
             tmem_wait_ld();
             const float4* inv = reinterpret_cast<const float4*>(shift + r0);
+            uint16_t* dst = dst0 + r0 * kDv + col / kN * 128;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float4 f = inv[k];
-              v2[4 * k] = __float_as_uint(__uint_as_float(v2[4 * k]) * f.x);
-              v2[4 * k + 1] = __float_as_uint(__uint_as_float(v2[4 * k + 1]) * f.y);
-              v2[4 * k + 2] = __float_as_uint(__uint_as_float(v2[4 * k + 2]) * f.z);
-              v2[4 * k + 3] = __float_as_uint(__uint_as_float(v2[4 * k + 3]) * f.w);
-            }
-            const int dim = blk * 128 + key;
-            if (!it.single) {
-              float* dst = p.ws_o + (slot * kN + r0) * kDv + dim;
+            for (int k = 0; k < 32; k += 4) {
+              const float4 f = inv[k / 4];
 #pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (r0 + k < nrow) dst[k * kDv] = __uint_as_float(v2[k]);
-            } else {
-              // neighbouring lanes hold neighbouring dims: even lanes store both of row k, odd
-              // lanes both of row k + 1
-              const bool odd = lane & 1;
-              uint16_t* dst = p.out + ((long long)it.b * p.rows + row0 + r0 + (odd ? 1 : 0)) * kDv + (dim & ~1);
-              const int left = nrow - r0 - (odd ? 1 : 0);
-#pragma unroll
-              for (int k = 0; k < 32; k += 2) {
-                const float a = __uint_as_float(v2[k]), b = __uint_as_float(v2[k + 1]);
+              for (int h = 0; h < 2; ++h) {
+                const float a = __uint_as_float(v2[k + 2 * h]) * (h ? f.z : f.x);
+                const float b = __uint_as_float(v2[k + 2 * h + 1]) * (h ? f.w : f.y);
                 const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-                const __nv_bfloat162 h = odd ? __floats2bfloat162_rn(got, b) : __floats2bfloat162_rn(a, got);
-                if (k < left) *reinterpret_cast<__nv_bfloat162*>(dst + k * kDv) = h;
+                const float lo = odd ? got : a, hi = odd ? b : got;
+                const __nv_bfloat162 o2 = __floats2bfloat162_rn(lo, hi);
+                const uint32_t o = it.single ? *reinterpret_cast<const uint32_t*>(&o2) : half2_of(lo, hi);
+                if (r0 + k + 2 * h < nrow) *reinterpret_cast<uint32_t*>(dst + (k + 2 * h) * kDv) = o;
               }
             }
           }
@@ -1040,7 +1076,7 @@ __global__ void __launch_bounds__(256) mla_q8_combine_kernel(const Params p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int kBlocks = kN / 8;
   const int u = blockIdx.x / kBlocks, rb = blockIdx.x % kBlocks;
-  const int b = u / p.row_tiles, rt = u - b * p.row_tiles;
+  const int b = (int)fdiv((unsigned)u, p.div_rt), rt = u - b * p.row_tiles;
   if (threadIdx.x == 0) {
     if (rt == 0 && rb == 0 && __ldg(p.seq_lens + b) > p.max_blocks * p.bs)
       atomicOr(p.status, MLA_STATUS_SEQ_TOO_LONG);
@@ -1069,15 +1105,15 @@ __global__ void __launch_bounds__(256) mla_q8_combine_kernel(const Params p) {
     if (p.lse != nullptr && lane == 0) p.lse[grow] = -INFINITY;
     return;
   }
-  const long long T = p.hdr[0];
-  auto holds = [&](int g) { return range_start(T, g, p.groups) < range_start(T, g + 1, p.groups); };
+  const unsigned int T = p.hdr[0];
+  auto holds = [&](int g) { return range_start(p, T, g) < range_start(p, T, g + 1); };
   auto slot_of = [&](int g) { return (2ll * (g * p.row_tiles + rt) + (g == m.x ? 1 : 0)) * kN + r; };
   float mx = -INFINITY;
   bool nan = false;
   for (int g0 = m.x; g0 <= m.y; g0 += 32) {
     const int g = g0 + lane;
     if (g <= m.y && holds(g)) {
-      const float l = p.ws_lse[slot_of(g)];
+      const float l = p.ws_lse[slot_of(g)].x;
       nan |= l != l;
       mx = fmaxf(mx, l);
     }
@@ -1092,34 +1128,40 @@ __global__ void __launch_bounds__(256) mla_q8_combine_kernel(const Params p) {
   if (mx != -INFINITY) {
     for (int g0 = m.x; g0 <= m.y; g0 += 32) {
       const int g = g0 + lane;
-      const float wl = g <= m.y && holds(g) ? exp2f(p.ws_lse[slot_of(g)] - mx) : 0.f;
+      float2 lw = make_float2(-INFINITY, 0.f);
+      if (g <= m.y && holds(g)) lw = p.ws_lse[slot_of(g)];
+      const float wl = exp2f(lw.x - mx), fl = wl * lw.y;
       const int nh = min(32, m.y - g0 + 1);
-#pragma unroll 2
+#pragma unroll 4
       for (int k = 0; k < nh; ++k) {
-        const float w = __shfl_sync(0xffffffffu, wl, k);
+        const float w = __shfl_sync(0xffffffffu, wl, k), f = __shfl_sync(0xffffffffu, fl, k);
         if (w == 0.f) continue;                     // nothing there, or nothing that counts
         wsum += w;
-        const float4* src = reinterpret_cast<const float4*>(p.ws_o + slot_of(g0 + k) * kDv);
+        const uint4* src = reinterpret_cast<const uint4*>(p.ws_o + slot_of(g0 + k) * kDv) + lane;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float4 v = __ldcs(src + 32 * j + lane);
-          acc[4 * j] = fmaf(w, v.x, acc[4 * j]);
-          acc[4 * j + 1] = fmaf(w, v.y, acc[4 * j + 1]);
-          acc[4 * j + 2] = fmaf(w, v.z, acc[4 * j + 2]);
-          acc[4 * j + 3] = fmaf(w, v.w, acc[4 * j + 3]);
+        for (int j = 0; j < 2; ++j) {
+          const uint4 v = __ldcs(src + 32 * j);
+          const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&x[e]));
+            acc[8 * j + 2 * e] = fmaf(f, t.x, acc[8 * j + 2 * e]);
+            acc[8 * j + 2 * e + 1] = fmaf(f, t.y, acc[8 * j + 2 * e + 1]);
+          }
         }
       }
     }
   }
   const float inv = mx == -INFINITY ? 0.f : 1.f / wsum;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(acc[4 * j] * inv, acc[4 * j + 1] * inv);
-    const __nv_bfloat162 c = __floats2bfloat162_rn(acc[4 * j + 2] * inv, acc[4 * j + 3] * inv);
-    uint2 w2;
-    w2.x = *reinterpret_cast<const uint32_t*>(&a);
-    w2.y = *reinterpret_cast<const uint32_t*>(&c);
-    *reinterpret_cast<uint2*>(o + 128 * j + 4 * lane) = w2;
+  for (int j = 0; j < 2; ++j) {
+    uint32_t w4[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(acc[8 * j + 2 * e] * inv, acc[8 * j + 2 * e + 1] * inv);
+      w4[e] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(o + 256 * j + 8 * lane) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
   }
   if (p.lse != nullptr && lane == 0)
     p.lse[grow] = mx == -INFINITY ? -INFINITY : (mx + log2f(wsum)) * p.lse_mul;
@@ -1147,8 +1189,8 @@ int rows_per_unit(int rows) { return rows <= 32 ? 32 : 64; }
 size_t ws_bytes(int units, int blocks, int kN) {
   size_t b = 256;                                                    // header
   b += ((size_t)units * sizeof(int2) + 255) / 256 * 256;
-  b += (2 * (size_t)blocks * kN * sizeof(float) + 255) / 256 * 256;
-  return b + 2 * (size_t)blocks * kN * kDv * sizeof(float);
+  b += (2 * (size_t)blocks * kN * sizeof(float2) + 255) / 256 * 256;
+  return b + 2 * (size_t)blocks * kN * kDv * sizeof(uint16_t);
 }
 
 struct Q8Device {
@@ -1186,6 +1228,8 @@ bool q8_supported(const DecodeArgs& a) {
   if ((long long)a.num_blocks * a.block_size + kTile >= (1LL << 31)) return false;
   if ((long long)a.max_blocks * a.block_size >= (1LL << 31) - 65536) return false;
   if (a.B * tiles > 0x7fffffffLL / 8) return false;
+  // the split line
+  if (a.B * ((long long)a.max_blocks * a.block_size / kTile + 1 + Cfg<32>::kSegTiles) >= (1LL << 31)) return false;
   return get_encoder() != nullptr;
 }
 
@@ -1212,7 +1256,7 @@ cudaError_t launch_decode_q8(const DecodeArgs& a, cudaStream_t stream) {
   p.rank = a.cp_rank;
   p.causal = a.causal ? 1 : 0;
   p.il = a.interleave;
-  p.span = (long long)a.cp_world * a.interleave;
+  p.span = a.cp_world * a.interleave;
   p.wait_ns = a.wait_ns;
   p.stall_test = a.stall_test;
   p.shard_B = a.shard_B;
@@ -1232,7 +1276,7 @@ cudaError_t launch_decode_q8(const DecodeArgs& a, cudaStream_t stream) {
   p.out = a.out;
   p.lse = a.lse;
   p.status = a.status;
-  p.seg_tiles = 3;
+  p.seg_tiles = n == 32 ? Cfg<32>::kSegTiles : Cfg<64>::kSegTiles;
 
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1245,13 +1289,13 @@ cudaError_t launch_decode_q8(const DecodeArgs& a, cudaStream_t stream) {
   p.groups = a.num_sms / p.row_tiles;
   if (a.workspace != nullptr && a.workspace_bytes >= ws_bytes(p.units, a.num_sms, n)) {
     char* ws = static_cast<char*>(a.workspace);
-    p.hdr = reinterpret_cast<long long*>(ws);
+    p.hdr = reinterpret_cast<unsigned int*>(ws);
     ws += 256;
     p.meta = reinterpret_cast<int2*>(ws);
     ws += ((size_t)p.units * sizeof(int2) + 255) / 256 * 256;
-    p.ws_lse = reinterpret_cast<float*>(ws);
-    ws += (2 * (size_t)a.num_sms * n * sizeof(float) + 255) / 256 * 256;
-    p.ws_o = reinterpret_cast<float*>(ws);
+    p.ws_lse = reinterpret_cast<float2*>(ws);
+    ws += (2 * (size_t)a.num_sms * n * sizeof(float2) + 255) / 256 * 256;
+    p.ws_o = reinterpret_cast<uint16_t*>(ws);
     p.whole_units = 0;
   } else {
     p.hdr = nullptr;
@@ -1262,6 +1306,10 @@ cudaError_t launch_decode_q8(const DecodeArgs& a, cudaStream_t stream) {
     if (p.groups > a.B) p.groups = a.B;
   }
   const int blocks = p.groups * p.row_tiles;
+  p.div_H = make_fastdiv((unsigned)a.H);
+  p.div_span = make_fastdiv((unsigned)p.span);
+  p.div_rt = make_fastdiv((unsigned)p.row_tiles);
+  p.div_groups = make_fastdiv((unsigned)p.groups);
 
   // the cache as rows of 576 bytes: boxes of 128 latent bytes (x = 0, 128, 256, 384; 128-byte
   // swizzle) and of the 64 rope bytes (x = 512; 64-byte swizzle)

@@ -3,12 +3,14 @@ quantising store (exact) and the decode, and a serving run of them together.
 
 Tolerance of the decode, per row, head and dim, with w_l = softmax weights, S_l the key's
 scale, v_l the stored e4m3 values, A = sum_l w_l S_l |v_l|, M = max_l w_l S_l:
-  * out is rounded to bf16 once: 2^-8 |out|; the warp-level kernel's splits and the tcgen05
-    kernel's partials are fp32 (no rounding worth counting);
-  * a weight that meets v_l is rounded to bf16 (warp-level kernel: 2^-8) or to an e5m2 value
-    plus an e4m3 remainder: 2^-3 * 2^-4 = 2^-7 of itself, plus, where the remainder is
-    subnormal, half a step, 2^-10, where the row's largest weight times scale is at least
-    2^5 when the reference is set: 2^-15 M, doubled to 2^-14 M:
+  * out is rounded to bf16 once: 2^-8 |out|; the warp-level kernel's partials are fp32;
+  * a weight that meets v_l is rounded to bf16 (warp-level kernel: 2^-8 of itself), or, in
+    [2^e, 2^(e+1)), to an e5m2 value, whose residue is at most 2^(e-3), plus that residue in
+    e4m3, whose half step up to there is 2^(e-8): 2^-8 of itself; to half precision before
+    (2^-11); and the tcgen05 kernel's partials are in half precision (2^-11 of a mean of at
+    most A): 2^-8 + 2^-10 < 2^-7 in all; where the remainder is subnormal, half a step, 2^-10,
+    where the row's largest weight times scale is at least 2^5 when the reference is set:
+    2^-15 M, doubled to 2^-14 M (half precision's own subnormals, 2^-25, are far below):
     (2^-7) A + 2^-14 M sum_l |v_l|;
   * scores: q times its row's power of two is the sum of two e4m3 values to within 2^-10 of a
     row maximum of at least 2^7 (exact above 2^-9 of the maximum): 2^-17 max|q| sum_d |k_d|;
