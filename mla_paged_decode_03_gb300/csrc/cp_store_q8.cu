@@ -54,22 +54,38 @@ __device__ __forceinline__ int local_len(const Params& p, int g) {
   return (int)(q * p.il + min(max(over, 0LL), (long long)p.il));
 }
 
-// Largest of the finite magnitudes of 8 bf16 values, as their 15 bits.
+// Largest magnitude of 8 bf16 values, as their 15 bits.
 __device__ __forceinline__ unsigned int peak8(const uint4& v) {
+  const unsigned int k = 0x7fff7fffu;
+  const unsigned int m = __vmaxu2(__vmaxu2(v.x & k, v.y & k), __vmaxu2(v.z & k, v.w & k));
+  return max(m & 0xffffu, m >> 16);
+}
+// The same over the finite ones.
+__device__ __noinline__ unsigned int finite_peak8(uint4 v) {
   const unsigned int w[4] = {v.x, v.y, v.z, v.w};
   unsigned int m = 0;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    unsigned int a = w[k] & 0x7fff7fffu;
-    a &= ~__vcmpgeu2(a, 0x7f807f80u);                    // NaN and infinities out
-    m = __vmaxu2(m, a);
+  for (int k = 0; k < 8; ++k) {
+    const unsigned int a = (w[k >> 1] >> (16 * (k & 1))) & 0x7fffu;
+    if (a < 0x7f80u) m = max(m, a);
   }
-  return max(m & 0xffffu, m >> 16);
+  return m;
 }
 
-// 8 bf16 values times `mul` (or over `div` where that is not exact) as e4m3; infinities and
-// NaN give NaN (0x7f).
-__device__ __forceinline__ uint2 encode8(const uint4& v, float mul, float div, bool exact) {
+// 8 bf16 values times `mul` as e4m3.
+__device__ __forceinline__ uint2 encode8(const uint4& v, float mul) {
+  const unsigned int w[4] = {v.x, v.y, v.z, v.w};
+  unsigned int o[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    o[k] = __nv_cvt_float2_to_fp8x2(make_float2(__uint_as_float(w[k] << 16) * mul,
+                                                __uint_as_float(w[k] & 0xffff0000u) * mul),
+                                    __NV_SATFINITE, __NV_E4M3);
+  return make_uint2(o[0] | o[1] << 16, o[2] | o[3] << 16);
+}
+// The same for values that may not be finite (NaN and infinities become NaN) and for a scale
+// that is no power of two, whose reciprocal is not exact: x / s.
+__device__ __noinline__ uint2 encode8_any(uint4 v, float s) {
   const unsigned int w[4] = {v.x, v.y, v.z, v.w};
   unsigned int o[4];
 #pragma unroll
@@ -77,8 +93,7 @@ __device__ __forceinline__ uint2 encode8(const uint4& v, float mul, float div, b
     float2 x = make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
     if ((w[k] & 0x7f80u) == 0x7f80u) x.x = __uint_as_float(0x7fc00000u);
     if ((w[k] & 0x7f800000u) == 0x7f800000u) x.y = __uint_as_float(0x7fc00000u);
-    x = exact ? make_float2(x.x * mul, x.y * mul) : make_float2(x.x / div, x.y / div);
-    o[k] = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+    o[k] = __nv_cvt_float2_to_fp8x2(make_float2(x.x / s, x.y / s), __NV_SATFINITE, __NV_E4M3);
   }
   return make_uint2(o[0] | o[1] << 16, o[2] | o[3] << 16);
 }
@@ -98,6 +113,7 @@ __device__ __forceinline__ uint2 again8(uint2 v, float ratio) {
 
 __global__ void __launch_bounds__(kThreads) cp_store_q8_kernel(const Params p) {
   __shared__ unsigned int s_peak[kThreads / 32];
+  __shared__ long long s_src[kGroup];                    // where each new row begins, in 16 bytes
   const int tid = threadIdx.x;
   const int b = blockIdx.x / p.groups, gi = blockIdx.x - b * p.groups;
   const int ctx = __ldg(p.ctx + b);
@@ -125,25 +141,33 @@ __global__ void __launch_bounds__(kThreads) cp_store_q8_kernel(const Params p) {
   const int lo = max(l0 - g0, 0), hi = min(l1 - g0, kGroup);   // new rows [lo, hi) of the group
 
   // ---- new rows into registers; the largest magnitude ----------------------------------
+  if (tid >= lo && tid < hi) {
+    const unsigned int l = (unsigned int)(g0 + tid);
+    const unsigned int seg = fdiv(l, p.div_il);
+    const long long pos = seg * p.span + (long long)p.rank * p.il + (l - seg * (unsigned int)p.il);
+    s_src[tid] = ((long long)b * p.N + (pos - ctx)) * kChunks;
+  }
+  const float old_raw = lo > 0 ? p.scales[slot0 / kGroup] : 0.f;
+  __syncthreads();
   uint4 v[kPer];
-  unsigned int peak = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int c = tid + i * kThreads;
     const int r = c / kChunks;
     v[i] = make_uint4(0, 0, 0, 0);
-    if (r >= lo && r < hi) {
-      const unsigned int l = (unsigned int)(g0 + r);
-      const unsigned int seg = fdiv(l, p.div_il);
-      const long long pos = seg * p.span + (long long)p.rank * p.il + (l - seg * (unsigned int)p.il);
-      v[i] = __ldcs(p.rows + ((long long)b * p.N + (pos - ctx)) * kChunks + (c - r * kChunks));
-    }
+    if (r >= lo && r < hi) v[i] = __ldcs(p.rows + s_src[r] + (c - r * kChunks));
   }
+  unsigned int peak = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) peak = max(peak, peak8(v[i]));
+  const bool wild = peak >= 0x7f80u;                     // this thread has a NaN or an infinity
+  if (wild) {
+    peak = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) peak = max(peak, finite_peak8(v[i]));
+  }
   peak = __reduce_max_sync(0xffffffffu, peak);
   if ((tid & 31) == 0) s_peak[tid >> 5] = peak;
-  const float old_raw = lo > 0 ? p.scales[slot0 / kGroup] : 0.f;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) peak = max(peak, s_peak[w]);
@@ -161,7 +185,7 @@ __global__ void __launch_bounds__(kThreads) cp_store_q8_kernel(const Params p) {
     }
     s = fmaxf(s, s_old);
   }
-  const bool exact = (__float_as_int(s) & 0x7fffff) == 0;      // 1 / s is a power of two
+  const bool plain = !wild && (__float_as_int(s) & 0x7fffff) == 0;   // 1 / s is exact
   const float inv = 1.f / s;
 
   uint2* dst = p.cache + slot0 * kChunks;
@@ -173,7 +197,7 @@ __global__ void __launch_bounds__(kThreads) cp_store_q8_kernel(const Params p) {
   for (int i = 0; i < kPer; ++i) {
     const int c = tid + i * kThreads;
     const int r = c / kChunks;
-    if (r >= lo && r < hi) dst[c] = encode8(v[i], inv, s, exact);
+    if (r >= lo && r < hi) dst[c] = plain ? encode8(v[i], inv) : encode8_any(v[i], s);
   }
   if (tid == 0 && (lo == 0 || s != old_raw)) p.scales[slot0 / kGroup] = s;
 }

@@ -138,23 +138,36 @@ def cp_step_tables(prev_lens: torch.Tensor, ctx_lens: torch.Tensor, new_lens: to
     if n_ranks < 1 or N < 0:
         raise ValueError(f"need n_ranks >= 1 and N >= 0, got {n_ranks} and {N}")
     device = prev_lens.device
+    # (outputs made here need no check; a user who cares for the last microseconds passes them)
     if total_lens is None:
         total_lens = torch.empty_like(prev_lens)
+        total = total_lens.data_ptr()
+    else:
+        total = _check(total_lens, "total_lens", i32, (B,), dev)
     if seq_lens is None:
         seq_lens = torch.empty((n_ranks, B), dtype=i32, device=device)
-    if positions is None:
-        positions = torch.empty((B, N), dtype=i64, device=device)
-    if slots is None:
-        slots = torch.empty((n_ranks, B, N), dtype=i64, device=device)
+        seq = seq_lens.data_ptr()
+    else:
+        seq = _check(seq_lens, "seq_lens", i32, (n_ranks, B), dev)
     if free_state_out is None:
         free_state_out = torch.empty_like(free_state)
+        state_out = free_state_out.data_ptr()
+    else:
+        state_out = _check(free_state_out, "free_state_out", i32, (2,), dev)
+    if positions is None:
+        positions = torch.empty((B, N), dtype=i64, device=device)
+        pos = positions.data_ptr()
+    else:
+        pos = _check(positions, "positions", i64, (B, N), dev)
+    if slots is None:
+        slots = torch.empty((n_ranks, B, N), dtype=i64, device=device)
+        slot = slots.data_ptr()
+    else:
+        slot = _check(slots, "slots", i64, (n_ranks, B, N), dev)
     rc = _lib.load().cp_step_tables(
         *lens, B, N, block_table.data_ptr(), stride, block_table.shape[1], free_pages.data_ptr(),
-        free_pages.shape[0], state, _check(free_state_out, "free_state_out", i32, (2,), dev), block_size,
-        cp_size, cp_rank, n_ranks, interleave, _check(total_lens, "total_lens", i32, (B,), dev),
-        _check(seq_lens, "seq_lens", i32, (n_ranks, B), dev),
-        _check(positions, "positions", i64, (B, N), dev), _check(slots, "slots", i64, (n_ranks, B, N), dev),
-        _stream(stream, dev))
+        free_pages.shape[0], state, state_out, block_size, cp_size, cp_rank, n_ranks, interleave,
+        total, seq, pos, slot, _stream(stream, dev))
     if rc:
         _lib.check(rc)
     return StepTables(total_lens, seq_lens, positions, slots, free_state_out)
@@ -221,8 +234,16 @@ def _decode(shards, q, kv_cache, kv_scales, block_table, seq_lens, gseq, q_len, 
     rows = (B * q_len, H) if shards is None else (n, B * q_len, H)
     if out is None:
         out = torch.empty((*rows, D_V), dtype=torch.bfloat16, device=q.device)
-    if lse is None and return_lse:
+        o = out.data_ptr()
+    else:
+        o = _check(out, "out", torch.bfloat16, (*rows, D_V), dev)
+    if lse is not None:
+        l = _check(lse, "lse", torch.float32, rows, dev)
+    elif return_lse:
         lse = torch.empty(rows, dtype=torch.float32, device=q.device)
+        l = lse.data_ptr()
+    else:
+        l = None
     if workspace is None:
         workspace = alloc_workspace_q8(n * B, H, q_len, q.device)
     if workspace.get_device() != dev or not workspace.is_contiguous():
@@ -231,9 +252,8 @@ def _decode(shards, q, kv_cache, kv_scales, block_table, seq_lens, gseq, q_len, 
     lib = _lib.load()
     head = (q.data_ptr(), kv_cache.data_ptr(), kv_scales.data_ptr(), block_table.data_ptr(), stride, seq, g,
             B, H, q_len, 1 if causal else 0, bs, nb, block_table.shape[1])
-    tail = (interleave, scale, _check(out, "out", torch.bfloat16, (*rows, D_V), dev),
-            None if lse is None else _check(lse, "lse", torch.float32, rows, dev), 1 if lse_base_e else 0,
-            workspace.data_ptr(), workspace.nbytes, _stream(stream, dev))
+    tail = (interleave, scale, o, l, 1 if lse_base_e else 0, workspace.data_ptr(), workspace.nbytes,
+            _stream(stream, dev))
     if shards is not None:
         rc = lib.mla_decode_shards_q8(*head, n, *tail)
     else:
