@@ -19,8 +19,8 @@
  *     returns one of the MLA_* codes.  Argument errors are found on the host before
  *     anything is launched; mla_last_error() then returns a message (thread-local).
  *   - Calls are stream-ordered: a call's kernels see every result issued before it on
- *     the stream.  The split-KV combine of mla_decode and the kernel of lse_merge are
- *     programmatic dependent launches: they may be scheduled while the kernel before
+ *     the stream.  The split-KV combine of mla_decode, the kernel of lse_merge and both
+ *     kernels of mla_decode_q8 are programmatic dependent launches: they may be scheduled while the kernel before
  *     them drains, but wait for its completion before they read or write memory.
  *   - bf16 means IEEE bfloat16 stored as 16-bit words; results are rounded to nearest
  *     even.  Tensors are dense and row-major unless a stride is given.

@@ -84,13 +84,12 @@ struct Cfg {
   static constexpr int kQChunk = 2 * kN * 128;             // hi and lo rows of 128 dims
   static constexpr int kOffQRope = 4 * kQChunk;
   static constexpr int kSegTiles = kN == 64 ? 3 : 6;       // cost of starting a segment, in tiles
-  static constexpr int kSlots = kN == 64 ? 8 : 9;          // latent chunks in the ring
-  static constexpr int kRopes = kN == 64 ? 1 : 2;
+  static constexpr int kSlots = kN == 64 ? 8 : 10;         // latent chunks in the ring (one rope chunk)
   static constexpr int kPBufs = kN == 64 ? 1 : 2;
   static constexpr int kPHalf = kTile * kN;                // hi or lo of P^T
   static constexpr int kOffK = 2 * kN * kD;
   static constexpr int kOffRope = kOffK + kSlots * kChunkBytes;
-  static constexpr int kOffP = kOffRope + kRopes * kRopeBytes;
+  static constexpr int kOffP = kOffRope + kRopeBytes;
   static constexpr int kOffBar = kOffP + kPBufs * 2 * kPHalf;
   static constexpr int kOffRow = kOffBar + 384;            // four words for each row (softmax warps)
   static constexpr int kOffMisc = kOffRow + 16 * kN;       // tmem base, abort, scan result
@@ -101,14 +100,14 @@ struct Cfg {
 };
 
 enum Bar : int {
-  B_KF = 0,        // [9] latent chunk loaded
-  B_KE = 9,        // [9] its PV done
-  B_RF = 18,       // [2] rope chunk loaded
-  B_RE = 20,       // [2] its QK done
-  B_SF = 22,       // [2] S^T written
-  B_SE = 24,       // [2] S^T read (the softmax warps)
-  B_PF = 26,       // [2] P^T written (the softmax warps)
-  B_PE = 28,       // [2] its PV done
+  B_KF = 0,        // [10] latent chunk loaded
+  B_KE = 10,       // [10] its PV done
+  B_SF = 20,       // [2] S^T written
+  B_SE = 22,       // [2] S^T read (the softmax warps)
+  B_PF = 24,       // [2] P^T written (the softmax warps)
+  B_PE = 26,       // [2] its PV done
+  B_RF = 28,       // rope chunk loaded
+  B_RE = 29,       // its QK done
   B_QF = 30,       // the segment's Q written (the softmax warps)
   B_DRAIN = 31,    // [2] the QK / PV warp's last operations
   B_NEVER = 33,    // never arrived at (tests of the timeout path)
@@ -438,6 +437,8 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
     tmem_alloc(s.base + C::kOffMisc, C::kTmemCols);
     tmem_relinquish();
   }
+  // a dependent launch (as the combine): nothing before this line touches global memory
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   unsigned int T = 0;
   {
     // T = length of the split line; the request that holds this group's first position.  The
@@ -497,8 +498,8 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
     const int nbox = kTile / p.box_rows;
     const uint32_t box_lat = (uint32_t)p.box_rows * 128, box_rope = (uint32_t)p.box_rows * 64;
     bool ok = true, bad = false;
-    int slot = 0, rope = 0;
-    uint32_t kpar = 1, rpar = 1;            // a slot's first use passes at once
+    int slot = 0;
+    uint32_t kpar = 1;                      // a slot's first use passes at once
     long long chunks = 0, ropes = 0;
     if (it.first(p, T, s_scan)) {
       do {
@@ -556,18 +557,13 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
             }
           }
           if (!ok) break;
-          ok = warp_all(wait<kN>(s, B_RE + rope, rpar, p));
+          ok = warp_all(wait<kN>(s, B_RE, (uint32_t)((ropes + 1) & 1), p));
           if (!ok) break;
-          const uint32_t fb = bar<kN>(s, B_RF + rope);
-          if (lane == 0) mbar_arrive_expect_tx(fb, kRopeBytes);
+          if (lane == 0) mbar_arrive_expect_tx(bar<kN>(s, B_RF), kRopeBytes);
           __syncwarp();
           if (lane < nbox)
-            tma_load_2d(s.base + C::kOffRope + rope * kRopeBytes + lane * box_rope, &rmap, kDv, y, fb);
+            tma_load_2d(s.base + C::kOffRope + lane * box_rope, &rmap, kDv, y, bar<kN>(s, B_RF));
           ++ropes;
-          if (++rope == C::kRopes) {
-            rope = 0;
-            rpar ^= 1u;
-          }
         }
       } while (ok && warp_all(*s.abort == 0) && it.next(p));
     }
@@ -576,8 +572,7 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
       // loads already issued land before the block exits
       for (long long m = chunks > C::kSlots ? chunks - C::kSlots : 0; m < chunks; ++m)
         mbar_wait_drain(bar<kN>(s, B_KF + (int)(m % C::kSlots)), (uint32_t)((m / C::kSlots) & 1));
-      for (long long m = ropes > C::kRopes ? ropes - C::kRopes : 0; m < ropes; ++m)
-        mbar_wait_drain(bar<kN>(s, B_RF + (int)(m % C::kRopes)), (uint32_t)((m / C::kRopes) & 1));
+      if (ropes > 0) mbar_wait_drain(bar<kN>(s, B_RF), (uint32_t)((ropes - 1) & 1));
     }
   } else if (warp == 1) {
     // ================= QK ========================================================================
@@ -592,7 +587,7 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
         ok = warp_all(wait<kN>(s, B_QF, (uint32_t)(nseg & 1), p));
         ++nseg;
         for (int t = it.t_begin; t < it.t_end && ok; ++t, ++n) {
-          const int g = (int)(n & 1), r = (int)(n % C::kRopes);
+          const int g = (int)(n & 1);
           ok = warp_all(wait<kN>(s, B_SE + g, (uint32_t)(((n >> 1) + 1) & 1), p));   // S^T read
           const uint32_t d = tmem + 4 * kN + g * 2 * kN;
 #pragma unroll
@@ -607,12 +602,12 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
               par ^= 1u;
             }
           }
-          ok = ok && warp_all(wait<kN>(s, B_RF + r, (uint32_t)((n / C::kRopes) & 1), p));
+          ok = ok && warp_all(wait<kN>(s, B_RF, (uint32_t)(n & 1), p));
           if (!ok) break;
           tc_fence_after();
-          qk_mma<2>(d, smem_desc(s.base + C::kOffRope + r * kRopeBytes, 16, 512, kSwizzle64B),
+          qk_mma<2>(d, smem_desc(s.base + C::kOffRope, 16, 512, kSwizzle64B),
                     smem_desc(s.base + C::kOffQRope, 16, 512, kSwizzle64B), id_qk, 1);
-          mma_commit_warp(bar<kN>(s, B_RE + r));
+          mma_commit_warp(bar<kN>(s, B_RE));
           mma_commit_warp(bar<kN>(s, B_SF + g));
         }
       } while (ok && warp_all(*s.abort == 0) && it.next(p));
@@ -890,6 +885,7 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
 #pragma unroll 1
               for (int c32 = 0; c32 < 2; ++c32) {
                 const uint32_t col = (uint32_t)(hr * 64 + c32 * 32);
+                if (!__any_sync(0xffffffffu, shift[col % kN + lane] != 0.f)) continue;
                 uint32_t v[32];
                 tmem_ld32(tmem + lane_off + col, v);
                 tmem_wait_ld();
@@ -1211,8 +1207,9 @@ void device_setup(Q8Device& d) {
 template <int kN>
 cudaError_t launch(const CUtensorMap& kmap, const CUtensorMap& rmap, const Params& p, int blocks,
                    cudaStream_t stream) {
-  mla_decode_q8_kernel<kN><<<blocks, Cfg<kN>::kThreads, Cfg<kN>::kSmem, stream>>>(kmap, rmap, p);
-  const cudaError_t e = cudaGetLastError();
+  DependentLaunch dk(dim3((unsigned)blocks), dim3(Cfg<kN>::kThreads), stream);
+  dk.cfg.dynamicSmemBytes = Cfg<kN>::kSmem;
+  const cudaError_t e = cudaLaunchKernelEx(&dk.cfg, mla_decode_q8_kernel<kN>, kmap, rmap, p);
   if (e != cudaSuccess) return e;
   DependentLaunch dl(dim3((unsigned)p.units * (kN / 8)), dim3(256), stream);
   return cudaLaunchKernelEx(&dl.cfg, mla_q8_combine_kernel<kN>, p);
