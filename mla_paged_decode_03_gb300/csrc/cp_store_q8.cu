@@ -111,7 +111,9 @@ __device__ __forceinline__ uint2 again8(uint2 v, float ratio) {
   return make_uint2(o[0] | o[1] << 16, o[2] | o[3] << 16);
 }
 
-__global__ void __launch_bounds__(kThreads) cp_store_q8_kernel(const Params p) {
+// (eight blocks an SM: with the 80 registers that the compiler takes otherwise, 33.4 instead of
+// 29.6 us for 16 prompts of up to 8,192 rows)
+__global__ void __launch_bounds__(kThreads, 8) cp_store_q8_kernel(const Params p) {
   __shared__ unsigned int s_peak[kThreads / 32];
   __shared__ long long s_src[kGroup];                    // where each new row begins, in 16 bytes
   const int tid = threadIdx.x;

@@ -1180,11 +1180,11 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encoder() {
 
 // Rows per unit: 32 where a request has no more (half the tensor and shared-memory time of a
 // tile), else 64.
-int rows_per_unit(int rows) { return rows <= 32 ? 32 : 64; }
+int rows_per_unit(long long rows) { return rows <= 32 ? 32 : 64; }
 
-size_t ws_bytes(int units, int blocks, int kN) {
+size_t ws_bytes(size_t units, int blocks, int kN) {
   size_t b = 256;                                                    // header
-  b += ((size_t)units * sizeof(int2) + 255) / 256 * 256;
+  b += (units * sizeof(int2) + 255) / 256 * 256;
   b += (2 * (size_t)blocks * kN * sizeof(float2) + 255) / 256 * 256;
   return b + 2 * (size_t)blocks * kN * kDv * sizeof(uint16_t);
 }
@@ -1231,8 +1231,9 @@ bool q8_supported(const DecodeArgs& a) {
 }
 
 size_t q8_workspace_size(int B, int H, int q_len, int num_sms) {
-  const int n = rows_per_unit(H * q_len);
-  return ws_bytes(B * ((H * q_len + n - 1) / n), num_sms, n);
+  const long long rows = (long long)H * q_len;
+  const int n = rows_per_unit(rows);
+  return ws_bytes((size_t)B * ((rows + n - 1) / n), num_sms, n);
 }
 
 cudaError_t launch_decode_q8(const DecodeArgs& a, cudaStream_t stream) {

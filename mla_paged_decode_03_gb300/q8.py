@@ -89,13 +89,19 @@ def _cache(kv_cache, kv_scales, dev: int) -> Tuple[int, int]:
     return nb, bs
 
 
-def _stream(stream, dev: int) -> int:
-    """The stream's handle (the current stream of the current device when None)."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
+def _on(stream, call, *args):
+    """``call`` with ``stream`` as the current stream, so that what it allocates (outputs, a
+    workspace) belongs to that stream and is not handed out again while its kernels run."""
+    dev = torch.cuda.current_device()
     if stream.device.index != dev:
         raise ValueError(f"stream is on {stream.device}, not on the current device cuda:{dev}")
-    return stream.cuda_stream
+    with torch.cuda.stream(stream):
+        return call(*args)
+
+
+def _stream(dev: int) -> int:
+    """The current stream's handle."""
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _device() -> int:
@@ -121,6 +127,10 @@ def cp_step_tables(prev_lens: torch.Tensor, ctx_lens: torch.Tensor, new_lens: to
     stays at its cached length, its positions are -1) and device_status() reports it.
     ``block_table`` and ``free_pages`` are updated in place; the outputs must not share memory
     with the inputs."""
+    if stream is not None:
+        return _on(stream, cp_step_tables, prev_lens, ctx_lens, new_lens, block_table, free_pages, free_state,
+                   block_size, N, cp_size, cp_rank, n_ranks, interleave, total_lens, seq_lens, positions,
+                   slots, free_state_out)
     if not isinstance(prev_lens, torch.Tensor) or prev_lens.dim() != 1:
         raise TypeError("prev_lens must be a 1-D int32 CUDA tensor")
     if not prev_lens.is_cuda:
@@ -167,7 +177,7 @@ def cp_step_tables(prev_lens: torch.Tensor, ctx_lens: torch.Tensor, new_lens: to
     rc = _lib.load().cp_step_tables(
         *lens, B, N, block_table.data_ptr(), stride, block_table.shape[1], free_pages.data_ptr(),
         free_pages.shape[0], state, state_out, block_size, cp_size, cp_rank, n_ranks, interleave,
-        total, seq, pos, slot, _stream(stream, dev))
+        total, seq, pos, slot, _stream(dev))
     if rc:
         _lib.check(rc)
     return StepTables(total_lens, seq_lens, positions, slots, free_state_out)
@@ -181,6 +191,9 @@ def cp_store_q8(kv_new: torch.Tensor, ctx_lens: torch.Tensor, total_lens: torch.
     total_lens[b] - 1 that rank ``cp_rank`` owns into kv_cache [num_blocks, block_size, 576]
     float8_e4m3fn and kv_scales [num_blocks, block_size / 16] float32 (a power of two for
     each 16 slots; a partly filled group's scale only grows).  Returns (kv_cache, kv_scales)."""
+    if stream is not None:
+        return _on(stream, cp_store_q8, kv_new, ctx_lens, total_lens, block_table, kv_cache, kv_scales, cp_size,
+                   cp_rank, interleave)
     _need(kv_new, "kv_new", torch.bfloat16, 3)
     dev = _device()
     B, N, d = kv_new.shape
@@ -194,7 +207,7 @@ def cp_store_q8(kv_new: torch.Tensor, ctx_lens: torch.Tensor, total_lens: torch.
         kv_new.data_ptr(), _check(ctx_lens, "ctx_lens", torch.int32, (B,), dev),
         _check(total_lens, "total_lens", torch.int32, (B,), dev), block_table.data_ptr(), stride,
         block_table.shape[1], B, N, bs, cp_size, cp_rank, interleave, kv_cache.data_ptr(),
-        kv_scales.data_ptr(), nb, _stream(stream, dev))
+        kv_scales.data_ptr(), nb, _stream(dev))
     if rc:
         _lib.check(rc)
     return kv_cache, kv_scales
@@ -215,6 +228,9 @@ def alloc_workspace_q8(B: int, H: int, q_len: int, device=None) -> torch.Tensor:
 
 def _decode(shards, q, kv_cache, kv_scales, block_table, seq_lens, gseq, q_len, cp, rank, scale, out,
             lse, lse_base_e, workspace, return_lse, stream, causal, interleave):
+    if stream is not None:
+        return _on(stream, _decode, shards, q, kv_cache, kv_scales, block_table, seq_lens, gseq, q_len, cp, rank,
+                   scale, out, lse, lse_base_e, workspace, return_lse, None, causal, interleave)
     if isinstance(q, torch.Tensor) and q.dim() == 3 and q_len >= 1 and q.shape[0] % q_len == 0:
         q = q.view(-1, q_len, q.shape[1], q.shape[2])
     _need(q, "q", torch.bfloat16, 4)
@@ -252,8 +268,8 @@ def _decode(shards, q, kv_cache, kv_scales, block_table, seq_lens, gseq, q_len, 
     lib = _lib.load()
     head = (q.data_ptr(), kv_cache.data_ptr(), kv_scales.data_ptr(), block_table.data_ptr(), stride, seq, g,
             B, H, q_len, 1 if causal else 0, bs, nb, block_table.shape[1])
-    tail = (interleave, scale, o, l, 1 if lse_base_e else 0, workspace.data_ptr(), workspace.nbytes,
-            _stream(stream, dev))
+    tail = (int(interleave), float(scale), o, l, 1 if lse_base_e else 0, workspace.data_ptr(), workspace.nbytes,
+            _stream(dev))
     if shards is not None:
         rc = lib.mla_decode_shards_q8(*head, n, *tail)
     else:

@@ -486,6 +486,79 @@ def test_decode_matches_oracle(B, H, q_len, G, bs, cp, il, causal, base_e, sprea
     print(f"[q8] {kernel} B{B} H{H} q{q_len}: bound used {worst:.3f}")
 
 
+@pytest.mark.parametrize("H,q_len", [(32, 1), (33, 1), (13, 5), (64, 2), (129, 1), (7, 16)])
+def test_decode_row_counts_around_a_unit(H, q_len):
+    # 32, 33, 65, 128, 129 and 112 rows: whole units, one row past a unit, odd head counts
+    q, G, table, pools = make_case(3, H, q_len, [129, 20, 256], 256, 1, 1, 60 + H)
+    cache, scales = gpu_pool(pools[0])
+    out, lse = M.mla_decode_q8(q.to(DEV), cache, scales, i32(table), i32(G), None, q_len, 1, 0, SCALE)
+    assert M.device_status() == 0
+    for b in range(3):
+        check_request(b, q, out, lse, G, table, pools[0], q_len, 1, 0, 1, True, True)
+
+
+@pytest.mark.parametrize("B,H,q_len,workspace", [(1500, 8, 1, True), (1300, 40, 1, True), (900, 8, 2, False),
+                                                 (700, 70, 1, False)])
+def test_decode_many_requests(B, H, q_len, workspace):
+    """More requests than a block has threads, some without a key; every request is checked
+    against attention over its pages (shared among requests here) in float64 on the GPU."""
+    g = torch.Generator().manual_seed(B)
+    rng = np.random.default_rng(B)
+    bs, nb, pages = 32, 64, 12
+    G = rng.integers(0, bs * pages + 1, B)
+    G[rng.random(B) < 0.1] = 0
+    G[rng.random(B) < 0.1] = 1
+    wide = torch.full((B, pages + 5), -1, dtype=torch.int32, device=DEV)
+    table = wide[:, 2:2 + pages]                          # a strided table
+    table.copy_(torch.randint(0, nb, (B, pages), generator=g))
+    x = torch.randn(nb, bs, 576, generator=g, device="cpu").numpy().astype(np.float64)
+    s = np.array([[Q.ref_scale(float(np.abs(x[p, 16 * j:16 * j + 16]).max())) for j in range(bs // 16)] for p in range(nb)])
+    v = Q.ref_e4m3(x / np.repeat(s, 16, 1)[..., None])
+    cache, scales = gpu_pool((v, s))
+    q = torch.randn(B, q_len, H, 576, generator=g).to(torch.bfloat16).to(DEV)
+    ws = None if workspace else torch.empty(0, dtype=torch.uint8, device=DEV)
+    out, lse = M.mla_decode_q8(q, cache, scales, table, i32(G), None, q_len, 1, 0, SCALE, workspace=ws)
+    assert M.device_status() == 0
+    keys = (cache.to(torch.float64) * torch.repeat_interleave(scales.double(), 16, 1)[..., None])
+    n = torch.arange(bs * pages, device=DEV)
+    Gt = torch.tensor(G, device=DEV)
+    for b0 in range(0, B, 100):
+        k = keys[table[b0:b0 + 100].long()].reshape(-1, bs * pages, 576)
+        see = Gt[b0:b0 + 100, None] - (q_len - 1 - torch.arange(q_len, device=DEV))
+        sc = SCALE * torch.einsum("bihd,bnd->bihn", q[b0:b0 + 100].double(), k)
+        sc = sc.masked_fill((n >= see[..., None])[:, :, None], -math.inf)
+        top = sc.amax(-1, keepdim=True)
+        w = torch.exp(sc - torch.where(top == -math.inf, 0.0, top))
+        z = w.sum(-1, keepdim=True)
+        o = torch.where(z > 0, torch.einsum("bihn,bnd->bihd", w, k[..., :512]) / z, 0.0)
+        l = (top + z.log())[..., 0]
+        T = slice(b0 * q_len, (b0 + k.shape[0]) * q_len)
+        go, gl = out[T].double().view_as(o), lse[T].double().view_as(l)
+        A = torch.where(z > 0, torch.einsum("bihn,bnd->bihd", w, k[..., :512].abs()) / z, 0.0)
+        # the docstring's bound, its terms in M and delta at most 2^-7 A for these values
+        assert bool(((go - o).abs() <= 2.0 ** -8 * o.abs() + 2.0 ** -6 * A).all())
+        assert torch.equal(torch.isneginf(gl), torch.isneginf(l))
+        fin = torch.isfinite(l)
+        assert bool(((gl - l)[fin].abs() <= 1e-3).all())
+
+
+def test_decode_on_another_stream_than_the_current_one():
+    q, G, table, pools = make_case(2, 64, 2, [300, 900], 64, 1, 1, 61)
+    cache, scales = gpu_pool(pools[0])
+    args = (q.to(DEV), cache, scales, i32(table), i32(G), None, 2, 1, 0, SCALE)
+    want = M.mla_decode_q8(*args)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        got.append(M.mla_decode_q8(*args, stream=s))
+        torch.full((1 << 20,), float("nan"), device=DEV)    # memory of the current stream, reused at once
+    s.synchronize()
+    for o, l in got:
+        assert torch.equal(o, want[0]) and torch.equal(l, want[1])
+    assert M.device_status() == 0
+
+
 @pytest.mark.parametrize("B,H,q_len,G", [(2, 128, 2, [700, 2000]), (3, 16, 1, [100, 1, 515])])
 def test_decode_without_workspace_and_without_lse(B, H, q_len, G):
     q, G, table, pools = make_case(B, H, q_len, G, 64, 1, 1, 41)
