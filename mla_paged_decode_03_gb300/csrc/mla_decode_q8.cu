@@ -52,6 +52,7 @@
 
 #include <functional>
 #include <mutex>
+#include <type_traits>
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -522,6 +523,15 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
         // lane l holds box i0 + l of the current window, the next window one ahead
         int i0 = it.t_begin * nbox;
         int cur = row_of(i0 + lane), nxt = row_of(i0 + 32 + lane);
+        // the segment's Q rows (consecutive bytes) on their way to L2: the softmax warps come to them
+        // up to a segment later
+        if (lane == 0) {
+          const int sh = shard_of(p, it.b);
+          const long long row = (long long)(it.b - sh * p.shard_B) * p.rows + it.rt * kN;
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.q + row * kD),
+                       "r"(min(kN, p.rows - it.rt * kN) * kD * 2)
+                       : "memory");
+        }
         // the owner of a unit's first tile records which groups hold the unit
         if (lane == 0 && it.t_begin == 0 && !p.whole_units)
           p.meta[it.b * p.row_tiles + it.rt] = make_int2(it.grp, owner_of(p, it.g0 + it.nt - 1, T));
@@ -642,23 +652,25 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
             mma_commit_warp(bar<kN>(s, B_KE + slot));
             if (++slot == C::kSlots) slot = 0;
           };
-          if ((t + 1) * kTile <= it.keys) {
-            // no branch between the products of a whole tile (one cost 3 % there)
+          // the steps that hold keys, in straight code for each count: a branch between two products
+          // costs more than a product (3 % of a long request, 2,500 cycles of a short one)
+          auto run = [&](auto steps) {
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) product(c, k);
+              for (int k = 0; k < decltype(steps)::value; ++k) product(c, k);
               release();
             }
-          } else {
-            const int steps = (it.keys - t * kTile + 31) / 32;
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-#pragma unroll 1
-              for (int k = 0; k < steps; ++k) product(c, k);
-              release();
-            }
-          }
+          };
+          const int left = it.keys - t * kTile;
+          if (left > 96)
+            run(std::integral_constant<int, 4>{});
+          else if (left > 64)
+            run(std::integral_constant<int, 3>{});
+          else if (left > 32)
+            run(std::integral_constant<int, 2>{});
+          else
+            run(std::integral_constant<int, 1>{});
           mma_commit_warp(bar<kN>(s, B_PE + pb));
         }
       } while (ok && warp_all(*s.abort == 0) && it.next(p));
@@ -685,35 +697,47 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
     const int groups_per_page = p.bs / MLA_Q8_GROUP;
     bool bad_scale = false;
     uint32_t n = 0;
-    if (it.first(p, T, s_scan)) {
-      do {
-        const int row0 = it.rt * kN;
-        // ---- scales: lanes 0-15 and 16-31 follow one group of 16 keys each, two steps ahead (the
-        // page of tile t + 2, the scale of tile t + 1); (pg, off) is the place of the group in
-        // the request, moved by 128 keys a tile --------------------------------------------------
-        const int32_t* btrow = p.bt + (long long)it.b * p.bt_stride;
-        int at = it.t_begin * kTile + q4 * 32 + (lane & 16);
-        int pg = (int)fdiv((unsigned)at, p.div_bs), off = at - pg * p.bs;
-        const int at_end = min(it.keys, it.t_end * kTile);
-        auto page_here = [&]() { return at < at_end ? __ldg(btrow + pg) : -1; };
-        auto scale_in = [&](int page) {
-          return page >= 0 && page < p.num_blocks
-                     ? __ldg(p.scales + (long long)page * groups_per_page + (off >> 4))
-                     : 1.f;
-        };
-        auto step = [&]() {
-          at += kTile;
-          pg += p.tile_pages;
-          off += p.tile_rest;
-          if (off >= p.bs) {
-            off -= p.bs;
-            ++pg;
-          }
-        };
-        const int page_first = page_here();
-        float sc_next;
-        int page_next;
+    // ---- scales: lanes 0-15 and 16-31 follow one group of 16 keys each, two steps ahead (the page
+    // of tile t + 2, the scale of tile t + 1); (pg, off) is the place of the group in the request,
+    // moved by 128 keys a tile
+    const int32_t* btrow = nullptr;
+    int at = 0, at_end = 0, pg = 0, off = 0, page_next = -1;
+    float sc_next = 1.f;
+    auto page_here = [&]() { return at < at_end ? __ldg(btrow + pg) : -1; };
+    auto scale_in = [&](int page) {
+      return page >= 0 && page < p.num_blocks
+                 ? __ldg(p.scales + (long long)page * groups_per_page + (off >> 4))
+                 : 1.f;
+    };
+    auto step = [&]() {
+      at += kTile;
+      pg += p.tile_pages;
+      off += p.tile_rest;
+      if (off >= p.bs) {
+        off -= p.bs;
+        ++pg;
+      }
+    };
 
+    // The order of a block's segments: Q of the next one is prepared (and its first QK may run)
+    // before the output of the one before is written, which waits for its last PV.
+    uint64_t w01 = 0, w23 = 0;                     // sums of the four rows' weights, this thread's keys
+    uint64_t l01 = 0, l23 = 0;                     // sums of the four rows' weights / S, this thread's keys
+    bool have = it.first(p, T, s_scan), pending = false;
+    // of the segment whose output is to be written: its request, whether it is a whole unit, which of
+    // the block's two partials it is
+    int out_b = 0, out_part = 0;
+    bool out_single = false;
+    float out_nm = 0.f;
+    for (;;) {
+      if (have) {
+        const int row0 = it.rt * kN;
+        btrow = p.bt + (long long)it.b * p.bt_stride;
+        at = it.t_begin * kTile + q4 * 32 + (lane & 16);
+        pg = (int)fdiv((unsigned)at, p.div_bs);
+        off = at - pg * p.bs;
+        at_end = min(it.keys, it.t_end * kTile);
+        const int page_first = page_here();
         // ---- Q: eight lanes a row, hi and lo written where the products read them --------------
         {
           static_assert(kN == 4 * C::kSoftWarps, "four rows a warp");
@@ -776,208 +800,10 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(bar<kN>(s, B_QF));
         }
-        soft_sync<kN>();                           // row constants and limits
-        const int all_see = lim[0];                // every row of the unit sees this many keys
-        const float4 a4 = *reinterpret_cast<const float4*>(row_a + my_rows);
-        float4 nm4 = make_float4(0.f, 0.f, 0.f, 0.f);
-
-        uint64_t w01 = 0, w23 = 0;                 // sums of the four rows' weights, this thread's keys
-        uint64_t l01 = 0, l23 = 0;                 // sums of the four rows' weights / S, this thread's keys
-        for (int t = it.t_begin; t < it.t_end; ++t, ++n) {
-          const uint32_t g = n & 1, pb = n % C::kPBufs;
-          float sc = sc_next;
-          sc_next = scale_in(page_next);
-          step();
-          page_next = page_here();
-          if (!(sc >= MLA_Q8_SCALE_MIN && sc <= MLA_Q8_SCALE_MAX)) {
-            bad_scale = true;
-            sc = 1.f;
-          }
-          // t' = acc * (a S) + (log2 S - m), for the group of keys i = 0, 1 and that of 2, 3
-          const float lg = fast_log2(sc), inv = __frcp_rn(sc);
-          uint64_t A[2][2], Bc[2][2];
-          float inv_g[2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float sj = __shfl_sync(0xffffffffu, sc, 16 * j), lj = __shfl_sync(0xffffffffu, lg, 16 * j);
-            inv_g[j] = __shfl_sync(0xffffffffu, inv, 16 * j);
-            A[j][0] = mul2(f32x2(a4.x, a4.y), f32x2(sj, sj));
-            A[j][1] = mul2(f32x2(a4.z, a4.w), f32x2(sj, sj));
-            Bc[j][0] = add2(f32x2(nm4.x, nm4.y), f32x2(lj, lj));
-            Bc[j][1] = add2(f32x2(nm4.z, nm4.w), f32x2(lj, lj));
-          }
-          wait<kN>(s, B_SF + g, (n >> 1) & 1, p);
-          tc_fence_after();
-          // y[i][k]: key lane / 4 + 8 i, row my_rows + k
-          float y[4][4];
-          {
-            uint32_t hi[2][8], lo[2][8];
-            const uint32_t src = tmem + lane_off + 4 * kN + g * 2 * kN + hr * kR;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              tmem_load_16x16(src + ((uint32_t)(16 * j) << 16), hi[j]);
-              tmem_load_16x16(src + ((uint32_t)(16 * j) << 16) + kN, lo[j]);
-            }
-            tmem_wait_ld();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar<kN>(s, B_SE + g));
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const int j = i >> 1, r = (i & 1) * 2 + k * 4;
-                const uint64_t acc =
-                    add2(f32x2(__uint_as_float(hi[j][r]), __uint_as_float(hi[j][r + 1])),
-                         f32x2(__uint_as_float(lo[j][r]), __uint_as_float(lo[j][r + 1])));
-                f32x2_split(fma2(acc, A[j][k], Bc[j][k]), y[i][2 * k], y[i][2 * k + 1]);
-              }
-          }
-          if ((t + 1) * kTile > all_see) {
-            // a key that a row does not see weighs nothing, whatever its slot holds
-            const int4 l4 = *reinterpret_cast<const int4*>(lim + my_rows);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int k_abs = t * kTile + q4 * 32 + (lane >> 2) + 8 * i;
-              if (k_abs >= l4.x) y[i][0] = -INFINITY;
-              if (k_abs >= l4.y) y[i][1] = -INFINITY;
-              if (k_abs >= l4.z) y[i][2] = -INFINITY;
-              if (k_abs >= l4.w) y[i][3] = -INFINITY;
-            }
-          }
-          float mx = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) mx = fmax3(fmax3(mx, y[i][0], y[i][1]), y[i][2], y[i][3]);
-          const bool first = t == it.t_begin;
-          if (soft_or<kN>(first || mx > kTop)) {
-            // ---- set or move the references: O must not be written to meanwhile ----------------
-            if (!first) {
-              wait<kN>(s, B_PE + (n - 1) % C::kPBufs, ((n - 1) / C::kPBufs) & 1, p);
-              tc_fence_after();
-            }
-            float* xm = reinterpret_cast<float*>(s.ptr + C::kOffP + pb * 2 * C::kPHalf);   // [4][kN]
-            {
-              float4 m;
-              m.x = fmaxf(fmax3(y[0][0], y[1][0], y[2][0]), y[3][0]);
-              m.y = fmaxf(fmax3(y[0][1], y[1][1], y[2][1]), y[3][1]);
-              m.z = fmaxf(fmax3(y[0][2], y[1][2], y[2][2]), y[3][2]);
-              m.w = fmaxf(fmax3(y[0][3], y[1][3], y[2][3]), y[3][3]);
-#pragma unroll
-              for (int o = 4; o <= 16; o <<= 1) {
-                m.x = fmaxf(m.x, __shfl_xor_sync(0xffffffffu, m.x, o));
-                m.y = fmaxf(m.y, __shfl_xor_sync(0xffffffffu, m.y, o));
-                m.z = fmaxf(m.z, __shfl_xor_sync(0xffffffffu, m.z, o));
-                m.w = fmaxf(m.w, __shfl_xor_sync(0xffffffffu, m.w, o));
-              }
-              if (lane < 4) *reinterpret_cast<float4*>(xm + q4 * kN + my_rows) = m;
-            }
-            soft_sync<kN>();
-            if (st < kN) {
-              const float m = fmaxf(fmaxf(xm[st], xm[kN + st]), fmaxf(xm[2 * kN + st], xm[3 * kN + st]));
-              float by = 0.f;
-              if (m != -INFINITY && (first || m > kMove)) by = kPlace - m;
-              shift[st] = by;
-              row_nm[st] += by;
-            }
-            soft_sync<kN>();
-            if (!first) {
-              // O^T, columns = rows: 64 of its columns for each group of 16 rows' warps
-#pragma unroll 1
-              for (int c32 = 0; c32 < 2; ++c32) {
-                const uint32_t col = (uint32_t)(hr * 64 + c32 * 32);
-                if (!__any_sync(0xffffffffu, shift[col % kN + lane] != 0.f)) continue;
-                uint32_t v[32];
-                tmem_ld32(tmem + lane_off + col, v);
-                tmem_wait_ld();
-                const float4* by = reinterpret_cast<const float4*>(shift + col % kN);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  const float4 f = by[k];
-                  v[4 * k] = __float_as_uint(__uint_as_float(v[4 * k]) * fast_exp2(f.x));
-                  v[4 * k + 1] = __float_as_uint(__uint_as_float(v[4 * k + 1]) * fast_exp2(f.y));
-                  v[4 * k + 2] = __float_as_uint(__uint_as_float(v[4 * k + 2]) * fast_exp2(f.z));
-                  v[4 * k + 3] = __float_as_uint(__uint_as_float(v[4 * k + 3]) * fast_exp2(f.w));
-                }
-                tmem_st32(tmem + lane_off + col, v);
-              }
-              tmem_wait_st();
-              tc_fence_before();
-            }
-            const float4 by = *reinterpret_cast<const float4*>(shift + my_rows);
-            nm4 = *reinterpret_cast<const float4*>(row_nm + my_rows);
-            const uint64_t b01 = f32x2(fast_exp2(by.x), fast_exp2(by.y));
-            const uint64_t b23 = f32x2(fast_exp2(by.z), fast_exp2(by.w));
-            l01 = mul2(l01, b01);
-            l23 = mul2(l23, b23);
-            w01 = mul2(w01, b01);
-            w23 = mul2(w23, b23);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              y[i][0] += by.x;
-              y[i][1] += by.y;
-              y[i][2] += by.z;
-              y[i][3] += by.w;
-            }
-          }
-          // ---- weights, their sums, and their two 8-bit parts ------------------------------------
-          // In half precision (11 bits): h = the value rounded to e5m2, that is to its upper byte;
-          // the residue is exact, and goes to e4m3.
-          uint32_t ph[4], pl[4];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint64_t s01 = 0, s23 = 0;
-#pragma unroll
-            for (int i = 2 * j; i < 2 * j + 2; ++i) {
-              const float e0 = fast_exp2(y[i][0]), e1 = fast_exp2(y[i][1]);
-              const float e2 = fast_exp2(y[i][2]), e3 = fast_exp2(y[i][3]);
-              s01 = add2(s01, f32x2(e0, e1));
-              s23 = add2(s23, f32x2(e2, e3));
-              const uint32_t u = half2_of(e0, e1), v = half2_of(e2, e3);
-              const uint32_t hu = (u + 0x00800080u) & 0xff00ff00u, hv = (v + 0x00800080u) & 0xff00ff00u;
-              ph[i] = __byte_perm(hu, hv, 0x7531);
-              pl[i] = e4m3x2_of_half2(sub_half2(u, hu)) | e4m3x2_of_half2(sub_half2(v, hv)) << 16;
-            }
-            const uint64_t ij = f32x2(inv_g[j], inv_g[j]);
-            l01 = fma2(s01, ij, l01);
-            l23 = fma2(s23, ij, l23);
-            w01 = add2(w01, s01);
-            w23 = add2(w23, s23);
-          }
-          wait<kN>(s, B_PE + pb, ((n / C::kPBufs) + 1) & 1, p);
-          {
-            // lane l gives the address of row l % 8 of matrix l / 8: key 32 q4 + l, its 16 bytes hr
-            const uint32_t dst = s.base + C::kOffP + pb * 2 * C::kPHalf + key * kN +
-                                 16 * (hr ^ (kN == 64 ? (key >> 1) & 3 : (key >> 2) & 1));
-            stmatrix_x4(dst, ph);
-            stmatrix_x4(dst + C::kPHalf, pl);
-          }
-          if (t * kTile + key >= all_see) {
-            // a weight of 0 does not keep a NaN out of O (0 * NaN): behind the request's last key,
-            // where slots may hold anything, a key's values become 0; a key that only some
-            // rows see loses its NaN (the rows that see it have a NaN score, so their whole
-            // output is NaN in any case).  The row's four chunks are shared out to the groups.
-            const bool gone = t * kTile + key >= it.keys;
-            constexpr int kShare = 64 / kN;
-#pragma unroll 1
-            for (int c = 0; c < kShare; ++c) {
-              const int vs = (int)((4 * n + kShare * hr + c) % C::kSlots);
-              uint4* row = reinterpret_cast<uint4*>(s.ptr + C::kOffK + vs * kChunkBytes + key * 128);
-#pragma unroll 1
-              for (int j = 0; j < 8; ++j) {
-                uint4 v = gone ? make_uint4(0, 0, 0, 0) : row[j];
-                v.x &= ~__vcmpeq4(v.x & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                v.y &= ~__vcmpeq4(v.y & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                v.z &= ~__vcmpeq4(v.z & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                v.w &= ~__vcmpeq4(v.w & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                row[j] = v;
-              }
-            }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar<kN>(s, B_PF + pb));
-        }
-
+      }
+      if (pending) {
+        const int out_row0 = it.rt * kN;
+        const long long out_row = (long long)out_b * p.rows + out_row0, out_slot = 2ll * blockIdx.x + out_part;
         // ---- the segment's output ---------------------------------------------------------------
         wait<kN>(s, B_PE + (n - 1) % C::kPBufs, ((n - 1) / C::kPBufs) & 1, p);
         tc_fence_after();
@@ -998,18 +824,17 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
             if (lane < 4) *reinterpret_cast<float4*>(xs + (v * 4 + q4) * kN + my_rows) = sum;
           }
           soft_sync<kN>();
-          const long long slot = 2ll * blockIdx.x + (it.t_begin == 0 ? 1 : 0);
           if (st < kN) {
             const float l = (xs[st] + xs[kN + st]) + (xs[2 * kN + st] + xs[3 * kN + st]);
             const float* xw = xs + 4 * kN;
             const float w = (xw[st] + xw[kN + st]) + (xw[2 * kN + st] + xw[3 * kN + st]);
-            const float lse2 = l == 0.f ? -INFINITY : log2f(l) - row_nm[st];
-            const float by = it.single ? l : w;
+            const float lse2 = l == 0.f ? -INFINITY : log2f(l) - out_nm;
+            const float by = out_single ? l : w;
             shift[st] = by == 0.f ? 0.f : 1.f / by;                       // NaN stays NaN
-            if (!it.single) {
-              p.ws_lse[slot * kN + st] = make_float2(lse2, l == 0.f ? 0.f : w / l);
-            } else if (p.lse != nullptr && row0 + st < p.rows) {
-              p.lse[(long long)it.b * p.rows + row0 + st] = lse2 * p.lse_mul;
+            if (!out_single) {
+              p.ws_lse[out_slot * kN + st] = make_float2(lse2, l == 0.f ? 0.f : w / l);
+            } else if (p.lse != nullptr && out_row0 + st < p.rows) {
+              p.lse[out_row + st] = lse2 * p.lse_mul;
             }
           }
           soft_sync<kN>();
@@ -1019,8 +844,8 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
           // e4m3 values, at most 448, so that half precision holds it to 2^-11 in half the bytes of
           // fp32; w / l goes with the row's LSE.
           const bool odd = lane & 1;
-          const int nrow = min(kN, p.rows - row0) - (odd ? 1 : 0);
-          uint16_t* dst0 = it.single ? p.out + ((long long)it.b * p.rows + row0) * kDv : p.ws_o + slot * kN * kDv;
+          const int nrow = min(kN, p.rows - out_row0) - (odd ? 1 : 0);
+          uint16_t* dst0 = out_single ? p.out + out_row * kDv : p.ws_o + out_slot * kN * kDv;
           dst0 += (odd ? kDv : 0) + (key & ~1);
 #pragma unroll 1
           for (int c32 = 0; c32 < 2; ++c32) {
@@ -1040,15 +865,222 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
                 const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
                 const float lo = odd ? got : a, hi = odd ? b : got;
                 const __nv_bfloat162 o2 = __floats2bfloat162_rn(lo, hi);
-                const uint32_t o = it.single ? *reinterpret_cast<const uint32_t*>(&o2) : half2_of(lo, hi);
+                const uint32_t o = out_single ? *reinterpret_cast<const uint32_t*>(&o2) : half2_of(lo, hi);
                 if (r0 + k + 2 * h < nrow) *reinterpret_cast<uint32_t*>(dst + (k + 2 * h) * kDv) = o;
               }
             }
           }
           tc_fence_before();
-          soft_sync<kN>();                             // shift and the row constants are free again
         }
-      } while (!soft_or<kN>(*s.abort != 0) && it.next(p));
+      }
+      if (!have) break;
+      soft_sync<kN>();                             // row constants and limits; shift is free again
+      const int all_see = lim[0];                // every row of the unit sees this many keys
+      const float4 a4 = *reinterpret_cast<const float4*>(row_a + my_rows);
+      float4 nm4 = make_float4(0.f, 0.f, 0.f, 0.f);
+
+      w01 = w23 = l01 = l23 = 0;
+      for (int t = it.t_begin; t < it.t_end; ++t, ++n) {
+        const uint32_t g = n & 1, pb = n % C::kPBufs;
+        float sc = sc_next;
+        sc_next = scale_in(page_next);
+        step();
+        page_next = page_here();
+        if (!(sc >= MLA_Q8_SCALE_MIN && sc <= MLA_Q8_SCALE_MAX)) {
+          bad_scale = true;
+          sc = 1.f;
+        }
+        // t' = acc * (a S) + (log2 S - m), for the group of keys i = 0, 1 and that of 2, 3
+        const float lg = fast_log2(sc), inv = __frcp_rn(sc);
+        uint64_t A[2][2], Bc[2][2];
+        float inv_g[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float sj = __shfl_sync(0xffffffffu, sc, 16 * j), lj = __shfl_sync(0xffffffffu, lg, 16 * j);
+          inv_g[j] = __shfl_sync(0xffffffffu, inv, 16 * j);
+          A[j][0] = mul2(f32x2(a4.x, a4.y), f32x2(sj, sj));
+          A[j][1] = mul2(f32x2(a4.z, a4.w), f32x2(sj, sj));
+          Bc[j][0] = add2(f32x2(nm4.x, nm4.y), f32x2(lj, lj));
+          Bc[j][1] = add2(f32x2(nm4.z, nm4.w), f32x2(lj, lj));
+        }
+        wait<kN>(s, B_SF + g, (n >> 1) & 1, p);
+        tc_fence_after();
+        // y[i][k]: key lane / 4 + 8 i, row my_rows + k
+        float y[4][4];
+        {
+          uint32_t hi[2][8], lo[2][8];
+          const uint32_t src = tmem + lane_off + 4 * kN + g * 2 * kN + hr * kR;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            tmem_load_16x16(src + ((uint32_t)(16 * j) << 16), hi[j]);
+            tmem_load_16x16(src + ((uint32_t)(16 * j) << 16) + kN, lo[j]);
+          }
+          tmem_wait_ld();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar<kN>(s, B_SE + g));
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int j = i >> 1, r = (i & 1) * 2 + k * 4;
+              const uint64_t acc =
+                  add2(f32x2(__uint_as_float(hi[j][r]), __uint_as_float(hi[j][r + 1])),
+                       f32x2(__uint_as_float(lo[j][r]), __uint_as_float(lo[j][r + 1])));
+              f32x2_split(fma2(acc, A[j][k], Bc[j][k]), y[i][2 * k], y[i][2 * k + 1]);
+            }
+        }
+        if ((t + 1) * kTile > all_see) {
+          // a key that a row does not see weighs nothing, whatever its slot holds
+          const int4 l4 = *reinterpret_cast<const int4*>(lim + my_rows);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int k_abs = t * kTile + q4 * 32 + (lane >> 2) + 8 * i;
+            if (k_abs >= l4.x) y[i][0] = -INFINITY;
+            if (k_abs >= l4.y) y[i][1] = -INFINITY;
+            if (k_abs >= l4.z) y[i][2] = -INFINITY;
+            if (k_abs >= l4.w) y[i][3] = -INFINITY;
+          }
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx = fmax3(fmax3(mx, y[i][0], y[i][1]), y[i][2], y[i][3]);
+        const bool first = t == it.t_begin;
+        if (soft_or<kN>(first || mx > kTop)) {
+          // ---- set or move the references: O must not be written to meanwhile ----------------
+          if (!first) {
+            wait<kN>(s, B_PE + (n - 1) % C::kPBufs, ((n - 1) / C::kPBufs) & 1, p);
+            tc_fence_after();
+          }
+          float* xm = reinterpret_cast<float*>(s.ptr + C::kOffP + pb * 2 * C::kPHalf);   // [4][kN]
+          {
+            float4 m;
+            m.x = fmaxf(fmax3(y[0][0], y[1][0], y[2][0]), y[3][0]);
+            m.y = fmaxf(fmax3(y[0][1], y[1][1], y[2][1]), y[3][1]);
+            m.z = fmaxf(fmax3(y[0][2], y[1][2], y[2][2]), y[3][2]);
+            m.w = fmaxf(fmax3(y[0][3], y[1][3], y[2][3]), y[3][3]);
+#pragma unroll
+            for (int o = 4; o <= 16; o <<= 1) {
+              m.x = fmaxf(m.x, __shfl_xor_sync(0xffffffffu, m.x, o));
+              m.y = fmaxf(m.y, __shfl_xor_sync(0xffffffffu, m.y, o));
+              m.z = fmaxf(m.z, __shfl_xor_sync(0xffffffffu, m.z, o));
+              m.w = fmaxf(m.w, __shfl_xor_sync(0xffffffffu, m.w, o));
+            }
+            if (lane < 4) *reinterpret_cast<float4*>(xm + q4 * kN + my_rows) = m;
+          }
+          soft_sync<kN>();
+          if (st < kN) {
+            const float m = fmaxf(fmaxf(xm[st], xm[kN + st]), fmaxf(xm[2 * kN + st], xm[3 * kN + st]));
+            float by = 0.f;
+            if (m != -INFINITY && (first || m > kMove)) by = kPlace - m;
+            shift[st] = by;
+            row_nm[st] += by;
+          }
+          soft_sync<kN>();
+          if (!first) {
+            // O^T, columns = rows: 64 of its columns for each group of 16 rows' warps
+#pragma unroll 1
+            for (int c32 = 0; c32 < 2; ++c32) {
+              const uint32_t col = (uint32_t)(hr * 64 + c32 * 32);
+              if (!__any_sync(0xffffffffu, shift[col % kN + lane] != 0.f)) continue;
+              uint32_t v[32];
+              tmem_ld32(tmem + lane_off + col, v);
+              tmem_wait_ld();
+              const float4* by = reinterpret_cast<const float4*>(shift + col % kN);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float4 f = by[k];
+                v[4 * k] = __float_as_uint(__uint_as_float(v[4 * k]) * fast_exp2(f.x));
+                v[4 * k + 1] = __float_as_uint(__uint_as_float(v[4 * k + 1]) * fast_exp2(f.y));
+                v[4 * k + 2] = __float_as_uint(__uint_as_float(v[4 * k + 2]) * fast_exp2(f.z));
+                v[4 * k + 3] = __float_as_uint(__uint_as_float(v[4 * k + 3]) * fast_exp2(f.w));
+              }
+              tmem_st32(tmem + lane_off + col, v);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+          }
+          const float4 by = *reinterpret_cast<const float4*>(shift + my_rows);
+          nm4 = *reinterpret_cast<const float4*>(row_nm + my_rows);
+          const uint64_t b01 = f32x2(fast_exp2(by.x), fast_exp2(by.y));
+          const uint64_t b23 = f32x2(fast_exp2(by.z), fast_exp2(by.w));
+          l01 = mul2(l01, b01);
+          l23 = mul2(l23, b23);
+          w01 = mul2(w01, b01);
+          w23 = mul2(w23, b23);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            y[i][0] += by.x;
+            y[i][1] += by.y;
+            y[i][2] += by.z;
+            y[i][3] += by.w;
+          }
+        }
+        // ---- weights, their sums, and their two 8-bit parts ------------------------------------
+        // In half precision (11 bits): h = the value rounded to e5m2, that is to its upper byte;
+        // the residue is exact, and goes to e4m3.
+        uint32_t ph[4], pl[4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          uint64_t s01 = 0, s23 = 0;
+#pragma unroll
+          for (int i = 2 * j; i < 2 * j + 2; ++i) {
+            const float e0 = fast_exp2(y[i][0]), e1 = fast_exp2(y[i][1]);
+            const float e2 = fast_exp2(y[i][2]), e3 = fast_exp2(y[i][3]);
+            s01 = add2(s01, f32x2(e0, e1));
+            s23 = add2(s23, f32x2(e2, e3));
+            const uint32_t u = half2_of(e0, e1), v = half2_of(e2, e3);
+            const uint32_t hu = (u + 0x00800080u) & 0xff00ff00u, hv = (v + 0x00800080u) & 0xff00ff00u;
+            ph[i] = __byte_perm(hu, hv, 0x7531);
+            pl[i] = e4m3x2_of_half2(sub_half2(u, hu)) | e4m3x2_of_half2(sub_half2(v, hv)) << 16;
+          }
+          const uint64_t ij = f32x2(inv_g[j], inv_g[j]);
+          l01 = fma2(s01, ij, l01);
+          l23 = fma2(s23, ij, l23);
+          w01 = add2(w01, s01);
+          w23 = add2(w23, s23);
+        }
+        wait<kN>(s, B_PE + pb, ((n / C::kPBufs) + 1) & 1, p);
+        {
+          // lane l gives the address of row l % 8 of matrix l / 8: key 32 q4 + l, its 16 bytes hr
+          const uint32_t dst = s.base + C::kOffP + pb * 2 * C::kPHalf + key * kN +
+                               16 * (hr ^ (kN == 64 ? (key >> 1) & 3 : (key >> 2) & 1));
+          stmatrix_x4(dst, ph);
+          stmatrix_x4(dst + C::kPHalf, pl);
+        }
+        if (t * kTile + key >= all_see) {
+          // a weight of 0 does not keep a NaN out of O (0 * NaN): behind the request's last key,
+          // where slots may hold anything, a key's values become 0; a key that only some
+          // rows see loses its NaN (the rows that see it have a NaN score, so their whole
+          // output is NaN in any case).  The row's four chunks are shared out to the groups.
+          const bool gone = t * kTile + key >= it.keys;
+          constexpr int kShare = 64 / kN;
+#pragma unroll 1
+          for (int c = 0; c < kShare; ++c) {
+            const int vs = (int)((4 * n + kShare * hr + c) % C::kSlots);
+            uint4* row = reinterpret_cast<uint4*>(s.ptr + C::kOffK + vs * kChunkBytes + key * 128);
+#pragma unroll 1
+            for (int j = 0; j < 8; ++j) {
+              uint4 v = gone ? make_uint4(0, 0, 0, 0) : row[j];
+              v.x &= ~__vcmpeq4(v.x & 0x7f7f7f7fu, 0x7f7f7f7fu);
+              v.y &= ~__vcmpeq4(v.y & 0x7f7f7f7fu, 0x7f7f7f7fu);
+              v.z &= ~__vcmpeq4(v.z & 0x7f7f7f7fu, 0x7f7f7f7fu);
+              v.w &= ~__vcmpeq4(v.w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+              row[j] = v;
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar<kN>(s, B_PF + pb));
+      }
+
+      out_b = it.b;
+      out_single = it.single;
+      out_part = it.t_begin == 0 ? 1 : 0;
+      if (st < kN) out_nm = row_nm[st];            // written by this thread
+      pending = true;
+      have = !soft_or<kN>(*s.abort != 0) && it.next(p);
     }
     if (__any_sync(0xffffffffu, bad_scale) && lane == 0) atomicOr(p.status, MLA_STATUS_BAD_SCALE);
   }
