@@ -687,7 +687,7 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
     const int q4 = warp & 3, hr = (warp - 4) >> 2;
     const int c4 = lane & 3;
     const int my_rows = hr * kR + 4 * c4;
-    const int key = q4 * 32 + lane;                // the key whose cache row this thread scrubs
+    const int key = q4 * 32 + lane;                // the key whose 16 bytes of P^T this thread addresses
     const int st = tid - 128;
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
     float* row_a = reinterpret_cast<float*>(s.ptr + C::kOffRow);     // log2 units per unit of S
@@ -1048,26 +1048,28 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
           stmatrix_x4(dst, ph);
           stmatrix_x4(dst + C::kPHalf, pl);
         }
-        if (t * kTile + key >= all_see) {
+        if (t * kTile + q4 * 32 + 32 > all_see) {
           // a weight of 0 does not keep a NaN out of O (0 * NaN): behind the request's last key,
           // where slots may hold anything, a key's values become 0; a key that only some
           // rows see loses its NaN (the rows that see it have a NaN score, so their whole
-          // output is NaN in any case).  The row's four chunks are shared out to the groups.
-          const bool gone = t * kTile + key >= it.keys;
+          // output is NaN in any case).  Four keys a time, eight lanes to a key's 128 bytes of a
+          // chunk; the four chunks are shared out to the groups of rows.
           constexpr int kShare = 64 / kN;
 #pragma unroll 1
-          for (int c = 0; c < kShare; ++c) {
-            const int vs = (int)((4 * n + kShare * hr + c) % C::kSlots);
-            uint4* row = reinterpret_cast<uint4*>(s.ptr + C::kOffK + vs * kChunkBytes + key * 128);
-#pragma unroll 1
-            for (int j = 0; j < 8; ++j) {
-              uint4 v = gone ? make_uint4(0, 0, 0, 0) : row[j];
+          for (int i = 0; i < 8 * kShare; ++i) {
+            const int k = q4 * 32 + (i & 7) * 4 + (lane >> 3), k_abs = t * kTile + k;
+            if (k_abs < all_see) continue;
+            const uint32_t vs = (4 * n + kShare * hr + (i >> 3)) % C::kSlots;
+            uint4* at16 = reinterpret_cast<uint4*>(s.ptr + C::kOffK + vs * kChunkBytes + k * 128) + (lane & 7);
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (k_abs < it.keys) {
+              v = *at16;
               v.x &= ~__vcmpeq4(v.x & 0x7f7f7f7fu, 0x7f7f7f7fu);
               v.y &= ~__vcmpeq4(v.y & 0x7f7f7f7fu, 0x7f7f7f7fu);
               v.z &= ~__vcmpeq4(v.z & 0x7f7f7f7fu, 0x7f7f7f7fu);
               v.w &= ~__vcmpeq4(v.w & 0x7f7f7f7fu, 0x7f7f7f7fu);
-              row[j] = v;
             }
+            *at16 = v;
           }
         }
         fence_proxy_async_smem();
