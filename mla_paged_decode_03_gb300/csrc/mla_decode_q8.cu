@@ -31,7 +31,8 @@
 // and one of rope dims each, chunk by chunk as PV frees them), warp 1 issues the QK products and
 // warp 2 the PV products, each when its inputs have come (one warp for both in a fixed order
 // waits for the later of two inputs; one that polls both takes issue slots from the softmax
-// warps of its scheduler), warp 3 only fills its group, the others take 32 keys and 16 rows each:
+// warps of its scheduler), warp 3 walks the schedule and
+// passes the block's segments on, the others take 32 keys and 16 rows each:
 // they read S^T, scale, mask, exponentiate and write P^T; they also prepare Q and write the output.
 //
 // Bounds: few rows by the cache's bytes; 64 rows by shared-memory bandwidth: a tile's
@@ -78,6 +79,13 @@ constexpr int kR = 16;                     // query rows per softmax warp
 // and of the excess that moves a reference when some row's weights pass the first
 constexpr float kTop = 12.f, kPlace = 5.f, kMove = 7.f;
 
+// One segment of a block: tiles [t_begin, t_end) of a request's unit (b < 0: no more).
+struct __align__(16) Seg {
+  int b, t_begin, t_end, keys;    // keys: of the unit
+  int cap, g, rank, single;       // the request's lengths; 1: the segment is the whole unit
+};
+constexpr int kSegRing = 4;
+
 template <int kN>
 struct Cfg {
   static constexpr int kSoftWarps = 4 * (kN / kR);         // 4 x 32 keys, kR rows each
@@ -94,7 +102,8 @@ struct Cfg {
   static constexpr int kOffBar = kOffP + kPBufs * 2 * kPHalf;
   static constexpr int kOffRow = kOffBar + 384;            // four words for each row (softmax warps)
   static constexpr int kOffMisc = kOffRow + 16 * kN;       // tmem base, abort, scan result
-  static constexpr int kSmem = kOffMisc + 48 + 1024;       // + alignment slack
+  static constexpr int kOffSeg = kOffMisc + 48;            // Seg[kSegRing]
+  static constexpr int kSmem = kOffSeg + 32 * kSegRing + 1024;   // + alignment slack
   static constexpr uint32_t kTmemCols = 8 * kN;            // O^T 4 kN, S^T 2 x 2 kN
   static_assert(kOffK % 1024 == 0 && kOffRope % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms");
   static_assert(kSmem <= 232448, "shared memory of a block");
@@ -112,7 +121,9 @@ enum Bar : int {
   B_QF = 30,       // the segment's Q written (the softmax warps)
   B_DRAIN = 31,    // [2] the QK / PV warp's last operations
   B_NEVER = 33,    // never arrived at (tests of the timeout path)
-  B_COUNT = 34
+  B_GF = 34,       // [4] a segment has been written
+  B_GE = 38,       // [4] and read by every role (three warps and the softmax warps)
+  B_COUNT = 42
 };
 
 struct Params {
@@ -296,32 +307,37 @@ __device__ __forceinline__ void pv_mma(uint32_t d, uint64_t a, uint64_t bh, uint
 __device__ __forceinline__ int shard_of(const Params& p, int b) {
   return (int)__umulhi((unsigned)b, p.shard_mul);
 }
-// Keys that row r (0-based within the request's q_len*H rows) of request b sees: the shard's
-// share of the row's global prefix, at most its keys.
-__device__ __forceinline__ int row_keys(const Params& p, int b, int r) {
+// A request's keys on its shard, its global length and its rank.
+struct Lens {
+  int cap, g, rank;
+};
+__device__ __forceinline__ Lens lens_of(const Params& p, int b) {
   const int sh = shard_of(p, b);
-  int keys = max(min(__ldg(p.seq_lens + b), p.max_blocks * p.bs), 0);
-  if (p.causal) {
-    const int i = (int)fdiv((unsigned)r, p.div_H);
-    const int g = max(max(__ldg(p.gseq + (b - sh * p.shard_B)), 0) - (p.q_len - 1 - i), 0);
-    const int q = (int)fdiv((unsigned)g, p.div_span);
-    const int over = g - q * p.span - (p.rank + sh) * p.il;
-    keys = min(keys, q * p.il + min(max(over, 0), p.il));
-  }
-  return keys;
+  Lens n;
+  n.cap = max(min(__ldg(p.seq_lens + b), p.max_blocks * p.bs), 0);
+  n.g = p.causal ? max(__ldg(p.gseq + (b - sh * p.shard_B)), 0) : 0;
+  n.rank = p.rank + sh;
+  return n;
+}
+// Keys that row r (0-based within the request's q_len*H rows) sees: the shard's share of the
+// row's global prefix, at most its keys.
+__device__ __forceinline__ int row_keys(const Params& p, const Lens& n, int r) {
+  if (!p.causal) return n.cap;
+  const int i = (int)fdiv((unsigned)r, p.div_H);
+  const int g = max(n.g - (p.q_len - 1 - i), 0);
+  const int q = (int)fdiv((unsigned)g, p.div_span);
+  const int over = g - q * p.span - n.rank * p.il;
+  return min(n.cap, q * p.il + min(max(over, 0), p.il));
 }
 template <int kN>
-__device__ __forceinline__ int unit_keys(const Params& p, int b, int rt) {
-  return row_keys(p, b, min((rt + 1) * kN, p.rows) - 1);     // its last row sees the most
+__device__ __forceinline__ int unit_keys(const Params& p, const Lens& n, int rt) {
+  return row_keys(p, n, min((rt + 1) * kN, p.rows) - 1);     // its last row sees the most
 }
-template <int kN>
-__device__ __forceinline__ int unit_tiles(const Params& p, int b, int rt) {
-  return (unit_keys<kN>(p, b, rt) + kTile - 1) / kTile;
-}
+__device__ __forceinline__ int tiles_of(int keys) { return (keys + kTile - 1) / kTile; }
 // A request's length on the split line: its tiles after the start-up share.
 template <int kN>
 __device__ __forceinline__ unsigned int req_span(const Params& p, int b) {
-  const int nt = unit_tiles<kN>(p, b, p.row_tiles - 1);
+  const int nt = tiles_of(unit_keys<kN>(p, lens_of(p, b), p.row_tiles - 1));
   return nt > 0 ? (unsigned)(nt + p.seg_tiles) : 0u;
 }
 // floor(T * c / G) for 0 <= c <= G (G <= 2^15)
@@ -334,40 +350,41 @@ __device__ __forceinline__ int owner_of(const Params& p, unsigned int x, unsigne
   return (int)((((unsigned long long)x + 1) * (unsigned)p.groups - 1) / T);
 }
 
-// One block's segments (request, tile range) in order; each role walks its own copy.
+// The block's segments in order (walked by one warp, which passes them on).
 template <int kN>
 struct SegIter {
-  int b, rt, grp;
-  int t_begin, t_end, keys, nt;
+  int rt, grp;
+  int nt, req_nt;                 // tiles of the unit, of the request (of its last unit)
   unsigned int g0, g_end;         // the request's first tile and the range's end on the line
-  bool single;                    // the segment covers its whole unit
+  Seg seg;
 
+  // request seg.b from tile tb of it on
   __device__ bool set(const Params& p, int tb) {
-    keys = unit_keys<kN>(p, b, rt);
-    nt = (keys + kTile - 1) / kTile;
+    const Lens n = lens_of(p, seg.b);
+    req_nt = tiles_of(unit_keys<kN>(p, n, p.row_tiles - 1));
+    seg.keys = unit_keys<kN>(p, n, rt);
+    seg.cap = n.cap;
+    seg.g = n.g;
+    seg.rank = n.rank;
+    nt = tiles_of(seg.keys);
     int te = nt;
     // a range may end inside the start-up share, before the request's first tile
     if (!p.whole_units) te = min(te, (int)(g_end - g0));
     if (tb >= te) return false;
-    t_begin = tb;
-    t_end = te;
-    single = tb == 0 && te == nt;
+    seg.t_begin = tb;
+    seg.t_end = te;
+    seg.single = tb == 0 && te == nt;
     return true;
   }
   __device__ bool next(const Params& p) {
-    if (p.whole_units) {
-      for (b += p.groups; b < p.B; b += p.groups)
-        if (set(p, 0)) return true;
-      return false;
-    }
     for (;;) {
-      const unsigned int g = g0 + unit_tiles<kN>(p, b, p.row_tiles - 1) + p.seg_tiles;
-      if (g >= g_end) return false;
-      int nb = b + 1;
-      while (nb < p.B && req_span<kN>(p, nb) == 0) ++nb;
-      if (nb >= p.B) return false;
-      b = nb;
-      g0 = g;
+      if (!p.whole_units) {
+        // past the request; one without a tile has no place on the line
+        if (req_nt > 0) g0 += req_nt + p.seg_tiles;
+        if (g0 >= g_end) return false;
+      }
+      seg.b += p.whole_units ? p.groups : 1;
+      if (seg.b >= p.B) return false;
       if (set(p, 0)) return true;
     }
   }
@@ -377,13 +394,14 @@ struct SegIter {
     rt = blockIdx.x - grp * p.row_tiles;
     if (p.whole_units) {
       g0 = g_end = 0;
-      b = grp - p.groups;
-      return next(p);
+      seg.b = grp;
+      if (seg.b >= p.B) return false;
+      return set(p, 0) || next(p);
     }
     const unsigned int a = range_start(p, T, grp);
     g_end = range_start(p, T, grp + 1);
     if (a >= g_end || scan[0] < 0) return false;
-    b = scan[0];
+    seg.b = scan[0];
     g0 = (unsigned)scan[1];
     return set(p, a > g0 ? (int)(a - g0) : 0) || next(p);
   }
@@ -404,6 +422,19 @@ __device__ __forceinline__ bool wait(const Ctx& s, int i, uint32_t parity, const
   return mbar_wait(bar<kN>(s, i), parity, s.abort, p.status, p.wait_ns);
 }
 __device__ __forceinline__ bool warp_all(bool ok) { return __all_sync(0xffffffffu, ok); }
+
+// The i-th segment of the block, for one warp; false after the last one or when a wait gave up.
+template <int kN>
+__device__ __forceinline__ bool take_segment(const Ctx& s, uint32_t i, const Params& p, Seg& seg) {
+  const uint32_t slot = i % kSegRing;
+  const bool ok = warp_all(wait<kN>(s, B_GF + slot, (i / kSegRing) & 1, p));
+  const int4* src = reinterpret_cast<const int4*>(s.ptr + Cfg<kN>::kOffSeg) + 2 * slot;
+  const int4 a = src[0], b = src[1];
+  seg = Seg{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar<kN>(s, B_GE + slot));
+  return ok && seg.b >= 0;
+}
 
 // ---------------------------------------------------------------------------------------------
 template <int kN>
@@ -430,7 +461,8 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
     *s.abort = 0;
     for (int i = 0; i < B_COUNT; ++i) {
       const bool by_warps = i == B_SE || i == B_SE + 1 || i == B_PF || i == B_PF + 1 || i == B_QF;
-      mbar_init(bar<kN>(s, i), by_warps ? C::kSoftWarps : 1);
+      const bool by_all = i >= B_GE && i < B_GE + kSegRing;
+      mbar_init(bar<kN>(s, i), by_all ? C::kSoftWarps + 3 : by_warps ? C::kSoftWarps : 1);
     }
     fence_mbar_init();
   }
@@ -493,7 +525,9 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
   const uint32_t tmem = misc[0];
   if (blockIdx.x == 0 && tid == 0 && !p.whole_units) p.hdr[0] = T;
 
-  SegIter<kN> it;
+  const int rt = (int)(blockIdx.x - fdiv(blockIdx.x, p.div_rt) * (unsigned)p.row_tiles);   // this block's units
+  Seg it;
+  uint32_t nseg = 0;                        // segments taken
   if (warp == 0) {
     // ================= loads: per tile four latent chunks and the rope chunk ====================
     const int nbox = kTile / p.box_rows;
@@ -502,8 +536,7 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
     int slot = 0;
     uint32_t kpar = 1;                      // a slot's first use passes at once
     long long chunks = 0, ropes = 0;
-    if (it.first(p, T, s_scan)) {
-      do {
+    while (ok && take_segment<kN>(s, nseg++, p, it)) {
         const int32_t* btrow = p.bt + (long long)it.b * p.bt_stride;
         // cache row of the segment's box i; a missing or invalid page becomes a row past the
         // cache, which TMA fills with zeros
@@ -527,14 +560,11 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
         // up to a segment later
         if (lane == 0) {
           const int sh = shard_of(p, it.b);
-          const long long row = (long long)(it.b - sh * p.shard_B) * p.rows + it.rt * kN;
+          const long long row = (long long)(it.b - sh * p.shard_B) * p.rows + rt * kN;
           asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.q + row * kD),
-                       "r"(min(kN, p.rows - it.rt * kN) * kD * 2)
+                       "r"(min(kN, p.rows - rt * kN) * kD * 2)
                        : "memory");
         }
-        // the owner of a unit's first tile records which groups hold the unit
-        if (lane == 0 && it.t_begin == 0 && !p.whole_units)
-          p.meta[it.b * p.row_tiles + it.rt] = make_int2(it.grp, owner_of(p, it.g0 + it.nt - 1, T));
         for (int t = it.t_begin; t < it.t_end && ok; ++t) {
           if (t * nbox >= i0 + 32) {
             i0 += 32;
@@ -575,7 +605,6 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
             tma_load_2d(s.base + C::kOffRope + lane * box_rope, &rmap, kDv, y, bar<kN>(s, B_RF));
           ++ropes;
         }
-      } while (ok && warp_all(*s.abort == 0) && it.next(p));
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.status, MLA_STATUS_BAD_PAGE);
     if (*s.abort && lane == 0) {
@@ -590,12 +619,10 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
     bool ok = true;
     if (p.stall_test) ok = warp_all(wait<kN>(s, B_NEVER, 0, p));
     long long n = 0;
-    int slot = 0, nseg = 0;
+    int slot = 0;
     uint32_t par = 0;
-    if (ok && it.first(p, T, s_scan)) {
-      do {
-        ok = warp_all(wait<kN>(s, B_QF, (uint32_t)(nseg & 1), p));
-        ++nseg;
+    while (ok && take_segment<kN>(s, nseg++, p, it)) {
+        ok = warp_all(wait<kN>(s, B_QF, (nseg - 1) & 1, p));
         for (int t = it.t_begin; t < it.t_end && ok; ++t, ++n) {
           const int g = (int)(n & 1);
           ok = warp_all(wait<kN>(s, B_SE + g, (uint32_t)(((n >> 1) + 1) & 1), p));   // S^T read
@@ -620,7 +647,6 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
           mma_commit_warp(bar<kN>(s, B_RE));
           mma_commit_warp(bar<kN>(s, B_SF + g));
         }
-      } while (ok && warp_all(*s.abort == 0) && it.next(p));
     }
     // every operation issued here completes before the block tears down
     mma_commit_warp(bar<kN>(s, B_DRAIN));
@@ -632,8 +658,7 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
     bool ok = true;
     long long n = 0;
     int slot = 0;
-    if (it.first(p, T, s_scan)) {
-      do {
+    while (ok && take_segment<kN>(s, nseg++, p, it)) {
         for (int t = it.t_begin; t < it.t_end; ++t, ++n) {
           const int pb = (int)(n % C::kPBufs);
           ok = warp_all(wait<kN>(s, B_PF + pb, (uint32_t)((n / C::kPBufs) & 1), p));
@@ -673,10 +698,30 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
             run(std::integral_constant<int, 1>{});
           mma_commit_warp(bar<kN>(s, B_PE + pb));
         }
-      } while (ok && warp_all(*s.abort == 0) && it.next(p));
     }
     mma_commit_warp(bar<kN>(s, B_DRAIN + 1));
     mbar_wait_drain(bar<kN>(s, B_DRAIN + 1), 0);
+  } else if (warp == 3) {
+    // ================= the block's segments, a few ahead of the other roles ======================
+    SegIter<kN> walk;
+    bool have = walk.first(p, T, s_scan);
+    for (;; ++nseg) {
+      const uint32_t slot = nseg % kSegRing;
+      if (!warp_all(wait<kN>(s, B_GE + slot, ((nseg / kSegRing) + 1) & 1, p))) break;
+      if (!have) walk.seg.b = -1;
+      if (lane == 0) {
+        int4* dst = reinterpret_cast<int4*>(s.ptr + C::kOffSeg) + 2 * slot;
+        dst[0] = make_int4(walk.seg.b, walk.seg.t_begin, walk.seg.t_end, walk.seg.keys);
+        dst[1] = make_int4(walk.seg.cap, walk.seg.g, walk.seg.rank, walk.seg.single);
+        mbar_arrive(bar<kN>(s, B_GF + slot));
+      }
+      __syncwarp();
+      if (!have) break;
+      // the owner of a unit's first tile records which groups hold the unit
+      if (lane == 0 && walk.seg.t_begin == 0 && !p.whole_units)
+        p.meta[walk.seg.b * p.row_tiles + rt] = make_int2(walk.grp, owner_of(p, walk.g0 + walk.nt - 1, T));
+      have = walk.next(p);
+    }
   } else if (warp >= 4) {
     // ================= softmax ===================================================================
     // A warp has keys 32 q4 .. + 31 of a tile and rows 16 hr .. + 15 of the unit.  S^T is read in
@@ -723,7 +768,7 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
     // before the output of the one before is written, which waits for its last PV.
     uint64_t w01 = 0, w23 = 0;                     // sums of the four rows' weights, this thread's keys
     uint64_t l01 = 0, l23 = 0;                     // sums of the four rows' weights / S, this thread's keys
-    bool have = it.first(p, T, s_scan), pending = false;
+    bool have = !soft_or<kN>(!take_segment<kN>(s, nseg++, p, it)), pending = false;
     // of the segment whose output is to be written: its request, whether it is a whole unit, which of
     // the block's two partials it is
     int out_b = 0, out_part = 0;
@@ -731,7 +776,7 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
     float out_nm = 0.f;
     for (;;) {
       if (have) {
-        const int row0 = it.rt * kN;
+        const int row0 = rt * kN;
         btrow = p.bt + (long long)it.b * p.bt_stride;
         at = it.t_begin * kTile + q4 * 32 + (lane & 16);
         pg = (int)fdiv((unsigned)at, p.div_bs);
@@ -752,7 +797,7 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
           sc_next = scale_in(page_first);
           step();
           page_next = page_here();
-          if (st < kN) lim[st] = row0 + st < p.rows ? row_keys(p, it.b, row0 + st) : it.keys;
+          if (st < kN) lim[st] = row0 + st < p.rows ? row_keys(p, Lens{it.cap, it.g, it.rank}, row0 + st) : it.keys;
           uint32_t m2 = 0;
 #pragma unroll
           for (int i = 0; i < 9; ++i) {
@@ -802,7 +847,7 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
         }
       }
       if (pending) {
-        const int out_row0 = it.rt * kN;
+        const int out_row0 = rt * kN;
         const long long out_row = (long long)out_b * p.rows + out_row0, out_slot = 2ll * blockIdx.x + out_part;
         // ---- the segment's output ---------------------------------------------------------------
         wait<kN>(s, B_PE + (n - 1) % C::kPBufs, ((n - 1) / C::kPBufs) & 1, p);
@@ -1078,11 +1123,12 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
       }
 
       out_b = it.b;
-      out_single = it.single;
+      out_single = it.single != 0;
       out_part = it.t_begin == 0 ? 1 : 0;
       if (st < kN) out_nm = row_nm[st];            // written by this thread
       pending = true;
-      have = !soft_or<kN>(*s.abort != 0) && it.next(p);
+      // (all of them go on together, also when a wait of some gave up)
+      have = !soft_or<kN>(!take_segment<kN>(s, nseg++, p, it) || *s.abort != 0);
     }
     if (__any_sync(0xffffffffu, bad_scale) && lane == 0) atomicOr(p.status, MLA_STATUS_BAD_SCALE);
   }
@@ -1110,7 +1156,7 @@ __global__ void __launch_bounds__(256) mla_q8_combine_kernel(const Params p) {
   if (threadIdx.x == 0) {
     if (rt == 0 && rb == 0 && __ldg(p.seq_lens + b) > p.max_blocks * p.bs)
       atomicOr(p.status, MLA_STATUS_SEQ_TOO_LONG);
-    const int nt = unit_tiles<kN>(p, b, rt);
+    const int nt = tiles_of(unit_keys<kN>(p, lens_of(p, b), rt));
     int2 m = make_int2(0, 0);
     if (nt > 0 && !p.whole_units) {
       m = p.meta[u];
