@@ -794,9 +794,6 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
           uint4 w[9];                              // elements 8 (l8 + 8 i) .. + 7
 #pragma unroll
           for (int i = 0; i < 9; ++i) w[i] = valid ? __ldg(src + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
-          sc_next = scale_in(page_first);
-          step();
-          page_next = page_here();
           if (st < kN) lim[st] = row0 + st < p.rows ? row_keys(p, Lens{it.cap, it.g, it.rank}, row0 + st) : it.keys;
           uint32_t m2 = 0;
 #pragma unroll
@@ -845,6 +842,9 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(bar<kN>(s, B_QF));
         }
+        sc_next = scale_in(page_first);
+        step();
+        page_next = page_here();
       }
       if (pending) {
         const int out_row0 = rt * kN;
@@ -1100,21 +1100,25 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
           // output is NaN in any case).  Four keys a time, eight lanes to a key's 128 bytes of a
           // chunk; the four chunks are shared out to the groups of rows.
           constexpr int kShare = 64 / kN;
+          const int k0 = t * kTile + q4 * 32;      // of the warp's 32 keys: those before `some` are
+          const int some = max(all_see - k0, 0), gone = max(it.keys - k0, 0);   // seen by every row
 #pragma unroll 1
-          for (int i = 0; i < 8 * kShare; ++i) {
-            const int k = q4 * 32 + (i & 7) * 4 + (lane >> 3), k_abs = t * kTile + k;
-            if (k_abs < all_see) continue;
-            const uint32_t vs = (4 * n + kShare * hr + (i >> 3)) % C::kSlots;
-            uint4* at16 = reinterpret_cast<uint4*>(s.ptr + C::kOffK + vs * kChunkBytes + k * 128) + (lane & 7);
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (k_abs < it.keys) {
-              v = *at16;
+          for (int c = 0; c < kShare; ++c) {
+            const uint32_t vs = (4 * n + kShare * hr + c) % C::kSlots;
+            uint4* row = reinterpret_cast<uint4*>(s.ptr + C::kOffK + vs * kChunkBytes + q4 * 32 * 128) + (lane & 7);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int k = 4 * i + (lane >> 3);
+              if (k >= gone) row[8 * k] = make_uint4(0, 0, 0, 0);
+            }
+            for (int k = some + (lane >> 3); k < min(gone, 32); k += 4) {
+              uint4 v = row[8 * k];
               v.x &= ~__vcmpeq4(v.x & 0x7f7f7f7fu, 0x7f7f7f7fu);
               v.y &= ~__vcmpeq4(v.y & 0x7f7f7f7fu, 0x7f7f7f7fu);
               v.z &= ~__vcmpeq4(v.z & 0x7f7f7f7fu, 0x7f7f7f7fu);
               v.w &= ~__vcmpeq4(v.w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+              row[8 * k] = v;
             }
-            *at16 = v;
           }
         }
         fence_proxy_async_smem();
