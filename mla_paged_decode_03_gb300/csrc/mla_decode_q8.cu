@@ -175,6 +175,11 @@ __device__ __forceinline__ float fast_log2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -263,39 +268,58 @@ __host__ __device__ constexpr uint32_t idesc_f8(int N, uint32_t b_format, bool m
 }
 constexpr uint32_t kSwizzle64B = 4, kSwizzle32B = 6;
 
-// kSteps products along K under one election, descriptors 32 bytes apart (K-major rows).
+// A matrix descriptor (sm100.cuh) is passed as its two words: the high one holds the strides and
+// the swizzle and is the same for every operand of a kind, the low one moves with the address
+// (in 16 bytes).  Built whole for each product, descriptors took more instructions than anything
+// else the issuing warps do.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr) {
+  return ((addr & 0x3FFFFu) >> 4) | (1u << 16);           // leading stride 16 bytes (not used here)
+}
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo, uint32_t swizzle) {
+  return (sbo >> 4) | (1u << 14) | (swizzle << 29);
+}
+
+// kSteps products along K under one election, operands 32 bytes apart (K-major rows).
 template <int kSteps>
-__device__ __forceinline__ void qk_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void qk_mma(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc,
+                                       uint32_t acc) {
   static_assert(kSteps == 2 || kSteps == 4, "chunks of 64 or 128 dims");
   if constexpr (kSteps == 4)
     asm volatile(
-        "{\n .reg .pred p, t, e;\n .reg .b64 x, y;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 t, %5, 0;\n"
-        " elect.sync _|e, 0xffffffff;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
-        " add.u64 x, %1, 2; add.u64 y, %2, 2;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, t;\n"
-        " add.u64 x, %1, 4; add.u64 y, %2, 4;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, t;\n"
-        " add.u64 x, %1, 6; add.u64 y, %2, 6;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, t;\n"
-        "}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(1u)
+        "{\n .reg .pred p, t, e;\n .reg .b32 u, v;\n .reg .b64 x, y;\n setp.ne.b32 p, %5, 0;\n"
+        " setp.ne.b32 t, %6, 0;\n elect.sync _|e, 0xffffffff;\n"
+        " mov.b64 x, {%1, %3}; mov.b64 y, {%2, %3};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %4, p;\n"
+        " add.u32 u, %1, 2; add.u32 v, %2, 2; mov.b64 x, {u, %3}; mov.b64 y, {v, %3};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %4, t;\n"
+        " add.u32 u, %1, 4; add.u32 v, %2, 4; mov.b64 x, {u, %3}; mov.b64 y, {v, %3};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %4, t;\n"
+        " add.u32 u, %1, 6; add.u32 v, %2, 6; mov.b64 x, {u, %3}; mov.b64 y, {v, %3};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %4, t;\n"
+        "}" ::"r"(d), "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc), "r"(1u)
         : "memory");
   else
     asm volatile(
-        "{\n .reg .pred p, t, e;\n .reg .b64 x, y;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 t, %5, 0;\n"
-        " elect.sync _|e, 0xffffffff;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
-        " add.u64 x, %1, 2; add.u64 y, %2, 2;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, t;\n"
-        "}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(1u)
+        "{\n .reg .pred p, t, e;\n .reg .b32 u, v;\n .reg .b64 x, y;\n setp.ne.b32 p, %5, 0;\n"
+        " setp.ne.b32 t, %6, 0;\n elect.sync _|e, 0xffffffff;\n"
+        " mov.b64 x, {%1, %3}; mov.b64 y, {%2, %3};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %4, p;\n"
+        " add.u32 u, %1, 2; add.u32 v, %2, 2; mov.b64 x, {u, %3}; mov.b64 y, {v, %3};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %4, t;\n"
+        "}" ::"r"(d), "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc), "r"(1u)
         : "memory");
 }
 
 // One step of 32 keys: the weights' e5m2 part (bh, ih) and their e4m3 part (bl, il).
-__device__ __forceinline__ void pv_mma(uint32_t d, uint64_t a, uint64_t bh, uint64_t bl, uint32_t ih,
-                                       uint32_t il, uint32_t acc) {
+__device__ __forceinline__ void pv_mma(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t bh, uint32_t bl,
+                                       uint32_t b_hi, uint32_t ih, uint32_t il, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p, t, e;\n setp.ne.b32 p, %6, 0;\n setp.ne.b32 t, %7, 0;\n"
+      "{\n .reg .pred p, t, e;\n .reg .b64 x, y, z;\n setp.ne.b32 p, %8, 0;\n setp.ne.b32 t, %9, 0;\n"
       " elect.sync _|e, 0xffffffff;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %4, p;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %3, %5, t;\n"
-      "}" ::"r"(d), "l"(a), "l"(bh), "l"(bl), "r"(ih), "r"(il), "r"(acc), "r"(1u)
+      " mov.b64 x, {%1, %2}; mov.b64 y, {%3, %5}; mov.b64 z, {%4, %5};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %6, p;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, z, %7, t;\n"
+      "}" ::"r"(d), "r"(a), "r"(a_hi), "r"(bh), "r"(bl), "r"(b_hi), "r"(ih), "r"(il), "r"(acc), "r"(1u)
       : "memory");
 }
 
@@ -616,6 +640,7 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
   } else if (warp == 1) {
     // ================= QK ========================================================================
     constexpr uint32_t id_qk = idesc_f8(2 * kN, 0, false);
+    const uint32_t ka = desc_lo(s.base + C::kOffK), qa = desc_lo(s.base);
     bool ok = true;
     if (p.stall_test) ok = warp_all(wait<kN>(s, B_NEVER, 0, p));
     long long n = 0;
@@ -632,8 +657,8 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
             ok = ok && warp_all(wait<kN>(s, B_KF + slot, par, p));
             if (!ok) break;
             tc_fence_after();
-            qk_mma<4>(d, smem_desc(s.base + C::kOffK + slot * kChunkBytes, 16, 1024, kSwizzle128B),
-                      smem_desc(s.base + c * C::kQChunk, 16, 1024, kSwizzle128B), id_qk, c != 0);
+            qk_mma<4>(d, ka + slot * (kChunkBytes / 16), qa + c * (C::kQChunk / 16),
+                      desc_hi(1024, kSwizzle128B), id_qk, c != 0);
             if (++slot == C::kSlots) {
               slot = 0;
               par ^= 1u;
@@ -642,8 +667,7 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
           ok = ok && warp_all(wait<kN>(s, B_RF, (uint32_t)(n & 1), p));
           if (!ok) break;
           tc_fence_after();
-          qk_mma<2>(d, smem_desc(s.base + C::kOffRope, 16, 512, kSwizzle64B),
-                    smem_desc(s.base + C::kOffQRope, 16, 512, kSwizzle64B), id_qk, 1);
+          qk_mma<2>(d, desc_lo(s.base + C::kOffRope), qa + C::kOffQRope / 16, desc_hi(512, kSwizzle64B), id_qk, 1);
           mma_commit_warp(bar<kN>(s, B_RE));
           mma_commit_warp(bar<kN>(s, B_SF + g));
         }
@@ -654,7 +678,8 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
   } else if (warp == 2) {
     // ================= PV ========================================================================
     constexpr uint32_t id_hi = idesc_f8(kN, 1, true), id_lo = idesc_f8(kN, 0, true);
-    constexpr uint32_t kPSwizzle = kN == 64 ? kSwizzle64B : kSwizzle32B;
+    constexpr uint32_t p_hi = desc_hi(8 * kN, kN == 64 ? kSwizzle64B : kSwizzle32B);
+    const uint32_t va = desc_lo(s.base + C::kOffK), pa0 = desc_lo(s.base + C::kOffP);
     bool ok = true;
     long long n = 0;
     int slot = 0;
@@ -664,13 +689,11 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
           ok = warp_all(wait<kN>(s, B_PF + pb, (uint32_t)((n / C::kPBufs) & 1), p));
           if (!ok) break;
           tc_fence_after();
-          const uint32_t pa = s.base + C::kOffP + pb * 2 * C::kPHalf;
+          const uint32_t pa = pa0 + pb * (2 * C::kPHalf / 16);
           // chunk c of the values (dims 128 c ..), step k of 32 keys
           auto product = [&](int c, int k) {
-            const uint32_t va = s.base + C::kOffK + slot * kChunkBytes + k * 4096;
-            pv_mma(tmem + c * kN, smem_desc(va, 16, 1024, kSwizzle128B),
-                   smem_desc(pa + k * 32 * kN, 16, 8 * kN, kPSwizzle),
-                   smem_desc(pa + C::kPHalf + k * 32 * kN, 16, 8 * kN, kPSwizzle), id_hi, id_lo,
+            pv_mma(tmem + c * kN, va + slot * (kChunkBytes / 16) + k * (4096 / 16), desc_hi(1024, kSwizzle128B),
+                   pa + k * (32 * kN / 16), pa + (C::kPHalf + k * 32 * kN) / 16, p_hi, id_hi, id_lo,
                    (t == it.t_begin && k == 0) ? 0u : 1u);
           };
           auto release = [&]() {
@@ -936,7 +959,7 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
           sc = 1.f;
         }
         // t' = acc * (a S) + (log2 S - m), for the group of keys i = 0, 1 and that of 2, 3
-        const float lg = fast_log2(sc), inv = __frcp_rn(sc);
+        const float lg = fast_log2(sc), inv = fast_rcp(sc);
         uint64_t A[2][2], Bc[2][2];
         float inv_g[2];
 #pragma unroll
@@ -1077,7 +1100,7 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
             const uint32_t u = half2_of(e0, e1), v = half2_of(e2, e3);
             const uint32_t hu = (u + 0x00800080u) & 0xff00ff00u, hv = (v + 0x00800080u) & 0xff00ff00u;
             ph[i] = __byte_perm(hu, hv, 0x7531);
-            pl[i] = e4m3x2_of_half2(sub_half2(u, hu)) | e4m3x2_of_half2(sub_half2(v, hv)) << 16;
+            pl[i] = __byte_perm(e4m3x2_of_half2(sub_half2(u, hu)), e4m3x2_of_half2(sub_half2(v, hv)), 0x5410);
           }
           const uint64_t ij = f32x2(inv_g[j], inv_g[j]);
           l01 = fma2(s01, ij, l01);
