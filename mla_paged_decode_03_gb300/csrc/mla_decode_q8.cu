@@ -31,9 +31,9 @@
 // and one of rope dims each, chunk by chunk as PV frees them), warp 1 issues the QK products and
 // warp 2 the PV products, each when its inputs have come (one warp for both in a fixed order
 // waits for the later of two inputs; one that polls both takes issue slots from the softmax
-// warps of its scheduler), warp 3 walks the schedule and
-// passes the block's segments on, the others take 32 keys and 16 rows each:
-// they read S^T, scale, mask, exponentiate and write P^T; they also prepare Q and write the output.
+// warps of its scheduler), warp 3 walks the schedule, passes the
+// block's segments on and looks the tiles' scales up, the others take 32 keys and 16 rows each: they
+// read S^T, scale, mask, exponentiate and write P^T; they also prepare Q and write the output.
 //
 // Bounds: few rows by the cache's bytes; 64 rows by shared-memory bandwidth: a tile's
 // QK reads 18 x (4 + 4) KB and its PV 32 x (4 + 2) KB, with TMA's and P's writes 426 KB, 3,330
@@ -103,7 +103,8 @@ struct Cfg {
   static constexpr int kOffRow = kOffBar + 384;            // four words for each row (softmax warps)
   static constexpr int kOffMisc = kOffRow + 16 * kN;       // tmem base, abort, scan result
   static constexpr int kOffSeg = kOffMisc + 48;            // Seg[kSegRing]
-  static constexpr int kSmem = kOffSeg + 32 * kSegRing + 1024;   // + alignment slack
+  static constexpr int kOffScale = kOffSeg + 32 * kSegRing;   // float4 [2 tiles][8 groups of 16 keys]
+  static constexpr int kSmem = kOffScale + 256 + 1024;     // + alignment slack
   static constexpr uint32_t kTmemCols = 8 * kN;            // O^T 4 kN, S^T 2 x 2 kN
   static_assert(kOffK % 1024 == 0 && kOffRope % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms");
   static_assert(kSmem <= 232448, "shared memory of a block");
@@ -112,8 +113,8 @@ struct Cfg {
 enum Bar : int {
   B_KF = 0,        // [10] latent chunk loaded
   B_KE = 10,       // [10] its PV done
-  B_SF = 20,       // [2] S^T written
-  B_SE = 22,       // [2] S^T read (the softmax warps)
+  B_SF = 20,       // [2] S^T and the tile's scales written
+  B_SE = 22,       // [2] both read (the softmax warps)
   B_PF = 24,       // [2] P^T written (the softmax warps)
   B_PE = 26,       // [2] its PV done
   B_RF = 28,       // rope chunk loaded
@@ -486,7 +487,8 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
     for (int i = 0; i < B_COUNT; ++i) {
       const bool by_warps = i == B_SE || i == B_SE + 1 || i == B_PF || i == B_PF + 1 || i == B_QF;
       const bool by_all = i >= B_GE && i < B_GE + kSegRing;
-      mbar_init(bar<kN>(s, i), by_all ? C::kSoftWarps + 3 : by_warps ? C::kSoftWarps : 1);
+      const int count = by_all ? C::kSoftWarps + 3 : by_warps ? C::kSoftWarps : i == B_SF || i == B_SF + 1 ? 2 : 1;
+      mbar_init(bar<kN>(s, i), count);
     }
     fence_mbar_init();
   }
@@ -725,26 +727,78 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
     mma_commit_warp(bar<kN>(s, B_DRAIN + 1));
     mbar_wait_drain(bar<kN>(s, B_DRAIN + 1), 0);
   } else if (warp == 3) {
-    // ================= the block's segments, a few ahead of the other roles ======================
+    // ================= the schedule and the tiles' scales =========================================
+    // Passes the block's segments on, one ahead of the tiles, and writes each tile's eight scales
+    // (lane l < 8: those of keys 16 l ..), with their logarithms and reciprocals, for the softmax
+    // warps, which otherwise looked them up 4 (kN / 16) times over.
     SegIter<kN> walk;
-    bool have = walk.first(p, T, s_scan);
-    for (;; ++nseg) {
+    const int groups_per_page = p.bs / MLA_Q8_GROUP;
+    bool have = walk.first(p, T, s_scan), bad_scale = false, ok = true;
+    uint32_t n = 0;
+    // the next segment's description into the ring (b = -1: no more)
+    auto publish = [&]() {
       const uint32_t slot = nseg % kSegRing;
-      if (!warp_all(wait<kN>(s, B_GE + slot, ((nseg / kSegRing) + 1) & 1, p))) break;
-      if (!have) walk.seg.b = -1;
+      ok = ok && warp_all(wait<kN>(s, B_GE + slot, ((nseg / kSegRing) + 1) & 1, p));
+      if (!ok) return;
+      ++nseg;
       if (lane == 0) {
         int4* dst = reinterpret_cast<int4*>(s.ptr + C::kOffSeg) + 2 * slot;
-        dst[0] = make_int4(walk.seg.b, walk.seg.t_begin, walk.seg.t_end, walk.seg.keys);
+        dst[0] = make_int4(have ? walk.seg.b : -1, walk.seg.t_begin, walk.seg.t_end, walk.seg.keys);
         dst[1] = make_int4(walk.seg.cap, walk.seg.g, walk.seg.rank, walk.seg.single);
         mbar_arrive(bar<kN>(s, B_GF + slot));
+        // the owner of a unit's first tile records which groups hold the unit
+        if (have && walk.seg.t_begin == 0 && !p.whole_units)
+          p.meta[walk.seg.b * p.row_tiles + rt] = make_int2(walk.grp, owner_of(p, walk.g0 + walk.nt - 1, T));
       }
       __syncwarp();
-      if (!have) break;
-      // the owner of a unit's first tile records which groups hold the unit
-      if (lane == 0 && walk.seg.t_begin == 0 && !p.whole_units)
-        p.meta[walk.seg.b * p.row_tiles + rt] = make_int2(walk.grp, owner_of(p, walk.g0 + walk.nt - 1, T));
+    };
+    publish();
+    while (have && ok) {
+      it = walk.seg;
+      // group l of a tile is at slot `at` of the request: page pg, offset off; the page is looked up
+      // two tiles ahead, the scale one
+      const int32_t* btrow = p.bt + (long long)it.b * p.bt_stride;
+      const int at_end = lane < 8 ? min(it.keys, it.t_end * kTile) : 0;
+      int at = it.t_begin * kTile + lane * MLA_Q8_GROUP;
+      int pg = (int)fdiv((unsigned)at, p.div_bs), off = at - pg * p.bs;
+      auto page_here = [&]() { return at < at_end ? __ldg(btrow + pg) : -1; };
+      auto scale_in = [&](int page) {
+        return page >= 0 && page < p.num_blocks
+                   ? __ldg(p.scales + (long long)page * groups_per_page + (off >> 4))
+                   : 1.f;
+      };
+      auto step = [&]() {
+        at += kTile;
+        pg += p.tile_pages;
+        off += p.tile_rest;
+        if (off >= p.bs) {
+          off -= p.bs;
+          ++pg;
+        }
+      };
+      float sc_next = scale_in(page_here());
+      step();
+      int page_next = page_here();
       have = walk.next(p);
+      publish();
+      for (int t = it.t_begin; t < it.t_end && ok; ++t, ++n) {
+        const uint32_t g = n & 1;
+        float sc = sc_next;
+        sc_next = scale_in(page_next);
+        step();
+        page_next = page_here();
+        if (!(sc >= MLA_Q8_SCALE_MIN && sc <= MLA_Q8_SCALE_MAX)) {
+          bad_scale = true;
+          sc = 1.f;
+        }
+        const float4 v = make_float4(sc, fast_log2(sc), fast_rcp(sc), 0.f);
+        ok = warp_all(wait<kN>(s, B_SE + g, ((n >> 1) + 1) & 1, p));
+        if (lane < 8) reinterpret_cast<float4*>(s.ptr + C::kOffScale)[g * 8 + lane] = v;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar<kN>(s, B_SF + g));
+      }
     }
+    if (__any_sync(0xffffffffu, bad_scale) && lane == 0) atomicOr(p.status, MLA_STATUS_BAD_SCALE);
   } else if (warp >= 4) {
     // ================= softmax ===================================================================
     // A warp has keys 32 q4 .. + 31 of a tile and rows 16 hr .. + 15 of the unit.  S^T is read in
@@ -762,31 +816,7 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
     float* row_nm = row_a + kN;                                      // minus the reference
     float* shift = row_nm + kN;                                      // its move; later 1 / l
     int* lim = reinterpret_cast<int*>(shift + kN);                   // keys the row sees
-    const int groups_per_page = p.bs / MLA_Q8_GROUP;
-    bool bad_scale = false;
     uint32_t n = 0;
-    // ---- scales: lanes 0-15 and 16-31 follow one group of 16 keys each, two steps ahead (the page
-    // of tile t + 2, the scale of tile t + 1); (pg, off) is the place of the group in the request,
-    // moved by 128 keys a tile
-    const int32_t* btrow = nullptr;
-    int at = 0, at_end = 0, pg = 0, off = 0, page_next = -1;
-    float sc_next = 1.f;
-    auto page_here = [&]() { return at < at_end ? __ldg(btrow + pg) : -1; };
-    auto scale_in = [&](int page) {
-      return page >= 0 && page < p.num_blocks
-                 ? __ldg(p.scales + (long long)page * groups_per_page + (off >> 4))
-                 : 1.f;
-    };
-    auto step = [&]() {
-      at += kTile;
-      pg += p.tile_pages;
-      off += p.tile_rest;
-      if (off >= p.bs) {
-        off -= p.bs;
-        ++pg;
-      }
-    };
-
     // The order of a block's segments: Q of the next one is prepared (and its first QK may run)
     // before the output of the one before is written, which waits for its last PV.
     uint64_t w01 = 0, w23 = 0;                     // sums of the four rows' weights, this thread's keys
@@ -800,12 +830,6 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
     for (;;) {
       if (have) {
         const int row0 = rt * kN;
-        btrow = p.bt + (long long)it.b * p.bt_stride;
-        at = it.t_begin * kTile + q4 * 32 + (lane & 16);
-        pg = (int)fdiv((unsigned)at, p.div_bs);
-        off = at - pg * p.bs;
-        at_end = min(it.keys, it.t_end * kTile);
-        const int page_first = page_here();
         // ---- Q: eight lanes a row, hi and lo written where the products read them --------------
         {
           static_assert(kN == 4 * C::kSoftWarps, "four rows a warp");
@@ -865,9 +889,6 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(bar<kN>(s, B_QF));
         }
-        sc_next = scale_in(page_first);
-        step();
-        page_next = page_here();
       }
       if (pending) {
         const int out_row0 = rt * kN;
@@ -950,31 +971,11 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
       w01 = w23 = l01 = l23 = 0;
       for (int t = it.t_begin; t < it.t_end; ++t, ++n) {
         const uint32_t g = n & 1, pb = n % C::kPBufs;
-        float sc = sc_next;
-        sc_next = scale_in(page_next);
-        step();
-        page_next = page_here();
-        if (!(sc >= MLA_Q8_SCALE_MIN && sc <= MLA_Q8_SCALE_MAX)) {
-          bad_scale = true;
-          sc = 1.f;
-        }
-        // t' = acc * (a S) + (log2 S - m), for the group of keys i = 0, 1 and that of 2, 3
-        const float lg = fast_log2(sc), inv = fast_rcp(sc);
-        uint64_t A[2][2], Bc[2][2];
-        float inv_g[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float sj = __shfl_sync(0xffffffffu, sc, 16 * j), lj = __shfl_sync(0xffffffffu, lg, 16 * j);
-          inv_g[j] = __shfl_sync(0xffffffffu, inv, 16 * j);
-          A[j][0] = mul2(f32x2(a4.x, a4.y), f32x2(sj, sj));
-          A[j][1] = mul2(f32x2(a4.z, a4.w), f32x2(sj, sj));
-          Bc[j][0] = add2(f32x2(nm4.x, nm4.y), f32x2(lj, lj));
-          Bc[j][1] = add2(f32x2(nm4.z, nm4.w), f32x2(lj, lj));
-        }
         wait<kN>(s, B_SF + g, (n >> 1) & 1, p);
         tc_fence_after();
         // y[i][k]: key lane / 4 + 8 i, row my_rows + k
         float y[4][4];
+        float inv_g[2];
         {
           uint32_t hi[2][8], lo[2][8];
           const uint32_t src = tmem + lane_off + 4 * kN + g * 2 * kN + hr * kR;
@@ -982,6 +983,17 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
           for (int j = 0; j < 2; ++j) {
             tmem_load_16x16(src + ((uint32_t)(16 * j) << 16), hi[j]);
             tmem_load_16x16(src + ((uint32_t)(16 * j) << 16) + kN, lo[j]);
+          }
+          // t' = acc * (a S) + (log2 S - m), for the group of keys i = 0, 1 and that of 2, 3
+          uint64_t A[2][2], Bc[2][2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float4 v = reinterpret_cast<const float4*>(s.ptr + C::kOffScale)[g * 8 + 2 * q4 + j];
+            inv_g[j] = v.z;
+            A[j][0] = mul2(f32x2(a4.x, a4.y), f32x2(v.x, v.x));
+            A[j][1] = mul2(f32x2(a4.z, a4.w), f32x2(v.x, v.x));
+            Bc[j][0] = add2(f32x2(nm4.x, nm4.y), f32x2(v.y, v.y));
+            Bc[j][1] = add2(f32x2(nm4.z, nm4.w), f32x2(v.y, v.y));
           }
           tmem_wait_ld();
           tc_fence_before();
@@ -1157,7 +1169,6 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
       // (all of them go on together, also when a wait of some gave up)
       have = !soft_or<kN>(!take_segment<kN>(s, nseg++, p, it) || *s.abort != 0);
     }
-    if (__any_sync(0xffffffffu, bad_scale) && lane == 0) atomicOr(p.status, MLA_STATUS_BAD_SCALE);
   }
 
   // ---- teardown ----------------------------------------------------------------------------------
