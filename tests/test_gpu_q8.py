@@ -197,6 +197,30 @@ def test_step_tables_strided_table_and_other_stream():
     assert (wide[:, :2] == -7).all() and (wide[:, 5:] == -7).all() and t.free_state.tolist() == [3, 1]
 
 
+def test_tables_and_store_on_a_given_stream():
+    """Everything on a stream passed to the calls, which allocate their outputs there."""
+    s = torch.cuda.Stream()
+    rows = torch.randn(3, 17, 576, generator=torch.Generator().manual_seed(8)).to(torch.bfloat16).to(DEV)
+    table = torch.full((3, 3), -1, dtype=torch.int32, device=DEV)
+    ring, state, zero, new = i32([3, 4, 5, 6, 7]), i32([0, 5]), i32([0, 0, 0]), i32([5, 0, 17])
+    cache, scales = new_pool(8, 16, poison=False)
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        t = M.cp_step_tables(zero, zero, new, table, ring, state, 16, 17, stream=s)
+        M.cp_store_q8(rows, zero, t.total_lens, table, cache, scales, stream=s)
+        got.append(t)
+        torch.full((1 << 16,), -7, dtype=torch.int32, device=DEV)
+    s.synchronize()
+    for t in got:
+        assert t.total_lens.tolist() == [5, 0, 17] and t.free_state.tolist() == [3, 2]
+        assert t.positions[2].tolist() == list(range(17)) and t.slots[0, 0, :5].tolist() == list(range(48, 53))
+    want, ws = Q.ref_store_q8(n64(rows), [0, 0, 0], [5, 0, 17], np.maximum(n64(table), 0), np.zeros((8, 16, 576)),
+                              np.ones((8, 1)), 1, 0)
+    assert np.array_equal(n64(cache.float()), want) and np.array_equal(n64(scales), ws)
+    assert M.device_status() == 0
+
+
 def test_step_tables_refuses_outputs_over_inputs():
     a, tab, ring, st = i32([0, 0]), torch.zeros(2, 2, dtype=torch.int32, device=DEV), i32([1, 2]), i32([0, 2])
     with pytest.raises(M.MlaError):
