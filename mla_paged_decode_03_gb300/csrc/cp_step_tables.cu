@@ -40,7 +40,7 @@ struct Params {
   int32_t* state_out;
   unsigned int vbs;                      // block_size * cp_size
   int block_size, cp_size, cp_rank, n_ranks, il;
-  FastDiv div_vbs, div_n, div_il, div_cp;
+  FastDiv div_vbs, div_n, div_il, div_cp, div_span, div_req;
   int32_t *total, *seq;
   long long *positions, *slots;
   int req;                               // requests per block (1 when chunks > 1)
@@ -55,22 +55,23 @@ __device__ __forceinline__ unsigned int fdiv(unsigned int n, const FastDiv& f) {
 
 // What phase 2 needs of a request.
 struct Req {
-  int ctx, fresh;        // cached tokens; new tokens (0 when not granted)
+  int ctx, fresh, total; // cached tokens; new tokens (0 when not granted); length after the step
   int held, keep, take;  // pages held before, kept, taken
   int take0, give0;      // pages taken / given back by the requests before
 };
 
 // Inclusive prefix sum over the block; `total` receives the block's sum.
-__device__ __forceinline__ long long block_scan(long long v, long long* s_warp, long long& total) {
+__device__ __forceinline__ unsigned long long block_scan(unsigned long long v, unsigned long long* s_warp,
+                                                         unsigned long long& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(0xffffffffu, v, o);
+    const unsigned long long u = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += u;
   }
   if (lane == 31) s_warp[warp] = v;
   __syncthreads();
-  long long before = 0;
+  unsigned long long before = 0;
   total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
@@ -83,7 +84,7 @@ __device__ __forceinline__ long long block_scan(long long v, long long* s_warp, 
 
 __global__ void __launch_bounds__(kThreads) cp_step_tables_kernel(const Params p) {
   __shared__ Req s_req[kMaxReq];
-  __shared__ long long s_warp[kWarps];
+  __shared__ unsigned long long s_warp[kWarps];
   const int tid = threadIdx.x;
   const int first = p.chunks > 1 ? blockIdx.x / p.chunks : blockIdx.x * p.req;
   const int chunk = p.chunks > 1 ? blockIdx.x - first * p.chunks : 0;
@@ -98,15 +99,14 @@ __global__ void __launch_bounds__(kThreads) cp_step_tables_kernel(const Params p
   }
 
   // ---- phase 1: the prefix sums, up to this block's requests (block 0: over all, for the
-  // ring's new state) -----------------------------------------------------------------
-  long long taken = 0, asked = 0, given = 0;         // of the requests before this round
+  // ring's new state).  In most steps of a decode loop no request of a round of 256 takes or gives
+  // a page, and the sums are skipped. ---------------------------------------------------------
+  unsigned long long asked = 0, moved = 0;           // before this round: pages asked for; given, taken
   const int upto = blockIdx.x == 0 ? p.B : last;
   for (int base = 0; base < upto; base += kThreads) {
     const int b = base + tid;
-    Req r = {};
-    long long want = 0;
     bool fits = true, bad = false;
-    int held = 0, prev = 0, ctx = 0, fresh = 0;
+    int held = 0, prev = 0, ctx = 0, fresh = 0, take = 0;
     if (b < upto) {
       prev = __ldg(p.prev + b);
       ctx = __ldg(p.ctx + b);
@@ -124,57 +124,74 @@ __global__ void __launch_bounds__(kThreads) cp_step_tables_kernel(const Params p
       const long long len = (long long)ctx + fresh;
       fits = len <= 0x7fffffffLL;
       if (fits) {
-        want = fdiv((unsigned int)len + p.vbs - 1u, p.div_vbs);
-        fits = want <= p.max_blocks;
+        const unsigned int want = fdiv((unsigned int)len + p.vbs - 1u, p.div_vbs);
+        fits = want <= (unsigned int)p.max_blocks;
+        if (fits) take = max((int)want - held, 0);
       }
     }
-    const long long take = fits ? max(want - held, 0LL) : 0;
-    long long sum;
-    const long long incl = asked + block_scan(take, s_warp, sum);
-    const bool granted = fits && (take == 0 || incl <= count);
+    bool granted = fits;
+    unsigned long long asked0 = asked;               // asked for by the requests before b
+    if (__syncthreads_or(take > 0)) {
+      unsigned long long sum;
+      const unsigned long long incl = asked + block_scan((unsigned long long)take, s_warp, sum);
+      granted = fits && (take == 0 || incl <= (unsigned long long)count);
+      asked0 = incl - take;
+      asked += sum;
+    }
     const int total = granted ? ctx + fresh : min(ctx, prev);
     const int keep = min((int)fdiv((unsigned int)total + p.vbs - 1u, p.div_vbs), p.max_blocks);
-    const long long give = max(held - keep, 0);
-    long long gsum, tsum;
-    const long long gincl = given + block_scan(give, s_warp, gsum);
-    block_scan(granted ? take : 0, s_warp, tsum);
-    asked += sum;
-    given += gsum;
-    taken += tsum;
+    const int give = max(held - keep, 0);
+    // pages given (upper half) and taken (lower): neither exceeds the ring in consistent tables
+    const unsigned long long mine = (unsigned long long)give << 32 | (unsigned)(granted ? take : 0);
+    unsigned long long moved0 = moved;
+    if (__syncthreads_or(mine != 0)) {
+      unsigned long long sum;
+      moved0 += block_scan(mine, s_warp, sum) - mine;
+      moved += sum;
+    }
     if (b >= first && b < last) {
+      Req r;
+      const unsigned int give0 = (unsigned int)(moved0 >> 32);
       r.ctx = ctx;
       r.fresh = granted ? fresh : 0;
       r.held = held;
       r.keep = keep;
-      r.take = granted ? (int)take : 0;
-      r.take0 = (int)min(incl - take, (long long)p.cap);
-      r.give0 = (int)min(gincl - give, (long long)p.cap);
+      r.take = granted ? take : 0;
+      r.take0 = (int)min(asked0, (unsigned long long)p.cap);
+      r.give0 = (int)min(give0, (unsigned int)p.cap);
+      r.total = total;
       s_req[b - first] = r;
       if (chunk == 0) {
         if (bad) flags |= MLA_STATUS_BAD_STEP;
         if (!fits) flags |= MLA_STATUS_SEQ_TOO_LONG;
         if (fits && !granted) flags |= MLA_STATUS_OUT_OF_PAGES;
-        if (gincl > p.cap - count && give > 0) flags |= MLA_STATUS_BAD_STEP;
+        if (give > 0 && (unsigned long long)give0 + give > (unsigned long long)(p.cap - count))
+          flags |= MLA_STATUS_BAD_STEP;
         p.total[b] = total;
-        if (p.seq != nullptr) {
-          const unsigned int q = (unsigned int)total / (unsigned int)(p.cp_size * (long long)p.il);
-          const long long rem = total - (long long)q * p.cp_size * p.il;
-          for (int k = 0; k < p.n_ranks; ++k) {
-            const long long over = rem - (long long)(p.cp_rank + k) * p.il;
-            p.seq[(long long)k * p.B + b] =
-                (int)((long long)q * p.il + min(max(over, 0LL), (long long)p.il));
-          }
-        }
       }
     }
   }
   if (blockIdx.x == 0 && tid == 0) {
     // pages that a full ring cannot hold were dropped (below)
-    const int h = head + (int)taken;
-    p.state_out[0] = h >= p.cap ? h - p.cap : h;
-    p.state_out[1] = count - (int)taken + (int)min(given, (long long)(p.cap - count));
+    const unsigned int taken = (unsigned int)moved, given = (unsigned int)(moved >> 32);
+    const unsigned int h = (unsigned int)head + taken;
+    p.state_out[0] = (int)(h >= (unsigned int)p.cap ? h - p.cap : h);
+    p.state_out[1] = count - (int)taken + (int)min(given, (unsigned int)(p.cap - count));
   }
   __syncthreads();
+
+  // ---- phase 2: shard-local lengths ---------------------------------------------------
+  if (p.seq != nullptr && chunk == 0) {
+    const int reqs = last - first;
+    for (int k = tid; k < reqs * p.n_ranks; k += kThreads) {
+      // (whole blocks of requests have p.req of them; the last may have fewer)
+      const int rk = reqs == p.req ? (int)fdiv((unsigned int)k, p.div_req) : k / reqs, i = k - rk * reqs;
+      const int total = s_req[i].total;
+      const int q = (int)fdiv((unsigned int)total, p.div_span);
+      const int over = total - q * (p.cp_size * p.il) - (p.cp_rank + rk) * p.il;
+      p.seq[(long long)rk * p.B + first + i] = q * p.il + min(max(over, 0), p.il);
+    }
+  }
 
   // ---- phase 2: pages ---------------------------------------------------------------
   auto ring_at = [&](int i) {                        // entry i behind the head, i < cap
@@ -189,13 +206,29 @@ __global__ void __launch_bounds__(kThreads) cp_step_tables_kernel(const Params p
     for (int i = one ? 0 : warp; i < last - first; i += one ? 1 : kWarps) {
       const Req r = s_req[i];
       int32_t* row = p.table + (long long)(first + i) * p.bt_stride;
-      const int k0 = one ? chunk * kThreads + tid : lane;
-      const int step = one ? p.chunks * kThreads : 32;
-      for (int k = k0; k < r.take; k += step) row[r.held + k] = p.ring[ring_at(r.take0 + k)];
-      const int give = r.held - r.keep;
-      for (int k = k0; k < give; k += step) {
-        const long long at = (long long)count + r.give0 + k;
-        if (at < p.cap) p.ring[ring_at((int)at)] = row[r.keep + k];
+      const long long k0 = one ? (long long)chunk * kThreads + tid : lane;
+      const long long step = one ? (long long)p.chunks * kThreads : 32;
+      // eight pages a thread at a time: the loads of a round do not wait for one another
+      constexpr int kAhead = 8;
+      for (long long k = k0; k < r.take; k += kAhead * step) {
+        int v[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+          if (k + j * step < r.take) v[j] = p.ring[ring_at((int)(r.take0 + k + j * step))];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+          if (k + j * step < r.take) row[r.held + k + j * step] = v[j];
+      }
+      // (pages behind a full ring are dropped)
+      const int give = min(r.held - r.keep, max(p.cap - count - r.give0, 0));
+      for (long long k = k0; k < give; k += kAhead * step) {
+        int v[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+          if (k + j * step < give) v[j] = row[r.keep + k + j * step];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+          if (k + j * step < give) p.ring[ring_at((int)(count + r.give0 + k + j * step))] = v[j];
       }
     }
   }
@@ -264,6 +297,7 @@ cudaError_t launch_cp_step_tables(const StepArgs& a, cudaStream_t stream) {
   p.div_n = make_fastdiv((unsigned int)(a.N > 0 ? a.N : 1));
   p.div_il = make_fastdiv((unsigned int)a.interleave);
   p.div_cp = make_fastdiv((unsigned int)a.cp_size);
+  p.div_span = make_fastdiv((unsigned int)(a.cp_size * a.interleave));
   p.total = a.total;
   p.seq = a.seq;
   p.positions = reinterpret_cast<long long*>(a.positions);
@@ -278,6 +312,7 @@ cudaError_t launch_cp_step_tables(const StepArgs& a, cudaStream_t stream) {
   p.req = p.chunks > 1 ? 1 : (a.N > 0 ? (int)(tile / a.N) : kMaxReq);
   if (p.req > kMaxReq) p.req = kMaxReq;
   if (p.req < 1) p.req = 1;
+  p.div_req = make_fastdiv((unsigned int)p.req);
   const long long blocks = p.chunks > 1 ? (long long)a.B * p.chunks : ((long long)a.B + p.req - 1) / p.req;
   cp_step_tables_kernel<<<(unsigned)(blocks > 0 ? blocks : 1), kThreads, 0, stream>>>(p);
   return cudaGetLastError();
