@@ -51,6 +51,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <functional>
 #include <mutex>
 #include <type_traits>
@@ -1296,9 +1297,20 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encoder() {
   return fn;
 }
 
-// Rows per unit: 32 where a request has no more (half the tensor and shared-memory time of a
-// tile), else 64.
-int rows_per_unit(long long rows) { return rows <= 32 ? 32 : 64; }
+// Rows per unit: 32 or 64.  A tile costs a unit of 32 rows 0.69 of what it costs one of 64, so
+// two of them take 1.4 times as long, but their start (Q, first loads) and output are 3 to 4 us
+// shorter.  32 where a request has no more rows (64 x 16 rows of up to 16k keys: 65.8 us,
+// 77.8 with units of 64), and where full tables would give a block fewer than 8 tiles in units
+// of 64 (8 x 128 rows: of 1,024 keys 15.0 / 19.3 us, of 4,096 21.4 / 23.7, of 8,192 29.4 / 30.0);
+// else 64 (16 x 80 rows of 16,384 keys 68.4 / 67.3 us, 64 x 128 of 32,768 560 / 405).
+int rows_per_unit(long long B, long long rows, long long max_keys, int num_sms) {
+  if (rows <= 32) return 32;
+  if ((rows + 31) / 32 > num_sms) return 64;
+  return B * ((rows + 63) / 64) * ((max_keys + kTile - 1) / kTile) < 8LL * num_sms ? 32 : 64;
+}
+int rows_per_unit(const DecodeArgs& a) {
+  return rows_per_unit(a.B, (long long)a.H * a.q_len, (long long)a.max_blocks * a.block_size, a.num_sms);
+}
 
 size_t ws_bytes(size_t units, int blocks, int kN) {
   size_t b = 256;                                                    // header
@@ -1336,7 +1348,7 @@ cudaError_t launch(const CUtensorMap& kmap, const CUtensorMap& rmap, const Param
 }  // namespace
 
 bool q8_supported(const DecodeArgs& a) {
-  const int rows = a.H * a.q_len, n = rows_per_unit(rows);
+  const int rows = a.H * a.q_len, n = rows_per_unit(a);
   const long long tiles = (rows + n - 1) / n;
   if (tiles > a.num_sms) return false;              // a block for every row tile of a request
   // token and cache row numbers, with the look-ahead of the page window, fit 32 bits
@@ -1350,8 +1362,9 @@ bool q8_supported(const DecodeArgs& a) {
 
 size_t q8_workspace_size(int B, int H, int q_len, int num_sms) {
   const long long rows = (long long)H * q_len;
-  const int n = rows_per_unit(rows);
-  return ws_bytes((size_t)B * ((rows + n - 1) / n), num_sms, n);
+  const size_t a = ws_bytes((size_t)B * ((rows + 31) / 32), num_sms, 32);
+  if (rows <= 32) return a;
+  return std::max(a, ws_bytes((size_t)B * ((rows + 63) / 64), num_sms, 64));   // whichever a call takes
 }
 
 cudaError_t launch_decode_q8(const DecodeArgs& a, cudaStream_t stream) {
@@ -1380,7 +1393,7 @@ cudaError_t launch_decode_q8(const DecodeArgs& a, cudaStream_t stream) {
                                  : (unsigned)((0x100000000ull + (unsigned long long)a.shard_B - 1) /
                                               (unsigned long long)a.shard_B);
   p.rows = a.H * a.q_len;
-  const int n = rows_per_unit(p.rows);
+  const int n = rows_per_unit(a);
   p.row_tiles = (p.rows + n - 1) / n;
   p.units = a.B * p.row_tiles;
   p.box_rows = a.block_size % 128 == 0 ? 128 : a.block_size % 64 == 0 ? 64 : a.block_size % 32 == 0 ? 32 : 16;

@@ -47,11 +47,37 @@ def _clean():
     M.set_decode_kernel(prev)
 
 
-@pytest.fixture(params=["mma", "auto"])
+_extra_columns = 0
+
+
+@pytest.fixture(params=["mma", "units32", "units64"])
 def kernel(request):
+    """The warp-level kernel, and the tcgen05 kernel with units of 32 and (requests of more than
+    32 rows only) of 64 rows."""
+    global _extra_columns
     prev = M.set_decode_kernel(M.KERNEL_MMA if request.param == "mma" else M.KERNEL_AUTO)
+    _extra_columns = 8 * torch.cuda.get_device_properties(DEV).multi_processor_count * 8 \
+        if request.param == "units64" else 0
     yield request.param
+    _extra_columns = 0
     M.set_decode_kernel(prev)
+
+
+@pytest.fixture(params=[32, 64])
+def units(request):
+    """As `kernel`, for tests of the tcgen05 kernel alone."""
+    global _extra_columns
+    _extra_columns = 8 * torch.cuda.get_device_properties(DEV).multi_processor_count * 8 \
+        if request.param == 64 else 0
+    yield request.param
+    _extra_columns = 0
+
+
+def bt32(table):
+    """A block table on the GPU.  The decode takes units of 64 rows when full tables would give
+    every SM eight tiles of 128 keys; that many more columns of 16 slots or more make it do so
+    at any length."""
+    return torch.nn.functional.pad(i32(table), (0, _extra_columns), value=-1)
 
 
 def i32(x):
@@ -501,7 +527,7 @@ def test_decode_matches_oracle(B, H, q_len, G, bs, cp, il, causal, base_e, sprea
         seq = R.ref_local_len(G, cp, rank, il)
         out = torch.full((B * q_len, H, 512), float("nan"), dtype=torch.bfloat16, device=DEV)
         lse = torch.full((B * q_len, H), float("nan"), device=DEV)
-        M.mla_decode_q8(q.to(DEV), cache, scales, i32(table), i32(seq), i32(G), q_len, cp, rank, SCALE,
+        M.mla_decode_q8(q.to(DEV), cache, scales, bt32(table), i32(seq), i32(G), q_len, cp, rank, SCALE,
                         out=out, lse=lse, lse_base_e=base_e, causal=causal, interleave=il)
         assert M.device_status() == 0
         for b in range(B):
@@ -511,11 +537,11 @@ def test_decode_matches_oracle(B, H, q_len, G, bs, cp, il, causal, base_e, sprea
 
 
 @pytest.mark.parametrize("H,q_len", [(32, 1), (33, 1), (13, 5), (64, 2), (129, 1), (7, 16)])
-def test_decode_row_counts_around_a_unit(H, q_len):
+def test_decode_row_counts_around_a_unit(H, q_len, units):
     # 32, 33, 65, 128, 129 and 112 rows: whole units, one row past a unit, odd head counts
     q, G, table, pools = make_case(3, H, q_len, [129, 20, 256], 256, 1, 1, 60 + H)
     cache, scales = gpu_pool(pools[0])
-    out, lse = M.mla_decode_q8(q.to(DEV), cache, scales, i32(table), i32(G), None, q_len, 1, 0, SCALE)
+    out, lse = M.mla_decode_q8(q.to(DEV), cache, scales, bt32(table), i32(G), None, q_len, 1, 0, SCALE)
     assert M.device_status() == 0
     for b in range(3):
         check_request(b, q, out, lse, G, table, pools[0], q_len, 1, 0, 1, True, True)
@@ -566,10 +592,10 @@ def test_decode_many_requests(B, H, q_len, workspace):
         assert bool(((gl - l)[fin].abs() <= 1e-3).all())
 
 
-def test_decode_on_another_stream_than_the_current_one():
+def test_decode_on_another_stream_than_the_current_one(units):
     q, G, table, pools = make_case(2, 64, 2, [300, 900], 64, 1, 1, 61)
     cache, scales = gpu_pool(pools[0])
-    args = (q.to(DEV), cache, scales, i32(table), i32(G), None, 2, 1, 0, SCALE)
+    args = (q.to(DEV), cache, scales, bt32(table), i32(G), None, 2, 1, 0, SCALE)
     want = M.mla_decode_q8(*args)
     s = torch.cuda.Stream()
     torch.cuda.synchronize()
@@ -584,11 +610,11 @@ def test_decode_on_another_stream_than_the_current_one():
 
 
 @pytest.mark.parametrize("B,H,q_len,G", [(2, 128, 2, [700, 2000]), (3, 16, 1, [100, 1, 515])])
-def test_decode_without_workspace_and_without_lse(B, H, q_len, G):
+def test_decode_without_workspace_and_without_lse(B, H, q_len, G, units):
     q, G, table, pools = make_case(B, H, q_len, G, 64, 1, 1, 41)
     cache, scales = gpu_pool(pools[0])
     none = torch.empty(0, dtype=torch.uint8, device=DEV)
-    args = (q.to(DEV), cache, scales, i32(table), i32(G), None, q_len, 1, 0, SCALE)
+    args = (q.to(DEV), cache, scales, bt32(table), i32(G), None, q_len, 1, 0, SCALE)
     out, lse = M.mla_decode_q8(*args, workspace=none)
     for b in range(B):
         check_request(b, q, out, lse, G, table, pools[0], q_len, 1, 0, 1, True, True)
@@ -601,7 +627,7 @@ def test_decode_any_scales(kernel):
     q, G, table, pools = make_case(2, 16, 2, [200, 75], 32, 1, 1, 43, spread=3, pow2=False)
     cache, scales = gpu_pool(pools[0])
     pool = (pools[0][0], n64(scales))
-    out, lse = M.mla_decode_q8(q.to(DEV), cache, scales, i32(table), i32(G), None, 2, 1, 0, SCALE)
+    out, lse = M.mla_decode_q8(q.to(DEV), cache, scales, bt32(table), i32(G), None, 2, 1, 0, SCALE)
     assert M.device_status() == 0
     for b in range(2):
         check_request(b, q, out, lse, G, table, pool, 2, 1, 0, 1, True, True)
@@ -622,7 +648,7 @@ def test_decode_zero_blocks_and_growing_scores(kernel):
         v[pg, sl] = Q.ref_e4m3(k / s[pg, sl // 16])
     cache, scales = gpu_pool((v, s))
     for ws in (None, torch.empty(0, dtype=torch.uint8, device=DEV)):
-        out, lse = M.mla_decode_q8(q.to(DEV), cache, scales, i32(table), i32(G), None, 2, 1, 0, SCALE, workspace=ws)
+        out, lse = M.mla_decode_q8(q.to(DEV), cache, scales, bt32(table), i32(G), None, 2, 1, 0, SCALE, workspace=ws)
         assert M.device_status() == 0
         check_request(0, q, out, lse, G, table, (v, s), 2, 1, 0, 1, True, True)
 
@@ -634,19 +660,19 @@ def test_decode_queries_of_any_size(kernel):
     q[:, :, 5] = 0
     q = q.to(torch.bfloat16)
     cache, scales = gpu_pool(pools[0])
-    out, lse = M.mla_decode_q8(q.to(DEV), cache, scales, i32(table), i32(G), None, 1, 1, 0, SCALE)
+    out, lse = M.mla_decode_q8(q.to(DEV), cache, scales, bt32(table), i32(G), None, 1, 1, 0, SCALE)
     for b in range(2):
         check_request(b, q, out, lse, G, table, pools[0], 1, 1, 0, 1, True, True)
     assert M.device_status() == 0
 
 
-def test_decode_nan_rows_and_nan_keys():
+def test_decode_nan_rows_and_nan_keys(units):
     """A NaN or an infinity in a row of q makes that row NaN, and only it; a NaN in a stored key
     makes the rows that see the key NaN, and only them."""
     for B, H, q_len, G in ((2, 64, 1, [333, 64]), (1, 16, 2, [4000])):
         q, G, table, pools = make_case(B, H, q_len, G, 64, 1, 1, 52)
         cache, scales = gpu_pool(pools[0])
-        args = (cache, scales, i32(table), i32(G), None, q_len, 1, 0, SCALE)
+        args = (cache, scales, bt32(table), i32(G), None, q_len, 1, 0, SCALE)
         out, lse = M.mla_decode_q8(q.to(DEV), *args)
         bad = q.clone()
         bad[0, 0, 7, 100] = float("nan")
@@ -662,7 +688,7 @@ def test_decode_nan_rows_and_nan_keys():
         v, s = pools[0]
         v[table[0, (G - 1) // 32], (G - 1) % 32, 5:576:70] = np.nan
         cache, scales = gpu_pool((v, s))
-        out, lse = M.mla_decode_q8(q.to(DEV), cache, scales, i32(table), i32(Gs), None, 4, 1, 0, SCALE)
+        out, lse = M.mla_decode_q8(q.to(DEV), cache, scales, bt32(table), i32(Gs), None, 4, 1, 0, SCALE)
         assert torch.isnan(out[3]).all() and torch.isnan(lse[3]).all()
         pre = np.concatenate([v[table[0, j]] for j in range(-(-G // 32))])[:G - 1]
         sc = np.concatenate([np.repeat(s[table[0, j]], 16) for j in range(-(-G // 32))])[:G - 1]
@@ -670,12 +696,12 @@ def test_decode_nan_rows_and_nan_keys():
     assert M.device_status() == 0
 
 
-def test_decode_timeout_reports_and_recovers():
+def test_decode_timeout_reports_and_recovers(units):
     """One role of every block first waits for an arrival that never comes, with a limit of 200 us:
     the call returns, reports it, and the next call is right."""
     q, G, table, pools = make_case(2, 128, 2, [3000, 200], 64, 1, 1, 54)
     cache, scales = gpu_pool(pools[0])
-    args = (q.to(DEV), cache, scales, i32(table), i32(G), None, 2, 1, 0, SCALE)
+    args = (q.to(DEV), cache, scales, bt32(table), i32(G), None, 2, 1, 0, SCALE)
     prev, stall = M.set_wait_limit_ns(200_000), M.set_test_stall(True)
     try:
         M.mla_decode_q8(*args)
@@ -698,7 +724,7 @@ def test_decode_bad_scale_and_bad_page_are_flagged(kernel):
         s2 = s.copy()
         s2[table[0, 2]] = bad
         cache, scales = gpu_pool((v, s2))
-        out, lse = M.mla_decode_q8(q.to(DEV), cache, scales, i32(table), i32(G), None, 1, 1, 0, SCALE)
+        out, lse = M.mla_decode_q8(q.to(DEV), cache, scales, bt32(table), i32(G), None, 1, 1, 0, SCALE)
         assert M.device_status() == BAD_SCALE
         s2[table[0, 2]] = 1.0
         check_request(0, q, out, lse, G, table, (v, s2), 1, 1, 0, 1, True, True)
@@ -706,7 +732,7 @@ def test_decode_bad_scale_and_bad_page_are_flagged(kernel):
     for page in (-1, cache.shape[0], 2 ** 31 - 1, -2 ** 31):
         t2 = table.copy()
         t2[0, 2] = page
-        out, lse = M.mla_decode_q8(q.to(DEV), cache, scales, i32(t2), i32(G), None, 1, 1, 0, SCALE)
+        out, lse = M.mla_decode_q8(q.to(DEV), cache, scales, bt32(t2), i32(G), None, 1, 1, 0, SCALE)
         assert M.device_status() == BAD_PAGE
         v2, s2 = v.copy(), s.copy()                       # its keys are read as zeros
         v2[table[0, 2]], s2[table[0, 2]] = 0.0, 1.0
@@ -732,7 +758,7 @@ def test_decode_shards_equals_rank_by_rank(cp, il, causal, kernel):
     scales = torch.cat([gpu_pool(p)[1] for p in pools])
     seq = np.concatenate([R.ref_local_len(G, cp, r, il) for r in range(cp)])
     bt = np.concatenate([table + r * nb for r in range(cp)])
-    out, lse = M.mla_decode_shards_q8(q.to(DEV), cache, scales, i32(bt), i32(seq), i32(G), q_len, cp, SCALE,
+    out, lse = M.mla_decode_shards_q8(q.to(DEV), cache, scales, bt32(bt), i32(seq), i32(G), q_len, cp, SCALE,
                                       causal=causal, interleave=il)
     for r in range(cp):
         for b in range(B):
@@ -790,10 +816,10 @@ def test_decode_on_a_stream_and_in_a_graph():
     assert M.device_status() == 0
 
 
-def test_decode_is_repeatable_and_leaves_its_inputs():
+def test_decode_is_repeatable_and_leaves_its_inputs(units):
     q, G, table, pools = make_case(4, 128, 2, [900, 33, 1500, 400], 64, 1, 1, 51)
     cache, scales = gpu_pool(pools[0])
-    a = (q.to(DEV), cache, scales, i32(table), i32(G), None, 2, 1, 0, SCALE)
+    a = (q.to(DEV), cache, scales, bt32(table), i32(G), None, 2, 1, 0, SCALE)
     ws = M.alloc_workspace_q8(4, 128, 2)
     before = cache.view(torch.uint8).clone()
     o1, l1 = M.mla_decode_q8(*a, workspace=ws)
@@ -802,6 +828,49 @@ def test_decode_is_repeatable_and_leaves_its_inputs():
         o2, l2 = M.mla_decode_q8(*a, workspace=ws)
         assert torch.equal(o1, o2) and torch.equal(l1, l2)
     assert torch.equal(cache.view(torch.uint8), before) and M.device_status() == 0
+
+
+def test_decode_most_rows_a_request_may_have():
+    # as many row tiles of 64 as SMs; one head more is refused
+    sms = torch.cuda.get_device_properties(DEV).multi_processor_count
+    q, G, table, pools = make_case(1, 4 * sms, 16, [150], 64, 1, 1, 55)
+    cache, scales = gpu_pool(pools[0])
+    args = (cache, scales, i32(table), i32(G), None, 16, 1, 0, SCALE)
+    out, lse = M.mla_decode_q8(q.to(DEV), *args)
+    assert M.device_status() == 0
+    check_request(0, q, out, lse, G, table, pools[0], 16, 1, 0, 1, True, True)
+    more = torch.zeros(1, 16, 4 * sms + 1, 576, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(RuntimeError, match="row tiles"):
+        M.mla_decode_q8(more, *args)
+
+
+def test_decode_pages_used_more_than_once(units):
+    # the same page twice in a request, and in two requests
+    q, G, table, pools = make_case(2, 64, 2, [330, 200], 32, 1, 1, 56)
+    table[0, 4], table[0, 9], table[1, 3] = table[0, 1], table[0, 1], table[0, 0]
+    cache, scales = gpu_pool(pools[0])
+    out, lse = M.mla_decode_q8(q.to(DEV), cache, scales, bt32(table), i32(G), None, 2, 1, 0, SCALE)
+    assert M.device_status() == 0
+    for b in range(2):
+        check_request(b, q, out, lse, G, table, pools[0], 2, 1, 0, 1, True, True)
+
+
+def test_decode_two_streams_at_once(units):
+    cases = []
+    for seed, (H, G) in enumerate(((128, [3000, 500, 40]), (16, [2000, 7000, 900]))):
+        q, G, table, pools = make_case(3, H, 2, G, 64, 1, 1, 57 + seed)
+        a = (q.to(DEV), *gpu_pool(pools[0]), bt32(table), i32(G), None, 2, 1, 0, SCALE)
+        cases.append((a, M.mla_decode_q8(*a), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(30):
+        for (a, _, s), g in zip(cases, got):
+            g.append(M.mla_decode_q8(*a, stream=s))
+    torch.cuda.synchronize()
+    for (_, want, _), g in zip(cases, got):
+        for o, l in g:
+            assert torch.equal(o, want[0]) and torch.equal(l, want[1])
+    assert M.device_status() == 0
 
 
 # =============================================================================================
