@@ -1,4 +1,5 @@
-"""ctypes binding of libmla_decode.so (C ABI in include/mla_decode.h).
+"""ctypes binding of libmla_decode.so (C ABI in include/mla_decode.h), and the loader of the native
+binding through which the 8-bit cache's calls go.
 
 Argument marshalling only: every computation happens in the library's CUDA kernels.
 The library must have been built (``mla_paged_decode_03_gb300.build.build()``); there is
@@ -7,6 +8,8 @@ no fallback, and loading fails loudly when the shared object is missing.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
@@ -29,6 +32,7 @@ EXPORTED = ("mla_decode_workspace_size", "mla_decode", "mla_decode_shards", "mla
 
 _lock = threading.Lock()
 _lib = None
+_q8 = None
 
 
 class MlaError(RuntimeError):
@@ -116,6 +120,31 @@ def load() -> ctypes.CDLL:
         lib.mla_abi_version.argtypes = []
         _lib = lib
         return lib
+
+
+def load_q8(tables_type):
+    """The native binding of the 8-bit cache's calls, bound to the library's functions;
+    ``tables_type`` is the tuple type of cp_step_tables' result."""
+    global _q8
+    if _q8 is not None:
+        return _q8
+    lib = load()
+    with _lock:
+        if _q8 is not None:
+            return _q8
+        path = _build.binding_path()
+        if not os.path.exists(path):
+            raise ImportError(
+                f"{path} is missing: build it with mla_paged_decode_03_gb300.build.build() "
+                "(there is no Python fallback)")
+        loader = importlib.machinery.ExtensionFileLoader(_build.BINDING, path)
+        m = importlib.util.module_from_spec(importlib.util.spec_from_loader(_build.BINDING, loader))
+        loader.exec_module(m)
+        m.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in
+                 ("cp_step_tables", "cp_store_q8", "mla_decode_q8", "mla_decode_shards_q8",
+                  "mla_decode_q8_workspace_size")), check, tables_type)
+        _q8 = m
+        return _q8
 
 
 def check(rc: int) -> None:

@@ -10,8 +10,9 @@ share the block table):
                              N, cp, rank, scale)
     # next step: prev = t.total_lens, free_state = t.free_state
 
-Marshalling and checks of arguments only, as in the package's other wrappers.  All tensors
-must live on the current CUDA device.
+Marshalling and checks of arguments only, as in the package's other wrappers, but in a native
+binding (csrc/q8_binding.cpp): these calls' smallest kernels take 3 to 12 us.  All tensors must
+live on the current CUDA device.
 """
 from __future__ import annotations
 
@@ -19,7 +20,7 @@ from typing import NamedTuple, Optional, Tuple
 
 import torch
 
-from . import D_QK, D_V, _lib, _need
+from . import _lib
 
 __all__ = ["Q8_GROUP", "StepTables", "cp_step_tables", "cp_store_q8", "mla_decode_q8",
            "mla_decode_shards_q8", "workspace_size_q8", "alloc_workspace_q8"]
@@ -36,59 +37,6 @@ class StepTables(NamedTuple):
     free_state: torch.Tensor               # int32 [2], the ring's new {head, count}
 
 
-# The checks below cost a call's latency (a small step's kernel takes a few microseconds), so
-# each argument is tested by one expression; only a failing one is looked at again for its error.
-
-def _here(t: torch.Tensor, name: str) -> None:
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, not on the current device "
-                         f"cuda:{torch.cuda.current_device()}")
-
-
-def _refuse(t, name: str, dtype, shape) -> None:
-    """The error of an argument that is not a contiguous ``dtype`` tensor of ``shape`` on the
-    current device."""
-    _need(t, name, dtype)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    _here(t, name)
-    raise ValueError(f"{name} is not usable")
-
-
-def _check(t, name: str, dtype, shape: tuple, dev: int) -> int:
-    """Checks a tensor argument; returns its address."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-            and t.get_device() == dev and t.is_contiguous()):
-        _refuse(t, name, dtype, shape)
-    return t.data_ptr()
-
-
-def _table(t, rows: int, dev: int) -> int:
-    """Checks a block table; returns its row stride (a single row's is its width at least)."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.dim() == 2 and t.is_cuda):
-        raise TypeError("block_table must be a 2-D int32 CUDA tensor")
-    n, width = t.shape
-    if n != rows or (width > 1 and t.stride(1) != 1):
-        raise ValueError(f"block_table must be [{rows}, max_blocks] with contiguous rows, got "
-                         f"{list(t.shape)} with strides {list(t.stride())}")
-    if t.get_device() != dev:
-        _here(t, "block_table")
-    return max(t.stride(0), width) if rows <= 1 else t.stride(0)
-
-
-def _cache(kv_cache, kv_scales, dev: int) -> Tuple[int, int]:
-    """Checks the cache and its scales; returns (num_blocks, block_size)."""
-    _need(kv_cache, "kv_cache", torch.float8_e4m3fn, 3)
-    nb, bs, d = kv_cache.shape
-    if d != D_QK or bs % Q8_GROUP:
-        raise ValueError(f"kv_cache must be [num_blocks, block_size, {D_QK}] with block_size a "
-                         f"multiple of {Q8_GROUP}, got {list(kv_cache.shape)}")
-    if kv_cache.get_device() != dev:
-        _here(kv_cache, "kv_cache")
-    _check(kv_scales, "kv_scales", torch.float32, (nb, bs // Q8_GROUP), dev)
-    return nb, bs
-
-
 def _on(stream, call, *args):
     """``call`` with ``stream`` as the current stream, so that what it allocates (outputs, a
     workspace) belongs to that stream and is not handed out again while its kernels run."""
@@ -99,13 +47,9 @@ def _on(stream, call, *args):
         return call(*args)
 
 
-def _stream(dev: int) -> int:
-    """The current stream's handle."""
-    return torch._C._cuda_getCurrentRawStream(dev)
-
-
-def _device() -> int:
-    return torch.cuda.current_device()
+def _native():
+    """The binding (checks of arguments, outputs, the current stream)."""
+    return _lib.load_q8(StepTables)
 
 
 def cp_step_tables(prev_lens: torch.Tensor, ctx_lens: torch.Tensor, new_lens: torch.Tensor,
@@ -131,56 +75,9 @@ def cp_step_tables(prev_lens: torch.Tensor, ctx_lens: torch.Tensor, new_lens: to
         return _on(stream, cp_step_tables, prev_lens, ctx_lens, new_lens, block_table, free_pages, free_state,
                    block_size, N, cp_size, cp_rank, n_ranks, interleave, total_lens, seq_lens, positions,
                    slots, free_state_out)
-    if not isinstance(prev_lens, torch.Tensor) or prev_lens.dim() != 1:
-        raise TypeError("prev_lens must be a 1-D int32 CUDA tensor")
-    if not prev_lens.is_cuda:
-        raise ValueError("prev_lens must be a CUDA tensor")
-    dev = _device()
-    B = prev_lens.shape[0]
-    i32, i64 = torch.int32, torch.int64
-    lens = (_check(prev_lens, "prev_lens", i32, (B,), dev), _check(ctx_lens, "ctx_lens", i32, (B,), dev),
-            _check(new_lens, "new_lens", i32, (B,), dev))
-    stride = _table(block_table, B, dev)
-    _need(free_pages, "free_pages", i32, 1)
-    if free_pages.get_device() != dev:
-        _here(free_pages, "free_pages")
-    state = _check(free_state, "free_state", i32, (2,), dev)
-    if n_ranks < 1 or N < 0:
-        raise ValueError(f"need n_ranks >= 1 and N >= 0, got {n_ranks} and {N}")
-    device = prev_lens.device
-    # (outputs made here need no check; a user who cares for the last microseconds passes them)
-    if total_lens is None:
-        total_lens = torch.empty_like(prev_lens)
-        total = total_lens.data_ptr()
-    else:
-        total = _check(total_lens, "total_lens", i32, (B,), dev)
-    if seq_lens is None:
-        seq_lens = torch.empty((n_ranks, B), dtype=i32, device=device)
-        seq = seq_lens.data_ptr()
-    else:
-        seq = _check(seq_lens, "seq_lens", i32, (n_ranks, B), dev)
-    if free_state_out is None:
-        free_state_out = torch.empty_like(free_state)
-        state_out = free_state_out.data_ptr()
-    else:
-        state_out = _check(free_state_out, "free_state_out", i32, (2,), dev)
-    if positions is None:
-        positions = torch.empty((B, N), dtype=i64, device=device)
-        pos = positions.data_ptr()
-    else:
-        pos = _check(positions, "positions", i64, (B, N), dev)
-    if slots is None:
-        slots = torch.empty((n_ranks, B, N), dtype=i64, device=device)
-        slot = slots.data_ptr()
-    else:
-        slot = _check(slots, "slots", i64, (n_ranks, B, N), dev)
-    rc = _lib.load().cp_step_tables(
-        *lens, B, N, block_table.data_ptr(), stride, block_table.shape[1], free_pages.data_ptr(),
-        free_pages.shape[0], state, state_out, block_size, cp_size, cp_rank, n_ranks, interleave,
-        total, seq, pos, slot, _stream(dev))
-    if rc:
-        _lib.check(rc)
-    return StepTables(total_lens, seq_lens, positions, slots, free_state_out)
+    return _native().step_tables(prev_lens, ctx_lens, new_lens, block_table, free_pages, free_state, block_size, N,
+                                 cp_size, cp_rank, n_ranks, interleave, total_lens, seq_lens, positions, slots,
+                                 free_state_out)
 
 
 def cp_store_q8(kv_new: torch.Tensor, ctx_lens: torch.Tensor, total_lens: torch.Tensor,
@@ -194,23 +91,8 @@ def cp_store_q8(kv_new: torch.Tensor, ctx_lens: torch.Tensor, total_lens: torch.
     if stream is not None:
         return _on(stream, cp_store_q8, kv_new, ctx_lens, total_lens, block_table, kv_cache, kv_scales, cp_size,
                    cp_rank, interleave)
-    _need(kv_new, "kv_new", torch.bfloat16, 3)
-    dev = _device()
-    B, N, d = kv_new.shape
-    if d != D_QK:
-        raise ValueError(f"kv_new must be [B, N, {D_QK}], got {list(kv_new.shape)}")
-    if kv_new.get_device() != dev:
-        _here(kv_new, "kv_new")
-    stride = _table(block_table, B, dev)
-    nb, bs = _cache(kv_cache, kv_scales, dev)
-    rc = _lib.load().cp_store_q8(
-        kv_new.data_ptr(), _check(ctx_lens, "ctx_lens", torch.int32, (B,), dev),
-        _check(total_lens, "total_lens", torch.int32, (B,), dev), block_table.data_ptr(), stride,
-        block_table.shape[1], B, N, bs, cp_size, cp_rank, interleave, kv_cache.data_ptr(),
-        kv_scales.data_ptr(), nb, _stream(dev))
-    if rc:
-        _lib.check(rc)
-    return kv_cache, kv_scales
+    return _native().store(kv_new, ctx_lens, total_lens, block_table, kv_cache, kv_scales, cp_size, cp_rank,
+                           interleave)
 
 
 def workspace_size_q8(B: int, H: int, q_len: int, device=None) -> int:
@@ -231,52 +113,8 @@ def _decode(shards, q, kv_cache, kv_scales, block_table, seq_lens, gseq, q_len, 
     if stream is not None:
         return _on(stream, _decode, shards, q, kv_cache, kv_scales, block_table, seq_lens, gseq, q_len, cp, rank,
                    scale, out, lse, lse_base_e, workspace, return_lse, None, causal, interleave)
-    if isinstance(q, torch.Tensor) and q.dim() == 3 and q_len >= 1 and q.shape[0] % q_len == 0:
-        q = q.view(-1, q_len, q.shape[1], q.shape[2])
-    _need(q, "q", torch.bfloat16, 4)
-    dev = _device()
-    B, ql, H, d = q.shape
-    if ql != q_len or d != D_QK:
-        raise ValueError(f"q must be [B, q_len={q_len}, H, {D_QK}], got {list(q.shape)}")
-    if q.get_device() != dev:
-        _here(q, "q")
-    nb, bs = _cache(kv_cache, kv_scales, dev)
-    n = shards if shards is not None else 1
-    if n < 1:
-        raise ValueError(f"need n_shards >= 1, got {n}")
-    stride = _table(block_table, n * B, dev)
-    seq = _check(seq_lens, "seq_lens", torch.int32, (n * B,), dev)
-    g = None if gseq is None else _check(gseq, "causal_seqlens_global", torch.int32, (B,), dev)
-    rows = (B * q_len, H) if shards is None else (n, B * q_len, H)
-    if out is None:
-        out = torch.empty((*rows, D_V), dtype=torch.bfloat16, device=q.device)
-        o = out.data_ptr()
-    else:
-        o = _check(out, "out", torch.bfloat16, (*rows, D_V), dev)
-    if lse is not None:
-        l = _check(lse, "lse", torch.float32, rows, dev)
-    elif return_lse:
-        lse = torch.empty(rows, dtype=torch.float32, device=q.device)
-        l = lse.data_ptr()
-    else:
-        l = None
-    if workspace is None:
-        workspace = alloc_workspace_q8(n * B, H, q_len, q.device)
-    if workspace.get_device() != dev or not workspace.is_contiguous():
-        _need(workspace, "workspace", workspace.dtype)
-        _here(workspace, "workspace")
-    lib = _lib.load()
-    head = (q.data_ptr(), kv_cache.data_ptr(), kv_scales.data_ptr(), block_table.data_ptr(), stride, seq, g,
-            B, H, q_len, 1 if causal else 0, bs, nb, block_table.shape[1])
-    tail = (int(interleave), float(scale), o, l, 1 if lse_base_e else 0, workspace.data_ptr(), workspace.nbytes,
-            _stream(dev))
-    if shards is not None:
-        rc = lib.mla_decode_shards_q8(*head, n, *tail)
-    else:
-        rc = lib.mla_decode_q8(*head, cp, rank, *tail)
-    if rc:
-        _lib.check(rc)
-    return out, lse
+    return _native().decode(shards, q, kv_cache, kv_scales, block_table, seq_lens, gseq, q_len, cp, rank, scale, out,
+                            lse, lse_base_e, workspace, return_lse, causal, interleave)
 
 
 def mla_decode_q8(q: torch.Tensor, kv_cache: torch.Tensor, kv_scales: torch.Tensor,

@@ -874,6 +874,106 @@ def test_decode_two_streams_at_once(units):
 
 
 # =============================================================================================
+# the wrappers' refusals: nothing is launched, the next call works
+# =============================================================================================
+def call_of(name):
+    a, t2 = i32([0, 0]), i32([[0, 1], [2, 3]])
+    cache, scales = new_pool(4, 16)
+    tables = dict(prev_lens=a, ctx_lens=a.clone(), new_lens=i32([1, 1]), block_table=t2, free_pages=i32(range(4)),
+                  free_state=i32([0, 4]), block_size=16, N=1)
+    store = dict(kv_new=torch.zeros(2, 1, 576, dtype=torch.bfloat16, device=DEV), ctx_lens=a, total_lens=i32([1, 1]),
+                 block_table=t2, kv_cache=cache, kv_scales=scales)
+    decode = dict(q=torch.zeros(2, 1, 8, 576, dtype=torch.bfloat16, device=DEV), kv_cache=cache, kv_scales=scales,
+                  block_table=t2, seq_lens=i32([0, 0]), causal_seqlens_global=None, q_len=1, scale=SCALE)
+    return {"cp_step_tables": tables, "cp_store_q8": store, "mla_decode_q8": dict(decode, cp_world=1, cp_rank=0),
+            "mla_decode_shards_q8": dict(decode, n_shards=1)}[name]
+
+
+def long_rows(n=4):
+    return torch.zeros(2, 2 * n, dtype=torch.int32, device=DEV)
+
+
+@pytest.mark.parametrize("name,change,error", [
+    ("cp_step_tables", lambda d: dict(prev_lens=d["prev_lens"].cpu()), ValueError),
+    ("cp_step_tables", lambda d: dict(prev_lens=d["prev_lens"].long()), TypeError),
+    ("cp_step_tables", lambda d: dict(prev_lens=[0, 0]), TypeError),
+    ("cp_step_tables", lambda d: dict(ctx_lens=i32([0])), ValueError),
+    ("cp_step_tables", lambda d: dict(new_lens=i32([1, 0, 1])[::2]), ValueError),
+    ("cp_step_tables", lambda d: dict(block_table=long_rows()[:, ::2]), ValueError),
+    ("cp_step_tables", lambda d: dict(block_table=d["block_table"][:1].expand(2, 2)), RuntimeError),
+    ("cp_step_tables", lambda d: dict(block_table=d["block_table"][0]), TypeError),
+    ("cp_step_tables", lambda d: dict(free_state=i32([0, 4, 0])), ValueError),
+    ("cp_step_tables", lambda d: dict(free_pages=i32([[0, 1]])), ValueError),
+    ("cp_step_tables", lambda d: dict(free_pages=i32([])), RuntimeError),
+    ("cp_step_tables", lambda d: dict(N=1.5), TypeError),
+    ("cp_step_tables", lambda d: dict(N=-1), ValueError),
+    ("cp_step_tables", lambda d: dict(N=1 << 40), ValueError),
+    ("cp_step_tables", lambda d: dict(N=1 << 30), ValueError),
+    ("cp_step_tables", lambda d: dict(n_ranks=0), ValueError),
+    ("cp_step_tables", lambda d: dict(n_ranks=2), RuntimeError),
+    ("cp_step_tables", lambda d: dict(slots=torch.zeros(1, 2, 1, device=DEV)), TypeError),
+    ("cp_step_tables", lambda d: dict(positions=torch.zeros(2, 2, dtype=torch.int64, device=DEV)), ValueError),
+    ("cp_store_q8", lambda d: dict(kv_new=d["kv_new"].float()), TypeError),
+    ("cp_store_q8", lambda d: dict(kv_new=d["kv_new"][..., :575]), ValueError),
+    ("cp_store_q8", lambda d: dict(kv_new=d["kv_new"][0]), ValueError),
+    ("cp_store_q8", lambda d: dict(kv_new=d["kv_new"].expand(2, 2, 576)), ValueError),
+    ("cp_store_q8", lambda d: dict(kv_cache=d["kv_cache"].view(torch.uint8)), TypeError),
+    ("cp_store_q8", lambda d: dict(kv_scales=d["kv_scales"][:3]), ValueError),
+    ("cp_store_q8", lambda d: dict(kv_scales=None), TypeError),
+    ("cp_store_q8", lambda d: dict(total_lens=i32([1])), ValueError),
+    ("cp_store_q8", lambda d: dict(interleave=3), RuntimeError),
+    ("mla_decode_q8", lambda d: dict(q=d["q"].float()), TypeError),
+    ("mla_decode_q8", lambda d: dict(q_len=0), ValueError),
+    ("mla_decode_q8", lambda d: dict(q_len=2), ValueError),
+    ("mla_decode_q8", lambda d: dict(q=d["q"][0, 0]), ValueError),
+    ("mla_decode_q8", lambda d: dict(q=d["q"].transpose(1, 2)), ValueError),
+    ("mla_decode_q8", lambda d: dict(kv_cache=d["kv_cache"][:, :8].contiguous()), ValueError),
+    ("mla_decode_q8", lambda d: dict(seq_lens=i32([0, 0, 0])), ValueError),
+    ("mla_decode_q8", lambda d: dict(causal_seqlens_global=i32([1])), ValueError),
+    ("mla_decode_q8", lambda d: dict(cp_world=2), RuntimeError),
+    ("mla_decode_q8", lambda d: dict(scale=0.0), RuntimeError),
+    ("mla_decode_q8", lambda d: dict(out=torch.zeros(2, 8, 512, device=DEV)), TypeError),
+    ("mla_decode_q8", lambda d: dict(lse=torch.zeros(2, 7, device=DEV)), ValueError),
+    ("mla_decode_q8", lambda d: dict(workspace=torch.zeros(1 << 20, device=DEV)[::2]), ValueError),
+    ("mla_decode_q8", lambda d: dict(workspace=torch.zeros(8)), ValueError),
+    ("mla_decode_q8", lambda d: dict(workspace=7), TypeError),
+    ("mla_decode_shards_q8", lambda d: dict(n_shards=0), ValueError),
+    ("mla_decode_shards_q8", lambda d: dict(n_shards=2), ValueError),
+    ("mla_decode_shards_q8", lambda d: dict(block_table=d["block_table"].repeat(2, 1)), ValueError),
+])
+def test_wrappers_refuse(name, change, error):
+    good = call_of(name)
+    with pytest.raises(error):
+        getattr(M, name)(**{**good, **change(good)})
+    getattr(M, name)(**good)
+    assert M.device_status() == 0
+
+
+def test_wrappers_take_what_they_may():
+    """A flat q, numpy and boolean numbers, empty batches, given outputs (returned as they are)."""
+    d = call_of("mla_decode_q8")
+    want = M.mla_decode_q8(**d)
+    flat = M.mla_decode_q8(**dict(d, q=d["q"].view(2, 8, 576)))
+    assert torch.equal(flat[0], want[0]) and torch.equal(flat[1], want[1])
+    out, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+    got = M.mla_decode_q8(**dict(d, q_len=np.int32(1), cp_world=True, scale=np.float64(SCALE), out=out, lse=lse))
+    assert got[0] is out and got[1] is lse and torch.equal(out, want[0])
+    assert M.mla_decode_q8(**dict(d, return_lse=False))[1] is None
+    e = M.mla_decode_q8(**dict(d, q=d["q"][:0], block_table=d["block_table"][:0], seq_lens=d["seq_lens"][:0]))
+    assert e[0].shape == (0, 8, 512) and e[1].shape == (0, 8)
+    s = call_of("cp_store_q8")
+    k = M.cp_store_q8(**dict(s, kv_new=s["kv_new"][:, :0]))
+    assert k[0] is s["kv_cache"] and k[1] is s["kv_scales"]
+    t = call_of("cp_step_tables")
+    total = torch.empty(2, dtype=torch.int32, device=DEV)
+    r = M.cp_step_tables(**dict(t, total_lens=total))
+    assert isinstance(r, tuple) and r.total_lens is total and r[0] is total and len(r) == 5
+    assert r.seq_lens.shape == (1, 2) and r.positions.shape == (2, 1) and r.slots.shape == (1, 2, 1)
+    assert r.total_lens.tolist() == [1, 1] and r.free_state.tolist() == [2, 2]
+    assert M.device_status() == 0
+
+
+# =============================================================================================
 # together
 # =============================================================================================
 @pytest.mark.parametrize("cp,il,bs,q_len,H", [(1, 1, 16, 4, 16), (2, 2, 16, 3, 64), (4, 1, 32, 1, 128)])

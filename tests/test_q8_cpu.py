@@ -110,7 +110,7 @@ def test_workspace_size(lib):  # noqa: F811
 
 
 # ---- refusals of the Python wrappers ----------------------------------------------------------
-def test_wrappers_refuse_cpu_tensors_and_wrong_types():
+def test_wrappers_refuse_cpu_tensors_and_wrong_types(lib):  # noqa: F811
     i32 = torch.zeros(2, dtype=torch.int32)
     bt = torch.zeros(2, 4, dtype=torch.int32)
     rows = torch.zeros(2, 1, 576, dtype=torch.bfloat16)
