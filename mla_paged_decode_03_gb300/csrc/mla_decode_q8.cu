@@ -91,46 +91,49 @@ template <int kN>
 struct Cfg {
   static constexpr int kSoftWarps = 4 * (kN / kR);         // 4 x 32 keys, kR rows each
   static constexpr int kThreads = 128 + 32 * kSoftWarps;   // warps 0-2: loads, QK, PV
+  static constexpr bool kQTmem = kN == 64;                 // Q's latent dims in tensor memory
+  static constexpr int kSBufs = kQTmem ? 1 : 2;            // S buffers
   static constexpr int kQChunk = 2 * kN * 128;             // hi and lo rows of 128 dims
-  static constexpr int kOffQRope = 4 * kQChunk;
+  static constexpr int kOffQRope = kQTmem ? 0 : 4 * kQChunk;
   static constexpr int kSegTiles = kN == 64 ? 3 : 6;       // cost of starting a segment, in tiles
-  static constexpr int kSlots = kN == 64 ? 8 : 10;         // latent chunks in the ring (one rope chunk)
-  static constexpr int kPBufs = kN == 64 ? 1 : 2;
+  static constexpr int kSlots = kN == 64 ? 11 : 10;        // latent chunks in the ring (one rope chunk)
+  static constexpr int kPBufs = 2;
   static constexpr int kPHalf = kTile * kN;                // hi or lo of P^T
-  static constexpr int kOffK = 2 * kN * kD;
+  static constexpr int kOffK = kOffQRope + 2 * kN * 64;
   static constexpr int kOffRope = kOffK + kSlots * kChunkBytes;
   static constexpr int kOffP = kOffRope + kRopeBytes;
   static constexpr int kOffBar = kOffP + kPBufs * 2 * kPHalf;
   static constexpr int kOffRow = kOffBar + 384;            // four words for each row (softmax warps)
   static constexpr int kOffMisc = kOffRow + 16 * kN;       // tmem base, abort, scan result
   static constexpr int kOffSeg = kOffMisc + 48;            // Seg[kSegRing]
-  static constexpr int kOffScale = kOffSeg + 32 * kSegRing;   // float4 [2 tiles][8 groups of 16 keys]
-  static constexpr int kSmem = kOffScale + 256 + 1024;     // + alignment slack
-  static constexpr uint32_t kTmemCols = 8 * kN;            // O^T 4 kN, S^T 2 x 2 kN
+  static constexpr int kOffScale = kOffSeg + 32 * kSegRing;   // float4 [kSBufs tiles][8 groups of 16 keys]
+  static constexpr int kSmem = kOffScale + 128 * kSBufs + 1008;   // + alignment slack
+  // tensor memory: O^T, then S, then Q
+  static constexpr uint32_t kColS = 4 * kN, kColQ = kColS + 128;
+  static constexpr uint32_t kTmemCols = 8 * kN;
   static_assert(kOffK % 1024 == 0 && kOffRope % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms");
   static_assert(kSmem <= 232448, "shared memory of a block");
 };
 
 enum Bar : int {
-  B_KF = 0,        // [10] latent chunk loaded
-  B_KE = 10,       // [10] its PV done
-  B_SF = 20,       // [2] S^T and the tile's scales written
-  B_SE = 22,       // [2] both read (the softmax warps)
-  B_PF = 24,       // [2] P^T written (the softmax warps)
-  B_PE = 26,       // [2] its PV done
-  B_RF = 28,       // rope chunk loaded
-  B_RE = 29,       // its QK done
-  B_QF = 30,       // the segment's Q written (the softmax warps)
-  B_DRAIN = 31,    // [2] the QK / PV warp's last operations
-  B_NEVER = 33,    // never arrived at (tests of the timeout path)
-  B_GF = 34,       // [4] a segment has been written
-  B_GE = 38,       // [4] and read by every role (three warps and the softmax warps)
-  B_COUNT = 42
+  B_KF = 0,        // [12] latent chunk loaded
+  B_KE = 12,       // [12] its PV done
+  B_SF = 24,       // [2] S and the tile's scales written
+  B_SE = 26,       // [2] both read (the softmax warps)
+  B_PF = 28,       // [2] P^T written (the softmax warps)
+  B_PE = 30,       // [2] its PV done
+  B_RF = 32,       // rope chunk loaded
+  B_RE = 33,       // its QK done
+  B_QF = 34,       // the segment's Q written (the softmax warps)
+  B_DRAIN = 35,    // [2] the QK / PV warp's last operations
+  B_NEVER = 37,    // never arrived at (tests of the timeout path)
+  B_GF = 38,       // [4] a segment has been written
+  B_GE = 42,       // [4] and read by every role (three warps and the softmax warps)
+  B_COUNT = 46
 };
 
 struct Params {
   const uint16_t* q;
-  const uint8_t* kv;
   const float* scales;
   const int32_t* bt;
   long long bt_stride;
@@ -242,6 +245,29 @@ __device__ __forceinline__ void stmatrix_x4(uint32_t addr, const uint32_t (&v)[4
                "r"(v[1]), "r"(v[2]), "r"(v[3])
                : "memory");
 }
+// The same layout over 16 lanes x 32 columns (four registers for eight columns), and written over
+// 16 x 16.
+__device__ __forceinline__ void tmem_load_16x32(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store_16x16(uint32_t addr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// Four 16 x 8 matrices of bytes, stored transposed (8 lines of 16 bytes): lane l holds rows l / 4
+// (bytes 0, 1) and l / 4 + 8 (bytes 2, 3), columns 2 (l % 4) and the next, of each, and gives the
+// address of line l % 8 of matrix l / 8.
+__device__ __forceinline__ void stmatrix_t_x4(uint32_t addr, const uint32_t (&v)[4]) {
+  asm volatile("stmatrix.sync.aligned.m16n8.x4.trans.shared.b8 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
+}
 __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -260,6 +286,32 @@ __device__ __forceinline__ uint32_t e4m3x2_of_half2(uint32_t a) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(a));
   return r;
+}
+
+// Largest magnitude of 8 bf16 values, as their 15 bits.
+__device__ __forceinline__ uint32_t peak8(const uint4& v) {
+  const uint32_t k = 0x7fff7fffu;
+  const uint32_t m = __vmaxu2(__vmaxu2(v.x & k, v.y & k), __vmaxu2(v.z & k, v.w & k));
+  return max(m & 0xffffu, m >> 16);
+}
+// 8 bf16 values times a power of two as e4m3 hi + lo; in half precision every scaled element is
+// exact but for what lies below 2^-24.
+__device__ __forceinline__ void split8(const uint4& w, float f, uint32_t (&hi)[2], uint32_t (&lo)[2]) {
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+  const uint64_t f2 = f32x2(f, f);
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float x0, x1;
+    f32x2_split(mul2(f32x2(__uint_as_float(x[k] << 16), __uint_as_float(x[k] & 0xffff0000u)), f2), x0, x1);
+    const uint32_t u = half2_of(x0, x1);
+    h[k] = e4m3x2_of_half2(u);
+    l[k] = e4m3x2_of_half2(sub_half2(u, half2_of_e4m3x2(h[k])));
+  }
+  hi[0] = h[0] | h[1] << 16;
+  hi[1] = h[2] | h[3] << 16;
+  lo[0] = l[0] | l[1] << 16;
+  lo[1] = l[2] | l[3] << 16;
 }
 
 // Instruction descriptor of kind::f8f6f4 with an fp32 accumulator; formats 0 = e4m3, 1 = e5m2;
@@ -310,6 +362,24 @@ __device__ __forceinline__ void qk_mma(uint32_t d, uint32_t a, uint32_t b, uint3
         " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %4, t;\n"
         "}" ::"r"(d), "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc), "r"(1u)
         : "memory");
+}
+
+// Four products along K under one election, A in tensor memory (32 bytes of K are eight columns).
+__device__ __forceinline__ void qk_mma_t(uint32_t d, uint32_t a, uint32_t b, uint32_t b_hi, uint32_t idesc,
+                                         uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, t, e;\n .reg .b32 u, v;\n .reg .b64 y;\n setp.ne.b32 p, %5, 0;\n"
+      " setp.ne.b32 t, %6, 0;\n elect.sync _|e, 0xffffffff;\n"
+      " mov.b64 y, {%2, %3};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], y, %4, p;\n"
+      " add.u32 u, %1, 8; add.u32 v, %2, 2; mov.b64 y, {v, %3};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [u], y, %4, t;\n"
+      " add.u32 u, %1, 16; add.u32 v, %2, 4; mov.b64 y, {v, %3};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [u], y, %4, t;\n"
+      " add.u32 u, %1, 24; add.u32 v, %2, 6; mov.b64 y, {v, %3};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [u], y, %4, t;\n"
+      "}" ::"r"(d), "r"(a), "r"(b), "r"(b_hi), "r"(idesc), "r"(acc), "r"(1u)
+      : "memory");
 }
 
 // One step of 32 keys: the weights' e5m2 part (bh, ih) and their e4m3 part (bl, il).
@@ -598,17 +668,8 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
             cur = nxt;
             nxt = row_of(i0 + 32 + lane);
           }
-          // lane l < nbox issues the tile's box l, and for units of 64 rows asks L2 for the next
-          // tile's (its rows are consecutive bytes): that ring holds two tiles, so a load begins only
-          // when PV has let go of a chunk, and must not wait for HBM then (8 % of 64 x 32k; with 32
-          // rows, where HBM bounds and the ring is longer, it cost 1 %)
-          const int at = t * nbox + lane - i0;
-          const int y = __shfl_sync(0xffffffffu, cur, at & 31);
-          const int y1 = __shfl_sync(0xffffffffu, (t + 1) * nbox >= i0 + 32 ? nxt : cur, (at + nbox) & 31);
-          if (kN == 64 && lane < nbox && t + 1 < it.t_end && y1 < p.num_blocks * p.bs)
-            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.kv + (long long)y1 * kD),
-                         "r"(p.box_rows * kD)
-                         : "memory");
+          // lane l < nbox issues the tile's box l
+          const int y = __shfl_sync(0xffffffffu, cur, (t * nbox + lane - i0) & 31);
           for (int c = 0; c < 4; ++c) {
             ok = warp_all(wait<kN>(s, B_KE + slot, kpar, p));
             if (!ok) break;
@@ -652,16 +713,20 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
     while (ok && take_segment<kN>(s, nseg++, p, it)) {
         ok = warp_all(wait<kN>(s, B_QF, (nseg - 1) & 1, p));
         for (int t = it.t_begin; t < it.t_end && ok; ++t, ++n) {
-          const int g = (int)(n & 1);
-          ok = warp_all(wait<kN>(s, B_SE + g, (uint32_t)(((n >> 1) + 1) & 1), p));   // S^T read
-          const uint32_t d = tmem + 4 * kN + g * 2 * kN;
+          const int g = (int)(n % C::kSBufs);
+          ok = warp_all(wait<kN>(s, B_SE + g, (uint32_t)((n / C::kSBufs + 1) & 1), p));   // S read
+          const uint32_t d = tmem + C::kColS + g * 2 * kN;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             ok = ok && warp_all(wait<kN>(s, B_KF + slot, par, p));
             if (!ok) break;
             tc_fence_after();
-            qk_mma<4>(d, ka + slot * (kChunkBytes / 16), qa + c * (C::kQChunk / 16),
-                      desc_hi(1024, kSwizzle128B), id_qk, c != 0);
+            if constexpr (C::kQTmem)
+              qk_mma_t(d, tmem + C::kColQ + c * 32, ka + slot * (kChunkBytes / 16), desc_hi(1024, kSwizzle128B), id_qk,
+                       c != 0);
+            else
+              qk_mma<4>(d, ka + slot * (kChunkBytes / 16), qa + c * (C::kQChunk / 16),
+                        desc_hi(1024, kSwizzle128B), id_qk, c != 0);
             if (++slot == C::kSlots) {
               slot = 0;
               par ^= 1u;
@@ -670,7 +735,8 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
           ok = ok && warp_all(wait<kN>(s, B_RF, (uint32_t)(n & 1), p));
           if (!ok) break;
           tc_fence_after();
-          qk_mma<2>(d, desc_lo(s.base + C::kOffRope), qa + C::kOffQRope / 16, desc_hi(512, kSwizzle64B), id_qk, 1);
+          const uint32_t kr = desc_lo(s.base + C::kOffRope), qr = qa + C::kOffQRope / 16;
+          qk_mma<2>(d, C::kQTmem ? qr : kr, C::kQTmem ? kr : qr, desc_hi(512, kSwizzle64B), id_qk, 1);
           mma_commit_warp(bar<kN>(s, B_RE));
           mma_commit_warp(bar<kN>(s, B_SF + g));
         }
@@ -783,7 +849,7 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
       have = walk.next(p);
       publish();
       for (int t = it.t_begin; t < it.t_end && ok; ++t, ++n) {
-        const uint32_t g = n & 1;
+        const uint32_t g = n % C::kSBufs;
         float sc = sc_next;
         sc_next = scale_in(page_next);
         step();
@@ -793,7 +859,7 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
           sc = 1.f;
         }
         const float4 v = make_float4(sc, fast_log2(sc), fast_rcp(sc), 0.f);
-        ok = warp_all(wait<kN>(s, B_SE + g, ((n >> 1) + 1) & 1, p));
+        ok = warp_all(wait<kN>(s, B_SE + g, (n / C::kSBufs + 1) & 1, p));
         if (lane < 8) reinterpret_cast<float4*>(s.ptr + C::kOffScale)[g * 8 + lane] = v;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar<kN>(s, B_SF + g));
@@ -802,26 +868,74 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
     if (__any_sync(0xffffffffu, bad_scale) && lane == 0) atomicOr(p.status, MLA_STATUS_BAD_SCALE);
   } else if (warp >= 4) {
     // ================= softmax ===================================================================
-    // A warp has keys 32 q4 .. + 31 of a tile and rows 16 hr .. + 15 of the unit.  S^T is read in
-    // pieces of 16 keys x 8 columns, of which a thread gets keys lane / 4 and + 8, columns 2 c and
-    // 2 c + 1 (c = lane % 4); Q's rows are laid out so that those columns of two pieces are rows
-    // 4 c .. 4 c + 3.  So a thread has four keys (lane / 4 + 8 i) and four consecutive rows: the
-    // rows' constants and sums stay in registers, a key's four weights are one word of P^T.
-    const int q4 = warp & 3, hr = (warp - 4) >> 2;
+    // A warp has 32 keys of a tile (from 32 kq) and 16 rows of the unit (from 16 rg).  S is read
+    // so that a thread's values need no exchange and leave as words of P^T:
+    //   64 rows: lanes of tensor memory are rows (16 hi, 16 lo for each 16 rows), columns keys.  A
+    //     thread has rows lane / 4 and + 8, keys 2 (lane % 4) and the next of each eight;
+    //   32 rows: lanes are keys, columns rows (hi, then lo).  A thread has keys lane / 4 + 8 i; Q's
+    //     rows are laid out so that its columns are rows 4 (lane % 4) .. + 3.
+    // y[i][k] is then row k / 2, key 8 i + k % 2, or key i, row k.
+    const int quad = warp & 3, part = (warp - 4) >> 2;
+    const int kq = C::kQTmem ? part : quad, rg = C::kQTmem ? quad : part;
     const int c4 = lane & 3;
-    const int my_rows = hr * kR + 4 * c4;
-    const int key = q4 * 32 + lane;                // the key whose 16 bytes of P^T this thread addresses
+    const int my_rows = C::kQTmem ? 16 * rg + (lane >> 2) : 16 * rg + 4 * c4;
+    const int my_keys = kq * 32 + (C::kQTmem ? 2 * c4 : lane >> 2);
+    const int key = kq * 32 + lane;                // the key whose 16 bytes of P^T this thread addresses
     const int st = tid - 128;
-    const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     float* row_a = reinterpret_cast<float*>(s.ptr + C::kOffRow);     // log2 units per unit of S
     float* row_nm = row_a + kN;                                      // minus the reference
     float* shift = row_nm + kN;                                      // its move; later 1 / l
     int* lim = reinterpret_cast<int*>(shift + kN);                   // keys the row sees
+    // the thread's rows' values of a row array (by k of y[i][k])
+    auto of_rows = [&](const auto* v) {
+      using T = std::remove_cv_t<std::remove_reference_t<decltype(*v)>>;
+      using T4 = std::conditional_t<std::is_same_v<T, float>, float4, int4>;
+      if constexpr (C::kQTmem) {
+        const T a = v[my_rows], b = v[my_rows + 8];
+        return T4{a, a, b, b};
+      } else {
+        return *reinterpret_cast<const T4*>(v + my_rows);
+      }
+    };
+    // v, combined over the warp's keys, into row array `to`
+    auto over_keys = [&](float4 v, auto op, float* to) {
+      if constexpr (C::kQTmem) {
+        float a = op(v.x, v.y), b = op(v.z, v.w);
+#pragma unroll
+        for (int o = 1; o <= 2; o <<= 1) {
+          a = op(a, __shfl_xor_sync(0xffffffffu, a, o));
+          b = op(b, __shfl_xor_sync(0xffffffffu, b, o));
+        }
+        if (c4 == 0) {
+          to[my_rows] = a;
+          to[my_rows + 8] = b;
+        }
+      } else {
+#pragma unroll
+        for (int o = 4; o <= 16; o <<= 1) {
+          v.x = op(v.x, __shfl_xor_sync(0xffffffffu, v.x, o));
+          v.y = op(v.y, __shfl_xor_sync(0xffffffffu, v.y, o));
+          v.z = op(v.z, __shfl_xor_sync(0xffffffffu, v.z, o));
+          v.w = op(v.w, __shfl_xor_sync(0xffffffffu, v.w, o));
+        }
+        if (lane < 4) *reinterpret_cast<float4*>(to + my_rows) = v;
+      }
+    };
+    // 2^up puts a maximum with exponent ex in [128, 256) (one below 2^-119 less far up); the row's
+    // constants
+    auto set_row = [&](int r, int ex) {
+      const int up = min(134 - ex, 126);
+      const float a = __int_as_float((127 - up) << 23) * p.scale_log2;
+      row_a[r] = ex == 255 ? __int_as_float(0x7fc00000) : a;          // NaN or infinity: a NaN row
+      row_nm[r] = 0.f;
+    };
+    auto factor = [](int ex) { return __int_as_float((min(134 - ex, 126) + 127) << 23); };
     uint32_t n = 0;
     // The order of a block's segments: Q of the next one is prepared (and its first QK may run)
     // before the output of the one before is written, which waits for its last PV.
-    uint64_t w01 = 0, w23 = 0;                     // sums of the four rows' weights, this thread's keys
-    uint64_t l01 = 0, l23 = 0;                     // sums of the four rows' weights / S, this thread's keys
+    uint64_t w01 = 0, w23 = 0;                     // sums of weights by k of y[i][k]
+    uint64_t l01 = 0, l23 = 0;                     // sums of weights / S
     bool have = !soft_or<kN>(!take_segment<kN>(s, nseg++, p, it)), pending = false;
     // of the segment whose output is to be written: its request, whether it is a whole unit, which of
     // the block's two partials it is
@@ -831,65 +945,112 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
     for (;;) {
       if (have) {
         const int row0 = rt * kN;
-        // ---- Q: eight lanes a row, hi and lo written where the products read them --------------
-        {
+        const int sh = shard_of(p, it.b);
+        const uint16_t* q0 = p.q + ((long long)(it.b - sh * p.shard_B) * p.rows + row0) * kD;
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        if (st < kN) lim[st] = row0 + st < p.rows ? row_keys(p, Lens{it.cap, it.g, it.rank}, row0 + st) : it.keys;
+        if constexpr (C::kQTmem) {
+          // ---- Q into tensor memory, rope dims into shared memory; a warp has its 16 rows' dims
+          // 128 kq .. + 127, a thread eight dims of each 32 of two rows, and eight rope dims of one ---
+          static_assert(kN == 64, "16 rows for each quarter of the lanes");
+          const bool v0 = row0 + my_rows < p.rows, v1 = row0 + my_rows + 8 < p.rows, second = c4 >= 2;
+          const uint16_t *s0 = q0 + (v0 ? my_rows : 0) * kD, *s1 = q0 + (v1 ? my_rows + 8 : 0) * kD;
+          uint4 w[2][4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int dim = kq * 128 + k * 32 + c4 * 8;
+            w[0][k] = v0 ? __ldg(reinterpret_cast<const uint4*>(s0 + dim)) : zero;
+            w[1][k] = v1 ? __ldg(reinterpret_cast<const uint4*>(s1 + dim)) : zero;
+          }
+          const int piece = 2 * kq + (c4 & 1);     // of the row's eight pieces of 8 rope dims
+          const uint4 wr =
+              (second ? v1 : v0) ? __ldg(reinterpret_cast<const uint4*>((second ? s1 : s0) + kDv + piece * 8)) : zero;
+          uint32_t m0 = second ? 0u : peak8(wr), m1 = second ? peak8(wr) : 0u;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            m0 = max(m0, peak8(w[0][k]));
+            m1 = max(m1, peak8(w[1][k]));
+          }
+#pragma unroll
+          for (int o = 1; o <= 2; o <<= 1) {
+            m0 = max(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+            m1 = max(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+          }
+          uint8_t* ex = reinterpret_cast<uint8_t*>(shift);            // [4][kN] exponents; shift is free here
+          if (c4 == 0) {
+            ex[kq * kN + my_rows] = (uint8_t)(m0 >> 7);
+            ex[kq * kN + my_rows + 8] = (uint8_t)(m1 >> 7);
+          }
+          soft_sync<kN>();
+          int e0 = 0, e1 = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            e0 = max(e0, (int)ex[k * kN + my_rows]);
+            e1 = max(e1, (int)ex[k * kN + my_rows + 8]);
+          }
+          if (kq == 0 && c4 == 0) {
+            set_row(my_rows, e0);
+            set_row(my_rows + 8, e1);
+          }
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t hi[8], lo[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t h[2], l[2];
+              split8(w[k & 1][2 * half + (k >> 1)], factor(k & 1 ? e1 : e0), h, l);
+              hi[2 * k] = h[0];
+              hi[2 * k + 1] = h[1];
+              lo[2 * k] = l[0];
+              lo[2 * k + 1] = l[1];
+            }
+            const uint32_t dst = tmem + lane_off + C::kColQ + kq * 32 + half * 16;
+            tmem_store_16x16(dst, hi);
+            tmem_store_16x16(dst + (16u << 16), lo);
+          }
+          {
+            uint32_t h[2], l[2];
+            split8(wr, factor(second ? e1 : e0), h, l);
+            const int line = 32 * rg + (lane >> 2) + (second ? 8 : 0);            // of hi; lo is 16 on
+            uint8_t* dst = s.ptr + C::kOffQRope + line * 64 + (((piece >> 1) ^ ((line >> 1) & 3)) << 4) +
+                           (piece & 1) * 8;
+            *reinterpret_cast<uint2*>(dst) = make_uint2(h[0], h[1]);
+            *reinterpret_cast<uint2*>(dst + 16 * 64) = make_uint2(l[0], l[1]);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+        } else {
+          // ---- Q into shared memory: eight lanes a row ------------------------------------------
           static_assert(kN == 4 * C::kSoftWarps, "four rows a warp");
           const int r = (warp - 4) * 4 + (lane >> 3), l8 = lane & 7;
           const bool valid = row0 + r < p.rows;
-          const int sh = shard_of(p, it.b);
-          const uint4* src = reinterpret_cast<const uint4*>(
-              p.q + ((long long)(it.b - sh * p.shard_B) * p.rows + row0 + (valid ? r : 0)) * kD) + l8;
+          const uint4* src = reinterpret_cast<const uint4*>(q0 + (valid ? r : 0) * kD) + l8;
           uint4 w[9];                              // elements 8 (l8 + 8 i) .. + 7
+          uint32_t m = 0;
 #pragma unroll
-          for (int i = 0; i < 9; ++i) w[i] = valid ? __ldg(src + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
-          if (st < kN) lim[st] = row0 + st < p.rows ? row_keys(p, Lens{it.cap, it.g, it.rank}, row0 + st) : it.keys;
-          uint32_t m2 = 0;
+          for (int i = 0; i < 9; ++i) w[i] = valid ? __ldg(src + 8 * i) : zero;
 #pragma unroll
-          for (int i = 0; i < 9; ++i) {
-            m2 = __vmaxu2(m2, __vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu));
-            m2 = __vmaxu2(m2, __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
-          }
-          uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+          for (int i = 0; i < 9; ++i) m = max(m, peak8(w[i]));
 #pragma unroll
           for (int o = 1; o <= 4; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-          // 2^up puts the row's maximum in [128, 256) (a maximum below 2^-119 less far up)
           const int ex = (int)(m >> 7);
-          const int up = min(134 - ex, 126);
-          const float f = __int_as_float((up + 127) << 23);
-          if (l8 == 0) {
-            const float a = __int_as_float((127 - up) << 23) * p.scale_log2;
-            row_a[r] = ex == 255 ? __int_as_float(0x7fc00000) : a;      // NaN or infinity: a NaN row
-            row_nm[r] = 0.f;
-          }
-          // its column of S^T (see above); in half precision every scaled element is exact but for
-          // what lies below 2^-24
-          const int col = (r & ~15) + ((r & 2) << 2) + ((r & 12) >> 1) + (r & 1);
+          if (l8 == 0) set_row(r, ex);
+          const int col = (r & ~15) + ((r & 2) << 2) + ((r & 12) >> 1) + (r & 1);   // its column of S^T
           uint8_t* lat = s.ptr + col * 128 + (l8 & 1) * 8;
           uint8_t* rope = s.ptr + C::kOffQRope + col * 64 + (((l8 >> 1) ^ ((col >> 1) & 3)) << 4) + (l8 & 1) * 8;
-          const uint64_t f2 = f32x2(f, f);
 #pragma unroll
           for (int i = 0; i < 9; ++i) {
-            const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              float x0, x1;
-              f32x2_split(mul2(f32x2(__uint_as_float(x[k] << 16), __uint_as_float(x[k] & 0xffff0000u)), f2),
-                          x0, x1);
-              const uint32_t u = half2_of(x0, x1);
-              hi[k] = e4m3x2_of_half2(u);
-              lo[k] = e4m3x2_of_half2(sub_half2(u, half2_of_e4m3x2(hi[k])));
-            }
+            uint32_t h[2], l[2];
+            split8(w[i], factor(ex), h, l);
             uint8_t* dst = i < 8 ? lat + (i >> 1) * C::kQChunk + ((((i & 1) * 4 + (l8 >> 1)) ^ (col & 7)) << 4)
                                  : rope;
-            *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-            *reinterpret_cast<uint2*>(dst + (i < 8 ? kN * 128 : kN * 64)) =
-                make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+            *reinterpret_cast<uint2*>(dst) = make_uint2(h[0], h[1]);
+            *reinterpret_cast<uint2*>(dst + (i < 8 ? kN * 128 : kN * 64)) = make_uint2(l[0], l[1]);
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar<kN>(s, B_QF));
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar<kN>(s, B_QF));
       }
       if (pending) {
         const int out_row0 = rt * kN;
@@ -904,14 +1065,7 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
             float4 sum;
             f32x2_split(v ? w01 : l01, sum.x, sum.y);
             f32x2_split(v ? w23 : l23, sum.z, sum.w);
-#pragma unroll
-            for (int o = 4; o <= 16; o <<= 1) {
-              sum.x += __shfl_xor_sync(0xffffffffu, sum.x, o);
-              sum.y += __shfl_xor_sync(0xffffffffu, sum.y, o);
-              sum.z += __shfl_xor_sync(0xffffffffu, sum.z, o);
-              sum.w += __shfl_xor_sync(0xffffffffu, sum.w, o);
-            }
-            if (lane < 4) *reinterpret_cast<float4*>(xs + (v * 4 + q4) * kN + my_rows) = sum;
+            over_keys(sum, [](float a, float b) { return a + b; }, xs + (v * 4 + kq) * kN);
           }
           soft_sync<kN>();
           if (st < kN) {
@@ -936,10 +1090,10 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
           const bool odd = lane & 1;
           const int nrow = min(kN, p.rows - out_row0) - (odd ? 1 : 0);
           uint16_t* dst0 = out_single ? p.out + out_row * kDv : p.ws_o + out_slot * kN * kDv;
-          dst0 += (odd ? kDv : 0) + (key & ~1);
+          dst0 += (odd ? kDv : 0) + quad * 32 + (lane & ~1);
 #pragma unroll 1
           for (int c32 = 0; c32 < 2; ++c32) {
-            const int col = hr * 64 + c32 * 32, r0 = col % kN;
+            const int col = part * 64 + c32 * 32, r0 = col % kN;
             uint32_t v2[32];
             tmem_ld32(tmem + lane_off + (uint32_t)col, v2);
             tmem_wait_ld();
@@ -966,30 +1120,34 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
       if (!have) break;
       soft_sync<kN>();                             // row constants and limits; shift is free again
       const int all_see = lim[0];                // every row of the unit sees this many keys
-      const float4 a4 = *reinterpret_cast<const float4*>(row_a + my_rows);
+      const float4 a4 = of_rows(row_a);
       float4 nm4 = make_float4(0.f, 0.f, 0.f, 0.f);
 
       w01 = w23 = l01 = l23 = 0;
       for (int t = it.t_begin; t < it.t_end; ++t, ++n) {
-        const uint32_t g = n & 1, pb = n % C::kPBufs;
-        wait<kN>(s, B_SF + g, (n >> 1) & 1, p);
+        const uint32_t g = n % C::kSBufs, pb = n % C::kPBufs;
+        wait<kN>(s, B_SF + g, (n / C::kSBufs) & 1, p);
         tc_fence_after();
-        // y[i][k]: key lane / 4 + 8 i, row my_rows + k
         float y[4][4];
         float inv_g[2];
         {
-          uint32_t hi[2][8], lo[2][8];
-          const uint32_t src = tmem + lane_off + 4 * kN + g * 2 * kN + hr * kR;
+          uint32_t hi[2][8], lo[2][8];             // [j]: group of keys j
+          const uint32_t src = tmem + lane_off + C::kColS + g * 2 * kN + (C::kQTmem ? 32 * kq : kR * rg);
+          if constexpr (C::kQTmem) {
+            tmem_load_16x32(src, reinterpret_cast<uint32_t(&)[16]>(hi));
+            tmem_load_16x32(src + (16u << 16), reinterpret_cast<uint32_t(&)[16]>(lo));
+          } else {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            tmem_load_16x16(src + ((uint32_t)(16 * j) << 16), hi[j]);
-            tmem_load_16x16(src + ((uint32_t)(16 * j) << 16) + kN, lo[j]);
+            for (int j = 0; j < 2; ++j) {
+              tmem_load_16x16(src + ((uint32_t)(16 * j) << 16), hi[j]);
+              tmem_load_16x16(src + ((uint32_t)(16 * j) << 16) + kN, lo[j]);
+            }
           }
           // t' = acc * (a S) + (log2 S - m), for the group of keys i = 0, 1 and that of 2, 3
           uint64_t A[2][2], Bc[2][2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float4 v = reinterpret_cast<const float4*>(s.ptr + C::kOffScale)[g * 8 + 2 * q4 + j];
+            const float4 v = reinterpret_cast<const float4*>(s.ptr + C::kOffScale)[g * 8 + 2 * kq + j];
             inv_g[j] = v.z;
             A[j][0] = mul2(f32x2(a4.x, a4.y), f32x2(v.x, v.x));
             A[j][1] = mul2(f32x2(a4.z, a4.w), f32x2(v.x, v.x));
@@ -1004,7 +1162,7 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
           for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const int j = i >> 1, r = (i & 1) * 2 + k * 4;
+              const int j = i >> 1, r = C::kQTmem ? (i & 1) * 4 + k * 2 : (i & 1) * 2 + k * 4;
               const uint64_t acc =
                   add2(f32x2(__uint_as_float(hi[j][r]), __uint_as_float(hi[j][r + 1])),
                        f32x2(__uint_as_float(lo[j][r]), __uint_as_float(lo[j][r + 1])));
@@ -1013,14 +1171,15 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
         }
         if ((t + 1) * kTile > all_see) {
           // a key that a row does not see weighs nothing, whatever its slot holds
-          const int4 l4 = *reinterpret_cast<const int4*>(lim + my_rows);
+          const int4 l4 = of_rows(lim);
+          constexpr int kStep = C::kQTmem ? 1 : 0;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int k_abs = t * kTile + q4 * 32 + (lane >> 2) + 8 * i;
+            const int k_abs = t * kTile + my_keys + 8 * i;
             if (k_abs >= l4.x) y[i][0] = -INFINITY;
-            if (k_abs >= l4.y) y[i][1] = -INFINITY;
+            if (k_abs + kStep >= l4.y) y[i][1] = -INFINITY;
             if (k_abs >= l4.z) y[i][2] = -INFINITY;
-            if (k_abs >= l4.w) y[i][3] = -INFINITY;
+            if (k_abs + kStep >= l4.w) y[i][3] = -INFINITY;
           }
         }
         float mx = -INFINITY;
@@ -1040,14 +1199,7 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
             m.y = fmaxf(fmax3(y[0][1], y[1][1], y[2][1]), y[3][1]);
             m.z = fmaxf(fmax3(y[0][2], y[1][2], y[2][2]), y[3][2]);
             m.w = fmaxf(fmax3(y[0][3], y[1][3], y[2][3]), y[3][3]);
-#pragma unroll
-            for (int o = 4; o <= 16; o <<= 1) {
-              m.x = fmaxf(m.x, __shfl_xor_sync(0xffffffffu, m.x, o));
-              m.y = fmaxf(m.y, __shfl_xor_sync(0xffffffffu, m.y, o));
-              m.z = fmaxf(m.z, __shfl_xor_sync(0xffffffffu, m.z, o));
-              m.w = fmaxf(m.w, __shfl_xor_sync(0xffffffffu, m.w, o));
-            }
-            if (lane < 4) *reinterpret_cast<float4*>(xm + q4 * kN + my_rows) = m;
+            over_keys(m, [](float a, float b) { return fmaxf(a, b); }, xm + kq * kN);
           }
           soft_sync<kN>();
           if (st < kN) {
@@ -1062,7 +1214,7 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
             // O^T, columns = rows: 64 of its columns for each group of 16 rows' warps
 #pragma unroll 1
             for (int c32 = 0; c32 < 2; ++c32) {
-              const uint32_t col = (uint32_t)(hr * 64 + c32 * 32);
+              const uint32_t col = (uint32_t)(part * 64 + c32 * 32);
               if (!__any_sync(0xffffffffu, shift[col % kN + lane] != 0.f)) continue;
               uint32_t v[32];
               tmem_ld32(tmem + lane_off + col, v);
@@ -1081,8 +1233,8 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
             tmem_wait_st();
             tc_fence_before();
           }
-          const float4 by = *reinterpret_cast<const float4*>(shift + my_rows);
-          nm4 = *reinterpret_cast<const float4*>(row_nm + my_rows);
+          const float4 by = of_rows(shift);
+          nm4 = of_rows(row_nm);
           const uint64_t b01 = f32x2(fast_exp2(by.x), fast_exp2(by.y));
           const uint64_t b23 = f32x2(fast_exp2(by.z), fast_exp2(by.w));
           l01 = mul2(l01, b01);
@@ -1123,25 +1275,30 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
         }
         wait<kN>(s, B_PE + pb, ((n / C::kPBufs) + 1) & 1, p);
         {
-          // lane l gives the address of row l % 8 of matrix l / 8: key 32 q4 + l, its 16 bytes hr
+          // lane l gives the address of key 32 kq + l's 16 bytes rg
           const uint32_t dst = s.base + C::kOffP + pb * 2 * C::kPHalf + key * kN +
-                               16 * (hr ^ (kN == 64 ? (key >> 1) & 3 : (key >> 2) & 1));
-          stmatrix_x4(dst, ph);
-          stmatrix_x4(dst + C::kPHalf, pl);
+                               16 * (rg ^ (kN == 64 ? (key >> 1) & 3 : (key >> 2) & 1));
+          if constexpr (C::kQTmem) {
+            stmatrix_t_x4(dst, ph);
+            stmatrix_t_x4(dst + C::kPHalf, pl);
+          } else {
+            stmatrix_x4(dst, ph);
+            stmatrix_x4(dst + C::kPHalf, pl);
+          }
         }
-        if (t * kTile + q4 * 32 + 32 > all_see) {
+        if (t * kTile + kq * 32 + 32 > all_see) {
           // a weight of 0 does not keep a NaN out of O (0 * NaN): behind the request's last key,
           // where slots may hold anything, a key's values become 0; a key that only some
           // rows see loses its NaN (the rows that see it have a NaN score, so their whole
           // output is NaN in any case).  Four keys a time, eight lanes to a key's 128 bytes of a
           // chunk; the four chunks are shared out to the groups of rows.
           constexpr int kShare = 64 / kN;
-          const int k0 = t * kTile + q4 * 32;      // of the warp's 32 keys: those before `some` are
+          const int k0 = t * kTile + kq * 32;      // of the warp's 32 keys: those before `some` are
           const int some = max(all_see - k0, 0), gone = max(it.keys - k0, 0);   // seen by every row
 #pragma unroll 1
           for (int c = 0; c < kShare; ++c) {
-            const uint32_t vs = (4 * n + kShare * hr + c) % C::kSlots;
-            uint4* row = reinterpret_cast<uint4*>(s.ptr + C::kOffK + vs * kChunkBytes + q4 * 32 * 128) + (lane & 7);
+            const uint32_t vs = (4 * n + kShare * rg + c) % C::kSlots;
+            uint4* row = reinterpret_cast<uint4*>(s.ptr + C::kOffK + vs * kChunkBytes + kq * 32 * 128) + (lane & 7);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const int k = 4 * i + (lane >> 3);
@@ -1370,7 +1527,6 @@ size_t q8_workspace_size(int B, int H, int q_len, int num_sms) {
 cudaError_t launch_decode_q8(const DecodeArgs& a, cudaStream_t stream) {
   Params p;
   p.q = a.q;
-  p.kv = reinterpret_cast<const uint8_t*>(a.kv);
   p.scales = a.kv_scales;
   p.bt = a.block_table;
   p.bt_stride = a.bt_stride;
