@@ -20,8 +20,9 @@
  *     anything is launched; mla_last_error() then returns a message (thread-local).
  *   - Calls are stream-ordered: a call's kernels see every result issued before it on
  *     the stream.  The split-KV combine of mla_decode, the kernel of lse_merge and both
- *     kernels of mla_decode_q8 are programmatic dependent launches: they may be scheduled while the kernel before
- *     them drains, but wait for its completion before they read or write memory.
+ *     kernels of mla_decode_q8 are programmatic dependent launches: they may be scheduled
+ *     while the kernel before them drains, but wait for its completion before they read or
+ *     write memory.
  *   - bf16 means IEEE bfloat16 stored as 16-bit words; results are rounded to nearest
  *     even.  Tensors are dense and row-major unless a stride is given.
  */
@@ -334,6 +335,8 @@ int cp_store_q8(const void* kv_new, const int32_t* ctx_lens, const int32_t* tota
  *                MLA_STATUS_BAD_SCALE; scales of other groups are not used.
  *   block_size   a multiple of 16.
  *   q            a row (one head of one token) with a NaN or an infinity gives NaN outputs.
+ *   scale        scale * s * |q| must stay below 2^127 for every scale s and element of q in
+ *                use (scores beyond float's range give NaN, 0 or -inf as floats do).
  *   ceil(q_len*H/64) <= SMs; num_blocks*block_size and max_blocks*block_size below
  *   2^31 - 65536 (else MLA_ERR_UNSUPPORTED).
  *   workspace    scratch for split-KV, sized by mla_decode_q8_workspace_size (for the shards

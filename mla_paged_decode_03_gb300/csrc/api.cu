@@ -145,8 +145,9 @@ namespace mla {
 
 // Shared by mla_decode (n_shards == 1, the given rank), mla_decode_shards (ranks
 // 0 .. n_shards-1 of cp_world == n_shards, shard-major tables and outputs), their forms over
-// the 8-bit cache (q8: kv_cache is e4m3 and kv_scales its scales) and mla_decode_noalloc (require_full_split: the workspace must hold the scratch of the full
-// split-KV schedule, else the call is refused after every other check).
+// the 8-bit cache (q8: kv_cache is e4m3 and kv_scales its scales) and mla_decode_noalloc
+// (require_full_split: the workspace must hold the scratch of the full split-KV schedule, else
+// the call is refused after every other check).
 int decode_entry(const char* fn, const void* q, const void* kv_cache, bool q8,
                  const float* kv_scales, const int32_t* block_table, int64_t bt_stride,
                  const int32_t* seq_lens, const int32_t* causal_seqlens_global, int B, int H,
@@ -269,9 +270,9 @@ int mla_decode(const void* q, const void* kv_cache, const int32_t* block_table,
                int interleave, float scale, void* out, float* lse, int lse_base_e,
                void* workspace, size_t workspace_bytes, mla_stream_t stream) {
   return mla::decode_entry("mla_decode", q, kv_cache, false, nullptr, block_table, bt_stride,
-                           seq_lens, causal_seqlens_global, B, H, q_len, causal, block_size, num_blocks,
-                           max_blocks, cp_world, cp_rank, interleave, 1, scale, out, lse,
-                           lse_base_e, workspace, workspace_bytes, false, stream);
+                           seq_lens, causal_seqlens_global, B, H, q_len, causal, block_size,
+                           num_blocks, max_blocks, cp_world, cp_rank, interleave, 1, scale, out,
+                           lse, lse_base_e, workspace, workspace_bytes, false, stream);
 }
 
 int mla_decode_shards(const void* q, const void* kv_cache, const int32_t* block_table,

@@ -69,9 +69,9 @@ size_t decode_workspace_for(int B, int H, int q_len, int num_sms, int block_size
 int api_fail(int code, const char* fmt, ...);
 
 // Validation and launch behind mla_decode, mla_decode_shards, mla_decode_noalloc and the
-// decode calls of the 8-bit cache (q8, with kv_scales; api.cu); `stream` is a cudaStream_t.  With require_full_split the workspace must hold
-// the scratch of the full split-KV schedule, else MLA_ERR_UNSUPPORTED (after every other
-// check).
+// decode calls of the 8-bit cache (q8, with kv_scales; api.cu); `stream` is a cudaStream_t.
+// With require_full_split the workspace must hold the scratch of the full split-KV schedule,
+// else MLA_ERR_UNSUPPORTED (after every other check).
 int decode_entry(const char* fn, const void* q, const void* kv_cache, bool q8,
                  const float* kv_scales, const int32_t* block_table, int64_t bt_stride,
                  const int32_t* seq_lens, const int32_t* causal_seqlens_global, int B,

@@ -74,7 +74,7 @@ extern "C" int mla_decode_noalloc(const void* q, const void* kv_cache, const int
   // every argument is checked as mla_decode checks it; only then is the size of the
   // split-KV scratch compared with the array's
   return mla::decode_entry("mla_decode_noalloc", q, kv_cache, false, nullptr, block_table,
-                           bt_stride, seq_lens, causal_seqlens_global, B, H, q_len, causal, block_size, num_blocks,
-                           max_blocks, cp_world, cp_rank, interleave, 1, scale, out, lse,
-                           lse_base_e, sp.ptr, kNoAllocScratchBytes, true, stream);
+                           bt_stride, seq_lens, causal_seqlens_global, B, H, q_len, causal,
+                           block_size, num_blocks, max_blocks, cp_world, cp_rank, interleave, 1,
+                           scale, out, lse, lse_base_e, sp.ptr, kNoAllocScratchBytes, true, stream);
 }

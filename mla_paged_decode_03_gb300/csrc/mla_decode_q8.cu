@@ -6,14 +6,17 @@
 // its group of 16 slots:
 //   t_l = scale S_l <q, k8_l>,  out = sum_l 2^(t'_l - m) S_l v8_l / sum_l 2^(t'_l - m)  (t' in log2).
 //
-// Transposed products.  A unit is kN query rows of one request (32 or 64).  Keys are the
-// M side of both products, query rows the N side:
-//   S^T [128 keys x rows] = K8 [128 x 576] Q^T,   O^T [512 dims x rows] += V8^T [512 x 128] P^T.
-// The tile of 128 keys lies in shared memory once, as TMA brings it (128-byte rows of 128
-// dims, 128-byte swizzle); QK reads it K-major, PV reads the same bytes M-major (the
-// transpose bit of the instruction).  O^T of 64 rows takes 256 tensor-memory columns, so S
-// and O fit one SM and a unit needs no second CTA; the time of both products goes with the
-// number of rows, where rows as M would always pay for 128.
+// Two forms of the products.  A unit is kN query rows of one request, 64 or 32 (rows_per_unit).
+// The tile of 128 keys lies in shared memory once, as TMA brings it (128-byte rows of 128 dims,
+// 128-byte swizzle); QK reads it K-major, PV reads the same bytes M-major (the transpose bit of
+// the instruction).  PV is O^T [512 dims x rows] += V8^T [512 x 128] P^T in both: the time goes
+// with the number of rows, where rows as M would always pay for 128, and O^T of 64 rows takes
+// 256 of the 512 tensor-memory columns, so that a unit needs no second SM.
+//   64 rows: S [hi and lo of 64 rows x 128 keys] = Q K8^T.  Q's latent dims are the tensor-memory
+//     operand, 128 columns beside O^T and one S (QK then reads keys and nothing else: 80 KB of
+//     shared memory a tile where Q in shared memory took 144), its rope dims are in shared memory.
+//   32 rows: S^T [128 keys x hi and lo of 32 rows] = K8 Q^T, Q in shared memory, two S^T: such
+//     units are bound by HBM or by their start, and rows as M = 128 would double QK's time.
 //
 // 8-bit operands without losing bits.  Both factors of a product must be 8-bit types, and
 // a query or a weight rounded to one e4m3 value would be off by up to 2^-4.  So:
@@ -30,15 +33,17 @@
 // Roles (20 warps, 12 for 32 rows): warp 0 loads tiles (TMA, four 16 KB chunks of latent dims
 // and one of rope dims each, chunk by chunk as PV frees them), warp 1 issues the QK products and
 // warp 2 the PV products, each when its inputs have come (one warp for both in a fixed order
-// waits for the later of two inputs; one that polls both takes issue slots from the softmax
-// warps of its scheduler), warp 3 walks the schedule, passes the
-// block's segments on and looks the tiles' scales up, the others take 32 keys and 16 rows each: they
-// read S^T, scale, mask, exponentiate and write P^T; they also prepare Q and write the output.
+// waits for the later of two inputs: 64 x 32k 376 -> 408 us; one that polls both takes issue
+// slots from the softmax warps of its scheduler), warp 3 walks the schedule, passes the block's
+// segments on and looks the tiles' scales up, the others take 32 keys and 16 rows each: they
+// read S, scale, mask, exponentiate and write P^T; they also prepare Q and write the output.
 //
-// Bounds: few rows by the cache's bytes; 64 rows by shared-memory bandwidth: a tile's
-// QK reads 18 x (4 + 4) KB and its PV 32 x (4 + 2) KB, with TMA's and P's writes 426 KB, 3,330
-// cycles at 128 bytes a cycle, against 2,176 cycles of tensor time and about 3,100 of this
-// SM's share of HBM.
+// Bounds: few rows by the cache's bytes (64 x 16 rows of 1k..16k keys: 65.7 us, 47.7 at the
+// copy rate); 64 rows by shared-memory bandwidth: a tile's QK reads 16 x 4 + 2 x (4 + 4) KB and its
+// PV 32 x (4 + 2) KB, TMA writes 72 KB and the softmax 16 KB, 2,880 cycles at 128 bytes a cycle of
+// the 3,100 that it takes, against 2,176 of tensor time.  64 x 128 rows of 32,768 keys: 376 us
+// (418 held for a second, at the power limit), 1.55 PFLOP/s, twice that as issued; 4 x 256
+// rows of 256k..512k: 641 us; 32 x 512 rows of 1k..16k: 225 us.
 //
 // Work split, partials and the combine: as in mla_decode_tc.cu (tiles of all requests on one
 // line, equal ranges, units cut between blocks merged by a second kernel); a block has at most

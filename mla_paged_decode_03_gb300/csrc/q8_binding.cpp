@@ -1,10 +1,10 @@
 // Python binding of the 8-bit cache's calls: argument checks, outputs, the current stream, and
 // the C ABI's functions (handed over by address, so that the library is loaded in one place).
 //
-// A small step's kernels take 3 to 12 us; with checks and allocations in Python and a ctypes call,
-// calls back to back took 26 us (cp_step_tables), 9 us (cp_store_q8) and 26 us (mla_decode_q8 of two
-// short requests); through this they take 8, 5 and 12.5 us.  Only the marshalling is here: what a call means, and every check
-// of sizes, is the C ABI's.
+// A small step's kernels take 3 to 12 us; with checks and allocations in Python and a ctypes
+// call, calls back to back took 26 us (cp_step_tables), 9 us (cp_store_q8) and 26 us
+// (mla_decode_q8 of two short requests); through this they take 8, 5 and 12.5 us.  Only the
+// marshalling is here: what a call means, and every check of sizes, is the C ABI's.
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
