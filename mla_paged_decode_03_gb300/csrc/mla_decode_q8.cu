@@ -157,6 +157,7 @@ struct Params {
   int row_tiles;               // R
   int units;
   int groups;                  // G: blocks g*R .. g*R + R-1 take the g-th range of the line
+  int comb_blocks, comb_warps; // combine: blocks a unit, warps a row
   int whole_units;             // no workspace: requests go round the groups uncut
   int box_rows;                // rows per TMA box (a page is whole boxes)
   FastDiv div_bs;
@@ -1344,15 +1345,17 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
 }
 
 // Merges the partials of units cut between blocks; a unit with no key gets out = 0, lse = -inf.
-// A warp per row, eight rows a block.  The unit's first holder wrote its slot 1, the others,
-// which continue the unit, their slot 0.
-template <int kN>
+// comb_blocks blocks a unit, comb_warps warps a row, which share its partials.  The unit's first
+// holder wrote its slot 1, the others, which continue the unit, their slot 0.
+// (kMany: more than one warp a row.  Then a warp loads four partials at a time, which takes 80
+// registers; with one warp a row and few partials that cost 2 us of 50 in fewer resident blocks.)
+template <int kN, bool kMany>
 __global__ void __launch_bounds__(256) mla_q8_combine_kernel(const Params p) {
   __shared__ int s_nt;
   __shared__ int2 s_m;
+  extern __shared__ float s_part[];                 // [8][kDv] sums and [8] (kMany)
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int kBlocks = kN / 8;
-  const int u = blockIdx.x / kBlocks, rb = blockIdx.x % kBlocks;
+  const int u = blockIdx.x / p.comb_blocks, rb = blockIdx.x - u * p.comb_blocks;
   const int b = (int)fdiv((unsigned)u, p.div_rt), rt = u - b * p.row_tiles;
   if (threadIdx.x == 0) {
     if (rt == 0 && rb == 0 && __ldg(p.seq_lens + b) > p.max_blocks * p.bs)
@@ -1370,78 +1373,123 @@ __global__ void __launch_bounds__(256) mla_q8_combine_kernel(const Params p) {
   }
   __syncthreads();
   const int2 m = s_m;
-  if (s_nt > 0 && m.x == m.y) return;               // one block wrote the result
-  const int lane = threadIdx.x & 31, r = rb * 8 + (threadIdx.x >> 5);
-  const int row = rt * kN + r;
-  if (row >= p.rows) return;
-  const long long grow = (long long)b * p.rows + row;
-  uint16_t* o = p.out + grow * kDv;
-  if (s_nt == 0) {
-    *reinterpret_cast<uint4*>(o + 8 * lane) = make_uint4(0, 0, 0, 0);
-    *reinterpret_cast<uint4*>(o + 256 + 8 * lane) = make_uint4(0, 0, 0, 0);
-    if (p.lse != nullptr && lane == 0) p.lse[grow] = -INFINITY;
-    return;
-  }
-  const unsigned int T = p.hdr[0];
+  const bool empty = s_nt == 0;
+  if (!empty && m.x == m.y) return;                 // one block wrote the result
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int W = kMany ? p.comb_warps : 1, at_once = 8 / W, mine = warp % W;
+  const int rows = kN / p.comb_blocks;              // the block's, from rb * rows on
+  const unsigned int T = empty ? 0u : p.hdr[0];
   auto holds = [&](int g) { return range_start(p, T, g) < range_start(p, T, g + 1); };
-  auto slot_of = [&](int g) { return (2ll * (g * p.row_tiles + rt) + (g == m.x ? 1 : 0)) * kN + r; };
-  float mx = -INFINITY;
-  bool nan = false;
-  for (int g0 = m.x; g0 <= m.y; g0 += 32) {
-    const int g = g0 + lane;
-    if (g <= m.y && holds(g)) {
-      const float l = p.ws_lse[slot_of(g)].x;
-      nan |= l != l;
-      mx = fmaxf(mx, l);
+  for (int r0 = 0; r0 < rows; r0 += at_once) {
+    const int r = rb * rows + r0 + warp / W, row = rt * kN + r;
+    const bool valid = row < p.rows;
+    const long long grow = (long long)b * p.rows + row;
+    uint16_t* o = p.out + grow * kDv;
+    if (empty) {
+      if (valid && mine == 0) {
+        *reinterpret_cast<uint4*>(o + 8 * lane) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(o + 256 + 8 * lane) = make_uint4(0, 0, 0, 0);
+        if (p.lse != nullptr && lane == 0) p.lse[grow] = -INFINITY;
+      }
+      continue;
     }
-  }
-#pragma unroll
-  for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-  if (__any_sync(0xffffffffu, nan)) mx = __int_as_float(0x7fc00000);
-  float acc[16];
-#pragma unroll
-  for (int k = 0; k < 16; ++k) acc[k] = 0.f;
-  float wsum = 0.f;
-  if (mx != -INFINITY) {
+    auto slot_of = [&](int g) { return (2ll * (g * p.row_tiles + rt) + (g == m.x ? 1 : 0)) * kN + r; };
+    float mx = -INFINITY;
+    bool nan = false;
     for (int g0 = m.x; g0 <= m.y; g0 += 32) {
       const int g = g0 + lane;
-      float2 lw = make_float2(-INFINITY, 0.f);
-      if (g <= m.y && holds(g)) lw = p.ws_lse[slot_of(g)];
-      const float wl = exp2f(lw.x - mx), fl = wl * lw.y;
-      const int nh = min(32, m.y - g0 + 1);
-#pragma unroll 4
-      for (int k = 0; k < nh; ++k) {
-        const float w = __shfl_sync(0xffffffffu, wl, k), f = __shfl_sync(0xffffffffu, fl, k);
-        if (w == 0.f) continue;                     // nothing there, or nothing that counts
-        wsum += w;
-        const uint4* src = reinterpret_cast<const uint4*>(p.ws_o + slot_of(g0 + k) * kDv) + lane;
+      if (g <= m.y && holds(g)) {
+        const float l = p.ws_lse[slot_of(g)].x;
+        nan |= l != l;
+        mx = fmaxf(mx, l);
+      }
+    }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint4 v = __ldcs(src + 32 * j);
-          const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+    for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+    if (__any_sync(0xffffffffu, nan)) mx = __int_as_float(0x7fc00000);
+    float acc[16];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&x[e]));
-            acc[8 * j + 2 * e] = fmaf(f, t.x, acc[8 * j + 2 * e]);
-            acc[8 * j + 2 * e + 1] = fmaf(f, t.y, acc[8 * j + 2 * e + 1]);
+    for (int k = 0; k < 16; ++k) acc[k] = 0.f;
+    float wsum = 0.f;
+    if (mx != -INFINITY) {
+      for (int g0 = m.x; g0 <= m.y; g0 += 32) {
+        const int g = g0 + lane;
+        float2 lw = make_float2(-INFINITY, 0.f);
+        if (g <= m.y && holds(g)) lw = p.ws_lse[slot_of(g)];
+        const float wl = exp2f(lw.x - mx), fl = wl * lw.y;
+        const int nh = min(32, m.y - g0 + 1);
+        constexpr int kAhead = kMany ? 4 : 1;       // partials whose loads are in flight together
+        for (int k0 = mine; k0 < nh; k0 += kAhead * W) {
+          float f[kAhead];
+          uint4 v[kAhead][2];
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) {
+            const int k = min(k0 + i * W, 31);
+            const float w = __shfl_sync(0xffffffffu, wl, k);
+            f[i] = __shfl_sync(0xffffffffu, fl, k);
+            // (what has no weight is not read: nothing there, or nothing that counts)
+            const bool use = k0 + i * W < nh && w != 0.f;
+            const uint4* src = reinterpret_cast<const uint4*>(p.ws_o + slot_of(g0 + k) * kDv) + lane;
+            if (use) wsum += w;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) v[i][j] = use ? __ldcs(src + 32 * j) : make_uint4(0u, 0u, 0u, 0u);
+            if (!use) f[i] = 0.f;
           }
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t x[4] = {v[i][j].x, v[i][j].y, v[i][j].z, v[i][j].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&x[e]));
+                acc[8 * j + 2 * e] = fmaf(f[i], t.x, acc[8 * j + 2 * e]);
+                acc[8 * j + 2 * e + 1] = fmaf(f[i], t.y, acc[8 * j + 2 * e + 1]);
+              }
+            }
         }
       }
     }
-  }
-  const float inv = mx == -INFINITY ? 0.f : 1.f / wsum;
+    if constexpr (kMany) {
+      // lane l has dims 8 l .. + 7 and 256 further; in shared memory as four words for each lane, so
+      // that a warp's access is 512 consecutive bytes
+      float4* to = reinterpret_cast<float4*>(s_part + warp * kDv) + lane;
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    uint32_t w4[4];
+      for (int k = 0; k < 4; ++k)
+        to[32 * k] = make_float4(acc[4 * k], acc[4 * k + 1], acc[4 * k + 2], acc[4 * k + 3]);
+      if (lane == 0) s_part[8 * kDv + warp] = wsum;
+      __syncthreads();
+      if (mine == 0) {
+        for (int q = 1; q < W; ++q) {
+          const float4* from = reinterpret_cast<const float4*>(s_part + (warp + q) * kDv) + lane;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(acc[8 * j + 2 * e] * inv, acc[8 * j + 2 * e + 1] * inv);
-      w4[e] = *reinterpret_cast<const uint32_t*>(&h);
+          for (int k = 0; k < 4; ++k) {
+            const float4 a = from[32 * k];
+            acc[4 * k] += a.x;
+            acc[4 * k + 1] += a.y;
+            acc[4 * k + 2] += a.z;
+            acc[4 * k + 3] += a.w;
+          }
+          wsum += s_part[8 * kDv + warp + q];
+        }
+      }
+      __syncthreads();
     }
-    *reinterpret_cast<uint4*>(o + 256 * j + 8 * lane) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+    if (mine != 0 || !valid) continue;
+    const float inv = mx == -INFINITY ? 0.f : 1.f / wsum;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      uint32_t w4[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(acc[8 * j + 2 * e] * inv, acc[8 * j + 2 * e + 1] * inv);
+        w4[e] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      *reinterpret_cast<uint4*>(o + 256 * j + 8 * lane) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+    }
+    if (p.lse != nullptr && lane == 0)
+      p.lse[grow] = mx == -INFINITY ? -INFINITY : (mx + log2f(wsum)) * p.lse_mul;
   }
-  if (p.lse != nullptr && lane == 0)
-    p.lse[grow] = mx == -INFINITY ? -INFINITY : (mx + log2f(wsum)) * p.lse_mul;
 }
 
 // ---- host ---------------------------------------------------------------------------------------
@@ -1503,8 +1551,10 @@ cudaError_t launch(const CUtensorMap& kmap, const CUtensorMap& rmap, const Param
   dk.cfg.dynamicSmemBytes = Cfg<kN>::kSmem;
   const cudaError_t e = cudaLaunchKernelEx(&dk.cfg, mla_decode_q8_kernel<kN>, kmap, rmap, p);
   if (e != cudaSuccess) return e;
-  DependentLaunch dl(dim3((unsigned)p.units * (kN / 8)), dim3(256), stream);
-  return cudaLaunchKernelEx(&dl.cfg, mla_q8_combine_kernel<kN>, p);
+  DependentLaunch dl(dim3((unsigned)p.units * (unsigned)p.comb_blocks), dim3(256), stream);
+  if (p.comb_warps == 1) return cudaLaunchKernelEx(&dl.cfg, mla_q8_combine_kernel<kN, false>, p);
+  dl.cfg.dynamicSmemBytes = 8 * (kDv + 1) * sizeof(float);
+  return cudaLaunchKernelEx(&dl.cfg, mla_q8_combine_kernel<kN, true>, p);
 }
 
 }  // namespace
@@ -1596,6 +1646,13 @@ cudaError_t launch_decode_q8(const DecodeArgs& a, cudaStream_t stream) {
     if (p.groups > a.B) p.groups = a.B;
   }
   const int blocks = p.groups * p.row_tiles;
+  // The combine: a unit has about groups / B partials.  Enough warps a row that each has few of
+  // them, and as many blocks as give every row its warps, but not many more than can be resident
+  // at once (most units have nothing to merge, and a block's start is all they cost).
+  const int parts = p.whole_units ? 1 : p.groups / a.B;
+  p.comb_warps = parts >= 24 ? 8 : parts >= 12 ? 4 : parts >= 6 ? 2 : 1;
+  p.comb_blocks = n * p.comb_warps / 8;
+  while (p.comb_blocks > 1 && (long long)p.units * p.comb_blocks > 16LL * a.num_sms) p.comb_blocks /= 2;
   p.div_H = make_fastdiv((unsigned)a.H);
   p.div_span = make_fastdiv((unsigned)p.span);
   p.div_rt = make_fastdiv((unsigned)p.row_tiles);
