@@ -274,6 +274,13 @@ __device__ __forceinline__ void stmatrix_t_x4(uint32_t addr, const uint32_t (&v)
                "r"(v[1]), "r"(v[2]), "r"(v[3])
                : "memory");
 }
+// Four 8 x 8 matrices of 16-bit elements, stored transposed: lane l holds elements 2 (l % 4) and the
+// next of row l / 4 of each, and gives the address of column l % 8 of matrix l / 8.
+__device__ __forceinline__ void stmatrix_t16_x4(uint32_t addr, const uint32_t (&v)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
+}
 __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -536,6 +543,51 @@ __device__ __forceinline__ bool take_segment(const Ctx& s, uint32_t i, const Par
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar<kN>(s, B_GE + slot));
   return ok && seg.b >= 0;
+}
+
+// A warp's part of a segment's output: 32 dims (of chunk col / kN) and twice 32 rows of O^T, which
+// go through 2 KB of shared memory (its share of P^T, which no product reads then) to become rows
+// of 64 bytes.  The unit's output (bf16) is O / l.  A partial is O / w, w the sum of the weights
+// (scales included): a mean of e4m3 values, at most 448, so that half precision holds it to 2^-11
+// in half the bytes of fp32; w / l goes with the row's LSE.  (A function of its own, so that its
+// registers do not weigh on the loop over the tiles.)
+template <int kN>
+__device__ __noinline__ void store_rows(uint32_t tmem, uint8_t* stage, const float* inv, uint16_t* dst, int part,
+                                        int nrow, bool single) {
+  using C = Cfg<kN>;
+  static_assert(C::kPBufs * 2 * C::kPHalf >= 2048 * C::kSoftWarps, "2 KB a warp");
+  const int lane = threadIdx.x & 31, c4 = lane & 3;
+#pragma unroll 1
+  for (int c32 = 0; c32 < 2; ++c32) {
+    const int col = part * 64 + c32 * 32, r0 = col % kN;
+    uint32_t v[2][16];                     // [h]: dims 16 h + lane / 4 and + 8
+    tmem_load_16x32(tmem + (uint32_t)col, v[0]);
+    tmem_load_16x32(tmem + (16u << 16) + (uint32_t)col, v[1]);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = *reinterpret_cast<const float2*>(inv + r0 + 8 * i + 2 * c4);
+      uint32_t u[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float a = __uint_as_float(v[k >> 1][4 * i + 2 * (k & 1)]) * f.x;
+        const float b = __uint_as_float(v[k >> 1][4 * i + 2 * (k & 1) + 1]) * f.y;
+        const __nv_bfloat162 o2 = __floats2bfloat162_rn(a, b);
+        u[k] = single ? *reinterpret_cast<const uint32_t*>(&o2) : half2_of(a, b);
+      }
+      // lane l gives the address of row l % 8 of the eight, dims 8 (l / 8) ..
+      const int r = 8 * i + (lane & 7);
+      stmatrix_t16_x4(smem_u32(stage) + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4), u);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + (lane >> 2);
+      const uint4 o = *reinterpret_cast<const uint4*>(stage + r * 64 + ((c4 ^ ((r >> 1) & 3)) << 4));
+      if (r0 + r < nrow) *reinterpret_cast<uint4*>(dst + (r0 + r) * kDv + col / kN * 128) = o;
+    }
+    __syncwarp();
+  }
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -1088,38 +1140,9 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
             }
           }
           soft_sync<kN>();
-          // O^T: a lane has one dim of 32 rows; neighbouring lanes have neighbouring dims, so even
-          // lanes store two dims of row k and odd lanes two of row k + 1.  The unit's output (bf16) is
-          // O / l.  A partial is O / w, w the sum of the weights (scales included): a mean of
-          // e4m3 values, at most 448, so that half precision holds it to 2^-11 in half the bytes of
-          // fp32; w / l goes with the row's LSE.
-          const bool odd = lane & 1;
-          const int nrow = min(kN, p.rows - out_row0) - (odd ? 1 : 0);
-          uint16_t* dst0 = out_single ? p.out + out_row * kDv : p.ws_o + out_slot * kN * kDv;
-          dst0 += (odd ? kDv : 0) + quad * 32 + (lane & ~1);
-#pragma unroll 1
-          for (int c32 = 0; c32 < 2; ++c32) {
-            const int col = part * 64 + c32 * 32, r0 = col % kN;
-            uint32_t v2[32];
-            tmem_ld32(tmem + lane_off + (uint32_t)col, v2);
-            tmem_wait_ld();
-            const float4* inv = reinterpret_cast<const float4*>(shift + r0);
-            uint16_t* dst = dst0 + r0 * kDv + col / kN * 128;
-#pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-              const float4 f = inv[k / 4];
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const float a = __uint_as_float(v2[k + 2 * h]) * (h ? f.z : f.x);
-                const float b = __uint_as_float(v2[k + 2 * h + 1]) * (h ? f.w : f.y);
-                const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-                const float lo = odd ? got : a, hi = odd ? b : got;
-                const __nv_bfloat162 o2 = __floats2bfloat162_rn(lo, hi);
-                const uint32_t o = out_single ? *reinterpret_cast<const uint32_t*>(&o2) : half2_of(lo, hi);
-                if (r0 + k + 2 * h < nrow) *reinterpret_cast<uint32_t*>(dst + (k + 2 * h) * kDv) = o;
-              }
-            }
-          }
+          const int nrow = min(kN, p.rows - out_row0);
+          uint16_t* dst = (out_single ? p.out + out_row * kDv : p.ws_o + out_slot * kN * kDv) + quad * 32 + c4 * 8;
+          store_rows<kN>(tmem + lane_off, s.ptr + C::kOffP + (warp - 4) * 2048, shift, dst, part, nrow, out_single);
           tc_fence_before();
         }
       }
