@@ -445,8 +445,8 @@ __device__ __forceinline__ int unit_keys(const Params& p, const Lens& n, int rt)
 __device__ __forceinline__ int tiles_of(int keys) { return (keys + kTile - 1) / kTile; }
 // A request's length on the split line: its tiles after the start-up share.
 template <int kN>
-__device__ __forceinline__ unsigned int req_span(const Params& p, int b) {
-  const int nt = tiles_of(unit_keys<kN>(p, lens_of(p, b), p.row_tiles - 1));
+__device__ __forceinline__ unsigned int req_span(const Params& p, const Lens& n) {
+  const int nt = tiles_of(unit_keys<kN>(p, n, p.row_tiles - 1));
   return nt > 0 ? (unsigned)(nt + p.seg_tiles) : 0u;
 }
 // floor(T * c / G) for 0 <= c <= G (G <= 2^15)
@@ -467,9 +467,8 @@ struct SegIter {
   unsigned int g0, g_end;         // the request's first tile and the range's end on the line
   Seg seg;
 
-  // request seg.b from tile tb of it on
-  __device__ bool set(const Params& p, int tb) {
-    const Lens n = lens_of(p, seg.b);
+  // request seg.b, of lengths n, from tile tb of it on
+  __device__ bool set(const Params& p, const Lens& n, int tb) {
     req_nt = tiles_of(unit_keys<kN>(p, n, p.row_tiles - 1));
     seg.keys = unit_keys<kN>(p, n, rt);
     seg.cap = n.cap;
@@ -494,10 +493,10 @@ struct SegIter {
       }
       seg.b += p.whole_units ? p.groups : 1;
       if (seg.b >= p.B) return false;
-      if (set(p, 0)) return true;
+      if (set(p, lens_of(p, seg.b), 0)) return true;
     }
   }
-  // scan: the request that holds the range's first position, and where its tiles begin
+  // scan: the request that holds the range's first position, where its tiles begin, its lengths
   __device__ bool first(const Params& p, unsigned int T, const int* scan) {
     grp = (int)fdiv(blockIdx.x, p.div_rt);
     rt = blockIdx.x - grp * p.row_tiles;
@@ -505,14 +504,14 @@ struct SegIter {
       g0 = g_end = 0;
       seg.b = grp;
       if (seg.b >= p.B) return false;
-      return set(p, 0) || next(p);
+      return set(p, lens_of(p, seg.b), 0) || next(p);
     }
     const unsigned int a = range_start(p, T, grp);
     g_end = range_start(p, T, grp + 1);
     if (a >= g_end || scan[0] < 0) return false;
     seg.b = scan[0];
     g0 = (unsigned)scan[1];
-    return set(p, a > g0 ? (int)(a - g0) : 0) || next(p);
+    return set(p, Lens{scan[2], scan[3], scan[4]}, a > g0 ? (int)(a - g0) : 0) || next(p);
   }
 };
 
@@ -650,11 +649,13 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
       __syncthreads();
       return incl;
     };
-    unsigned int n = tid < p.B ? req_span<kN>(p, tid) : 0u, total;
+    Lens own{0, 0, 0};
+    if (tid < p.B) own = lens_of(p, tid);
+    unsigned int n = tid < p.B ? req_span<kN>(p, own) : 0u, total;
     unsigned int end = scan(n, total);
     T = total;
     for (int b0 = kThreads; b0 < p.B; b0 += kThreads) {
-      scan(b0 + tid < p.B ? req_span<kN>(p, b0 + tid) : 0u, total);
+      scan(b0 + tid < p.B ? req_span<kN>(p, lens_of(p, b0 + tid)) : 0u, total);
       T += total;
     }
     if (!p.whole_units && T > 0) {
@@ -662,13 +663,17 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
       unsigned int running = 0;
       for (int b0 = 0; b0 < p.B; b0 += kThreads) {
         if (p.B > kThreads) {                      // more requests than threads: summed again
-          n = b0 + tid < p.B ? req_span<kN>(p, b0 + tid) : 0u;
+          if (b0 + tid < p.B) own = lens_of(p, b0 + tid);
+          n = b0 + tid < p.B ? req_span<kN>(p, own) : 0u;
           end = scan(n, total);
         }
         const unsigned int excl = running + end - n;
         if (n > 0 && excl <= a && a < excl + n) {
           s_scan[0] = b0 + tid;
           s_scan[1] = (int)(excl + p.seg_tiles);
+          s_scan[2] = own.cap;
+          s_scan[3] = own.g;
+          s_scan[4] = own.rank;
         }
         running += total;
       }
@@ -1376,6 +1381,7 @@ template <int kN, bool kMany>
 __global__ void __launch_bounds__(256) mla_q8_combine_kernel(const Params p) {
   __shared__ int s_nt;
   __shared__ int2 s_m;
+  __shared__ unsigned int s_T;
   extern __shared__ float s_part[];                 // [8][kDv] sums and [8] (kMany)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int u = blockIdx.x / p.comb_blocks, rb = blockIdx.x - u * p.comb_blocks;
@@ -1383,16 +1389,19 @@ __global__ void __launch_bounds__(256) mla_q8_combine_kernel(const Params p) {
   if (threadIdx.x == 0) {
     if (rt == 0 && rb == 0 && __ldg(p.seq_lens + b) > p.max_blocks * p.bs)
       atomicOr(p.status, MLA_STATUS_SEQ_TOO_LONG);
-    const int nt = tiles_of(unit_keys<kN>(p, lens_of(p, b), rt));
+    s_nt = tiles_of(unit_keys<kN>(p, lens_of(p, b), rt));
+  } else if (threadIdx.x == 32) {
+    // (three threads, so that the loads do not wait for one another)
     int2 m = make_int2(0, 0);
-    if (nt > 0 && !p.whole_units) {
+    if (!p.whole_units) {
       m = p.meta[u];
-      // inside [0, groups) whatever a decode that gave up early left there
+      // inside [0, groups) whatever a decode that gave up early left there; not set for no keys
       m.x = min(max(m.x, 0), p.groups - 1);
       m.y = min(max(m.y, m.x), p.groups - 1);
     }
-    s_nt = nt;
     s_m = m;
+  } else if (threadIdx.x == 64) {
+    s_T = p.whole_units ? 0u : p.hdr[0];
   }
   __syncthreads();
   const int2 m = s_m;
@@ -1401,7 +1410,7 @@ __global__ void __launch_bounds__(256) mla_q8_combine_kernel(const Params p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int W = kMany ? p.comb_warps : 1, at_once = 8 / W, mine = warp % W;
   const int rows = kN / p.comb_blocks;              // the block's, from rb * rows on
-  const unsigned int T = empty ? 0u : p.hdr[0];
+  const unsigned int T = s_T;
   auto holds = [&](int g) { return range_start(p, T, g) < range_start(p, T, g + 1); };
   for (int r0 = 0; r0 < rows; r0 += at_once) {
     const int r = rb * rows + r0 + warp / W, row = rt * kN + r;
