@@ -610,9 +610,9 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
     prefetch_tensormap(&kmap);
     prefetch_tensormap(&rmap);
   }
-  if (tid == 0) {
-    *s.abort = 0;
-    for (int i = 0; i < B_COUNT; ++i) {
+  if (warp == 2) {
+    if (lane == 0) *s.abort = 0;
+    for (int i = lane; i < B_COUNT; i += 32) {
       const bool by_warps = i == B_SE || i == B_SE + 1 || i == B_PF || i == B_PF + 1 || i == B_QF;
       const bool by_all = i >= B_GE && i < B_GE + kSegRing;
       const int count = by_all ? C::kSoftWarps + 3 : by_warps ? C::kSoftWarps : i == B_SF || i == B_SF + 1 ? 2 : 1;
