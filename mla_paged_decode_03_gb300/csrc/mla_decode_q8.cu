@@ -1386,6 +1386,8 @@ __global__ void __launch_bounds__(256) mla_q8_combine_kernel(const Params p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int u = blockIdx.x / p.comb_blocks, rb = blockIdx.x - u * p.comb_blocks;
   const int b = (int)fdiv((unsigned)u, p.div_rt), rt = u - b * p.row_tiles;
+  const int rows = kN / p.comb_blocks;              // the block's, from rb * rows on
+  if (rt * kN + rb * rows >= p.rows) return;        // rows of no request
   if (threadIdx.x == 0) {
     if (rt == 0 && rb == 0 && __ldg(p.seq_lens + b) > p.max_blocks * p.bs)
       atomicOr(p.status, MLA_STATUS_SEQ_TOO_LONG);
@@ -1409,7 +1411,6 @@ __global__ void __launch_bounds__(256) mla_q8_combine_kernel(const Params p) {
   if (!empty && m.x == m.y) return;                 // one block wrote the result
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int W = kMany ? p.comb_warps : 1, at_once = 8 / W, mine = warp % W;
-  const int rows = kN / p.comb_blocks;              // the block's, from rb * rows on
   const unsigned int T = s_T;
   auto holds = [&](int g) { return range_start(p, T, g) < range_start(p, T, g + 1); };
   for (int r0 = 0; r0 < rows; r0 += at_once) {
@@ -1430,7 +1431,7 @@ __global__ void __launch_bounds__(256) mla_q8_combine_kernel(const Params p) {
     bool nan = false;
     for (int g0 = m.x; g0 <= m.y; g0 += 32) {
       const int g = g0 + lane;
-      if (g <= m.y && holds(g)) {
+      if (valid && g <= m.y && holds(g)) {
         const float l = p.ws_lse[slot_of(g)].x;
         nan |= l != l;
         mx = fmaxf(mx, l);
@@ -1539,16 +1540,16 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encoder() {
   return fn;
 }
 
-// Rows per unit: 32 or 64.  A tile costs a unit of 32 rows 0.69 of what it costs one of 64, so
-// two of them take 1.4 times as long, but their start (Q, first loads) and output are 3 to 4 us
-// shorter.  32 where a request has no more rows (64 x 16 rows of up to 16k keys: 65.8 us,
-// 77.8 with units of 64), and where full tables would give a block fewer than 8 tiles in units
-// of 64 (8 x 128 rows: of 1,024 keys 15.0 / 19.3 us, of 4,096 21.4 / 23.7, of 8,192 29.4 / 30.0);
-// else 64 (16 x 80 rows of 16,384 keys 68.4 / 67.3 us, 64 x 128 of 32,768 560 / 405).
+// Rows per unit: 32 or 64.  A tile costs a unit of 32 rows 0.85 of what it costs one of 64, so
+// two of them take 1.7 times as long, but their start (Q, first loads) and output are 3 to 4 us
+// shorter.  32 where a request has no more rows, and where full tables would give a block fewer
+// than 5 tiles in units of 64 (units of 32 / 64, 8 x 128 rows of 1,024 keys 14.4 / 17.5 us, of
+// 4,096 20.5 / 21.4, of 8,192 28.6 / 27.4; 64 x 128 of 512 24.0 / 26.3, of 1,024 33.6 / 33.0;
+// 1 x 128 of 8,192 15.1 / 18.6; 16 x 80 of 1,024 17.1 / 19.1, of 16,384 67.0 / 60.5); else 64.
 int rows_per_unit(long long B, long long rows, long long max_keys, int num_sms) {
   if (rows <= 32) return 32;
   if ((rows + 31) / 32 > num_sms) return 64;
-  return B * ((rows + 63) / 64) * ((max_keys + kTile - 1) / kTile) < 8LL * num_sms ? 32 : 64;
+  return B * ((rows + 63) / 64) * ((max_keys + kTile - 1) / kTile) < 5LL * num_sms ? 32 : 64;
 }
 int rows_per_unit(const DecodeArgs& a) {
   return rows_per_unit(a.B, (long long)a.H * a.q_len, (long long)a.max_blocks * a.block_size, a.num_sms);

@@ -29,7 +29,8 @@ Q8_GROUP = 16      # consecutive slots of a page that share a scale
 
 
 class StepTables(NamedTuple):
-    """What ``cp_step_tables`` gives besides the updated block table and ring."""
+    """What ``cp_step_tables`` gives besides the updated block table and ring (new outputs of one
+    type share an allocation)."""
     total_lens: torch.Tensor               # int32 [B], global lengths after the step
     seq_lens: torch.Tensor                 # int32 [n_ranks, B], shard-local lengths
     positions: torch.Tensor                # int64 [B, N], -1 where there is no new token

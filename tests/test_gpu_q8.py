@@ -75,8 +75,8 @@ def units(request):
 
 def bt32(table):
     """A block table on the GPU.  The decode takes units of 64 rows when full tables would give
-    every SM eight tiles of 128 keys; that many more columns of 16 slots or more make it do so
-    at any length."""
+    every SM some tiles of 128 keys; columns for eight (of 16 slots or more) make it do so at any
+    length."""
     return torch.nn.functional.pad(i32(table), (0, _extra_columns), value=-1)
 
 
