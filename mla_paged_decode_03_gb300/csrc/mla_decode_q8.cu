@@ -108,8 +108,8 @@ struct Cfg {
   static constexpr int kOffRope = kOffK + kSlots * kChunkBytes;
   static constexpr int kOffP = kOffRope + kRopeBytes;
   static constexpr int kOffBar = kOffP + kPBufs * 2 * kPHalf;
-  static constexpr int kOffRow = kOffBar + 384;            // four words for each row (softmax warps)
-  static constexpr int kOffMisc = kOffRow + 16 * kN;       // tmem base, abort, scan result
+  static constexpr int kOffRow = kOffBar + 384;            // five words for each row (softmax warps)
+  static constexpr int kOffMisc = kOffRow + 20 * kN;       // tmem base, abort, scan result
   static constexpr int kOffSeg = kOffMisc + 48;            // Seg[kSegRing]
   static constexpr int kOffScale = kOffSeg + 32 * kSegRing;   // float4 [kSBufs tiles][8 groups of 16 keys]
   static constexpr int kSmem = kOffScale + 128 * kSBufs + 1008;   // + alignment slack
@@ -949,7 +949,8 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
     float* row_a = reinterpret_cast<float*>(s.ptr + C::kOffRow);     // log2 units per unit of S
     float* row_nm = row_a + kN;                                      // minus the reference
     float* shift = row_nm + kN;                                      // its move; later 1 / l
-    int* lim = reinterpret_cast<int*>(shift + kN);                   // keys the row sees
+    float* factor = shift + kN;                                      // 2^shift
+    int* lim = reinterpret_cast<int*>(factor + kN);                  // keys the row sees
     // the thread's rows' values of a row array (by k of y[i][k])
     auto of_rows = [&](const auto* v) {
       using T = std::remove_cv_t<std::remove_reference_t<decltype(*v)>>;
@@ -993,7 +994,7 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
       row_a[r] = ex == 255 ? __int_as_float(0x7fc00000) : a;          // NaN or infinity: a NaN row
       row_nm[r] = 0.f;
     };
-    auto factor = [](int ex) { return __int_as_float((min(134 - ex, 126) + 127) << 23); };
+    auto q_factor = [](int ex) { return __int_as_float((min(134 - ex, 126) + 127) << 23); };
     uint32_t n = 0;
     // The order of a block's segments: Q of the next one is prepared (and its first QK may run)
     // before the output of the one before is written, which waits for its last PV.
@@ -1061,7 +1062,7 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               uint32_t h[2], l[2];
-              split8(w[k & 1][2 * half + (k >> 1)], factor(k & 1 ? e1 : e0), h, l);
+              split8(w[k & 1][2 * half + (k >> 1)], q_factor(k & 1 ? e1 : e0), h, l);
               hi[2 * k] = h[0];
               hi[2 * k + 1] = h[1];
               lo[2 * k] = l[0];
@@ -1073,7 +1074,7 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
           }
           {
             uint32_t h[2], l[2];
-            split8(wr, factor(second ? e1 : e0), h, l);
+            split8(wr, q_factor(second ? e1 : e0), h, l);
             const int line = 32 * rg + (lane >> 2) + (second ? 8 : 0);            // of hi; lo is 16 on
             uint8_t* dst = s.ptr + C::kOffQRope + line * 64 + (((piece >> 1) ^ ((line >> 1) & 3)) << 4) +
                            (piece & 1) * 8;
@@ -1104,7 +1105,7 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 9; ++i) {
             uint32_t h[2], l[2];
-            split8(w[i], factor(ex), h, l);
+            split8(w[i], q_factor(ex), h, l);
             uint8_t* dst = i < 8 ? lat + (i >> 1) * C::kQChunk + ((((i & 1) * 4 + (l8 >> 1)) ^ (col & 7)) << 4)
                                  : rope;
             *reinterpret_cast<uint2*>(dst) = make_uint2(h[0], h[1]);
@@ -1241,6 +1242,7 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
             float by = 0.f;
             if (m != -INFINITY && (first || m > kMove)) by = kPlace - m;
             shift[st] = by;
+            factor[st] = fast_exp2(by);
             row_nm[st] += by;
           }
           soft_sync<kN>();
@@ -1253,14 +1255,14 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
               uint32_t v[32];
               tmem_ld32(tmem + lane_off + col, v);
               tmem_wait_ld();
-              const float4* by = reinterpret_cast<const float4*>(shift + col % kN);
+              const float4* by = reinterpret_cast<const float4*>(factor + col % kN);
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
                 const float4 f = by[k];
-                v[4 * k] = __float_as_uint(__uint_as_float(v[4 * k]) * fast_exp2(f.x));
-                v[4 * k + 1] = __float_as_uint(__uint_as_float(v[4 * k + 1]) * fast_exp2(f.y));
-                v[4 * k + 2] = __float_as_uint(__uint_as_float(v[4 * k + 2]) * fast_exp2(f.z));
-                v[4 * k + 3] = __float_as_uint(__uint_as_float(v[4 * k + 3]) * fast_exp2(f.w));
+                v[4 * k] = __float_as_uint(__uint_as_float(v[4 * k]) * f.x);
+                v[4 * k + 1] = __float_as_uint(__uint_as_float(v[4 * k + 1]) * f.y);
+                v[4 * k + 2] = __float_as_uint(__uint_as_float(v[4 * k + 2]) * f.z);
+                v[4 * k + 3] = __float_as_uint(__uint_as_float(v[4 * k + 3]) * f.w);
               }
               tmem_st32(tmem + lane_off + col, v);
             }
@@ -1269,8 +1271,8 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
           }
           const float4 by = of_rows(shift);
           nm4 = of_rows(row_nm);
-          const uint64_t b01 = f32x2(fast_exp2(by.x), fast_exp2(by.y));
-          const uint64_t b23 = f32x2(fast_exp2(by.z), fast_exp2(by.w));
+          const float4 f4 = of_rows(factor);
+          const uint64_t b01 = f32x2(f4.x, f4.y), b23 = f32x2(f4.z, f4.w);
           l01 = mul2(l01, b01);
           l23 = mul2(l23, b23);
           w01 = mul2(w01, b01);
