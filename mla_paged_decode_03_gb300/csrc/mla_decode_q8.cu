@@ -1242,7 +1242,7 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
             float by = 0.f;
             if (m != -INFINITY && (first || m > kMove)) by = kPlace - m;
             shift[st] = by;
-            factor[st] = fast_exp2(by);
+            factor[st] = first ? 1.f : fast_exp2(by);   // (a first reference may lie far down: 0 * inf)
             row_nm[st] += by;
           }
           soft_sync<kN>();

@@ -653,6 +653,30 @@ def test_decode_zero_blocks_and_growing_scores(kernel):
         check_request(0, q, out, lse, G, table, (v, s), 2, 1, 0, 1, True, True)
 
 
+@pytest.mark.parametrize("turn", [None, 140, 256])
+def test_decode_scores_far_below_zero(kernel, turn):
+    """Every key's score is about -150 (natural units; 2^-216 of a score of 0), or those of the keys
+    before `turn`: a row's weights are relative to its own largest score."""
+    q, G, table, pools = make_case(2, 48, 1, [300, 700], 64, 1, 1, 59)
+    g = torch.Generator().manual_seed(59)
+    base = torch.randn(576, generator=g).double().numpy()
+    q = (torch.tensor(base) + 0.05 * torch.randn(q.shape, generator=g)).to(torch.bfloat16)
+    away = -150.0 / SCALE / float(base @ base) * base
+    v, s = pools[0]
+    for b in range(2):
+        for l in range(int(G[b])):
+            x = 0.3 * torch.randn(576, generator=g).double().numpy() + (away if turn is None or l < turn else 0.0)
+            pg, sl = table[b, l // 64], l % 64
+            s[pg, sl // 16] = 0.125                          # (|x| is below 448 / 8)
+            v[pg, sl] = Q.ref_e4m3(x / 0.125)
+    cache, scales = gpu_pool((v, s))
+    for ws in (None, torch.empty(0, dtype=torch.uint8, device=DEV)):
+        out, lse = M.mla_decode_q8(q.to(DEV), cache, scales, bt32(table), i32(G), None, 1, 1, 0, SCALE, workspace=ws)
+        assert M.device_status() == 0
+        for b in range(2):
+            check_request(b, q, out, lse, G, table, (v, s), 1, 1, 0, 1, True, True)
+
+
 def test_decode_queries_of_any_size(kernel):
     # rows of q from 1e-30 to 1, one of zeros
     q, G, table, pools = make_case(2, 64, 1, [333, 64], 64, 1, 1, 45)
