@@ -1221,12 +1221,10 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) mx = fmax3(fmax3(mx, y[i][0], y[i][1]), y[i][2], y[i][3]);
         const bool first = t == it.t_begin;
-        if (soft_or<kN>(first || mx > kTop)) {
-          // ---- set or move the references: O must not be written to meanwhile ----------------
-          if (!first) {
-            wait<kN>(s, B_PE + (n - 1) % C::kPBufs, ((n - 1) / C::kPBufs) & 1, p);
-            tc_fence_after();
-          }
+        const bool move = soft_or<kN>(first || mx > kTop);
+        if (move) {
+          // ---- set or move the references ---------------------------------------------------
+          wait<kN>(s, B_PE + pb, ((n / C::kPBufs) + 1) & 1, p);          // this P^T (xm) is free
           float* xm = reinterpret_cast<float*>(s.ptr + C::kOffP + pb * 2 * C::kPHalf);   // [4][kN]
           {
             float4 m;
@@ -1246,29 +1244,6 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
             row_nm[st] += by;
           }
           soft_sync<kN>();
-          if (!first) {
-            // O^T, columns = rows: 64 of its columns for each group of 16 rows' warps
-#pragma unroll 1
-            for (int c32 = 0; c32 < 2; ++c32) {
-              const uint32_t col = (uint32_t)(part * 64 + c32 * 32);
-              if (!__any_sync(0xffffffffu, shift[col % kN + lane] != 0.f)) continue;
-              uint32_t v[32];
-              tmem_ld32(tmem + lane_off + col, v);
-              tmem_wait_ld();
-              const float4* by = reinterpret_cast<const float4*>(factor + col % kN);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float4 f = by[k];
-                v[4 * k] = __float_as_uint(__uint_as_float(v[4 * k]) * f.x);
-                v[4 * k + 1] = __float_as_uint(__uint_as_float(v[4 * k + 1]) * f.y);
-                v[4 * k + 2] = __float_as_uint(__uint_as_float(v[4 * k + 2]) * f.z);
-                v[4 * k + 3] = __float_as_uint(__uint_as_float(v[4 * k + 3]) * f.w);
-              }
-              tmem_st32(tmem + lane_off + col, v);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-          }
           const float4 by = of_rows(shift);
           nm4 = of_rows(row_nm);
           const float4 f4 = of_rows(factor);
@@ -1309,7 +1284,7 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
           w01 = add2(w01, s01);
           w23 = add2(w23, s23);
         }
-        wait<kN>(s, B_PE + pb, ((n / C::kPBufs) + 1) & 1, p);
+        if (!move) wait<kN>(s, B_PE + pb, ((n / C::kPBufs) + 1) & 1, p);
         {
           // lane l gives the address of key 32 kq + l's 16 bytes rg
           const uint32_t dst = s.base + C::kOffP + pb * 2 * C::kPHalf + key * kN +
@@ -1349,6 +1324,32 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
               row[8 * k] = v;
             }
           }
+        }
+        if (move && !first) {
+          // ---- O^T (columns are rows; 64 of them a warp) moves with the references: nothing may
+          // write to it meanwhile, so after the PV before, which has run since S was read --------
+          wait<kN>(s, B_PE + (n - 1) % C::kPBufs, ((n - 1) / C::kPBufs) & 1, p);
+          tc_fence_after();
+#pragma unroll 1
+          for (int c32 = 0; c32 < 2; ++c32) {
+            const uint32_t col = (uint32_t)(part * 64 + c32 * 32);
+            if (!__any_sync(0xffffffffu, shift[col % kN + lane] != 0.f)) continue;
+            uint32_t v[32];
+            tmem_ld32(tmem + lane_off + col, v);
+            tmem_wait_ld();
+            const float4* by = reinterpret_cast<const float4*>(factor + col % kN);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float4 f = by[k];
+              v[4 * k] = __float_as_uint(__uint_as_float(v[4 * k]) * f.x);
+              v[4 * k + 1] = __float_as_uint(__uint_as_float(v[4 * k + 1]) * f.y);
+              v[4 * k + 2] = __float_as_uint(__uint_as_float(v[4 * k + 2]) * f.z);
+              v[4 * k + 3] = __float_as_uint(__uint_as_float(v[4 * k + 3]) * f.w);
+            }
+            tmem_st32(tmem + lane_off + col, v);
+          }
+          tmem_wait_st();
+          tc_fence_before();
         }
         fence_proxy_async_smem();
         __syncwarp();
