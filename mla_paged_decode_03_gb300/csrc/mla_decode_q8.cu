@@ -38,12 +38,12 @@
 // segments on and looks the tiles' scales up, the others take 32 keys and 16 rows each: they
 // read S, scale, mask, exponentiate and write P^T; they also prepare Q and write the output.
 //
-// Bounds: few rows by the cache's bytes (64 x 16 rows of 1k..16k keys: 65.7 us, 47.7 at the
+// Bounds: few rows by the cache's bytes (64 x 16 rows of 1k..16k keys: 64.7 us, 47.7 at the
 // copy rate); 64 rows by shared-memory bandwidth: a tile's QK reads 16 x 4 + 2 x (4 + 4) KB and its
 // PV 32 x (4 + 2) KB, TMA writes 72 KB and the softmax 16 KB, 2,880 cycles at 128 bytes a cycle of
-// the 3,100 that it takes, against 2,176 of tensor time.  64 x 128 rows of 32,768 keys: 376 us
-// (418 held for a second, at the power limit), 1.55 PFLOP/s, twice that as issued; 4 x 256
-// rows of 256k..512k: 641 us; 32 x 512 rows of 1k..16k: 225 us.
+// the 3,100 that it takes, against 2,176 of tensor time.  64 x 128 rows of 32,768 keys: 370 us
+// (415 held for a second, at the power limit), 1.58 PFLOP/s, twice that as issued; 4 x 256 rows
+// of 256k..512k with outliers: 550 us; 32 x 512 rows of 1k..16k: 222 us.
 //
 // Work split, partials and the combine: as in mla_decode_tc.cu (tiles of all requests on one
 // line, equal ranges, units cut between blocks merged by a second kernel); a block has at most
