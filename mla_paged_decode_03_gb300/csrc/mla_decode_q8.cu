@@ -544,18 +544,21 @@ __device__ __forceinline__ bool take_segment(const Ctx& s, uint32_t i, const Par
   return ok && seg.b >= 0;
 }
 
-// A warp's part of a segment's output: 32 dims (of chunk col / kN) and twice 32 rows of O^T, which
-// go through 2 KB of shared memory (its share of P^T, which no product reads then) to become rows
-// of 64 bytes.  The unit's output (bf16) is O / l.  A partial is O / w, w the sum of the weights
-// (scales included): a mean of e4m3 values, at most 448, so that half precision holds it to 2^-11
-// in half the bytes of fp32; w / l goes with the row's LSE.  (A function of its own, so that its
-// registers do not weigh on the loop over the tiles.)
+// Four warps' part of a segment's output: the 128 dims of chunk col / kN (32 a warp) and twice 32
+// rows of O^T, which go through 8 KB of shared memory (their share of P^T, which no product reads
+// then) to become rows of 256 bytes (64 bytes, a warp by itself: 228 x 768 rows of 66 keys 164.6 us
+// instead of 162.4).
+// The unit's output (bf16) is O / l.  A partial is O / w, w the sum of the weights (scales
+// included): a mean of e4m3 values, at most 448, so that half precision holds it to 2^-11 in half
+// the bytes of fp32; w / l goes with the row's LSE.  (A function of its own, so that its registers
+// do not weigh on the loop over the tiles.)
 template <int kN>
-__device__ __noinline__ void store_rows(uint32_t tmem, uint8_t* stage, const float* inv, uint16_t* dst, int part,
-                                        int nrow, bool single) {
+__device__ __noinline__ void store_rows(uint32_t tmem, uint8_t* stage, const float* inv, uint16_t* dst, int quad,
+                                        int part, int nrow, bool single) {
   using C = Cfg<kN>;
   static_assert(C::kPBufs * 2 * C::kPHalf >= 2048 * C::kSoftWarps, "2 KB a warp");
   const int lane = threadIdx.x & 31, c4 = lane & 3;
+  auto sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(2 + part) : "memory"); };
 #pragma unroll 1
   for (int c32 = 0; c32 < 2; ++c32) {
     const int col = part * 64 + c32 * 32, r0 = col % kN;
@@ -563,6 +566,7 @@ __device__ __noinline__ void store_rows(uint32_t tmem, uint8_t* stage, const flo
     tmem_load_16x32(tmem + (uint32_t)col, v[0]);
     tmem_load_16x32(tmem + (16u << 16) + (uint32_t)col, v[1]);
     tmem_wait_ld();
+    if (c32) sync();                       // the rows before have been read
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 f = *reinterpret_cast<const float2*>(inv + r0 + 8 * i + 2 * c4);
@@ -574,18 +578,17 @@ __device__ __noinline__ void store_rows(uint32_t tmem, uint8_t* stage, const flo
         const __nv_bfloat162 o2 = __floats2bfloat162_rn(a, b);
         u[k] = single ? *reinterpret_cast<const uint32_t*>(&o2) : half2_of(a, b);
       }
-      // lane l gives the address of row l % 8 of the eight, dims 8 (l / 8) ..
+      // lane l gives the address of row l % 8 of the eight, dims 32 quad + 8 (l / 8) ..
       const int r = 8 * i + (lane & 7);
-      stmatrix_t16_x4(smem_u32(stage) + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4), u);
+      stmatrix_t16_x4(smem_u32(stage) + r * 256 + ((4 * quad + (lane >> 3)) ^ (lane & 7)) * 16, u);
     }
-    __syncwarp();
+    sync();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int r = 8 * i + (lane >> 2);
-      const uint4 o = *reinterpret_cast<const uint4*>(stage + r * 64 + ((c4 ^ ((r >> 1) & 3)) << 4));
-      if (r0 + r < nrow) *reinterpret_cast<uint4*>(dst + (r0 + r) * kDv + col / kN * 128) = o;
+      const int r = 8 * quad + 2 * i + (lane >> 4), unit = lane & 15;
+      const uint4 o = *reinterpret_cast<const uint4*>(stage + r * 256 + (unit ^ (r & 7)) * 16);
+      if (r0 + r < nrow) *reinterpret_cast<uint4*>(dst + (r0 + r) * kDv + col / kN * 128 + unit * 8) = o;
     }
-    __syncwarp();
   }
 }
 
@@ -1147,8 +1150,8 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
           }
           soft_sync<kN>();
           const int nrow = min(kN, p.rows - out_row0);
-          uint16_t* dst = (out_single ? p.out + out_row * kDv : p.ws_o + out_slot * kN * kDv) + quad * 32 + c4 * 8;
-          store_rows<kN>(tmem + lane_off, s.ptr + C::kOffP + (warp - 4) * 2048, shift, dst, part, nrow, out_single);
+          uint16_t* dst = out_single ? p.out + out_row * kDv : p.ws_o + out_slot * kN * kDv;
+          store_rows<kN>(tmem + lane_off, s.ptr + C::kOffP + part * 8192, shift, dst, quad, part, nrow, out_single);
           tc_fence_before();
         }
       }
