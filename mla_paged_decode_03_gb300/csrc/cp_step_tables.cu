@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kThreads) cp_step_tables_kernel(const Params p
   // ---- phase 1: the prefix sums, up to this block's requests (block 0: over all, for the
   // ring's new state).  In most steps of a decode loop no request of a round of 256 takes or gives
   // a page, and the sums are skipped. ---------------------------------------------------------
-  unsigned long long asked = 0, moved = 0;           // before this round: pages asked for; given, taken
+  unsigned long long asked = 0, moved = 0;           // by the requests before these 256: asked for; given, taken
   const int upto = blockIdx.x == 0 ? p.B : last;
   for (int base = 0; base < upto; base += kThreads) {
     const int b = base + tid;
