@@ -128,8 +128,10 @@ __global__ void __launch_bounds__(kThreads, 8) cp_store_q8_kernel(const Params p
   }
   if (fresh <= 0) return;
   const int l0 = local_len(p, ctx), l1 = local_len(p, ctx + (int)fresh);
-  const int g0 = (l0 / kGroup + gi) * kGroup;            // the group's first local key
-  if (l1 <= l0 || g0 >= l1) return;
+  // (compared as groups: past the last one the first key may lie beyond 2^31)
+  const int group = l0 / kGroup + gi;
+  if (l1 <= l0 || group > (l1 - 1) / kGroup) return;
+  const int g0 = group * kGroup;                         // the group's first local key
   const int vb = g0 / p.block_size;
   if (vb >= p.max_blocks) {
     if (tid == 0) atomicOr(p.status, MLA_STATUS_BAD_VBLOCK);

@@ -380,6 +380,30 @@ def test_store_bad_data_writes_nothing():
     assert not call([5, 7, 3], [5, 6, 0], [[0], [1], [2]], 0).any()   # nothing new
 
 
+@pytest.mark.parametrize("N", [1, 3, 16, 100, 8200])
+@pytest.mark.parametrize("total", [(1 << 31) - 1, (1 << 31) - 20])
+def test_store_lengths_up_to_the_largest(N, total):
+    """New tokens up to position 2^31 - 2.  A block behind a request's last group may have a group
+    whose first key is 2^31 (3, 100 or 8,200 tokens up to the very end).  The table does not reach
+    that far: flagged, nothing written."""
+    ctx = total - N
+    cache, scales = new_pool(4, 16)
+    before = cache.view(torch.uint8).clone(), scales.view(torch.int32).clone()
+    rows = torch.ones(2, N, 576, dtype=torch.bfloat16, device=DEV)
+    M.cp_store_q8(rows, i32([ctx, 0]), i32([total, 0]), i32([[0, 1, 2, 3], [3, 2, 1, 0]]), cache, scales)
+    assert M.device_status() == BAD_VBLOCK
+    assert torch.equal(cache.view(torch.uint8), before[0]) and torch.equal(scales.view(torch.int32), before[1])
+    # one of 2^26 ranks, whose tables do reach there
+    cp = 1 << 26
+    cache, scales = new_pool(4, 16, poison=False)
+    M.cp_store_q8(rows[:1, :1].contiguous(), i32([ctx]), i32([ctx + 1]), i32([[0, 1, 2, 3]]), cache, scales,
+                  cp, ctx // 16 % cp, interleave=16)
+    assert M.device_status() == 0
+    local = ctx // (cp * 16) * 16 + ctx % 16
+    got = cache.view(4 * 16, 576)[local].float() * scales.view(-1)[local // 16]
+    assert torch.equal(got, torch.ones_like(got))
+
+
 def test_store_offsets_beyond_31_bits():
     """A pool of more than 2^31 bytes: pages behind byte 2^31 and 2^32."""
     bs = 64
