@@ -25,10 +25,20 @@
 //     is at most 8 units of q's last place; exact for elements within 2^-9 of the maximum,
 //     off by at most 2^-10 (2^-17 of the maximum) below.  hi and lo are columns of one
 //     product with N = 2 kN (the keys are read once), added when S is read.
-//   * a weight p = S_l 2^(t'_l - m) is an e5m2 value (3 bits, range to 2^-16) plus its residue
-//     in e4m3: off by at most 2^-7 p or 2^-10; two products into the same accumulator.
-// p stays within 2^12 (the residue within e4m3's 448): m is set 2^5 below a tile's largest
-// S_l 2^t'_l and moved only when a tile exceeds 2^12 (then O, l and m move together).
+//   * a weight p = S_l 2^(t'_l - m) is an e5m2 value (3 bits, range to 2^-16) plus its residue,
+//     two products into the same accumulator.  The residue is an e4m3 value: p is off by at
+//     most 2^-8 p, or 2^-10 below 2^-2.  Where some row's largest p of 16 keys is below 2^-3 (and
+//     not below 2^-22), the residues of a tile are e5m2 values for all the unit's rows: off by
+//     at most 2^-7 p, or 2^-17 below 2^-10.  Both have a dither of up to half the type's smallest
+//     step, spread evenly over the keys, so that the sum of many small weights comes out right:
+//     thousands of equal ones far below one large one may be most of the output (with e4m3 alone
+//     and without dithers, 16,384 of e^-8 of the largest lost 5 % of the output, of e^-15 40 %).
+// An e4m3 residue (at most 448) serves p up to 2^12.  m is set 2^6 below a tile's largest S_l 2^t'_l
+// and moved (then O, l and m move together) only when a tile exceeds 2^12.  Nearer to 2^12 small
+// weights would have more of the range, but a move costs half a tile's time (64 x 128 rows of 32k keys,
+// set 2^8 / 2^7 / 2^6 below: 389 / 383 / 380 us); at 2^12 where a segment has but one tile.  Where a tile's largest stands alone (as first tokens
+// do, with nearly all the weight and little value), the rest counts: that is set to 2^3 or more as far
+// as 2^12 for the largest allows.
 //
 // Roles (20 warps, 12 for 32 rows): warp 0 loads tiles (TMA, four 16 KB chunks of latent dims
 // and one of rope dims each, chunk by chunk as PV frees them), warp 1 issues the QK products and
@@ -81,9 +91,13 @@ constexpr int kTile = 128;                 // keys per tile
 constexpr int kChunkBytes = kTile * 128;   // 128 keys x 128 dims
 constexpr int kRopeBytes = kTile * 64;
 constexpr int kR = 16;                     // query rows per softmax warp
-// log2 of the largest weight a tile may have, of where a new reference puts a tile's largest,
-// and of the excess that moves a reference when some row's weights pass the first
-constexpr float kTop = 12.f, kPlace = 5.f, kMove = 7.f;
+// log2 of the largest weight that a reference may stay with, of where a new reference puts a tile's
+// largest, and of the excess that moves a row's when some row's weights pass the first
+constexpr float kTop = 12.f, kPlace = 6.f, kMove = 9.f;
+// A largest weight that stands alone in its tile is put higher, so that the rest is at 2^kRest, up to kTop
+constexpr float kRest = 3.f;
+// A tile has fine weights where some row's largest of 16 keys is between 2^kNone and 2^kFine (see above)
+constexpr float kNone = -22.f, kFine = -3.f;
 
 // One segment of a block: tiles [t_begin, t_end) of a request's unit (b < 0: no more).
 struct __align__(16) Seg {
@@ -91,6 +105,9 @@ struct __align__(16) Seg {
   int cap, g, rank, single;       // the request's lengths; 1: the segment is the whole unit
 };
 constexpr int kSegRing = 4;
+// Tiles whose mark of fine weights is kept.  That of tile n is read before its PV is over; the softmax
+// warps wait for that PV in tile n + 2, before they come to tile n + 4's mark.
+constexpr int kFineRing = 4;
 
 template <int kN>
 struct Cfg {
@@ -112,7 +129,8 @@ struct Cfg {
   static constexpr int kOffMisc = kOffRow + 20 * kN;       // tmem base, abort, scan result
   static constexpr int kOffSeg = kOffMisc + 48;            // Seg[kSegRing]
   static constexpr int kOffScale = kOffSeg + 32 * kSegRing;   // float4 [kSBufs tiles][8 groups of 16 keys]
-  static constexpr int kSmem = kOffScale + 128 * kSBufs + 1008;   // + alignment slack
+  static constexpr int kOffFine = kOffScale + 128 * kSBufs;   // int [kFineRing]
+  static constexpr int kSmem = kOffFine + 4 * kFineRing + 1008;   // + alignment slack
   // tensor memory: O^T, then S, then Q
   static constexpr uint32_t kColS = 4 * kN, kColQ = kColS + 128;
   static constexpr uint32_t kTmemCols = 8 * kN;
@@ -136,6 +154,9 @@ enum Bar : int {
   B_GE = 42,       // [4] and read by every role (three warps and the softmax warps)
   B_COUNT = 46
 };
+
+// 2^32 / the golden ratio: the upper bytes of its multiples are spread evenly over any run of keys
+constexpr uint32_t kTurn = 0x9E3779B1u;
 
 struct Params {
   const uint16_t* q;
@@ -289,6 +310,44 @@ __device__ __forceinline__ uint32_t sub_half2(uint32_t a, uint32_t b) {
   const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// Cut towards 0.
+__device__ __forceinline__ uint32_t half2_cut(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t add_half2(uint32_t a, uint32_t b) {
+  const __half2 h = __hadd2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// 2^-16 (x 2^-32 - 1/2), by way of a float 1 + x 2^-32; its last bit set, so that half a step, 2^-17,
+// is not reached on either side (a weight of 0 stays 0)
+__device__ __forceinline__ float dither_of(uint32_t x) {
+  return fmaf(__uint_as_float((x >> 9) | 0x3f800001u), 0x1p-16f, -0x1.8p-16f);
+}
+// 2^-9 (x 2^-16 - 1/2) for two 16-bit x, of their upper bytes, by way of halves 1024 + byte.  `minus`:
+// kDown or kUp for each, which are off by half a step of a byte, 2^-18, either way.
+constexpr uint32_t kDown = 0xa080u, kUp = 0xa07fu;         // -1152 and -1151 times 2^-17
+__device__ __forceinline__ uint32_t dither2_of(uint32_t x, uint32_t minus) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(__byte_perm(x, 0x64u, 0x4341)), "r"(0x00800080u), "r"(minus));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Is a half of v between kNone and kFine?  (not so: NaN, -inf)
+__device__ __forceinline__ bool any_fine(uint32_t v) {
+  constexpr float kMid = (kFine + kNone) / 2, kHalf = (kFine - kNone) / 2;
+  return fabsf(__uint_as_float(v << 16) - kMid) < kHalf || fabsf(__uint_as_float(v & 0xffff0000u) - kMid) < kHalf;
+}
 __device__ __forceinline__ uint32_t half2_of_e4m3x2(uint32_t a) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)a));
@@ -395,16 +454,15 @@ __device__ __forceinline__ void qk_mma_t(uint32_t d, uint32_t a, uint32_t b, uin
       : "memory");
 }
 
-// One step of 32 keys: the weights' e5m2 part (bh, ih) and their e4m3 part (bl, il).
-__device__ __forceinline__ void pv_mma(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t bh, uint32_t bl,
-                                       uint32_t b_hi, uint32_t ih, uint32_t il, uint32_t acc) {
+// One product over 32 keys: values times one part of the weights.
+__device__ __forceinline__ void pv_mma(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi,
+                                       uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p, t, e;\n .reg .b64 x, y, z;\n setp.ne.b32 p, %8, 0;\n setp.ne.b32 t, %9, 0;\n"
+      "{\n .reg .pred p, e;\n .reg .b64 x, y;\n setp.ne.b32 p, %6, 0;\n"
       " elect.sync _|e, 0xffffffff;\n"
-      " mov.b64 x, {%1, %2}; mov.b64 y, {%3, %5}; mov.b64 z, {%4, %5};\n"
-      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %6, p;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, z, %7, t;\n"
-      "}" ::"r"(d), "r"(a), "r"(a_hi), "r"(bh), "r"(bl), "r"(b_hi), "r"(ih), "r"(il), "r"(acc), "r"(1u)
+      " mov.b64 x, {%1, %2}; mov.b64 y, {%3, %4};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %5, p;\n"
+      "}" ::"r"(d), "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "r"(acc)
       : "memory");
 }
 
@@ -825,11 +883,13 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
           if (!ok) break;
           tc_fence_after();
           const uint32_t pa = pa0 + pb * (2 * C::kPHalf / 16);
-          // chunk c of the values (dims 128 c ..), step k of 32 keys
-          auto product = [&](int c, int k) {
+          // (comes while the first products, which it does not concern, are issued)
+          const int fine = reinterpret_cast<const int*>(s.ptr + C::kOffFine)[n % kFineRing];
+          // chunk c of the values (dims 128 c ..), step k of 32 keys: the weights' first part, or the second
+          auto product = [&](int c, int k, bool second, uint32_t id) {
             pv_mma(tmem + c * kN, va + slot * (kChunkBytes / 16) + k * (4096 / 16), desc_hi(1024, kSwizzle128B),
-                   pa + k * (32 * kN / 16), pa + (C::kPHalf + k * 32 * kN) / 16, p_hi, id_hi, id_lo,
-                   (t == it.t_begin && k == 0) ? 0u : 1u);
+                   pa + ((second ? C::kPHalf : 0) + k * 32 * kN) / 16, p_hi, id,
+                   (t == it.t_begin && k == 0 && !second) ? 0u : 1u);
           };
           auto release = [&]() {
             mma_commit_warp(bar<kN>(s, B_KE + slot));
@@ -838,12 +898,24 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
           // the steps that hold keys, in straight code for each count: a branch between two products
           // costs more than a product (3 % of a long request, 2,500 cycles of a short one)
           auto run = [&](auto steps) {
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
+            constexpr int kSteps = decltype(steps)::value;
 #pragma unroll
-              for (int k = 0; k < decltype(steps)::value; ++k) product(c, k);
+            for (int k = 0; k < kSteps; ++k) product(0, k, false, id_hi);
+            auto rest = [&](uint32_t id) {
+#pragma unroll
+              for (int k = 0; k < kSteps; ++k) product(0, k, true, id);
               release();
-            }
+#pragma unroll 1
+              for (int c = 1; c < 4; ++c) {
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) {
+                  product(c, k, false, id_hi);
+                  product(c, k, true, id);
+                }
+                release();
+              }
+            };
+            rest(fine ? id_hi : id_lo);
           };
           const int left = it.keys - t * kTile;
           if (left > 96)
@@ -1220,28 +1292,53 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
             if (k_abs + kStep >= l4.w) y[i][3] = -INFINITY;
           }
         }
-        float mx = -INFINITY;
+        // the rows' largest of this thread's keys (by k of y[i][k])
+        float4 m4;
+        if constexpr (C::kQTmem) {
+          m4.x = m4.y = fmax3(fmax3(fmax3(y[0][0], y[0][1], y[1][0]), y[1][1], y[2][0]),
+                              fmax3(y[2][1], y[3][0], y[3][1]), -INFINITY);
+          m4.z = m4.w = fmax3(fmax3(fmax3(y[0][2], y[0][3], y[1][2]), y[1][3], y[2][2]),
+                              fmax3(y[2][3], y[3][2], y[3][3]), -INFINITY);
+        } else {
+          m4.x = fmaxf(fmax3(y[0][0], y[1][0], y[2][0]), y[3][0]);
+          m4.y = fmaxf(fmax3(y[0][1], y[1][1], y[2][1]), y[3][1]);
+          m4.z = fmaxf(fmax3(y[0][2], y[1][2], y[2][2]), y[3][2]);
+          m4.w = fmaxf(fmax3(y[0][3], y[1][3], y[2][3]), y[3][3]);
+        }
+        // does a row's largest of 16 keys, this thread's and its neighbours', ask for fine weights?
+        auto asks = [&]() {
+          if constexpr (C::kQTmem) {
+            uint32_t v = bf16x2_of(m4.x, m4.z);
+            v = max_bf16x2(v, __shfl_xor_sync(0xffffffffu, v, 1));
+            return any_fine(v);
+          } else {
+            uint32_t v = bf16x2_of(m4.x, m4.y), w = bf16x2_of(m4.z, m4.w);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mx = fmax3(fmax3(mx, y[i][0], y[i][1]), y[i][2], y[i][3]);
-        const bool first = t == it.t_begin;
-        const bool move = soft_or<kN>(first || mx > kTop);
+            for (int o = 4; o <= 8; o <<= 1) {
+              v = max_bf16x2(v, __shfl_xor_sync(0xffffffffu, v, o));
+              w = max_bf16x2(w, __shfl_xor_sync(0xffffffffu, w, o));
+            }
+            return any_fine(v) || any_fine(w);
+          }
+        };
+        // one barrier in most tiles; where that finds something, another tells whether references have to
+        // move (those tiles have fine weights in any case: to ask again would take one more)
+        const bool first = t == it.t_begin, ask = !first && asks(), over = fmaxf(fmax3(m4.x, m4.y, m4.z), m4.w) > kTop;
+        bool fine = !first && soft_or<kN>(ask || over);
+        const bool move = first || (fine && soft_or<kN>(over));
         if (move) {
           // ---- set or move the references ---------------------------------------------------
           wait<kN>(s, B_PE + pb, ((n / C::kPBufs) + 1) & 1, p);          // this P^T (xm) is free
           float* xm = reinterpret_cast<float*>(s.ptr + C::kOffP + pb * 2 * C::kPHalf);   // [4][kN]
-          {
-            float4 m;
-            m.x = fmaxf(fmax3(y[0][0], y[1][0], y[2][0]), y[3][0]);
-            m.y = fmaxf(fmax3(y[0][1], y[1][1], y[2][1]), y[3][1]);
-            m.z = fmaxf(fmax3(y[0][2], y[1][2], y[2][2]), y[3][2]);
-            m.w = fmaxf(fmax3(y[0][3], y[1][3], y[2][3]), y[3][3]);
-            over_keys(m, [](float a, float b) { return fmaxf(a, b); }, xm + kq * kN);
-          }
+          over_keys(m4, [](float a, float b) { return fmaxf(a, b); }, xm + kq * kN);
           soft_sync<kN>();
           if (st < kN) {
-            const float m = fmaxf(fmaxf(xm[st], xm[kN + st]), fmaxf(xm[2 * kN + st], xm[3 * kN + st]));
+            const float x0 = xm[st], x1 = xm[kN + st], x2 = xm[2 * kN + st], x3 = xm[3 * kN + st];
+            const float m = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)), rest = fmaxf(fminf(x0, x1), fminf(x2, x3));
+            const bool one = it.t_end - it.t_begin == 1;
             float by = 0.f;
-            if (m != -INFINITY && (first || m > kMove)) by = kPlace - m;
+            if (m != -INFINITY && (first || m > kMove))
+              by = (one ? kTop : rest == -INFINITY ? kPlace : fminf(fmaxf(kPlace, kRest + (m - rest)), kTop)) - m;
             shift[st] = by;
             factor[st] = first ? 1.f : fast_exp2(by);   // (a first reference may lie far down: 0 * inf)
             row_nm[st] += by;
@@ -1262,31 +1359,66 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
             y[i][2] += by.z;
             y[i][3] += by.w;
           }
+          if (first) {
+            m4 = make_float4(m4.x + by.x, m4.y + by.y, m4.z + by.z, m4.w + by.w);
+            fine = soft_or<kN>(asks());
+          }
         }
+        if (st == 0) reinterpret_cast<int*>(s.ptr + C::kOffFine)[n % kFineRing] = fine;
         // ---- weights, their sums, and their two 8-bit parts ------------------------------------
         // In half precision (11 bits): h = the value rounded to e5m2, that is to its upper byte;
-        // the residue is exact, and goes to e4m3.
+        // the residue is exact, and goes to e4m3 or (fine) e5m2, with a dither of up to half of that
+        // type's smallest step (0 stays 0).  The e4m3 residue's is added in half precision;
+        // the e5m2 residue's, whose step is 2^8 of half precision's last, to the weight before, which
+        // is then cut to half precision, so that this rounding does not move the sum either.
         uint32_t ph[4], pl[4];
+        auto weights = [&](auto is_fine) {
+          const uint32_t key0 = (uint32_t)(t * kTile + my_keys);
+          // 16-bit multiples of 2^16 / the golden ratio for the keys of a pair (a carry between them
+          // is one of 2^16)
+          const uint32_t pair = (key0 * (kTurn >> 16) & 0xffffu) * 0x10001u + (C::kQTmem ? kTurn & 0xffff0000u : 0u);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          uint64_t s01 = 0, s23 = 0;
+          for (int j = 0; j < 2; ++j) {
+            uint64_t s01 = 0, s23 = 0;
 #pragma unroll
-          for (int i = 2 * j; i < 2 * j + 2; ++i) {
-            const float e0 = fast_exp2(y[i][0]), e1 = fast_exp2(y[i][1]);
-            const float e2 = fast_exp2(y[i][2]), e3 = fast_exp2(y[i][3]);
-            s01 = add2(s01, f32x2(e0, e1));
-            s23 = add2(s23, f32x2(e2, e3));
-            const uint32_t u = half2_of(e0, e1), v = half2_of(e2, e3);
-            const uint32_t hu = (u + 0x00800080u) & 0xff00ff00u, hv = (v + 0x00800080u) & 0xff00ff00u;
-            ph[i] = __byte_perm(hu, hv, 0x7531);
-            pl[i] = __byte_perm(e4m3x2_of_half2(sub_half2(u, hu)), e4m3x2_of_half2(sub_half2(v, hv)), 0x5410);
+            for (int i = 2 * j; i < 2 * j + 2; ++i) {
+              float e0 = fast_exp2(y[i][0]), e1 = fast_exp2(y[i][1]);
+              float e2 = fast_exp2(y[i][2]), e3 = fast_exp2(y[i][3]);
+              s01 = add2(s01, f32x2(e0, e1));
+              s23 = add2(s23, f32x2(e2, e3));
+              if constexpr (is_fine) {
+                const float da = dither_of((key0 + 8 * i) * kTurn);
+                const float db = C::kQTmem ? dither_of((key0 + 8 * i + 1) * kTurn) : da;
+                e0 += da;
+                e1 += db;
+                e2 += da;
+                e3 += db;
+              }
+              const uint32_t u = is_fine ? half2_cut(e0, e1) : half2_of(e0, e1);
+              const uint32_t v = is_fine ? half2_cut(e2, e3) : half2_of(e2, e3);
+              const uint32_t hu = (u + 0x00800080u) & 0xff00ff00u, hv = (v + 0x00800080u) & 0xff00ff00u;
+              const uint32_t ru = sub_half2(u, hu), rv = sub_half2(v, hv);
+              ph[i] = __byte_perm(hu, hv, 0x7531);
+              if constexpr (is_fine) {
+                // (a residue of minus half a step, from a weight of half a step, stays: + 0x7f)
+                pl[i] = __byte_perm(ru + 0x007f007fu, rv + 0x007f007fu, 0x7531);
+              } else {
+                const uint32_t d = dither2_of(pair + i * (8 * (kTurn >> 16) & 0xffffu) * 0x10001u,
+                                              C::kQTmem ? kDown | kUp << 16 : (i & 1 ? kUp : kDown) * 0x10001u);
+                pl[i] = __byte_perm(e4m3x2_of_half2(add_half2(ru, d)), e4m3x2_of_half2(add_half2(rv, d)), 0x5410);
+              }
+            }
+            const uint64_t ij = f32x2(inv_g[j], inv_g[j]);
+            l01 = fma2(s01, ij, l01);
+            l23 = fma2(s23, ij, l23);
+            w01 = add2(w01, s01);
+            w23 = add2(w23, s23);
           }
-          const uint64_t ij = f32x2(inv_g[j], inv_g[j]);
-          l01 = fma2(s01, ij, l01);
-          l23 = fma2(s23, ij, l23);
-          w01 = add2(w01, s01);
-          w23 = add2(w23, s23);
-        }
+        };
+        if (fine)
+          weights(std::true_type{});
+        else
+          weights(std::false_type{});
         if (!move) wait<kN>(s, B_PE + pb, ((n / C::kPBufs) + 1) & 1, p);
         {
           // lane l gives the address of key 32 kq + l's 16 bytes rg

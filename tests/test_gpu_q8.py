@@ -646,6 +646,116 @@ def test_decode_without_workspace_and_without_lse(B, H, q_len, G, units):
     assert l2 is None and torch.equal(out, o2) and M.device_status() == 0
 
 
+@pytest.mark.parametrize("n", [16384, 131072, 524288])
+@pytest.mark.parametrize("where,big,raised", [(0, 1, 0), (0, 32, 0), (5000, 1, 0), (5000, 32, 0), (0, 1, 192),
+                                              (5000, 32, 192), (0, 1, 384)])
+def test_decode_many_small_weights_below_one_large(n, where, big, raised, kernel):
+    """One key of value 0 above n - 1 equal ones, whose weights are e^-5 to e^-15 of its (336 rows,
+    0.03 apart), in one block's hands (no workspace); the large key's 16 slots have the others'
+    scale or 32 times that.  With `raised` every 32nd key is e^3.5 or e^6.9 above the others and of
+    value 0.  Every rounding of the small weights is the same or follows the key's number, so
+    nothing averages out that the kernel does not make average out.
+
+    Bound, A = sum_l w_l S_l |v_l| = |ref| here, M the large key's weight times scale, Z all other
+    weights' sum: the output 2^-8; a weight 2^-7 of itself; what the dithers leave of a sum of equal
+    weights: a few steps (8) of 2^-16 against a reference of 2^6 or more: 2^-19 M, or, where 16 keys'
+    largest is 2^-3 or more, 8 of 2^-9 over n / 32 such (2^-6 / (512 2^-3) = 2^-12 Z); the 31 keys
+    beside the large one 2^-3 of themselves: 2^-3 31 / 16,384 < 2^-11; scores: below 2^-12.
+    2^-8 + 2^-7 + 2^-11 + 2^-12 < 2^-6 of A, 2^-19 M, and with raised keys 2^-12 Z."""
+    if kernel == "mma" and n > 16384:
+        pytest.skip("the warp-level kernel rounds to bf16; one length is enough")
+    rows, bs = 336, 64
+    gap = torch.linspace(5.0, 15.0, rows)
+    q = torch.zeros(1, 3, rows // 3, 576)
+    q.view(rows, 576)[:, 575] = gap / (4 * SCALE)
+    q[..., 574] = 16.0
+    q = q.to(torch.bfloat16)
+    c = (torch.arange(512) % 13 + 1) * 4.0 * (1 - 2 * (torch.arange(512) % 2))
+    keys = torch.zeros(n, 576)
+    keys[:, :512] = c
+    high = n // 32 if raised else 0
+    if raised:
+        keys[16::32] = 0
+        keys[16::32, 574] = raised
+    keys[where // 16 * 16:where // 16 * 16 + 16] /= big
+    keys[where] = 0
+    keys[where, 575] = 256 / big
+    cache = keys.to(torch.float8_e4m3fn).to(DEV).view(n // bs, bs, 576)
+    assert torch.equal(cache.view(n, 576).float().cpu(), keys)
+    scales = torch.full((n // bs, bs // 16), 2.0 ** -6, device=DEV)
+    scales.view(-1)[where // 16] *= big
+    table = bt32(np.arange(n // bs)[None])
+    out, lse = M.mla_decode_q8(q.to(DEV), cache, scales, table, i32([n]), None, 3, 1, 0, SCALE, causal=False,
+                               workspace=torch.empty(0, dtype=torch.uint8, device=DEV))
+    assert M.device_status() == 0
+    s = SCALE * 4 * n64(q).reshape(rows, 576)[:, 575]
+    low_w, high_w = (n - 1 - high) * np.exp(-s), high * np.exp(SCALE * 16 * raised / 64 - s)
+    z = 1 + low_w + high_w
+    ref = (low_w / z)[:, None] * c.double().numpy()[None] / 64
+    cmax = float(c.abs().max())
+    bound = 2.0 ** -6 * np.abs(ref) + (2.0 ** -19 * big / z)[:, None] * cmax / 64
+    if raised:
+        bound += 2.0 ** -12 * ((low_w + high_w) / z)[:, None] * cmax / 64
+    err = np.abs(n64(out).reshape(rows, 512) - ref)
+    print(f"[q8] {kernel} n {n} at {where} x{big} raised {raised}: {float((err / np.abs(ref)).max()):.5f} of the output, "
+          f"bound used {float((err / bound).max()):.3f}")
+    assert (err <= bound).all()
+    # the LSE's sum: a thread adds twice a tile of 128 keys to a float that grows to its share of the
+    # sum (2 n / 128 roundings of at most 2^-24 of it), and fewer than 16 more join the shares (the
+    # warp-level kernel: 4 a tile of 32); scores up to 15 / ln 2 and reference as in this file's header
+    # (8 u (22 + 64 + 6) < 5e-5), 1e-6 (1 + |lse|) of the logarithm and the result's rounding
+    adds = (n / 8 if kernel == "mma" else n / 64) + 16
+    assert np.abs(n64(lse).reshape(rows) - (s + np.log(z))).max() <= adds * 2.0 ** -24 + 5e-5 + 2e-5
+
+
+@pytest.mark.parametrize("gap,big", [(6.0, 1), (12.0, 1), (12.0, 16), (16.0, 1)])
+def test_decode_values_beside_one_large_weight(gap, big, kernel):
+    """A key of value 0 takes nearly all the weight (as first tokens do); the output is what the
+    others make of the rest.  Their weights are used to within 2^-7 of themselves, however small
+    against the large one: bound as in this file's header, but the term in M is two halves of a step
+    of 2^-16 against a reference of 2^6, 2^-21 M; 12 units and more (2^17, and 2^13 above the others'
+    largest) of 2^11 or more: 2^-26 M.  The norm of the error is at most 2^-7 of the output's, and the
+    dithers' own: each is a step of 2^-16 or nothing, off by at most half a step in the mean square
+    (p (1 - p) <= 1 / 4): 2^-17 against the reference, (sum_l |v_l|^2)^1/2 M, twice that for their
+    dependence on one another."""
+    n, rows, bs = 4096, 128, 64
+    g = torch.Generator().manual_seed(int(gap) + big)
+    q = torch.randn(1, 1, rows, 576, generator=g)
+    q[..., 575] = 32.0
+    q = q.to(torch.bfloat16)
+    x = torch.randn(n, 576, generator=g).numpy().astype(np.float64) * 0.6
+    x[:, 575] = 0
+    at = 700
+    x[at] = 0
+    x[at, 575] = gap / (32 * SCALE)
+    sc = np.array([Q.ref_scale(float(np.abs(t).max())) for t in x.reshape(-1, 16 * 576)])
+    sc[at // 16] *= big
+    v = Q.ref_e4m3(x / np.repeat(sc, 16)[:, None])
+    cache, scales = gpu_pool((v.reshape(n // bs, bs, 576), sc.reshape(n // bs, bs // 16)))
+    out, lse = M.mla_decode_q8(q.to(DEV), cache, scales, bt32(np.arange(n // bs)[None]), i32([n]), None, 1, 1, 0, SCALE,
+                               workspace=torch.empty(0, dtype=torch.uint8, device=DEV))
+    assert M.device_status() == 0
+    k = v * np.repeat(sc, 16)[:, None]
+    s = SCALE * (n64(q)[0, 0] @ k.T)
+    w = np.exp(s - s.max(1, keepdims=True))
+    w /= w.sum(1, keepdims=True)
+    ref, A = w @ k[:, :512], w @ np.abs(k[:, :512])
+    Mx = (w * np.repeat(sc, 16)).max(1, keepdims=True)
+    u = 2.0 ** -24
+    delta = SCALE * (2.0 ** -17 * 32 * np.abs(k).sum(1)[None] + 132 * u * (np.abs(n64(q)[0, 0]) @ np.abs(k).T))
+    delta = (delta + 8 * u * (np.abs(s) + 64) + 2.0 ** -22).max(1)[:, None]
+    o = n64(out)[0]
+    ref_at = 2.0 ** (6 if gap < 12 else 11)
+    bound = (2.0 ** -8 * np.abs(ref) + (2.0 ** -7 + 2.0 ** -10 + 2 * np.expm1(2 * delta)) * A
+             + 2.0 ** -15 / ref_at * Mx * np.abs(v[:, :512]).sum(0)[None])
+    noise = 2.0 ** -16 / ref_at * float(np.linalg.norm(Mx)) * math.sqrt(float((v[:, :512] ** 2).sum()))
+    off, size = float(np.linalg.norm(o - ref)), float(np.linalg.norm(ref))
+    print(f"[q8] {kernel} gap {gap} x{big}: error {off / size:.5f} of the output (dithers {noise / size:.5f}), bound used "
+          f"{float((np.abs(o - ref) / bound).max()):.3f}")
+    assert (np.abs(o - ref) <= bound).all()
+    assert off <= 2.0 ** -7 * size + noise
+
+
 def test_decode_any_scales(kernel):
     # scales that are no powers of two, from 2^-32 to 2^64
     q, G, table, pools = make_case(2, 16, 2, [200, 75], 32, 1, 1, 43, spread=3, pow2=False)
