@@ -767,6 +767,37 @@ def test_decode_any_scales(kernel):
         check_request(b, q, out, lse, G, table, pool, 2, 1, 0, 1, True, True)
 
 
+@pytest.mark.parametrize("ends", ["large", "small", "both", "large, no power of two"])
+@pytest.mark.parametrize("split", [True, False])
+def test_decode_scales_at_the_ends_of_their_range(ends, split, kernel):
+    """Scales of 2^64 and of 2^-32 over values that are not 0, queries of a size that gives ordinary
+    scores; and both ends and 1 in turn in one request, the keys of 2^64 with weights about 2^-64 of
+    the others', so that they matter as much in the output and nothing in the LSE."""
+    q, G, table, pools = make_case(2, 40, 2, [300, 1203], 32, 1, 1, 47, pow2=ends != "large, no power of two")
+    v, s = pools[0]
+    if ends == "both":
+        s[:] = np.array([2.0 ** 64, 1.0, 2.0 ** -32])[np.arange(s.size) % 3].reshape(s.shape)
+        v[..., 512:] = 0
+        rope = np.random.default_rng(5).choice([-36.0, -40.0, -44.0], v.shape[:2] + (64,))
+        v[..., 575] = rope[..., 0]                                     # scores of -42, -46, -51 at 2^64
+        q = torch.zeros_like(q)
+        q[..., 575] = 2.0 ** -60
+    else:
+        top = float(np.nanmax(s))
+        # (over powers of two: as they are, and up to 2^64 exactly)
+        s *= (2.0 ** 64 if ends.startswith("large") else 2.0 ** -32) / (top if ends != "small" else float(np.nanmin(s)))
+        s = np.float32(s).astype(np.float64)
+        x = float(np.nanmedian(s)) * 150                               # about a key's size
+        q = (q.double() / (SCALE * x * 24)).to(torch.bfloat16)
+        assert np.nanmax(s) <= 2.0 ** 64 and np.nanmin(s) >= 2.0 ** -32
+    cache, scales = gpu_pool((v, s))
+    ws = None if split else torch.empty(0, dtype=torch.uint8, device=DEV)
+    out, lse = M.mla_decode_q8(q.to(DEV), cache, scales, bt32(table), i32(G), None, 2, 1, 0, SCALE, workspace=ws)
+    assert M.device_status() == 0
+    for b in range(2):
+        check_request(b, q, out, lse, G, table, (v, s), 2, 1, 0, 1, True, True)
+
+
 def test_decode_zero_blocks_and_growing_scores(kernel):
     """Blocks of zeros (smallest scale) among ordinary ones, and scores that grow along the
     context by far more than a weight's 8-bit range."""
