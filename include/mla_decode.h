@@ -337,8 +337,10 @@ int cp_store_q8(const void* kv_new, const int32_t* ctx_lens, const int32_t* tota
  *   q            a row (one head of one token) with a NaN or an infinity gives NaN outputs.
  *   scale        scale * s * |q| must stay below 2^127 for every scale s and element of q in
  *                use (scores beyond float's range give NaN, 0 or -inf as floats do).
- *   ceil(q_len*H/64) <= SMs; num_blocks*block_size and max_blocks*block_size below
- *   2^31 - 65536 (else MLA_ERR_UNSUPPORTED).
+ *   Limits (else MLA_ERR_UNSUPPORTED, and mla_last_error() names the one that was passed), with R the
+ *   requests of all shards: ceil(q_len*H/64) <= SMs; num_blocks*block_size and
+ *   max_blocks*block_size below 2^31 - 65536; R * (max_blocks*block_size/128 + 7) below 2^31 (a
+ *   table of 131,072 slots: 2,080,000 requests); R * ceil(q_len*H/64) below 2^28.
  *   workspace    scratch for split-KV, sized by mla_decode_q8_workspace_size (for the shards
  *                call with n_shards*B), or NULL / 0: without all of it no request is split.
  * Accuracy: products and sums are fp32; q is used to within 2^-17 of its row's largest

@@ -238,9 +238,11 @@ int decode_entry(const char* fn, const void* q, const void* kv_cache, bool q8,
   const mla::DecodeKernel k = mla::choose_decode_kernel(a);
   if (k == mla::kDecodeNone && q8)
     return fail(MLA_ERR_UNSUPPORTED,
-                "%s: q_len*H = %d rows may be %d row tiles of 64, and num_blocks*block_size and "
-                "max_blocks*block_size must stay below 2^31 - 65536",
-                fn, q_len * H, dev->num_sms);
+                "%s: %s (B=%d%s, q_len*H=%d, max_blocks=%d, num_blocks=%d, block_size=%d, %d SMs)", fn,
+                mla::q8_limit(a), a.B, n_shards > 1 ? " over all shards" : "", q_len * H, max_blocks,
+                num_blocks, block_size, dev->num_sms);
+  if (k == mla::kDecodeQ8 && !mla::q8_driver_ok())
+    return fail(MLA_ERR_CUDA, "%s: the CUDA driver has no cuTensorMapEncodeTiled", fn);
   if (k == mla::kDecodeNone)
     return fail(MLA_ERR_UNSUPPORTED,
                 "%s: no decode kernel for this layout (block_size %d: the tcgen05 kernel takes "

@@ -25,7 +25,7 @@ size_t decode_workspace_for(int B, int H, int q_len, int num_sms, int block_size
 
 DecodeKernel choose_decode_kernel(const DecodeArgs& a) {
   if (g_choice == 1) return kDecodeMma;
-  if (a.kv_scales != nullptr) return q8_supported(a) ? kDecodeQ8 : kDecodeNone;
+  if (a.kv_scales != nullptr) return q8_limit(a) == nullptr ? kDecodeQ8 : kDecodeNone;
   return tc_supported(a) ? kDecodeTc : kDecodeNone;
 }
 

@@ -58,7 +58,8 @@ size_t mma_workspace_size(int B, int H, int q_len, int num_sms);
 cudaError_t launch_decode_mma(const DecodeArgs& a, cudaStream_t stream);
 
 // tcgen05 kernel over the 8-bit cache (mla_decode_q8.cu)
-bool q8_supported(const DecodeArgs& a);
+const char* q8_limit(const DecodeArgs& a);   // the limit that a call exceeds, or null
+bool q8_driver_ok();                         // the driver encodes tensor maps
 size_t q8_workspace_size(int B, int H, int q_len, int num_sms);
 cudaError_t launch_decode_q8(const DecodeArgs& a, cudaStream_t stream);
 

@@ -1730,18 +1730,24 @@ cudaError_t launch(const CUtensorMap& kmap, const CUtensorMap& rmap, const Param
 
 }  // namespace
 
-bool q8_supported(const DecodeArgs& a) {
+const char* q8_limit(const DecodeArgs& a) {
   const int rows = a.H * a.q_len, n = rows_per_unit(a);
   const long long tiles = (rows + n - 1) / n;
-  if (tiles > a.num_sms) return false;              // a block for every row tile of a request
+  // a block for every row tile of a request
+  if (tiles > a.num_sms) return "ceil(q_len*H / 64) row tiles of a request are more than the SMs";
   // token and cache row numbers, with the look-ahead of the page window, fit 32 bits
-  if ((long long)a.num_blocks * a.block_size + kTile >= (1LL << 31)) return false;
-  if ((long long)a.max_blocks * a.block_size >= (1LL << 31) - 65536) return false;
-  if (a.B * tiles > 0x7fffffffLL / 8) return false;
-  // the split line
-  if (a.B * ((long long)a.max_blocks * a.block_size / kTile + 1 + Cfg<32>::kSegTiles) >= (1LL << 31)) return false;
-  return get_encoder() != nullptr;
+  if ((long long)a.num_blocks * a.block_size >= (1LL << 31) - 65536)
+    return "num_blocks*block_size must stay below 2^31 - 65536";
+  if ((long long)a.max_blocks * a.block_size >= (1LL << 31) - 65536)
+    return "max_blocks*block_size must stay below 2^31 - 65536";
+  if (a.B * tiles > 0x7fffffffLL / 8) return "requests (of all shards) times row tiles must stay below 2^28";
+  // the split line, were every request as long as its table
+  if (a.B * ((long long)a.max_blocks * a.block_size / kTile + 1 + Cfg<32>::kSegTiles) >= (1LL << 31))
+    return "requests (of all shards) times (max_blocks*block_size / 128 + 7) must stay below 2^31";
+  return nullptr;
 }
+
+bool q8_driver_ok() { return get_encoder() != nullptr; }
 
 size_t q8_workspace_size(int B, int H, int q_len, int num_sms) {
   const long long rows = (long long)H * q_len;

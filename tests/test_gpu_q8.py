@@ -22,7 +22,9 @@ scale, v_l the stored e4m3 values, A = sum_l w_l S_l |v_l|, M = max_l w_l S_l:
     rounding and log).
 Besides, the norm of the output's error is at most 2^-7 of the output's (roundings are
 independent; each is at most that)."""
+import ctypes
 import math
+import re
 
 import numpy as np
 import pytest
@@ -31,6 +33,7 @@ import torch
 import mla_paged_decode_03_gb300 as M
 import oracle.mla_ref as R
 import oracle.q8_ref as Q
+from mla_paged_decode_03_gb300 import _lib
 
 pytestmark = pytest.mark.gpu
 
@@ -1135,6 +1138,29 @@ def test_wrappers_refuse(name, change, error):
     with pytest.raises(error):
         getattr(M, name)(**{**good, **change(good)})
     getattr(M, name)(**good)
+    assert M.device_status() == 0
+
+
+@pytest.mark.parametrize("change,message", [
+    (dict(H=64 * 200), "row tiles of a request"),
+    (dict(nb=(1 << 27) - 4096, bs=16), "num_blocks.block_size must stay below 2.31 - 65536"),
+    (dict(maxb=(1 << 27) - 4096, bs=16), "max_blocks.block_size must stay below 2.31 - 65536"),
+    (dict(B=1 << 20, maxb=1 << 14, bs=16), "times .max_blocks.block_size / 128 . 7. must stay below 2.31"),
+    (dict(B=1 << 15, maxb=1 << 18, bs=16, shards=2), "2.31 .B=65536 over all shards"),
+    (dict(B=1 << 28, H=1), "row tiles must stay below 2.28"),
+])
+def test_decode_limits_are_named(change, message):
+    """What the tcgen05 kernel does not take is refused on the host, before the (made-up) addresses are
+    used, by the limit that was passed."""
+    a = dict(B=1, H=16, bs=16, nb=4, maxb=4, shards=1)
+    a.update(change)
+    head = [16, 16, 16, 16, a["maxb"], 16, 16, a["B"], a["H"], 1, 1, a["bs"], a["nb"], a["maxb"]]
+    tail = [1, ctypes.c_float(0.1), 16, 16, 1, None, 0, None]
+    lib = _lib.load()
+    rc = (lib.mla_decode_shards_q8(*head, a["shards"], *tail) if a["shards"] > 1
+          else lib.mla_decode_q8(*head, 1, 0, *tail))
+    assert rc == _lib.MLA_ERR_UNSUPPORTED
+    assert re.search(message, lib.mla_last_error().decode()), lib.mla_last_error()
     assert M.device_status() == 0
 
 
