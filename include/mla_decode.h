@@ -59,6 +59,9 @@ typedef struct CUstream_st* mla_stream_t;
 #define MLA_STATUS_OUT_OF_PAGES 32u   /* cp_step_tables: too few free pages             */
 #define MLA_STATUS_BAD_STEP 64u       /* a length or a ring state outside its range     */
 
+/* (major << 16) | minor: what mla_abi_version() of a library built with this header returns. */
+#define MLA_ABI_VERSION ((2 << 16) | 1)
+
 /* The 8-bit cache: e4m3 rows, one float scale for every MLA_Q8_GROUP consecutive slots of
  * a page; a scale is at least MLA_Q8_SCALE_MIN and at most MLA_Q8_SCALE_MAX. */
 #define MLA_Q8_GROUP 16

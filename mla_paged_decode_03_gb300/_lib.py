@@ -142,7 +142,7 @@ def load_q8(tables_type):
         loader.exec_module(m)
         m.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in
                  ("cp_step_tables", "cp_store_q8", "mla_decode_q8", "mla_decode_shards_q8",
-                  "mla_decode_q8_workspace_size")), check, tables_type)
+                  "mla_decode_q8_workspace_size", "mla_abi_version")), check, tables_type)
         _q8 = m
         return _q8
 

@@ -1,7 +1,8 @@
 """Builds libmla_decode.so in-tree (``mla_paged_decode_03_gb300/lib/``) with nvcc for
 sm_103a.  Each translation unit compiles in parallel; the CUDA runtime is linked
 statically so the library needs only the driver at run time.  Beside it q8_binding.so, the
-Python binding of the 8-bit cache's calls, host code against PyTorch's headers."""
+Python binding of the 8-bit cache's calls, host code against PyTorch's headers; the library
+is there without it."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -53,12 +54,13 @@ def binding_path() -> str:
 
 
 def _build_binding() -> str:
+    """Compiles the binding; returns its path until it takes its place beside the library."""
     import sysconfig
 
     import torch
 
     home = os.path.dirname(torch.__file__)
-    out = binding_path()
+    tmp = binding_path() + ".tmp"
     # (symbols of libtorch come from the process that imports it)
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
@@ -66,13 +68,12 @@ def _build_binding() -> str:
                                 os.path.join(home, "include", "torch", "csrc", "api", "include"),
                                 sysconfig.get_path("include"),
                                 os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include"))),
-           os.path.join(CSRC, BINDING + ".cpp"), "-o", out + ".tmp", "-L" + os.path.join(home, "lib"),
+           os.path.join(CSRC, BINDING + ".cpp"), "-o", tmp, "-L" + os.path.join(home, "lib"),
            "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{BINDING} failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(out + ".tmp", out)
-    return out
+    return tmp
 
 
 def build(verbose: bool = False, extra=None) -> str:
@@ -82,7 +83,6 @@ def build(verbose: bool = False, extra=None) -> str:
     with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
         binding = ex.submit(_build_binding)
         objs = list(ex.map(lambda s: _compile(s, extra), srcs))
-        binding.result()
     out = lib_path()
     tmp = out + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", tmp, *objs]
@@ -92,6 +92,13 @@ def build(verbose: bool = False, extra=None) -> str:
     os.replace(tmp, out)
     if verbose:
         print("built", out)
+    # the library stands; a binding that does not compile leaves no older one beside it
+    try:
+        os.replace(binding.result(), binding_path())
+    except BaseException:
+        if os.path.exists(binding_path()):
+            os.remove(binding_path())
+        raise
     return out
 
 

@@ -97,7 +97,7 @@ int api_fail(int code, const char* fmt, ...) {
 
 extern "C" {
 
-int mla_abi_version(void) { return (2 << 16) | 1; }
+int mla_abi_version(void) { return MLA_ABI_VERSION; }
 
 int mla_set_decode_kernel(int choice) {
   static std::atomic<int> current{0};

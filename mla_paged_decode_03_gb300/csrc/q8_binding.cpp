@@ -208,26 +208,31 @@ void arguments(Py_ssize_t n, Py_ssize_t want) {
   if (g.check == nullptr) refuse(PyExc_RuntimeError, "the library has not been bound");
 }
 
-// bind(step_tables, store, decode, decode_shards, workspace_size, check, tables_type)
+// bind(step_tables, store, decode, decode_shards, workspace_size, abi_version, check, tables_type);
+// refuses a library that was built with another ABI than this binding
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   try {
-    if (n != 7) refuse(PyExc_TypeError, "%zd arguments, not 7", n);
-    void* f[5];
-    for (int i = 0; i < 5; ++i) {
+    if (n != 8) refuse(PyExc_TypeError, "%zd arguments, not 8", n);
+    void* f[6];
+    for (int i = 0; i < 6; ++i) {
       f[i] = PyLong_AsVoidPtr(a[i]);
       if (f[i] == nullptr) refuse(PyExc_ValueError, "no address of function %d", i);
     }
-    if (!PyType_Check(a[6]) || !PyType_IsSubtype(reinterpret_cast<PyTypeObject*>(a[6]), &PyTuple_Type))
+    if (!PyType_Check(a[7]) || !PyType_IsSubtype(reinterpret_cast<PyTypeObject*>(a[7]), &PyTuple_Type))
       refuse(PyExc_TypeError, "the result type must be a tuple");
+    const int abi = reinterpret_cast<decltype(&mla_abi_version)>(f[5])();
+    if (abi != MLA_ABI_VERSION)
+      refuse(PyExc_ImportError, "the library has ABI version %d.%d, the binding was built for %d.%d: build both again",
+             abi >> 16, abi & 0xffff, MLA_ABI_VERSION >> 16, MLA_ABI_VERSION & 0xffff);
     g.step_tables = reinterpret_cast<decltype(g.step_tables)>(f[0]);
     g.store = reinterpret_cast<decltype(g.store)>(f[1]);
     g.decode = reinterpret_cast<decltype(g.decode)>(f[2]);
     g.decode_shards = reinterpret_cast<decltype(g.decode_shards)>(f[3]);
     g.workspace_size = reinterpret_cast<decltype(g.workspace_size)>(f[4]);
-    Py_XSETREF(g.check, Py_NewRef(a[5]));
+    Py_XSETREF(g.check, Py_NewRef(a[6]));
     PyTypeObject* old = g.tables_type;
-    g.tables_type = reinterpret_cast<PyTypeObject*>(Py_NewRef(a[6]));
+    g.tables_type = reinterpret_cast<PyTypeObject*>(Py_NewRef(a[7]));
     Py_XDECREF(reinterpret_cast<PyObject*>(old));
     Py_RETURN_NONE;
   } catch (const Raised&) {

@@ -1,6 +1,8 @@
 """The 8-bit paged cache without a GPU: what the C entry points and the Python wrappers
 refuse, and checks that pin its oracle (torch's e4m3 conversion, hand-worked steps)."""
 import ctypes
+import os
+import shutil
 
 import numpy as np
 import pytest
@@ -8,7 +10,7 @@ import torch
 
 import mla_paged_decode_03_gb300 as M
 import oracle.q8_ref as Q
-from mla_paged_decode_03_gb300 import _lib
+from mla_paged_decode_03_gb300 import _lib, build
 
 from test_abi_cpu import lib  # noqa: F401  (the built library)
 
@@ -172,3 +174,55 @@ def test_oracle_store_by_hand():
     assert s[1, 0] == 2.0 ** -6 and c[1, 0, :2].tolist() == [64.0, -112.0]
     assert c[1, 1, 0] == 448.0 and np.isnan(c[1, 1, 1:3]).all()
     assert np.allclose(Q.ref_dequantised(c, s)[1, 0, :2], [1.0, -1.75])
+
+
+# ---- the library and its binding ---------------------------------------------------------------
+def _use_objects(lib, monkeypatch, tmp_path):  # noqa: F811
+    """build() into tmp_path, from the objects that the library was built of."""
+    objs, here = build.OBJDIR, build._compile
+    monkeypatch.setattr(build, "LIBDIR", str(tmp_path))
+    monkeypatch.setattr(build, "OBJDIR", str(tmp_path / "obj"))
+
+    def compiled(src, extra):
+        obj = os.path.join(objs, os.path.basename(src)[:-3] + ".o")
+        if not os.path.exists(obj):
+            return here(src, extra)
+        return shutil.copy(obj, build.OBJDIR)
+    monkeypatch.setattr(build, "_compile", compiled)
+
+
+def test_library_is_built_without_its_binding(lib, monkeypatch, tmp_path):  # noqa: F811
+    """Where the binding does not compile (no C++ compiler here; no headers of Python or PyTorch) the
+    C library is still built, no older binding stays beside it, and the failure is raised."""
+    _use_objects(lib, monkeypatch, tmp_path)
+    monkeypatch.setenv("CXX", "false")
+    (tmp_path / "q8_binding.so").write_bytes(b"of an older build")
+    with pytest.raises(RuntimeError, match="q8_binding"):
+        build.build()
+    assert ctypes.CDLL(build.lib_path()).mla_abi_version() == lib.mla_abi_version()
+    assert not os.path.exists(build.binding_path())
+
+
+def test_library_that_does_not_link_leaves_the_old_pair(lib, monkeypatch, tmp_path):  # noqa: F811
+    _use_objects(lib, monkeypatch, tmp_path)
+    monkeypatch.setattr(build, "_build_binding", lambda: str(tmp_path / "new"))
+    monkeypatch.setattr(build, "ARCH", ["--no-such-option"])
+    for f in (build.lib_path(), build.binding_path()):
+        open(f, "w").write("old")
+    with pytest.raises(RuntimeError, match="link failed"):
+        build.build()
+    for f in (build.lib_path(), build.binding_path()):
+        assert open(f).read() == "old"
+
+
+def test_binding_refuses_a_library_of_another_abi(lib):  # noqa: F811
+    b = _lib.load_q8(M.StepTables)
+    other = ctypes.CFUNCTYPE(ctypes.c_int)(lambda: lib.mla_abi_version() + 1)
+    address = [ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
+               for f in ("cp_step_tables", "cp_store_q8", "mla_decode_q8", "mla_decode_shards_q8",
+                         "mla_decode_q8_workspace_size")]
+    with pytest.raises(ImportError, match="ABI version"):
+        b.bind(*address, ctypes.cast(other, ctypes.c_void_p).value, _lib.check, M.StepTables)
+    # and goes on with the one it was bound to
+    with pytest.raises((ValueError, TypeError)):
+        M.cp_store_q8(None, None, None, None, None, None)
