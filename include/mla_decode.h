@@ -350,14 +350,12 @@ int cp_store_q8(const void* kv_new, const int32_t* ctx_lens, const int32_t* tota
  * magnitude (exactly, for elements within 2^-9 of it).  A softmax weight meets the values in
  * fewer bits than its sum (the LSE) is made of, where the bf16 cache's decode rounds it to bf16
  * (2^-8 of itself).  With p = weight times scale, P the row's largest p, and p' the largest of 16
- * neighbouring keys:
- *   - where p' of all rows of a block (64, or 32 in small calls) is at least 2^-9 P, each p is used
- *     to within 2^-8 of itself plus 2^-6 p';
- *   - else, down to p' = 2^-28 P, to within 2^-7 of itself plus 2^-22 P (2^-28 P where P's key stands
- *     alone among some 100 around it, 2^9 above the rest).
- * The second terms are bounds for one key; they are rounded up or down evenly over the keys, so
- * that sums over many keep them (n equal weights: 2^-7 of their sum and some times the second term,
- * not n times).
+ * neighbouring keys: p is used to within 2^-7 of itself (2^-8 in tiles of 128 keys where p' is at least
+ * 2^-9 P throughout for all rows of a block and P does not grow) plus 2^-6 p', or 2^-22 P where p' is
+ * smaller than 2^-9 P (2^-28 P where P's key stands alone among some 100 around it, 2^9 above the
+ * rest).  The second term bounds a single key's: it is rounded up or down evenly over the keys, so
+ * that sums over many keep it (n equal weights: 2^-7 of their sum and some times that term, not n
+ * times).
  * Errors: as mla_decode / mla_decode_shards.
  */
 size_t mla_decode_q8_workspace_size(int B, int H, int q_len, int num_sms);

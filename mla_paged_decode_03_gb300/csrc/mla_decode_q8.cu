@@ -93,9 +93,11 @@ constexpr int kRopeBytes = kTile * 64;
 constexpr int kR = 16;                     // query rows per softmax warp
 // log2 of the largest weight that a reference may stay with, of where a new reference puts a tile's
 // largest, and of the excess that moves a row's when some row's weights pass the first
-constexpr float kTop = 12.f, kPlace = 6.f, kMove = 9.f;
-// A largest weight that stands alone in its tile is put higher, so that the rest is at 2^kRest, up to kTop
-constexpr float kRest = 3.f;
+// (2^12.125: hi's residue is below 448 up to 2^12.149)
+constexpr float kTop = 12.125f, kPlace = 6.f, kMove = 9.f;
+// A largest weight that stands alone in its tile is put higher, so that the rest is at 2^kRest, up to
+// 2^kAlone: below kTop, or another key of the same score would move the reference
+constexpr float kRest = 3.f, kAlone = 12.f;
 // A tile has fine weights where some row's largest of 16 keys is between 2^kNone and 2^kFine (see above)
 constexpr float kNone = -22.f, kFine = -3.f;
 
@@ -1338,7 +1340,7 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
             const bool one = it.t_end - it.t_begin == 1;
             float by = 0.f;
             if (m != -INFINITY && (first || m > kMove))
-              by = (one ? kTop : rest == -INFINITY ? kPlace : fminf(fmaxf(kPlace, kRest + (m - rest)), kTop)) - m;
+              by = (one ? kAlone : rest == -INFINITY ? kPlace : fminf(fmaxf(kPlace, kRest + (m - rest)), kAlone)) - m;
             shift[st] = by;
             factor[st] = first ? 1.f : fast_exp2(by);   // (a first reference may lie far down: 0 * inf)
             row_nm[st] += by;

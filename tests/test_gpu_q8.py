@@ -711,8 +711,9 @@ def test_decode_many_small_weights_below_one_large(n, where, big, raised, kernel
     assert np.abs(n64(lse).reshape(rows) - (s + np.log(z))).max() <= adds * 2.0 ** -24 + 5e-5 + 2e-5
 
 
+@pytest.mark.parametrize("split", [False, True])
 @pytest.mark.parametrize("gap,big", [(6.0, 1), (12.0, 1), (12.0, 16), (16.0, 1)])
-def test_decode_values_beside_one_large_weight(gap, big, kernel):
+def test_decode_values_beside_one_large_weight(gap, big, split, kernel):
     """A key of value 0 takes nearly all the weight (as first tokens do); the output is what the
     others make of the rest.  Their weights are used to within 2^-7 of themselves, however small
     against the large one: bound as in this file's header, but the term in M is two halves of a step
@@ -736,7 +737,7 @@ def test_decode_values_beside_one_large_weight(gap, big, kernel):
     v = Q.ref_e4m3(x / np.repeat(sc, 16)[:, None])
     cache, scales = gpu_pool((v.reshape(n // bs, bs, 576), sc.reshape(n // bs, bs // 16)))
     out, lse = M.mla_decode_q8(q.to(DEV), cache, scales, bt32(np.arange(n // bs)[None]), i32([n]), None, 1, 1, 0, SCALE,
-                               workspace=torch.empty(0, dtype=torch.uint8, device=DEV))
+                               workspace=None if split else torch.empty(0, dtype=torch.uint8, device=DEV))
     assert M.device_status() == 0
     k = v * np.repeat(sc, 16)[:, None]
     s = SCALE * (n64(q)[0, 0] @ k.T)
