@@ -14,8 +14,8 @@
 // when a request's N positions fit, else one request's next `tile` positions.
 //
 // Bound: the launch and the chain lengths -> scan -> table or ring -> slot of dependent L2
-// accesses (8 requests, a token each: 3.0 us; 256 requests of 4 tokens on 8 ranks, 32 of them
-// finished: 5.1; 32 prompts of up to 8,192: 6.4 for 4.2 MB of positions and slots, 0.6 at
+// accesses (8 requests, a token each: 3.2 us; 256 requests of 4 tokens on 8 ranks, 32 of them
+// finished: 5.5; 32 prompts of up to 8,192: 7.0 for 4.2 MB of positions and slots, 0.6 at
 // the copy rate).
 #include <cuda_runtime.h>
 

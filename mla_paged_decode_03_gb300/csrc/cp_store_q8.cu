@@ -14,8 +14,10 @@
 // no second launch.  The group's up to 16 new rows (1,152 bytes each) stay in registers
 // between the maximum and the rounding, 16 bytes a load, nine a thread.
 //
-// HBM-bound for prompts: 1,152 bytes in and 576.25 out per row (16 prompts, 98,000 rows: 29.6 us,
-// 5.7 TB/s; 25.0 at the copy rate).  Few rows: the launch and two dependent loads (64 rows 2.9 us).
+// HBM for prompts: 1,152 bytes in and 576.25 out per row (16 prompts, 98,000 rows: 33.4 us, 5.1 TB/s;
+// 25.0 at the copy rate): a block loads its group, waits for the maximum, rounds and writes, with
+// nothing of its own under way meanwhile, and only the SM's seven other blocks cover that.  Few
+// rows: the launch and two dependent loads (64 rows 3.1 us).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -113,7 +115,7 @@ __device__ __forceinline__ uint2 again8(uint2 v, float ratio) {
 }
 
 // (eight blocks an SM: with the 80 registers that the compiler takes otherwise, 33.4 instead of
-// 29.6 us for 16 prompts of up to 8,192 rows)
+// 29.6 us for 16 prompts of up to 8,192 rows that are the same, and half in L2, in every call)
 __global__ void __launch_bounds__(kThreads, 8) cp_store_q8_kernel(const Params p) {
   __shared__ unsigned int s_peak[kThreads / 32];
   __shared__ long long s_src[kGroup];                    // where each new row begins, in 16 bytes

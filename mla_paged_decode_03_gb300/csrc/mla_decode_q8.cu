@@ -18,7 +18,7 @@
 //   32 rows: S^T [128 keys x hi and lo of 32 rows] = K8 Q^T, Q in shared memory, two S^T: such
 //     units are bound by HBM or by their start, and rows as M = 128 would double QK's time.
 //
-// 8-bit operands without losing bits.  Both factors of a product must be 8-bit types, and
+// 8-bit operands in two parts.  Both factors of a product must be 8-bit types, and
 // a query or a weight rounded to one e4m3 value would be off by up to 2^-4.  So:
 //   * q, times a power of two that puts its row's maximum in [128, 256), is the sum of two
 //     e4m3 values hi + lo: a bf16 has 8 significant bits, each e4m3 holds 4, and hi's residue
@@ -35,25 +35,27 @@
 //     and without dithers, 16,384 of e^-8 of the largest lost 5 % of the output, of e^-15 40 %).
 // An e4m3 residue (at most 448) serves p up to 2^12.  m is set 2^6 below a tile's largest S_l 2^t'_l
 // and moved (then O, l and m move together) only when a tile exceeds 2^12.  Nearer to 2^12 small
-// weights would have more of the range, but a move costs half a tile's time (64 x 128 rows of 32k keys,
-// set 2^8 / 2^7 / 2^6 below: 389 / 383 / 380 us); at 2^12 where a segment has but one tile.  Where a tile's largest stands alone (as first tokens
-// do, with nearly all the weight and little value), the rest counts: that is set to 2^3 or more as far
-// as 2^12 for the largest allows.
+// weights would have more of the range, but a move costs half a tile's time (2^10 / 2^8 / 2^6 / 2^5
+// below: 64 x 128 rows of 32k keys 404 / 383 / 376 / 373 us, 8 x 256 of 512..4k 27.2 / 25.5 / 24.6 /
+// 24.3); at 2^12 where a segment has but one tile.  Where a tile's largest stands alone (as first
+// tokens do, with nearly all the weight and little value), the rest counts: that is set to 2^3 or
+// more, as far as 2^12 for the largest allows.  All this takes 2 to 8 % of the time (e4m3 residues
+// alone, without dithers, set 2^5 below: 368 us, with outliers 565).
 //
 // Roles (20 warps, 12 for 32 rows): warp 0 loads tiles (TMA, four 16 KB chunks of latent dims
 // and one of rope dims each, chunk by chunk as PV frees them), warp 1 issues the QK products and
 // warp 2 the PV products, each when its inputs have come (one warp for both in a fixed order
-// waits for the later of two inputs: 64 x 32k 376 -> 408 us; one that polls both takes issue
-// slots from the softmax warps of its scheduler), warp 3 walks the schedule, passes the block's
+// waits for the later of two inputs: 8 % of 64 x 32k; one that polls both takes issue slots from the
+// softmax warps of its scheduler), warp 3 walks the schedule, passes the block's
 // segments on and looks the tiles' scales up, the others take 32 keys and 16 rows each: they
 // read S, scale, mask, exponentiate and write P^T; they also prepare Q and write the output.
 //
-// Bounds: few rows by the cache's bytes (64 x 16 rows of 1k..16k keys: 64.7 us, 47.7 at the
-// copy rate); 64 rows by shared-memory bandwidth: a tile's QK reads 16 x 4 + 2 x (4 + 4) KB and its
+// Bounds: few rows by the cache's bytes (64 x 16 rows of 1k..16k keys: 67 us, 47.7 at the copy
+// rate); 64 rows by shared-memory bandwidth: a tile's QK reads 16 x 4 + 2 x (4 + 4) KB and its
 // PV 32 x (4 + 2) KB, TMA writes 72 KB and the softmax 16 KB, 2,880 cycles at 128 bytes a cycle of
-// the 3,100 that it takes, against 2,176 of tensor time.  64 x 128 rows of 32,768 keys: 370 us
-// (415 held for a second, at the power limit), 1.58 PFLOP/s, twice that as issued; 4 x 256 rows
-// of 256k..512k with outliers: 550 us; 32 x 512 rows of 1k..16k: 222 us.
+// the 3,150 that it takes, against 2,176 of tensor time.  64 x 128 rows of 32,768 keys: 376 us
+// (430 call after call, at the power limit), 1.55 PFLOP/s, twice that as issued; 4 x 256 rows of
+// 256k..512k with outliers: 608 us (616); 32 x 512 rows of 1k..16k: 214 us (227).
 //
 // Work split, partials and the combine: as in mla_decode_tc.cu (tiles of all requests on one
 // line, equal ranges, units cut between blocks merged by a second kernel); a block has at most
@@ -606,8 +608,8 @@ __device__ __forceinline__ bool take_segment(const Ctx& s, uint32_t i, const Par
 
 // Four warps' part of a segment's output: the 128 dims of chunk col / kN (32 a warp) and twice 32
 // rows of O^T, which go through 8 KB of shared memory (their share of P^T, which no product reads
-// then) to become rows of 256 bytes (64 bytes, a warp by itself: 228 x 768 rows of 66 keys 164.6 us
-// instead of 162.4).
+// then) to become rows of 256 bytes (64 bytes, a warp by itself: 2 us more for 228 x 768 rows of 66
+// keys, 163 us).
 // The unit's output (bf16) is O / l.  A partial is O / w, w the sum of the weights (scales
 // included): a mean of e4m3 values, at most 448, so that half precision holds it to 2^-11 in half
 // the bytes of fp32; w / l goes with the row's LSE.  (A function of its own, so that its registers
@@ -1325,7 +1327,8 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
         };
         // one barrier in most tiles; where that finds something, another tells whether references have to
         // move (those tiles have fine weights in any case: to ask again would take one more)
-        const bool first = t == it.t_begin, ask = !first && asks(), over = fmaxf(fmax3(m4.x, m4.y, m4.z), m4.w) > kTop;
+        const bool first = t == it.t_begin, ask = !first && asks();
+        const bool over = fmaxf(fmax3(m4.x, m4.y, m4.z), m4.w) > kTop;
         bool fine = !first && soft_or<kN>(ask || over);
         const bool move = first || (fine && soft_or<kN>(over));
         if (move) {
@@ -1680,12 +1683,12 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encoder() {
   return fn;
 }
 
-// Rows per unit: 32 or 64.  A tile costs a unit of 32 rows 0.85 of what it costs one of 64, so
-// two of them take 1.7 times as long, but their start (Q, first loads) and output are 3 to 4 us
+// Rows per unit: 32 or 64.  A tile costs a unit of 32 rows 0.8 of what it costs one of 64, so
+// two of them take 1.6 times as long, but their start (Q, first loads) and output are 3 to 4 us
 // shorter.  32 where a request has no more rows, and where full tables would give a block fewer
-// than 5 tiles in units of 64 (units of 32 / 64, 8 x 128 rows of 1,024 keys 14.4 / 17.5 us, of
-// 4,096 20.5 / 21.4, of 8,192 28.6 / 27.4; 64 x 128 of 512 24.0 / 26.3, of 1,024 33.6 / 33.0;
-// 1 x 128 of 8,192 15.1 / 18.6; 16 x 80 of 1,024 17.1 / 19.1, of 16,384 67.0 / 60.5); else 64.
+// than 5 tiles in units of 64 (units of 32 / 64, 8 x 128 rows of 1,024 keys 14.8 / 17.3 us, of
+// 4,096 21.5 / 21.4, of 8,192 29.9 / 27.9; 64 x 128 of 512 25.6 / 26.4, of 1,024 35.4 / 33.5;
+// 1 x 128 of 8,192 15.6 / 18.7; 16 x 80 of 1,024 17.8 / 19.3, of 16,384 72.7 / 60.7); else 64.
 int rows_per_unit(long long B, long long rows, long long max_keys, int num_sms) {
   if (rows <= 32) return 32;
   if ((rows + 31) / 32 > num_sms) return 64;
