@@ -654,7 +654,8 @@ def test_decode_without_workspace_and_without_lse(B, H, q_len, G, units):
 # e5m2 (tiles with a row whose largest of 16 weights is below 2^-9 of its reference, and tiles that
 # move one) by 2^-7 of the weight, where 2^-8 and 2^-10 for partials and half precision are counted, and
 # a step of 2^-16: the difference, 2^-8 of a weight, is inside 2^-14 M per key for weights below
-# 2^-6 M, and for the few above it inside 2^-14 M of the 64 keys or more that such a tile has.
+# 2^-6 M, and for the few above it inside 2^-14 M of each of the 64 keys or more that there are (a
+# request of fewer is one tile, whose rows' largest are put at 2^12 and have no error).
 @pytest.mark.parametrize("n", [16384, 131072, 524288])
 @pytest.mark.parametrize("where,big,raised", [(0, 1, 0), (0, 32, 0), (5000, 1, 0), (5000, 32, 0), (0, 1, 192),
                                               (5000, 32, 192), (0, 1, 384)])
