@@ -1,8 +1,10 @@
 /*
  * mla_decode.h -- C ABI of libmla_decode.so: paged multi-head-latent-attention (MLA)
  * decode with decode-context-parallel (DCP) shards, the LSE merge of shard partials,
- * DCP slot mapping, and the 8-bit form of the paged cache (a step's tables from request
- * lengths, the quantising store, the decode over it), for NVIDIA GB300 (sm_103a).
+ * DCP slot mapping, the 8-bit form of the paged cache (a step's tables from request
+ * lengths, the quantising store, the decode over it), and prompt processing (rotary positions,
+ * the append with rotation, the heads' keys and values, the attention of chunks of new
+ * tokens), for NVIDIA GB300 (sm_103a).
  *
  * Sources (web pages summarising vLLM pull requests):
  *   [#52188] "支持 Kimi-K3 DSpark 推测解码与 DCP 并行组合" (vLLM PR 52188)
@@ -60,7 +62,7 @@ typedef struct CUstream_st* mla_stream_t;
 #define MLA_STATUS_BAD_STEP 64u       /* a length or a ring state outside its range     */
 
 /* (major << 16) | minor: what mla_abi_version() of a library built with this header returns. */
-#define MLA_ABI_VERSION ((2 << 16) | 1)
+#define MLA_ABI_VERSION ((2 << 16) | 2)
 
 /* The 8-bit cache: e4m3 rows, one float scale for every MLA_Q8_GROUP consecutive slots of
  * a page; a scale is at least MLA_Q8_SCALE_MIN and at most MLA_Q8_SCALE_MAX. */
@@ -376,6 +378,128 @@ int mla_decode_shards_q8(const void* q, const void* kv_cache, const float* kv_sc
                          mla_stream_t stream);
 
 /*
+ * mla_rope -- rotary positions: turns the 32 pairs of each rope part (64 dims) of
+ * x [T, H, 64] by the token's position p = positions[t]:
+ *     a_i = 2 pi frac(p * freqs[i] * 2^-64),
+ *     y0 = mscale (x0 cos a_i - x1 sin a_i),  y1 = mscale (x0 sin a_i + x1 cos a_i),
+ * with the pairs (2i, 2i+1) (half == 0) or (i, i+32) (half != 0), rounded to bf16 once.  Tokens
+ * at negative positions (rejected or padded ones) are left as they were in out.
+ *
+ * Arguments:
+ *   x            bf16, 64 contiguous dims at x + t*x_stride_t + h*x_stride_h (elements): the last
+ *                dims of queries of any width; 16-byte aligned, strides multiples of 8.
+ *   positions    int64 [T];  freqs  int64 [32], turns a position in units of 2^-64.
+ *   out          as x, with its own strides (so that absorbed queries, 576 wide, take their rope
+ *                part where it belongs); may be x itself, may not overlap it otherwise.
+ *   T >= 0, H >= 1, finite mscale.
+ * Errors: MLA_ERR_INVALID_ARGUMENT, MLA_ERR_CUDA.
+ */
+int mla_rope(const void* x, int64_t x_stride_t, int64_t x_stride_h, const int64_t* positions,
+             const int64_t* freqs, int T, int H, int half, float mscale, void* out,
+             int64_t out_stride_t, int64_t out_stride_h, mla_stream_t stream);
+
+/*
+ * cp_rope_store -- writes new tokens into this rank's pool at the slots cp_local_slot gives them,
+ * the rope part of their keys rotated on the way:
+ *     kv_cache[s] = [ latent[b, n] (512, bit for bit) | rotated k_rope[b, n] (64, see mla_rope) ];
+ * positions this rank does not own, and negative ones, write nothing and are not read.
+ *
+ * Arguments (as cp_local_slot_scatter and mla_rope unless stated):
+ *   latent       bf16, row b*N + n (512 contiguous) at latent + (b*N + n)*latent_stride;
+ *   k_rope       bf16, row b*N + n (64 contiguous) at k_rope + (b*N + n)*k_rope_stride: both may
+ *                be parts of one tensor; 16-byte aligned, strides multiples of 8 elements.
+ * A table entry outside [0, num_blocks) writes nothing and sets MLA_STATUS_BAD_PAGE.
+ * Errors: as cp_local_slot_scatter.
+ */
+int cp_rope_store(const void* latent, int64_t latent_stride, const void* k_rope,
+                  int64_t k_rope_stride, const int64_t* positions, const int64_t* freqs,
+                  const int32_t* block_table, int64_t bt_stride, int max_blocks, int B, int N,
+                  int block_size, int cp_size, int cp_rank, int interleave, int half, float mscale,
+                  void* kv_cache, int num_blocks, int64_t* slots, mla_stream_t stream);
+
+/*
+ * mla_expand -- keys and values of all heads (the expanded form of latent attention) from the
+ * paged cache.  Local key l of request b, with cache row c, becomes row r = kv_starts[b] + l of
+ *     kv[h, r, 0:128]   = w_kv[h, 0:128] c[0:512]     (the key's part without position),
+ *     kv[h, r, 128:256] = w_kv[h, 128:256] c[0:512]   (the value),
+ *     k_rope[r]         = c[512:576],
+ * products summed in fp32 and rounded to bf16 once.  Rows of no request are left as they were.
+ *
+ * Arguments:
+ *   kv_cache     bf16 [num_blocks, block_size, 576], or, with kv_scales (not NULL), the 8-bit cache
+ *                (see mla_decode_q8; its rows times their scales are rounded to bf16, exactly so
+ *                for powers of two); 16-byte aligned; any block_size >= 1 (8-bit: multiples of 16).
+ *   block_table, seq_lens  as mla_decode (shard-local lengths).
+ *   kv_starts    int32 [B]: the requests' first rows, in order and apart
+ *                (kv_starts[b] + seq_lens[b] <= kv_starts[b+1]).
+ *   w_kv         bf16 [H, 256, 512], 16-byte aligned.
+ *   kv           bf16 [H, S, 256];  k_rope  bf16 [S, 64]; 16-byte aligned.  Rows from S on are not
+ *                written.
+ *   B >= 0, S >= 0, 1 <= H <= 2^22, 1 <= max_blocks <= bt_stride, num_blocks >= 1.
+ * A page outside [0, num_blocks) reads as zeros with MLA_STATUS_BAD_PAGE, a length beyond the table
+ * is cut with MLA_STATUS_SEQ_TOO_LONG, a scale out of range is taken as 1 with
+ * MLA_STATUS_BAD_SCALE.  kv_starts out of order leave rows unwritten or give them to another request.
+ * Errors: MLA_ERR_INVALID_ARGUMENT, MLA_ERR_UNSUPPORTED (max_blocks*block_size beyond 2^31-1),
+ *   MLA_ERR_CUDA.
+ */
+int mla_expand(const void* kv_cache, const float* kv_scales, const int32_t* block_table,
+               int64_t bt_stride, const int32_t* seq_lens, const int32_t* kv_starts, int B,
+               int block_size, int num_blocks, int max_blocks, const void* w_kv, int H, int S,
+               void* kv, void* k_rope, mla_stream_t stream);
+
+/*
+ * mla_prefill -- attention of chunks of new tokens, of any and different lengths, over expanded
+ * keys and values (those mla_expand gives, or others of these shapes).
+ *
+ * Request b brings the query rows cu_q_lens[b] .. cu_q_lens[b+1] - 1, n of them, and has
+ * seq_lens[b] local keys, the rows from kv_starts[b] on.  Its row i sees the first L_i of them, as
+ * in mla_decode with q_len = n: L_i = min(seq_lens[b], local_len(max(0, G_b - (n-1-i)))), G_b =
+ * causal_seqlens_global[b], the new tokens included; all of them when causal == 0.  With
+ *     s_l = scale * (<q[0:128], k_nope_l> + <q[128:192], k_rope_l>),
+ *     out = sum_l softmax(s)_l v_l,   lse = log(sum_l exp(s_l))   (natural, or log2),
+ * a row with L_i = 0 gets out = 0 and lse = -inf.  Rows of no request are left as they were.
+ * The results of a shard's keys are partial ones, which lse_merge_v joins.
+ *
+ * Arguments:
+ *   q            bf16, 192 contiguous dims (128 without position, 64 rotated) at
+ *                q + t*q_stride_t + h*q_stride_h (elements), T rows.
+ *   k_nope, v    bf16, 128 contiguous dims at + s*stride_s + h*stride_h, S rows;
+ *   k_rope       bf16, 64 contiguous dims at + s*k_rope_stride, S rows, shared by the heads.
+ *                All 16-byte aligned, strides multiples of 8 elements and positive.
+ *   cu_q_lens    int32 [B+1];  kv_starts, seq_lens  int32 [B].
+ *   causal_seqlens_global  int32 [B]; may be NULL when cp_world == 1 (then seq_lens is used) or
+ *                causal == 0 (then it is not read).
+ *   out          bf16 [T, H, 128], 16-byte aligned;  lse  float [T, H] or NULL.
+ *   workspace    scratch of mla_prefill_workspace_size bytes, 256-byte aligned, or NULL / 0: without
+ *                all of it the keys of few rows are not split over the SMs.
+ *   T, B, S >= 0 (S >= 1 with any row), 1 <= H <= 65535; cp_world, cp_rank, interleave, scale as
+ *   mla_decode (interleave need not divide anything here).
+ * Values of a request's keys must be finite where any of its rows sees them: a row that does not
+ * see a key may still get NaN from a value of it that is NaN or infinite.  Rows behind the last key
+ * may hold anything.
+ * cu_q_lens out of order or beyond T (the request is skipped), and kv_starts or seq_lens beyond S
+ * (cut), set MLA_STATUS_BAD_STEP.
+ * Accuracy: scores and sums in fp32; a softmax weight is rounded to bf16 where it meets the values.
+ * Errors: MLA_ERR_INVALID_ARGUMENT, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA.
+ */
+size_t mla_prefill_workspace_size(int T, int B, int H, int S, int num_sms);
+
+int mla_prefill(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k_nope,
+                int64_t k_stride_s, int64_t k_stride_h, const void* k_rope, int64_t k_rope_stride,
+                const void* v, int64_t v_stride_s, int64_t v_stride_h, const int32_t* cu_q_lens,
+                const int32_t* kv_starts, const int32_t* seq_lens,
+                const int32_t* causal_seqlens_global, int T, int B, int H, int S, int causal,
+                int cp_world, int cp_rank, int interleave, float scale, void* out, float* lse,
+                int lse_base_e, void* workspace, size_t workspace_bytes, mla_stream_t stream);
+
+/*
+ * lse_merge_v -- lse_merge for partials [n_shards, T, H, dv] and out [T, H, dv], dv 512 or 128 (the
+ * outputs of mla_prefill).  Errors: as lse_merge, and MLA_ERR_UNSUPPORTED for another dv.
+ */
+int lse_merge_v(const void* partials, int partials_fp32, const float* lses, int n_shards, int T,
+                int H, int dv, void* out, float* out_lse, int lse_base_e, mla_stream_t stream);
+
+/*
  * mla_decode_noalloc -- mla_decode for callers that cannot allocate device memory.
  *
  * The pages have no counterpart to this call.  It computes exactly what mla_decode
@@ -453,7 +577,7 @@ int mla_set_test_stall(int on);
 /* Message of the calling thread's last failed call (empty string if none). */
 const char* mla_last_error(void);
 
-/* ABI version of this library: (major << 16) | minor (2.1). */
+/* ABI version of this library: (major << 16) | minor (2.2). */
 int mla_abi_version(void);
 
 #ifdef __cplusplus

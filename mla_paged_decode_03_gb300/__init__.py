@@ -11,6 +11,10 @@ Thin PyTorch-facing wrappers over the C ABI of ``libmla_decode.so``:
   cp_step_tables         a step's pages, lengths, positions and slots from request lengths
   cp_store_q8            quantise new KV rows into the 8-bit cache (e4m3, a scale per 16 slots)
   mla_decode_q8          mla_decode over the 8-bit cache (mla_decode_shards_q8: every shard)
+  mla_rope               rotary positions of queries (rope_freqs: frequencies, scaled or not)
+  cp_rope_store          write new tokens into the pool, their rope part rotated on the way
+  mla_expand             keys and values of all heads from the cached latent rows
+  mla_prefill            attention of chunks of new tokens over those keys
 
 PyTorch provides device memory and the current stream; every step of the computation
 runs in the library's CUDA kernels.  All tensors must live on the current CUDA device.
@@ -32,7 +36,9 @@ __all__ = ["mla_decode", "mla_decode_shards", "lse_merge", "cp_local_slot",
            "cp_local_slot_scatter", "workspace_size", "device_status", "set_decode_kernel",
            "set_rescale_budget", "set_wait_limit_ns", "PAD_SLOT_ID", "MlaError", "D_QK", "D_V",
            "cp_step_tables", "cp_store_q8", "mla_decode_q8", "mla_decode_shards_q8", "StepTables",
-           "workspace_size_q8", "alloc_workspace_q8", "Q8_GROUP"]
+           "workspace_size_q8", "alloc_workspace_q8", "Q8_GROUP", "rope_freqs", "mla_rope",
+           "cp_rope_store", "mla_expand", "mla_prefill", "workspace_size_prefill",
+           "alloc_workspace_prefill", "D_ROPE", "D_NOPE", "D_HEAD_V"]
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -181,25 +187,25 @@ def mla_decode_shards(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torc
 def lse_merge(partials: torch.Tensor, lses: torch.Tensor, out: Optional[torch.Tensor] = None,
               out_lse: Optional[torch.Tensor] = None, lse_base_e: bool = True,
               stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
-    """Merge partials [n, T, H, 512] (bf16 or float32) with lses [n, T, H] float32 into
-    out [T, H, 512] bf16 (and out_lse [T, H] float32 when given)."""
+    """Merge partials [n, T, H, D] (bf16 or float32; D 512, or 128 as mla_prefill gives) with lses
+    [n, T, H] float32 into out [T, H, D] bf16 (and out_lse [T, H] float32 when given)."""
     if partials.dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("partials must be bf16 or float32")
     _need(partials, "partials", partials.dtype, 4)
     n, T, H, Dv = partials.shape
-    if Dv != D_V:
-        raise ValueError("partials must be [n, T, H, 512]")
+    if Dv not in (D_V, 128):
+        raise ValueError("partials must be [n, T, H, 512] or [n, T, H, 128]")
     _need(lses, "lses", torch.float32, 3)
     if tuple(lses.shape) != (n, T, H):
         raise ValueError("lses must be [n, T, H]")
     if out is None:
-        out = torch.empty(T, H, D_V, dtype=torch.bfloat16, device=partials.device)
+        out = torch.empty(T, H, Dv, dtype=torch.bfloat16, device=partials.device)
     _need(out, "out", torch.bfloat16)
     if out_lse is not None:
         _need(out_lse, "out_lse", torch.float32)
-    rc = _lib.load().lse_merge(partials.data_ptr(), 1 if partials.dtype == torch.float32 else 0,
-                               lses.data_ptr(), n, T, H, out.data_ptr(), _ptr(out_lse),
-                               1 if lse_base_e else 0, _stream(stream))
+    rc = _lib.load().lse_merge_v(partials.data_ptr(), 1 if partials.dtype == torch.float32 else 0,
+                                 lses.data_ptr(), n, T, H, Dv, out.data_ptr(), _ptr(out_lse),
+                                 1 if lse_base_e else 0, _stream(stream))
     _lib.check(rc)
     return out, out_lse
 
@@ -312,3 +318,5 @@ def device_status(stream=None) -> int:
 
 from .q8 import (Q8_GROUP, StepTables, alloc_workspace_q8, cp_step_tables,  # noqa: E402,F401
                  cp_store_q8, mla_decode_q8, mla_decode_shards_q8, workspace_size_q8)
+from .prompt import (D_HEAD_V, D_NOPE, D_ROPE, alloc_workspace_prefill, cp_rope_store,  # noqa: E402,F401
+                     mla_expand, mla_prefill, mla_rope, rope_freqs, workspace_size_prefill)

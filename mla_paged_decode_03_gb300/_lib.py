@@ -1,5 +1,5 @@
 """ctypes binding of libmla_decode.so (C ABI in include/mla_decode.h), and the loader of the native
-binding through which the 8-bit cache's calls go.
+binding through which the calls of the 8-bit cache and of prompt processing go.
 
 Argument marshalling only: every computation happens in the library's CUDA kernels.
 The library must have been built (``mla_paged_decode_03_gb300.build.build()``); there is
@@ -25,7 +25,8 @@ PAD_SLOT_ID = -1
 EXPORTED = ("mla_decode_workspace_size", "mla_decode", "mla_decode_shards", "mla_decode_noalloc",
             "lse_merge", "cp_local_slot", "cp_local_slot_scatter", "cp_step_tables",
             "cp_store_q8", "mla_decode_q8_workspace_size", "mla_decode_q8",
-            "mla_decode_shards_q8",
+            "mla_decode_shards_q8", "mla_rope", "cp_rope_store", "mla_expand",
+            "mla_prefill_workspace_size", "mla_prefill", "lse_merge_v",
             "mla_get_device_status", "mla_set_decode_kernel", "mla_set_rescale_budget",
             "mla_set_wait_limit_ns", "mla_set_test_stall", "mla_last_error",
             "mla_abi_version")
@@ -104,6 +105,25 @@ def load() -> ctypes.CDLL:
         lib.mla_decode_shards_q8.restype = c_int
         lib.mla_decode_shards_q8.argtypes = head8 + [c_int, c_int, c_f, c_vp, c_vp, c_int, c_vp,
                                                      c_sz, c_vp]
+        lib.mla_rope.restype = c_int
+        lib.mla_rope.argtypes = [c_vp, c_i64, c_i64, c_vp, c_vp, c_int, c_int, c_int, c_f, c_vp,
+                                 c_i64, c_i64, c_vp]
+        lib.cp_rope_store.restype = c_int
+        lib.cp_rope_store.argtypes = [c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_vp, c_i64, c_int,
+                                      c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_f, c_vp,
+                                      c_int, c_vp, c_vp]
+        lib.mla_expand.restype = c_int
+        lib.mla_expand.argtypes = [c_vp, c_vp, c_vp, c_i64, c_vp, c_vp, c_int, c_int, c_int, c_int,
+                                   c_vp, c_int, c_int, c_vp, c_vp, c_vp]
+        lib.mla_prefill_workspace_size.restype = c_sz
+        lib.mla_prefill_workspace_size.argtypes = [c_int, c_int, c_int, c_int, c_int]
+        lib.mla_prefill.restype = c_int
+        lib.mla_prefill.argtypes = [c_vp, c_i64, c_i64, c_vp, c_i64, c_i64, c_vp, c_i64, c_vp, c_i64,
+                                    c_i64, c_vp, c_vp, c_vp, c_vp, c_int, c_int, c_int, c_int, c_int,
+                                    c_int, c_int, c_int, c_f, c_vp, c_vp, c_int, c_vp, c_sz, c_vp]
+        lib.lse_merge_v.restype = c_int
+        lib.lse_merge_v.argtypes = [c_vp, c_int, c_vp, c_int, c_int, c_int, c_int, c_vp, c_vp, c_int,
+                                    c_vp]
         lib.mla_get_device_status.restype = c_int
         lib.mla_get_device_status.argtypes = [c_vp, ctypes.POINTER(ctypes.c_uint32)]
         lib.mla_last_error.restype = ctypes.c_char_p
@@ -123,7 +143,7 @@ def load() -> ctypes.CDLL:
 
 
 def load_q8(tables_type):
-    """The native binding of the 8-bit cache's calls, bound to the library's functions;
+    """The native binding of those calls, bound to the library's functions;
     ``tables_type`` is the tuple type of cp_step_tables' result."""
     global _q8
     if _q8 is not None:
@@ -143,6 +163,9 @@ def load_q8(tables_type):
         m.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in
                  ("cp_step_tables", "cp_store_q8", "mla_decode_q8", "mla_decode_shards_q8",
                   "mla_decode_q8_workspace_size", "mla_abi_version")), check, tables_type)
+        m.bind_prompt(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in
+                        ("mla_rope", "cp_rope_store", "mla_expand", "mla_prefill",
+                         "mla_prefill_workspace_size")))
         _q8 = m
         return _q8
 

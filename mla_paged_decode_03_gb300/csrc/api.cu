@@ -1,5 +1,6 @@
 // C ABI of libmla_decode.so (declared in include/mla_decode.h): host-side argument
 // validation, error reporting and kernel launches.  Nothing here allocates memory.
+#include <limits.h>
 #include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
@@ -13,6 +14,7 @@
 
 #include "internal.h"
 #include "sm100.cuh"
+#include "tma_map.h"
 #include "../../include/mla_decode.h"
 
 namespace {
@@ -543,6 +545,266 @@ int cp_store_q8(const void* kv_new, const int32_t* ctx_lens, const int32_t* tota
   a.num_blocks = num_blocks;
   a.status = dev->status;
   cudaError_t e = mla::launch_cp_store_q8(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "%s launch: %s", fn, cudaGetErrorString(e));
+  return ok();
+}
+
+int lse_merge_v(const void* partials, int partials_fp32, const float* lses, int n_shards, int T,
+                int H, int dv, void* out, float* out_lse, int lse_base_e, mla_stream_t stream) {
+  const char* fn = "lse_merge_v";
+  if (dv != 128 && dv != MLA_HEAD_DIM_V)
+    return fail(MLA_ERR_UNSUPPORTED, "%s: dv=%d is neither 128 nor %d", fn, dv, MLA_HEAD_DIM_V);
+  if (dv == MLA_HEAD_DIM_V)
+    return lse_merge(partials, partials_fp32, lses, n_shards, T, H, out, out_lse, lse_base_e, stream);
+  if (n_shards < 1) return fail(MLA_ERR_INVALID_ARGUMENT, "%s: n_shards=%d < 1", fn, n_shards);
+  if (T < 0 || H < 1) return fail(MLA_ERR_INVALID_ARGUMENT, "%s: need T >= 0, H >= 1", fn);
+  if (T == 0) return ok();
+  if (!partials || !lses || !out)
+    return fail(MLA_ERR_INVALID_ARGUMENT, "%s: null partials/lses/out", fn);
+  if (!aligned(partials, 16) || !aligned(out, 16) || !aligned(lses, 4) ||
+      (out_lse && !aligned(out_lse, 4)))
+    return fail(MLA_ERR_INVALID_ARGUMENT, "%s: partials/out need 16-byte alignment", fn);
+  const long long rows = (long long)T * H;
+  if (rows > (1LL << 34)) return fail(MLA_ERR_UNSUPPORTED, "%s: too many rows", fn);
+  cudaError_t e = mla::launch_lse_combine128(partials, partials_fp32 != 0, lses, n_shards, rows, !lse_base_e,
+                                             lse_base_e ? 0.6931471805599453f : 1.f,
+                                             static_cast<uint16_t*>(out), out_lse, nullptr, 0, H,
+                                             reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "%s launch: %s", fn, cudaGetErrorString(e));
+  return ok();
+}
+
+// Row strides in elements of a tensor whose rows start on 16 bytes.
+static bool strides_ok(int64_t s) { return s >= 0 && s % 8 == 0 && s < (1LL << 36); }
+
+int mla_rope(const void* x, int64_t x_stride_t, int64_t x_stride_h, const int64_t* positions,
+             const int64_t* freqs, int T, int H, int half, float mscale, void* out,
+             int64_t out_stride_t, int64_t out_stride_h, mla_stream_t stream) {
+  const char* fn = "mla_rope";
+  if (T < 0 || H < 1) return fail(MLA_ERR_INVALID_ARGUMENT, "%s: need T >= 0 (%d), H >= 1 (%d)", fn, T, H);
+  if (!isfinite(mscale)) return fail(MLA_ERR_INVALID_ARGUMENT, "%s: mscale must be finite", fn);
+  if (!strides_ok(x_stride_t) || !strides_ok(x_stride_h) || !strides_ok(out_stride_t) || !strides_ok(out_stride_h))
+    return fail(MLA_ERR_INVALID_ARGUMENT, "%s: strides must be multiples of 8 elements, 0 <= stride < 2^36", fn);
+  if ((T > 1 && out_stride_t < 64) || (H > 1 && out_stride_h < 64))
+    return fail(MLA_ERR_INVALID_ARGUMENT, "%s: out's rows overlap (strides below 64 elements)", fn);
+  if (T == 0) return ok();
+  if (!x || !positions || !freqs || !out)
+    return fail(MLA_ERR_INVALID_ARGUMENT, "%s: null x/positions/freqs/out", fn);
+  if (!aligned(x, 16) || !aligned(out, 16) || !aligned(positions, 8) || !aligned(freqs, 8))
+    return fail(MLA_ERR_INVALID_ARGUMENT, "%s: misaligned pointer (x and out need 16 bytes)", fn);
+  DeviceInfo* dev = nullptr;
+  int rc = device_info(&dev);
+  if (rc != MLA_OK) return rc;
+  mla::RopeArgs a;
+  a.x = static_cast<const uint16_t*>(x);
+  a.x_t = x_stride_t;
+  a.x_h = x_stride_h;
+  a.out = static_cast<uint16_t*>(out);
+  a.out_t = out_stride_t;
+  a.out_h = out_stride_h;
+  a.positions = positions;
+  a.freqs = freqs;
+  a.T = T;
+  a.H = H;
+  a.half = half != 0;
+  a.mscale = mscale;
+  a.num_sms = dev->num_sms;
+  cudaError_t e = mla::launch_mla_rope(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "%s launch: %s", fn, cudaGetErrorString(e));
+  return ok();
+}
+
+int cp_rope_store(const void* latent, int64_t latent_stride, const void* k_rope, int64_t k_rope_stride,
+                  const int64_t* positions, const int64_t* freqs, const int32_t* block_table,
+                  int64_t bt_stride, int max_blocks, int B, int N, int block_size, int cp_size,
+                  int cp_rank, int interleave, int half, float mscale, void* kv_cache, int num_blocks,
+                  int64_t* slots, mla_stream_t stream) {
+  const char* fn = "cp_rope_store";
+  int rc = slot_args_check(fn, B, N, block_size, cp_size, cp_rank, interleave, max_blocks, bt_stride);
+  if (rc != MLA_OK) return rc;
+  if (num_blocks < 1) return fail(MLA_ERR_INVALID_ARGUMENT, "%s: num_blocks < 1", fn);
+  if (!isfinite(mscale)) return fail(MLA_ERR_INVALID_ARGUMENT, "%s: mscale must be finite", fn);
+  if (!strides_ok(latent_stride) || !strides_ok(k_rope_stride))
+    return fail(MLA_ERR_INVALID_ARGUMENT, "%s: strides must be multiples of 8 elements, 0 <= stride < 2^36", fn);
+  if ((long long)B * N == 0) return ok();
+  if (!latent || !k_rope || !positions || !freqs || !block_table || !kv_cache)
+    return fail(MLA_ERR_INVALID_ARGUMENT, "%s: null latent/k_rope/positions/freqs/block_table/kv_cache", fn);
+  if (!aligned(latent, 16) || !aligned(k_rope, 16) || !aligned(kv_cache, 16) || !aligned(positions, 8) ||
+      !aligned(freqs, 8) || !aligned(block_table, 4) || (slots && !aligned(slots, 8)))
+    return fail(MLA_ERR_INVALID_ARGUMENT,
+                "%s: misaligned pointer (latent, k_rope and kv_cache need 16 bytes)", fn);
+  DeviceInfo* dev = nullptr;
+  rc = device_info(&dev);
+  if (rc != MLA_OK) return rc;
+  mla::RopeStoreArgs a;
+  a.latent = static_cast<const uint16_t*>(latent);
+  a.k_rope = static_cast<const uint16_t*>(k_rope);
+  a.latent_t = latent_stride;
+  a.k_rope_t = k_rope_stride;
+  a.positions = positions;
+  a.freqs = freqs;
+  a.block_table = block_table;
+  a.bt_stride = bt_stride;
+  a.max_blocks = max_blocks;
+  a.B = B;
+  a.N = N;
+  a.block_size = block_size;
+  a.cp_size = cp_size;
+  a.cp_rank = cp_rank;
+  a.interleave = interleave;
+  a.half = half != 0;
+  a.mscale = mscale;
+  a.cache = static_cast<uint16_t*>(kv_cache);
+  a.num_blocks = num_blocks;
+  a.slots = slots;
+  a.num_sms = dev->num_sms;
+  a.status = dev->status;
+  cudaError_t e = mla::launch_cp_rope_store(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "%s launch: %s", fn, cudaGetErrorString(e));
+  return ok();
+}
+
+int mla_expand(const void* kv_cache, const float* kv_scales, const int32_t* block_table,
+               int64_t bt_stride, const int32_t* seq_lens, const int32_t* kv_starts, int B,
+               int block_size, int num_blocks, int max_blocks, const void* w_kv, int H, int S, void* kv,
+               void* k_rope, mla_stream_t stream) {
+  const char* fn = "mla_expand";
+  if (B < 0 || S < 0) return fail(MLA_ERR_INVALID_ARGUMENT, "%s: B, S must be >= 0", fn);
+  if (H < 1) return fail(MLA_ERR_INVALID_ARGUMENT, "%s: H=%d < 1", fn, H);
+  if (block_size < 1 || num_blocks < 1)
+    return fail(MLA_ERR_INVALID_ARGUMENT, "%s: block_size and num_blocks must be >= 1", fn);
+  if (kv_scales && block_size % MLA_Q8_GROUP != 0)
+    return fail(MLA_ERR_INVALID_ARGUMENT, "%s: block_size (%d) must be a multiple of %d", fn, block_size,
+                MLA_Q8_GROUP);
+  if (max_blocks < 1 || bt_stride < max_blocks)
+    return fail(MLA_ERR_INVALID_ARGUMENT, "%s: need 1 <= max_blocks (%d) <= bt_stride (%lld)", fn, max_blocks,
+                (long long)bt_stride);
+  if ((long long)max_blocks * block_size > (1LL << 31) - 1)
+    return fail(MLA_ERR_UNSUPPORTED, "%s: max_blocks*block_size exceeds 2^31-1", fn);
+  if (H > (1 << 22)) return fail(MLA_ERR_UNSUPPORTED, "%s: H exceeds 2^22", fn);
+  if (B == 0 || S == 0) return ok();
+  if (!kv_cache || !block_table || !seq_lens || !kv_starts || !w_kv || !kv || !k_rope)
+    return fail(MLA_ERR_INVALID_ARGUMENT, "%s: null kv_cache/block_table/seq_lens/kv_starts/w_kv/kv/k_rope", fn);
+  if (!aligned(kv_cache, 16) || !aligned(w_kv, 16) || !aligned(kv, 16) || !aligned(k_rope, 16))
+    return fail(MLA_ERR_INVALID_ARGUMENT, "%s: kv_cache, w_kv, kv and k_rope must be 16-byte aligned", fn);
+  if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(kv_starts, 4) ||
+      (kv_scales && !aligned(kv_scales, 4)))
+    return fail(MLA_ERR_INVALID_ARGUMENT, "%s: misaligned int32/float argument", fn);
+  DeviceInfo* dev = nullptr;
+  int rc = device_info(&dev);
+  if (rc != MLA_OK) return rc;
+  if (!mla::tile_maps_ok()) return fail(MLA_ERR_CUDA, "%s: the CUDA driver has no cuTensorMapEncodeTiled", fn);
+  mla::ExpandArgs a;
+  a.cache = kv_cache;
+  a.scales = kv_scales;
+  a.block_table = block_table;
+  a.bt_stride = bt_stride;
+  a.max_blocks = max_blocks;
+  a.num_blocks = num_blocks;
+  a.block_size = block_size;
+  a.seq_lens = seq_lens;
+  a.starts = kv_starts;
+  a.B = B;
+  a.w = static_cast<const uint16_t*>(w_kv);
+  a.H = H;
+  a.S = S;
+  a.kv = static_cast<uint16_t*>(kv);
+  a.k_rope = static_cast<uint16_t*>(k_rope);
+  const unsigned long long wait_ns = g_wait_ns.load();
+  a.wait_ns = wait_ns ? wait_ns : mla::sm100::kDefaultWaitNs;
+  a.num_sms = dev->num_sms;
+  a.status = dev->status;
+  cudaError_t e = mla::launch_mla_expand(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "%s launch: %s", fn, cudaGetErrorString(e));
+  return ok();
+}
+
+size_t mla_prefill_workspace_size(int T, int B, int H, int S, int num_sms) {
+  if (T <= 0 || B <= 0 || H <= 0 || S <= 0 || num_sms <= 0) return 0;
+  return mla::prefill_workspace_size(T, B, H, S, num_sms);
+}
+
+int mla_prefill(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k_nope,
+                int64_t k_stride_s, int64_t k_stride_h, const void* k_rope, int64_t k_rope_stride,
+                const void* v, int64_t v_stride_s, int64_t v_stride_h, const int32_t* cu_q_lens,
+                const int32_t* kv_starts, const int32_t* seq_lens,
+                const int32_t* causal_seqlens_global, int T, int B, int H, int S, int causal,
+                int cp_world, int cp_rank, int interleave, float scale, void* out, float* lse,
+                int lse_base_e, void* workspace, size_t workspace_bytes, mla_stream_t stream) {
+  const char* fn = "mla_prefill";
+  if (T < 0 || B < 0 || S < 0) return fail(MLA_ERR_INVALID_ARGUMENT, "%s: T, B, S must be >= 0", fn);
+  if (H < 1) return fail(MLA_ERR_INVALID_ARGUMENT, "%s: H=%d < 1", fn, H);
+  if (cp_world < 1 || cp_rank < 0 || cp_rank >= cp_world)
+    return fail(MLA_ERR_INVALID_ARGUMENT, "%s: need 0 <= cp_rank (%d) < cp_world (%d)", fn, cp_rank, cp_world);
+  if (interleave < 1) return fail(MLA_ERR_INVALID_ARGUMENT, "%s: interleave=%d < 1", fn, interleave);
+  if ((long long)cp_world * interleave > (1LL << 31) - 1)
+    return fail(MLA_ERR_UNSUPPORTED, "%s: cp_world*interleave exceeds 2^31-1", fn);
+  if (!isfinite(scale) || !(scale > 0.f))
+    return fail(MLA_ERR_INVALID_ARGUMENT, "%s: scale must be finite and > 0", fn);
+  const struct {
+    int64_t stride;
+    int size;
+  } dims[] = {{q_stride_t, T}, {q_stride_h, H}, {k_stride_s, S}, {k_stride_h, H}, {k_rope_stride, S},
+              {v_stride_s, S}, {v_stride_h, H}};
+  for (const auto& d : dims)
+    if (!strides_ok(d.stride) || (d.size > 1 && d.stride == 0))
+      return fail(MLA_ERR_INVALID_ARGUMENT, "%s: strides must be multiples of 8 elements, 0 < stride < 2^36", fn);
+  if (T == 0 || B == 0) return ok();
+  if (S < 1) return fail(MLA_ERR_INVALID_ARGUMENT, "%s: S=0 key rows (a request without keys needs one row of memory)", fn);
+  if (!q || !k_nope || !k_rope || !v || !cu_q_lens || !kv_starts || !seq_lens || !out)
+    return fail(MLA_ERR_INVALID_ARGUMENT, "%s: null q/k_nope/k_rope/v/cu_q_lens/kv_starts/seq_lens/out", fn);
+  if (causal_seqlens_global == nullptr && cp_world != 1 && causal)
+    return fail(MLA_ERR_INVALID_ARGUMENT, "%s: causal_seqlens_global is required when cp_world > 1", fn);
+  if (!aligned(q, 16) || !aligned(k_nope, 16) || !aligned(k_rope, 16) || !aligned(v, 16) || !aligned(out, 16))
+    return fail(MLA_ERR_INVALID_ARGUMENT, "%s: q, k_nope, k_rope, v and out must be 16-byte aligned", fn);
+  if (!aligned(cu_q_lens, 4) || !aligned(kv_starts, 4) || !aligned(seq_lens, 4) ||
+      !aligned(causal_seqlens_global, 4) || !aligned(lse, 4))
+    return fail(MLA_ERR_INVALID_ARGUMENT, "%s: misaligned int32/float argument", fn);
+  if (workspace && !aligned(workspace, 256))
+    return fail(MLA_ERR_INVALID_ARGUMENT, "%s: workspace must be 256-byte aligned", fn);
+  if (!mla::prefill_grid_ok(T, B, H)) return fail(MLA_ERR_UNSUPPORTED, "%s: H=%d exceeds 65535", fn, H);
+  if (S > INT_MAX - 256 || T > INT_MAX - 512)
+    return fail(MLA_ERR_UNSUPPORTED, "%s: T or S too close to 2^31", fn);
+  DeviceInfo* dev = nullptr;
+  int rc = device_info(&dev);
+  if (rc != MLA_OK) return rc;
+  if (!mla::tile_maps_ok()) return fail(MLA_ERR_CUDA, "%s: the CUDA driver has no cuTensorMapEncodeTiled", fn);
+  mla::PrefillArgs a = {};
+  a.cu = cu_q_lens;
+  a.starts = kv_starts;
+  a.seq_lens = seq_lens;
+  a.gseq = causal_seqlens_global;
+  a.T = T;
+  a.B = B;
+  a.H = H;
+  a.S = S;
+  a.causal = causal ? 1 : 0;
+  a.cp = cp_world;
+  a.rank = cp_rank;
+  a.il = interleave;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.lse_mul = lse_base_e ? 0.6931471805599453f : 1.f;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  const unsigned long long wait_ns = g_wait_ns.load();
+  a.wait_ns = wait_ns ? wait_ns : mla::sm100::kDefaultWaitNs;
+  a.num_sms = dev->num_sms;
+  a.status = dev->status;
+  mla::PrefillTensors x;
+  x.q = q;
+  x.q_t = q_stride_t;
+  x.q_h = q_stride_h;
+  x.k_nope = k_nope;
+  x.k_s = k_stride_s;
+  x.k_h = k_stride_h;
+  x.k_rope = k_rope;
+  x.r_s = k_rope_stride;
+  x.v = v;
+  x.v_s = v_stride_s;
+  x.v_h = v_stride_h;
+  x.workspace = workspace;
+  x.workspace_bytes = workspace_bytes;
+  cudaError_t e = mla::launch_mla_prefill(a, x, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "%s launch: %s", fn, cudaGetErrorString(e));
   return ok();
 }

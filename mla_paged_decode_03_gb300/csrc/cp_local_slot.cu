@@ -19,6 +19,7 @@
 // the new rows to its slot (512 contiguous bytes per warp instruction); positions this rank
 // does not own are neither read nor written.
 #include "internal.h"
+#include "slots.cuh"
 #include "../../include/mla_decode.h"
 
 namespace mla {
@@ -26,54 +27,6 @@ namespace {
 
 constexpr int kRowBytes = 576 * 2;
 constexpr int kRowChunks = kRowBytes / 16;     // 72 16-byte pieces per KV row
-
-struct SlotParams {
-  const int32_t* block_table;
-  int64_t bt_stride;
-  int max_blocks, block_size, cp_size, cp_rank, interleave;
-  unsigned int vbs;          // block_size * cp_size (checked < 2^31 on the host)
-  FastDiv div_vbs, div_il, div_cp;
-  unsigned int* status;
-};
-
-__device__ __forceinline__ unsigned int fdiv(unsigned int n, const FastDiv& f) {
-  return f.d == 1u ? n : (unsigned int)__umul64hi(f.m, (unsigned long long)n);
-}
-
-// Slot of `pos` on this rank (>= 0), or MLA_PAD_SLOT_ID if the rank does not own it, the
-// position is negative, or its virtual block lies past the table (then `bad` is set and
-// the table is not read).
-__device__ __forceinline__ long long map_one(long long pos, int b, const SlotParams& p,
-                                             bool& bad) {
-  if (pos < 0) return MLA_PAD_SLOT_ID;
-  long long vb;
-  unsigned int off;
-  if (pos <= 0xffffffffLL) {
-    const unsigned int q = fdiv((unsigned int)pos, p.div_vbs);
-    vb = q;
-    off = (unsigned int)pos - q * p.vbs;
-  } else {
-    vb = pos / p.vbs;
-    off = (unsigned int)(pos - vb * p.vbs);
-  }
-  if (vb >= p.max_blocks) {
-    bad = true;
-    return MLA_PAD_SLOT_ID;
-  }
-  unsigned int local;
-  if (p.cp_size == 1) {
-    local = off;
-  } else {
-    // segment of `interleave` positions, its owner (segment mod cp) and its round
-    const unsigned int seg = fdiv(off, p.div_il);
-    const unsigned int rin = off - seg * (unsigned int)p.interleave;
-    const unsigned int rnd = fdiv(seg, p.div_cp);
-    if ((int)(seg - rnd * (unsigned int)p.cp_size) != p.cp_rank) return MLA_PAD_SLOT_ID;
-    local = rnd * (unsigned int)p.interleave + rin;
-  }
-  const long long page = __ldg(p.block_table + (long long)b * p.bt_stride + vb);
-  return page * p.block_size + local;
-}
 
 // One thread per pair of positions; rows of even length and 16-byte aligned pointers.
 __global__ void __launch_bounds__(256) cp_local_slot_vec2(const longlong2* __restrict__ pos,
@@ -167,25 +120,6 @@ __global__ void __launch_bounds__(256) cp_local_slot_scatter_kernel(
   if (__any_sync(0xffffffffu, bad_page) && lane == 0) atomicOr(p.status, MLA_STATUS_BAD_PAGE);
 }
 
-SlotParams make_params(const int32_t* block_table, int64_t bt_stride, int max_blocks,
-                       int block_size, int cp_size, int cp_rank, int interleave,
-                       unsigned int* status) {
-  SlotParams p;
-  p.block_table = block_table;
-  p.bt_stride = bt_stride;
-  p.max_blocks = max_blocks;
-  p.block_size = block_size;
-  p.cp_size = cp_size;
-  p.cp_rank = cp_rank;
-  p.interleave = interleave;
-  p.vbs = (unsigned int)block_size * (unsigned int)cp_size;
-  p.div_vbs = make_fastdiv(p.vbs);
-  p.div_il = make_fastdiv((unsigned int)interleave);
-  p.div_cp = make_fastdiv((unsigned int)cp_size);
-  p.status = status;
-  return p;
-}
-
 int sm_count() {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -205,8 +139,8 @@ cudaError_t launch_cp_local_slot(const int64_t* positions, const int32_t* block_
                                  int64_t* slots, unsigned int* status, cudaStream_t stream) {
   const long long total = (long long)B * N;
   if (total == 0) return cudaSuccess;
-  const SlotParams p = make_params(block_table, bt_stride, max_blocks, block_size, cp_size,
-                                   cp_rank, interleave, status);
+  const SlotParams p = make_slot_params(block_table, bt_stride, max_blocks, block_size, cp_size,
+                                        cp_rank, interleave, status);
   const int sms = sm_count();
   const bool vec = (N % 2 == 0) && ((uintptr_t)positions % 16 == 0) &&
                    ((uintptr_t)slots % 16 == 0);
@@ -235,8 +169,8 @@ cudaError_t launch_cp_local_slot_scatter(const int64_t* positions, const uint16_
                                          cudaStream_t stream) {
   const long long total = (long long)B * N;
   if (total == 0) return cudaSuccess;
-  const SlotParams p = make_params(block_table, bt_stride, max_blocks, block_size, cp_size,
-                                   cp_rank, interleave, status);
+  const SlotParams p = make_slot_params(block_table, bt_stride, max_blocks, block_size, cp_size,
+                                        cp_rank, interleave, status);
   const int sms = sm_count();
   long long blocks = (total + 255) / 256;        // 8 warps per block, 32 positions per warp
   const long long cap = (long long)sms * 16;

@@ -174,4 +174,84 @@ struct StoreQ8Args {
 };
 cudaError_t launch_cp_store_q8(const StoreQ8Args& a, cudaStream_t stream);
 
+// Rotation of a rope part (mla_rope.cu): x and out [T, H, 64], strides in elements.
+struct RopeArgs {
+  const uint16_t* x;
+  int64_t x_t, x_h;
+  uint16_t* out;
+  int64_t out_t, out_h;
+  const int64_t *positions, *freqs;      // [T], [32] (units of 2^-64 turns)
+  int T, H;
+  bool half;
+  float mscale;
+  int num_sms;
+};
+cudaError_t launch_mla_rope(const RopeArgs& a, cudaStream_t stream);
+
+// New tokens into the bf16 cache, their rope part rotated (mla_rope.cu).
+struct RopeStoreArgs {
+  const uint16_t *latent, *k_rope;       // [B*N] rows of 512 and 64
+  int64_t latent_t, k_rope_t;            // row strides, elements
+  const int64_t *positions, *freqs;
+  const int32_t* block_table;
+  int64_t bt_stride;
+  int max_blocks, B, N, block_size, cp_size, cp_rank, interleave;
+  bool half;
+  float mscale;
+  uint16_t* cache;
+  int num_blocks;
+  int64_t* slots;
+  int num_sms;
+  unsigned int* status;
+};
+cudaError_t launch_cp_rope_store(const RopeStoreArgs& a, cudaStream_t stream);
+
+// Keys and values of all heads from the pages (mla_expand.cu).
+struct ExpandArgs {
+  const void* cache;                     // bf16, or e4m3 with scales
+  const float* scales;
+  const int32_t* block_table;
+  int64_t bt_stride;
+  int max_blocks, num_blocks, block_size;
+  const int32_t *seq_lens, *starts;      // [B]
+  int B;
+  const uint16_t* w;                     // [H, 256, 512]
+  int H, S;
+  uint16_t *kv, *k_rope;                 // [H, S, 256], [S, 64]
+  unsigned long long wait_ns;
+  int num_sms;
+  unsigned int* status;
+};
+cudaError_t launch_mla_expand(const ExpandArgs& a, cudaStream_t stream);
+
+// Attention of ragged chunks over expanded keys (mla_prefill.cu).
+struct PrefillArgs {
+  const int32_t *cu, *starts, *seq_lens, *gseq;   // gseq may be null: seq_lens
+  int T, B, H, S, causal, cp, rank, il;
+  float scale_log2, lse_mul;
+  uint16_t* out;                         // [T, H, 128]
+  float* lse;                            // [T, H] or null
+  unsigned long long wait_ns;
+  int num_sms;
+  unsigned int* status;
+  int splits;                            // set by the launch, with its scratch
+  float *ws_o, *ws_lse;
+};
+struct PrefillTensors {
+  const void *q, *k_nope, *k_rope, *v;
+  int64_t q_t, q_h, k_s, k_h, r_s, v_s, v_h;      // strides, elements
+  void* workspace;
+  size_t workspace_bytes;
+};
+bool prefill_grid_ok(int T, int B, int H);
+size_t prefill_workspace_size(int T, int B, int H, int S, int num_sms);
+cudaError_t launch_mla_prefill(PrefillArgs a, const PrefillTensors& x, cudaStream_t stream);
+
+// launch_lse_combine for rows of 128 values.  With cu ([B+1], may be null), only rows
+// cu[0]*H .. cu[B]*H - 1 are read and written.
+cudaError_t launch_lse_combine128(const void* partials, bool partials_fp32, const float* lses, int n,
+                                  long long rows, bool in_log2, float out_lse_mul, uint16_t* out,
+                                  float* out_lse, const int32_t* cu, int B, int H,
+                                  cudaStream_t stream);
+
 }  // namespace mla

@@ -171,7 +171,78 @@ lse_combine_split_kernel(const T* __restrict__ partials, const float* __restrict
     out_lse[row] = wsum > 0.f ? (m2 + log2f(wsum)) * out_lse_mul : -INFINITY;
 }
 
+// Rows of 128 values (the expanded form's outputs): half a warp a row, eight values a lane, four
+// shards in flight.
+constexpr int kDv128 = 128;
+
+template <typename T>
+__global__ void __launch_bounds__(kWarps * 32)
+lse_combine128_kernel(const T* __restrict__ partials, const float* __restrict__ lses, int n,
+                      long long rows, float lse_to_log2, float out_lse_mul,
+                      __nv_bfloat16* __restrict__ out, float* __restrict__ out_lse,
+                      const int32_t* __restrict__ cu, int B, int H) {
+  // launched as a dependent of the kernel that wrote the partials
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31, sub = lane & 15;
+  const long long row = ((long long)blockIdx.x * kWarps + (threadIdx.x >> 5)) * 2 + (lane >> 4);
+  if (row >= rows) return;
+  if (cu != nullptr && (row < (long long)__ldg(cu) * H || row >= (long long)__ldg(cu + B) * H)) return;
+  const unsigned both = 0xffffu << (lane & 16);
+
+  float m2 = -INFINITY;                       // max LSE, in log2 units
+  for (int s = sub; s < n; s += 16) m2 = fmaxf(m2, __ldg(lses + s * rows + row) * lse_to_log2);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) m2 = fmaxf(m2, __shfl_xor_sync(both, m2, o));
+
+  float acc[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) acc[k] = 0.f;
+  float wsum = 0.f;
+  if (m2 != -INFINITY) {
+    for (int s0 = 0; s0 < n; s0 += 4) {
+      float w[4], v[4][8];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        w[u] = s0 + u < n ? exp2f(__ldg(lses + (s0 + u) * rows + row) * lse_to_log2 - m2) : 0.f;
+        if (w[u] != 0.f)                      // empty shard: weight 0, partial unread
+          load8(partials + ((s0 + u) * rows + row) * (long long)kDv128 + 8 * sub, v[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (w[u] != 0.f) {
+          wsum += w[u];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) acc[k] = fmaf(w[u], v[u][k], acc[k]);
+        }
+    }
+  }
+  const float inv = wsum != 0.f ? 1.f / wsum : 0.f;
+  uint4 packed;
+  __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&packed);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) h[k] = __floats2bfloat162_rn(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+  *reinterpret_cast<uint4*>(out + row * kDv128 + 8 * sub) = packed;
+  if (out_lse != nullptr && sub == 0)
+    out_lse[row] = wsum != 0.f ? (m2 + log2f(wsum)) * out_lse_mul : -INFINITY;
+}
+
 }  // namespace
+
+cudaError_t launch_lse_combine128(const void* partials, bool partials_fp32, const float* lses, int n,
+                                  long long rows, bool in_log2, float out_lse_mul, uint16_t* out,
+                                  float* out_lse, const int32_t* cu, int B, int H,
+                                  cudaStream_t stream) {
+  if (rows == 0) return cudaSuccess;
+  const float k = in_log2 ? 1.0f : 1.4426950408889634f;
+  __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(out);
+  DependentLaunch dl(dim3((unsigned)((rows + 2 * kWarps - 1) / (2 * kWarps))), dim3(kWarps * 32), stream);
+  if (partials_fp32)
+    return cudaLaunchKernelEx(&dl.cfg, lse_combine128_kernel<float>, static_cast<const float*>(partials), lses,
+                              n, rows, k, out_lse_mul, o, out_lse, cu, B, H);
+  return cudaLaunchKernelEx(&dl.cfg, lse_combine128_kernel<__nv_bfloat16>,
+                            static_cast<const __nv_bfloat16*>(partials), lses, n, rows, k, out_lse_mul, o,
+                            out_lse, cu, B, H);
+}
 
 cudaError_t launch_lse_combine(const void* partials, bool partials_fp32, const float* lses,
                                int n, long long rows, long long shard_stride_rows,
