@@ -472,8 +472,8 @@ int mla_expand(const void* kv_cache, const float* kv_scales, const int32_t* bloc
  *   out          bf16 [T, H, 128], 16-byte aligned;  lse  float [T, H] or NULL.
  *   workspace    scratch of mla_prefill_workspace_size bytes, 256-byte aligned, or NULL / 0: without
  *                all of it the keys of few rows are not split over the SMs.
- *   T, B, S >= 0 (S >= 1 with any row), 1 <= H <= 65535; cp_world, cp_rank, interleave, scale as
- *   mla_decode (interleave need not divide anything here).
+ *   T, B, S >= 0 (S >= 1 with any row), H >= 1, (T/256 + min(B, T)) * H below 2^31; cp_world,
+ *   cp_rank, interleave, scale as mla_decode (interleave need not divide anything here).
  * Values of a request's keys must be finite where any of its rows sees them: a row that does not
  * see a key may still get NaN from a value of it that is NaN or infinite.  Rows behind the last key
  * may hold anything.

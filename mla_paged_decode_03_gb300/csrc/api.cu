@@ -762,7 +762,7 @@ int mla_prefill(const void* q, int64_t q_stride_t, int64_t q_stride_h, const voi
     return fail(MLA_ERR_INVALID_ARGUMENT, "%s: misaligned int32/float argument", fn);
   if (workspace && !aligned(workspace, 256))
     return fail(MLA_ERR_INVALID_ARGUMENT, "%s: workspace must be 256-byte aligned", fn);
-  if (!mla::prefill_grid_ok(T, B, H)) return fail(MLA_ERR_UNSUPPORTED, "%s: H=%d exceeds 65535", fn, H);
+  if (!mla::prefill_grid_ok(T, B, H)) return fail(MLA_ERR_UNSUPPORTED, "%s: (T/256 + B) * H exceeds 2^31-1", fn);
   if (S > INT_MAX - 256 || T > INT_MAX - 512)
     return fail(MLA_ERR_UNSUPPORTED, "%s: T or S too close to 2^31", fn);
   DeviceInfo* dev = nullptr;

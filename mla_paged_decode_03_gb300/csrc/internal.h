@@ -234,7 +234,8 @@ struct PrefillArgs {
   unsigned long long wait_ns;
   int num_sms;
   unsigned int* status;
-  int splits;                            // set by the launch, with its scratch
+  int tiles, group;                      // set by the launch: row tiles, heads that run at a time,
+  int splits;                            // parts of the keys, with their scratch
   float *ws_o, *ws_lse;
 };
 struct PrefillTensors {

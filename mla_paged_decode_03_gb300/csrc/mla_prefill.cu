@@ -52,7 +52,10 @@ constexpr int kTile = 128;                    // keys a tile
 constexpr int kSlotBytes = 16384;
 constexpr int kSlots = 8;
 constexpr int kQChunks = 3, kKSlots = 3, kVSlots = 2;
-constexpr int kThreads = 384;                 // warp 0 TMA, 1 MMA; 4-7 and 8-11 softmax of a stream
+// Group 2j is tile j's keys, group 2j + 1 its values; the slots they take one after another make
+// group n's slots free once group n - 3 has been used.
+constexpr int kGroups = 3;
+constexpr int kThreads = 384;                 // warp 0 TMA; 1, 2 MMA and 4-7, 8-11 softmax of a stream
 constexpr float kRise = 8.0f;                 // log2 units that a maximum may rise before O is rescaled
 
 constexpr int kOffQ = 0;                                     // 2 x 48 KB, then the output's staging
@@ -63,13 +66,14 @@ constexpr int kSmemBytes = kOffMisc + 128 + 1024;
 
 enum Bar : int {
   B_QFULL = 0,                   // [2]
-  B_FULL = 2,                    // [8]
-  B_EMPTY = B_FULL + kSlots,     // [8]
-  B_SFULL = B_EMPTY + kSlots,    // [2] S of a stream's tile computed (and all products before)
-  B_PFULL = B_SFULL + 2,         // [2] P in tensor memory, O rescaled
-  B_OFULL = B_PFULL + 2,         // [2] the stream's last product is done
-  B_DRAIN = B_OFULL + 2,
-  B_COUNT = B_DRAIN + 1
+  B_FULL = 2,                    // [3] keys or values of a tile
+  B_EMPTY = B_FULL + kGroups,    // [3] both streams have used them
+  B_SFULL = B_EMPTY + kGroups,   // [2] S of a stream's tile computed (and all products before)
+  B_PFULL = B_SFULL + 2,         // [2][2] P of half a tile in tensor memory, O rescaled
+  B_OFULL = B_PFULL + 4,         // [2] the stream's last product is done
+  B_TURN = B_OFULL + 2,          // [2] a stream's products may be issued
+  B_DRAIN = B_TURN + 2,          // [2]
+  B_COUNT = B_DRAIN + 2
 };
 static_assert(B_COUNT * 8 <= 256, "barriers");
 
@@ -165,14 +169,34 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
+// Two single-precision multiply-adds in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
 mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap rmap, const __grid_constant__ CUtensorMap vmap,
                    const __grid_constant__ PrefillArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sp = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int head = blockIdx.y;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  // blocks of one group of heads after another; in a group all heads' longest tiles first
+  const unsigned per = (unsigned)a.tiles * a.group;
+  const unsigned grp = blockIdx.x / per, in = blockIdx.x - grp * per;
+  const unsigned heads = min((unsigned)a.group, (unsigned)a.H - grp * a.group);
+  const int tile_x = (int)(in / heads), head = (int)(grp * a.group + in % heads);
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(sp + kOffMisc);
   Unit* su = reinterpret_cast<Unit*>(sp + kOffMisc + 16);
   Ctx s;
@@ -183,7 +207,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
 
   if (warp == 0) {
     Unit u;
-    const bool any = find_unit(a, blockIdx.x, lane, u);
+    const bool any = find_unit(a, tile_x, lane, u);
     if (lane == 0) {
       misc[2] = any;
       if (any) *su = u;
@@ -191,16 +215,16 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
   } else if (warp == 1) {
     tmem_alloc(s.base + kOffMisc, 512);
     tmem_relinquish();
-  } else if (tid == 64) {
+  } else if (tid == 96) {
     *s.abort = 0;
     for (int i = 0; i < B_COUNT; ++i)
-      mbar_init(s.bar(i), i == B_PFULL || i == B_PFULL + 1 ? 4 : 1);
+      mbar_init(s.bar(i), i >= B_PFULL && i < B_PFULL + 4 ? 4 : i >= B_EMPTY && i < B_EMPTY + kGroups ? 2 : 1);
     fence_mbar_init();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = misc[0];
+  const uint32_t tmem = __shfl_sync(0xffffffffu, misc[0], 0);
   const bool any = misc[2] != 0;
 
   if (any) {
@@ -214,8 +238,8 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
     }
     if (a.splits > 1) {
       const int most = max(tiles[0], tiles[1]);
-      begin = (int)((long long)most * blockIdx.z / a.splits);
-      const int end = (int)((long long)most * (blockIdx.z + 1) / a.splits);
+      begin = (int)((long long)most * blockIdx.y / a.splits);
+      const int end = (int)((long long)most * (blockIdx.y + 1) / a.splits);
       tiles[0] = max(min(tiles[0], end), begin);
       tiles[1] = max(min(tiles[1], end), begin);
     }
@@ -231,100 +255,113 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
             tma_load_3d_warp(s.base + kOffQ + (t * kQChunks + c) * kSlotBytes, &qmap, 64 * c, head,
                              un.row0 + un.first + t * kM, s.bar(B_QFULL + t));
         }
-      int st = 0;
+      int sl = 0, g = 0, issued = 0;
       uint32_t par = 1;
-      int issued = 0;
       bool ok = true;
       for (int j = begin; j < most && ok; ++j) {
         const int y = un.key0 + j * kTile;
 #pragma unroll
-        for (int c = 0; c < kKSlots + kVSlots; ++c) {
-          ok = s.wait(B_EMPTY + st, par);
+        for (int part = 0; part < 2; ++part) {
+          ok = s.wait(B_EMPTY + g, par);
           if (!ok) break;
-          const uint32_t fb = s.bar(B_FULL + st), dst = s.base + kOffRing + st * kSlotBytes;
-          mbar_arrive_expect_tx_warp(fb, kSlotBytes);
-          if (c < 2) {
-            tma_load_3d_warp(dst, &kmap, 64 * c, head, y, fb);
-          } else if (c == 2) {
-            tma_load_2d_warp(dst, &rmap, 0, y, fb);
-          } else {
-            tma_load_3d_warp(dst, &vmap, 0, head, y + 64 * (c - 3), fb);
-            tma_load_3d_warp(dst + kSlotBytes / 2, &vmap, 64, head, y + 64 * (c - 3), fb);
+          const uint32_t fb = s.bar(B_FULL + g);
+          mbar_arrive_expect_tx_warp(fb, (part == 0 ? kKSlots : kVSlots) * kSlotBytes);
+#pragma unroll
+          for (int c = 0; c < (part == 0 ? kKSlots : kVSlots); ++c) {
+            const uint32_t dst = s.base + kOffRing + sl * kSlotBytes;
+            if (part == 1) {
+              tma_load_3d_warp(dst, &vmap, 0, head, y + 64 * c, fb);
+              tma_load_3d_warp(dst + kSlotBytes / 2, &vmap, 64, head, y + 64 * c, fb);
+            } else if (c < 2) {
+              tma_load_3d_warp(dst, &kmap, 64 * c, head, y, fb);
+            } else {
+              tma_load_2d_warp(dst, &rmap, 0, y, fb);
+            }
+            sl = (sl + 1) % kSlots;
           }
           ++issued;
-          if (++st == kSlots) {
-            st = 0;
+          if (++g == kGroups) {
+            g = 0;
             par ^= 1u;
           }
         }
       }
       if (*s.abort) {
         // let loads in flight land before the block ends
-        for (int m = issued > kSlots ? issued - kSlots : 0; m < issued; ++m)
-          mbar_wait_drain(s.bar(B_FULL + m % kSlots), (uint32_t)((m / kSlots) & 1));
+        for (int m = issued > kGroups ? issued - kGroups : 0; m < issued; ++m)
+          mbar_wait_drain(s.bar(B_FULL + m % kGroups), (uint32_t)((m / kGroups) & 1));
 #pragma unroll
         for (int t = 0; t < 2; ++t)
           if (tiles[t] > begin) mbar_wait_drain(s.bar(B_QFULL + t), 0);
       }
-    } else if (warp == 1) {
-      // ---- products -----------------------------------------------------------------------
+    } else if (warp <= 2) {
+      // ---- products of a stream, the streams in turn ------------------------------------------
+      const int t = warp - 1;
       const uint32_t id_qk = idesc_bf16(kM, kTile, false, false), id_pv = idesc_bf16(kM, 128, false, true);
-      bool ok = true;
-      int kq = 0;                               // slots used before this tile's keys
-      for (int j = begin; j <= most && ok; ++j, kq += kKSlots + kVSlots) {
-        const int vq = kq - kVSlots;            // tile j - 1's values lie right before
-        const int left = un.keys - (j - 1) * kTile;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (j > begin && j - 1 < tiles[t]) {
-            // PV of tile j - 1
-            ok = s.wait(B_PFULL + t, (uint32_t)((j - 1 - begin) & 1));
-            for (int h = 0; h < kVSlots && ok; ++h) {
-              const int sl = (vq + h) % kSlots;
-              ok = s.wait(B_FULL + sl, (uint32_t)((vq + h) / kSlots & 1));
-              if (!ok) break;
-              uint8_t* v = sp + kOffRing + sl * kSlotBytes;
-              if (left < 64 * h + 64) {
-                // rows behind the last key: P is zero there, the values may be anything
-                for (int i = max(left - 64 * h, 0) * 8 + lane; i < 64 * 8; i += 32) {
-                  *reinterpret_cast<uint4*>(v + i * 16) = make_uint4(0, 0, 0, 0);
-                  *reinterpret_cast<uint4*>(v + kSlotBytes / 2 + i * 16) = make_uint4(0, 0, 0, 0);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
+      const uint64_t qd = smem_desc(s.base + kOffQ + t * kQChunks * kSlotBytes, 16, 1024, kSwizzle128B);
+      const uint64_t kd = smem_desc(s.base + kOffRing, 16, 1024, kSwizzle128B);
+      const uint64_t vd = smem_desc(s.base + kOffRing, kSlotBytes / 2, 1024, kSwizzle128B);
+      constexpr unsigned kStep = kSlotBytes / 16;
+      const uint32_t ds = tmem + t * 128, d_o = ds + 256;
+      const int mine = tiles[t];
+      bool ok = begin >= mine || s.wait(B_QFULL + t, 0);
+      unsigned sl = 0;                          // slot of tile j's keys
+      int g = 0;                                // its group's barriers, and their parity
+      uint32_t par = 0, ph = 0;                 // parity of the tile before, and of the turn
+      for (int j = begin; j <= most && ok; ++j) {
+        const int gv = g == 0 ? kGroups - 1 : g - 1;      // tile j - 1's values: the group and slots before
+        const unsigned v0 = (sl + kSlots - 2) % kSlots, v1 = (sl + kSlots - 1) % kSlots;
+        const bool pv = j > begin && j <= mine, qk = j < mine;
+        if (pv) {
+          ok = s.wait(B_FULL + gv, g == 0 ? par ^ 1u : par);
+          const int left = un.keys - (j - 1) * kTile;
+          if (ok && left < kTile) {
+            // rows behind the last key: P is zero there, the values may be anything
+            for (int h = 0; h < kVSlots; ++h) {
+              uint8_t* v = sp + kOffRing + (h == 0 ? v0 : v1) * kSlotBytes;
+              for (int i = max(left - 64 * h, 0) * 8 + lane; i < 64 * 8; i += 32) {
+                *reinterpret_cast<uint4*>(v + i * 16) = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(v + kSlotBytes / 2 + i * 16) = make_uint4(0, 0, 0, 0);
               }
-              tc_fence_after();
-              mma4_ts_mn_warp(tmem + 256 + t * 128, tmem + t * 128 + h * 32,
-                              smem_desc(s.base + kOffRing + sl * kSlotBytes, kSlotBytes / 2, 1024, kSwizzle128B),
-                              id_pv, h != 0 || j - 1 > begin);
             }
-            if (ok && j == tiles[t]) mma_commit_warp(s.bar(B_OFULL + t));
+            fence_proxy_async_smem();
+            __syncwarp();
           }
-          if (ok && j < tiles[t]) {
-            // QK of tile j
-            if (j == begin) ok = s.wait(B_QFULL + t, 0);
-            for (int c = 0; c < kKSlots && ok; ++c) {
-              const int sl = (kq + c) % kSlots;
-              ok = s.wait(B_FULL + sl, (uint32_t)((kq + c) / kSlots & 1));
-              if (!ok) break;
-              tc_fence_after();
-              mma4_ss_warp(tmem + t * 128,
-                           smem_desc(s.base + kOffQ + (t * kQChunks + c) * kSlotBytes, 16, 1024, kSwizzle128B),
-                           smem_desc(s.base + kOffRing + sl * kSlotBytes, 16, 1024, kSwizzle128B), id_qk, c != 0);
-            }
-            if (ok) mma_commit_warp(s.bar(B_SFULL + t));
-          }
-          if (!ok) break;
+          ok = ok && s.wait(B_PFULL + 2 * t, ph ^ 1u);
         }
+        // the other stream's products are issued
+        if (t == 1 || j > begin) ok = ok && s.wait(B_TURN + t, t == 1 ? ph : ph ^ 1u);
         if (!ok) break;
-        // both streams have used tile j - 1's values and tile j's keys
-        if (j > begin)
-          for (int h = 0; h < kVSlots; ++h) mma_commit_warp(s.bar(B_EMPTY + (vq + h) % kSlots));
-        if (j < most)
-          for (int c = 0; c < kKSlots; ++c) mma_commit_warp(s.bar(B_EMPTY + (kq + c) % kSlots));
+        tc_fence_after();
+        if (pv) {
+          mma4_ts_mn_warp(d_o, ds, vd + v0 * kStep, id_pv, j - 1 > begin);
+          ok = s.wait(B_PFULL + 2 * t + 1, ph ^ 1u);
+          if (!ok) break;
+          tc_fence_after();
+          mma4_ts_mn_warp(d_o, ds + 32, vd + v1 * kStep, id_pv, 1);
+        }
+        if (j > begin) mma_commit_warp(s.bar(B_EMPTY + gv));
+        if (qk) {
+          ok = s.wait(B_FULL + g, par);
+          if (!ok) break;
+          tc_fence_after();
+          mma12_ss_warp(ds, qd, kd + sl * kStep, kd + (sl + 1) % kSlots * kStep, kd + (sl + 2) % kSlots * kStep, id_qk);
+          mma_commit_warp(s.bar(B_SFULL + t));
+        }
+        if (lane == 0) mbar_arrive(s.bar(B_TURN + (t ^ 1)));
+        __syncwarp();
+        if (pv && j == mine) mma_commit_warp(s.bar(B_OFULL + t));
+        if (j < most) mma_commit_warp(s.bar(B_EMPTY + g));
+        sl = (sl + kKSlots + kVSlots) % kSlots;
+        ph ^= 1u;
+        g += 2;
+        if (g >= kGroups) {
+          g -= kGroups;
+          par ^= 1u;
+        }
       }
-      mma_commit_warp(s.bar(B_DRAIN));
-      mbar_wait_drain(s.bar(B_DRAIN), 0);
+      mma_commit_warp(s.bar(B_DRAIN + t));
+      mbar_wait_drain(s.bar(B_DRAIN + t), 0);
     } else if (warp >= 4) {
       // ---- softmax: thread = row ------------------------------------------------------------
       const int t = (warp >> 2) - 1, q = warp & 3;
@@ -351,9 +388,11 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
         }
         float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int c = 4; c < 128; c += 4)
+        for (int c = 4; c < 124; c += 8)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], x[c + k]);
+          for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], x[c + 2 * k], x[c + 2 * k + 1]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], x[124 + k]);
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
         // the reference moves where a maximum rose too far (from nothing at the first)
         const bool moves = top > m + kRise;
@@ -373,25 +412,27 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
             }
         }
         const float ref = m == -INFINITY ? 0.f : m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const float2 mul = make_float2(a.scale_log2, a.scale_log2), sub = make_float2(-ref, -ref);
+        const float2 one = make_float2(1.f, 1.f);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        // P of 64 keys, then of the other 64: the first half's product starts meanwhile
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int h = 0; h < 2; ++h) {
           uint32_t pk[32];
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
-            const float p0 = exp2_fast(fmaf(x[64 * c + 2 * k], a.scale_log2, -ref));
-            const float p1 = exp2_fast(fmaf(x[64 * c + 2 * k + 1], a.scale_log2, -ref));
-            sum[2 * (k & 1)] += p0;
-            sum[2 * (k & 1) + 1] += p1;
-            pk[k] = pack(p0, p1);
+            const float2 e = fma2(make_float2(x[64 * h + 2 * k], x[64 * h + 2 * k + 1]), mul, sub);
+            const float2 p = make_float2(exp2_fast(e.x), exp2_fast(e.y));
+            sum[k & 1] = fma2(p, one, sum[k & 1]);
+            pk[k] = pack(p.x, p.y);
           }
-          tmem_st32(ts + 32 * c, pk);
+          tmem_st32(ts + 32 * h, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s.bar(B_PFULL + 2 * t + h));
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(s.bar(B_PFULL + t));
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
       if (ok && n_tiles > begin) {
         ok = s.wait(B_OFULL + t, 0);
@@ -433,7 +474,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
                   *reinterpret_cast<const uint4*>(stage + r * 256 + ((ch ^ (r & 7)) << 4));
           }
         } else {
-          const long long part = (long long)blockIdx.z * a.T * a.H;
+          const long long part = (long long)blockIdx.y * a.T * a.H;
           if (lane < rows) a.ws_lse[part + row + (long long)lane * a.H] = none ? -INFINITY : m + log2f(l);
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
@@ -492,11 +533,18 @@ int parts(int T, int B, int H, int S, int num_sms) {
   return n < 1 ? 1 : (int)n;
 }
 
+// Heads whose blocks run at a time, longest tiles first: as many as have their keys and values in half
+// of the L2 together.
+int head_group(int S, int H) {
+  const long long n = (64LL << 20) / ((long long)S * 512);
+  return n < 1 ? 1 : n < H ? (int)n : H;
+}
+
 size_t lse_bytes(int n, int T, int H) { return ((size_t)n * T * H * sizeof(float) + 255) / 256 * 256; }
 
 }  // namespace
 
-bool prefill_grid_ok(int T, int B, int H) { return row_tiles(T, B) < (1LL << 31) && H <= 65535; }
+bool prefill_grid_ok(int T, int B, int H) { return row_tiles(T, B) * H < (1LL << 31); }
 
 size_t prefill_workspace_size(int T, int B, int H, int S, int num_sms) {
   const int n = parts(T, B, H, S, num_sms);
@@ -531,7 +579,9 @@ cudaError_t launch_mla_prefill(PrefillArgs a, const PrefillTensors& x, cudaStrea
   if (!encode_tile_map(&qmap, x.q, 3, qd, qs, box) || !encode_tile_map(&kmap, x.k_nope, 3, kd, ks, box) ||
       !encode_tile_map(&rmap, x.k_rope, 2, rd, rs, rbox) || !encode_tile_map(&vmap, x.v, 3, kd, vs, vbox))
     return cudaErrorInvalidValue;
-  const dim3 grid((unsigned)row_tiles(a.T, a.B), (unsigned)a.H, (unsigned)a.splits);
+  a.tiles = (int)row_tiles(a.T, a.B);
+  a.group = head_group(a.S, a.H);
+  const dim3 grid((unsigned)a.tiles * (unsigned)a.H, (unsigned)a.splits);
   mla_prefill_kernel<<<grid, kThreads, kSmemBytes, stream>>>(qmap, kmap, rmap, vmap, a);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.splits == 1) return e;

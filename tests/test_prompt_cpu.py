@@ -99,7 +99,7 @@ def _prefill(lib, **kw):
     (dict(kr=None), E), (dict(v=None), E), (dict(cu=None), E), (dict(starts=None), E), (dict(seq=None), E),
     (dict(out=None), E), (dict(cp=2, gseq=None), E), (dict(q=24), E), (dict(k=24), E), (dict(kr=24), E), (dict(v=24), E),
     (dict(out=24), E), (dict(cu=18), E), (dict(lse=18), E), (dict(gseq=18), E), (dict(ws=272, ws_bytes=1 << 20), E),
-    (dict(H=65536), U), (dict(cp=1 << 16, il=1 << 16), U), (dict(T=0, q=None), OK), (dict(B=0, q=None), OK),
+    (dict(H=1 << 30, T=1 << 10), U), (dict(cp=1 << 16, il=1 << 16), U), (dict(T=0, q=None), OK), (dict(B=0, q=None), OK),
 ])
 def test_prefill_refuses(lib, kw, code):  # noqa: F811
     assert _prefill(lib, **kw) == code
