@@ -477,8 +477,8 @@ int mla_expand(const void* kv_cache, const float* kv_scales, const int32_t* bloc
  * Values of a request's keys must be finite where any of its rows sees them: a row that does not
  * see a key may still get NaN from a value of it that is NaN or infinite.  Rows behind the last key
  * may hold anything.
- * cu_q_lens out of order or beyond T (the request is skipped), and kv_starts or seq_lens beyond S
- * (cut), set MLA_STATUS_BAD_STEP.
+ * A request whose cu_q_lens are out of order (before the largest so far) or beyond T is skipped, and
+ * kv_starts or seq_lens beyond S are cut; both set MLA_STATUS_BAD_STEP.
  * Accuracy: scores and sums in fp32; a softmax weight is rounded to bf16 where it meets the values.
  * Errors: MLA_ERR_INVALID_ARGUMENT, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA.
  */

@@ -55,27 +55,35 @@ constexpr int kQChunks = 3, kKSlots = 3, kVSlots = 2;
 // Group 2j is tile j's keys, group 2j + 1 its values; the slots they take one after another make
 // group n's slots free once group n - 3 has been used.
 constexpr int kGroups = 3;
-constexpr int kThreads = 384;                 // warp 0 TMA; 1, 2 MMA and 4-7, 8-11 softmax of a stream
+constexpr int kThreads = 384;                 // warp 0 TMA; 1, 2 MMA and 4-7, 8-11 softmax of a stream; 3 units
 constexpr float kRise = 8.0f;                 // log2 units that a maximum may rise before O is rescaled
 
-constexpr int kOffQ = 0;                                     // 2 x 48 KB, then the output's staging
+constexpr int kOffQ = 0;                                     // 2 x 48 KB
 constexpr int kOffRing = 2 * kQChunks * kSlotBytes;
 constexpr int kOffBar = kOffRing + kSlots * kSlotBytes;
 constexpr int kOffMisc = kOffBar + 256;
-constexpr int kSmemBytes = kOffMisc + 128 + 1024;
+constexpr int kSmemBytes = kOffMisc + 160 + 1024;
 
 enum Bar : int {
   B_QFULL = 0,                   // [2]
-  B_FULL = 2,                    // [3] keys or values of a tile
+  B_QEMPTY = 2,                  // [2] the unit's last QK of a stream is done
+  B_FULL = 4,                    // [3] keys or values of a tile
   B_EMPTY = B_FULL + kGroups,    // [3] both streams have used them
   B_SFULL = B_EMPTY + kGroups,   // [2] S of a stream's tile computed (and all products before)
   B_PFULL = B_SFULL + 2,         // [2][2] P of half a tile in tensor memory, O rescaled
-  B_OFULL = B_PFULL + 4,         // [2] the stream's last product is done
-  B_TURN = B_OFULL + 2,          // [2] a stream's products may be issued
-  B_DRAIN = B_TURN + 2,          // [2]
+  B_OFULL = B_PFULL + 4,         // [2] the unit's last product of a stream is done
+  B_OFREE = B_OFULL + 2,         // [2] O read
+  B_TURN = B_OFREE + 2,          // [2] a stream's products may be issued
+  B_UFULL = B_TURN + 2,          // the next unit is known
+  B_UEMPTY = B_UFULL + 1,        // every role has read it
+  B_ASK = B_UEMPTY + 1,          // the unit's last loads are on their way
+  B_NEXT = B_ASK + 1,            // the answer about the next block of the grid is here
+  B_DRAIN = B_NEXT + 1,          // [2]
   B_COUNT = B_DRAIN + 2
 };
 static_assert(B_COUNT * 8 <= 256, "barriers");
+constexpr int kReaders = 11;     // warps that read a unit: loads, products (2), softmax (8)
+constexpr int kOffNext = kOffMisc + 16, kOffUnit = kOffMisc + 32;
 
 struct Ctx {
   uint32_t base;
@@ -88,74 +96,110 @@ struct Ctx {
   }
 };
 
-// What a block works on.
+// What a block works on at a time.
 struct Unit {
   int row0, n;                   // first row (of q) of the request's chunk, its rows
-  int first;                     // the block's first row within the chunk
+  int first;                     // the unit's first row within the chunk
   int key0, keys;                // first key row, keys of the shard
   int global;                    // global length
+  int head, part;                // -1: no more units
+  int begin, end0, end1;         // first tile of keys, the streams' ends
+  __device__ __forceinline__ int end(int t) const { return t == 0 ? end0 : end1; }
+  __device__ __forceinline__ int most() const { return max(max(end0, end1), begin); }
 };
+static_assert(kOffUnit + 2 * (int)sizeof(Unit) <= kOffMisc + 160, "units");
 
-// One warp: the request and rows of tile x.  False: there is no such tile.
-__device__ bool find_unit(const PrefillArgs& a, int x, int lane, Unit& un) {
-  unsigned flags = 0;
-  int before = 0;                // tiles of the requests before this round's
-  bool found = false;
-  for (int b0 = 0; b0 < a.B && !found; b0 += 32) {
-    const int b = b0 + lane;
-    int row0 = 0, n = 0;
+// 32 requests, one a lane: rows and keys, checked, and the row tiles before them.
+struct Round {
+  int row0, n, key0, keys, global;
+  int tiles, before;             // its tiles, those of the requests before it
+  int all, top;                  // of the round's end: tiles so far, end of the rows so far
+
+  __device__ void load(const PrefillArgs& a, int b, int lane, int tiles_before, int top_before) {
+    unsigned flags = 0;
+    int end = 0;
+    row0 = n = key0 = keys = global = 0;
     if (b < a.B) {
       row0 = __ldg(a.cu + b);
-      const int end = __ldg(a.cu + b + 1);
-      if (row0 < 0 || end < row0 || end > a.T) flags |= MLA_STATUS_BAD_STEP;
+      end = __ldg(a.cu + b + 1);
+      keys = __ldg(a.seq_lens + b);
+      key0 = __ldg(a.starts + b);
+      global = a.gseq != nullptr ? __ldg(a.gseq + b) : keys;
+      if (keys < 0 || key0 < 0 || keys > a.S - key0) {
+        flags |= MLA_STATUS_BAD_STEP;
+        key0 = min(max(key0, 0), a.S);
+        keys = min(max(keys, 0), a.S - key0);
+      }
+    }
+    // rows in order: none before the largest value so far
+    int high = row0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, high, o);
+      if (lane >= o) high = max(high, v);
+    }
+    high = max(high, top_before);
+    top = __shfl_sync(0xffffffffu, max(high, end), 31);
+    if (b < a.B) {
+      if (row0 < high || end < row0 || end > a.T) flags |= MLA_STATUS_BAD_STEP;
       else n = end - row0;
     }
-    const int tiles = (n + 2 * kM - 1) / (2 * kM);
+    tiles = (n + 2 * kM - 1) / (2 * kM);
     int incl = tiles;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += v;
     }
-    const int at = x - (before + incl - tiles);
-    const unsigned hit = __ballot_sync(0xffffffffu, at >= 0 && at < tiles);
-    before += __shfl_sync(0xffffffffu, incl, 31);
-    if (hit) {
-      found = true;
-      const int who = __ffs(hit) - 1;
-      un.row0 = __shfl_sync(0xffffffffu, row0, who);
-      un.n = __shfl_sync(0xffffffffu, n, who);
-      // the last rows, which see the most keys, first
-      un.first = 2 * kM * __shfl_sync(0xffffffffu, tiles - 1 - at, who);
-      const int r = b0 + who;
-      int keys = __ldg(a.seq_lens + r), key0 = __ldg(a.starts + r), g = keys;
-      if (a.gseq != nullptr) g = __ldg(a.gseq + r);
-      if (keys < 0 || key0 < 0 || keys > a.S - key0) {
-        flags |= MLA_STATUS_BAD_STEP;
-        key0 = min(max(key0, 0), a.S);
-        keys = min(max(keys, 0), a.S - key0);
-      }
-      un.key0 = key0;
-      un.keys = keys;
-      un.global = g;
-    }
+    before = tiles_before + incl - tiles;
+    all = tiles_before + __shfl_sync(0xffffffffu, incl, 31);
+    if (flags) atomicOr(a.status, flags);
   }
-  if (flags) atomicOr(a.status, flags);
-  return found;
+  // The unit of row tile x, if it is one of the round's.
+  __device__ bool find(int x, Unit& un) const {
+    const int at = x - before;
+    const unsigned hit = __ballot_sync(0xffffffffu, at >= 0 && at < tiles);
+    if (hit == 0) return false;
+    const int who = __ffs(hit) - 1;
+    un.row0 = __shfl_sync(0xffffffffu, row0, who);
+    un.n = __shfl_sync(0xffffffffu, n, who);
+    // the last rows, which see the most keys, first
+    un.first = 2 * kM * __shfl_sync(0xffffffffu, tiles - 1 - at, who);
+    un.key0 = __shfl_sync(0xffffffffu, key0, who);
+    un.keys = __shfl_sync(0xffffffffu, keys, who);
+    un.global = __shfl_sync(0xffffffffu, global, who);
+    return true;
+  }
+};
+
+// The unit of row tile x; `first` holds the first 32 requests.  False: there is none.
+__device__ __forceinline__ bool find_unit(const PrefillArgs& a, const Round& first, int x, int lane, Unit& un) {
+  if (first.find(x, un)) return true;
+  int all = first.all, top = first.top;
+  for (int b0 = 32; b0 < a.B; b0 += 32) {
+    Round r;
+    r.load(a, b0 + lane, lane, all, top);
+    if (r.find(x, un)) return true;
+    all = r.all;
+    top = r.top;
+  }
+  return false;
 }
 
 // Keys that row i of the chunk sees.
 __device__ __forceinline__ int seen(const PrefillArgs& a, const Unit& u, int i) {
   if (!a.causal) return u.keys;
-  const long long g = (long long)u.global - (u.n - 1 - i);
+  if (u.global <= 0) return 0;
+  const int g = u.global - (u.n - 1 - i);
   if (g <= 0) return 0;
-  long long l = g;
+  int l = g;
   if (a.cp > 1) {
-    const long long span = (long long)a.cp * a.il;
-    const long long rem = g % span - (long long)a.rank * a.il;
-    l = g / span * a.il + (rem < 0 ? 0 : rem > a.il ? a.il : rem);
+    // cp * il < 2^31; a round's positions before this rank's segment, those of its segment
+    const unsigned span = (unsigned)a.cp * (unsigned)a.il, rounds = (unsigned)g / span;
+    const long long rem = (long long)((unsigned)g - rounds * span) - (long long)a.rank * a.il;
+    l = (int)rounds * a.il + (int)(rem < 0 ? 0 : rem > a.il ? a.il : rem);
   }
-  return (int)(l < u.keys ? l : u.keys);
+  return min(l, u.keys);
 }
 
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {
@@ -185,6 +229,93 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return d;
 }
 
+// Asks for a block of the grid that has not begun: its index, or that there is none, comes into 16
+// bytes of shared memory.
+__device__ __forceinline__ void ask_next(uint32_t dst, uint32_t bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst),
+      "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ bool read_next(uint32_t src, uint32_t& x, uint32_t& y) {
+  uint32_t some;
+  asm volatile(
+      "{\n .reg .b128 h;\n .reg .pred p;\n .reg .b32 z, w;\n"
+      " ld.shared.b128 h, [%3];\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n"
+      " selp.u32 %0, 1, 0, p;\n mov.b32 %1, 0;\n mov.b32 %2, 0;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, %2, z, w}, h;\n}"
+      : "=r"(some), "=r"(x), "=r"(y)
+      : "r"(src)
+      : "memory");
+  // the read is done before the next answer is written there
+  fence_proxy_async_smem();
+  return some != 0;
+}
+
+// Eight lanes with eight 16-byte pieces each exchange them: lane i gets piece i of each lane's, so
+// that a warp writes four rows of 128 bytes at a time (32 rows of 32 bytes, straight from the
+// registers, kept the store unit busy for 6,000 clocks a unit).
+__device__ __forceinline__ void transpose8(uint32_t (&v)[32], int lane) {
+#pragma unroll
+  for (int b = 1; b < 8; b <<= 1) {
+    const bool up = lane & b;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      if (p & b) continue;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint32_t &lo = v[4 * p + w], &hi = v[4 * (p | b) + w];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, b);
+        if (up) lo = got;
+        else hi = got;
+      }
+    }
+  }
+}
+
+// One warp: O's 32 rows at tensor memory `to` times `inv` (0: nothing was seen, zeros), as fp32 or
+// bf16, to `dst` and on, a token's H heads apart; the first `rows` are stored.  Arrives on `free` once
+// O is read.  Out of line: inlined, its registers spill the tile loop's.
+template <bool kFp32>
+__device__ __noinline__ void write_rows(uint32_t to, bool any, float inv, uint8_t* dst, int H, int rows, int lane,
+                                        uint32_t free) {
+  constexpr int kPasses = kFp32 ? 4 : 2;          // 128 bytes of each row at a time
+  const long long step = (long long)H * (128 * kPasses);
+  dst += (lane & 24) * step + (lane & 7) * 16;
+  const bool none = inv == 0.f || !any;
+#pragma unroll 1
+  for (int c = 0; c < kPasses; ++c) {
+    uint32_t v[32];
+    if (kFp32) {
+      tmem_ld32(to + 32 * c, v);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = none ? 0u : __float_as_uint(__uint_as_float(v[i]) * inv);
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t o[32];
+        tmem_ld32(to + 64 * c + 32 * h, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          v[16 * h + i] = none ? 0u : pack(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+      }
+    }
+    if (c == kPasses - 1 && any) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(free);
+    }
+    transpose8(v, lane);
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+      if ((lane & 24) + r < rows)
+        *reinterpret_cast<uint4*>(dst + r * step + c * 128) = make_uint4(v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]);
+  }
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
 mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap rmap, const __grid_constant__ CUtensorMap vmap,
@@ -192,74 +323,111 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sp = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  // blocks of one group of heads after another; in a group all heads' longest tiles first
-  const unsigned per = (unsigned)a.tiles * a.group;
-  const unsigned grp = blockIdx.x / per, in = blockIdx.x - grp * per;
-  const unsigned heads = min((unsigned)a.group, (unsigned)a.H - grp * a.group);
-  const int tile_x = (int)(in / heads), head = (int)(grp * a.group + in % heads);
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(sp + kOffMisc);
-  Unit* su = reinterpret_cast<Unit*>(sp + kOffMisc + 16);
+  Unit* su = reinterpret_cast<Unit*>(sp + kOffUnit);
   Ctx s;
   s.base = smem_u32(sp);
   s.abort = reinterpret_cast<volatile int*>(misc + 1);
   s.status = a.status;
   s.wait_ns = a.wait_ns;
 
-  if (warp == 0) {
-    Unit u;
-    const bool any = find_unit(a, tile_x, lane, u);
-    if (lane == 0) {
-      misc[2] = any;
-      if (any) *su = u;
-    }
-  } else if (warp == 1) {
+  if (warp == 1) {
     tmem_alloc(s.base + kOffMisc, 512);
     tmem_relinquish();
-  } else if (tid == 96) {
+  } else if (tid == 0) {
     *s.abort = 0;
-    for (int i = 0; i < B_COUNT; ++i)
-      mbar_init(s.bar(i), i >= B_PFULL && i < B_PFULL + 4 ? 4 : i >= B_EMPTY && i < B_EMPTY + kGroups ? 2 : 1);
+    for (int i = 0; i < B_COUNT; ++i) {
+      const bool of_warps = (i >= B_PFULL && i < B_PFULL + 4) || i == B_OFREE || i == B_OFREE + 1;
+      mbar_init(s.bar(i), of_warps ? 4 : i >= B_EMPTY && i < B_EMPTY + kGroups ? 2 : i == B_UEMPTY ? kReaders : 1);
+    }
     fence_mbar_init();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, misc[0], 0);
-  const bool any = misc[2] != 0;
 
-  if (any) {
-    const Unit un = *su;
-    // tiles of each stream: the bound grows with the row, so a stream's last row has the most
-    int begin = 0, tiles[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int i0 = un.first + t * kM;
-      tiles[t] = i0 < un.n ? (seen(a, un, min(i0 + kM, un.n) - 1) + kTile - 1) / kTile : 0;
-    }
-    if (a.splits > 1) {
-      const int most = max(tiles[0], tiles[1]);
-      begin = (int)((long long)most * blockIdx.y / a.splits);
-      const int end = (int)((long long)most * (blockIdx.y + 1) / a.splits);
-      tiles[0] = max(min(tiles[0], end), begin);
-      tiles[1] = max(min(tiles[1], end), begin);
-    }
-    const int most = max(max(tiles[0], tiles[1]), begin);
+  // Every role goes through the same units: next() waits for the k-th one.  False: there is none, or
+  // a wait has run out.
+  // A unit stays where it is until the role has asked for the one after it.
+  const auto next = [&](uint32_t& k, const Unit*& u) {
+    if (!s.wait(B_UFULL, k & 1)) return false;
+    u = su + (k & 1);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(s.bar(B_UEMPTY));
+    ++k;
+    return u->head >= 0;
+  };
 
-    if (warp == 0) {
-      // ---- loads --------------------------------------------------------------------------
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-        if (tiles[t] > begin) {
-          mbar_arrive_expect_tx_warp(s.bar(B_QFULL + t), kQChunks * kSlotBytes);
-          for (int c = 0; c < kQChunks; ++c)
-            tma_load_3d_warp(s.base + kOffQ + (t * kQChunks + c) * kSlotBytes, &qmap, 64 * c, head,
-                             un.row0 + un.first + t * kM, s.bar(B_QFULL + t));
+  if (warp == 3) {
+    // ---- units: this block's own, then those of blocks that have not begun ---------------------
+    uint32_t x = blockIdx.x, y = blockIdx.y, asked = 0, k = 0;
+    bool some = true, ok = true;
+    Round requests;
+    requests.load(a, lane, lane, 0, 0);
+    while (ok) {
+      Unit u;
+      u.head = -1;
+      if (some) {
+        // blocks of one group of heads after another; in a group all heads' longest tiles first
+        const unsigned per = (unsigned)a.tiles * a.group;
+        const unsigned grp = x / per, in = x - grp * per;
+        const unsigned heads = min((unsigned)a.group, (unsigned)a.H - grp * a.group);
+        if (find_unit(a, requests, (int)(in / heads), lane, u)) {
+          u.head = (int)(grp * a.group + in % heads);
+          u.part = (int)y;
+          u.begin = 0;
+          // the bound grows with the row, so a stream's last row has the most tiles
+          u.end0 = (seen(a, u, min(u.first + kM, u.n) - 1) + kTile - 1) / kTile;
+          u.end1 = u.first + kM < u.n ? (seen(a, u, min(u.first + 2 * kM, u.n) - 1) + kTile - 1) / kTile : 0;
+          if (a.splits > 1) {
+            const int most = u.most();
+            u.begin = (int)((long long)most * y / a.splits);
+            const int end = (int)((long long)most * (y + 1) / a.splits);
+            u.end0 = max(min(u.end0, end), u.begin);
+            u.end1 = max(min(u.end1, end), u.begin);
+          }
         }
-      int sl = 0, g = 0, issued = 0;
-      uint32_t par = 1;
-      bool ok = true;
-      for (int j = begin; j < most && ok; ++j) {
-        const int y = un.key0 + j * kTile;
+      }
+      if (u.head >= 0 || !some) {
+        ok = s.wait(B_UEMPTY, (k & 1) ^ 1u);
+        if (!ok) break;
+        if (lane == 0) {
+          su[k & 1] = u;
+          mbar_arrive(s.bar(B_UFULL));
+        }
+        __syncwarp();
+        ++k;
+        if (!some) break;
+        // the next one only when this one's last loads go out: what is asked for early runs late
+        ok = s.wait(B_ASK, (k & 1) ^ 1u);
+        if (!ok) break;
+      }
+      if (lane == 0) {
+        mbar_arrive_expect_tx(s.bar(B_NEXT), 16);
+        ask_next(s.base + kOffNext, s.bar(B_NEXT));
+      }
+      __syncwarp();
+      ok = s.wait(B_NEXT, asked & 1);
+      ++asked;
+      some = ok && read_next(s.base + kOffNext, x, y);
+    }
+    if (!ok && asked > 0) mbar_wait_drain(s.bar(B_NEXT), (asked - 1) & 1);
+  } else if (warp == 0) {
+    // ---- loads ------------------------------------------------------------------------------
+    const Unit* unit;
+    uint32_t k = 0, nq[2] = {0, 0};
+    int sl = 0, g = 0;
+    long long issued = 0;
+    uint32_t par = 1;
+    bool ok = true;
+    while (ok && next(k, unit)) {
+      const Unit u = *unit;
+      const int most = u.most();
+      if (most == u.begin && lane == 0) mbar_arrive(s.bar(B_ASK));
+      for (int j = u.begin; j < most && ok; ++j) {
+        if (j + 1 == most && lane == 0) mbar_arrive(s.bar(B_ASK));
+        const int y = u.key0 + j * kTile;
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
           ok = s.wait(B_EMPTY + g, par);
@@ -270,10 +438,10 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
           for (int c = 0; c < (part == 0 ? kKSlots : kVSlots); ++c) {
             const uint32_t dst = s.base + kOffRing + sl * kSlotBytes;
             if (part == 1) {
-              tma_load_3d_warp(dst, &vmap, 0, head, y + 64 * c, fb);
-              tma_load_3d_warp(dst + kSlotBytes / 2, &vmap, 64, head, y + 64 * c, fb);
+              tma_load_3d_warp(dst, &vmap, 0, u.head, y + 64 * c, fb);
+              tma_load_3d_warp(dst + kSlotBytes / 2, &vmap, 64, u.head, y + 64 * c, fb);
             } else if (c < 2) {
-              tma_load_3d_warp(dst, &kmap, 64 * c, head, y, fb);
+              tma_load_3d_warp(dst, &kmap, 64 * c, u.head, y, fb);
             } else {
               tma_load_2d_warp(dst, &rmap, 0, y, fb);
             }
@@ -284,37 +452,60 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
             g = 0;
             par ^= 1u;
           }
+          if (part == 0 && j == u.begin) {
+            // the unit's queries, after its first keys
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+              if (u.end(t) > u.begin) {
+                ok = ok && s.wait(B_QEMPTY + t, (nq[t] & 1) ^ 1u);
+                if (!ok) break;
+                mbar_arrive_expect_tx_warp(s.bar(B_QFULL + t), kQChunks * kSlotBytes);
+                for (int c = 0; c < kQChunks; ++c)
+                  tma_load_3d_warp(s.base + kOffQ + (t * kQChunks + c) * kSlotBytes, &qmap, 64 * c, u.head,
+                                   u.row0 + u.first + t * kM, s.bar(B_QFULL + t));
+                ++nq[t];
+              }
+            if (!ok) break;
+          }
         }
       }
-      if (*s.abort) {
-        // let loads in flight land before the block ends
-        for (int m = issued > kGroups ? issued - kGroups : 0; m < issued; ++m)
-          mbar_wait_drain(s.bar(B_FULL + m % kGroups), (uint32_t)((m / kGroups) & 1));
+    }
+    if (*s.abort) {
+      // let loads in flight land before the block ends
+      for (long long m = issued > kGroups ? issued - kGroups : 0; m < issued; ++m)
+        mbar_wait_drain(s.bar(B_FULL + (int)(m % kGroups)), (uint32_t)((m / kGroups) & 1));
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if (tiles[t] > begin) mbar_wait_drain(s.bar(B_QFULL + t), 0);
-      }
-    } else if (warp <= 2) {
-      // ---- products of a stream, the streams in turn ------------------------------------------
-      const int t = warp - 1;
-      const uint32_t id_qk = idesc_bf16(kM, kTile, false, false), id_pv = idesc_bf16(kM, 128, false, true);
-      const uint64_t qd = smem_desc(s.base + kOffQ + t * kQChunks * kSlotBytes, 16, 1024, kSwizzle128B);
-      const uint64_t kd = smem_desc(s.base + kOffRing, 16, 1024, kSwizzle128B);
-      const uint64_t vd = smem_desc(s.base + kOffRing, kSlotBytes / 2, 1024, kSwizzle128B);
-      constexpr unsigned kStep = kSlotBytes / 16;
-      const uint32_t ds = tmem + t * 128, d_o = ds + 256;
-      const int mine = tiles[t];
-      bool ok = begin >= mine || s.wait(B_QFULL + t, 0);
-      unsigned sl = 0;                          // slot of tile j's keys
-      int g = 0;                                // its group's barriers, and their parity
-      uint32_t par = 0, ph = 0;                 // parity of the tile before, and of the turn
-      for (int j = begin; j <= most && ok; ++j) {
+      for (int t = 0; t < 2; ++t)
+        if (nq[t] > 0) mbar_wait_drain(s.bar(B_QFULL + t), (nq[t] - 1) & 1);
+    }
+  } else if (warp <= 2) {
+    // ---- products of a stream, the streams in turn ----------------------------------------------
+    const int t = warp - 1;
+    const uint32_t id_qk = idesc_bf16(kM, kTile, false, false), id_pv = idesc_bf16(kM, 128, false, true);
+    const uint64_t qd = smem_desc(s.base + kOffQ + t * kQChunks * kSlotBytes, 16, 1024, kSwizzle128B);
+    const uint64_t kd = smem_desc(s.base + kOffRing, 16, 1024, kSwizzle128B);
+    const uint64_t vd = smem_desc(s.base + kOffRing, kSlotBytes / 2, 1024, kSwizzle128B);
+    constexpr unsigned kStep = kSlotBytes / 16;
+    const uint32_t ds = tmem + t * 128, d_o = ds + 256;
+    const Unit* unit;
+    uint32_t k = 0;
+    unsigned sl = 0;                            // slot of tile j's keys
+    int g = 0;                                  // its group's barriers, and their parity
+    uint32_t par = 0;
+    uint32_t units = 0, pv_tiles = 0;           // units and tiles of this stream so far
+    uint32_t turn = 0;
+    bool ok = true;
+    while (ok && next(k, unit)) {
+      const Unit u = *unit;
+      const int most = u.most(), mine = u.end(t);
+      if (u.begin < mine) ok = s.wait(B_QFULL + t, units & 1);
+      for (int j = u.begin; j <= most && ok; ++j) {
         const int gv = g == 0 ? kGroups - 1 : g - 1;      // tile j - 1's values: the group and slots before
         const unsigned v0 = (sl + kSlots - 2) % kSlots, v1 = (sl + kSlots - 1) % kSlots;
-        const bool pv = j > begin && j <= mine, qk = j < mine;
+        const bool pv = j > u.begin && j <= mine, qk = j < mine, first = j - 1 == u.begin;
         if (pv) {
           ok = s.wait(B_FULL + gv, g == 0 ? par ^ 1u : par);
-          const int left = un.keys - (j - 1) * kTile;
+          const int left = u.keys - (j - 1) * kTile;
           if (ok && left < kTile) {
             // rows behind the last key: P is zero there, the values may be anything
             for (int h = 0; h < kVSlots; ++h) {
@@ -327,20 +518,22 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
             fence_proxy_async_smem();
             __syncwarp();
           }
-          ok = ok && s.wait(B_PFULL + 2 * t, ph ^ 1u);
+          if (first) ok = ok && s.wait(B_OFREE + t, (units & 1) ^ 1u);
+          ok = ok && s.wait(B_PFULL + 2 * t, pv_tiles & 1);
         }
         // the other stream's products are issued
-        if (t == 1 || j > begin) ok = ok && s.wait(B_TURN + t, t == 1 ? ph : ph ^ 1u);
+        if (t == 1 || turn > 0) ok = ok && s.wait(B_TURN + t, t == 1 ? turn & 1 : (turn & 1) ^ 1u);
         if (!ok) break;
         tc_fence_after();
         if (pv) {
-          mma4_ts_mn_warp(d_o, ds, vd + v0 * kStep, id_pv, j - 1 > begin);
-          ok = s.wait(B_PFULL + 2 * t + 1, ph ^ 1u);
+          mma4_ts_mn_warp(d_o, ds, vd + v0 * kStep, id_pv, !first);
+          ok = s.wait(B_PFULL + 2 * t + 1, pv_tiles & 1);
           if (!ok) break;
           tc_fence_after();
           mma4_ts_mn_warp(d_o, ds + 32, vd + v1 * kStep, id_pv, 1);
+          ++pv_tiles;
         }
-        if (j > begin) mma_commit_warp(s.bar(B_EMPTY + gv));
+        if (j > u.begin) mma_commit_warp(s.bar(B_EMPTY + gv));
         if (qk) {
           ok = s.wait(B_FULL + g, par);
           if (!ok) break;
@@ -350,30 +543,37 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
         }
         if (lane == 0) mbar_arrive(s.bar(B_TURN + (t ^ 1)));
         __syncwarp();
+        ++turn;
         if (pv && j == mine) mma_commit_warp(s.bar(B_OFULL + t));
-        if (j < most) mma_commit_warp(s.bar(B_EMPTY + g));
+        if (qk && j + 1 == mine) mma_commit_warp(s.bar(B_QEMPTY + t));
+        if (j == most) break;
+        mma_commit_warp(s.bar(B_EMPTY + g));
         sl = (sl + kKSlots + kVSlots) % kSlots;
-        ph ^= 1u;
         g += 2;
         if (g >= kGroups) {
           g -= kGroups;
           par ^= 1u;
         }
       }
-      mma_commit_warp(s.bar(B_DRAIN + t));
-      mbar_wait_drain(s.bar(B_DRAIN + t), 0);
-    } else if (warp >= 4) {
-      // ---- softmax: thread = row ------------------------------------------------------------
-      const int t = (warp >> 2) - 1, q = warp & 3;
-      const int i0 = un.first + t * kM + q * 32;               // the warp's first row in the chunk
-      const int mine = seen(a, un, min(i0 + lane, un.n - 1));  // rows behind the chunk: not stored
+      if (u.begin < mine) ++units;
+    }
+    mma_commit_warp(s.bar(B_DRAIN + t));
+    mbar_wait_drain(s.bar(B_DRAIN + t), 0);
+  } else {
+    // ---- softmax and output: thread = row ---------------------------------------------------------
+    const int t = (warp >> 2) - 1, q = warp & 3;
+    const uint32_t ts = tmem + ((uint32_t)q << 21) + t * 128, to = ts + 256;
+    const Unit* u;
+    uint32_t k = 0, s_tiles = 0, units = 0;
+    bool ok = true;
+    while (ok && next(k, u)) {
+      // keys that the row sees (rows behind the chunk are not stored), the fewest of the warp
+      const int mine = seen(a, *u, min(u->first + t * kM + q * 32 + lane, u->n - 1));
       const int least = __shfl_sync(0xffffffffu, mine, 0);
-      const uint32_t ts = tmem + ((uint32_t)q << 21) + t * 128, to = ts + 256;
       float m = -INFINITY, l = 0.f;
-      bool ok = true;
-      const int n_tiles = tiles[t];
-      for (int j = begin; j < n_tiles; ++j) {
-        ok = s.wait(B_SFULL + t, (uint32_t)((j - begin) & 1));
+      const int begin = u->begin, n_tiles = u->end(t);
+      for (int j = begin; j < n_tiles; ++j, ++s_tiles) {
+        ok = s.wait(B_SFULL + t, s_tiles & 1);
         if (!ok) break;
         tc_fence_after();
         float x[128];
@@ -390,9 +590,9 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
 #pragma unroll
         for (int c = 4; c < 124; c += 8)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], x[c + 2 * k], x[c + 2 * k + 1]);
+          for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], x[c + 2 * i], x[c + 2 * i + 1]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], x[124 + k]);
+        for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], x[124 + i]);
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
         // the reference moves where a maximum rose too far (from nothing at the first)
         const bool moves = top > m + kRise;
@@ -402,13 +602,13 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
           l *= f;
           if (j > begin)
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t o[32];
-              tmem_ld32(to + 32 * c, o);
+            for (int c = 0; c < 8; ++c) {
+              uint32_t o[16];
+              tmem_ld16(to + 16 * c, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-              tmem_st32(to + 32 * c, o);
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st16(to + 16 * c, o);
             }
         }
         const float ref = m == -INFINITY ? 0.f : m;
@@ -418,15 +618,19 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
         // P of 64 keys, then of the other 64: the first half's product starts meanwhile
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          uint32_t pk[32];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const float2 e = fma2(make_float2(x[64 * h + 2 * k], x[64 * h + 2 * k + 1]), mul, sub);
-            const float2 p = make_float2(exp2_fast(e.x), exp2_fast(e.y));
-            sum[k & 1] = fma2(p, one, sum[k & 1]);
-            pk[k] = pack(p.x, p.y);
+          for (int c = 0; c < 2; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int d = 64 * h + 32 * c + 2 * i;
+              const float2 e = fma2(make_float2(x[d], x[d + 1]), mul, sub);
+              const float2 p = make_float2(exp2_fast(e.x), exp2_fast(e.y));
+              sum[i & 1] = fma2(p, one, sum[i & 1]);
+              pk[i] = pack(p.x, p.y);
+            }
+            tmem_st16(ts + 32 * h + 16 * c, pk);
           }
-          tmem_st32(ts + 32 * h, pk);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
@@ -434,78 +638,35 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
-      if (ok && n_tiles > begin) {
-        ok = s.wait(B_OFULL + t, 0);
+      if (!ok) break;
+      const bool any = n_tiles > begin;
+      if (any) {
+        ok = s.wait(B_OFULL + t, units & 1);
+        if (!ok) break;
         tc_fence_after();
+        ++units;
       }
-      const int rows = un.n - i0;                              // the warp's rows that are stored
-      if (ok && rows > 0) {
-        const long long row = (long long)(un.row0 + i0) * a.H + head;
-        const bool none = l == 0.f;
-        const float inv = none ? 0.f : 1.f / l;
-        uint8_t* stage = sp + kOffQ + t * kQChunks * kSlotBytes + q * 32 * 256;
-        if (a.splits == 1) {
-          if (a.lse != nullptr && lane < rows)
-            a.lse[row + (long long)lane * a.H] = none ? -INFINITY : (m + log2f(l)) * a.lse_mul;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t v[64];
-            if (n_tiles > begin) {
-              tmem_ld32(to + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(v));
-              tmem_ld32(to + 64 * h + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
-              tmem_wait_ld();
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = none ? 0u : pack(__uint_as_float(v[8 * k + 2 * e]) * inv, __uint_as_float(v[8 * k + 2 * e + 1]) * inv);
-              *reinterpret_cast<uint4*>(stage + lane * 256 + (((8 * h + k) ^ (lane & 7)) << 4)) =
-                  make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          }
-          __syncwarp();
-#pragma unroll 4
-          for (int k = 0; k < 16; ++k) {
-            const int r = 2 * k + (lane >> 4), ch = lane & 15;
-            if (r < rows)
-              *reinterpret_cast<uint4*>(a.out + (row + (long long)r * a.H) * 128 + ch * 8) =
-                  *reinterpret_cast<const uint4*>(stage + r * 256 + ((ch ^ (r & 7)) << 4));
-          }
-        } else {
-          const long long part = (long long)blockIdx.y * a.T * a.H;
-          if (lane < rows) a.ws_lse[part + row + (long long)lane * a.H] = none ? -INFINITY : m + log2f(l);
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            uint32_t v[64];
-            if (n_tiles > begin) {
-              tmem_ld32(to + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(v));
-              tmem_ld32(to + 64 * h + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
-              tmem_wait_ld();
-            }
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) w[e] = none ? 0u : __float_as_uint(__uint_as_float(v[4 * k + e]) * inv);
-              *reinterpret_cast<uint4*>(stage + lane * 256 + ((k ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-            __syncwarp();
-#pragma unroll 4
-            for (int k = 0; k < 16; ++k) {
-              const int r = 2 * k + (lane >> 4), ch = lane & 15;
-              if (r < rows)
-                *reinterpret_cast<uint4*>(a.ws_o + (part + row + (long long)r * a.H) * 128 + 64 * h + ch * 4) =
-                    *reinterpret_cast<const uint4*>(stage + r * 256 + ((ch ^ (r & 7)) << 4));
-            }
-            __syncwarp();
-          }
-        }
+      // O / l: bf16, or fp32 where the keys are split
+      const int i0 = u->first + t * kM + q * 32;             // the warp's first row in the chunk
+      const int rows = u->n - i0;                            // the warp's rows that are stored
+      const long long row0 = (long long)(u->row0 + i0) * a.H + u->head, row = row0 + (long long)lane * a.H;
+      const bool none = l == 0.f;
+      const float inv = none ? 0.f : 1.f / l;
+      const bool split = a.splits > 1;
+      const long long part = (long long)u->part * a.T * a.H;
+      if (lane < rows) {
+        if (split) a.ws_lse[part + row] = none ? -INFINITY : m + log2f(l);
+        else if (a.lse != nullptr) a.lse[row] = none ? -INFINITY : (m + log2f(l)) * a.lse_mul;
       }
+      if (split)
+        write_rows<true>(to, any, inv, reinterpret_cast<uint8_t*>(a.ws_o + (part + row0) * 128), a.H, rows, lane,
+                         s.bar(B_OFREE + t));
+      else
+        write_rows<false>(to, any, inv, reinterpret_cast<uint8_t*>(a.out + row0 * 128), a.H, rows, lane,
+                          s.bar(B_OFREE + t));
     }
-    __syncwarp();
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, 512);
@@ -533,11 +694,14 @@ int parts(int T, int B, int H, int S, int num_sms) {
   return n < 1 ? 1 : (int)n;
 }
 
-// Heads whose blocks run at a time, longest tiles first: as many as have their keys and values in half
-// of the L2 together.
-int head_group(int S, int H) {
-  const long long n = (64LL << 20) / ((long long)S * 512);
-  return n < 1 ? 1 : n < H ? (int)n : H;
+// Heads whose units run at a time, longest first: enough for two units an SM, so that the last ones
+// to run are short, unless their keys and values would not stay in half of the L2; in equal groups.
+int head_group(int tiles, int S, int H, int num_sms) {
+  long long n = (2LL * num_sms + tiles - 1) / tiles;
+  const long long fit = (64LL << 20) / ((long long)S * 512);
+  n = n < fit ? n : fit;
+  const long long groups = n < 1 ? H : n < H ? H / n : 1;
+  return (int)((H + groups - 1) / groups);
 }
 
 size_t lse_bytes(int n, int T, int H) { return ((size_t)n * T * H * sizeof(float) + 255) / 256 * 256; }
@@ -580,7 +744,7 @@ cudaError_t launch_mla_prefill(PrefillArgs a, const PrefillTensors& x, cudaStrea
       !encode_tile_map(&rmap, x.k_rope, 2, rd, rs, rbox) || !encode_tile_map(&vmap, x.v, 3, kd, vs, vbox))
     return cudaErrorInvalidValue;
   a.tiles = (int)row_tiles(a.T, a.B);
-  a.group = head_group(a.S, a.H);
+  a.group = head_group(a.tiles, a.S, a.H, a.num_sms);
   const dim3 grid((unsigned)a.tiles * (unsigned)a.H, (unsigned)a.splits);
   mla_prefill_kernel<<<grid, kThreads, kSmemBytes, stream>>>(qmap, kmap, rmap, vmap, a);
   e = cudaGetLastError();
