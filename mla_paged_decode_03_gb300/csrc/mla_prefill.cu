@@ -92,7 +92,8 @@ struct Ctx {
   unsigned long long wait_ns;
   __device__ __forceinline__ uint32_t bar(int i) const { return base + kOffBar + 8 * i; }
   __device__ __forceinline__ bool wait(int i, uint32_t parity) const {
-    return __all_sync(0xffffffffu, mbar_wait(bar(i), parity, abort, status, wait_ns));
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar(i), parity))) return true;
+    return __all_sync(0xffffffffu, mbar_wait_slow(bar(i), parity, abort, status, wait_ns, false));
   }
 };
 
@@ -229,6 +230,52 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return d;
 }
 
+// Two weights 2^(s mul + sub), added to `sum`, as two bf16.
+__device__ __forceinline__ uint32_t weights(float2 s, float2 mul, float sub, float2& sum) {
+  const float2 e = fma2(s, mul, make_float2(sub, sub));
+  const float2 p = make_float2(exp2_fast(e.x), exp2_fast(e.y));
+  sum = fma2(p, make_float2(1.f, 1.f), sum);
+  return pack(p.x, p.y);
+}
+
+// Descriptors here are lower words; the upper ones are the same for all operands of a kind.
+// O (+)= P V of 64 keys: four products, P at tensor memory `p`, one election.
+__device__ __forceinline__ void pv_half(uint32_t d, uint32_t p, uint32_t v, uint32_t hi, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n .reg .pred e, ac, on;\n .reg .b32 x, y;\n .reg .b64 k;\n elect.sync _|e, 0xffffffff;\n"
+      " setp.ne.b32 ac, %5, 0;\n setp.eq.b32 on, 0, 0;\n"
+      " add.u32 x, %2, 0; mov.b64 k, {x, %3}; add.u32 y, %1, 0;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], k, %4, ac;\n"
+      " add.u32 x, %2, 128; mov.b64 k, {x, %3}; add.u32 y, %1, 8;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], k, %4, on;\n"
+      " add.u32 x, %2, 256; mov.b64 k, {x, %3}; add.u32 y, %1, 16;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], k, %4, on;\n"
+      " add.u32 x, %2, 384; mov.b64 k, {x, %3}; add.u32 y, %1, 24;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], k, %4, on;\n"
+      "}" ::"r"(d), "r"(p), "r"(v), "r"(hi), "r"(idesc), "r"(add)
+      : "memory");
+}
+// S = Q K^T: twelve products over three chunks of 64 dims (Q's 16 KB apart), then the other stream's
+// turn, then S's barrier, one election.
+__device__ __forceinline__ void qk_turn(uint32_t d, uint32_t q, uint32_t k0, uint32_t k1, uint32_t k2, uint32_t hi,
+                                        uint32_t idesc, uint32_t b_turn, uint32_t b_s) {
+  asm volatile(
+      "{\n .reg .pred e, on;\n .reg .b32 x, y;\n .reg .b64 k, q;\n elect.sync _|e, 0xffffffff;\n"
+      " setp.eq.b32 on, 0, 0;\n"
+      " add.u32 x, %2, 0; mov.b64 k, {x, %5}; add.u32 y, %1, 0; mov.b64 q, {y, %5};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %6, !on;\n"
+      " add.u32 x, %2, 2; mov.b64 k, {x, %5}; add.u32 y, %1, 2; mov.b64 q, {y, %5};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %6, on;\n"
+      " add.u32 x, %2, 4; mov.b64 k, {x, %5}; add.u32 y, %1, 4; mov.b64 q, {y, %5};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %6, on;\n"
+      " add.u32 x, %2, 6; mov.b64 k, {x, %5}; add.u32 y, %1, 6; mov.b64 q, {y, %5};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %6, on;\n"
+      " add.u32 x, %3, 0; mov.b64 k, {x, %5}; add.u32 y, %1, 1024; mov.b64 q, {y, %5};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %6, on;\n"
+      " add.u32 x, %3, 2; mov.b64 k, {x, %5}; add.u32 y, %1, 1026; mov.b64 q, {y, %5};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %6, on;\n"
+      " add.u32 x, %3, 4; mov.b64 k, {x, %5}; add.u32 y, %1, 1028; mov.b64 q, {y, %5};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %6, on;\n"
+      " add.u32 x, %3, 6; mov.b64 k, {x, %5}; add.u32 y, %1, 1030; mov.b64 q, {y, %5};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %6, on;\n"
+      " add.u32 x, %4, 0; mov.b64 k, {x, %5}; add.u32 y, %1, 2048; mov.b64 q, {y, %5};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %6, on;\n"
+      " add.u32 x, %4, 2; mov.b64 k, {x, %5}; add.u32 y, %1, 2050; mov.b64 q, {y, %5};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %6, on;\n"
+      " add.u32 x, %4, 4; mov.b64 k, {x, %5}; add.u32 y, %1, 2052; mov.b64 q, {y, %5};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %6, on;\n"
+      " add.u32 x, %4, 6; mov.b64 k, {x, %5}; add.u32 y, %1, 2054; mov.b64 q, {y, %5};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %6, on;\n"
+      " @e mbarrier.arrive.shared::cta.b64 _, [%7];\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%8];\n}" ::"r"(d),
+      "r"(q), "r"(k0), "r"(k1), "r"(k2), "r"(hi), "r"(idesc), "r"(b_turn), "r"(b_s)
+      : "memory");
+}
+
 // Asks for a block of the grid that has not begun: its index, or that there is none, comes into 16
 // bytes of shared memory.
 __device__ __forceinline__ void ask_next(uint32_t dst, uint32_t bar) {
@@ -331,10 +378,15 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
   s.status = a.status;
   s.wait_ns = a.wait_ns;
 
+  Round requests;                // warp 3: the first 32 requests
   if (warp == 1) {
     tmem_alloc(s.base + kOffMisc, 512);
     tmem_relinquish();
-  } else if (tid == 0) {
+  } else if (warp == 3) {
+    requests.load(a, lane, lane, 0, 0);
+  } else if (tid < 4) {
+    prefetch_tensormap(tid == 0 ? &qmap : tid == 1 ? &kmap : tid == 2 ? &rmap : &vmap);
+  } else if (tid == 64) {
     *s.abort = 0;
     for (int i = 0; i < B_COUNT; ++i) {
       const bool of_warps = (i >= B_PFULL && i < B_PFULL + 4) || i == B_OFREE || i == B_OFREE + 1;
@@ -363,8 +415,6 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
     // ---- units: this block's own, then those of blocks that have not begun ---------------------
     uint32_t x = blockIdx.x, y = blockIdx.y, asked = 0, k = 0;
     bool some = true, ok = true;
-    Round requests;
-    requests.load(a, lane, lane, 0, 0);
     while (ok) {
       Unit u;
       u.head = -1;
@@ -483,10 +533,10 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
     const int t = warp - 1;
     const uint32_t id_qk = idesc_bf16(kM, kTile, false, false), id_pv = idesc_bf16(kM, 128, false, true);
     const uint64_t qd = smem_desc(s.base + kOffQ + t * kQChunks * kSlotBytes, 16, 1024, kSwizzle128B);
-    const uint64_t kd = smem_desc(s.base + kOffRing, 16, 1024, kSwizzle128B);
+    const uint32_t kd = (uint32_t)smem_desc(s.base + kOffRing, 16, 1024, kSwizzle128B);
     const uint64_t vd = smem_desc(s.base + kOffRing, kSlotBytes / 2, 1024, kSwizzle128B);
     constexpr unsigned kStep = kSlotBytes / 16;
-    const uint32_t ds = tmem + t * 128, d_o = ds + 256;
+    const uint32_t ds = tmem + t * 128, d_o = ds + 256, hi = (uint32_t)(qd >> 32), vhi = (uint32_t)(vd >> 32);
     const Unit* unit;
     uint32_t k = 0;
     unsigned sl = 0;                            // slot of tile j's keys
@@ -526,11 +576,11 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
         if (!ok) break;
         tc_fence_after();
         if (pv) {
-          mma4_ts_mn_warp(d_o, ds, vd + v0 * kStep, id_pv, !first);
+          pv_half(d_o, ds, (uint32_t)vd + v0 * kStep, vhi, id_pv, !first);
           ok = s.wait(B_PFULL + 2 * t + 1, pv_tiles & 1);
           if (!ok) break;
           tc_fence_after();
-          mma4_ts_mn_warp(d_o, ds + 32, vd + v1 * kStep, id_pv, 1);
+          pv_half(d_o, ds + 32, (uint32_t)vd + v1 * kStep, vhi, id_pv, 1);
           ++pv_tiles;
         }
         if (j > u.begin) mma_commit_warp(s.bar(B_EMPTY + gv));
@@ -538,11 +588,12 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
           ok = s.wait(B_FULL + g, par);
           if (!ok) break;
           tc_fence_after();
-          mma12_ss_warp(ds, qd, kd + sl * kStep, kd + (sl + 1) % kSlots * kStep, kd + (sl + 2) % kSlots * kStep, id_qk);
-          mma_commit_warp(s.bar(B_SFULL + t));
+          qk_turn(ds, (uint32_t)qd, kd + sl * kStep, kd + (sl + 1) % kSlots * kStep, kd + (sl + 2) % kSlots * kStep, hi,
+                  id_qk, s.bar(B_TURN + (t ^ 1)), s.bar(B_SFULL + t));
+        } else {
+          if (lane == 0) mbar_arrive(s.bar(B_TURN + (t ^ 1)));
+          __syncwarp();
         }
-        if (lane == 0) mbar_arrive(s.bar(B_TURN + (t ^ 1)));
-        __syncwarp();
         ++turn;
         if (pv && j == mine) mma_commit_warp(s.bar(B_OFULL + t));
         if (qk && j + 1 == mine) mma_commit_warp(s.bar(B_QEMPTY + t));
@@ -586,6 +637,11 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
 #pragma unroll
           for (int c = 0; c < 128; ++c) x[c] = c < lim ? x[c] : -INFINITY;
         }
+        // P of the first 64 keys by the reference so far, beside the maximum: it seldom moves
+        const float2 mul = make_float2(a.scale_log2, a.scale_log2);
+        float ref = m == -INFINITY ? 0.f : m;
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        uint32_t pk[32];
         float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
         for (int c = 4; c < 124; c += 8)
@@ -594,6 +650,8 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
 #pragma unroll
         for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], x[124 + i]);
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) pk[i] = weights(make_float2(x[2 * i], x[2 * i + 1]), mul, -ref, sum[i & 1]);
         // the reference moves where a maximum rose too far (from nothing at the first)
         const bool moves = top > m + kRise;
         if (__any_sync(0xffffffffu, moves)) {
@@ -610,32 +668,37 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
               for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
               tmem_st16(to + 16 * c, o);
             }
-        }
-        const float ref = m == -INFINITY ? 0.f : m;
-        const float2 mul = make_float2(a.scale_log2, a.scale_log2), sub = make_float2(-ref, -ref);
-        const float2 one = make_float2(1.f, 1.f);
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        // P of 64 keys, then of the other 64: the first half's product starts meanwhile
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
+          // and P again, from S
+          ref = m == -INFINITY ? 0.f : m;
+          sum[0] = sum[1] = make_float2(0.f, 0.f);
+          const int lim = mine - j * kTile;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            uint32_t pk[16];
+            uint32_t y[32];
+            tmem_ld32(ts + 32 * c, y);
+            tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const int d = 64 * h + 32 * c + 2 * i;
-              const float2 e = fma2(make_float2(x[d], x[d + 1]), mul, sub);
-              const float2 p = make_float2(exp2_fast(e.x), exp2_fast(e.y));
-              sum[i & 1] = fma2(p, one, sum[i & 1]);
-              pk[i] = pack(p.x, p.y);
+              const int d = 32 * c + 2 * i;
+              pk[16 * c + i] = weights(make_float2(d < lim ? __uint_as_float(y[2 * i]) : -INFINITY,
+                                                   d + 1 < lim ? __uint_as_float(y[2 * i + 1]) : -INFINITY),
+                                       mul, -ref, sum[i & 1]);
             }
-            tmem_st16(ts + 32 * h + 16 * c, pk);
           }
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(s.bar(B_PFULL + 2 * t + h));
         }
+        // the first half's product starts while P of the other is computed
+        tmem_st32(ts, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s.bar(B_PFULL + 2 * t));
+#pragma unroll
+        for (int i = 0; i < 32; ++i) pk[i] = weights(make_float2(x[64 + 2 * i], x[65 + 2 * i]), mul, -ref, sum[i & 1]);
+        tmem_st32(ts + 32, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s.bar(B_PFULL + 2 * t + 1));
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
       if (!ok) break;
@@ -683,7 +746,8 @@ void device_setup(PrefillDevice& d) {
   d.err = cudaFuncSetAttribute(mla_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
 }
 
-long long row_tiles(int T, int B) { return (long long)T / (2 * kM) + (B < T ? B : T); }
+// Row tiles at most: sum ceil(n_b / 256) <= sum (n_b + 255) / 256, requests without rows left out.
+long long row_tiles(int T, int B) { return (T + (2LL * kM - 1) * (B < T ? B : T)) / (2 * kM); }
 
 // Parts that each request's keys are cut into: as many as fill the SMs, each of 256 keys or more
 // if a request had all key rows.
