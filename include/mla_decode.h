@@ -435,12 +435,12 @@ int cp_rope_store(const void* latent, int64_t latent_stride, const void* k_rope,
  *   w_kv         bf16 [H, 256, 512], 16-byte aligned.
  *   kv           bf16 [H, S, 256];  k_rope  bf16 [S, 64]; 16-byte aligned.  Rows from S on are not
  *                written.
- *   B >= 0, S >= 0, 1 <= H <= 2^22, 1 <= max_blocks <= bt_stride, num_blocks >= 1.
+ *   B >= 0, S >= 0, H >= 1, (S/256 + 1) * 2 H below 2^31 - 512, 1 <= max_blocks <= bt_stride, num_blocks >= 1.
  * A page outside [0, num_blocks) reads as zeros with MLA_STATUS_BAD_PAGE, a length beyond the table
  * is cut with MLA_STATUS_SEQ_TOO_LONG, a scale out of range is taken as 1 with
  * MLA_STATUS_BAD_SCALE.  kv_starts out of order leave rows unwritten or give them to another request.
- * Errors: MLA_ERR_INVALID_ARGUMENT, MLA_ERR_UNSUPPORTED (max_blocks*block_size beyond 2^31-1),
- *   MLA_ERR_CUDA.
+ * Errors: MLA_ERR_INVALID_ARGUMENT, MLA_ERR_UNSUPPORTED (max_blocks*block_size beyond 2^31-1, or
+ *   too many tiles), MLA_ERR_CUDA.
  */
 int mla_expand(const void* kv_cache, const float* kv_scales, const int32_t* block_table,
                int64_t bt_stride, const int32_t* seq_lens, const int32_t* kv_starts, int B,

@@ -681,7 +681,8 @@ int mla_expand(const void* kv_cache, const float* kv_scales, const int32_t* bloc
                 (long long)bt_stride);
   if ((long long)max_blocks * block_size > (1LL << 31) - 1)
     return fail(MLA_ERR_UNSUPPORTED, "%s: max_blocks*block_size exceeds 2^31-1", fn);
-  if (H > (1 << 22)) return fail(MLA_ERR_UNSUPPORTED, "%s: H exceeds 2^22", fn);
+  if (S > INT_MAX - 512 || (S / 256 + 1LL) * 2 * H > INT_MAX - 512)
+    return fail(MLA_ERR_UNSUPPORTED, "%s: S or (S/256 + 1) * 2 H too close to 2^31", fn);
   if (B == 0 || S == 0) return ok();
   if (!kv_cache || !block_table || !seq_lens || !kv_starts || !w_kv || !kv || !k_rope)
     return fail(MLA_ERR_INVALID_ARGUMENT, "%s: null kv_cache/block_table/seq_lens/kv_starts/w_kv/kv/k_rope", fn);

@@ -7,20 +7,22 @@
 // A matrix product of K = 512 with gathered rows: 1,024 operations for each 2-byte output, so
 // bound by the tensor cores, with an output stream of over half the memory's rate beside it.
 //
-// Design.  A tile is 128 rows x 128 output dims (half of a head).  The gathered rows are the A
-// operand and stay in tensor memory (512 dims are 256 columns), since each is used for all heads;
-// the other 256 columns are two accumulators, so that one is written out while the other is
-// computed.  Only W passes through shared memory: 16 KB chunks of 128 dims x 64 in a ring of 12, by
-// TMA.  A pair of SMs (a cluster of two) works on two neighbouring row tiles with the same W: each
-// loads half of a chunk and multicasts it to both, which halves what W takes of the L2's rate (32
-// bytes a clock and SM).  The tiles of all row pairs are one sequence, row pair after row pair, cut
-// evenly over the clusters; a cluster gathers rows only when its row pair changes.
+// Design.  A pair of SMs (a cluster of two, cta_group::2) computes tiles of 256 rows x 128 output dims
+// (half of a head).  The gathered rows are the A operand and stay in tensor memory, 128 rows an SM
+// (512 dims are 256 columns), since each is used for all heads; 256 more columns are two accumulators,
+// so that one is written out while the other is computed.  Only W passes through shared memory, by
+// TMA, 64 of a tile's 128 dims on each SM: 32 KB (64 dims x 256 latent dims) in a ring of five, 32 bytes
+// a clock and SM at the full rate of the products (a tile of 128 rows on each SM by itself takes twice
+// that, and was bound by it: 223 us for 8,192 rows and 128 heads).  The tiles of all row pairs are one
+// sequence, row pair after row pair, cut evenly over the clusters; a cluster gathers rows only when
+// its row pair changes.  The first SM of a pair issues all products.
 //
 // Rows are gathered by four warps, a thread a row, straight into tensor memory: any page size and
 // any start, and the 8-bit form's conversion costs nothing but there.
 //
 // Safety: every wait is bounded (sm100.cuh); rows of no request, and pages or lengths out of range,
 // are read as zeros and not written (the latter flagged).
+#include <limits.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -33,6 +35,7 @@
 #include <cudaTypedefs.h>
 
 #include "internal.h"
+#include "lanes.cuh"
 #include "sm100.cuh"
 #include "tma_map.h"
 #include "../../include/mla_decode.h"
@@ -43,25 +46,31 @@ namespace {
 using namespace sm100;
 
 constexpr int kLatent = 512, kRow = 576;
-constexpr int kM = 128, kN = 128;
-constexpr int kChunkBytes = kN * 128;              // 128 dims of W x 64 latent dims, bf16
-constexpr int kChunks = kLatent / 64;
-constexpr int kStages = 12;
-constexpr int kThreads = 384;                      // warp 0 TMA, 1 MMA; 4-7 epilogue; 8-11 rows
+constexpr int kM = 128, kN = 128;                  // rows an SM, output dims of a tile
+constexpr int kStageDims = 256;                    // latent dims of a stage of W
+constexpr int kBoxBytes = (kN / 2) * 128;          // 64 dims of W x 64 latent dims, bf16
+constexpr int kStageBytes = kStageDims / 64 * kBoxBytes;
+constexpr int kStages = 5;
+constexpr int kRowDims = 128;                      // latent dims that are handed over with a row tile
+constexpr int kRowSteps = kLatent / kRowDims;
+// warp 0 TMA, 1 MMA; 4-7 and 8-11 outputs, a set an accumulator; 12-15 and 16-19 rows, a set every other
+// 128 dims
+constexpr int kThreads = 640;
 constexpr uint32_t kColD = 256;                    // accumulators; A is columns 0..255
 
-constexpr int kOffStage = kStages * kChunkBytes;   // 4 warps x 32 rows x 256 bytes
-constexpr int kOffBar = kOffStage + 4 * 32 * 256;
+constexpr int kOffStage = kStages * kStageBytes;   // 8 warps x 32 rows x 256 bytes
+constexpr int kOffBar = kOffStage + 8 * 32 * 256;
 constexpr int kOffMisc = kOffBar + 512;
 constexpr int kSmemBytes = kOffMisc + 64 + 1024;
 
+// Those marked "pair" are the first SM's, for both; commits arrive on the others in both SMs.
 enum Bar : int {
-  B_FULL = 0,                    // [12] W chunk here (both halves)
-  B_EMPTY = B_FULL + kStages,    // [12] both SMs have used it
-  B_AFULL = B_EMPTY + kStages,   // [8] 64 dims of the rows in tensor memory
-  B_AFREE = B_AFULL + kChunks,   // the row tile's last product is done
-  B_DFULL = B_AFREE + 1,         // [2]
-  B_DFREE = B_DFULL + 2,         // [2]
+  B_FULL = 0,                    // [5] pair: W here, both SMs' parts
+  B_EMPTY = B_FULL + kStages,    // [5] the products have read it
+  B_AFULL = B_EMPTY + kStages,   // [4] pair: 128 dims of the rows in tensor memory
+  B_AFREE = B_AFULL + kRowSteps,    // [4] the row tile's last product of these dims is done
+  B_DFULL = B_AFREE + kRowSteps,    // [2]
+  B_DFREE = B_DFULL + 2,         // [2] pair
   B_DRAIN = B_DFREE + 2,
   B_COUNT = B_DRAIN + 1
 };
@@ -79,36 +88,50 @@ struct Ctx {
   unsigned long long wait_ns;
   __device__ __forceinline__ uint32_t bar(int i) const { return base + kOffBar + 8 * i; }
   __device__ __forceinline__ bool wait(int i, uint32_t parity, bool cluster = false) const {
-    return __all_sync(0xffffffffu, mbar_wait(bar(i), parity, abort, status, wait_ns, cluster));
+    if (__all_sync(0xffffffffu, cluster ? mbar_try_wait_cluster(bar(i), parity) : mbar_try_wait(bar(i), parity)))
+      return true;
+    return __all_sync(0xffffffffu, mbar_wait_slow(bar(i), parity, abort, status, wait_ns, cluster));
   }
 };
 
-// The key that output row r holds: the request is the last one that starts at r or before.
+// The key that output row r holds (a row a lane): the request is the last one that starts at r or before.
 struct Key {
   const uint8_t* row;            // null: none
   float scale;
 };
 
 template <bool kQ8>
-__device__ __forceinline__ Key find_key(const ExpandArgs& a, long long r, unsigned& flags) {
+__device__ __forceinline__ Key find_key(const ExpandArgs& a, int r, int lane, unsigned& flags) {
   Key k{nullptr, 0.f};
-  if (r >= a.S) return k;
-  int lo = 0, hi = a.B;          // starts[lo - 1] <= r < starts[hi]
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(a.starts + mid) <= r) lo = mid + 1;
-    else hi = mid;
+  int lo = 0, start = 0, have = 0;              // requests that start at r or before
+  if (a.B <= 32) {
+    // a request a lane, one round trip
+    const int mine = lane < a.B ? __ldg(a.starts + lane) : INT_MAX;
+    const int lens = lane < a.B ? __ldg(a.seq_lens + lane) : 0;
+    for (int b = 0; b < a.B; ++b) lo += __shfl_sync(0xffffffffu, mine, b) <= r;
+    start = __shfl_sync(0xffffffffu, mine, max(lo - 1, 0));
+    have = __shfl_sync(0xffffffffu, lens, max(lo - 1, 0));
+  } else {
+    int hi = a.B;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(a.starts + mid) <= r) lo = mid + 1;
+      else hi = mid;
+    }
+    if (lo > 0) {
+      start = __ldg(a.starts + lo - 1);
+      have = __ldg(a.seq_lens + lo - 1);
+    }
   }
-  if (lo == 0) return k;
+  if (lo == 0 || r >= a.S) return k;
   const int b = lo - 1;
-  const long long l = r - __ldg(a.starts + b);
-  long long have = __ldg(a.seq_lens + b);
-  if (have > (long long)a.max_blocks * a.block_size) {
-    have = (long long)a.max_blocks * a.block_size;
+  const unsigned l = (unsigned)r - (unsigned)start;                    // r >= start
+  if (have > a.max_blocks * a.block_size) {                            // (below 2^31)
+    have = a.max_blocks * a.block_size;
     flags |= MLA_STATUS_SEQ_TOO_LONG;
   }
-  if (l >= have) return k;
-  const int blk = (int)(l / a.block_size), off = (int)(l - (long long)blk * a.block_size);
+  if (have < 0 || l >= (unsigned)have) return k;
+  const unsigned blk = l / (unsigned)a.block_size, off = l - blk * (unsigned)a.block_size;
   const int page = __ldg(a.block_table + (long long)b * a.bt_stride + blk);
   if (page < 0 || page >= a.num_blocks) {
     flags |= MLA_STATUS_BAD_PAGE;
@@ -116,7 +139,7 @@ __device__ __forceinline__ Key find_key(const ExpandArgs& a, long long r, unsign
     k.scale = -1.f;              // a row of the request all the same: zeros are written
     return k;
   }
-  const long long slot = (long long)page * a.block_size + off;
+  const long long slot = (long long)page * a.block_size + (int)off;
   k.row = static_cast<const uint8_t*>(a.cache) + slot * (kQ8 ? kRow : 2 * kRow);
   k.scale = 1.f;
   if (kQ8) {
@@ -134,50 +157,117 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// 64 dims of a row, from dim `d`, as 32 words of two bf16.
-template <bool kQ8>
-__device__ __forceinline__ void load64(const Key& k, int d, uint32_t (&v)[32]) {
-  if (k.row == nullptr) {
+// 128 bytes of the rows of a warp's lanes, from byte `at` on, each lane its own row's; absent rows
+// give zeros.  Eight lanes read a row's.
+__device__ __forceinline__ void load_rows(const uint8_t* row, int at, int lane, uint32_t (&v)[32]) {
+  const unsigned long long mine = reinterpret_cast<unsigned long long>(row);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = 0;
-  } else if (!kQ8) {
-    const uint4* s = reinterpret_cast<const uint4*>(k.row + 2 * d);
+  for (int r = 0; r < 8; ++r) {
+    const uint8_t* src = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, mine, (lane & 24) + r));
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (src != nullptr) x = __ldg(reinterpret_cast<const uint4*>(src + at) + (lane & 7));
+    v[4 * r] = x.x;
+    v[4 * r + 1] = x.y;
+    v[4 * r + 2] = x.z;
+    v[4 * r + 3] = x.w;
+  }
+}
+// 64 e4m3 values from word kFirst on, times the scale, as 32 words of two bf16.
+template <int kFirst>
+__device__ __forceinline__ void widen(const uint32_t (&v)[32], float scale, uint32_t (&o)[32]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint4 x = __ldg(s + i);
-      v[4 * i] = x.x;
-      v[4 * i + 1] = x.y;
-      v[4 * i + 2] = x.z;
-      v[4 * i + 3] = x.w;
-    }
-  } else {
-    const uint4* s = reinterpret_cast<const uint4*>(k.row + d);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint4 x = __ldg(s + i);
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        uint32_t h;
-        const uint16_t two = (uint16_t)(w[q >> 1] >> (16 * (q & 1)));
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        v[8 * i + q] = pack(f.x * k.scale, f.y * k.scale);
-      }
-    }
+  for (int q = 0; q < 32; ++q) {
+    uint32_t h;
+    const uint16_t two = (uint16_t)(v[kFirst + (q >> 1)] >> (16 * (q & 1)));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    o[q] = pack(f.x * scale, f.y * scale);
   }
 }
 
-// W chunk: 64 rows (output dims) x 64 latent dims into both SMs of the pair.
-__device__ __forceinline__ void tma_load_2d_both_warp(uint32_t dst, const CUtensorMap* map, int x,
-                                                      int y, uint32_t bar) {
+// A cluster's tiles: of row pair `pair` from output tile `col` on, `n` of them, row pair after row pair.
+struct Range {
+  int pair, col, n;
+};
+// Tiles are cut evenly over the C clusters; or each row pair's over clusters of its own, where that
+// gives none more than kGather tiles more: gathering rows takes as long as that.  (8,192 rows, 128
+// heads: 32 row pairs, 76 clusters; cut evenly, 108 tiles each and often two row pairs, 190 us before
+// and after for 128 tiles of one.)
+constexpr int kGather = 2;
+__device__ __forceinline__ Range cut(unsigned pairs, unsigned cols, unsigned C, unsigned c) {
+  const unsigned all = pairs * cols;             // below 2^31 - 256
+  unsigned u0 = 0, u1 = 0;
+  if (pairs > 0 && pairs <= C && (cols + C / pairs - 1) / (C / pairs) <= all / C + kGather) {
+    const unsigned mp = ((c + 1) * pairs - 1) / C;             // its clusters: from c0, before c1
+    const unsigned c0 = mp * C / pairs, c1 = (mp + 1) * C / pairs;
+    u0 = mp * cols + cols * (c - c0) / (c1 - c0);
+    u1 = mp * cols + cols * (c + 1 - c0) / (c1 - c0);
+  } else {
+    u0 = (unsigned)((unsigned long long)all * c / C);
+    u1 = (unsigned)((unsigned long long)all * (c + 1) / C);
+  }
+  Range r;
+  r.pair = (int)(u0 / cols);
+  r.col = (int)(u0 - (u0 / cols) * cols);
+  r.n = (int)(u1 - u0);
+  return r;
+}
+
+// ---- instructions of a pair of SMs ------------------------------------------------------------
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish_pair() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// Arrive on a barrier at a shared::cluster address.  What is handed over lies in tensor memory, which
+// tcgen05's own waits and fences order; with .release.cluster the arrival waited until the output
+// rows stored before it had reached the L2 (2,000 clocks and more a tile).
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+// A tile into this SM's shared memory, its bytes counted by the barrier at a shared::cluster address
+// (the pair's first SM's).  Warp-collective.
+__device__ __forceinline__ void tma_load_2d_pair_warp(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                                      uint32_t cluster_bar) {
   asm volatile(
       "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
-      " @e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".multicast::cluster [%0], [%1, {%2, %3}], [%4], %5;\n}" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "h"((uint16_t)3)
+      " @e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3}], [%4];\n}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(cluster_bar)
       : "memory");
 }
+// Eight products along K (A: tensor memory columns +8 each; B: +32 bytes each, the second four in the
+// next box), 256 rows on two SMs; `add` applies to the first.  Warp-collective, one election.
+__device__ __forceinline__ void mma8_pair_warp(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n .reg .pred p, t, e;\n .reg .b32 y;\n .reg .b64 k;\n"
+      " setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, 0, 0;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n"
+      " add.u32 y, %1, 8; add.u64 k, %2, 2;\n @e tcgen05.mma.cta_group::2.kind::f16 [%0], [y], k, %3, t;\n"
+      " add.u32 y, %1, 16; add.u64 k, %2, 4;\n @e tcgen05.mma.cta_group::2.kind::f16 [%0], [y], k, %3, t;\n"
+      " add.u32 y, %1, 24; add.u64 k, %2, 6;\n @e tcgen05.mma.cta_group::2.kind::f16 [%0], [y], k, %3, t;\n"
+      " add.u32 y, %1, 32; add.u64 k, %2, 512;\n @e tcgen05.mma.cta_group::2.kind::f16 [%0], [y], k, %3, t;\n"
+      " add.u32 y, %1, 40; add.u64 k, %2, 514;\n @e tcgen05.mma.cta_group::2.kind::f16 [%0], [y], k, %3, t;\n"
+      " add.u32 y, %1, 48; add.u64 k, %2, 516;\n @e tcgen05.mma.cta_group::2.kind::f16 [%0], [y], k, %3, t;\n"
+      " add.u32 y, %1, 56; add.u64 k, %2, 518;\n @e tcgen05.mma.cta_group::2.kind::f16 [%0], [y], k, %3, t;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(add)
+      : "memory");
+}
+// An arrival on `bar` in both SMs once all products before are done.
+__device__ __forceinline__ void commit_pair_warp(uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}" ::
+          "r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+static_assert(kBoxBytes / 16 == 512, "the second box's descriptors");
 
 template <bool kQ8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -197,51 +287,53 @@ mla_expand_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
     *s.abort = 0;
     for (int i = 0; i < kStages; ++i) {
       mbar_init(s.bar(B_FULL + i), 1);
-      mbar_init(s.bar(B_EMPTY + i), 2);
+      mbar_init(s.bar(B_EMPTY + i), 1);
     }
-    for (int i = 0; i < kChunks; ++i) mbar_init(s.bar(B_AFULL + i), 4);
-    mbar_init(s.bar(B_AFREE), 1);
+    for (int i = 0; i < kRowSteps; ++i) {
+      mbar_init(s.bar(B_AFULL + i), 8);
+      mbar_init(s.bar(B_AFREE + i), 1);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(s.bar(B_DFULL + i), 1);
-      mbar_init(s.bar(B_DFREE + i), 4);
+      mbar_init(s.bar(B_DFREE + i), 8);
     }
     mbar_init(s.bar(B_DRAIN), 1);
     fence_mbar_init();
   }
+  if (tid == 32) prefetch_tensormap(&wmap);
   if (warp == 1) {
-    tmem_alloc(s.base + kOffMisc, 512);
-    tmem_relinquish();
+    tmem_alloc_pair(s.base + kOffMisc, 512);
+    tmem_relinquish_pair();
   }
   // rows in use: the last request's end (requests are in the order of their rows)
-  long long rows = 0;
-  if (p.a.B > 0)
-    rows = (long long)__ldg(p.a.starts + p.a.B - 1) + max(0, __ldg(p.a.seq_lens + p.a.B - 1));
-  rows = rows < 0 ? 0 : rows > p.a.S ? p.a.S : rows;
+  long long end = (long long)__ldg(p.a.starts + p.a.B - 1) + max(0, __ldg(p.a.seq_lens + p.a.B - 1));
+  const int rows = (int)(end < 0 ? 0 : end > p.a.S ? p.a.S : end);
   tc_fence_before();
   __syncthreads();
-  cluster_sync();
+  cluster_sync_relaxed();        // the barriers are initialised (fence_mbar_init) in both SMs
   tc_fence_after();
   const uint32_t tmem = misc[0];
 
-  const long long units = (rows + 2 * kM - 1) / (2 * kM) * p.col_tiles;
-  const long long C = nclusters_x(), c = cluster_id_x();
-  const long long u0 = units * c / C, u1 = units * (c + 1) / C;
+  const Range range = cut((rows + 2 * kM - 1) / (2 * kM), p.col_tiles, nclusters_x(), cluster_id_x());
   unsigned flags = 0;
 
   if (warp == 0) {
-    // ---- W chunks ---------------------------------------------------------------------
+    // ---- W: this SM's 64 of a tile's 128 dims ---------------------------------------------
     int st = 0;
     uint32_t par = 1;
-    long long issued = 0;
+    unsigned issued = 0;
     bool ok = true;
-    for (long long u = u0; u < u1 && ok; ++u) {
-      const int n0 = (int)(u % p.col_tiles) * kN + 64 * (int)cr;
-      for (int k = 0; k < kChunks; ++k) {
+    int col = range.col;
+    for (int i = 0; i < range.n && ok; ++i, col = col + 1 == p.col_tiles ? 0 : col + 1) {
+      const int n0 = col * kN + (kN / 2) * (int)cr;
+      for (int k = 0; k < kLatent; k += kStageDims) {
         ok = s.wait(B_EMPTY + st, par, true);
         if (!ok) break;
-        mbar_arrive_expect_tx_warp(s.bar(B_FULL + st), kChunkBytes);
-        tma_load_2d_both_warp(s.base + st * kChunkBytes + cr * (kChunkBytes / 2), &wmap, 64 * k, n0,
-                              s.bar(B_FULL + st));
+        if (cr == 0) mbar_arrive_expect_tx_warp(s.bar(B_FULL + st), 2 * kStageBytes);
+        const uint32_t full = mapa(s.bar(B_FULL + st), 0), dst = s.base + st * kStageBytes;
+#pragma unroll
+        for (int c = 0; c < kStageDims / 64; ++c)
+          tma_load_2d_pair_warp(dst + c * kBoxBytes, &wmap, k + 64 * c, n0, full);
         ++issued;
         if (++st == kStages) {
           st = 0;
@@ -249,122 +341,161 @@ mla_expand_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
         }
       }
     }
-    // the peer's last releases arrive here before this SM ends; after an abort, the copies do
-    for (long long m = issued > kStages ? issued - kStages : 0; m < issued; ++m) {
+    // the last releases arrive here, and so all copies have, before this SM ends; after an abort the
+    // first SM waits for the copies themselves
+    for (unsigned m = issued > kStages ? issued - kStages : 0; m < issued; ++m) {
       const int i = (int)(m % kStages);
-      const uint32_t ph = (uint32_t)((m / kStages) & 1);
-      if (!ok || !s.wait(B_EMPTY + i, ph, true)) mbar_wait_drain(s.bar(B_FULL + i), ph);
+      const uint32_t ph = m / kStages & 1;
+      if ((!ok || !s.wait(B_EMPTY + i, ph, true)) && cr == 0) mbar_wait_drain(s.bar(B_FULL + i), ph);
     }
   } else if (warp == 1) {
-    // ---- products ---------------------------------------------------------------------
-    const uint32_t idesc = idesc_bf16(kM, kN, false, false);
+    // ---- products (the first SM's warp, for both) -------------------------------------------
+    const uint32_t idesc = idesc_bf16(2 * kM, kN, false, false);
+    const uint64_t wd = smem_desc(s.base, 16, 1024, kSwizzle128B);
     int st = 0;
     uint32_t par = 0, apar = 0;
-    bool ok = true;
-    long long n = 0;
-    for (long long u = u0; u < u1 && ok; ++u, ++n) {
-      const bool fresh = u == u0 || u % p.col_tiles == 0;
-      const bool last = u + 1 == u1 || (u + 1) % p.col_tiles == 0;
-      const int g = (int)(n & 1);
-      ok = s.wait(B_DFREE + g, (uint32_t)(((n >> 1) + 1) & 1));
-      for (int k = 0; k < kChunks && ok; ++k) {
-        if (fresh) ok = s.wait(B_AFULL + k, apar);
-        ok = ok && s.wait(B_FULL + st, par, true);
+    bool ok = cr == 0;
+    int col = range.col;
+    for (int n = 0; n < range.n && ok; ++n, col = col + 1 == p.col_tiles ? 0 : col + 1) {
+      const bool fresh = n == 0 || col == 0;
+      const bool last = n + 1 == range.n || col + 1 == p.col_tiles;
+      const int g = n & 1;
+      ok = s.wait(B_DFREE + g, (uint32_t)(((n >> 1) + 1) & 1), true);
+#pragma unroll
+      for (int k = 0; k < kRowSteps && ok; ++k) {
+        const bool stage = k % (kStageDims / kRowDims) == 0;        // W's next stage begins
+        if (fresh) ok = s.wait(B_AFULL + k, apar, true);
+        if (stage) ok = ok && s.wait(B_FULL + st, par, true);
         if (!ok) break;
-        tc_fence_after();
-        mma4_ts_warp(tmem + kColD + g * kN, tmem + 32 * k,
-                     smem_desc(s.base + st * kChunkBytes, 16, 1024, kSwizzle128B), idesc, k != 0);
-        mma_commit_multicast_warp(s.bar(B_EMPTY + st), (uint16_t)3);
+        if (fresh || stage) tc_fence_after();
+        mma8_pair_warp(tmem + kColD + g * kN, tmem + 64 * k,
+                       wd + st * (kStageBytes / 16) + (stage ? 0 : 2 * kBoxBytes / 16), idesc, k != 0);
+        if (last) commit_pair_warp(s.bar(B_AFREE + k));
+        if (stage) continue;
+        commit_pair_warp(s.bar(B_EMPTY + st));
         if (++st == kStages) {
           st = 0;
           par ^= 1u;
         }
       }
       if (!ok) break;
-      mma_commit_warp(s.bar(B_DFULL + g));
+      commit_pair_warp(s.bar(B_DFULL + g));
       if (fresh) apar ^= 1u;
-      if (last) mma_commit_warp(s.bar(B_AFREE));
     }
-    mma_commit_warp(s.bar(B_DRAIN));
-    mbar_wait_drain(s.bar(B_DRAIN), 0);
-  } else if (warp >= 8) {
+    if (cr == 0) commit_pair_warp(s.bar(B_DRAIN));
+  } else if (warp >= 12) {
     // ---- rows into tensor memory: thread = row ------------------------------------------
     const uint32_t ta = tmem + ((uint32_t)(warp & 3) << 21);
+    const int set = warp >= 16;
     bool ok = true;
-    long long m = 0;
-    for (long long u = u0; u < u1 && ok; u = (u / p.col_tiles + 1) * p.col_tiles, ++m) {
-      const long long r = (u / p.col_tiles * 2 + cr) * kM + (warp & 3) * 32 + lane;
-      const Key key = find_key<kQ8>(p.a, r, flags);
-      ok = s.wait(B_AFREE, (uint32_t)((m + 1) & 1));
-      if (!ok) break;
-      tc_fence_after();
+    uint32_t m = 0;
+    // its row pairs: the first from output tile range.col on, the others from 0
+    for (int col = range.col, left = range.n; left > 0 && ok; left -= p.col_tiles - col, col = 0, ++m) {
+      const int r = ((range.pair + (int)m) * 2 + (int)cr) * kM + (warp & 3) * 32 + lane;
+      const Key key = find_key<kQ8>(p.a, r, lane, flags);
 #pragma unroll 1
-      for (int k = 0; k < kChunks; k += 2) {
+      for (int k = set; k < kRowSteps; k += 2) {
+        // 128 dims of the row: 128 bytes of e4m3 or twice that of bf16
         uint32_t v[32], w[32];
-        load64<kQ8>(key, 64 * k, v);
-        load64<kQ8>(key, 64 * k + 64, w);
-        tmem_st32(ta + 32 * k, v);
-        tmem_st32(ta + 32 * k + 32, w);
+        load_rows(key.row, kRowDims * (kQ8 ? 1 : 2) * k, lane, v);
+        if (!kQ8) load_rows(key.row, kRowDims * 2 * k + 128, lane, w);
+        ok = s.wait(B_AFREE + k, (m + 1) & 1, true);
+        if (!ok) break;
+        tc_fence_after();
+        transpose8(v, lane);
+        if (kQ8) {
+          uint32_t o[32];
+          widen<0>(v, key.scale, o);
+          tmem_st32(ta + 64 * k, o);
+          widen<16>(v, key.scale, o);
+          tmem_st32(ta + 64 * k + 32, o);
+        } else {
+          tmem_st32(ta + 64 * k, v);
+          transpose8(w, lane);
+          tmem_st32(ta + 64 * k + 32, w);
+        }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(s.bar(B_AFULL + k));
-          mbar_arrive(s.bar(B_AFULL + k + 1));
-        }
+        if (lane == 0) mbar_arrive_pair(mapa(s.bar(B_AFULL + k), 0));
       }
+      if (!ok) break;
       // the cluster that has a row tile's first unit copies its rope keys
-      if (u % p.col_tiles == 0 && (key.row != nullptr || key.scale != 0.f)) {
-        uint32_t v[32];
-        load64<kQ8>(key, kLatent, v);
-        uint4* o = reinterpret_cast<uint4*>(p.a.k_rope + r * 64);
+      if (set == 0 && col == 0) {
+        const bool mine = key.row != nullptr || key.scale != 0.f;
+        uint8_t* out = reinterpret_cast<uint8_t*>(p.a.k_rope + (long long)r * 64);
+        if (kQ8) {
+          if (mine) {
+            uint4* dst = reinterpret_cast<uint4*>(out);
+            const uint4* src = reinterpret_cast<const uint4*>(key.row + kLatent);
+            uint32_t v[32], o[32];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            for (int i = 0; i < 4; ++i) {
+              const uint4 x = key.row != nullptr ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+              v[4 * i] = x.x;
+              v[4 * i + 1] = x.y;
+              v[4 * i + 2] = x.z;
+              v[4 * i + 3] = x.w;
+            }
+            widen<0>(v, key.scale, o);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        } else {
+          // bit for bit, eight lanes a row
+          uint32_t v[32];
+          load_rows(key.row, 2 * kLatent, lane, v);
+          const unsigned rows_here = __ballot_sync(0xffffffffu, mine);
+          out -= (lane & 7) * 128 - (lane & 7) * 16;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (rows_here >> ((lane & 24) + i) & 1u)
+              *reinterpret_cast<uint4*>(out + i * 128) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        }
       }
     }
   } else if (warp >= 4) {
     // ---- outputs: accumulator rows (thread = row) -> 256 bytes a row in shared memory ->
     // half a warp a row to memory
-    const int q = warp & 3;
-    uint8_t* stage = sp + kOffStage + q * 32 * 256;
-    const uint32_t td = tmem + kColD + ((uint32_t)q << 21);
+    const int q = warp & 3, g = (warp >> 2) - 1;  // the set's accumulator: every other tile
+    uint8_t* stage = sp + kOffStage + (warp - 4) * 32 * 256;
+    const uint32_t td = tmem + kColD + g * kN + ((uint32_t)q << 21);
     unsigned valid = 0;                           // the warp's rows that are somebody's
     bool ok = true;
-    long long n = 0, m0 = -1;
-    for (long long u = u0; u < u1 && ok; ++u, ++n) {
-      const long long mp = u / p.col_tiles;
-      const int nt = (int)(u - mp * p.col_tiles);
-      const long long r0 = (mp * 2 + cr) * kM + q * 32;
+    int m0 = -1, mp = range.pair, nt = range.col + g;
+    for (int n = 0; 2 * n + g < range.n && ok; ++n, nt += 2) {
+      while (nt >= p.col_tiles) {
+        nt -= p.col_tiles;
+        ++mp;
+      }
+      const int r0 = (mp * 2 + (int)cr) * kM + q * 32;
       if (mp != m0) {
         unsigned f = 0;
-        const Key key = find_key<kQ8>(p.a, r0 + lane, f);
+        const Key key = find_key<kQ8>(p.a, r0 + lane, lane, f);
         valid = __ballot_sync(0xffffffffu, key.row != nullptr || key.scale != 0.f);
         m0 = mp;
       }
-      const int g = (int)(n & 1);
-      ok = s.wait(B_DFULL + g, (uint32_t)((n >> 1) & 1));
+      ok = s.wait(B_DFULL + g, n & 1, true);
       if (!ok) break;
       tc_fence_after();
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t v[32], w[32];
-        tmem_ld32(td + g * kN + 64 * h, v);
-        tmem_ld32(td + g * kN + 64 * h + 32, w);
+#pragma unroll 1
+      for (int h = 0; h < 4; ++h) {
+        uint32_t v[32];
+        tmem_ld32(td + 32 * h, v);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t* x = i < 4 ? v + 8 * i : w + 8 * (i - 4);
+        for (int i = 0; i < 4; ++i) {
           uint4 o;
-          o.x = pack(__uint_as_float(x[0]), __uint_as_float(x[1]));
-          o.y = pack(__uint_as_float(x[2]), __uint_as_float(x[3]));
-          o.z = pack(__uint_as_float(x[4]), __uint_as_float(x[5]));
-          o.w = pack(__uint_as_float(x[6]), __uint_as_float(x[7]));
-          *reinterpret_cast<uint4*>(stage + lane * 256 + (((8 * h + i) ^ (lane & 7)) << 4)) = o;
+          o.x = pack(__uint_as_float(v[8 * i]), __uint_as_float(v[8 * i + 1]));
+          o.y = pack(__uint_as_float(v[8 * i + 2]), __uint_as_float(v[8 * i + 3]));
+          o.z = pack(__uint_as_float(v[8 * i + 4]), __uint_as_float(v[8 * i + 5]));
+          o.w = pack(__uint_as_float(v[8 * i + 6]), __uint_as_float(v[8 * i + 7]));
+          *reinterpret_cast<uint4*>(stage + lane * 256 + (((4 * h + i) ^ (lane & 7)) << 4)) = o;
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(s.bar(B_DFREE + g));
+      if (lane == 0) mbar_arrive_pair(mapa(s.bar(B_DFREE + g), 0));
       uint16_t* out = p.a.kv + ((long long)(nt >> 1) * p.a.S + r0) * 256 + (nt & 1) * 128;
 #pragma unroll 8
       for (int i = 0; i < 16; ++i) {
@@ -378,12 +509,18 @@ mla_expand_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
   }
   if (flags) atomicOr(p.a.status, flags);
   // an SM that gave up stops the other one too
-  if (*s.abort && lane == 0) st_cluster_u32(mapa(smem_u32((const void*)(sp + kOffMisc + 4)), cr ^ 1), 1);
+  if (*s.abort && lane == 0) {
+    st_cluster_u32(mapa(smem_u32((const void*)(sp + kOffMisc + 4)), cr ^ 1), 1);
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  cluster_sync();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  // every product is done before either SM ends (it reads both SMs' memory)
+  if (warp == 1) mbar_wait_drain(s.bar(B_DRAIN), 0);
+  __syncwarp();
+  cluster_sync_relaxed();
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
 // Set once per device: the shared-memory attributes and how many clusters run at a time.
@@ -433,8 +570,8 @@ cudaError_t launch_mla_expand(const ExpandArgs& a, cudaStream_t stream) {
   const uint64_t dims[2] = {(uint64_t)kLatent, (uint64_t)a.H * 256}, strides[1] = {kLatent * 2};
   const uint32_t box[2] = {64, 64};
   if (!encode_tile_map(&wmap, a.w, 2, dims, strides, box)) return cudaErrorInvalidValue;
-  const long long units = ((long long)a.S + 2 * kM - 1) / (2 * kM) * p.col_tiles;
-  const int clusters = (int)(units < g_dev[dev].clusters ? units : g_dev[dev].clusters);
+  const int units = (a.S + 2 * kM - 1) / (2 * kM) * p.col_tiles;
+  const int clusters = units < g_dev[dev].clusters ? units : g_dev[dev].clusters;
   if (a.scales != nullptr)
     mla_expand_kernel<true><<<2 * clusters, kThreads, kSmemBytes, stream>>>(wmap, p);
   else

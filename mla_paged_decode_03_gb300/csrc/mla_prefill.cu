@@ -38,6 +38,7 @@
 #include <cuda_bf16.h>
 
 #include "internal.h"
+#include "lanes.cuh"
 #include "sm100.cuh"
 #include "tma_map.h"
 #include "../../include/mla_decode.h"
@@ -298,27 +299,6 @@ __device__ __forceinline__ bool read_next(uint32_t src, uint32_t& x, uint32_t& y
   // the read is done before the next answer is written there
   fence_proxy_async_smem();
   return some != 0;
-}
-
-// Eight lanes with eight 16-byte pieces each exchange them: lane i gets piece i of each lane's, so
-// that a warp writes four rows of 128 bytes at a time (32 rows of 32 bytes, straight from the
-// registers, kept the store unit busy for 6,000 clocks a unit).
-__device__ __forceinline__ void transpose8(uint32_t (&v)[32], int lane) {
-#pragma unroll
-  for (int b = 1; b < 8; b <<= 1) {
-    const bool up = lane & b;
-#pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      if (p & b) continue;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        uint32_t &lo = v[4 * p + w], &hi = v[4 * (p | b) + w];
-        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, b);
-        if (up) lo = got;
-        else hi = got;
-      }
-    }
-  }
 }
 
 // One warp: O's 32 rows at tensor memory `to` times `inv` (0: nothing was seen, zeros), as fp32 or

@@ -178,6 +178,12 @@ __device__ __forceinline__ void cluster_sync() {
   cluster_wait();
 }
 
+// The same where no memory is handed over: with release the arrival waits until all stores before it
+// have reached the L2 (1.4 us after a kernel's last output rows).
+__device__ __forceinline__ void cluster_sync_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
+}
+
 __device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }

@@ -73,7 +73,7 @@ def _expand(lib, **kw):
     (dict(B=-1), E), (dict(S=-1), E), (dict(H=0), E), (dict(bs=0), E), (dict(nb=0), E), (dict(maxb=0), E), (dict(maxb=5), E),
     (dict(sc=16, bs=24), E), (dict(cache=None), E), (dict(table=None), E), (dict(seq=None), E), (dict(starts=None), E),
     (dict(w=None), E), (dict(kv=None), E), (dict(kr=None), E), (dict(cache=24), E), (dict(w=8), E), (dict(kv=8), E),
-    (dict(kr=8), E), (dict(table=18), E), (dict(seq=18), E), (dict(starts=18), E), (dict(sc=18), E), (dict(H=(1 << 22) + 1), U),
+    (dict(kr=8), E), (dict(table=18), E), (dict(seq=18), E), (dict(starts=18), E), (dict(sc=18), E), (dict(H=1 << 30), U), (dict(S=2**31 - 1, H=1), U),
     (dict(bs=1 << 20, maxb=1 << 12, stride=1 << 12), U), (dict(B=0, cache=None), OK), (dict(S=0, kv=None), OK),
 ])
 def test_expand_refuses(lib, kw, code):  # noqa: F811
