@@ -104,12 +104,12 @@ cudaError_t launch_lse_combine(const void* partials, bool partials_fp32, const f
 struct DependentLaunch {
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
-  DependentLaunch(dim3 grid, dim3 block, cudaStream_t stream) {
+  DependentLaunch(dim3 grid, dim3 block, cudaStream_t stream, size_t shared_bytes = 0) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = grid;
     cfg.blockDim = block;
-    cfg.dynamicSmemBytes = 0;
+    cfg.dynamicSmemBytes = shared_bytes;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;

@@ -305,6 +305,8 @@ mla_expand_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
     tmem_alloc_pair(s.base + kOffMisc, 512);
     tmem_relinquish_pair();
   }
+  grid_wait();
+  grid_release();
   // rows in use: the last request's end (requests are in the order of their rows)
   long long end = (long long)__ldg(p.a.starts + p.a.B - 1) + max(0, __ldg(p.a.seq_lens + p.a.B - 1));
   const int rows = (int)(end < 0 ? 0 : end > p.a.S ? p.a.S : end);
@@ -572,11 +574,9 @@ cudaError_t launch_mla_expand(const ExpandArgs& a, cudaStream_t stream) {
   if (!encode_tile_map(&wmap, a.w, 2, dims, strides, box)) return cudaErrorInvalidValue;
   const int units = (a.S + 2 * kM - 1) / (2 * kM) * p.col_tiles;
   const int clusters = units < g_dev[dev].clusters ? units : g_dev[dev].clusters;
-  if (a.scales != nullptr)
-    mla_expand_kernel<true><<<2 * clusters, kThreads, kSmemBytes, stream>>>(wmap, p);
-  else
-    mla_expand_kernel<false><<<2 * clusters, kThreads, kSmemBytes, stream>>>(wmap, p);
-  return cudaGetLastError();
+  DependentLaunch dl(dim3(2 * clusters), dim3(kThreads), stream, kSmemBytes);
+  if (a.scales != nullptr) return cudaLaunchKernelEx(&dl.cfg, mla_expand_kernel<true>, wmap, p);
+  return cudaLaunchKernelEx(&dl.cfg, mla_expand_kernel<false>, wmap, p);
 }
 
 }  // namespace mla

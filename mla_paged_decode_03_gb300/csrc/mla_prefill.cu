@@ -363,6 +363,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
     tmem_alloc(s.base + kOffMisc, 512);
     tmem_relinquish();
   } else if (warp == 3) {
+    grid_wait();
     requests.load(a, lane, lane, 0, 0);
   } else if (tid < 4) {
     prefetch_tensormap(tid == 0 ? &qmap : tid == 1 ? &kmap : tid == 2 ? &rmap : &vmap);
@@ -374,6 +375,8 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
     }
     fence_mbar_init();
   }
+  grid_wait();
+  grid_release();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -790,8 +793,8 @@ cudaError_t launch_mla_prefill(PrefillArgs a, const PrefillTensors& x, cudaStrea
   a.tiles = (int)row_tiles(a.T, a.B);
   a.group = head_group(a.tiles, a.S, a.H, a.num_sms);
   const dim3 grid((unsigned)a.tiles * (unsigned)a.H, (unsigned)a.splits);
-  mla_prefill_kernel<<<grid, kThreads, kSmemBytes, stream>>>(qmap, kmap, rmap, vmap, a);
-  e = cudaGetLastError();
+  DependentLaunch dl(grid, dim3(kThreads), stream, kSmemBytes);
+  e = cudaLaunchKernelEx(&dl.cfg, mla_prefill_kernel, qmap, kmap, rmap, vmap, a);
   if (e != cudaSuccess || a.splits == 1) return e;
   return launch_lse_combine128(a.ws_o, true, a.ws_lse, a.splits, (long long)a.T * a.H, true, a.lse_mul, a.out,
                                a.lse, a.cu, a.B, a.H, stream);

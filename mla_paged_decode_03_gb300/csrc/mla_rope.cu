@@ -17,6 +17,7 @@
 
 #include "internal.h"
 #include "slots.cuh"
+#include "sm100.cuh"
 #include "../../include/mla_decode.h"
 
 namespace mla {
@@ -75,6 +76,8 @@ __device__ __forceinline__ void turn(uint4& a, uint4& b, const Turns& t, bool ha
 
 // A warp takes `heads` consecutive heads (a multiple of 8) of one token, eight at a time.
 __global__ void __launch_bounds__(256) mla_rope_kernel(RopeArgs p, int heads, int groups) {
+  sm100::grid_wait();
+  sm100::grid_release();
   const int lane = threadIdx.x & 31, j = lane & 3;
   const long long w = (blockIdx.x * (long long)blockDim.x + threadIdx.x) >> 5;
   const long long tok = w / groups;
@@ -114,6 +117,8 @@ __global__ void __launch_bounds__(256) mla_rope_kernel(RopeArgs p, int heads, in
 // four lanes (lanes 4u .. 4u+3 that of the round's row u).
 __global__ void __launch_bounds__(256) cp_rope_store_kernel(RopeStoreArgs a, SlotParams p,
                                                             FastDiv div_row, int group) {
+  sm100::grid_wait();
+  sm100::grid_release();
   const int lane = threadIdx.x & 31;
   const long long total = (long long)a.B * a.N;
   const long long rows = (long long)a.num_blocks * a.block_size;
@@ -196,8 +201,8 @@ cudaError_t launch_mla_rope(const RopeArgs& a, cudaStream_t stream) {
     heads = (heads / 2 + 7) / 8 * 8;
   const int groups = (a.H + heads - 1) / heads;
   const long long warps = (long long)a.T * groups;
-  mla_rope_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(a, heads, groups);
-  return cudaGetLastError();
+  DependentLaunch dl(dim3((unsigned)((warps + 7) / 8)), dim3(256), stream);
+  return cudaLaunchKernelEx(&dl.cfg, mla_rope_kernel, a, heads, groups);
 }
 
 cudaError_t launch_cp_rope_store(const RopeStoreArgs& a, cudaStream_t stream) {
@@ -207,9 +212,8 @@ cudaError_t launch_cp_rope_store(const RopeStoreArgs& a, cudaStream_t stream) {
   // a position a warp while that keeps all warps resident, then 32
   const int group = total <= 32LL * a.num_sms ? 1 : 32;
   const long long warps = (total + group - 1) / group;
-  cp_rope_store_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(
-      a, p, make_fastdiv((unsigned int)a.N), group);
-  return cudaGetLastError();
+  DependentLaunch dl(dim3((unsigned)((warps + 7) / 8)), dim3(256), stream);
+  return cudaLaunchKernelEx(&dl.cfg, cp_rope_store_kernel, a, p, make_fastdiv((unsigned int)a.N), group);
 }
 
 }  // namespace mla
