@@ -92,6 +92,16 @@ struct Ctx {
   unsigned int* status;
   unsigned long long wait_ns;
   __device__ __forceinline__ uint32_t bar(int i) const { return base + kOffBar + 8 * i; }
+  // Without waiting (try_wait may suspend the warp).
+  __device__ __forceinline__ bool ready(int i, uint32_t parity) const {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(done)
+        : "r"(bar(i)), "r"(parity)
+        : "memory");
+    return __all_sync(0xffffffffu, done != 0);
+  }
   __device__ __forceinline__ bool wait(int i, uint32_t parity) const {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar(i), parity))) return true;
     return __all_sync(0xffffffffu, mbar_wait_slow(bar(i), parity, abort, status, wait_ns, false));
@@ -274,6 +284,38 @@ __device__ __forceinline__ void qk_turn(uint32_t d, uint32_t q, uint32_t k0, uin
       " @e mbarrier.arrive.shared::cta.b64 _, [%7];\n"
       " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%8];\n}" ::"r"(d),
       "r"(q), "r"(k0), "r"(k1), "r"(k2), "r"(hi), "r"(idesc), "r"(b_turn), "r"(b_s)
+      : "memory");
+}
+
+// The rest of a turn whose keys are here: the second half of O += P V, the release of V, then as
+// qk_turn, under one election (apart from one another, with a wait between, 200 clocks more).
+__device__ __forceinline__ void pv_qk_turn(uint32_t d_o, uint32_t p, uint32_t v, uint32_t vhi, uint32_t id_pv,
+                                           uint32_t b_v, uint32_t d, uint32_t q, uint32_t k0, uint32_t k1, uint32_t k2,
+                                           uint32_t hi, uint32_t idesc, uint32_t b_turn, uint32_t b_s) {
+  asm volatile(
+      "{\n .reg .pred e, on;\n .reg .b32 x, y;\n .reg .b64 k, q;\n elect.sync _|e, 0xffffffff;\n"
+      " setp.eq.b32 on, 0, 0;\n"
+      " add.u32 x, %2, 0; mov.b64 k, {x, %3}; add.u32 y, %1, 0;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], k, %4, on;\n"
+      " add.u32 x, %2, 128; mov.b64 k, {x, %3}; add.u32 y, %1, 8;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], k, %4, on;\n"
+      " add.u32 x, %2, 256; mov.b64 k, {x, %3}; add.u32 y, %1, 16;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], k, %4, on;\n"
+      " add.u32 x, %2, 384; mov.b64 k, {x, %3}; add.u32 y, %1, 24;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], k, %4, on;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n"
+      " add.u32 x, %8, 0; mov.b64 k, {x, %11}; add.u32 y, %7, 0; mov.b64 q, {y, %11};\n @e tcgen05.mma.cta_group::1.kind::f16 [%6], q, k, %12, !on;\n"
+      " add.u32 x, %8, 2; mov.b64 k, {x, %11}; add.u32 y, %7, 2; mov.b64 q, {y, %11};\n @e tcgen05.mma.cta_group::1.kind::f16 [%6], q, k, %12, on;\n"
+      " add.u32 x, %8, 4; mov.b64 k, {x, %11}; add.u32 y, %7, 4; mov.b64 q, {y, %11};\n @e tcgen05.mma.cta_group::1.kind::f16 [%6], q, k, %12, on;\n"
+      " add.u32 x, %8, 6; mov.b64 k, {x, %11}; add.u32 y, %7, 6; mov.b64 q, {y, %11};\n @e tcgen05.mma.cta_group::1.kind::f16 [%6], q, k, %12, on;\n"
+      " add.u32 x, %9, 0; mov.b64 k, {x, %11}; add.u32 y, %7, 1024; mov.b64 q, {y, %11};\n @e tcgen05.mma.cta_group::1.kind::f16 [%6], q, k, %12, on;\n"
+      " add.u32 x, %9, 2; mov.b64 k, {x, %11}; add.u32 y, %7, 1026; mov.b64 q, {y, %11};\n @e tcgen05.mma.cta_group::1.kind::f16 [%6], q, k, %12, on;\n"
+      " add.u32 x, %9, 4; mov.b64 k, {x, %11}; add.u32 y, %7, 1028; mov.b64 q, {y, %11};\n @e tcgen05.mma.cta_group::1.kind::f16 [%6], q, k, %12, on;\n"
+      " add.u32 x, %9, 6; mov.b64 k, {x, %11}; add.u32 y, %7, 1030; mov.b64 q, {y, %11};\n @e tcgen05.mma.cta_group::1.kind::f16 [%6], q, k, %12, on;\n"
+      " add.u32 x, %10, 0; mov.b64 k, {x, %11}; add.u32 y, %7, 2048; mov.b64 q, {y, %11};\n @e tcgen05.mma.cta_group::1.kind::f16 [%6], q, k, %12, on;\n"
+      " add.u32 x, %10, 2; mov.b64 k, {x, %11}; add.u32 y, %7, 2050; mov.b64 q, {y, %11};\n @e tcgen05.mma.cta_group::1.kind::f16 [%6], q, k, %12, on;\n"
+      " add.u32 x, %10, 4; mov.b64 k, {x, %11}; add.u32 y, %7, 2052; mov.b64 q, {y, %11};\n @e tcgen05.mma.cta_group::1.kind::f16 [%6], q, k, %12, on;\n"
+      " add.u32 x, %10, 6; mov.b64 k, {x, %11}; add.u32 y, %7, 2054; mov.b64 q, {y, %11};\n @e tcgen05.mma.cta_group::1.kind::f16 [%6], q, k, %12, on;\n"
+      " @e mbarrier.arrive.shared::cta.b64 _, [%13];\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%14];\n}" ::"r"(d_o),
+      "r"(p), "r"(v), "r"(vhi), "r"(id_pv), "r"(b_v), "r"(d), "r"(q), "r"(k0), "r"(k1), "r"(k2), "r"(hi), "r"(idesc),
+      "r"(b_turn), "r"(b_s)
       : "memory");
 }
 
@@ -554,28 +596,34 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
           if (first) ok = ok && s.wait(B_OFREE + t, (units & 1) ^ 1u);
           ok = ok && s.wait(B_PFULL + 2 * t, pv_tiles & 1);
         }
+        const bool keys = qk && s.ready(B_FULL + g, par);
         // the other stream's products are issued
         if (t == 1 || turn > 0) ok = ok && s.wait(B_TURN + t, t == 1 ? turn & 1 : (turn & 1) ^ 1u);
         if (!ok) break;
         tc_fence_after();
+        const uint32_t k0 = kd + sl * kStep, k1 = kd + (sl + 1) % kSlots * kStep, k2 = kd + (sl + 2) % kSlots * kStep;
         if (pv) {
           pv_half(d_o, ds, (uint32_t)vd + v0 * kStep, vhi, id_pv, !first);
           ok = s.wait(B_PFULL + 2 * t + 1, pv_tiles & 1);
           if (!ok) break;
           tc_fence_after();
-          pv_half(d_o, ds + 32, (uint32_t)vd + v1 * kStep, vhi, id_pv, 1);
           ++pv_tiles;
         }
-        if (j > u.begin) mma_commit_warp(s.bar(B_EMPTY + gv));
-        if (qk) {
-          ok = s.wait(B_FULL + g, par);
-          if (!ok) break;
-          tc_fence_after();
-          qk_turn(ds, (uint32_t)qd, kd + sl * kStep, kd + (sl + 1) % kSlots * kStep, kd + (sl + 2) % kSlots * kStep, hi,
-                  id_qk, s.bar(B_TURN + (t ^ 1)), s.bar(B_SFULL + t));
+        if (pv && keys) {
+          pv_qk_turn(d_o, ds + 32, (uint32_t)vd + v1 * kStep, vhi, id_pv, s.bar(B_EMPTY + gv), ds, (uint32_t)qd, k0, k1,
+                     k2, hi, id_qk, s.bar(B_TURN + (t ^ 1)), s.bar(B_SFULL + t));
         } else {
-          if (lane == 0) mbar_arrive(s.bar(B_TURN + (t ^ 1)));
-          __syncwarp();
+          if (pv) pv_half(d_o, ds + 32, (uint32_t)vd + v1 * kStep, vhi, id_pv, 1);
+          if (j > u.begin) mma_commit_warp(s.bar(B_EMPTY + gv));
+          if (qk) {
+            ok = s.wait(B_FULL + g, par);
+            if (!ok) break;
+            tc_fence_after();
+            qk_turn(ds, (uint32_t)qd, k0, k1, k2, hi, id_qk, s.bar(B_TURN + (t ^ 1)), s.bar(B_SFULL + t));
+          } else {
+            if (lane == 0) mbar_arrive(s.bar(B_TURN + (t ^ 1)));
+            __syncwarp();
+          }
         }
         ++turn;
         if (pv && j == mine) mma_commit_warp(s.bar(B_OFULL + t));
