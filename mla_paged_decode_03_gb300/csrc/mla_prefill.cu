@@ -77,7 +77,7 @@ enum Bar : int {
   B_TURN = B_OFREE + 2,          // [2] a stream's products may be issued
   B_UFULL = B_TURN + 2,          // the next unit is known
   B_UEMPTY = B_UFULL + 1,        // every role has read it
-  B_ASK = B_UEMPTY + 1,          // the unit's last loads are on their way
+  B_ASK = B_UEMPTY + 1,          // the unit's last but one tile is on its way
   B_NEXT = B_ASK + 1,            // the answer about the next block of the grid is here
   B_DRAIN = B_NEXT + 1,          // [2]
   B_COUNT = B_DRAIN + 2
@@ -474,7 +474,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
         __syncwarp();
         ++k;
         if (!some) break;
-        // the next one only when this one's last loads go out: what is asked for early runs late
+        // the next one only when this one is nearly loaded: what is asked for early runs late
         ok = s.wait(B_ASK, (k & 1) ^ 1u);
         if (!ok) break;
       }
@@ -500,8 +500,13 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
       const Unit u = *unit;
       const int most = u.most();
       if (most == u.begin && lane == 0) mbar_arrive(s.bar(B_ASK));
+      // its queries into the L2: their place is free only when the unit before has no more products
+      for (int t = 0; t < 2; ++t)
+        if (u.end(t) > u.begin)
+          for (int c = 0; c < kQChunks; ++c)
+            tma_prefetch_3d_warp(&qmap, 64 * c, u.head, u.row0 + u.first + t * kM);
       for (int j = u.begin; j < most && ok; ++j) {
-        if (j + 1 == most && lane == 0) mbar_arrive(s.bar(B_ASK));
+        if (j == max(u.begin, most - 2) && lane == 0) mbar_arrive(s.bar(B_ASK));
         const int y = u.key0 + j * kTile;
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
@@ -664,9 +669,13 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
           tmem_ld32(ts + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(x + 32 * c));
         tmem_wait_ld();
         if (least < (j + 1) * kTile) {
-          const int lim = mine - j * kTile;
+          const int lim = mine - j * kTile, all = least - j * kTile;    // the row's and the warp's bound
 #pragma unroll
-          for (int c = 0; c < 128; ++c) x[c] = c < lim ? x[c] : -INFINITY;
+          for (int b = 0; b < 128; b += 32) {
+            if (all >= b + 32) continue;
+#pragma unroll
+            for (int c = b; c < b + 32; ++c) x[c] = c < lim ? x[c] : -INFINITY;
+          }
         }
         // P of the first 64 keys by the reference so far, beside the maximum: it seldom moves
         const float2 mul = make_float2(a.scale_log2, a.scale_log2);
@@ -789,10 +798,11 @@ int parts(int T, int B, int H, int S, int num_sms) {
   return n < 1 ? 1 : (int)n;
 }
 
-// Heads whose units run at a time, longest first: enough for two units an SM, so that the last ones
-// to run are short, unless their keys and values would not stay in half of the L2; in equal groups.
+// Heads whose units run at a time, longest first: enough for four units an SM, so that the last ones
+// to run are short (two shards' prompts of 64 heads: 169 us; for one an SM 181, two 172, 16 169), unless
+// their keys and values would not stay in half of the L2; in equal groups.
 int head_group(int tiles, int S, int H, int num_sms) {
-  long long n = (2LL * num_sms + tiles - 1) / tiles;
+  long long n = (4LL * num_sms + tiles - 1) / tiles;
   const long long fit = (64LL << 20) / ((long long)S * 512);
   n = n < fit ? n : fit;
   const long long groups = n < 1 ? H : n < H ? H / n : 1;

@@ -568,6 +568,16 @@ __device__ __forceinline__ void tma_load_3d_warp(uint32_t smem_dst, const CUtens
       : "memory");
 }
 
+// Brings a 3-D tile into the L2 only, warp-collective.
+__device__ __forceinline__ void tma_prefetch_3d_warp(const CUtensorMap* map, int x, int y, int z) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];\n}" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
 __device__ __forceinline__ void mbar_arrive_expect_tx_warp(uint32_t bar, uint32_t bytes) {
   asm volatile(
       "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
