@@ -21,10 +21,11 @@
  *     returns one of the MLA_* codes.  Argument errors are found on the host before
  *     anything is launched; mla_last_error() then returns a message (thread-local).
  *   - Calls are stream-ordered: a call's kernels see every result issued before it on
- *     the stream.  The split-KV combine of mla_decode, the kernel of lse_merge and both
- *     kernels of mla_decode_q8 are programmatic dependent launches: they may be scheduled
- *     while the kernel before them drains, but wait for its completion before they read or
- *     write memory.
+ *     the stream.  The split-KV combine of mla_decode, the kernel of lse_merge, both
+ *     kernels of mla_decode_q8 and those of mla_rope, cp_rope_store, mla_expand, mla_prefill
+ *     and lse_merge_v are programmatic dependent launches: they may be scheduled while the
+ *     kernel before them drains, but wait for its completion before they read or write
+ *     memory (and let one behind them be scheduled in the same way).
  *   - bf16 means IEEE bfloat16 stored as 16-bit words; results are rounded to nearest
  *     even.  Tensors are dense and row-major unless a stride is given.
  */
@@ -472,7 +473,7 @@ int mla_expand(const void* kv_cache, const float* kv_scales, const int32_t* bloc
  *   out          bf16 [T, H, 128], 16-byte aligned;  lse  float [T, H] or NULL.
  *   workspace    scratch of mla_prefill_workspace_size bytes, 256-byte aligned, or NULL / 0: without
  *                all of it the keys of few rows are not split over the SMs.
- *   T, B, S >= 0 (S >= 1 with any row), H >= 1, (T/256 + min(B, T)) * H below 2^31; cp_world,
+ *   T, B, S >= 0 (k_nope, v and k_rope may be NULL for S = 0), H >= 1, (T/256 + min(B, T)) * H below 2^31; cp_world,
  *   cp_rank, interleave, scale as mla_decode (interleave need not divide anything here).
  * Values of a request's keys must be finite where any of its rows sees them: a row that does not
  * see a key may still get NaN from a value of it that is NaN or infinite.  Rows behind the last key

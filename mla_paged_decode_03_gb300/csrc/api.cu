@@ -585,8 +585,15 @@ int mla_rope(const void* x, int64_t x_stride_t, int64_t x_stride_h, const int64_
   if (!isfinite(mscale)) return fail(MLA_ERR_INVALID_ARGUMENT, "%s: mscale must be finite", fn);
   if (!strides_ok(x_stride_t) || !strides_ok(x_stride_h) || !strides_ok(out_stride_t) || !strides_ok(out_stride_h))
     return fail(MLA_ERR_INVALID_ARGUMENT, "%s: strides must be multiples of 8 elements, 0 <= stride < 2^36", fn);
-  if ((T > 1 && out_stride_t < 64) || (H > 1 && out_stride_h < 64))
-    return fail(MLA_ERR_INVALID_ARGUMENT, "%s: out's rows overlap (strides below 64 elements)", fn);
+  {
+    // the rows of out may lie in any order, but apart
+    const bool by_t = out_stride_t >= out_stride_h;
+    const int64_t wide = by_t ? out_stride_t : out_stride_h, narrow = by_t ? out_stride_h : out_stride_t;
+    const int64_t n_wide = by_t ? T : H, n_narrow = by_t ? H : T;
+    if ((n_narrow > 1 && narrow < 64) || (n_wide > 1 && wide < (n_narrow > 1 ? narrow * (n_narrow - 1) : 0) + 64))
+      return fail(MLA_ERR_INVALID_ARGUMENT, "%s: out's rows overlap (strides %lld, %lld)", fn,
+                  (long long)out_stride_t, (long long)out_stride_h);
+  }
   if (T == 0) return ok();
   if (!x || !positions || !freqs || !out)
     return fail(MLA_ERR_INVALID_ARGUMENT, "%s: null x/positions/freqs/out", fn);
@@ -751,8 +758,7 @@ int mla_prefill(const void* q, int64_t q_stride_t, int64_t q_stride_h, const voi
     if (!strides_ok(d.stride) || (d.size > 1 && d.stride == 0))
       return fail(MLA_ERR_INVALID_ARGUMENT, "%s: strides must be multiples of 8 elements, 0 < stride < 2^36", fn);
   if (T == 0 || B == 0) return ok();
-  if (S < 1) return fail(MLA_ERR_INVALID_ARGUMENT, "%s: S=0 key rows (a request without keys needs one row of memory)", fn);
-  if (!q || !k_nope || !k_rope || !v || !cu_q_lens || !kv_starts || !seq_lens || !out)
+  if (!q || (S > 0 && (!k_nope || !k_rope || !v)) || !cu_q_lens || !kv_starts || !seq_lens || !out)
     return fail(MLA_ERR_INVALID_ARGUMENT, "%s: null q/k_nope/k_rope/v/cu_q_lens/kv_starts/seq_lens/out", fn);
   if (causal_seqlens_global == nullptr && cp_world != 1 && causal)
     return fail(MLA_ERR_INVALID_ARGUMENT, "%s: causal_seqlens_global is required when cp_world > 1", fn);

@@ -343,12 +343,17 @@ mla_expand_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
         }
       }
     }
-    // the last releases arrive here, and so all copies have, before this SM ends; after an abort the
-    // first SM waits for the copies themselves
-    for (unsigned m = issued > kStages ? issued - kStages : 0; m < issued; ++m) {
-      const int i = (int)(m % kStages);
-      const uint32_t ph = m / kStages & 1;
-      if ((!ok || !s.wait(B_EMPTY + i, ph, true)) && cr == 0) mbar_wait_drain(s.bar(B_FULL + i), ph);
+    // the last releases arrive here, and so all copies have, before this SM ends
+    for (unsigned m = issued > kStages ? issued - kStages : 0; m < issued && ok; ++m)
+      ok = s.wait(B_EMPTY + (int)(m % kStages), m / kStages & 1, true);
+    if (!ok) {
+      // after an abort: the first SM waits for the copies that it counts, the other one, whose copies
+      // are counted there, for as long as any copy takes
+      for (unsigned m = issued > kStages ? issued - kStages : 0; m < issued && cr == 0; ++m)
+        mbar_wait_drain(s.bar(B_FULL + (int)(m % kStages)), m / kStages & 1);
+      const unsigned long long t0 = globaltimer();
+      while (globaltimer() - t0 < 100000ull) {
+      }
     }
   } else if (warp == 1) {
     // ---- products (the first SM's warp, for both) -------------------------------------------

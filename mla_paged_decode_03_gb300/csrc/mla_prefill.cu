@@ -125,10 +125,22 @@ static_assert(kOffUnit + 2 * (int)sizeof(Unit) <= kOffMisc + 160, "units");
 struct Round {
   int row0, n, key0, keys, global;
   int tiles, before;             // its tiles, those of the requests before it
-  int all, top;                  // of the round's end: tiles so far, end of the rows so far
+  int base, top, from, all;      // of the round: its first request, the end of the rows so far, tiles
+                                 // before it and with it
 
-  __device__ void load(const PrefillArgs& a, int b, int lane, int tiles_before, int top_before) {
+  // The round behind the one at hand.
+  __device__ void next(const PrefillArgs& a, int lane) {
+    base += 32;
+    from = all;
+    load(a, lane);
+  }
+  __device__ void first(const PrefillArgs& a, int lane) {
+    base = top = from = 0;
+    load(a, lane);
+  }
+  __device__ void load(const PrefillArgs& a, int lane) {
     unsigned flags = 0;
+    const int b = base + lane;
     int end = 0;
     row0 = n = key0 = keys = global = 0;
     if (b < a.B) {
@@ -150,12 +162,12 @@ struct Round {
       const int v = __shfl_up_sync(0xffffffffu, high, o);
       if (lane >= o) high = max(high, v);
     }
-    high = max(high, top_before);
-    top = __shfl_sync(0xffffffffu, max(high, end), 31);
+    high = max(high, top);
     if (b < a.B) {
       if (row0 < high || end < row0 || end > a.T) flags |= MLA_STATUS_BAD_STEP;
       else n = end - row0;
     }
+    top = __shfl_sync(0xffffffffu, max(high, end), 31);
     tiles = (n + 2 * kM - 1) / (2 * kM);
     int incl = tiles;
 #pragma unroll
@@ -163,12 +175,15 @@ struct Round {
       const int v = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += v;
     }
-    before = tiles_before + incl - tiles;
-    all = tiles_before + __shfl_sync(0xffffffffu, incl, 31);
+    before = from + incl - tiles;
+    all = from + __shfl_sync(0xffffffffu, incl, 31);
     if (flags) atomicOr(a.status, flags);
   }
-  // The unit of row tile x, if it is one of the round's.
-  __device__ bool find(int x, Unit& un) const {
+  // The unit of row tile x, whose request may lie in another round: a block's tiles mostly grow, so
+  // that it goes on from where it is.  False: there is none.
+  __device__ __forceinline__ bool find(const PrefillArgs& a, int x, int lane, Unit& un) {
+    if (x < from) first(a, lane);
+    while (x >= all && base + 32 < a.B) next(a, lane);
     const int at = x - before;
     const unsigned hit = __ballot_sync(0xffffffffu, at >= 0 && at < tiles);
     if (hit == 0) return false;
@@ -183,20 +198,6 @@ struct Round {
     return true;
   }
 };
-
-// The unit of row tile x; `first` holds the first 32 requests.  False: there is none.
-__device__ __forceinline__ bool find_unit(const PrefillArgs& a, const Round& first, int x, int lane, Unit& un) {
-  if (first.find(x, un)) return true;
-  int all = first.all, top = first.top;
-  for (int b0 = 32; b0 < a.B; b0 += 32) {
-    Round r;
-    r.load(a, b0 + lane, lane, all, top);
-    if (r.find(x, un)) return true;
-    all = r.all;
-    top = r.top;
-  }
-  return false;
-}
 
 // Keys that row i of the chunk sees.
 __device__ __forceinline__ int seen(const PrefillArgs& a, const Unit& u, int i) {
@@ -400,13 +401,13 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
   s.status = a.status;
   s.wait_ns = a.wait_ns;
 
-  Round requests;                // warp 3: the first 32 requests
+  Round requests;                // warp 3's
   if (warp == 1) {
     tmem_alloc(s.base + kOffMisc, 512);
     tmem_relinquish();
   } else if (warp == 3) {
     grid_wait();
-    requests.load(a, lane, lane, 0, 0);
+    requests.first(a, lane);
   } else if (tid < 4) {
     prefetch_tensormap(tid == 0 ? &qmap : tid == 1 ? &kmap : tid == 2 ? &rmap : &vmap);
   } else if (tid == 64) {
@@ -448,7 +449,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
         const unsigned per = (unsigned)a.tiles * a.group;
         const unsigned grp = x / per, in = x - grp * per;
         const unsigned heads = min((unsigned)a.group, (unsigned)a.H - grp * a.group);
-        if (find_unit(a, requests, (int)(in / heads), lane, u)) {
+        if (requests.find(a, (int)(in / heads), lane, u)) {
           u.head = (int)(grp * a.group + in % heads);
           u.part = (int)y;
           u.begin = 0;
@@ -803,7 +804,7 @@ int parts(int T, int B, int H, int S, int num_sms) {
 // their keys and values would not stay in half of the L2; in equal groups.
 int head_group(int tiles, int S, int H, int num_sms) {
   long long n = (4LL * num_sms + tiles - 1) / tiles;
-  const long long fit = (64LL << 20) / ((long long)S * 512);
+  const long long fit = (64LL << 20) / ((long long)(S > 0 ? S : 1) * 512);
   n = n < fit ? n : fit;
   const long long groups = n < 1 ? H : n < H ? H / n : 1;
   return (int)((H + groups - 1) / groups);
@@ -838,15 +839,18 @@ cudaError_t launch_mla_prefill(PrefillArgs a, const PrefillTensors& x, cudaStrea
   }
   // [rows][heads][dims] of q and v and of the keys' first part, boxes of one head; rope keys [rows][64]
   CUtensorMap qmap, kmap, rmap, vmap;
-  const uint64_t H = (uint64_t)a.H, T = (uint64_t)a.T, S = (uint64_t)a.S;
+  // (without key rows the maps of the keys stand on q; nothing is loaded through them)
+  const bool keys = a.S > 0;
+  const uint64_t H = (uint64_t)a.H, T = (uint64_t)a.T, S = keys ? (uint64_t)a.S : 1;
   const uint64_t qd[3] = {192, H, T}, kd[3] = {128, H, S}, rd[2] = {64, S};
   // strides in bytes; that of a dimension of one is any
   const auto by = [](uint64_t n, int64_t stride) { return n > 1 ? (uint64_t)stride * 2 : (uint64_t)16; };
   const uint64_t qs[2] = {by(H, x.q_h), by(T, x.q_t)}, ks[2] = {by(H, x.k_h), by(S, x.k_s)},
                  vs[2] = {by(H, x.v_h), by(S, x.v_s)}, rs[1] = {by(S, x.r_s)};
   const uint32_t box[3] = {64, 1, 128}, vbox[3] = {64, 1, 64}, rbox[2] = {64, 128};
-  if (!encode_tile_map(&qmap, x.q, 3, qd, qs, box) || !encode_tile_map(&kmap, x.k_nope, 3, kd, ks, box) ||
-      !encode_tile_map(&rmap, x.k_rope, 2, rd, rs, rbox) || !encode_tile_map(&vmap, x.v, 3, kd, vs, vbox))
+  if (!encode_tile_map(&qmap, x.q, 3, qd, qs, box) || !encode_tile_map(&kmap, keys ? x.k_nope : x.q, 3, kd, ks, box) ||
+      !encode_tile_map(&rmap, keys ? x.k_rope : x.q, 2, rd, rs, rbox) ||
+      !encode_tile_map(&vmap, keys ? x.v : x.q, 3, kd, vs, vbox))
     return cudaErrorInvalidValue;
   a.tiles = (int)row_tiles(a.T, a.B);
   a.group = head_group(a.tiles, a.S, a.H, a.num_sms);

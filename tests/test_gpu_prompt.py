@@ -273,6 +273,22 @@ def test_expand(lens, H, bs, gap, extra, form):
     assert torch.equal(k2[m], k[m]) and torch.equal(v2[m], v[m]) and torch.equal(r2[m], r[m])
 
 
+def test_expand_many_requests():
+    """More requests than a warp's lanes: the rows' requests are found by search."""
+    g = gen(9)
+    lens = [(7 * i) % 23 for i in range(70)]
+    table, nb = paged(g, lens, 16)
+    starts, S = starts_of(lens)
+    cache, w = randn(g, nb, 16, 576), randn(g, 3, 256, 512, scale=512 ** -0.5)
+    k, v, r = M.mla_expand(cache, table.to(DEV), i32(lens), i32(starts), w, S)
+    want, wr, mag, mine = P.ref_expand(lambda b: R.ref_gather_pages(n64(cache), table[b].numpy(), lens[b]), lens, starts,
+                                       n64(w), S)
+    assert mine.all()
+    got = np.concatenate([n64(k), n64(v)], -1).transpose(1, 0, 2)
+    within(got, want, BF * np.abs(want) + 92 * U * mag, "kv")
+    assert np.array_equal(n64(r), wr) and M.device_status() == 0
+
+
 def test_expand_bad_inputs_are_bounded():
     g = gen(3)
     w = randn(g, 2, 256, 512, scale=0.05)
@@ -428,6 +444,24 @@ def test_merge_of_128_wide_rows(n, T, H, dtype, base_e):
     within(n64(out_lse)[some], wl[some], 2.0 ** -20 * (1 + np.abs(wl[some])), "lse")
 
 
+def test_prefill_many_requests():
+    """Several rounds of 32 requests, empty ones among them; heads in several groups."""
+    new = [(5 * i) % 11 if i % 7 else 0 for i in range(150)] + [300] + [1] * 40
+    ctx = [(13 * i) % 200 for i in range(len(new))]
+    d = prefill_case(new, ctx, 2)
+    out, lse = call(d)
+    check(d, out, lse, split=True)
+    assert M.device_status() == 0
+
+
+def test_prefill_without_any_key():
+    """A shard that holds no key yet: no row of memory for keys either."""
+    d = prefill_case([3, 130], [0, 0], 2)
+    e = dict(d, k=d["k"][:0], v=d["v"][:0], kr=d["kr"][:0], lens=[0, 0], starts=[0, 0], cp=300, rank=299)
+    out, lse = call(e)
+    assert (out == 0).all() and (lse == -math.inf).all() and M.device_status() == 0
+
+
 def test_prefill_strided_inputs():
     """Token-major keys (a library product's layout), queries inside a wider tensor, rope keys inside
     cache rows, values in a tensor of their own."""
@@ -536,6 +570,99 @@ def test_prefill_in_a_graph_follows_new_lengths():
         graph.replay()
         torch.cuda.synchronize()
         check(d, out, lse, split=True)
+
+
+def test_prompt_calls_on_two_streams():
+    """Two layers' worth of calls at once, each on its own stream, with their own outputs and workspaces,
+    queued behind one another without waiting: the same as one at a time."""
+    freqs = M.rope_freqs()
+    def step(seed):
+        g = gen(seed)
+        lens = [200 + seed, 33]
+        table, nb = paged(g, lens, 16)
+        cache, w = randn(g, nb, 16, 576), randn(g, 3, 256, 512, scale=512 ** -0.5)
+        starts, S = starts_of(lens)
+        args = (cache, table.to(DEV), i32(lens), i32(starts), w, S)
+        q, cu, pos = randn(g, 70, 3, 192), i32([0, 60, 70]), i64(torch.arange(70))
+        def run(stream=None):
+            r = M.mla_rope(q[..., 128:], pos, freqs, stream=stream)
+            k, v, kr = M.mla_expand(*args, stream=stream)
+            o, l = M.mla_prefill(q, k, kr, v, cu, args[3], args[2], args[2], SCALE, stream=stream)
+            return r, k, v, kr, o, l
+        return run
+    a, b = step(1), step(2)
+    want = a(), b()
+    torch.cuda.synchronize()
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    got = [(a(s), b(t)) for _ in range(20)]
+    torch.cuda.synchronize()
+    for x, y in got:
+        assert all(torch.equal(p, q) for p, q in zip(want[0], x)) and all(torch.equal(p, q) for p, q in zip(want[1], y))
+    assert M.device_status() == 0
+
+
+def test_prompt_calls_in_a_graph():
+    """Rotation, append, expansion and attention captured once and replayed over other inputs."""
+    g = gen(11)
+    B, N, H, bs = 2, 40, 2, 16
+    freqs, w = M.rope_freqs(**FREQS["yarn"]), randn(g, H, 256, 512, scale=512 ** -0.5)
+    nb = 12
+    table = i32([[3, 1, 7, 9], [0, 2, 5, 11]])
+    cache = torch.zeros(nb, bs, 576, dtype=torch.bfloat16, device=DEV)
+    kv, q = randn(g, B, N, 576), randn(g, B * N, H, 192)
+    pos = torch.arange(N, device=DEV).repeat(B, 1)
+    seq, starts, cu = i32([N, N]), i32([0, N]), i32([0, N, 2 * N])
+    out = [torch.empty(B * N, H, 64, dtype=torch.bfloat16, device=DEV), torch.empty(H, B * N, 256, dtype=torch.bfloat16, device=DEV),
+           torch.empty(B * N, 64, dtype=torch.bfloat16, device=DEV), torch.empty(B * N, H, 128, dtype=torch.bfloat16, device=DEV),
+           torch.empty(B * N, H, device=DEV)]
+
+    def step():
+        M.mla_rope(q[..., 128:], pos.view(-1), freqs, out=out[0])
+        M.cp_rope_store(kv[..., :512], kv[..., 512:], pos, freqs, table, cache)
+        k, v, kr = M.mla_expand(cache, table, seq, starts, w, B * N, kv=out[1], k_rope=out[2])
+        M.mla_prefill(q, k, kr, v, cu, starts, seq, None, SCALE, out=out[3], lse=out[4], workspace=torch.empty(0, dtype=torch.uint8, device=DEV))
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in (12, 13):
+        h = gen(seed)
+        kv.copy_(randn(h, B, N, 576))
+        q.copy_(randn(h, B * N, H, 192))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out] + [cache.clone()]
+        cache.zero_()
+        step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, out + [cache]))
+    assert M.device_status() == 0
+
+
+def test_tiny_wait_limit_returns():
+    """As the decode's: with a limit of 1 ns a wait that is not satisfied at once may run out.  The calls
+    return either way, the status holds at most that bit, and with the default limit all is well."""
+    d = prefill_case([300, 40], [500, 0], 2)
+    good = call(d)
+    g = gen(3)
+    lens = [300, 77]
+    table, nb = paged(g, lens, 16)
+    args = (randn(g, nb, 16, 576), table.to(DEV), i32(lens), i32([0, 300]), randn(g, 4, 256, 512, scale=0.04), 377)
+    kv = M.mla_expand(*args)
+    prev = M.set_wait_limit_ns(1)
+    try:
+        call(d)
+        M.mla_expand(*args)
+        torch.cuda.synchronize()
+        bits = M.device_status()
+    finally:
+        M.set_wait_limit_ns(prev)
+    assert bits & ~8 == 0
+    again, kv2 = call(d), M.mla_expand(*args)
+    torch.cuda.synchronize()
+    assert M.device_status() == 0
+    assert all(torch.equal(x, y) for x, y in zip(good + kv, again + kv2))
 
 
 # =============================================================================================

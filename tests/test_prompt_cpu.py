@@ -33,7 +33,7 @@ def _rope(lib, **kw):
     (dict(T=-1), E), (dict(H=0), E), (dict(m=math.nan), E), (dict(m=math.inf), E), (dict(xt=-8), E), (dict(xh=12), E),
     (dict(ot=4), E), (dict(oh=68), E), (dict(oh=56), E), (dict(ot=0), E), (dict(xt=1 << 40), E), (dict(x=None), E),
     (dict(pos=None), E), (dict(freqs=None), E), (dict(out=None), E), (dict(x=24), E), (dict(out=8), E), (dict(pos=12), E),
-    (dict(freqs=20), E), (dict(T=0, x=None), OK),
+    (dict(freqs=20), E), (dict(ot=64, oh=64), E), (dict(ot=64, oh=120), E), (dict(T=3, ot=64, oh=184), E), (dict(T=0, x=None), OK),
 ])
 def test_rope_refuses(lib, kw, code):  # noqa: F811
     assert _rope(lib, **kw) == code
@@ -92,7 +92,7 @@ def _prefill(lib, **kw):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(T=-1), E), (dict(B=-1), E), (dict(S=-1), E), (dict(S=0), E), (dict(H=0), E), (dict(cp=0), E), (dict(rank=1), E),
+    (dict(T=-1), E), (dict(B=-1), E), (dict(S=-1), E), (dict(H=0), E), (dict(cp=0), E), (dict(rank=1), E),
     (dict(rank=-1), E), (dict(il=0), E), (dict(scale=0.0), E), (dict(scale=-1.0), E), (dict(scale=math.nan), E),
     (dict(scale=math.inf), E), (dict(qt=4), E), (dict(qt=0), E), (dict(qh=-192), E), (dict(ks=12), E), (dict(ks=0), E),
     (dict(kh=0), E), (dict(rs=0), E), (dict(vs=0), E), (dict(vh=12), E), (dict(q=None), E), (dict(k=None), E),
