@@ -53,24 +53,23 @@ constexpr int kTile = 128;                    // keys a tile
 constexpr int kSlotBytes = 16384;
 constexpr int kSlots = 8;
 constexpr int kQChunks = 3, kKSlots = 3, kVSlots = 2;
-// Group 2j is tile j's keys, group 2j + 1 its values; the slots they take one after another make
-// group n's slots free once group n - 3 has been used.
-constexpr int kGroups = 3;
+// Tiles take the ring's slots one after another: three of keys, two of values.  Tile g's first keys
+// slot is free once the keys of tile g - 2 have been used, the other two once its values have, its
+// values' once the keys of tile g - 1 have.
 constexpr int kThreads = 384;                 // warp 0 TMA; 1, 2 MMA and 4-7, 8-11 softmax of a stream; 3 units
 constexpr float kRise = 8.0f;                 // log2 units that a maximum may rise before O is rescaled
 
 constexpr int kOffQ = 0;                                     // 2 x 48 KB
 constexpr int kOffRing = 2 * kQChunks * kSlotBytes;
 constexpr int kOffBar = kOffRing + kSlots * kSlotBytes;
-constexpr int kOffMisc = kOffBar + 256;
+constexpr int kOffMisc = kOffBar + 320;
 constexpr int kSmemBytes = kOffMisc + 160 + 1024;
 
 enum Bar : int {
   B_QFULL = 0,                   // [2]
   B_QEMPTY = 2,                  // [2] the unit's last QK of a stream is done
-  B_FULL = 4,                    // [3] keys or values of a tile
-  B_EMPTY = B_FULL + kGroups,    // [3] both streams have used them
-  B_SFULL = B_EMPTY + kGroups,   // [2] S of a stream's tile computed (and all products before)
+  B_KFULL = 4,                   // [3][2] 64 dims of the keys of an even, an odd tile
+  B_SFULL = B_KFULL + 6,         // [2] S of a stream's tile computed (and all products before)
   B_PFULL = B_SFULL + 2,         // [2][2] P of half a tile in tensor memory, O rescaled
   B_OFULL = B_PFULL + 4,         // [2] the unit's last product of a stream is done
   B_OFREE = B_OFULL + 2,         // [2] O read
@@ -80,9 +79,12 @@ enum Bar : int {
   B_ASK = B_UEMPTY + 1,          // the unit's last but one tile is on its way
   B_NEXT = B_ASK + 1,            // the answer about the next block of the grid is here
   B_DRAIN = B_NEXT + 1,          // [2]
-  B_COUNT = B_DRAIN + 2
+  B_VFULL = B_DRAIN + 2,         // [2] the values of an even, an odd tile
+  B_KEMPTY = B_VFULL + 2,        // [2] both streams have used its keys
+  B_VEMPTY = B_KEMPTY + 2,       // [2] and its values
+  B_COUNT = B_VEMPTY + 2
 };
-static_assert(B_COUNT * 8 <= 256, "barriers");
+static_assert(B_COUNT * 8 <= 320, "barriers");
 constexpr int kReaders = 11;     // warps that read a unit: loads, products (2), softmax (8)
 constexpr int kOffNext = kOffMisc + 16, kOffUnit = kOffMisc + 32;
 
@@ -263,33 +265,22 @@ __device__ __forceinline__ void pv_half(uint32_t d, uint32_t p, uint32_t v, uint
       "}" ::"r"(d), "r"(p), "r"(v), "r"(hi), "r"(idesc), "r"(add)
       : "memory");
 }
-// S = Q K^T: twelve products over three chunks of 64 dims (Q's 16 KB apart), then the other stream's
-// turn, then S's barrier, one election.
-__device__ __forceinline__ void qk_turn(uint32_t d, uint32_t q, uint32_t k0, uint32_t k1, uint32_t k2, uint32_t hi,
-                                        uint32_t idesc, uint32_t b_turn, uint32_t b_s) {
+// S (+)= Q K^T of 64 dims: four products, one election.
+__device__ __forceinline__ void qk_chunk(uint32_t d, uint32_t q, uint32_t k, uint32_t hi, uint32_t idesc, uint32_t add) {
   asm volatile(
-      "{\n .reg .pred e, on;\n .reg .b32 x, y;\n .reg .b64 k, q;\n elect.sync _|e, 0xffffffff;\n"
-      " setp.eq.b32 on, 0, 0;\n"
-      " add.u32 x, %2, 0; mov.b64 k, {x, %5}; add.u32 y, %1, 0; mov.b64 q, {y, %5};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %6, !on;\n"
-      " add.u32 x, %2, 2; mov.b64 k, {x, %5}; add.u32 y, %1, 2; mov.b64 q, {y, %5};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %6, on;\n"
-      " add.u32 x, %2, 4; mov.b64 k, {x, %5}; add.u32 y, %1, 4; mov.b64 q, {y, %5};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %6, on;\n"
-      " add.u32 x, %2, 6; mov.b64 k, {x, %5}; add.u32 y, %1, 6; mov.b64 q, {y, %5};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %6, on;\n"
-      " add.u32 x, %3, 0; mov.b64 k, {x, %5}; add.u32 y, %1, 1024; mov.b64 q, {y, %5};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %6, on;\n"
-      " add.u32 x, %3, 2; mov.b64 k, {x, %5}; add.u32 y, %1, 1026; mov.b64 q, {y, %5};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %6, on;\n"
-      " add.u32 x, %3, 4; mov.b64 k, {x, %5}; add.u32 y, %1, 1028; mov.b64 q, {y, %5};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %6, on;\n"
-      " add.u32 x, %3, 6; mov.b64 k, {x, %5}; add.u32 y, %1, 1030; mov.b64 q, {y, %5};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %6, on;\n"
-      " add.u32 x, %4, 0; mov.b64 k, {x, %5}; add.u32 y, %1, 2048; mov.b64 q, {y, %5};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %6, on;\n"
-      " add.u32 x, %4, 2; mov.b64 k, {x, %5}; add.u32 y, %1, 2050; mov.b64 q, {y, %5};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %6, on;\n"
-      " add.u32 x, %4, 4; mov.b64 k, {x, %5}; add.u32 y, %1, 2052; mov.b64 q, {y, %5};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %6, on;\n"
-      " add.u32 x, %4, 6; mov.b64 k, {x, %5}; add.u32 y, %1, 2054; mov.b64 q, {y, %5};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %6, on;\n"
-      " @e mbarrier.arrive.shared::cta.b64 _, [%7];\n"
-      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%8];\n}" ::"r"(d),
-      "r"(q), "r"(k0), "r"(k1), "r"(k2), "r"(hi), "r"(idesc), "r"(b_turn), "r"(b_s)
+      "{\n .reg .pred e, ac, on;\n .reg .b32 x, y;\n .reg .b64 k, q;\n elect.sync _|e, 0xffffffff;\n"
+      " setp.ne.b32 ac, %5, 0;\n setp.eq.b32 on, 0, 0;\n"
+      " add.u32 x, %2, 0; mov.b64 k, {x, %3}; add.u32 y, %1, 0; mov.b64 q, {y, %3};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %4, ac;\n"
+      " add.u32 x, %2, 2; mov.b64 k, {x, %3}; add.u32 y, %1, 2; mov.b64 q, {y, %3};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %4, on;\n"
+      " add.u32 x, %2, 4; mov.b64 k, {x, %3}; add.u32 y, %1, 4; mov.b64 q, {y, %3};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %4, on;\n"
+      " add.u32 x, %2, 6; mov.b64 k, {x, %3}; add.u32 y, %1, 6; mov.b64 q, {y, %3};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], q, k, %4, on;\n"
+      "}" ::"r"(d), "r"(q), "r"(k), "r"(hi), "r"(idesc), "r"(add)
       : "memory");
 }
 
-// The rest of a turn whose keys are here: the second half of O += P V, the release of V, then as
-// qk_turn, under one election (apart from one another, with a wait between, 200 clocks more).
+// The rest of a turn whose keys are all here: the second half of O += P V, the release of V, S = Q K^T
+// (three chunks of 64 dims, Q's 16 KB apart), the other stream's turn, S's barrier, under one election
+// (apart from one another, with a wait between, 200 clocks more).
 __device__ __forceinline__ void pv_qk_turn(uint32_t d_o, uint32_t p, uint32_t v, uint32_t vhi, uint32_t id_pv,
                                            uint32_t b_v, uint32_t d, uint32_t q, uint32_t k0, uint32_t k1, uint32_t k2,
                                            uint32_t hi, uint32_t idesc, uint32_t b_turn, uint32_t b_s) {
@@ -414,7 +405,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
     *s.abort = 0;
     for (int i = 0; i < B_COUNT; ++i) {
       const bool of_warps = (i >= B_PFULL && i < B_PFULL + 4) || i == B_OFREE || i == B_OFREE + 1;
-      mbar_init(s.bar(i), of_warps ? 4 : i >= B_EMPTY && i < B_EMPTY + kGroups ? 2 : i == B_UEMPTY ? kReaders : 1);
+      mbar_init(s.bar(i), of_warps ? 4 : i >= B_KEMPTY ? 2 : i == B_UEMPTY ? kReaders : 1);
     }
     fence_mbar_init();
   }
@@ -493,10 +484,14 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
     // ---- loads ------------------------------------------------------------------------------
     const Unit* unit;
     uint32_t k = 0, nq[2] = {0, 0};
-    int sl = 0, g = 0;
-    long long issued = 0;
-    uint32_t par = 1;
+    int sl = 0;
+    uint32_t g = 0;                             // tiles so far
     bool ok = true;
+    const auto slot = [&]() {
+      const uint32_t dst = s.base + kOffRing + sl * kSlotBytes;
+      sl = (sl + 1) % kSlots;
+      return dst;
+    };
     while (ok && next(k, unit)) {
       const Unit u = *unit;
       const int most = u.most();
@@ -506,55 +501,58 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
         if (u.end(t) > u.begin)
           for (int c = 0; c < kQChunks; ++c)
             tma_prefetch_3d_warp(&qmap, 64 * c, u.head, u.row0 + u.first + t * kM);
-      for (int j = u.begin; j < most && ok; ++j) {
+      for (int j = u.begin; j < most && ok; ++j, ++g) {
         if (j == max(u.begin, most - 2) && lane == 0) mbar_arrive(s.bar(B_ASK));
         const int y = u.key0 + j * kTile;
+        const uint32_t e = g & 1, use = g >> 1 & 1;           // even or odd tile; parity of its phase
+        ok = s.wait(B_KEMPTY + e, use ^ 1u);
+        if (!ok) break;
+        mbar_arrive_expect_tx_warp(s.bar(B_KFULL + e), kSlotBytes);
+        tma_load_3d_warp(slot(), &kmap, 0, u.head, y, s.bar(B_KFULL + e));
+        ok = s.wait(B_VEMPTY + e, use ^ 1u);
+        if (!ok) {
+          ++g;
+          break;
+        }
+        mbar_arrive_expect_tx_warp(s.bar(B_KFULL + 2 + e), kSlotBytes);
+        tma_load_3d_warp(slot(), &kmap, 64, u.head, y, s.bar(B_KFULL + 2 + e));
+        mbar_arrive_expect_tx_warp(s.bar(B_KFULL + 4 + e), kSlotBytes);
+        tma_load_2d_warp(slot(), &rmap, 0, y, s.bar(B_KFULL + 4 + e));
+        if (j == u.begin) {
+          // the unit's queries, after its first keys
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          ok = s.wait(B_EMPTY + g, par);
-          if (!ok) break;
-          const uint32_t fb = s.bar(B_FULL + g);
-          mbar_arrive_expect_tx_warp(fb, (part == 0 ? kKSlots : kVSlots) * kSlotBytes);
-#pragma unroll
-          for (int c = 0; c < (part == 0 ? kKSlots : kVSlots); ++c) {
-            const uint32_t dst = s.base + kOffRing + sl * kSlotBytes;
-            if (part == 1) {
-              tma_load_3d_warp(dst, &vmap, 0, u.head, y + 64 * c, fb);
-              tma_load_3d_warp(dst + kSlotBytes / 2, &vmap, 64, u.head, y + 64 * c, fb);
-            } else if (c < 2) {
-              tma_load_3d_warp(dst, &kmap, 64 * c, u.head, y, fb);
-            } else {
-              tma_load_2d_warp(dst, &rmap, 0, y, fb);
+          for (int t = 0; t < 2; ++t)
+            if (u.end(t) > u.begin) {
+              ok = ok && s.wait(B_QEMPTY + t, (nq[t] & 1) ^ 1u);
+              if (!ok) break;
+              mbar_arrive_expect_tx_warp(s.bar(B_QFULL + t), kQChunks * kSlotBytes);
+              for (int c = 0; c < kQChunks; ++c)
+                tma_load_3d_warp(s.base + kOffQ + (t * kQChunks + c) * kSlotBytes, &qmap, 64 * c, u.head,
+                                 u.row0 + u.first + t * kM, s.bar(B_QFULL + t));
+              ++nq[t];
             }
-            sl = (sl + 1) % kSlots;
-          }
-          ++issued;
-          if (++g == kGroups) {
-            g = 0;
-            par ^= 1u;
-          }
-          if (part == 0 && j == u.begin) {
-            // the unit's queries, after its first keys
+        }
+        if (ok && g > 0) ok = s.wait(B_KEMPTY + (e ^ 1), (g - 1) >> 1 & 1);
+        if (!ok) {
+          ++g;
+          break;
+        }
+        mbar_arrive_expect_tx_warp(s.bar(B_VFULL + e), kVSlots * kSlotBytes);
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-              if (u.end(t) > u.begin) {
-                ok = ok && s.wait(B_QEMPTY + t, (nq[t] & 1) ^ 1u);
-                if (!ok) break;
-                mbar_arrive_expect_tx_warp(s.bar(B_QFULL + t), kQChunks * kSlotBytes);
-                for (int c = 0; c < kQChunks; ++c)
-                  tma_load_3d_warp(s.base + kOffQ + (t * kQChunks + c) * kSlotBytes, &qmap, 64 * c, u.head,
-                                   u.row0 + u.first + t * kM, s.bar(B_QFULL + t));
-                ++nq[t];
-              }
-            if (!ok) break;
-          }
+        for (int c = 0; c < kVSlots; ++c) {
+          const uint32_t dst = slot();
+          tma_load_3d_warp(dst, &vmap, 0, u.head, y + 64 * c, s.bar(B_VFULL + e));
+          tma_load_3d_warp(dst + kSlotBytes / 2, &vmap, 64, u.head, y + 64 * c, s.bar(B_VFULL + e));
         }
       }
     }
     if (*s.abort) {
-      // let loads in flight land before the block ends
-      for (long long m = issued > kGroups ? issued - kGroups : 0; m < issued; ++m)
-        mbar_wait_drain(s.bar(B_FULL + (int)(m % kGroups)), (uint32_t)((m / kGroups) & 1));
+      // let loads in flight land before the block ends (those that were not issued are not waited for
+      // longer than a drain's limit)
+      for (uint32_t m = g > 2 ? g - 2 : 0; m < g; ++m) {
+        for (int c = 0; c < kKSlots; ++c) mbar_wait_drain(s.bar(B_KFULL + 2 * c + (int)(m & 1)), m >> 1 & 1);
+        mbar_wait_drain(s.bar(B_VFULL + (int)(m & 1)), m >> 1 & 1);
+      }
 #pragma unroll
       for (int t = 0; t < 2; ++t)
         if (nq[t] > 0) mbar_wait_drain(s.bar(B_QFULL + t), (nq[t] - 1) & 1);
@@ -571,8 +569,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
     const Unit* unit;
     uint32_t k = 0;
     unsigned sl = 0;                            // slot of tile j's keys
-    int g = 0;                                  // its group's barriers, and their parity
-    uint32_t par = 0;
+    uint32_t g = 0;                             // tiles before it
     uint32_t units = 0, pv_tiles = 0;           // units and tiles of this stream so far
     uint32_t turn = 0;
     bool ok = true;
@@ -581,11 +578,13 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
       const int most = u.most(), mine = u.end(t);
       if (u.begin < mine) ok = s.wait(B_QFULL + t, units & 1);
       for (int j = u.begin; j <= most && ok; ++j) {
-        const int gv = g == 0 ? kGroups - 1 : g - 1;      // tile j - 1's values: the group and slots before
+        // barriers and phases of tile j's keys and of tile j - 1's values, whose slots are the two before
+        const int e = (int)(g & 1), ev = e ^ 1;
+        const uint32_t use = g >> 1 & 1, vuse = (g - 1) >> 1 & 1;
         const unsigned v0 = (sl + kSlots - 2) % kSlots, v1 = (sl + kSlots - 1) % kSlots;
         const bool pv = j > u.begin && j <= mine, qk = j < mine, first = j - 1 == u.begin;
         if (pv) {
-          ok = s.wait(B_FULL + gv, g == 0 ? par ^ 1u : par);
+          ok = s.wait(B_VFULL + ev, vuse);
           const int left = u.keys - (j - 1) * kTile;
           if (ok && left < kTile) {
             // rows behind the last key: P is zero there, the values may be anything
@@ -602,7 +601,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
           if (first) ok = ok && s.wait(B_OFREE + t, (units & 1) ^ 1u);
           ok = ok && s.wait(B_PFULL + 2 * t, pv_tiles & 1);
         }
-        const bool keys = qk && s.ready(B_FULL + g, par);
+        const bool keys = qk && s.ready(B_KFULL + e, use) && s.ready(B_KFULL + 2 + e, use) && s.ready(B_KFULL + 4 + e, use);
         // the other stream's products are issued
         if (t == 1 || turn > 0) ok = ok && s.wait(B_TURN + t, t == 1 ? turn & 1 : (turn & 1) ^ 1u);
         if (!ok) break;
@@ -616,16 +615,28 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
           ++pv_tiles;
         }
         if (pv && keys) {
-          pv_qk_turn(d_o, ds + 32, (uint32_t)vd + v1 * kStep, vhi, id_pv, s.bar(B_EMPTY + gv), ds, (uint32_t)qd, k0, k1,
+          pv_qk_turn(d_o, ds + 32, (uint32_t)vd + v1 * kStep, vhi, id_pv, s.bar(B_VEMPTY + ev), ds, (uint32_t)qd, k0, k1,
                      k2, hi, id_qk, s.bar(B_TURN + (t ^ 1)), s.bar(B_SFULL + t));
         } else {
           if (pv) pv_half(d_o, ds + 32, (uint32_t)vd + v1 * kStep, vhi, id_pv, 1);
-          if (j > u.begin) mma_commit_warp(s.bar(B_EMPTY + gv));
+          if (j > u.begin) mma_commit_warp(s.bar(B_VEMPTY + ev));
           if (qk) {
-            ok = s.wait(B_FULL + g, par);
+            // a chunk at a time, as they come
+            ok = s.wait(B_KFULL + e, use);
             if (!ok) break;
             tc_fence_after();
-            qk_turn(ds, (uint32_t)qd, k0, k1, k2, hi, id_qk, s.bar(B_TURN + (t ^ 1)), s.bar(B_SFULL + t));
+            qk_chunk(ds, (uint32_t)qd, k0, hi, id_qk, 0);
+            ok = s.wait(B_KFULL + 2 + e, use);
+            if (!ok) break;
+            tc_fence_after();
+            qk_chunk(ds, (uint32_t)qd + kStep, k1, hi, id_qk, 1);
+            ok = s.wait(B_KFULL + 4 + e, use);
+            if (!ok) break;
+            tc_fence_after();
+            qk_chunk(ds, (uint32_t)qd + 2 * kStep, k2, hi, id_qk, 1);
+            if (lane == 0) mbar_arrive(s.bar(B_TURN + (t ^ 1)));
+            __syncwarp();
+            mma_commit_warp(s.bar(B_SFULL + t));
           } else {
             if (lane == 0) mbar_arrive(s.bar(B_TURN + (t ^ 1)));
             __syncwarp();
@@ -635,13 +646,9 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
         if (pv && j == mine) mma_commit_warp(s.bar(B_OFULL + t));
         if (qk && j + 1 == mine) mma_commit_warp(s.bar(B_QEMPTY + t));
         if (j == most) break;
-        mma_commit_warp(s.bar(B_EMPTY + g));
+        mma_commit_warp(s.bar(B_KEMPTY + e));
         sl = (sl + kKSlots + kVSlots) % kSlots;
-        g += 2;
-        if (g >= kGroups) {
-          g -= kGroups;
-          par ^= 1u;
-        }
+        ++g;
       }
       if (u.begin < mine) ++units;
     }
