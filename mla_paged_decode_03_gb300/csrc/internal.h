@@ -225,6 +225,12 @@ struct ExpandArgs {
 cudaError_t launch_mla_expand(const ExpandArgs& a, cudaStream_t stream);
 
 // Attention of ragged chunks over expanded keys (mla_prefill.cu).
+struct PrefillTensors {
+  const void *q, *k_nope, *k_rope, *v;
+  int64_t q_t, q_h, k_s, k_h, r_s, v_s, v_h;      // strides, elements
+  void* workspace;
+  size_t workspace_bytes;
+};
 struct PrefillArgs {
   const int32_t *cu, *starts, *seq_lens, *gseq;   // gseq may be null: seq_lens
   int T, B, H, S, causal, cp, rank, il;
@@ -237,12 +243,7 @@ struct PrefillArgs {
   int tiles, group;                      // set by the launch: row tiles, heads that run at a time,
   int splits;                            // parts of the keys, with their scratch
   float *ws_o, *ws_lse;
-};
-struct PrefillTensors {
-  const void *q, *k_nope, *k_rope, *v;
-  int64_t q_t, q_h, k_s, k_h, r_s, v_s, v_h;      // strides, elements
-  void* workspace;
-  size_t workspace_bytes;
+  PrefillTensors x;
 };
 bool prefill_grid_ok(int T, int B, int H);
 size_t prefill_workspace_size(int T, int B, int H, int S, int num_sms);

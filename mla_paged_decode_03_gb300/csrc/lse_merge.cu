@@ -175,6 +175,13 @@ lse_combine_split_kernel(const T* __restrict__ partials, const float* __restrict
 // shards in flight.
 constexpr int kDv128 = 128;
 
+// A NaN is the larger: a row none of whose LSEs is a number is no empty row.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32)
 lse_combine128_kernel(const T* __restrict__ partials, const float* __restrict__ lses, int n,
@@ -190,9 +197,9 @@ lse_combine128_kernel(const T* __restrict__ partials, const float* __restrict__ 
   const unsigned both = 0xffffu << (lane & 16);
 
   float m2 = -INFINITY;                       // max LSE, in log2 units
-  for (int s = sub; s < n; s += 16) m2 = fmaxf(m2, __ldg(lses + s * rows + row) * lse_to_log2);
+  for (int s = sub; s < n; s += 16) m2 = max_nan(m2, __ldg(lses + s * rows + row) * lse_to_log2);
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) m2 = fmaxf(m2, __shfl_xor_sync(both, m2, o));
+  for (int o = 8; o > 0; o >>= 1) m2 = max_nan(m2, __shfl_xor_sync(both, m2, o));
 
   float acc[8];
 #pragma unroll

@@ -337,20 +337,24 @@ __device__ __forceinline__ bool read_next(uint32_t src, uint32_t& x, uint32_t& y
 
 // One warp: O's 32 rows at tensor memory `to` times `inv` (0: nothing was seen, zeros), as fp32 or
 // bf16, to `dst` and on, a token's H heads apart; the first `rows` are stored.  Arrives on `free` once
-// O is read.  Out of line: inlined, its registers spill the tile loop's.
+// O is read.  True: the thread's row holds a NaN or an infinity.  Out of line: inlined, its registers
+// spill the tile loop's.
 template <bool kFp32>
-__device__ __noinline__ void write_rows(uint32_t to, bool any, float inv, uint8_t* dst, int H, int rows, int lane,
+__device__ __noinline__ bool write_rows(uint32_t to, bool any, float inv, uint8_t* dst, int H, int rows, int lane,
                                         uint32_t free) {
   constexpr int kPasses = kFp32 ? 4 : 2;          // 128 bytes of each row at a time
   const long long step = (long long)H * (128 * kPasses);
   dst += (lane & 24) * step + (lane & 7) * 16;
   const bool none = inv == 0.f || !any;
+  float2 zero = make_float2(0.f, 0.f);            // 0 x each value
 #pragma unroll 1
   for (int c = 0; c < kPasses; ++c) {
     uint32_t v[32];
     if (kFp32) {
       tmem_ld32(to + 32 * c, v);
       tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) zero = fma2(make_float2(0.f, 0.f), make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), zero);
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = none ? 0u : __float_as_uint(__uint_as_float(v[i]) * inv);
     } else {
@@ -359,6 +363,8 @@ __device__ __noinline__ void write_rows(uint32_t to, bool any, float inv, uint8_
         uint32_t o[32];
         tmem_ld32(to + 64 * c + 32 * h, o);
         tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) zero = fma2(make_float2(0.f, 0.f), make_float2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), zero);
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           v[16 * h + i] = none ? 0u : pack(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
@@ -374,6 +380,77 @@ __device__ __noinline__ void write_rows(uint32_t to, bool any, float inv, uint8_
     for (int r = 0; r < 8; ++r)
       if ((lane & 24) + r < rows)
         *reinterpret_cast<uint4*>(dst + r * step + c * 128) = make_uint4(v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]);
+  }
+  return !none && zero.x + zero.y != 0.f;
+}
+
+// A key that some rows of a tile do not see has the weight 0 there, and 0 times a value that is NaN or
+// infinite is NaN.  One warp: its rows `bad` (with such outputs) once more, over their own keys alone,
+// where a value of a key that not every row sees is the reason; else they stay.  Scores: lane = key, the
+// row's query is read by all lanes; values: lane = 4 dims.  Some 25 clocks a row and key, against
+// none (64 multiply-adds a row for the test) where all values are finite.
+// m, inv: the row's reference and 1 / (sum of weights).
+template <bool kFp32>
+__device__ __noinline__ void redo_rows(const PrefillArgs& a, const Unit& u, int begin, int end, int least, int mine,
+                                       float m, float inv, unsigned bad, int row0, uint8_t* dst, int lane) {
+  const PrefillTensors& x = a.x;
+  const uint16_t* v = static_cast<const uint16_t*>(x.v) + (long long)u.key0 * x.v_s + u.head * x.v_h + 4 * lane;
+  const uint16_t* k = static_cast<const uint16_t*>(x.k_nope) + (long long)u.key0 * x.k_s + u.head * x.k_h;
+  const uint16_t* kr = static_cast<const uint16_t*>(x.k_rope) + (long long)u.key0 * x.r_s;
+  bool found = false;
+#pragma unroll 4
+  for (int l = max(least, begin); l < end; ++l) {
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(v + l * x.v_s));
+    found = found || (((w.x & 0x7fff7fffu) + 0x00800080u) | ((w.y & 0x7fff7fffu) + 0x00800080u)) & 0x80008000u;
+  }
+  if (!__any_sync(0xffffffffu, found)) return;
+  for (; bad != 0; bad &= bad - 1) {
+    const int r = __ffs(bad) - 1;
+    const int keys = min(__shfl_sync(0xffffffffu, mine, r), end);
+    const float ref = __shfl_sync(0xffffffffu, m, r), f = __shfl_sync(0xffffffffu, inv, r);
+    const uint16_t* q = static_cast<const uint16_t*>(x.q) + (long long)(row0 + r) * x.q_t + u.head * x.q_h;
+    float o[2][4] = {};
+    for (int l0 = begin; l0 < keys; l0 += 32) {
+      float p = 0.f;
+      if (l0 + lane < keys) {
+        // eight sums of 24 products
+        const uint16_t* kn = k + (l0 + lane) * x.k_s;
+        const uint16_t* rope = kr + (l0 + lane) * x.r_s;
+        float2 t[4] = {};
+#pragma unroll 2
+        for (int c = 0; c < 24; ++c) {
+          const uint4 qa = __ldg(reinterpret_cast<const uint4*>(q + 8 * c));
+          const uint4 ka = __ldg(reinterpret_cast<const uint4*>(c < 16 ? kn + 8 * c : rope + 8 * (c - 16)));
+          const uint32_t qw[4] = {qa.x, qa.y, qa.z, qa.w}, kw[4] = {ka.x, ka.y, ka.z, ka.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            t[i] = fma2(make_float2(__uint_as_float(qw[i] << 16), __uint_as_float(qw[i] & 0xffff0000u)),
+                        make_float2(__uint_as_float(kw[i] << 16), __uint_as_float(kw[i] & 0xffff0000u)), t[i]);
+        }
+        const float s = ((t[0].x + t[0].y) + (t[1].x + t[1].y)) + ((t[2].x + t[2].y) + (t[3].x + t[3].y));
+        // rounded as where it meets the values on the tensor cores
+        p = __bfloat162float(__float2bfloat16_rn(exp2_fast(fmaf(s, a.scale_log2, -ref))));
+      }
+      const int some = min(32, keys - l0);
+#pragma unroll 2
+      for (int i = 0; i < some; ++i) {
+        const float w = __shfl_sync(0xffffffffu, p, i);
+        const uint2 b = __ldg(reinterpret_cast<const uint2*>(v + (l0 + i) * x.v_s));
+        float* const at = o[i & 1];
+        at[0] = fmaf(w, __uint_as_float(b.x << 16), at[0]);
+        at[1] = fmaf(w, __uint_as_float(b.x & 0xffff0000u), at[1]);
+        at[2] = fmaf(w, __uint_as_float(b.y << 16), at[2]);
+        at[3] = fmaf(w, __uint_as_float(b.y & 0xffff0000u), at[3]);
+      }
+    }
+    float y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = (o[0][i] + o[1][i]) * f;
+    uint8_t* const to = dst + (long long)r * a.H * (kFp32 ? 512 : 256);
+    if (kFp32)
+      *reinterpret_cast<float4*>(to + 16 * lane) = make_float4(y[0], y[1], y[2], y[3]);
+    else
+      *reinterpret_cast<uint2*>(to + 8 * lane) = make_uint2(pack(y[0], y[1]), pack(y[2], y[3]));
   }
 }
 
@@ -769,12 +846,16 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
         if (split) a.ws_lse[part + row] = none ? -INFINITY : m + log2f(l);
         else if (a.lse != nullptr) a.lse[row] = none ? -INFINITY : (m + log2f(l)) * a.lse_mul;
       }
-      if (split)
-        write_rows<true>(to, any, inv, reinterpret_cast<uint8_t*>(a.ws_o + (part + row0) * 128), a.H, rows, lane,
-                         s.bar(B_OFREE + t));
-      else
-        write_rows<false>(to, any, inv, reinterpret_cast<uint8_t*>(a.out + row0 * 128), a.H, rows, lane,
-                          s.bar(B_OFREE + t));
+      uint8_t* const dst = split ? reinterpret_cast<uint8_t*>(a.ws_o + (part + row0) * 128)
+                                 : reinterpret_cast<uint8_t*>(a.out + row0 * 128);
+      const bool odd = split ? write_rows<true>(to, any, inv, dst, a.H, rows, lane, s.bar(B_OFREE + t))
+                             : write_rows<false>(to, any, inv, dst, a.H, rows, lane, s.bar(B_OFREE + t));
+      const unsigned bad = __ballot_sync(0xffffffffu, odd && lane < rows);
+      const int end = min(n_tiles * kTile, u->keys);
+      if (bad != 0 && least < end) {
+        if (split) redo_rows<true>(a, *u, begin * kTile, end, least, mine, m, inv, bad, u->row0 + i0, dst, lane);
+        else redo_rows<false>(a, *u, begin * kTile, end, least, mine, m, inv, bad, u->row0 + i0, dst, lane);
+      }
     }
   }
   __syncwarp();
@@ -835,6 +916,7 @@ cudaError_t launch_mla_prefill(PrefillArgs a, const PrefillTensors& x, cudaStrea
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   std::call_once(g_dev[dev].once, device_setup, std::ref(g_dev[dev]));
   if (g_dev[dev].err != cudaSuccess) return g_dev[dev].err;
+  a.x = x;
   a.splits = parts(a.T, a.B, a.H, a.S, a.num_sms);
   if (a.splits > 1) {
     if (x.workspace == nullptr || x.workspace_bytes < prefill_workspace_size(a.T, a.B, a.H, a.S, a.num_sms)) {

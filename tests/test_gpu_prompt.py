@@ -520,6 +520,55 @@ def test_prefill_nan_key_reaches_only_rows_that_see_it():
     assert np.isfinite(o[:140]).all() and np.isnan(o[140:]).all() and np.isfinite(n64(lse)[:140]).all()
 
 
+def test_merge_128_nan_lse():
+    """A NaN among a row's LSEs, or nothing but NaN and empty shards, gives NaN; other rows keep theirs."""
+    n, T, H = 3, 5, 2
+    g = gen(5)
+    parts, lses = randn(g, n, T, H, 128), torch.randn(n, T, H, generator=g).to(DEV)
+    lses[:, 0, 0] = math.nan
+    lses[1, 1, 1] = math.nan
+    lses[0, 2, 0], lses[1:, 2, 0] = math.nan, -math.inf
+    out_lse = torch.empty(T, H, device=DEV)
+    out, _ = M.lse_merge(parts, lses, out_lse=out_lse)
+    bad = torch.isnan(lses).any(0)
+    assert torch.isnan(out[bad]).all() and torch.isnan(out_lse[bad]).all()
+    assert torch.isfinite(out[~bad]).all() and torch.isfinite(out_lse[~bad]).all()
+
+
+
+@pytest.mark.parametrize("new,ctx,cp,at", [
+    ([300], [0], 1, [140]), ([300], [0], 1, [0, 5, 130, 299]), ([5], [2000], 1, [2001, 2004]), ([37, 130], [0, 500], 1, [36, 140, 600]),
+    ([260, 3], [128, 700], 2, [150, 193, 540]), ([600], [0], 1, [127, 128, 383, 599]), ([2], [0], 1, [1]),
+])
+def test_prefill_values_that_are_not_finite(new, ctx, cp, at):
+    """NaN and infinite values and keys reach the rows that see them and no others: rows before them in the
+    same block keep their results within the usual bounds."""
+    H = 2
+    d = prefill_case(new, ctx, H, cp=cp)
+    at = [x for x in at if x < d["S"]]
+    for i, x in enumerate(at):
+        d["v"][x, 0] = math.nan
+        d["v"][x, 1, i:i + 9] = math.inf
+        if i % 2:
+            d["k"][x, 1] = math.nan
+    for kw in ({}, {"workspace": torch.empty(0, dtype=torch.uint8, device=DEV)}):
+        out, lse = call(d, **kw)
+        with np.errstate(invalid="ignore"):
+            o, l, A, D, mine = P.ref_prefill(n64(d["q"]), n64(d["k"]), n64(d["kr"]), n64(d["v"]), d["cu"], d["starts"],
+                                             d["lens"], d["G"], SCALE, cp, 0, 1, True)
+        assert mine.all()
+        got, fin = n64(out), np.isfinite(o)
+        assert np.array_equal(np.isnan(got), np.isnan(o)) and np.array_equal(got == np.inf, o == np.inf)
+        assert fin.any() and (at == [] or not fin.all())
+        n = max(d["lens"])
+        D = np.where(np.isfinite(D), D, 0.0)
+        delta = 60 * U * D + 2.0 ** -20
+        A = np.where(fin, A, 0.0)
+        tol = BF * np.abs(np.where(fin, o, 0)) + (BF + 2 * (np.exp(2 * delta) - 1) + (n + 64) * U + 2.0 ** -20)[..., None] * A
+        within(got[fin], o[fin], tol[fin], "out")
+    assert M.device_status() == 0
+
+
 def test_prefill_large_scores():
     """Outlying keys: the reference maximum moves far and often."""
     for H, new, ctx in [(1, [200], [900]), (2, [130], [0])]:
