@@ -387,8 +387,10 @@ __device__ __noinline__ bool write_rows(uint32_t to, bool any, float inv, uint8_
 // A key that some rows of a tile do not see has the weight 0 there, and 0 times a value that is NaN or
 // infinite is NaN.  One warp: its rows `bad` (with such outputs) once more, over their own keys alone,
 // where a value of a key that not every row sees is the reason; else they stay.  Scores: lane = key, the
-// row's query is read by all lanes; values: lane = 4 dims.  Some 25 clocks a row and key, against
-// none (64 multiply-adds a row for the test) where all values are finite.
+// row's query is read by all lanes; values: lane = 4 dims.  Slow, by the loads' latency (256 rows, 8,448
+// keys, 16 heads: 28 ms instead of 0.14): where all values are finite it costs only the test, 64
+// multiply-adds a row.  Running the unit again on the tensor cores with such values cleared, in a second
+// copy of the block's code, took 0.3 ms here but 3 to 6% of every other call's time.
 // m, inv: the row's reference and 1 / (sum of weights).
 template <bool kFp32>
 __device__ __noinline__ void redo_rows(const PrefillArgs& a, const Unit& u, int begin, int end, int least, int mine,
@@ -417,7 +419,7 @@ __device__ __noinline__ void redo_rows(const PrefillArgs& a, const Unit& u, int 
         const uint16_t* kn = k + (l0 + lane) * x.k_s;
         const uint16_t* rope = kr + (l0 + lane) * x.r_s;
         float2 t[4] = {};
-#pragma unroll 2
+#pragma unroll 12
         for (int c = 0; c < 24; ++c) {
           const uint4 qa = __ldg(reinterpret_cast<const uint4*>(q + 8 * c));
           const uint4 ka = __ldg(reinterpret_cast<const uint4*>(c < 16 ? kn + 8 * c : rope + 8 * (c - 16)));
@@ -431,16 +433,21 @@ __device__ __noinline__ void redo_rows(const PrefillArgs& a, const Unit& u, int 
         // rounded as where it meets the values on the tensor cores
         p = __bfloat162float(__float2bfloat16_rn(exp2_fast(fmaf(s, a.scale_log2, -ref))));
       }
-      const int some = min(32, keys - l0);
-#pragma unroll 2
-      for (int i = 0; i < some; ++i) {
-        const float w = __shfl_sync(0xffffffffu, p, i);
-        const uint2 b = __ldg(reinterpret_cast<const uint2*>(v + (l0 + i) * x.v_s));
-        float* const at = o[i & 1];
-        at[0] = fmaf(w, __uint_as_float(b.x << 16), at[0]);
-        at[1] = fmaf(w, __uint_as_float(b.x & 0xffff0000u), at[1]);
-        at[2] = fmaf(w, __uint_as_float(b.y << 16), at[2]);
-        at[3] = fmaf(w, __uint_as_float(b.y & 0xffff0000u), at[3]);
+      // sixteen keys' values in flight
+#pragma unroll 1
+      for (int i0 = 0; i0 < min(32, keys - l0); i0 += 16) {
+        uint2 b[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          b[i] = l0 + i0 + i < keys ? __ldg(reinterpret_cast<const uint2*>(v + (l0 + i0 + i) * x.v_s)) : make_uint2(0, 0);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float w = __shfl_sync(0xffffffffu, p, i0 + i);
+          o[i & 1][0] = fmaf(w, __uint_as_float(b[i].x << 16), o[i & 1][0]);
+          o[i & 1][1] = fmaf(w, __uint_as_float(b[i].x & 0xffff0000u), o[i & 1][1]);
+          o[i & 1][2] = fmaf(w, __uint_as_float(b[i].y << 16), o[i & 1][2]);
+          o[i & 1][3] = fmaf(w, __uint_as_float(b[i].y & 0xffff0000u), o[i & 1][3]);
+        }
       }
     }
     float y[4];
