@@ -172,7 +172,8 @@ lse_combine_split_kernel(const T* __restrict__ partials, const float* __restrict
 }
 
 // Rows of 128 values (the expanded form's outputs): half a warp a row, eight values a lane, four
-// shards in flight.
+// shards in flight.  Bound by the way of the LSEs and then the partials: 9 parts of 512 tokens x 8 heads
+// (fp32, 19 MB) in 9.6 us, no less with a warp a row and more loads in flight.
 constexpr int kDv128 = 128;
 
 // A NaN is the larger: a row none of whose LSEs is a number is no empty row.

@@ -17,8 +17,14 @@
 // sequence, row pair after row pair, cut evenly over the clusters; a cluster gathers rows only when
 // its row pair changes.  The first SM of a pair issues all products.
 //
-// Rows are gathered by four warps, a thread a row, straight into tensor memory: any page size and
-// any start, and the 8-bit form's conversion costs nothing but there.
+// Rows are gathered by eight warps (two sets, which take 128 dims in turn), eight lanes a row so that a
+// load reads whole lines, and turned by lane exchanges into a lane a row for tensor memory: any page
+// size and any start, and the 8-bit form's conversion costs nothing but there.  Outputs leave by two
+// sets of four warps, a set an accumulator, through shared memory as rows of 256 bytes.
+//
+// Measured: 8,192 rows x 128 heads in 170 to 189 us (1.46 to 1.62 PFLOP/s by the clock that the power
+// limit leaves, 3 TB/s written), 67,583 8-bit rows x 32 heads in 345 (1.64 PFLOP/s); 2,064 rows x 8
+// heads in 10.7, nearly all of it the way of the first rows and weights and the last outputs.
 //
 // Safety: every wait is bounded (sm100.cuh); rows of no request, and pages or lengths out of range,
 // are read as zeros and not written (the latter flagged).
@@ -190,10 +196,11 @@ struct Range {
   int pair, col, n;
 };
 // Tiles are cut evenly over the C clusters; or each row pair's over clusters of its own, where that
-// gives none more than kGather tiles more: gathering rows takes as long as that.  (8,192 rows, 128
-// heads: 32 row pairs, 76 clusters; cut evenly, 108 tiles each and often two row pairs, 190 us before
-// and after for 128 tiles of one.)
-constexpr int kGather = 2;
+// gives none more than kGather tiles more: the rows of a second row pair are gathered in about that
+// time.  (76 clusters, 128 heads; tiles of the busiest cluster cut evenly and by row pairs, times:
+// 2,048 rows 27 and 29, 52.4 and 47.5 us; 2,816 rows 38 and 43, 63.5 and 63.8; 4,096 rows 54 and 64,
+// 90 and 97.)
+constexpr int kGather = 6;
 __device__ __forceinline__ Range cut(unsigned pairs, unsigned cols, unsigned C, unsigned c) {
   const unsigned all = pairs * cols;             // below 2^31 - 256
   unsigned u0 = 0, u1 = 0;

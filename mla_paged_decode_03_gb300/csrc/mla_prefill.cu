@@ -10,20 +10,31 @@
 // Bound by the tensor cores on long chunks (640 operations a row and key against 512 bytes a key
 // and head), by memory on chunks below some 150 rows.
 //
-// Design.  A block takes 256 query rows of one request and head, as two streams of 128 rows that
+// Design.  A unit of work is 256 query rows of one request and head, as two streams of 128 rows that
 // share every key and value tile (128 keys); per tile and stream 12 products of 128 x 128 x 16 for
 // S = Q K^T (768 clocks) and 8 for O += P V (512).  Tensor memory holds S (then P in its place) and
-// O of both streams: 4 x 128 columns.  One warp issues PV of a stream's tile j-1 and QK of its tile j
-// back to back and then turns to the other stream: while a stream's softmax (128 threads, a row
-// each) works, the tensor cores work for the other.  Products complete in the order of issue, so
-// that S of tile j, once there, says that PV of tile j-1 is done: the softmax threads may rescale O
-// then without another barrier, which they do only where a row's maximum rose by more than 2^8.
+// O of both streams: 4 x 128 columns.  A warp a stream issues PV of tile j-1 and QK of tile j back to
+// back, and the two warps do so in turn (issued as each is ready, both streams' softmax fell into step
+// and the tensor cores idled): while a stream's softmax (128 threads, a row each) works, the tensor
+// cores work for the other.  Products complete in the order of issue, so that S of tile j, once there,
+// says that PV of tile j-1 is done: the softmax threads may rescale O then without another barrier,
+// which they do only where a row's maximum rose by more than 2^8.  The first half's weights are
+// computed beside the maximum, by the reference so far, and its PV starts before the second half's.
 // Shared memory: Q of both streams (96 KB) and a ring of eight 16 KB slots: three of keys (128 keys
-// x 64 dims) and two of values (64 keys x 128 dims) a tile.
+// x 64 dims, waited for one by one) and two of values (64 keys x 128 dims) a tile.
 //
-// Blocks run the last (longest) rows of a request first; neighbouring blocks share a head's keys in
-// the L2.  Where all blocks would not fill the SMs, each request's tiles are cut into parts whose
-// partial results (fp32) the LSE combine joins.
+// Units are the grid's blocks, one of which runs on an SM for as long as there are others: it asks the
+// launch for blocks that have not begun (clusterlaunchcontrol), so that the next unit's loads overlap
+// the last one's output and long and short units even out.  It asks late, when a unit's last but one
+// tile is on its way; asked for at a unit's start, the last units ran on a few SMs.  The last (longest)
+// rows of a request come first; neighbouring units share a head's keys in the L2.  Where all units
+// would not fill the SMs, each request's tiles are cut into parts whose partial results (fp32) the LSE
+// combine joins.  Outputs go from a row a thread to whole lines by lane exchanges.
+//
+// Measured: one prompt of 8,192 tokens x 128 heads in 1.45 to 1.69 ms (1.6 to 1.9 PFLOP/s of masked
+// work; the clock falls to 1.4 GHz under the power limit); 512 tokens behind 32,256 x 8 heads in 61 us
+// (1.39 PFLOP/s with the combine's 10 us); 24 requests of 1 to 700 tokens, 32 heads, in 290, whose units
+// of few tiles spend 5,000 to 8,000 clocks each on what no tile hides.
 //
 // Safety: every wait is bounded (sm100.cuh); lengths and starts out of range are clamped and
 // flagged; value rows behind a request's last key are zeroed in shared memory before they meet P

@@ -13,6 +13,10 @@
 // HBM-bound: 128 bytes in and out for each head of a token, 1152 for a stored token; a lane turns
 // eight pairs of one token, so that its eight sines and cosines serve all heads that its warp
 // takes.  Four lanes hold a rope part: two 16-byte chunks each, 64 bytes apart in either layout.
+//
+// Measured: 8,192 tokens x 128 heads out of rows of 192 in 47 us (5.8 TB/s, 86% of a copy's rate; the
+// 128 bytes read of each 384 are whole lines); 64 tokens x 128 heads in 2.6 us in a graph.  Stores: some
+// 24,500 rows of 49,200 positions in 13.2 us (4.3 TB/s), 64 in 2.8.
 #include <cuda_bf16.h>
 
 #include "internal.h"
@@ -209,7 +213,8 @@ cudaError_t launch_cp_rope_store(const RopeStoreArgs& a, cudaStream_t stream) {
   const long long total = (long long)a.B * a.N;
   const SlotParams p = make_slot_params(a.block_table, a.bt_stride, a.max_blocks, a.block_size,
                                         a.cp_size, a.cp_rank, a.interleave, a.status);
-  // a position a warp while that keeps all warps resident, then 32
+  // a position a warp while that keeps all warps resident (64 positions 2.8 us; 32 a warp would put them
+  // on two warps), then 32 (65,536 positions, two ranks: 4 a warp 18.8 us, 8 13.9, 16 14.3, 32 13.0)
   const int group = total <= 32LL * a.num_sms ? 1 : 32;
   const long long warps = (total + group - 1) / group;
   DependentLaunch dl(dim3((unsigned)((warps + 7) / 8)), dim3(256), stream);

@@ -435,64 +435,6 @@ __device__ __forceinline__ void mma4_ts_warp(uint32_t d_tmem, uint32_t a_tmem, u
       : "memory");
 }
 
-// Four SS MMAs that walk K by 16 (both descriptors' starts +32 bytes each) under one election;
-// `accumulate` applies to the first, the other three always accumulate.
-__device__ __forceinline__ void mma4_ss_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                             uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p, t, e;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n"
-      " setp.ne.b32 p, %4, 0;\n setp.ne.b32 t, %5, 0;\n"
-      " add.u64 a1, %1, 2;\n add.u64 a2, %1, 4;\n add.u64 a3, %1, 6;\n"
-      " add.u64 b1, %2, 2;\n add.u64 b2, %2, 4;\n add.u64 b3, %2, 6;\n"
-      " elect.sync _|e, 0xffffffff;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(1u)
-      : "memory");
-}
-
-// Four TS MMAs that walk K by 16 with B rows of 128 bytes along K (B start +2048 bytes each).
-__device__ __forceinline__ void mma4_ts_mn_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                                uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p, t, e;\n .reg .b32 a1, a2, a3;\n .reg .b64 b1, b2, b3;\n"
-      " setp.ne.b32 p, %4, 0;\n setp.ne.b32 t, %5, 0;\n"
-      " add.u32 a1, %1, 8;\n add.u32 a2, %1, 16;\n add.u32 a3, %1, 24;\n"
-      " add.u64 b1, %2, 128;\n add.u64 b2, %2, 256;\n add.u64 b3, %2, 384;\n"
-      " elect.sync _|e, 0xffffffff;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(1u)
-      : "memory");
-}
-
-// Twelve SS MMAs over three chunks of 64 dims under one election: A's chunks 16 KB apart, B's where
-// b0, b1, b2 say, four K-steps of 16 (+32 bytes) each.  The first overwrites D.
-__device__ __forceinline__ void mma12_ss_warp(uint32_t d_tmem, uint64_t a0, uint64_t b0, uint64_t b1, uint64_t b2,
-                                              uint32_t idesc) {
-  asm volatile(
-      "{\n .reg .pred p, t, e;\n .reg .b64 a, b;\n"
-      " setp.ne.b32 p, %6, 0;\n setp.ne.b32 t, %7, 0;\n elect.sync _|e, 0xffffffff;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %5, p;\n"
-      " add.u64 a, %1, 2; add.u64 b, %2, 2;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, t;\n"
-      " add.u64 a, %1, 4; add.u64 b, %2, 4;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, t;\n"
-      " add.u64 a, %1, 6; add.u64 b, %2, 6;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, t;\n"
-      " add.u64 a, %1, 1024;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, %3, %5, t;\n"
-      " add.u64 a, %1, 1026; add.u64 b, %3, 2;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, t;\n"
-      " add.u64 a, %1, 1028; add.u64 b, %3, 4;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, t;\n"
-      " add.u64 a, %1, 1030; add.u64 b, %3, 6;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, t;\n"
-      " add.u64 a, %1, 2048;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, %4, %5, t;\n"
-      " add.u64 a, %1, 2050; add.u64 b, %4, 2;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, t;\n"
-      " add.u64 a, %1, 2052; add.u64 b, %4, 4;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, t;\n"
-      " add.u64 a, %1, 2054; add.u64 b, %4, 6;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, t;\n"
-      "}" ::"r"(d_tmem), "l"(a0), "l"(b0), "l"(b1), "l"(b2), "r"(idesc), "r"(0u), "r"(1u)
-      : "memory");
-}
-
 // Twelve TS MMAs of one three-chunk key group under one election: chunk c (A at TMEM
 // column a_c, B descriptor b0 advanced by c x 8 KB) times four K-steps of 16 (A columns
 // +8, B start +32 bytes).  `accumulate` applies to the first MMA only.
