@@ -409,7 +409,9 @@ int mla_rope(const void* x, int64_t x_stride_t, int64_t x_stride_h, const int64_
  *   latent       bf16, row b*N + n (512 contiguous) at latent + (b*N + n)*latent_stride;
  *   k_rope       bf16, row b*N + n (64 contiguous) at k_rope + (b*N + n)*k_rope_stride: both may
  *                be parts of one tensor; 16-byte aligned, strides multiples of 8 elements.
- * A table entry outside [0, num_blocks) writes nothing and sets MLA_STATUS_BAD_PAGE.
+ * A table entry outside [0, num_blocks) writes nothing and sets MLA_STATUS_BAD_PAGE.  The positions of
+ * a request, and the pages of different ones that get rows, are distinct: of two tokens for one slot
+ * the row may hold parts of either.
  * Errors: as cp_local_slot_scatter.
  */
 int cp_rope_store(const void* latent, int64_t latent_stride, const void* k_rope,
