@@ -569,6 +569,24 @@ def test_prefill_values_that_are_not_finite(new, ctx, cp, at):
     assert M.device_status() == 0
 
 
+@pytest.mark.parametrize("new,ctx,H,cp", [([3, 300, 40, 1], [0, 10, 5000, 2500], 90, 1), ([260, 5, 17], [0, 6000, 900], 60, 2),
+                                          ([2] * 31 + [600], [3000] + [4] * 31, 9, 1)])
+def test_prefill_uneven_requests(new, ctx, H, cp):
+    """More units than SMs, some of them long: every unit of every head is run, whatever runs first."""
+    d = prefill_case(new, ctx, H, cp=cp)
+    out, lse = call(d)
+    # every row against the call with its request alone; a few heads against the oracle
+    for b in range(len(new)):
+        rows = slice(d["cu"][b], d["cu"][b + 1])
+        e = dict(d, q=d["q"][rows], cu=[0, new[b]], starts=d["starts"][b:b + 1], lens=d["lens"][b:b + 1], G=d["G"][b:b + 1], T=new[b])
+        o1, l1 = call(e, workspace=torch.empty(0, dtype=torch.uint8, device=DEV))
+        assert torch.equal(o1, out[rows]) and torch.equal(l1, lse[rows])
+    few = [0, H // 2, H - 1]
+    e = dict(d, q=d["q"][:, few], k=d["k"][:, few], v=d["v"][:, few], H=3)
+    check(e, out[:, few], lse[:, few])
+    assert M.device_status() == 0
+
+
 def test_prefill_large_scores():
     """Outlying keys: the reference maximum moves far and often."""
     for H, new, ctx in [(1, [200], [900]), (2, [130], [0])]:
