@@ -124,7 +124,7 @@ struct Ctx {
 // What a block works on at a time.
 struct Unit {
   int row0, n;                   // first row (of q) of the request's chunk, its rows
-  int first;                     // the unit's first row within the chunk
+  int first, from;               // first row of the streams within the chunk, of those to be stored
   int key0, keys;                // first key row, keys of the shard
   int global;                    // global length
   int head, part;                // -1: no more units
@@ -566,6 +566,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
         if (requests.find(a, (int)(in / heads), of_early, lane, u)) {
           u.head = (int)(grp * a.group + in % heads);
           u.part = (int)y;
+          u.from = u.first;
           u.begin = 0;
           // the bound grows with the row, so a stream's last row has the most tiles
           u.end0 = (seen(a, u, min(u.first + kM, u.n) - 1) + kTile - 1) / kTile;
@@ -576,6 +577,13 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
             const int end = (int)((long long)most * (y + 1) / a.splits);
             u.end0 = max(min(u.end0, end), u.begin);
             u.end1 = max(min(u.end1, end), u.begin);
+          }
+          if (u.n - u.first <= kM && (k & 1) != 0) {
+            // rows of one stream alone: units take the streams in turn, so that one's output is written
+            // while the other works
+            u.end1 = u.end0;
+            u.end0 = u.begin;
+            u.first -= kM;
           }
         }
       }
@@ -808,8 +816,10 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
             for (int c = b; c < b + 32; ++c) x[c] = c < lim ? x[c] : -INFINITY;
           }
         }
-        // P of the first 64 keys by the reference so far, beside the maximum: it seldom moves
+        // P of the first 64 keys by the reference so far, beside the maximum: it seldom moves.  The first
+        // one is that of four keys
         const float2 mul = make_float2(a.scale_log2, a.scale_log2);
+        if (j == begin) m = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * a.scale_log2;
         float ref = m == -INFINITY ? 0.f : m;
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         uint32_t pk[32];
@@ -823,7 +833,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
 #pragma unroll
         for (int i = 0; i < 32; ++i) pk[i] = weights(make_float2(x[2 * i], x[2 * i + 1]), mul, -ref, sum[i & 1]);
-        // the reference moves where a maximum rose too far (from nothing at the first)
+        // the reference moves where a maximum rose too far
         const bool moves = top > m + kRise;
         if (__any_sync(0xffffffffu, moves)) {
           const float f = moves ? exp2_fast(m - top) : 1.f;
@@ -882,7 +892,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
       }
       // O / l: bf16, or fp32 where the keys are split
       const int i0 = u->first + t * kM + q * 32;             // the warp's first row in the chunk
-      const int rows = u->n - i0;                            // the warp's rows that are stored
+      const int rows = i0 < u->from ? 0 : u->n - i0;         // the warp's rows that are stored
       const long long row0 = (long long)(u->row0 + i0) * a.H + u->head, row = row0 + (long long)lane * a.H;
       const bool none = l == 0.f;
       const float inv = none ? 0.f : 1.f / l;
@@ -894,6 +904,10 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
       }
       uint8_t* const dst = split ? reinterpret_cast<uint8_t*>(a.ws_o + (part + row0) * 128)
                                  : reinterpret_cast<uint8_t*>(a.out + row0 * 128);
+      if (rows <= 0) {
+        if (any && lane == 0) mbar_arrive(s.bar(B_OFREE + t));
+        continue;
+      }
       const bool odd = split ? write_rows<true>(to, any, inv, dst, a.H, rows, lane, s.bar(B_OFREE + t))
                              : write_rows<false>(to, any, inv, dst, a.H, rows, lane, s.bar(B_OFREE + t));
       const unsigned bad = __ballot_sync(0xffffffffu, odd && lane < rows);

@@ -587,6 +587,18 @@ def test_prefill_uneven_requests(new, ctx, H, cp):
     assert M.device_status() == 0
 
 
+def test_prefill_many_units_with_a_short_rest():
+    """Units of up to 128 rows take the two streams in turn: rows of the units beside them are not touched,
+    whichever is written last."""
+    d = prefill_case([300, 385, 70], [0, 3, 500], 128)
+    outs = [call(d) for _ in range(4)]
+    for o, l in outs[1:]:
+        assert torch.equal(o, outs[0][0]) and torch.equal(l, outs[0][1])
+    few = [0, 41, 77, 127]
+    for o, l in outs[:2]:
+        check(dict(d, q=d["q"][:, few], k=d["k"][:, few], v=d["v"][:, few], H=4), o[:, few], l[:, few])
+
+
 def test_prefill_large_scores():
     """Outlying keys: the reference maximum moves far and often."""
     for H, new, ctx in [(1, [200], [900]), (2, [130], [0])]:
