@@ -19,7 +19,8 @@
 // cores work for the other.  Products complete in the order of issue, so that S of tile j, once there,
 // says that PV of tile j-1 is done: the softmax threads may rescale O then without another barrier,
 // which they do only where a row's maximum rose by more than 2^8.  The first half's weights are
-// computed beside the maximum, by the reference so far, and its PV starts before the second half's.
+// computed beside the maximum, by the reference so far (at first the largest of four scores: none would
+// mean all weights of a unit's first tile twice), and its PV starts before the second half's.
 // Shared memory: Q of both streams (96 KB) and a ring of eight 16 KB slots: three of keys (128 keys
 // x 64 dims, waited for one by one) and two of values (64 keys x 128 dims) a tile.
 //
@@ -29,12 +30,13 @@
 // tile is on its way; asked for at a unit's start, the last units ran on a few SMs.  The last (longest)
 // rows of a request come first; neighbouring units share a head's keys in the L2.  Where all units
 // would not fill the SMs, each request's tiles are cut into parts whose partial results (fp32) the LSE
-// combine joins.  Outputs go from a row a thread to whole lines by lane exchanges.
+// combine joins.  Units of up to 128 rows take the streams by turns.  Outputs go
+// from a row a thread to whole lines by lane exchanges.
 //
 // Measured: one prompt of 8,192 tokens x 128 heads in 1.45 to 1.69 ms (1.6 to 1.9 PFLOP/s of masked
 // work; the clock falls to 1.4 GHz under the power limit); 512 tokens behind 32,256 x 8 heads in 61 us
-// (1.39 PFLOP/s with the combine's 10 us); 24 requests of 1 to 700 tokens, 32 heads, in 290, whose units
-// of few tiles spend 5,000 to 8,000 clocks each on what no tile hides.
+// (1.39 PFLOP/s with the combine); 24 requests of 1 to 700 tokens, 32 heads, in 283, whose units of few
+// tiles spend 4,000 to 7,000 clocks each on what no tile hides.
 //
 // Safety: every wait is bounded (sm100.cuh); lengths and starts out of range are clamped and
 // flagged; value rows behind a request's last key are zeroed in shared memory before they meet P
