@@ -249,8 +249,8 @@ bool prefill_grid_ok(int T, int B, int H);
 size_t prefill_workspace_size(int T, int B, int H, int S, int num_sms);
 cudaError_t launch_mla_prefill(PrefillArgs a, const PrefillTensors& x, cudaStream_t stream);
 
-// launch_lse_combine for rows of 128 values.  With cu ([B+1], may be null), only rows
-// cu[0]*H .. cu[B]*H - 1 are read and written.
+// launch_lse_combine for rows of 128 values.  With cu ([B+1], may be null; fewer than 2^31 rows), only the
+// H rows each of tokens of requests that mla_prefill does not skip are read and written.
 cudaError_t launch_lse_combine128(const void* partials, bool partials_fp32, const float* lses, int n,
                                   long long rows, bool in_log2, float out_lse_mul, uint16_t* out,
                                   float* out_lse, const int32_t* cu, int B, int H,

@@ -183,6 +183,37 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return y;
 }
 
+// Rows that mla_prefill computed: those of requests in order (none begins before the largest value so far)
+// that end within T, as its kernel takes them.  What lies between cu[0] and cu[B] is not enough: the
+// workspace holds nothing for a skipped request's rows.  32 requests a round, one a lane, their cu at lo and
+// end; both halves of the warp look for their own token (-1: none).
+__device__ __forceinline__ bool computed(const int32_t* __restrict__ cu, int B, int T, int token, int lane, int lo,
+                                         int end) {
+  bool found = token < 0;
+  int top = 0;
+  for (int b = lane;;) {
+    int high = lo;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, high, o);
+      if (lane >= o) high = max(high, v);
+    }
+    high = max(high, top);
+    const bool fine = b < B && lo >= high && end <= T;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int t = __shfl_sync(0xffffffffu, token, 16 * h);
+      if (__any_sync(0xffffffffu, fine && lo <= t && t < end) && (lane >> 4) == h) found = true;
+    }
+    top = __shfl_sync(0xffffffffu, high, 31);
+    b += 32;
+    if (b - lane >= B || __all_sync(0xffffffffu, found)) break;
+    lo = b < B ? __ldg(cu + b) : 0;
+    end = b < B ? __ldg(cu + b + 1) : 0;
+  }
+  return found && token >= 0;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32)
 lse_combine128_kernel(const T* __restrict__ partials, const float* __restrict__ lses, int n,
@@ -193,14 +224,21 @@ lse_combine128_kernel(const T* __restrict__ partials, const float* __restrict__ 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, sub = lane & 15;
   const long long row = ((long long)blockIdx.x * kWarps + (threadIdx.x >> 5)) * 2 + (lane >> 4);
-  if (row >= rows) return;
-  if (cu != nullptr && (row < (long long)__ldg(cu) * H || row >= (long long)__ldg(cu + B) * H)) return;
-  const unsigned both = 0xffffu << (lane & 16);
+  const bool live = row < rows;
+  int lo = 0, end = 0;
+  if (cu != nullptr && lane < B) {
+    lo = __ldg(cu + lane);
+    end = __ldg(cu + lane + 1);
+  }
 
   float m2 = -INFINITY;                       // max LSE, in log2 units
-  for (int s = sub; s < n; s += 16) m2 = max_nan(m2, __ldg(lses + s * rows + row) * lse_to_log2);
+  if (live)
+    for (int s = sub; s < n; s += 16) m2 = max_nan(m2, __ldg(lses + s * rows + row) * lse_to_log2);
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) m2 = max_nan(m2, __shfl_xor_sync(both, m2, o));
+  for (int o = 8; o > 0; o >>= 1) m2 = max_nan(m2, __shfl_xor_sync(0xffffffffu, m2, o));
+  // (the parts of mla_prefill are few rows, below 2^31)
+  if (cu != nullptr && !computed(cu, B, (int)rows / H, live ? (int)row / H : -1, lane, lo, end)) return;
+  if (!live) return;
 
   float acc[8];
 #pragma unroll

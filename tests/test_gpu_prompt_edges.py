@@ -1,0 +1,76 @@
+"""Prompt processing at the edges that test_gpu_prompt.py leaves out; the tolerances are those of its head."""
+
+import pytest
+import torch
+
+import mla_paged_decode_03_gb300 as M
+from test_gpu_prompt import BAD_STEP, DEV, call, check, prefill_case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _clean():
+    M.device_status()
+    yield
+
+
+# =============================================================================================
+# attention of chunks
+# =============================================================================================
+def alone(d, b, rows):
+    """The call of request b by itself, with the rows that it has in another one's cu_q_lens."""
+    return dict(d, q=d["q"][rows], cu=[0, rows.stop - rows.start], starts=[d["starts"][b]], lens=[d["lens"][b]], G=[d["G"][b]],
+                T=rows.stop - rows.start)
+
+
+# cu_q_lens and which requests are in order: {request: its rows}
+BAD_ROWS = [
+    ([0, 30, 20, 90], {0: (0, 30)}), ([0, 30, 60, 900], {0: (0, 30), 1: (30, 60)}),
+    ([-5, 30, 60, 90], {1: (30, 60), 2: (60, 90)}), ([0, 60, 30, 30], {0: (0, 60)}), ([0, 60, 30, 90], {0: (0, 60)}),
+    ([0, 200, 60, 90], {}), ([0, 90, 90, 30], {0: (0, 90)}), ([10, 40, 40, 90], {0: (10, 40), 2: (40, 90)}),
+]
+
+
+@pytest.mark.parametrize("cu,fine", BAD_ROWS)
+@pytest.mark.parametrize("split", [True, False])
+def test_prefill_leaves_rows_of_skipped_requests(cu, fine, split):
+    """Requests whose rows are out of order or beyond T are skipped, their rows left as they were, the others
+    complete: also where the keys are split and the parts joined, whatever the workspace holds."""
+    d = prefill_case([30, 30, 30], [1500, 10, 1200], 2)
+    ws = torch.full((M.workspace_size_prefill(90, 3, 2, d["S"]) if split else 0,), 255, dtype=torch.uint8, device=DEV)
+    assert (ws.numel() > 0) == split
+    out = torch.full((90, 2, 128), 9.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((90, 2), 9.0, device=DEV)
+    call(dict(d, cu=cu), out=out, lse=lse, workspace=ws)
+    assert M.device_status() == (0 if cu[0] == 10 else BAD_STEP)
+    left = torch.ones(90, dtype=torch.bool)
+    for b, (lo, hi) in fine.items():
+        left[lo:hi] = False
+        check(alone(d, b, slice(lo, hi)), out[lo:hi], lse[lo:hi], split=True)
+    left = left.to(DEV)
+    assert (out[left] == 9).all() and (lse[left] == 9).all()
+
+
+def test_prefill_split_skips_among_many_requests():
+    """The same behind the first 32 requests, with requests of no rows among them."""
+    new = [0 if b % 5 == 3 else 2 for b in range(64)]
+    ctx = [(37 * b) % 60 for b in range(64)]
+    d = prefill_case(new, ctx, 1)
+    T, cu = d["T"], list(d["cu"])
+    fine = {b: (cu[b], cu[b + 1]) for b in range(64) if new[b]}
+    cu[40] = cu[35] - 1                            # rows of 39 end before those of 35 begin
+    for b in (39, 40):
+        fine.pop(b, None)
+    ws = torch.full((M.workspace_size_prefill(T, 64, 1, d["S"]),), 255, dtype=torch.uint8, device=DEV)
+    assert ws.numel() > 0
+    out = torch.full((T, 1, 128), 9.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((T, 1), 9.0, device=DEV)
+    call(dict(d, cu=cu), out=out, lse=lse, workspace=ws)
+    assert M.device_status() == BAD_STEP
+    left = torch.ones(T, dtype=torch.bool)
+    for b, (lo, hi) in fine.items():
+        left[lo:hi] = False
+        check(alone(d, b, slice(lo, hi)), out[lo:hi], lse[lo:hi], split=True)
+    left = left.to(DEV)
+    assert left.any() and (out[left] == 9).all() and (lse[left] == 9).all()
