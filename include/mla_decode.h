@@ -479,8 +479,7 @@ int mla_expand(const void* kv_cache, const float* kv_scales, const int32_t* bloc
  *   cp_rank, interleave, scale as mla_decode (interleave need not divide anything here).
  * Keys and values that a row does not see, and rows behind the last key, may hold anything (where
  * they are NaN or infinite, rows of the same 256 that do not see them are computed again, slowly:
- * 32 of them over 130,000 keys take 0.6 s, so that with 400,000 keys or more in one part that may
- * pass the default wait limit).
+ * 32 of them over 130,000 keys take 0.6 s.  The wait limit does not count that time).
  * A request whose cu_q_lens are out of order (before the largest so far) or beyond T is skipped, and
  * kv_starts or seq_lens beyond S are cut; both set MLA_STATUS_BAD_STEP.
  * Accuracy: scores and sums in fp32; a softmax weight is rounded to bf16 where it meets the values.

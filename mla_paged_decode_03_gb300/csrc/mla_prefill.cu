@@ -101,9 +101,39 @@ static_assert(B_COUNT * 8 <= 320, "barriers");
 constexpr int kReaders = 11;     // warps that read a unit: loads, products (2), softmax (8)
 constexpr int kOffNext = kOffMisc + 16, kOffUnit = kOffMisc + 32;
 
+extern __shared__ uint8_t smem_raw[];
+__device__ __forceinline__ uint8_t* smem_1024(uint8_t* raw) { return raw + ((1024 - (smem_u32(raw) & 1023)) & 1023); }
+
+// Warps that compute rows again (redo_rows): those at it in the lower half, those that began in the upper.  (Looked up
+// where it is used: handed over as an argument, it cost every call 1 to 2% through the compiler's schedule.)
+__device__ __forceinline__ unsigned* redo_word() { return reinterpret_cast<unsigned*>(smem_1024(smem_raw) + kOffMisc + 8); }
+constexpr unsigned kRedoBegins = 0x10001u, kRedoEnds = 0xffffffffu;
+
+// mbar_wait_slow with a limit that starts anew while rows are computed again, or were since the last look:
+// that takes as long as the keys are many, and ends by itself.  The word lies behind `abort`.
+static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, unsigned int* status,
+                                              unsigned long long limit_ns) {
+  unsigned redo = (unsigned)abort[1];
+  unsigned long long t0 = globaltimer();
+  for (uint32_t i = 0;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    if ((i & 63u) == 63u && globaltimer() - t0 > limit_ns) {
+      const unsigned now = (unsigned)abort[1];
+      if (now == redo && (now & 0xffffu) == 0) {
+        *abort = 1;
+        atomicOr(status, MLA_STATUS_WAIT_TIMEOUT);
+        return false;
+      }
+      redo = now;
+      t0 = globaltimer();
+    }
+  }
+}
+
 struct Ctx {
   uint32_t base;
-  volatile int* abort;
+  volatile int* abort;           // and redo_word() behind it
   unsigned int* status;
   unsigned long long wait_ns;
   __device__ __forceinline__ uint32_t bar(int i) const { return base + kOffBar + 8 * i; }
@@ -119,7 +149,7 @@ struct Ctx {
   }
   __device__ __forceinline__ bool wait(int i, uint32_t parity) const {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar(i), parity))) return true;
-    return __all_sync(0xffffffffu, mbar_wait_slow(bar(i), parity, abort, status, wait_ns, false));
+    return __all_sync(0xffffffffu, wait_slow(bar(i), parity, abort, status, wait_ns));
   }
 };
 
@@ -433,6 +463,8 @@ __device__ __noinline__ bool write_rows(uint32_t to, bool any, float inv, uint8_
 template <bool kFp32>
 __device__ __noinline__ void redo_rows(const PrefillArgs& a, const Unit& u, int begin, int end, int least, int mine,
                                        float m, float inv, unsigned bad, int row0, uint8_t* dst, int lane) {
+  unsigned* const redo = redo_word();
+  if (lane == 0) atomicAdd(redo, kRedoBegins);
   const PrefillTensors& x = a.x;
   const uint16_t* v = static_cast<const uint16_t*>(x.v) + (long long)u.key0 * x.v_s + u.head * x.v_h + 4 * lane;
   const uint16_t* k = static_cast<const uint16_t*>(x.k_nope) + (long long)u.key0 * x.k_s + u.head * x.k_h;
@@ -443,7 +475,7 @@ __device__ __noinline__ void redo_rows(const PrefillArgs& a, const Unit& u, int 
     const uint2 w = __ldg(reinterpret_cast<const uint2*>(v + l * x.v_s));
     found = found || (((w.x & 0x7fff7fffu) + 0x00800080u) | ((w.y & 0x7fff7fffu) + 0x00800080u)) & 0x80008000u;
   }
-  if (!__any_sync(0xffffffffu, found)) return;
+  if (!__any_sync(0xffffffffu, found)) bad = 0;
   for (; bad != 0; bad &= bad - 1) {
     const int r = __ffs(bad) - 1;
     const int keys = min(__shfl_sync(0xffffffffu, mine, r), end);
@@ -497,14 +529,14 @@ __device__ __noinline__ void redo_rows(const PrefillArgs& a, const Unit& u, int 
     else
       *reinterpret_cast<uint2*>(to + 8 * lane) = make_uint2(pack(y[0], y[1]), pack(y[2], y[3]));
   }
+  if (lane == 0) atomicAdd(redo, kRedoEnds);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
 mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap rmap, const __grid_constant__ CUtensorMap vmap,
                    const __grid_constant__ PrefillArgs a) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* sp = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* sp = smem_1024(smem_raw);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(sp + kOffMisc);
   Unit* su = reinterpret_cast<Unit*>(sp + kOffUnit);
@@ -524,7 +556,7 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
   } else if (tid < 4) {
     prefetch_tensormap(tid == 0 ? &qmap : tid == 1 ? &kmap : tid == 2 ? &rmap : &vmap);
   } else if (tid == 64) {
-    *s.abort = 0;
+    s.abort[0] = s.abort[1] = 0;
     for (int i = 0; i < B_COUNT; ++i) {
       const bool of_warps = (i >= B_PFULL && i < B_PFULL + 4) || i == B_OFREE || i == B_OFREE + 1;
       mbar_init(s.bar(i), of_warps ? 4 : i >= B_KEMPTY ? 2 : i == B_UEMPTY ? kReaders : 1);

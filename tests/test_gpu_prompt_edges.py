@@ -1,10 +1,13 @@
 """Prompt processing at the edges that test_gpu_prompt.py leaves out; the tolerances are those of its head."""
+import math
 
+import numpy as np
 import pytest
 import torch
 
 import mla_paged_decode_03_gb300 as M
-from test_gpu_prompt import BAD_STEP, DEV, call, check, prefill_case
+import oracle.prompt_ref as P
+from test_gpu_prompt import BAD_STEP, BF, DEV, SCALE, U, call, check, n64, prefill_case, within
 
 pytestmark = pytest.mark.gpu
 
@@ -74,3 +77,29 @@ def test_prefill_split_skips_among_many_requests():
         check(alone(d, b, slice(lo, hi)), out[lo:hi], lse[lo:hi], split=True)
     left = left.to(DEV)
     assert left.any() and (out[left] == 9).all() and (lse[left] == 9).all()
+
+
+def test_prefill_rows_computed_again_do_not_run_out_of_time():
+    """Rows that a NaN in a value they do not see has them computed again take longer than the wait limit, here
+    some 3 ms against 0.5; the block's other warps wait that long, and its next unit is complete as well."""
+    n, ctx, H = 256, 768, 304                      # two units a block
+    d = prefill_case([n], [ctx], H)
+    few = [0, 150, 151, 152, H - 1]
+    sub = dict(d, q=d["q"][:, few], k=d["k"][:, few], v=d["v"][:, few], H=len(few))
+    o, l, A, D, _ = P.ref_prefill(n64(sub["q"]), n64(sub["k"]), n64(sub["kr"]), n64(sub["v"]), d["cu"], d["starts"], d["lens"],
+                                  d["G"], SCALE, 1, 0, 1, True)
+    d["v"][n + ctx - 1] = math.nan                 # seen by the last row alone
+    call(d)
+    torch.cuda.synchronize()
+    prev = M.set_wait_limit_ns(500_000)
+    try:
+        out, lse = call(d)
+        torch.cuda.synchronize()
+        bits = M.device_status()
+    finally:
+        M.set_wait_limit_ns(prev)
+    assert bits == 0
+    assert torch.isnan(out[-1]).all() and torch.isfinite(out[:-1]).all() and torch.isfinite(lse).all()
+    delta = 60 * U * D + 2.0 ** -20
+    tol = BF * np.abs(o) + (BF + 2 * (np.exp(2 * delta) - 1) + (n + ctx + 64) * U)[..., None] * A
+    within(n64(out[:-1, few]), o[:-1], tol[:-1], "out")
