@@ -760,6 +760,7 @@ int mla_prefill(const void* q, int64_t q_stride_t, int64_t q_stride_h, const voi
   if (T == 0 || B == 0) return ok();
   if (!q || (S > 0 && (!k_nope || !k_rope || !v)) || !cu_q_lens || !kv_starts || !seq_lens || !out)
     return fail(MLA_ERR_INVALID_ARGUMENT, "%s: null q/k_nope/k_rope/v/cu_q_lens/kv_starts/seq_lens/out", fn);
+  if (!causal) causal_seqlens_global = nullptr;            // not read, whatever it holds
   if (causal_seqlens_global == nullptr && cp_world != 1 && causal)
     return fail(MLA_ERR_INVALID_ARGUMENT, "%s: causal_seqlens_global is required when cp_world > 1", fn);
   if (!aligned(q, 16) || !aligned(k_nope, 16) || !aligned(k_rope, 16) || !aligned(v, 16) || !aligned(out, 16))
