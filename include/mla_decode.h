@@ -430,8 +430,8 @@ int cp_rope_store(const void* latent, int64_t latent_stride, const void* k_rope,
  *
  * Arguments:
  *   kv_cache     bf16 [num_blocks, block_size, 576], or, with kv_scales (not NULL), the 8-bit cache
- *                (see mla_decode_q8; its rows times their scales are rounded to bf16, exactly so
- *                for powers of two); 16-byte aligned; any block_size >= 1 (8-bit: multiples of 16).
+ *                (see mla_decode_q8; c is exact in the products whatever the scales, and k_rope is rounded
+ *                once); 16-byte aligned; any block_size >= 1 (8-bit: multiples of 16).
  *   block_table, seq_lens  as mla_decode (shard-local lengths).
  *   kv_starts    int32 [B]: the requests' first rows, in order and apart
  *                (kv_starts[b] + seq_lens[b] <= kv_starts[b+1]).

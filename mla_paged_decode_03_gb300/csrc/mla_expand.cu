@@ -163,6 +163,12 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// A scale (positive, normal) is 2^e f, 1 <= f < 2: e4m3 values times 2^e are exact in bf16, and f multiplies the
+// row's fp32 sums, so that no scale adds a rounding.  Warps whose rows all have f = 1, as the store makes them, skip
+// that product (67,583 rows x 32 heads in a graph: 299 us, with it 308).
+__device__ __forceinline__ float scale_power(float s) { return __uint_as_float(__float_as_uint(s) & 0xff800000u); }
+__device__ __forceinline__ float scale_rest(float s) { return __uint_as_float((__float_as_uint(s) & 0x7fffffu) | 0x3f800000u); }
+
 // 128 bytes of the rows of a warp's lanes, from byte `at` on, each lane its own row's; absent rows
 // give zeros.  Eight lanes read a row's.
 __device__ __forceinline__ void load_rows(const uint8_t* row, int at, int lane, uint32_t (&v)[32]) {
@@ -178,7 +184,7 @@ __device__ __forceinline__ void load_rows(const uint8_t* row, int at, int lane, 
     v[4 * r + 3] = x.w;
   }
 }
-// 64 e4m3 values from word kFirst on, times the scale, as 32 words of two bf16.
+// 64 e4m3 values from word kFirst on, times the scale, as 32 words of two bf16 (exact for powers of two).
 template <int kFirst>
 __device__ __forceinline__ void widen(const uint32_t (&v)[32], float scale, uint32_t (&o)[32]) {
 #pragma unroll
@@ -419,9 +425,9 @@ mla_expand_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
         transpose8(v, lane);
         if (kQ8) {
           uint32_t o[32];
-          widen<0>(v, key.scale, o);
+          widen<0>(v, scale_power(key.scale), o);
           tmem_st32(ta + 64 * k, o);
-          widen<16>(v, key.scale, o);
+          widen<16>(v, scale_power(key.scale), o);
           tmem_st32(ta + 64 * k + 32, o);
         } else {
           tmem_st32(ta + 64 * k, v);
@@ -475,6 +481,8 @@ mla_expand_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
     uint8_t* stage = sp + kOffStage + (warp - 4) * 32 * 256;
     const uint32_t td = tmem + kColD + g * kN + ((uint32_t)q << 21);
     unsigned valid = 0;                           // the warp's rows that are somebody's
+    float rest = 1.f;                             // scale_rest of the thread's row
+    bool powers = true;                           // and whether the warp's are all 1
     bool ok = true;
     int m0 = -1, mp = range.pair, nt = range.col + g;
     for (int n = 0; 2 * n + g < range.n && ok; ++n, nt += 2) {
@@ -487,6 +495,10 @@ mla_expand_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
         unsigned f = 0;
         const Key key = find_key<kQ8>(p.a, r0 + lane, lane, f);
         valid = __ballot_sync(0xffffffffu, key.row != nullptr || key.scale != 0.f);
+        if (kQ8) {
+          rest = scale_rest(key.scale);
+          powers = __all_sync(0xffffffffu, rest == 1.f);
+        }
         m0 = mp;
       }
       ok = s.wait(B_DFULL + g, n & 1, true);
@@ -497,6 +509,10 @@ mla_expand_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constan
         uint32_t v[32];
         tmem_ld32(td + 32 * h, v);
         tmem_wait_ld();
+        if (kQ8 && !powers) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * rest);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint4 o;

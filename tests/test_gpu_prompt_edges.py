@@ -7,7 +7,8 @@ import torch
 
 import mla_paged_decode_03_gb300 as M
 import oracle.prompt_ref as P
-from test_gpu_prompt import BAD_STEP, BF, DEV, SCALE, U, call, check, n64, prefill_case, within
+from test_gpu_prompt import (BAD_STEP, BF, DEV, SCALE, U, call, check, gen, i32, n64, paged, prefill_case, randn,
+                             starts_of, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -103,3 +104,56 @@ def test_prefill_rows_computed_again_do_not_run_out_of_time():
     delta = 60 * U * D + 2.0 ** -20
     tol = BF * np.abs(o) + (BF + 2 * (np.exp(2 * delta) - 1) + (n + ctx + 64) * U)[..., None] * A
     within(n64(out[:-1, few]), o[:-1], tol[:-1], "out")
+
+
+# =============================================================================================
+# expanded keys and values
+# =============================================================================================
+def expand_case(seed, lens, H, bs, gap, form):
+    g = gen(seed)
+    table, nb = paged(g, lens, bs)
+    starts, S = starts_of(lens, gap)
+    w = randn(g, H, 256, 512, scale=512 ** -0.5)
+    x = torch.randn(nb, bs, 576, generator=g)
+    scales = None
+    if form == "bf16":
+        cache = x.to(torch.bfloat16).to(DEV)
+    else:
+        cache = (x * 8).to(torch.float8_e4m3fn).to(DEV)
+        s = torch.exp2(torch.randint(-12, 5, (nb, bs // 16), generator=g).float())
+        if form == "q8 odd scales":
+            s = s * (1 + torch.rand(nb, bs // 16, generator=g))
+        scales = s.to(DEV)
+    return cache, scales, table, starts, S, w
+
+
+def source_rows(cache, scales, table, lens, starts, at):
+    """The cache rows (float64) behind output rows `at`; None where there is no request."""
+    bs = cache.shape[1]
+    slot = np.full(len(at), -1)
+    for b, n in enumerate(lens):
+        l = at - starts[b]
+        ok = (l >= 0) & (l < n)
+        slot[ok] = table[b].numpy()[l[ok] // bs] * bs + l[ok] % bs
+    t = torch.from_numpy(np.maximum(slot, 0)).to(DEV)
+    rows = n64(cache.reshape(-1, 576).view(torch.uint8 if scales is not None else torch.bfloat16)[t].view(cache.dtype).float())
+    if scales is not None:
+        rows = rows * n64(scales.reshape(-1)[t // 16])[:, None]
+    return rows, slot >= 0
+
+
+@pytest.mark.parametrize("form", ["q8 odd scales"])
+@pytest.mark.parametrize("lens,H", [([5, 0, 130], 2), ([700], 5)])
+def test_expand_8bit_scales_are_exact(lens, H, form):
+    """The 8-bit rows' scales multiply the sums in fp32, whatever they are: one rounding to bf16, no other.
+    (The sum of exact products: 92 u of the magnitudes, the product with the scale: u |y|.)"""
+    cache, scales, table, starts, S, w = expand_case(31 + H, lens, H, 32, 3, form)
+    k, v, r = M.mla_expand(cache, table.to(DEV), i32(lens), i32(starts), w, S, kv_scales=scales)
+    at = np.arange(S)
+    rows, mine = source_rows(cache, scales, table, lens, starts, at)
+    want = np.einsum("sc,hdc->shd", rows[mine, :512], n64(w))
+    mag = np.einsum("sc,hdc->shd", np.abs(rows[mine, :512]), np.abs(n64(w)))
+    got = np.concatenate([n64(k), n64(v)], -1)[mine]
+    within(got, want, (BF + U) * np.abs(want) + 92 * U * mag, "kv")
+    within(n64(r)[mine], rows[mine, 512:], BF * np.abs(rows[mine, 512:]), "rope key")
+    assert M.device_status() == 0
