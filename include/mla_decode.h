@@ -167,7 +167,8 @@ int mla_decode_shards(const void* q, const void* kv_cache, const int32_t* block_
  *   out[t,h,:] = sum_s w_s partials[s,t,h,:] / sum_s w_s,
  *   out_lse[t,h] = M + log_base(sum_s w_s),
  * base e when lse_base_e != 0, else 2.  A shard with lse = -inf has weight 0 and its
- * partial is not read; if every shard has -inf, out = 0 and out_lse = -inf.
+ * partial is not read; if every shard has -inf, out = 0 and out_lse = -inf.  A NaN among the
+ * row's LSEs makes both NaN.
  *
  * Arguments:
  *   partials        [n_shards, T, H, 512], bf16 when partials_fp32 == 0 else float,

@@ -188,7 +188,8 @@ def lse_merge(partials: torch.Tensor, lses: torch.Tensor, out: Optional[torch.Te
               out_lse: Optional[torch.Tensor] = None, lse_base_e: bool = True,
               stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Merge partials [n, T, H, D] (bf16 or float32; D 512, or 128 as mla_prefill gives) with lses
-    [n, T, H] float32 into out [T, H, D] bf16 (and out_lse [T, H] float32 when given)."""
+    [n, T, H] float32 into out [T, H, D] bf16 (and out_lse [T, H] float32 when given).  A shard with
+    lse = -inf plays no part (rows of nothing else: 0 and -inf); a NaN lse makes its row NaN."""
     if partials.dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("partials must be bf16 or float32")
     _need(partials, "partials", partials.dtype, 4)

@@ -41,6 +41,13 @@ __device__ __forceinline__ void load8(const float* p, float* v) {
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
+// A NaN is the larger: a row none of whose LSEs is a number is no empty row.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32)
 lse_combine_kernel(const T* __restrict__ partials, const float* __restrict__ lses, int n,
@@ -55,9 +62,9 @@ lse_combine_kernel(const T* __restrict__ partials, const float* __restrict__ lse
 
   float m2 = -INFINITY;                       // max LSE, in log2 units
   for (int s = lane; s < n; s += 32)
-    m2 = fmaxf(m2, __ldg(lses + s * shard_stride_rows + row) * lse_to_log2);
+    m2 = max_nan(m2, __ldg(lses + s * shard_stride_rows + row) * lse_to_log2);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m2 = fmaxf(m2, __shfl_xor_sync(0xffffffffu, m2, o));
+  for (int o = 16; o > 0; o >>= 1) m2 = max_nan(m2, __shfl_xor_sync(0xffffffffu, m2, o));
 
   float acc[16];
 #pragma unroll
@@ -79,7 +86,7 @@ lse_combine_kernel(const T* __restrict__ partials, const float* __restrict__ lse
       for (int k = 0; k < 8; ++k) acc[8 + k] = fmaf(w, v[k], acc[8 + k]);
     }
   }
-  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+  const float inv = wsum != 0.f ? 1.f / wsum : 0.f;
   __nv_bfloat16* o = out + row * kDv;
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
@@ -91,7 +98,7 @@ lse_combine_kernel(const T* __restrict__ partials, const float* __restrict__ lse
     *reinterpret_cast<uint4*>(o + 256 * c + 8 * lane) = packed;
   }
   if (out_lse != nullptr && lane == 0)
-    out_lse[row] = wsum > 0.f ? (m2 + log2f(wsum)) * out_lse_mul : -INFINITY;
+    out_lse[row] = wsum != 0.f ? (m2 + log2f(wsum)) * out_lse_mul : -INFINITY;
 }
 
 // The same merge for few rows of many shards: S warps per row, warp q of a row taking
@@ -117,9 +124,9 @@ lse_combine_split_kernel(const T* __restrict__ partials, const float* __restrict
   float m2 = -INFINITY;                       // max LSE over all shards, in log2 units
   if (valid)
     for (int s = lane; s < n; s += 32)
-      m2 = fmaxf(m2, __ldg(lses + s * shard_stride_rows + row) * lse_to_log2);
+      m2 = max_nan(m2, __ldg(lses + s * shard_stride_rows + row) * lse_to_log2);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m2 = fmaxf(m2, __shfl_xor_sync(0xffffffffu, m2, o));
+  for (int o = 16; o > 0; o >>= 1) m2 = max_nan(m2, __shfl_xor_sync(0xffffffffu, m2, o));
 
   float acc[16];
 #pragma unroll
@@ -156,7 +163,7 @@ lse_combine_split_kernel(const T* __restrict__ partials, const float* __restrict
     }
     wsum += s_w[warp + q];
   }
-  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+  const float inv = wsum != 0.f ? 1.f / wsum : 0.f;
   __nv_bfloat16* o = out + row * kDv;
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
@@ -168,20 +175,13 @@ lse_combine_split_kernel(const T* __restrict__ partials, const float* __restrict
     *reinterpret_cast<uint4*>(o + 256 * c + 8 * lane) = packed;
   }
   if (out_lse != nullptr && lane == 0)
-    out_lse[row] = wsum > 0.f ? (m2 + log2f(wsum)) * out_lse_mul : -INFINITY;
+    out_lse[row] = wsum != 0.f ? (m2 + log2f(wsum)) * out_lse_mul : -INFINITY;
 }
 
 // Rows of 128 values (the expanded form's outputs): half a warp a row, eight values a lane, four
 // shards in flight.  Bound by the way of the LSEs and then the partials: 9 parts of 512 tokens x 8 heads
 // (fp32, 19 MB) in 9.6 us, no less with a warp a row and more loads in flight.
 constexpr int kDv128 = 128;
-
-// A NaN is the larger: a row none of whose LSEs is a number is no empty row.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float y;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-  return y;
-}
 
 // Rows that mla_prefill computed: those of requests in order (none begins before the largest value so far)
 // that end within T, as its kernel takes them.  What lies between cu[0] and cu[B] is not enough: the

@@ -157,3 +157,30 @@ def test_expand_8bit_scales_are_exact(lens, H, form):
     within(got, want, (BF + U) * np.abs(want) + 92 * U * mag, "kv")
     within(n64(r)[mine], rows[mine, 512:], BF * np.abs(rows[mine, 512:]), "rope key")
     assert M.device_status() == 0
+
+
+# =============================================================================================
+# merge
+# =============================================================================================
+@pytest.mark.parametrize("n,T,H", [(3, 5, 2), (16, 3, 2), (3, 4000, 2), (40, 300, 4)])
+@pytest.mark.parametrize("D", [512, 128])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_merge_nan_lse(n, T, H, D, dtype):
+    """A NaN among a row's LSEs, or nothing but NaN and empty shards, gives NaN in both widths; rows of empty
+    shards alone give 0 and -inf, and all others are as they would be without such rows."""
+    g = gen(n + T + D)
+    parts = torch.randn(n, T, H, D, generator=g).to(dtype).to(DEV)
+    lses = torch.randn(n, T, H, generator=g).to(DEV)
+    clean, clean_lse = torch.empty(T, H, D, dtype=torch.bfloat16, device=DEV), torch.empty(T, H, device=DEV)
+    M.lse_merge(parts, lses, out=clean, out_lse=clean_lse)
+    lses[:, 0, 0] = math.nan
+    lses[1, 1, 1] = math.nan
+    lses[0, 2, 0], lses[1:, 2, 0] = math.nan, -math.inf
+    lses[:, 2, 1] = -math.inf
+    out_lse = torch.empty(T, H, device=DEV)
+    out, _ = M.lse_merge(parts, lses, out_lse=out_lse)
+    bad, empty = torch.isnan(lses).any(0), (lses == -math.inf).all(0)
+    assert bad.sum() == 3 and torch.isnan(out[bad]).all() and torch.isnan(out_lse[bad]).all()
+    assert (out[empty] == 0).all() and (out_lse[empty] == -math.inf).all()
+    rest = ~bad & ~empty
+    assert torch.equal(out[rest], clean[rest]) and torch.equal(out_lse[rest], clean_lse[rest])
