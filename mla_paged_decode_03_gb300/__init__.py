@@ -202,8 +202,13 @@ def lse_merge(partials: torch.Tensor, lses: torch.Tensor, out: Optional[torch.Te
     if out is None:
         out = torch.empty(T, H, Dv, dtype=torch.bfloat16, device=partials.device)
     _need(out, "out", torch.bfloat16)
+    # (of rows of 512 a larger buffer has always been taken)
+    if out.numel() < T * H * Dv or (Dv != D_V and tuple(out.shape) != (T, H, Dv)):
+        raise ValueError(f"out must be [{T}, {H}, {Dv}], got {tuple(out.shape)}")
     if out_lse is not None:
         _need(out_lse, "out_lse", torch.float32)
+        if out_lse.numel() < T * H:
+            raise ValueError(f"out_lse must be [{T}, {H}], got {tuple(out_lse.shape)}")
     rc = _lib.load().lse_merge_v(partials.data_ptr(), 1 if partials.dtype == torch.float32 else 0,
                                  lses.data_ptr(), n, T, H, Dv, out.data_ptr(), _ptr(out_lse),
                                  1 if lse_base_e else 0, _stream(stream))
