@@ -159,6 +159,47 @@ def test_expand_8bit_scales_are_exact(lens, H, form):
     assert M.device_status() == 0
 
 
+@pytest.mark.parametrize("lens,H,bs,gap", [
+    ([9000, 0, 700, 31000, 17], 1, 64, 37),           # more row pairs than clusters of two SMs: several a cluster
+    ([21000, 133], 2, 192, 0),
+    ([1500, 3, 0, 2000, 600], 128, 64, 5),            # fewer, but too uneven for clusters of their own: cut evenly
+])
+@pytest.mark.parametrize("form", ["bf16", "q8"])
+def test_expand_clusters_go_from_pair_to_pair(lens, H, bs, gap, form):
+    """Tiles of all row pairs cut evenly over the clusters: a cluster ends one pair's columns, gathers the
+    next pair's rows while products of the last are under way, and begins or ends inside a pair."""
+    cache, scales, table, starts, S, w = expand_case(sum(lens) + H, lens, H, bs, gap, form)
+    kv = torch.full((H, S, 256), 9.0, dtype=torch.bfloat16, device=DEV)
+    kr = torch.full((S, 64), 9.0, dtype=torch.bfloat16, device=DEV)
+    M.mla_expand(cache, table.to(DEV), i32(lens), i32(starts), w, S, kv_scales=scales, kv=kv, k_rope=kr)
+    rng = np.random.default_rng(S)
+    edges = np.concatenate([np.arange(0, S, 128) + x for x in (-1, 0)] + [np.array(starts) + x for x in (-1, 0, 1)] +
+                           [np.array(starts) + np.array(lens) + x for x in (-1, 0)])
+    at = np.unique(np.concatenate([edges[(edges >= 0) & (edges < S)], rng.integers(0, S, 700)]))
+    rows, mine = source_rows(cache, scales, table, lens, starts, at)
+    heads = sorted({0, H // 2, H - 1, int(rng.integers(0, H))})
+    t = torch.from_numpy(at).to(DEV)
+    got, wn = n64(kv[heads][:, t]), n64(w[heads])
+    for i in range(len(heads)):
+        want, mag = rows[:, :512] @ wn[i].T, np.abs(rows[:, :512]) @ np.abs(wn[i]).T
+        within(got[i, mine], want[mine], (BF * np.abs(want) + 92 * U * mag)[mine], f"head {heads[i]}")
+    assert np.array_equal(n64(kr[t])[mine], rows[mine, 512:])
+    # every row of every head: written where it is somebody's, and there alone
+    somebody = torch.zeros(S, dtype=torch.bool)
+    for s, n in zip(starts, lens):
+        somebody[s:s + n] = True
+    somebody = somebody.to(DEV)
+    assert (kv[:, ~somebody] == 9).all() and (kr[~somebody] == 9).all()
+    assert ((kv == 9).all(-1) == ~somebody).all() and ((kr == 9).all(-1) == ~somebody).all()
+    # and equal to a call that has a request alone
+    for b in (0, len(lens) - 1):
+        k1, v1, r1 = M.mla_expand(cache, table[b:b + 1].to(DEV), i32(lens[b:b + 1]), i32([0]), w, lens[b], kv_scales=scales)
+        at = slice(starts[b], starts[b] + lens[b])
+        assert torch.equal(kv[:, at, :128].transpose(0, 1), k1) and torch.equal(kv[:, at, 128:].transpose(0, 1), v1)
+        assert torch.equal(kr[at], r1)
+    assert M.device_status() == 0
+
+
 # =============================================================================================
 # merge
 # =============================================================================================
