@@ -106,6 +106,27 @@ def test_prefill_rows_computed_again_do_not_run_out_of_time():
     within(n64(out[:-1, few]), o[:-1], tol[:-1], "out")
 
 
+def test_prefill_many_requests_and_head_groups():
+    """More than 32 requests and several groups of heads, the last one smaller: a block that goes on from one
+    group to the next finds its request again from the first.  (152 SMs: 111 row tiles, so 6 heads' units
+    are four an SM; 33 heads are 5 groups of 7, the last one of 5.)"""
+    new = [(11 * b) % 59 for b in range(100)]
+    ctx = [(29 * b) % 331 for b in range(100)]
+    H = 33
+    d = prefill_case(new, ctx, H)
+    out, lse = call(d)
+    none = torch.empty(0, dtype=torch.uint8, device=DEV)
+    for b in range(100):
+        if new[b] == 0:
+            continue
+        rows = slice(d["cu"][b], d["cu"][b + 1])
+        o1, l1 = call(alone(d, b, rows), workspace=none)
+        assert torch.equal(o1, out[rows]) and torch.equal(l1, lse[rows]), b
+    few = [0, 6, 7, 27, 28, 32]
+    check(dict(d, q=d["q"][:, few], k=d["k"][:, few], v=d["v"][:, few], H=len(few)), out[:, few], lse[:, few])
+    assert M.device_status() == 0
+
+
 # =============================================================================================
 # expanded keys and values
 # =============================================================================================
