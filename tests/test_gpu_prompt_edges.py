@@ -6,9 +6,10 @@ import pytest
 import torch
 
 import mla_paged_decode_03_gb300 as M
+import oracle.mla_ref as R
 import oracle.prompt_ref as P
-from test_gpu_prompt import (BAD_STEP, BF, DEV, SCALE, U, call, check, gen, i32, n64, paged, prefill_case, randn,
-                             starts_of, within)
+from test_gpu_prompt import (BAD_STEP, BF, DEV, FREQS, SCALE, U, call, check, gen, i32, i64, n64, paged, pair_sum,
+                             prefill_case, randn, starts_of, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -218,6 +219,74 @@ def test_expand_clusters_go_from_pair_to_pair(lens, H, bs, gap, form):
         at = slice(starts[b], starts[b] + lens[b])
         assert torch.equal(kv[:, at, :128].transpose(0, 1), k1) and torch.equal(kv[:, at, 128:].transpose(0, 1), v1)
         assert torch.equal(kr[at], r1)
+    assert M.device_status() == 0
+
+
+# =============================================================================================
+# rotation and append
+# =============================================================================================
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("T,H,width,into", [(5000, 128, 192, 0), (5000, 128, 192, 576), (4999, 37, 192, 0), (5003, 37, 64, 576),
+                                            (70001, 1, 576, 64), (70001, 1, 576, 0), (30000, 4, 64, 0)])
+def test_rope_of_many_tokens(T, H, width, into, half):
+    """Enough tokens for a warp to take all of a token's heads, several in flight and in several rounds:
+    in place, and into rows of another width."""
+    g = gen(T + H + into)
+    freqs = M.rope_freqs(**FREQS["yarn"])
+    q = torch.randn(T, H, width, generator=g, dtype=torch.float32).to(torch.bfloat16).to(DEV)
+    x = q[..., width - 64:]
+    pos = torch.randint(0, 1 << 20, (T,), generator=g)
+    pos[::97] = -1
+    whole = torch.full((T, H, into), 9.0, dtype=torch.bfloat16, device=DEV) if into else q.clone()
+    start = whole.clone()
+    out = whole[..., whole.shape[-1] - 64:]
+    y = M.mla_rope(x if into else out, i64(pos), freqs, out=out, half=half, mscale=1.25)
+    assert y is out
+    at = np.unique(np.concatenate([np.arange(0, T, 97)[:40], np.arange(0, T, 97)[:40] + 1, [T - 1],
+                                   np.random.default_rng(T).integers(0, T, 200)]))
+    t = torch.from_numpy(at).to(DEV)
+    xs = n64(x[t])
+    want = P.ref_rope(xs, pos.numpy()[at], freqs.tolist(), half, 1.25, n64(start[t])[..., -64:])
+    within(n64(out[t]), want, BF * np.abs(want) + 2.0 ** -20 * 1.25 * pair_sum(xs, half), "rope")
+    assert torch.equal(whole[..., :-64], start[..., :-64])
+    stay = (pos < 0).to(DEV)
+    assert torch.equal(whole[stay], start[stay])
+    # every token as in a call of few tokens at a time
+    pieces = torch.cat([M.mla_rope(x[a:a + 300], i64(pos[a:a + 300]), freqs, half=half, mscale=1.25)
+                        for a in range(0, min(T, 6000), 300)])
+    assert torch.equal(out[:len(pieces)][~stay[:len(pieces)]], pieces[~stay[:len(pieces)]])
+
+
+@pytest.mark.parametrize("B,N", [(1, 4864), (1, 4865), (64, 76), (5, 973), (3, 2731), (1, 16384)])
+@pytest.mark.parametrize("cp,rank,il", [(1, 0, 1), (2, 1, 1), (3, 0, 4)])
+def test_rope_store_of_thousands(B, N, cp, rank, il):
+    """Around the number of positions from which a warp takes 32 of them (32 an SM: 4,864 with 152)."""
+    g = gen(B + N + cp)
+    freqs, bs = M.rope_freqs(**FREQS["ntk"]), 32
+    ctx = torch.randint(0, 2000, (B, 1), generator=g)
+    pos = ctx + torch.arange(N)[None]
+    pos[:, N - N // 9:] = -1
+    width = (2000 + N) // (bs * cp) + 1
+    nb = B * width + 1
+    table = torch.randperm(nb, generator=g)[:B * width].view(B, width).to(torch.int32).to(DEV)
+    kv = torch.randn(B, N, 576, generator=g).to(torch.bfloat16).to(DEV)
+    cache = torch.full((nb, bs, 576), 9.0, dtype=torch.bfloat16, device=DEV)
+    slots = torch.empty(B, N, dtype=torch.int64, device=DEV)
+    M.cp_rope_store(kv[..., :512], kv[..., 512:], i64(pos), freqs, table, cache, cp, rank, il, slots=slots)
+    want_slots = R.ref_cp_local_slot(pos.numpy(), table.cpu().numpy(), bs, cp, rank, il)
+    assert np.array_equal(n64(slots), want_slots)
+    own = torch.from_numpy(want_slots >= 0).to(DEV)
+    flat, at = cache.view(-1, 576), slots[own]
+    assert torch.equal(flat[at, :512], kv[own][:, :512])
+    left = torch.ones(nb * bs, dtype=torch.bool, device=DEV)
+    left[at] = False
+    assert (flat[left] == 9).all()
+    p, x, got = n64(i64(pos)[own]), n64(kv[own][:, 512:]), n64(flat[at, 512:])
+    some = np.unique(np.concatenate([np.arange(min(64, len(p))), [len(p) - 1], np.random.default_rng(N).integers(0, len(p), 150)]))
+    want = np.stack([P.ref_rope_row(x[i], int(p[i]), freqs.tolist(), False, 1.0) for i in some])
+    within(got[some], want, BF * np.abs(want) + 2.0 ** -20 * pair_sum(x[some], False), "rope key")
+    turned = M.mla_rope(kv[own][:, None, 512:], i64(pos)[own], freqs)
+    assert torch.equal(flat[at, 512:], turned[:, 0])
     assert M.device_status() == 0
 
 
