@@ -2,14 +2,22 @@
 heads' keys and values, and the attention of chunks of new tokens (C ABI: mla_rope, cp_rope_store,
 mla_expand, mla_prefill).
 
-One layer of a step whose requests bring chunks of any length (cp_step_tables gives positions and
-lengths; all token-major tensors hold the requests' new tokens one after another):
+One layer of a step whose requests bring chunks of any and different lengths (cp_step_tables gives
+positions and lengths).  The append takes the new tokens as [B, N, ...], padded to the longest
+chunk, its padding at position -1 as the step's positions have it; the queries, and what belongs to
+them, hold the requests' new tokens one after another without padding:
 
     freqs = rope_freqs(theta, "yarn", factor=40.0, original_max_position=4096)   # once
+    t = cp_step_tables(prev, ctx, new, block_table, free_pages, free_state, bs, N, cp, rank)
+    cp_rope_store(latent, k_rope, t.positions, freqs, block_table, kv_cache, cp, rank)
+    positions = t.positions[t.positions >= 0]       # (the host waits; with its own lengths it need not)
     mla_rope(q[..., 128:], positions, freqs, out=q[..., 128:])
-    cp_rope_store(latent, k_rope, positions, freqs, block_table, kv_cache, cp, rank)
+    seq_lens = t.seq_lens[0]                        # kv_starts = cumsum(seq_lens) - seq_lens
     k, v, kr = mla_expand(kv_cache, block_table, seq_lens, kv_starts, w_kv, S)
-    out, lse = mla_prefill(q, k, kr, v, cu_q_lens, kv_starts, seq_lens, total_lens, scale, cp, rank)
+    out, lse = mla_prefill(q, k, kr, v, cu_q_lens, kv_starts, seq_lens, t.total_lens, scale, cp, rank)
+
+Tokens without padding are appended as T requests of one token each, latent [T, 1, 512] and positions
+[T, 1], with the table's row of each token's request: block_table[request_of_token].
 
 Single tokens beside the chunks may go this way too; where all requests bring one (or a few), the
 absorbed form (mla_rope into the absorbed queries, cp_rope_store, mla_decode) reads far less.

@@ -291,6 +291,57 @@ def test_rope_store_of_thousands(B, N, cp, rank, il):
 
 
 # =============================================================================================
+# together
+# =============================================================================================
+@pytest.mark.parametrize("cp,rank", [(1, 0), (2, 1)])
+def test_layer_of_uneven_chunks(cp, rank):
+    """A step's layer as the module's example has it, for requests of different lengths; the append of
+    tokens without padding, as requests of one token each, writes the same rows."""
+    g = gen(77 + cp)
+    new, ctx, H, bs, N = [37, 130, 0, 1], [20, 0, 5, 300], 2, 16, 130
+    B, width = 4, 40
+    nb = B * width
+    table = torch.full((B, width), -1, dtype=torch.int32, device=DEV)
+    ring = torch.randperm(nb, generator=g).to(torch.int32).to(DEV)
+    w, freqs = randn(g, H, 256, 512, scale=512 ** -0.5), M.rope_freqs(**FREQS["yarn"])
+    t0 = M.cp_step_tables(i32([0] * B), i32([0] * B), i32(ctx), table, ring, i32([0, nb]), bs, 300, cp, rank)
+    cache = randn(g, nb, bs, 576)                   # what the tokens before left
+    t = M.cp_step_tables(t0.total_lens, i32(ctx), i32(new), table, ring, t0.free_state, bs, N, cp, rank)
+    again = cache.clone()
+    kv = randn(g, B, N, 576)
+    M.cp_rope_store(kv[..., :512], kv[..., 512:], t.positions, freqs, table, cache, cp, rank)
+    real = t.positions >= 0
+    positions = t.positions[real]
+    assert positions.tolist() == [c + j for n, c in zip(new, ctx) for j in range(n)]
+    flat = kv[real]
+    owner = i64([b for b in range(B) for _ in range(new[b])])
+    M.cp_rope_store(flat[:, None, :512], flat[:, None, 512:], positions[:, None], freqs, table[owner], again, cp, rank)
+    assert torch.equal(cache, again)
+    q = randn(g, sum(new), H, 192)
+    before = n64(q)
+    M.mla_rope(q[..., 128:], positions, freqs, out=q[..., 128:])
+    turned = P.ref_rope(before[..., 128:], positions.tolist(), freqs.tolist(), False, 1.0, before[..., 128:])
+    within(n64(q)[..., 128:], turned, BF * np.abs(turned) + 2.0 ** -20 * pair_sum(before[..., 128:], False), "rope")
+    seq = t.seq_lens[0]
+    G = [a + b for a, b in zip(new, ctx)]
+    lens = [int(R.ref_local_len(x, cp, rank, 1)) for x in G]
+    assert seq.tolist() == lens and t.total_lens.tolist() == G
+    starts, S = starts_of(lens)
+    kv_starts = torch.cumsum(seq, 0, dtype=torch.int32) - seq
+    assert kv_starts.tolist() == starts
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(int).tolist()
+    k, v, kr = M.mla_expand(cache, table, seq, kv_starts, w, S)
+    want, wr, mag, mine = P.ref_expand(lambda b: R.ref_gather_pages(n64(cache), table[b].cpu().numpy(), lens[b]), lens, starts,
+                                       n64(w), S)
+    got = np.concatenate([n64(k), n64(v)], -1).transpose(1, 0, 2)
+    assert mine.all() and np.array_equal(n64(kr), wr)
+    within(got, want, BF * np.abs(want) + 92 * U * mag, "kv")
+    out, lse = M.mla_prefill(q, k, kr, v, i32(cu), kv_starts, seq, t.total_lens, SCALE, cp, rank)
+    check(dict(q=q, k=k, kr=kr, v=v, cu=cu, starts=starts, lens=lens, G=G, cp=cp, rank=rank, il=1), out, lse, split=True)
+    assert M.device_status() == 0
+
+
+# =============================================================================================
 # merge
 # =============================================================================================
 @pytest.mark.parametrize("n,T,H", [(3, 5, 2), (16, 3, 2), (3, 4000, 2), (40, 300, 4)])
