@@ -23,8 +23,8 @@
 // sets of four warps, a set an accumulator, through shared memory as rows of 256 bytes.
 //
 // Measured: 8,192 rows x 128 heads in 170 to 189 us (1.46 to 1.62 PFLOP/s by the clock that the power
-// limit leaves, 3 TB/s written), 67,583 8-bit rows x 32 heads in 345 (1.64 PFLOP/s); 2,064 rows x 8
-// heads in 10.7, nearly all of it the way of the first rows and weights and the last outputs.
+// limit leaves, 3 TB/s written), 67,583 8-bit rows x 32 heads in 300 to 352 (1.89 to 1.61 PFLOP/s);
+// 2,064 rows x 8 heads in 10.6, nearly all of it the way of the first rows and weights and the last outputs.
 //
 // Safety: every wait is bounded (sm100.cuh); rows of no request, and pages or lengths out of range,
 // are read as zeros and not written (the latter flagged).

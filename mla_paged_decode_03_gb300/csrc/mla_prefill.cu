@@ -33,10 +33,10 @@
 // combine joins.  Units of up to 128 rows take the streams by turns.  Outputs go
 // from a row a thread to whole lines by lane exchanges.
 //
-// Measured: one prompt of 8,192 tokens x 128 heads in 1.45 to 1.69 ms (1.6 to 1.9 PFLOP/s of masked
-// work; the clock falls to 1.4 GHz under the power limit); 512 tokens behind 32,256 x 8 heads in 61 us
-// (1.39 PFLOP/s with the combine); 24 requests of 1 to 700 tokens, 32 heads, in 283, whose units of few
-// tiles spend 4,000 to 7,000 clocks each on what no tile hides.
+// Measured, in a graph and as calls for a second: one prompt of 8,192 tokens x 128 heads in 1.47 and 1.68 ms
+// (1.9 and 1.6 PFLOP/s of masked work; the clock falls to 1.4 GHz under the power limit); 512 tokens
+// behind 32,256 x 8 heads in 60 and 63 us (1.4 PFLOP/s with the combine); 24 requests of 1 to 700 tokens,
+// 32 heads, in 282 and 306, whose units of few tiles spend 4,000 to 7,000 clocks each on what no tile hides.
 //
 // Safety: every wait is bounded (sm100.cuh); lengths and starts out of range are clamped and
 // flagged; value rows behind a request's last key are zeroed in shared memory before they meet P
@@ -312,7 +312,11 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return d;
 }
 
-// Two weights 2^(s mul + sub), added to `sum`, as two bf16.
+// Two weights 2^(s mul + sub), added to `sum`, as two bf16.  The values are bf16, and both operands of a product
+// have one type, so a weight has 8 bits there: with 16 (two bf16 words, the products twice) PV would take as
+// long again, a third more in all.  The rounding is unbiased, at most 2^-8 of each term; beside the output's own it
+// makes the mean error sqrt(2) times what that alone would (0.0022 of the values instead of 0.0016).  The sum
+// keeps 32 bits, and so does the LSE.
 __device__ __forceinline__ uint32_t weights(float2 s, float2 mul, float sub, float2& sum) {
   const float2 e = fma2(s, mul, make_float2(sub, sub));
   const float2 p = make_float2(exp2_fast(e.x), exp2_fast(e.y));

@@ -14,9 +14,10 @@
 // eight pairs of one token, so that its eight sines and cosines serve all heads that its warp
 // takes.  Four lanes hold a rope part: two 16-byte chunks each, 64 bytes apart in either layout.
 //
-// Measured: 8,192 tokens x 128 heads out of rows of 192 in 47 us (5.8 TB/s, 86% of a copy's rate; the
-// 128 bytes read of each 384 are whole lines); 64 tokens x 128 heads in 2.6 us in a graph.  Stores: some
-// 24,500 rows of 49,200 positions in 13.2 us (4.3 TB/s), 64 in 2.8.
+// Measured in graphs: 8,192 tokens x 128 heads out of rows of 192 in 47 us (5.8 TB/s, 86% of a copy's rate;
+// the 128 bytes read of each 384 are whole lines); 64 tokens x 128 heads in 3.0 us.  One head leaves 28 of a
+// warp's lanes idle: 8,192 tokens in 7.2 us, 65,536 in 42, where their 17 MB would pass in 2.5.  Stores: some
+// 24,500 rows of 49,200 positions in 12.9 us (4.4 TB/s), 64 in 2.8.
 #include <cuda_bf16.h>
 
 #include "internal.h"
@@ -213,8 +214,17 @@ cudaError_t launch_cp_rope_store(const RopeStoreArgs& a, cudaStream_t stream) {
   const long long total = (long long)a.B * a.N;
   const SlotParams p = make_slot_params(a.block_table, a.bt_stride, a.max_blocks, a.block_size,
                                         a.cp_size, a.cp_rank, a.interleave, a.status);
-  // a position a warp while that keeps all warps resident (64 positions 2.8 us; 32 a warp would put them
-  // on two warps), then 32 (65,536 positions, two ranks: 4 a warp 18.8 us, 8 13.9, 16 14.3, 32 13.0)
+  // a position a warp while that keeps all warps resident, then 32.  us in a graph, one rank (one of two), by
+  // positions a warp:
+  //   positions       1              8              32
+  //          64    3.2 (3.2)      4.7 (3.7)      8.6 (5.6)
+  //       4,864    6.6 (6.0)      5.4 (4.1)     12.7 (7.9)
+  //       8,192   10.3 (9.5)      5.9 (4.4)     12.9 (8.0)
+  //      16,384   17.5 (15.7)     8.1 (5.6)     13.4 (8.2)
+  //      32,768   33.5 (28.9)    16.0 (9.6)     17.3 (9.1)
+  //      65,536   65.9 (56.1)    28.3 (17.6)    27.9 (15.4)
+  // so both ends are served, and 8 would be the better choice from a thousand to 32,000 positions: with 32 they
+  // are on few SMs (4,865 positions on 20 blocks, every SM has one from 38,900 on).
   const int group = total <= 32LL * a.num_sms ? 1 : 32;
   const long long warps = (total + group - 1) / group;
   DependentLaunch dl(dim3((unsigned)((warps + 7) / 8)), dim3(256), stream);
