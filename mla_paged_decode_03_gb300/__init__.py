@@ -21,6 +21,7 @@ runs in the library's CUDA kernels.  All tensors must live on the current CUDA d
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Optional, Tuple
 
@@ -48,6 +49,12 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 def _stream(stream) -> int:
     s = torch.cuda.current_stream() if stream is None else stream
     return s.cuda_stream
+
+
+def _allocating(stream):
+    """What is allocated inside belongs to the given stream (None: the current one), so that it is neither
+    memory that the current stream still uses nor handed out again there while the call's kernels run."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _need(t: torch.Tensor, name: str, dtype, ndim=None):
@@ -109,15 +116,16 @@ def mla_decode(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torch.Tenso
     _need(seq_lens, "seq_lens", torch.int32, 1)
     if causal_seqlens_global is not None:
         _need(causal_seqlens_global, "causal_seqlens_global", torch.int32, 1)
-    if out is None:
-        out = torch.empty(B * q_len, H, D_V, dtype=torch.bfloat16, device=q.device)
+    with _allocating(stream):
+        if out is None:
+            out = torch.empty(B * q_len, H, D_V, dtype=torch.bfloat16, device=q.device)
+        if lse is None and return_lse:
+            lse = torch.empty(B * q_len, H, dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = alloc_workspace(B, H, q_len, q.device)
     _need(out, "out", torch.bfloat16)
-    if lse is None and return_lse:
-        lse = torch.empty(B * q_len, H, dtype=torch.float32, device=q.device)
     if lse is not None:
         _need(lse, "lse", torch.float32)
-    if workspace is None:
-        workspace = alloc_workspace(B, H, q_len, q.device)
     ws_bytes = workspace.numel() * workspace.element_size()
     L = _lib.load()
     rc = L.mla_decode(q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(),
@@ -163,14 +171,15 @@ def mla_decode_shards(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torc
         raise ValueError("seq_lens must be [n_shards*B]")
     if causal_seqlens_global is not None:
         _need(causal_seqlens_global, "causal_seqlens_global", torch.int32, 1)
-    if out is None:
-        out = torch.empty(n_shards, B * q_len, H, D_V, dtype=torch.bfloat16, device=q.device)
+    with _allocating(stream):
+        if out is None:
+            out = torch.empty(n_shards, B * q_len, H, D_V, dtype=torch.bfloat16, device=q.device)
+        if lse is None:
+            lse = torch.empty(n_shards, B * q_len, H, dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = alloc_workspace(n_shards * B, H, q_len, q.device)
     _need(out, "out", torch.bfloat16)
-    if lse is None:
-        lse = torch.empty(n_shards, B * q_len, H, dtype=torch.float32, device=q.device)
     _need(lse, "lse", torch.float32)
-    if workspace is None:
-        workspace = alloc_workspace(n_shards * B, H, q_len, q.device)
     ws_bytes = workspace.numel() * workspace.element_size()
     L = _lib.load()
     rc = L.mla_decode_shards(q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(),
@@ -200,7 +209,8 @@ def lse_merge(partials: torch.Tensor, lses: torch.Tensor, out: Optional[torch.Te
     if tuple(lses.shape) != (n, T, H):
         raise ValueError("lses must be [n, T, H]")
     if out is None:
-        out = torch.empty(T, H, Dv, dtype=torch.bfloat16, device=partials.device)
+        with _allocating(stream):
+            out = torch.empty(T, H, Dv, dtype=torch.bfloat16, device=partials.device)
     _need(out, "out", torch.bfloat16)
     # (of rows of 512 a larger buffer has always been taken)
     if out.numel() < T * H * Dv or (Dv != D_V and tuple(out.shape) != (T, H, Dv)):
@@ -232,7 +242,8 @@ def cp_local_slot(positions: torch.Tensor, block_table: torch.Tensor, block_size
     if block_table.shape[0] != B:
         raise ValueError("block_table must have one row per positions row")
     if slots is None:
-        slots = torch.empty_like(positions)
+        with _allocating(stream):
+            slots = torch.empty_like(positions)
     _need(slots, "slots", torch.int64, 2)
     rc = _lib.load().cp_local_slot(positions.data_ptr(), block_table.data_ptr(),
                                    block_table.stride(0), block_table.shape[1], B, N,
