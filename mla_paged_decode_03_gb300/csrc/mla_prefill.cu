@@ -635,6 +635,9 @@ mla_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
         __syncwarp();
         ++k;
         if (!some) break;
+        // requests behind the last row tile's, which nobody looks for, are checked here
+        if (x + 1 == gridDim.x && y == 0)
+          while (requests.base + 32 < a.B) requests.next(a, lane);
         // the next one only when this one is nearly loaded: what is asked for early runs late
         ok = s.wait(B_ASK, (k & 1) ^ 1u);
         if (!ok) break;

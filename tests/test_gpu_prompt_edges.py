@@ -81,6 +81,34 @@ def test_prefill_split_skips_among_many_requests():
     assert left.any() and (out[left] == 9).all() and (lse[left] == 9).all()
 
 
+@pytest.mark.parametrize("what", ["rows", "rows before", "keys", "start"])
+@pytest.mark.parametrize("B", [33, 65, 100])
+@pytest.mark.parametrize("split", [True, False])
+def test_prefill_reports_requests_behind_the_last_rows(what, B, split):
+    """A request out of order or range is reported wherever it stands: here behind all rows, in a round of 32
+    requests of which no other one has any."""
+    new = [1, 1] + [0] * (B - 2)
+    d = prefill_case(new, [900, 3] + [1] * (B - 2), 1)
+    good, good_lse = call(d)
+    assert M.device_status() == 0
+    cu, lens, starts = list(d["cu"]), list(d["lens"]), list(d["starts"])
+    if what == "rows":
+        cu[B] = 3                                  # beyond T
+    elif what == "rows before":
+        cu[B] = 1
+    elif what == "keys":
+        lens[B - 1] = -1
+    else:
+        starts[B - 1] = d["S"] + 1
+    n = M.workspace_size_prefill(2, B, 1, d["S"])
+    assert n > 0
+    ws = torch.empty(n if split else 0, dtype=torch.uint8, device=DEV)
+    for _ in range(2):
+        out, lse = call(dict(d, cu=cu, lens=lens, starts=starts), workspace=ws)
+        assert M.device_status() == BAD_STEP
+        check(dict(d, cu=d["cu"][:3], lens=lens[:2], starts=starts[:2], G=d["G"][:2]), out, lse, split=True)
+
+
 def test_prefill_rows_computed_again_do_not_run_out_of_time():
     """Rows that a NaN in a value they do not see has them computed again take longer than the wait limit, here
     some 3 ms against 0.5; the block's other warps wait that long, and its next unit is complete as well."""
