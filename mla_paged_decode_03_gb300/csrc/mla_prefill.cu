@@ -313,8 +313,8 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 
 // Two weights 2^(s mul + sub), added to `sum`, as two bf16.  The values are bf16, and both operands of a product
-// have one type, so a weight has 8 bits there: with 16 (two bf16 words, the products twice) PV would take as
-// long again, a third more in all.  The rounding is unbiased, at most 2^-8 of each term; beside the output's own it
+// have one type, so a weight has 8 bits there: with 16 (two bf16 words, the products twice) PV would take
+// twice its time, 40% more products in all.  The rounding is unbiased, at most 2^-8 of each term; beside the output's own it
 // makes the mean error sqrt(2) times what that alone would (0.0022 of the values instead of 0.0016).  The sum
 // keeps 32 bits, and so does the LSE.
 __device__ __forceinline__ uint32_t weights(float2 s, float2 mul, float sub, float2& sum) {
